@@ -1,0 +1,473 @@
+"""Measured cases of the operators around the expert layer.
+
+Three operators: the residual addition with an RMS norm and an 8-bit output
+(kind "norm"); the tokens sorted by expert (kind "sort"), brought back with
+their weights (kind "unsort") and the gradients of both (kind "grads"); the
+matrix-vector products with 4-bit weights and group scales ("w4").
+
+`run` with `own` false computes them in elementary torch operations, with
+`own` true through the package's entry points.  `exact` computes the same
+outputs in 64 bits from the definitions.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+own = False
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+SIZE = {"bf16": 2, "fp16": 2, "fp32": 4, "int8": 1}
+EPS = 1e-6
+
+
+# ------------------------------------------------------------------- cases --
+def _norm(name, T, H, dtype, q, group, y):
+    return {"name": name, "kind": "norm", "T": T, "H": H, "dtype": dtype, "q": q, "group": group,
+            "y": y}
+
+
+def _sort(name, T, k, E, ids, H, dtype):
+    return {"name": name, "kind": "sort", "T": T, "k": k, "E": E, "ids": ids, "H": H,
+            "dtype": dtype}
+
+
+def _back(name, kind, T, k, E, H, dtype, out):
+    return {"name": name, "kind": kind, "T": T, "k": k, "E": E, "H": H, "dtype": dtype,
+            "out": out}
+
+
+def _w4(name, E, R, N, K, group, x, out, up, zeros):
+    return {"name": name, "kind": "w4", "E": E, "R": R, "N": N, "K": K, "group": group, "x": x,
+            "out": out, "up": up, "zeros": zeros}
+
+
+def listed():
+    return [
+        # one decoded token of a 7168-channel model ahead of an int8 layer: latency only
+        _norm("norm_one_token", 1, 7168, "bf16", "int8", 0, True),
+        # a ragged batch in fp16 whose consumer takes e4m3 with a scale for every 128 channels
+        _norm("norm_fp8_groups", 457, 5120, "fp16", "e4m3", 128, False),
+        # a prefill chunk: the new residual, the router's 16-bit rows and the experts' int8 codes
+        _norm("norm_prefill", 8192, 7168, "bf16", "int8", 0, True),
+        # a decode batch; a third of the picks go to zero-computation experts and are dropped
+        _sort("sort_decode", 64, 12, 512, 768, 6144, "bf16"),
+        # a prefill chunk over 256 experts with skewed popularity
+        _sort("sort_prefill", 8192, 8, 256, 256, 7168, "bf16"),
+        # a decode batch's fp32 expert outputs back to bf16 tokens
+        _back("unsort_decode", "unsort", 128, 8, 256, 7168, "fp32", "bf16"),
+        # gradients of a small fp32 model with a ragged hidden size
+        _back("grads_ragged", "grads", 333, 2, 8, 1000, "fp32", "fp32"),
+        # gradients of a training micro-batch
+        _back("grads_train", "grads", 4096, 8, 64, 5120, "bf16", "bf16"),
+        # one decoded token through one expert's down projection: latency
+        _w4("w4_one_row", 1, 1, 7168, 2048, 128, "bf16", "bf16", False, False),
+        # a few rows of int8 codes (the norm's output) through one square projection
+        _w4("w4_codes", 1, 12, 6144, 6144, 64, "int8", "fp32", False, False),
+        # sixteen experts held by one card, ragged loads, zero points, small groups
+        _w4("w4_down", 16, 37, 7168, 2048, 32, "fp16", "fp16", False, True),
+        # 64 experts' gate and up projections with SwiGLU for a decode batch
+        _w4("w4_gate_up", 64, 192, 1536, 5120, 128, "bf16", "bf16", True, False),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    case = _drawn(rng)
+    while 3072 in case.values():  # no configuration of this repository has this size
+        case = _drawn(rng)
+    return case
+
+
+def _drawn(rng):
+    kind = rng.choice(["norm", "sort", "unsort", "grads", "w4", "w4"])
+    dtype = rng.choice(["bf16", "bf16", "fp16", "fp32"])
+    if kind == "w4":
+        E = rng.choice([1, 1, 4, 8, 16, 32, 64])
+        # at most the work of the largest listed case: N * K of an expert shrinks with E
+        most = min(1536 * 5120 * 64 // E, 7168 * 7168)
+        K = 32 * max(1, _log(rng, 256, 7168) // 32)
+        N = min(_log(rng, 64, 7168), most // K)
+        if rng.random() < 0.5:
+            N = max(16, N // 16 * 16)
+        group = rng.choice([32, 64, 128, 0])
+        group = group if group == 0 or K % group == 0 else 32
+        return {"kind": kind, "E": E, "R": _log(rng, 1, 16) if E == 1 else _log(rng, E // 2, 3 * E),
+                "N": N, "K": K, "group": group, "x": rng.choice(["bf16", "bf16", "fp16", "int8"]),
+                "out": rng.choice(["bf16", "fp32"]), "up": rng.random() < 0.5,
+                "zeros": rng.random() < 0.3}
+    T = _log(rng, 1, 4096)
+    H = _log(rng, 256, 7168)
+    H = H if rng.random() < 0.2 else max(128, H // 8 * 8)
+    if kind == "norm":
+        q, group = rng.choice([("int8", 0), ("int8", 0), ("e4m3", 0), ("e4m3", 128), ("int8", 64)])
+        return {"kind": kind, "T": T, "H": H, "dtype": dtype, "q": q, "group": group,
+                "y": rng.random() < 0.5}
+    E = rng.choice([8, 16, 64, 160, 256, 512])
+    k = min(rng.choice([1, 2, 4, 6, 8]), E)
+    if kind == "sort":
+        ids = E if rng.random() < 0.5 else E + E // 2
+        return {"kind": kind, "T": T, "k": k, "E": E, "ids": ids, "H": H, "dtype": dtype}
+    return {"kind": kind, "T": T, "k": k, "E": E, "H": H, "dtype": dtype,
+            "out": rng.choice([dtype, "fp32"])}
+
+
+# ------------------------------------------------------------------ inputs --
+def _randn(g, *shape, dtype=torch.float32):
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+def _picks(g, T, k, E):
+    """Top-k picks of distinct experts under a skewed popularity, and their weights."""
+    popularity = -0.7 * torch.log1p(torch.randperm(E, generator=g, device="cuda").float())
+    logits = _randn(g, T, E) + popularity
+    top = torch.topk(torch.softmax(logits, dim=-1), k, dim=-1)
+    return top.indices.to(torch.int32), top.values / top.values.sum(-1, keepdim=True)
+
+
+def _order(ids, E):
+    """Plan of the sorted order, as a training step keeps it between forward and backward."""
+    key = torch.where((ids >= 0) & (ids < E), ids, E).reshape(-1)
+    s2e = torch.sort(key, stable=True).indices
+    e2s = torch.empty_like(s2e)
+    e2s[s2e] = torch.arange(s2e.numel(), device=s2e.device)
+    bounds = torch.arange(E + 1, device=key.device)
+    offsets = (key[None, :] < bounds[:, None]).sum(1)
+    return (x.to(torch.int32) for x in (s2e, e2s, offsets))
+
+
+def _hit(case):
+    """Experts with rows: seven in eight, and no more than there are rows."""
+    return max(1, min(case["R"], case["E"] - case["E"] // 8))
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    s = {"case": case}
+    dev = "cuda"
+    if case["kind"] == "norm":
+        T, H, dt = case["T"], case["H"], DT[case["dtype"]]
+        # a residual stream has a few channels far above the rest
+        loud = 1.0 + 12.0 * (torch.rand(H, generator=g, device=dev) < 0.01).float()
+        s["x"] = _randn(g, T, H, dtype=dt)
+        s["res"] = (2.0 * _randn(g, T, H) * loud).to(dt)
+        s["gamma"] = (1.0 + 0.2 * _randn(g, H)).to(dt)
+        s["sum"] = torch.empty(T, H, dtype=dt, device=dev)
+        s["y"] = torch.empty(T, H, dtype=dt, device=dev) if case["y"] else None
+        s["q"] = torch.empty(T, H, dtype=torch.int8 if case["q"] == "int8" else torch.float8_e4m3fn,
+                             device=dev)
+        G = -(-H // case["group"]) if case["group"] else 1
+        s["scale"] = torch.empty(T, G, device=dev)
+        return s
+    if case["kind"] == "w4":
+        E, R, N, K = case["E"], case["R"], case["N"], case["K"]
+        G = K // case["group"] if case["group"] else 1
+        xdt = DT.get(case["x"])
+        if xdt is None:
+            s["x"] = torch.randint(-127, 128, (R, K), generator=g, device=dev, dtype=torch.int8)
+            s["x_scale"] = 0.01 + 0.05 * torch.rand(R, generator=g, device=dev)
+        else:
+            s["x"], s["x_scale"] = _randn(g, R, K, dtype=xdt), None
+        for m in ("gate", "up")[: 2 if case["up"] else 1]:
+            s["w_" + m] = torch.randint(0, 256, (E, N, K // 2), generator=g, device=dev,
+                                        dtype=torch.uint8)
+            s["s_" + m] = ((0.3 + torch.rand(E, N, G, generator=g, device=dev)) / (4.6 * K**0.5)).to(
+                xdt or torch.float32)
+            s["z_" + m] = (torch.randint(5, 11, (E, N, G), generator=g, device=dev,
+                                         dtype=torch.uint8) if case["zeros"] else None)
+        # rows of each expert: some experts empty, the others at least one row, the rest skewed
+        hit = torch.randperm(E, generator=g, device=dev)[:_hit(case)]
+        share = 1e-3 + torch.rand(len(hit), generator=g, device=dev) ** 2
+        more = torch.multinomial(share.expand(1, -1), max(1, R - len(hit)), replacement=True,
+                                 generator=g)[0, :R - len(hit)]
+        expert = torch.sort(torch.cat([hit, hit[more]])).values
+        bounds = torch.arange(E + 1, device=dev)
+        s["offsets"] = (expert[None, :] < bounds[:, None]).sum(1).to(torch.int32)
+        s["out"] = torch.empty(R, N, dtype=DT[case["out"]], device=dev)
+        return s
+    T, k, E, H, dt = case["T"], case["k"], case["E"], case["H"], DT[case["dtype"]]
+    ids, w = _picks(g, T, k, case.get("ids", E))
+    if case["kind"] == "sort":
+        s["ids"], s["x"] = ids, _randn(g, T, H, dtype=dt)
+        s["counts"] = torch.empty(E, dtype=torch.int32, device=dev)
+        s["offsets"] = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        s["s2e"] = torch.empty(T * k, dtype=torch.int32, device=dev)
+        s["e2s"] = torch.empty(T * k, dtype=torch.int32, device=dev)
+        s["x_sorted"] = torch.empty(T * k, H, dtype=dt, device=dev)
+        return s
+    odt = DT[case["out"]]
+    _, s["e2s"], s["offsets"] = _order(ids, E)
+    s["w"] = w.contiguous()
+    s["y_sorted"] = _randn(g, T * k, H, dtype=dt)
+    if case["kind"] == "unsort":
+        s["out"] = torch.empty(T, H, dtype=odt, device=dev)
+        return s
+    s["dout"] = _randn(g, T, H, dtype=odt)
+    s["dx_sorted"] = _randn(g, T * k, H, dtype=dt)
+    s["dy_sorted"] = torch.empty(T * k, H, dtype=dt, device=dev)
+    s["dw"] = torch.empty(T, k, device=dev)
+    s["dx"] = torch.empty(T, H, dtype=dt, device=dev)
+    return s
+
+
+# ------------------------------------------------------------- plain forms --
+def _plain_norm(s):
+    c = s["case"]
+    T, H = s["x"].shape
+    r = s["x"].float() + s["res"].float()
+    y = r * torch.rsqrt((r * r).mean(-1, keepdim=True) + EPS) * s["gamma"].float()
+    G = s["scale"].shape[1]
+    width = c["group"] or H
+    yg = torch.nn.functional.pad(y, (0, G * width - H)).view(T, G, width)
+    most = 127.0 if c["q"] == "int8" else 448.0
+    scale = yg.abs().amax(-1, keepdim=True) / most
+    t = torch.where(scale > 0, yg / scale, 0.0)
+    if c["q"] == "int8":
+        code = torch.round(t).clamp(-127, 127)
+    else:
+        code = t.clamp(-448, 448).to(torch.float8_e4m3fn).float()
+    value = (code * scale).view(T, G * width)[:, :H].to(torch.bfloat16)
+    out = [r.to(s["x"].dtype), value, scale.view(T, G)]
+    return out + ([y.to(s["x"].dtype)] if c["y"] else [])
+
+
+def _plain_sort(s):
+    c = s["case"]
+    E, k = c["E"], c["k"]
+    key = torch.where((s["ids"] >= 0) & (s["ids"] < E), s["ids"], E).reshape(-1)
+    s2e = torch.sort(key, stable=True).indices
+    e2s = torch.empty_like(s2e)
+    e2s[s2e] = torch.arange(s2e.numel(), device=s2e.device)
+    counts = torch.zeros(E + 1, dtype=torch.int64, device=key.device)
+    counts.scatter_add_(0, key.long(), torch.ones_like(s2e))
+    offsets = torch.cat([counts.new_zeros(1), counts[:E].cumsum(0)])
+    kept = (key[s2e] < E)[:, None]
+    x_sorted = torch.where(kept, s["x"][s2e // k], 0)
+    return [x_sorted, counts[:E].int(), offsets.int(), s2e.int(), e2s.int()]
+
+
+def _plain_unsort(s):
+    c = s["case"]
+    T, k = c["T"], c["k"]
+    rows = s["y_sorted"][s["e2s"].long()].float().view(T, k, -1)
+    return [(rows * s["w"][:, :, None]).sum(1).to(DT[c["out"]])]
+
+
+def _plain_grads(s):
+    c = s["case"]
+    T, k, dt = c["T"], c["k"], DT[c["dtype"]]
+    e2s = s["e2s"].long()
+    dout = s["dout"].float()
+    dw = (s["y_sorted"][e2s].float().view(T, k, -1) * dout[:, None, :]).sum(-1)
+    dy = torch.empty_like(s["y_sorted"])
+    dy[e2s] = (s["w"][:, :, None] * dout[:, None, :]).reshape(T * k, -1).to(dt)
+    dx = s["dx_sorted"][e2s].float().view(T, k, -1).sum(1).to(dt)
+    return [dy, dw, dx]
+
+
+def _plain_dequant(w, scale, zero):
+    E, N, half = w.shape
+    q = torch.stack([w & 15, w >> 4], dim=-1).view(E, N, scale.shape[2], -1).float()
+    z = 8.0 if zero is None else zero.float()[..., None]
+    return ((q - z) * scale.float()[..., None]).view(E, N, 2 * half)
+
+
+def _plain_w4(s):
+    c = s["case"]
+    row = torch.arange(c["R"], device="cuda")
+    mask = (row >= s["offsets"][:-1, None]) & (row < s["offsets"][1:, None])  # [E, R]
+    x = s["x"].float()
+    if s["x_scale"] is not None:
+        x = x * s["x_scale"][:, None]
+    xe = x[None] * mask[:, :, None]
+    y = torch.bmm(xe, _plain_dequant(s["w_gate"], s["s_gate"], s["z_gate"]).mT).sum(0)
+    if c["up"]:
+        u = torch.bmm(xe, _plain_dequant(s["w_up"], s["s_up"], s["z_up"]).mT).sum(0)
+        y = y / (1.0 + torch.exp(-y)) * u
+    return [y.to(DT[c["out"]])]
+
+
+# -------------------------------------------------------- the package's calls --
+def _own_norm(s, moe):
+    c = s["case"]
+    moe.moe_add_rmsnorm(s["x"], s["res"], s["gamma"], EPS, s["sum"], s["y"], s["q"], s["scale"],
+                        c["group"])
+    # the codes as the values they stand for
+    T, H = s["x"].shape
+    G, width = s["scale"].shape[1], c["group"] or H
+    q = s["q"] if c["q"] == "int8" else s["q"].to(torch.bfloat16)
+    value = torch.empty(T, H, dtype=torch.bfloat16, device=q.device)
+    if H == G * width:
+        torch.mul(q.view(T, G, width), s["scale"][:, :, None], out=value.view(T, G, width))
+    else:
+        torch.mul(q, s["scale"].repeat_interleave(width, 1)[:, :H], out=value)
+    return [s["sum"], value, s["scale"]] + ([s["y"]] if c["y"] else [])
+
+
+def _own_sort(s, moe):
+    c = s["case"]
+    if "ws" not in s:  # the workspace a program keeps
+        s["ws"] = moe.sort_workspace(c["T"], c["k"], c["E"])
+    moe.moe_sort_tokens(c["E"], s["ids"], s["x"], None, s["counts"], s["offsets"], s["s2e"],
+                        s["e2s"], s["x_sorted"], None, s["ws"], zero_dropped=True)
+    return [s["x_sorted"], s["counts"], s["offsets"], s["s2e"], s["e2s"]]
+
+
+def _own_unsort(s, moe):
+    moe.moe_unsort_tokens(s["y_sorted"], s["offsets"], s["e2s"], s["w"], s["out"])
+    return [s["out"]]
+
+
+def _own_grads(s, moe):
+    moe.moe_unsort_tokens_backward(s["dout"], s["y_sorted"], s["offsets"], s["e2s"], s["w"],
+                                   s["dy_sorted"], s["dw"])
+    moe.moe_sort_tokens_backward(s["dx_sorted"], s["offsets"], s["e2s"], s["case"]["k"], s["dx"])
+    return [s["dy_sorted"], s["dw"], s["dx"]]
+
+
+def _own_w4(s, moe):
+    c = s["case"]
+    moe.moe_w4_gemv(s["x"], s["x_scale"], s["offsets"], s["w_gate"], s["s_gate"], s["z_gate"],
+                    s["out"], s.get("w_up"), s.get("s_up"), s.get("z_up"))
+    return [s["out"]]
+
+
+def run(state):
+    kind = state["case"]["kind"]
+    if own:
+        import sparse_expert_layer_gb300 as moe
+
+        return {"norm": _own_norm, "sort": _own_sort, "unsort": _own_unsort, "grads": _own_grads,
+                "w4": _own_w4}[kind](state, moe)
+    return {"norm": _plain_norm, "sort": _plain_sort, "unsort": _plain_unsort,
+            "grads": _plain_grads, "w4": _plain_w4}[kind](state)
+
+
+# -------------------------------------------------------------------- work --
+def work(case):
+    c = case
+    if c["kind"] == "norm":
+        n, b = c["T"] * c["H"], SIZE[c["dtype"]]
+        G = -(-c["H"] // c["group"]) if c["group"] else 1
+        return {"bytes": n * (3 * b + 1 + (b if c["y"] else 0)) + c["H"] * b + 4 * c["T"] * G,
+                "flops": 8 * n}
+    if c["kind"] == "w4":
+        mats = 2 if c["up"] else 1
+        hit = _hit(c)  # an expert without rows is not read
+        G = c["K"] // c["group"] if c["group"] else 1
+        per = c["N"] * c["K"] // 2 + c["N"] * G * (SIZE[c["x"]] if c["x"] != "int8" else 4)
+        per += c["N"] * G if c["zeros"] else 0
+        return {"bytes": hit * mats * per + c["R"] * c["K"] * SIZE[c["x"]]
+                + c["R"] * c["N"] * SIZE[c["out"]], "flops": 2 * mats * c["R"] * c["N"] * c["K"]}
+    R, H, b = c["T"] * c["k"], c["H"], SIZE[c["dtype"]]
+    if c["kind"] == "sort":
+        return {"bytes": c["T"] * H * b + R * H * b + 12 * R + 8 * c["E"], "flops": 0}
+    bo = SIZE[c["out"]]
+    if c["kind"] == "unsort":
+        return {"bytes": R * H * b + c["T"] * H * bo + 8 * R, "flops": 2 * R * H}
+    return {"bytes": (c["T"] * H * bo + 2 * R * H * b + 12 * R) + (R * H * b + c["T"] * H * b + 4 * R),
+            "flops": 4 * R * H}
+
+
+# ------------------------------------------------------------- in 64 bits --
+def _exact_norm(s):
+    c = s["case"]
+    T, H = s["x"].shape
+    step = c["group"] or H
+    r = torch.add(s["x"].double(), s["res"].double())
+    ms = torch.linalg.vector_norm(r, dim=1) ** 2 / H
+    y = r / torch.sqrt(ms + EPS)[:, None] * s["gamma"].double()
+    value, scale = torch.empty_like(y), []
+    for a in range(0, H, step):
+        part = y[:, a:a + step]
+        amax = torch.maximum(part.max(1).values, -part.min(1).values)
+        if c["q"] == "int8":
+            sc = amax / 127
+            code = torch.round(part / torch.where(sc > 0, sc, 1.0)[:, None])
+        else:
+            sc = amax / 448
+            t = part / torch.where(sc > 0, sc, 1.0)[:, None]
+            # e4m3: three mantissa bits, smallest exponent -6
+            e = torch.floor(torch.log2(t.abs().clamp_min(2.0**-6))).clamp_min(-6)
+            ulp = torch.exp2(e - 3)
+            code = torch.round(t / ulp) * ulp
+        value[:, a:a + step] = code * sc[:, None]
+        scale.append(sc)
+    return [r, value, torch.stack(scale, 1)] + ([y] if c["y"] else [])
+
+
+def _exact_sort(s):
+    import numpy as np
+
+    c = s["case"]
+    ids, E, k = s["ids"].cpu().numpy().reshape(-1), c["E"], c["k"]
+    buckets = [np.flatnonzero(ids == e) for e in range(E)]
+    buckets.append(np.flatnonzero((ids < 0) | (ids >= E)))
+    order = np.concatenate(buckets)
+    inverse = np.argsort(order)
+    counts = np.array([len(b) for b in buckets[:E]])
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    rows = torch.zeros(len(ids), c["H"], dtype=torch.float64, device="cuda")
+    n = int(offsets[-1])
+    rows[:n] = s["x"].double()[torch.from_numpy(order[:n] // k).cuda()]
+    return [rows, counts.astype("int32"), offsets.astype("int32"), order.astype("int32"),
+            inverse.astype("int32")]
+
+
+def _exact_unsort(s):
+    c = s["case"]
+    acc = torch.zeros(c["T"], c["H"], dtype=torch.float64, device="cuda")
+    at = s["e2s"].view(c["T"], c["k"]).long()
+    for j in range(c["k"]):
+        acc += s["w"][:, j, None].double() * s["y_sorted"][at[:, j]].double()
+    return [acc]
+
+
+def _exact_grads(s):
+    c = s["case"]
+    at = s["e2s"].view(c["T"], c["k"]).long()
+    dout = s["dout"].double()
+    dy = torch.zeros(c["T"] * c["k"], c["H"], dtype=torch.float64, device="cuda")
+    dw = torch.zeros(c["T"], c["k"], dtype=torch.float64, device="cuda")
+    dx = torch.zeros(c["T"], c["H"], dtype=torch.float64, device="cuda")
+    for j in range(c["k"]):
+        dy[at[:, j]] = s["w"][:, j, None].double() * dout
+        dw[:, j] = torch.einsum("th,th->t", s["y_sorted"][at[:, j]].double(), dout)
+        dx += s["dx_sorted"][at[:, j]].double()
+    return [dy, dw, dx]
+
+
+def _exact_w4(s):
+    c = s["case"]
+    width = c["group"] or c["K"]
+    bounds = s["offsets"].tolist()
+    out = torch.zeros(c["R"], c["N"], dtype=torch.float64, device="cuda")
+    for e in range(c["E"]):
+        a, b = bounds[e], bounds[e + 1]
+        if a == b:
+            continue
+        x = s["x"][a:b].double()
+        if s["x_scale"] is not None:
+            x = s["x_scale"][a:b, None].double() * x
+        got = []
+        for m in ("gate", "up")[: 2 if c["up"] else 1]:
+            packed = s["w_" + m][e].to(torch.int64)
+            q = torch.empty(c["N"], c["K"], dtype=torch.float64, device="cuda")
+            q[:, 0::2] = (packed % 16).double()
+            q[:, 1::2] = (packed // 16).double()
+            z = s["z_" + m]
+            q -= 8 if z is None else z[e].double().repeat_interleave(width, 1)
+            q *= s["s_" + m][e].double().repeat_interleave(width, 1)
+            got.append(x @ q.T)
+        out[a:b] = got[0] if len(got) == 1 else got[0] * torch.sigmoid(got[0]) * got[1]
+    return [out]
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    return {"norm": _exact_norm, "sort": _exact_sort, "unsort": _exact_unsort,
+            "grads": _exact_grads, "w4": _exact_w4}[case["kind"]](s)
