@@ -109,6 +109,8 @@ def _drawn(rng):
                 "y": rng.random() < 0.5}
     E = rng.choice([8, 16, 64, 160, 256, 512])
     k = min(rng.choice([1, 2, 4, 6, 8]), E)
+    # at most the rows of the listed training case
+    T = min(T, 4096 * 8 * 5120 * 2 // (k * H * SIZE[dtype]))
     if kind == "sort":
         ids = E if rng.random() < 0.5 else E + E // 2
         return {"kind": kind, "T": T, "k": k, "E": E, "ids": ids, "H": H, "dtype": dtype}
