@@ -269,6 +269,106 @@ moe_status moe_tile_choice(const moe_config* cfg, int32_t T, int32_t* gemv_max_r
 /* *ffn_one_launch: 0 = two launches, 1 = one launch, 2 = one launch with
  * 256-channel down tiles (MOE_FFN_LAUNCH_ONE_WIDE). */
 
+/* ---- Operators around the layer ----
+ * They share the conventions above and need no moe_config.  Tensor types are
+ * given per call; row strides (ld*) are in elements and at least the row's
+ * length, arrays without one are contiguous.  Rows whose length or stride is
+ * not a multiple of 16 bytes are taken by slower element-wise accesses. */
+typedef enum {
+  MOE_DT_BF16 = 0,
+  MOE_DT_FP16 = 1,
+  MOE_DT_FP32 = 2,
+  MOE_DT_INT8 = 3,
+  MOE_DT_E4M3 = 4
+} moe_dtype;
+
+/* Residual addition, RMS norm and 8-bit codes, in one pass:
+ *   r = x + residual;  y = r / sqrt(mean(r^2) + eps) * gamma
+ *   int8:  scale = max|y| / 127, code = round half to even of y / scale
+ *   e4m3:  scale = max|y| / 448, code = y / scale rounded to e4m3
+ * r, y and the code's quotient are fp32, each rounded once where it is stored
+ * (the norm takes r before that rounding).  A row (group) of zeros has scale 0
+ * and codes 0; where r holds a NaN or an infinity the scale is NaN, or the
+ * group's codes stand for zeros (a finite group beside an infinity).
+ *  dtype     MOE_DT_BF16, MOE_DT_FP16 or MOE_DT_FP32: x, residual, gamma, sum, y
+ *  x         [T, H], row stride ldx; 1 <= H <= 32768
+ *  residual  [T, H], row stride ldr, or NULL (r = x)
+ *  gamma     [H], or NULL (ones)
+ *  eps       finite, >= 0
+ *  sum       [T, H] out, row stride lds: r (the next residual), or NULL
+ *  y         [T, H] out, row stride ldy, or NULL
+ *  q_dtype   MOE_DT_INT8 or MOE_DT_E4M3 (read only when q is given)
+ *  q_group   channels that share a scale: 0 (the row), 32, 64, 128 or 256
+ *  q         [T, H] out codes, or NULL
+ *  q_scale   fp32 [T, ceil(H / q_group)] out ([T] for q_group 0)
+ * One of sum, y, q is required.  sum and y may each be x or residual themselves
+ * (same pointer and stride), but not both the same. */
+moe_status moe_add_rmsnorm(int32_t T, int32_t H, int32_t dtype, const void* x, int64_t ldx,
+                           const void* residual, int64_t ldr, const void* gamma, float eps,
+                           void* sum, int64_t lds, void* y, int64_t ldy, int32_t q_dtype,
+                           int32_t q_group, void* q, float* q_scale, moe_stream_t stream);
+
+/* Tokens sorted by expert: the stable order of moe_permute ([DS-ASC] "2. MOE
+ * 算子优化", InitialRouting), for rows of any type and without a layer
+ * description, and with gradients.  A pick whose id lies outside [0, n_experts)
+ * is dropped (a masked slot, an expert held elsewhere): dropped picks take the
+ * positions after the kept ones, in pick order.  A token may pick one expert
+ * several times.
+ *  ids                 int32 [T, k]; k <= 32, n_experts <= 4096, T * k <= 2^30
+ *  counts              int32 [n_experts] out
+ *  offsets             int32 [n_experts + 1] out; offsets[n_experts] = kept picks
+ *  sorted_to_expanded  int32 [T*k] out: position -> pick t*k + j (a permutation)
+ *  expanded_to_sorted  int32 [T*k] out: its inverse
+ *  dtype               any moe_dtype: x and x_sorted
+ *  x                   [T, H], row stride ldx
+ *  x_sorted            [T*k, H] out: row p = x[sorted_to_expanded[p] / k] for
+ *                      p < offsets[n_experts]; NULL: only the order is wanted
+ *  x_scale             fp32 [T], rows' scales that go along, or NULL
+ *  scale_sorted        fp32 [T*k] out, or NULL
+ *  zero_dropped        1: the rows (and scales) of dropped picks are zeroed,
+ *                      0: they are not written
+ *  ws                  moe_sort_workspace_size bytes (NULL when that is 0),
+ *                      256-byte aligned; need not be initialised */
+moe_status moe_sort_workspace_size(int32_t T, int32_t k, int32_t n_experts, size_t* bytes);
+moe_status moe_sort_tokens(int32_t T, int32_t k, int32_t n_experts, int32_t H, int32_t dtype,
+                           const int32_t* ids, const void* x, int64_t ldx, const float* x_scale,
+                           int32_t* counts, int32_t* offsets, int32_t* sorted_to_expanded,
+                           int32_t* expanded_to_sorted, void* x_sorted, float* scale_sorted,
+                           int32_t zero_dropped, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Gradient of x through moe_sort_tokens:
+ *   dx[t] = sum over the kept picks j of dx_sorted[expanded_to_sorted[t*k + j]]
+ * added in slot order in fp32 (the same bits on every call), rounded once.
+ *  dtype      dx_sorted [T*k, H]: MOE_DT_BF16, MOE_DT_FP16 or MOE_DT_FP32
+ *  out_dtype  dx [T, H], row stride lddx: one of the same types
+ *  offsets, expanded_to_sorted  as written by moe_sort_tokens */
+moe_status moe_sort_tokens_backward(int32_t T, int32_t k, int32_t n_experts, int32_t H,
+                                    int32_t dtype, const void* dx_sorted, const int32_t* offsets,
+                                    const int32_t* expanded_to_sorted, int32_t out_dtype, void* dx,
+                                    int64_t lddx, moe_stream_t stream);
+
+/* Sorted rows back to their tokens, weights applied:
+ *   out[t] = sum over the kept picks j of topk_w[t, j] * y_sorted[expanded_to_sorted[t*k + j]]
+ * added in slot order in fp32, rounded once (zeros for a token without kept picks).
+ *  topk_w  fp32 [T, k]; types, strides and plan as above */
+moe_status moe_unsort_tokens(int32_t T, int32_t k, int32_t n_experts, int32_t H, int32_t dtype,
+                             const void* y_sorted, const int32_t* offsets,
+                             const int32_t* expanded_to_sorted, const float* topk_w,
+                             int32_t out_dtype, void* out, int64_t ldo, moe_stream_t stream);
+
+/* Gradients through moe_unsort_tokens, for each kept pick r = t*k + j at
+ * position p (products and sums in fp32, a fixed order):
+ *   dy_sorted[p] = topk_w[r] * dout[t];   dtopk_w[r] = sum_h dout[t, h] * y_sorted[p, h]
+ * A dropped pick has dtopk_w = 0, and its dy_sorted row is zeroed
+ * (zero_dropped = 1) or not written (0).
+ *  dout  [T, H] of out_dtype, row stride ldd; y_sorted, dy_sorted [T*k, H] of dtype */
+moe_status moe_unsort_tokens_backward(int32_t T, int32_t k, int32_t n_experts, int32_t H,
+                                      int32_t dtype, int32_t out_dtype, const void* dout,
+                                      int64_t ldd, const void* y_sorted, const int32_t* offsets,
+                                      const int32_t* expanded_to_sorted, const float* topk_w,
+                                      void* dy_sorted, float* dtopk_w, int32_t zero_dropped,
+                                      moe_stream_t stream);
+
 /* Synchronises `stream`, reads and clears the device status word in `ws`.
  * MOE_OK, MOE_ERR_DEVICE_CHECK or MOE_ERR_DEVICE_TIMEOUT (or MOE_ERR_CUDA). */
 moe_status moe_check_device_status(void* ws, moe_stream_t stream);
@@ -300,6 +400,12 @@ typedef enum {
   MOE_K_COMBINE,
   MOE_K_W8_EXACT,
   MOE_K_SORT,  /* small batches: count, scan, scatter and work list in one launch */
+  MOE_K_NORM,  /* moe_add_rmsnorm */
+  MOE_K_SORT_PLAN,   /* moe_sort_tokens: counting passes of large batches */
+  MOE_K_SORT_ROWS,   /* moe_sort_tokens: rows (small batches: positions too) */
+  MOE_K_UNSORT,      /* moe_unsort_tokens, moe_sort_tokens_backward */
+  MOE_K_UNSORT_GRAD, /* moe_unsort_tokens_backward */
+  MOE_K_W4,          /* moe_w4_gemv */
   MOE_K_COUNT
 } moe_kernel_kind;
 

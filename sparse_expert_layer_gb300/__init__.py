@@ -43,7 +43,7 @@ FFN_LAUNCH_DEFAULT, FFN_LAUNCH_TWO, FFN_LAUNCH_ONE, FFN_LAUNCH_ONE_WIDE = 0, 1, 
 
 KERNELS = ["router", "topk", "perm_count", "perm_scan", "perm_scatter", "perm_gather",
            "worklist", "gemv_gate_up", "gemv_down", "tc_gate_up", "tc_down", "quant_h", "combine",
-           "w8_exact", "sort"]
+           "w8_exact", "sort", "norm", "sort_plan", "sort_rows", "unsort", "unsort_grad", "w4"]
 N_KERNELS = len(KERNELS)
 
 
@@ -65,6 +65,8 @@ class MoeError(RuntimeError):
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_L = ctypes.c_int64
+_F = ctypes.c_float
 _C = ctypes.POINTER(MoeConfig)
 _SZ = ctypes.c_size_t
 
@@ -85,6 +87,14 @@ _SIGS = {
     "moe_tile_choice": [_C, _I, ctypes.POINTER(_I), ctypes.POINTER(_I)],
     "moe_qgemm_s8_workspace_size": [_I, _I, _I, _I, ctypes.POINTER(_SZ)],
     "moe_qgemm_s8": [_I, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P],
+    "moe_add_rmsnorm": [_I, _I, _I, _P, _L, _P, _L, _P, _F, _P, _L, _P, _L, _I, _I, _P, _P, _P],
+    "moe_sort_workspace_size": [_I, _I, _I, ctypes.POINTER(_SZ)],
+    "moe_sort_tokens": [_I, _I, _I, _I, _I, _P, _P, _L, _P, _P, _P, _P, _P, _P, _P, _I, _P, _SZ,
+                        _P],
+    "moe_sort_tokens_backward": [_I, _I, _I, _I, _I, _P, _P, _P, _I, _P, _L, _P],
+    "moe_unsort_tokens": [_I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _L, _P],
+    "moe_unsort_tokens_backward": [_I, _I, _I, _I, _I, _I, _P, _L, _P, _P, _P, _P, _P, _P, _I,
+                                   _P],
     "moe_selftest_wait_timeout": [_P, ctypes.c_int64, _P],
     "moe_timing_enable": [_I],
     "moe_timing_collect": [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(_I), _I],
@@ -96,6 +106,22 @@ for _name, _args in _SIGS.items():
     _f.restype = ctypes.c_int
 
 EXPORTS = sorted(list(_SIGS) + ["moe_status_string", "moe_kernel_name"])
+
+
+# Operators around the layer, bound in operators.py (loaded on first use, since
+# it needs torch at import).
+_OPERATORS = ("moe_add_rmsnorm", "moe_sort_workspace_size", "sort_workspace", "moe_sort_tokens",
+              "moe_sort_tokens_backward", "moe_unsort_tokens", "moe_unsort_tokens_backward")
+
+
+def __getattr__(name):
+    if name not in _OPERATORS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import operators
+
+    for n in _OPERATORS:
+        globals()[n] = getattr(operators, n)
+    return globals()[name]
 
 
 def _ptr(t):

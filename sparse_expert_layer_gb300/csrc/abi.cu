@@ -790,6 +790,15 @@ void set_smem_attr_once(const void* func, int bytes, int slot) {
 
 moe_status launch_status_take() { return finish(); }
 
+moe_status open_launch(moe_stream_t stream, Launch* L) {
+  const int d = current_device();
+  if (d < 0) return MOE_ERR_CUDA;
+  L->stream = reinterpret_cast<cudaStream_t>(stream);
+  L->num_sms = sm_count(d);
+  L->status = nullptr;
+  return MOE_OK;
+}
+
 void launch_note(cudaError_t e) {
   if (e != cudaSuccess && t_launch_error == cudaSuccess) t_launch_error = e;
 }
@@ -857,7 +866,7 @@ const char* moe_kernel_name(int32_t kind) {
   static const char* names[MOE_K_COUNT] = {
       "router", "topk", "perm_count", "perm_scan", "perm_scatter", "perm_gather", "worklist",
       "gemv_gate_up", "gemv_down", "tc_gate_up", "tc_down", "quant_h", "combine", "w8_exact",
-      "sort"};
+      "sort", "norm", "sort_plan", "sort_rows", "unsort", "unsort_grad", "w4"};
   return (kind >= 0 && kind < MOE_K_COUNT) ? names[kind] : "unknown";
 }
 

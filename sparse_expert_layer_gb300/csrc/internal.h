@@ -429,6 +429,15 @@ enum {
 };
 void set_smem_attr_once(const void* func, int bytes, int slot);
 
+// A launch context on `stream` for the entry points without a workspace (no
+// status word): MOE_OK, or MOE_ERR_CUDA without a usable device.
+moe_status open_launch(moe_stream_t stream, Launch* L);
+// Whether any of the given pointers (NULL passes) is not 16-byte aligned.
+template <typename... P>
+bool misaligned16(P... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & 15u) != 0;
+}
+
 // Per-launch bookkeeping (abi.cu): call before/after each kernel launch.
 void launch_begin(const Launch& L, int kind);
 void launch_end(const Launch& L, int kind);

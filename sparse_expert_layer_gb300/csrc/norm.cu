@@ -1,0 +1,277 @@
+// Residual addition, RMS norm and 8-bit codes in one pass over the rows.
+//
+//   r = x + residual;  y = r * rstd * gamma,  rstd = 1 / sqrt(mean(r^2) + eps)
+//   codes of y with one scale per row, or per group of channels.
+//
+// With v = r * gamma, |y| = rstd * |v|, so a row's (or group's) largest |y| is
+// rstd * max|v| and the code of y is the code of v against max|v|: rstd cancels.
+// The sum of squares and the largest |v| are therefore one reduction, the row
+// stays in registers between it and the stores, and nothing is read twice.
+// Sums, v and scales are fp32; the new residual, y and the codes are each
+// rounded once, from fp32 values.
+#include <math.h>
+
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "rows.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kNormMaxHidden = 32768;
+
+struct NormArgs {
+  const void* x;
+  const void* res;    // nullptr: none
+  const void* gamma;  // nullptr: ones
+  void* sum;          // nullptr: not wanted
+  void* y;            // nullptr: not wanted
+  void* q;            // nullptr: not wanted
+  float* scale;       // [T, groups]
+  int64_t ldx, ldr, lds, ldy;
+  int T, H, nslots;
+  int q_e4m3;         // codes are e4m3 instead of int8
+  int q_group;        // channels per scale, 0 = the row
+  int groups;
+  float eps;
+};
+
+// The factor from v to its code's value, `most` / amax, as pre * inv: where amax
+// is so small that most / amax overflows, v is scaled up by a power of two first.
+__device__ __forceinline__ void code_factor(float amax, float most, float* pre, float* inv) {
+  *pre = amax < 0x1p-96f ? 0x1p64f : 1.f;
+  const float a = amax * *pre;
+  *inv = a > 0.f ? most / a : 0.f;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_codes(const NormArgs& a, size_t at, int n,
+                                            const float (&v)[kSlot], float pre, float inv) {
+  uint32_t w[2];
+  if (a.q_e4m3) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+          make_float2(v[4 * i] * pre * inv, v[4 * i + 1] * pre * inv), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+          make_float2(v[4 * i + 2] * pre * inv, v[4 * i + 3] * pre * inv), __NV_SATFINITE,
+          __NV_E4M3);
+      w[i] = (lo & 0xffffu) | (hi << 16);
+    }
+  } else {
+    // |v * inv| is at most 127 + rounding, so rounding to nearest needs no clamp;
+    // a row with a NaN or infinity has a NaN scale, whatever its codes
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t u = 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        u |= (uint32_t)(__float2int_rn(v[4 * i + j] * pre * inv) & 0xff) << (8 * j);
+      w[i] = u;
+    }
+  }
+  uint8_t* q = static_cast<uint8_t*>(a.q) + at;
+  if constexpr (VEC) {
+    *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kSlot; ++i)
+      if (i < n) q[i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+  }
+}
+
+// blockDim.x threads work on one row, blockDim.y rows at a time; slot i of a
+// row belongs to thread i % blockDim.x.
+template <typename T, int VPT, bool VEC, int MAXT>
+__global__ void __launch_bounds__(MAXT) add_rmsnorm_kernel(NormArgs a) {
+  pdl_enter();
+  __shared__ float2 part[2][32];  // per warp: sum of squares, largest |v|; two rows alternate
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int nwarps = blockDim.x / 32;
+  const float most = a.q_e4m3 ? 448.f : 127.f;
+  int turn = 0;
+  for (int t = blockIdx.x * blockDim.y + threadIdx.y; t < a.T; t += gridDim.x * blockDim.y) {
+    const T* x = static_cast<const T*>(a.x) + (int64_t)t * a.ldx;
+    const T* res = static_cast<const T*>(a.res) + (int64_t)t * a.ldr;
+    Raw8<T> rx[VPT], rr[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int s = threadIdx.x + i * blockDim.x, n = min(kSlot, a.H - s * kSlot);
+      if (s < a.nslots) {
+        rx[i] = load_raw8<T, VEC>(x + s * kSlot, n);
+        if (a.res) rr[i] = load_raw8<T, VEC>(res + s * kSlot, n);
+      }
+    }
+    float v[VPT][kSlot];
+    float ss = 0.f, amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int s = threadIdx.x + i * blockDim.x, n = min(kSlot, a.H - s * kSlot);
+#pragma unroll
+      for (int j = 0; j < kSlot; ++j) v[i][j] = 0.f;
+      if (s < a.nslots) {
+        unpack8<T>(rx[i], v[i]);
+        if (a.res) {
+          float r[kSlot];
+          unpack8<T>(rr[i], r);
+#pragma unroll
+          for (int j = 0; j < kSlot; ++j) v[i][j] += r[j];
+        }
+        if (a.sum)
+          store8<T, VEC>(static_cast<T*>(a.sum) + (int64_t)t * a.lds + s * kSlot, n, v[i]);
+#pragma unroll
+        for (int j = 0; j < kSlot; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+        if (a.gamma) {
+          float g[kSlot];
+          load8<T, VEC>(static_cast<const T*>(a.gamma) + s * kSlot, n, g);
+#pragma unroll
+          for (int j = 0; j < kSlot; ++j) v[i][j] *= g[j];
+        }
+#pragma unroll
+        for (int j = 0; j < kSlot; ++j) amax = fmaxf(amax, fabsf(v[i][j]));
+      }
+    }
+    ss = warp_sum(ss);
+    amax = warp_max(amax);
+    if (nwarps > 1) {
+      if (lane == 0) part[turn][warp] = make_float2(ss, amax);
+      __syncthreads();
+      // every warp adds the warps' parts in the same order
+      const float2 p = lane < nwarps ? part[turn][lane] : make_float2(0.f, 0.f);
+      ss = warp_sum(p.x);
+      amax = warp_max(p.y);
+      turn ^= 1;  // the next row's parts go elsewhere, so one barrier a row is enough
+    }
+    const float rstd = 1.f / sqrtf(ss / (float)a.H + a.eps);
+    float pre = 1.f, inv = 0.f;
+    if (a.q && a.q_group == 0) {
+      code_factor(amax, most, &pre, &inv);
+      if (threadIdx.x == 0) a.scale[t] = rstd * amax / most;
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int s = threadIdx.x + i * blockDim.x, n = min(kSlot, a.H - s * kSlot);
+      if (a.q && a.q_group > 0) {
+        // a group's slots lie in consecutive lanes of one warp (slots past the
+        // row hold zeros)
+        const int lanes = a.q_group / kSlot;
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < kSlot; ++j) m = fmaxf(m, fabsf(v[i][j]));
+        for (int o = lanes / 2; o > 0; o >>= 1)
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        code_factor(m, most, &pre, &inv);
+        if (s < a.nslots && lane % lanes == 0)
+          a.scale[(size_t)t * a.groups + s / lanes] = rstd * m / most;
+      }
+      if (s < a.nslots) {
+        if (a.q) store_codes<VEC>(a, (size_t)t * a.H + (size_t)s * kSlot, n, v[i], pre, inv);
+        if (a.y) {
+          float o[kSlot];
+#pragma unroll
+          for (int j = 0; j < kSlot; ++j) o[j] = v[i][j] * rstd;
+          store8<T, VEC>(static_cast<T*>(a.y) + (int64_t)t * a.ldy + s * kSlot, n, o);
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int VPT, bool VEC, int MAXT>
+void launch_as(const Launch& L, const NormArgs& a, int threads, int rows) {
+  // a few CTAs' worth of threads on every SM; each goes on to further rows
+  const int per_sm = std::max(1, 2048 / (threads * rows));
+  const int grid = (int)std::min<int64_t>(((int64_t)a.T + rows - 1) / rows,
+                                          (int64_t)L.num_sms * per_sm);
+  launch_begin(L, MOE_K_NORM);
+  launch_kernel(add_rmsnorm_kernel<T, VPT, VEC, MAXT>, grid, dim3(threads, rows), 0, L.stream, a);
+  launch_end(L, MOE_K_NORM);
+}
+
+template <typename T, bool VEC>
+void launch_norm(const Launch& L, const NormArgs& a) {
+  const int slots32 = (a.nslots + 31) / 32;  // warps at one slot a thread
+  if (slots32 <= 4 && a.T > L.num_sms) {
+    // short rows of a large batch: a warp holds a row, four rows a CTA
+    launch_as<T, 4, VEC, 128>(L, a, 32, 4);
+  } else if (slots32 <= 32 && a.T <= L.num_sms) {
+    // few rows: one slot a thread, the shortest chain from load to store
+    launch_as<T, 1, VEC, 1024>(L, a, 32 * slots32, 1);
+  } else if (slots32 <= 32) {
+    launch_as<T, 2, VEC, 512>(L, a, 32 * ((slots32 + 1) / 2), 1);
+  } else if (slots32 <= 64) {
+    launch_as<T, 4, VEC, 512>(L, a, 32 * ((slots32 + 3) / 4), 1);
+  } else {
+    launch_as<T, 4, VEC, 1024>(L, a, 32 * ((slots32 + 3) / 4), 1);
+  }
+}
+
+template <typename T>
+void launch_norm(const Launch& L, const NormArgs& a, bool vec) {
+  if (vec)
+    launch_norm<T, true>(L, a);
+  else
+    launch_norm<T, false>(L, a);
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_add_rmsnorm(int32_t T, int32_t H, int32_t dtype, const void* x,
+                                      int64_t ldx, const void* residual, int64_t ldr,
+                                      const void* gamma, float eps, void* sum, int64_t lds,
+                                      void* y, int64_t ldy, int32_t q_dtype, int32_t q_group,
+                                      void* q, float* q_scale, moe_stream_t stream) {
+  if (T < 0 || H < 1 || !(eps >= 0.f) || !isfinite(eps)) return MOE_ERR_INVALID_ARG;
+  if (dtype < MOE_DT_BF16 || dtype > MOE_DT_FP32) return MOE_ERR_INVALID_ARG;
+  if (q && q_dtype != MOE_DT_INT8 && q_dtype != MOE_DT_E4M3) return MOE_ERR_INVALID_ARG;
+  if (q && q_group != 0 && q_group != 32 && q_group != 64 && q_group != 128 && q_group != 256)
+    return MOE_ERR_INVALID_ARG;
+  if (!sum && !y && !q) return MOE_ERR_INVALID_ARG;
+  if (H > kNormMaxHidden) return MOE_ERR_UNSUPPORTED;
+  if (ldx < H || (residual && ldr < H) || (sum && lds < H) || (y && ldy < H))
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || (q && !q_scale)) return MOE_ERR_INVALID_ARG;
+  if (misaligned16(x, residual, gamma, sum, y, q, q ? q_scale : nullptr)) return MOE_ERR_ALIGNMENT;
+  const int es = dtype == MOE_DT_FP32 ? 4 : 2;
+  NormArgs a{};
+  a.x = x;
+  a.res = residual;
+  a.gamma = gamma;
+  a.sum = sum;
+  a.y = y;
+  a.q = q;
+  a.scale = q_scale;
+  a.ldx = ldx;
+  a.ldr = ldr;
+  a.lds = lds;
+  a.ldy = ldy;
+  a.T = T;
+  a.H = H;
+  a.nslots = (H + kSlot - 1) / kSlot;
+  a.q_e4m3 = q_dtype == MOE_DT_E4M3;
+  a.q_group = q_group;
+  a.groups = q_group > 0 ? (H + q_group - 1) / q_group : 1;
+  a.eps = eps;
+  // whole slots at 16-byte aligned addresses in every row
+  auto whole = [&](const void* p, int64_t ld) { return !p || T == 1 || ld * es % 16 == 0; };
+  const bool vec = H % kSlot == 0 && whole(x, ldx) && whole(residual, ldr) && whole(sum, lds) &&
+                   whole(y, ldy);
+  Launch L;
+  moe_status s = open_launch(stream, &L);
+  if (s != MOE_OK) return s;
+  if (dtype == MOE_DT_BF16)
+    launch_norm<__nv_bfloat16>(L, a, vec);
+  else if (dtype == MOE_DT_FP16)
+    launch_norm<__half>(L, a, vec);
+  else
+    launch_norm<float>(L, a, vec);
+  return launch_status_take();
+}
