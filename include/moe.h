@@ -369,6 +369,33 @@ moe_status moe_unsort_tokens_backward(int32_t T, int32_t k, int32_t n_experts, i
                                       void* dy_sorted, float* dtopk_w, int32_t zero_dropped,
                                       moe_stream_t stream);
 
+/* Matrix-vector products with 4-bit weights and group scales, for the few rows
+ * an expert has in decode ([PANGU] SwiftGMM: expert weight movement is the
+ * bottleneck):
+ *   out[r, n] = sum_k (q[e, n, k] - z[e, n, k / group]) * s[e, n, k / group] * x[r, k]
+ * for the rows offsets[e] <= r < offsets[e+1] of each expert e (other rows of
+ * out are not written); with w_up, out = silu(first) * second (SwiGLU).  Codes
+ * times x and their sums over a group are exact products added in fp32; scales
+ * are applied in fp32; out is rounded once.  Any number of rows is taken; an
+ * expert's weights are read once for every 8 rows (16 where R > 8 * n_experts).
+ *  K            a multiple of 32 and of group
+ *  group        channels that share a scale: 32, 64, 128, or 0 (one scale a row)
+ *  offsets      int32 [n_experts + 1], device; NULL: one expert, all R rows
+ *  x_dtype      MOE_DT_BF16, MOE_DT_FP16, or MOE_DT_INT8 (codes, with x_scale)
+ *  x            [R, K]; x_scale fp32 [R] for int8 rows, else NULL
+ *  w, w_up      uint8 [n_experts, N, K / 2]: channel k in the low (even k) or
+ *               high (odd k) nibble of byte k / 2, codes 0 .. 15; w_up may be NULL
+ *  scale_dtype  MOE_DT_BF16, MOE_DT_FP16 or MOE_DT_FP32
+ *  scales       [n_experts, N, K / group]; scales_up with w_up
+ *  zeros        uint8 [n_experts, N, K / group], 0 .. 31 (the low five bits are
+ *               taken), or NULL: 8; zeros_up given exactly when zeros and w_up are
+ *  out_dtype    MOE_DT_BF16, MOE_DT_FP16 or MOE_DT_FP32: out [R, N] */
+moe_status moe_w4_gemv(int32_t n_experts, int32_t N, int32_t K, int32_t group, int32_t R,
+                       const int32_t* offsets, int32_t x_dtype, const void* x,
+                       const float* x_scale, const void* w, const void* w_up, int32_t scale_dtype,
+                       const void* scales, const void* scales_up, const uint8_t* zeros,
+                       const uint8_t* zeros_up, int32_t out_dtype, void* out, moe_stream_t stream);
+
 /* Synchronises `stream`, reads and clears the device status word in `ws`.
  * MOE_OK, MOE_ERR_DEVICE_CHECK or MOE_ERR_DEVICE_TIMEOUT (or MOE_ERR_CUDA). */
 moe_status moe_check_device_status(void* ws, moe_stream_t stream);

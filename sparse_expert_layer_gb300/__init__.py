@@ -95,6 +95,7 @@ _SIGS = {
     "moe_unsort_tokens": [_I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _L, _P],
     "moe_unsort_tokens_backward": [_I, _I, _I, _I, _I, _I, _P, _L, _P, _P, _P, _P, _P, _P, _I,
                                    _P],
+    "moe_w4_gemv": [_I, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _P, _P],
     "moe_selftest_wait_timeout": [_P, ctypes.c_int64, _P],
     "moe_timing_enable": [_I],
     "moe_timing_collect": [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(_I), _I],
@@ -111,7 +112,8 @@ EXPORTS = sorted(list(_SIGS) + ["moe_status_string", "moe_kernel_name"])
 # Operators around the layer, bound in operators.py (loaded on first use, since
 # it needs torch at import).
 _OPERATORS = ("moe_add_rmsnorm", "moe_sort_workspace_size", "sort_workspace", "moe_sort_tokens",
-              "moe_sort_tokens_backward", "moe_unsort_tokens", "moe_unsort_tokens_backward")
+              "moe_sort_tokens_backward", "moe_unsort_tokens", "moe_unsort_tokens_backward",
+              "moe_w4_gemv", "pack_w4")
 
 
 def __getattr__(name):

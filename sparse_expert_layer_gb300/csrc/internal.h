@@ -425,7 +425,9 @@ enum {
   kAttrSortSmall,
   kAttrTcFfn,
   kAttrRouteSmall,
-  kAttrSlots
+  kAttrW4Base,                   // x type x row blocks x group x zero points
+  kAttrW4Slots = 3 * 2 * 3 * 2,
+  kAttrSlots = kAttrW4Base + kAttrW4Slots
 };
 void set_smem_attr_once(const void* func, int bytes, int slot);
 

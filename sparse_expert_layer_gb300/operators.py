@@ -187,3 +187,44 @@ def moe_unsort_tokens_backward(dout, y_sorted, offsets, expanded_to_sorted, topk
                                           DTYPES[dout.dtype], pd, ld, py, po, p2, pw, pg, pdw,
                                           int(zero_dropped), _stream(stream)),
            "moe_unsort_tokens_backward")
+
+
+def pack_w4(codes):
+    """uint8 codes 0 .. 15 [..., K] (K even) as moe_w4_gemv takes them, two a byte."""
+    return (codes[..., 0::2] | (codes[..., 1::2] << 4)).contiguous()
+
+
+def moe_w4_gemv(x, x_scale, offsets, w, scales, zeros, out, w_up=None, scales_up=None,
+                zeros_up=None, stream=None):
+    """out[r] = (codes - zeros) * scales @ x[r] with the weights of row r's expert;
+    with w_up, silu(first) * second.
+
+    x [R, K] bf16, fp16 or int8 (with x_scale [R] fp32); offsets int32 [E + 1] or
+    None (one expert); w, w_up uint8 [E, N, K / 2]; scales [E, N, groups] bf16,
+    fp16 or fp32; zeros uint8 of their shape or None (8); out [R, N].
+    """
+    R, K = _matrix_shape(x, "x")
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise TypeError("w: expected [experts, N, K / 2]")
+    E, N, _ = w.shape
+    px = _tensor(x, "x", (torch.bfloat16, torch.float16, torch.int8), (R, K))
+    pw = _tensor(w, "w", torch.uint8, (E, N, K // 2), x)
+    if not isinstance(scales, torch.Tensor) or scales.dim() != 3:
+        raise TypeError("scales: expected [experts, N, groups]")
+    G = scales.shape[2]
+    if G < 1 or K % G:
+        raise ValueError(f"scales: {G} groups do not divide K = {K}")
+    ps = _tensor(scales, "scales", _FLOATS, (E, N, G), x)
+    pxs = None if x_scale is None else _tensor(x_scale, "x_scale", torch.float32,
+                                               tuple(x_scale.shape), x)
+    if pxs is not None and x_scale.numel() != R:
+        raise ValueError(f"x_scale: expected {R} values")
+    pof = None if offsets is None else _tensor(offsets, "offsets", torch.int32, (E + 1,), x)
+    pz = None if zeros is None else _tensor(zeros, "zeros", torch.uint8, (E, N, G), x)
+    pwu = None if w_up is None else _tensor(w_up, "w_up", torch.uint8, (E, N, K // 2), x)
+    psu = None if scales_up is None else _tensor(scales_up, "scales_up", scales.dtype, (E, N, G), x)
+    pzu = None if zeros_up is None else _tensor(zeros_up, "zeros_up", torch.uint8, (E, N, G), x)
+    po = _tensor(out, "out", _FLOATS, (R, N), x)
+    _check(lib.moe_w4_gemv(E, N, K, K // G if G > 1 else 0, R, pof, DTYPES[x.dtype], px, pxs, pw,
+                           pwu, DTYPES[scales.dtype], ps, psu, pz, pzu, DTYPES[out.dtype], po,
+                           _stream(stream)), "moe_w4_gemv")

@@ -517,3 +517,171 @@ def test_side_stream_and_graph_replay(m):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(results, want))
+
+
+# ---------------------------------------------------------------- 4 bits ----
+INT8 = torch.int8
+
+
+def w4_case(g, E, R, N, K, group, xdt, sdt, up, zeros, rows=None):
+    G = K // group if group else 1
+    t = dict(up=up, group=group or K)
+    t["x_scale"] = None
+    if xdt == INT8:
+        t["x"] = torch.randint(-127, 128, (R, K), generator=g, device="cuda", dtype=INT8)
+        t["x_scale"] = 0.01 + torch.rand(R, generator=g, device="cuda")
+    else:
+        t["x"] = randn(g, R, K, dtype=xdt)
+    for n in ("", "_up")[:2 if up else 1]:
+        t["codes" + n] = torch.randint(0, 16, (E, N, K), generator=g, device="cuda",
+                                       dtype=torch.uint8)
+        t["scales" + n] = ((0.5 + torch.rand(E, N, G, generator=g, device="cuda")) / K**0.5).to(sdt)
+        t["zeros" + n] = torch.randint(0, 17, (E, N, G), generator=g, device="cuda",
+                                       dtype=torch.uint8) if zeros else None
+    if rows is None:
+        cut = torch.sort(torch.randint(0, R + 1, (E - 1,), generator=g, device="cuda")).values
+        rows = [0] + cut.tolist() + [R]
+    t["bounds"] = rows
+    t["offsets"] = torch.tensor(rows, dtype=torch.int32, device="cuda")
+    return t
+
+
+def w4_exact(t, e, n=""):
+    q = t["codes" + n][e].double()
+    z = t["zeros" + n]
+    q = q - (8 if z is None else z[e].double().repeat_interleave(t["group"], 1))
+    q = q * t["scales" + n][e].double().repeat_interleave(t["group"], 1)
+    a, b = t["bounds"][e], t["bounds"][e + 1]
+    x = t["x"][a:b].double()
+    if t["x_scale"] is not None:
+        x = x * t["x_scale"][a:b, None].double()
+    return x @ q.T, x.abs() @ q.abs().T
+
+
+def run_w4(m, t, out_dtype, offsets="given", fill=7.0):
+    R, N = t["x"].shape[0], t["codes"].shape[1]
+    out = torch.full((R, N), fill, device="cuda", dtype=out_dtype)
+    up = [None] * 3
+    if t["up"]:
+        up = [m.pack_w4(t["codes_up"]), t["scales_up"], t["zeros_up"]]
+    m.moe_w4_gemv(t["x"], t["x_scale"], t["offsets"] if offsets == "given" else offsets,
+                  m.pack_w4(t["codes"]), t["scales"], t["zeros"], out, *up)
+    torch.cuda.synchronize()
+    return out
+
+
+def check_w4(m, t, out_dtype, offsets="given"):
+    out = run_w4(m, t, out_dtype, offsets)
+    K = t["x"].shape[1]
+    # products are exact; a sum of at most 128 of them is 8 MMA steps that may
+    # each lose a step of 2^-23 per term, then one fp32 addition a group, the K
+    # parts, the scales and the row scale
+    rel = (8 * 17 + K // 32 + 20) * 2.0**-23
+    for e in range(len(t["bounds"]) - 1):
+        a, b = t["bounds"][e], t["bounds"][e + 1]
+        if a == b:
+            continue
+        y, mag = w4_exact(t, e)
+        tol = rel * mag
+        if t["up"]:
+            u, umag = w4_exact(t, e, "_up")
+            silu = y * torch.sigmoid(y)
+            # |d silu / dy| <= 1.1
+            tol = 1.1 * tol * (u.abs() + rel * umag) + silu.abs() * rel * umag \
+                + 8 * U * (silu * u).abs()
+            y = silu * u
+        within(out[a:b], y, half_step(y, out_dtype) * (1 + rel) + tol, f"expert {e}")
+    covered = t["bounds"][-1]
+    assert (out[covered:] == 7).all()
+
+
+@pytest.mark.parametrize("xdt", [BF16, FP16, INT8])
+@pytest.mark.parametrize("group", [32, 64, 128, 0])
+@pytest.mark.parametrize("up,zeros", [(False, False), (True, False), (False, True), (True, True)])
+def test_w4_types_and_groups(m, xdt, group, up, zeros):
+    g = gen(group + 2 * up + zeros)
+    t = w4_case(g, 3, 21, 200, 640, group, xdt, FP32 if xdt == INT8 else xdt, up, zeros)
+    check_w4(m, t, FP32)
+    check_w4(m, t, BF16)
+
+
+@pytest.mark.parametrize("E,R,N,K,group", [
+    (1, 1, 1, 32, 32), (1, 1, 16, 64, 64), (1, 8, 127, 96, 0), (1, 9, 129, 160, 32),
+    (1, 16, 64, 2048, 128), (1, 17, 65, 2080, 32), (1, 40, 130, 1056, 0), (1, 1, 7168, 2048, 128),
+    (1, 3, 33, 16384, 128), (1, 2, 500, 7200, 32), (4, 5, 256, 512, 64), (16, 37, 1000, 1024, 32),
+    (64, 9, 96, 256, 128), (2, 100, 300, 544, 32), (5, 64, 72, 4096, 64)])
+@pytest.mark.parametrize("xdt,up", [(BF16, False), (INT8, True)])
+def test_w4_shapes(m, E, R, N, K, group, xdt, up):
+    g = gen(E + R + N + K)
+    check_w4(m, w4_case(g, E, R, N, K, group, xdt, BF16, up, False), FP32)
+
+
+@pytest.mark.parametrize("sdt", [BF16, FP16, FP32])
+@pytest.mark.parametrize("out_dtype", [BF16, FP16, FP32])
+def test_w4_scale_and_output_types(m, sdt, out_dtype):
+    check_w4(m, w4_case(gen(1), 2, 12, 136, 384, 128, FP16, sdt, True, True), out_dtype)
+
+
+@pytest.mark.parametrize("rows", [[0, 0, 0, 5, 5], [0, 5, 5, 5, 5], [0, 1, 2, 3, 4],
+                                  [0, 0, 40, 40, 41], [0, 0, 0, 0, 0], [0, 8, 16, 24, 30]])
+def test_w4_loads(m, rows):
+    # empty experts, one expert with everything, rows that no expert owns
+    check_w4(m, w4_case(gen(3), 4, 41, 150, 256, 64, BF16, BF16, False, False, rows), BF16)
+
+
+def test_w4_one_expert_without_offsets(m):
+    t = w4_case(gen(4), 1, 6, 100, 512, 32, FP16, FP16, True, False)
+    check_w4(m, t, FP32, offsets=None)
+
+
+def test_w4_offsets_that_are_not_a_plan_stay_inside(m):
+    t = w4_case(gen(5), 3, 10, 64, 128, 32, BF16, BF16, False, False)
+    bad = torch.tensor([-5, 4, 10**9, 2], dtype=torch.int32, device="cuda")
+    run_w4(m, t, BF16, bad)  # rows 0-3, 4-9 and none: nothing outside is touched
+    out = run_w4(m, t, BF16, torch.full((4,), 99, dtype=torch.int32, device="cuda"))
+    assert (out == 7).all()
+
+
+def test_w4_rows_do_not_mix(m):
+    t = w4_case(gen(6), 2, 11, 96, 256, 64, BF16, BF16, False, False, [0, 7, 11])
+    clean = run_w4(m, t, FP32)
+    t["x"][2, 5] = float("nan")
+    t["x"][9, 0] = float("inf")
+    got = run_w4(m, t, FP32)
+    rest = [r for r in range(11) if r not in (2, 9)]
+    assert torch.equal(got[rest], clean[rest])
+    assert torch.isnan(got[2]).all() and not torch.isfinite(got[9]).all()
+
+
+def test_w4_same_bits_every_call_and_graph_replay(m):
+    t = w4_case(gen(7), 8, 24, 512, 2048, 128, BF16, BF16, True, False)
+    first = run_w4(m, t, FP32)
+    for _ in range(3):
+        assert torch.equal(run_w4(m, t, FP32), first)
+    w, wu = m.pack_w4(t["codes"]), m.pack_w4(t["codes_up"])
+    out = torch.zeros_like(first)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.moe_w4_gemv(t["x"], None, t["offsets"], w, t["scales"], None, out, wu, t["scales_up"])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first)
+
+
+def test_w4_weights_past_32_bits(m):
+    # 2.4e9 bytes of codes: the last experts lie beyond 2^31
+    E, N, K = 320, 2048, 7168
+    g = gen(8)
+    w = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.full((E, N, 1), 0.01, device="cuda", dtype=BF16)
+    x = randn(g, 2, K, dtype=BF16)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[E - 1:] = torch.tensor([1, 2], dtype=torch.int32)
+    out = torch.empty(2, N, device="cuda")
+    m.moe_w4_gemv(x, None, off, w, s, None, out)
+    torch.cuda.synchronize()
+    for r, e in ((0, E - 2), (1, E - 1)):
+        q = torch.stack([w[e] & 15, w[e] >> 4], -1).view(N, K).double() - 8
+        q *= float(s[0, 0, 0])
+        rel = (8 * 17 + K // 32 + 20) * 2.0**-23
+        within(out[r], q @ x[r].double(), rel * (q.abs() @ x[r].abs().double()) + TINY[FP32])

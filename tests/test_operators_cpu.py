@@ -115,6 +115,41 @@ def test_unsort_backward_refusals(moe, kw, status):
     assert grad(moe, **kw) == status
 
 
+def w4(moe, **kw):
+    a = dict(E=2, N=64, K=128, group=32, R=4, offsets=FAKE, x_dtype=BF16, x=FAKE, x_scale=None,
+             w=FAKE, w_up=None, scale_dtype=BF16, scales=FAKE, scales_up=None, zeros=None,
+             zeros_up=None, out_dtype=BF16, out=FAKE)
+    a.update(kw)
+    return moe.lib.moe_w4_gemv(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(E=0), INVALID), (dict(N=0), INVALID), (dict(K=0), INVALID), (dict(K=48), INVALID),
+    (dict(R=-1), INVALID), (dict(group=16), INVALID), (dict(group=256), INVALID),
+    (dict(group=128, K=160), INVALID), (dict(x_dtype=FP32), INVALID), (dict(x_dtype=E4M3), INVALID),
+    (dict(scale_dtype=INT8), INVALID), (dict(out_dtype=INT8), INVALID),
+    (dict(offsets=None), INVALID), (dict(w_up=FAKE), INVALID), (dict(scales_up=FAKE), INVALID),
+    (dict(zeros_up=FAKE), INVALID), (dict(w_up=FAKE, scales_up=FAKE, zeros=FAKE), INVALID),
+    (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(scales=None), INVALID),
+    (dict(out=None), INVALID), (dict(x_scale=FAKE), INVALID), (dict(x_dtype=INT8), INVALID),
+    (dict(E=4097), UNSUPPORTED), (dict(N=1 << 23), UNSUPPORTED), (dict(w=FAKE + 8), ALIGNMENT),
+    (dict(x=FAKE + 2), ALIGNMENT), (dict(zeros=FAKE + 1), ALIGNMENT), (dict(out=FAKE + 4), ALIGNMENT),
+])
+def test_w4_refusals(moe, kw, status):
+    assert w4(moe, **kw) == status
+
+
+def test_w4_without_rows_is_a_no_op(moe):
+    assert w4(moe, R=0, x=None, w=None, scales=None, out=None) == 0
+
+
+def test_pack_w4(moe):
+    codes = torch.randint(0, 16, (2, 3, 64), dtype=torch.uint8)
+    packed = moe.pack_w4(codes)
+    assert packed.shape == (2, 3, 32)
+    assert torch.equal(packed & 15, codes[..., 0::2]) and torch.equal(packed >> 4, codes[..., 1::2])
+
+
 def test_empty_batches_are_no_ops(moe):
     assert back(moe, T=0, rows=None, offsets=None, e2s=None, out=None) == 0
     assert grad(moe, T=0, dout=None, rows=None, offsets=None, e2s=None, w=None, drows=None,
