@@ -425,8 +425,8 @@ enum {
   kAttrSortSmall,
   kAttrTcFfn,
   kAttrRouteSmall,
-  kAttrW4Base,                   // x type x row blocks x group x zero points
-  kAttrW4Slots = 3 * 2 * 3 * 2,
+  kAttrW4Base,                   // x type x group x zero points
+  kAttrW4Slots = 3 * 3 * 2,
   kAttrSlots = kAttrW4Base + kAttrW4Slots
 };
 void set_smem_attr_once(const void* func, int bytes, int slot);

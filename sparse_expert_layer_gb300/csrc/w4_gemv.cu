@@ -34,9 +34,10 @@ constexpr int kW4Threads = 32 * kW4Warps;
 constexpr int kW4Rows = 128;               // weight rows of a CTA
 constexpr int kW4Panel = 512;              // K of a panel of x and scales
 constexpr int kW4Stage = 128;              // K of a ring stage
-constexpr int kW4Stages = 4;
-constexpr int kW4RowBytes = kW4Stage / 2 + 16;  // padded: ldmatrix rows fall in distinct banks
+constexpr int kW4MaxRows = 16;              // token rows of one pass over the weights
+constexpr int kW4RowBytes = kW4Stage / 2;  // 64: four 16-byte pieces, swizzled
 constexpr int kW4StageBytes = 32 * kW4RowBytes;
+constexpr int kW4XStride = kW4Panel * 2 + 64;  // token rows 64 bytes apart modulo the banks
 constexpr int kW4RedStride = kW4Rows + 4;
 constexpr int kW4MaxSplit = 8;
 
@@ -52,12 +53,28 @@ struct W4Args {
   int channels;   // channels of a CTA: 128, or 64 with a second matrix
   int up;
   int scale_dtype, out_dtype;
+  // shared memory of the scales and zero points of a panel: bytes between rows,
+  // and the copy unit (a power of two of at least 4 bytes)
+  int sstride, zstride, sunit, zunit;
+  int64_t sbytes, zbytes;  // of the whole tensors
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
-  const int n = real ? 16 : 0;  // 0: the 16 bytes become zeros, src is not read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// real false: the 16 bytes become zeros, src is not read
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
                : "memory");
+}
+__device__ __forceinline__ void cp_async_unit(uint32_t dst, const void* src, int bytes) {
+  if (bytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else if (bytes == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -107,19 +124,45 @@ struct MmaFp16 {
   }
 };
 
-// The x types: bytes of a channel, the MMA type, and a thread's eight channels
-// k0 .. k7 of one row as the four words (k0,k4) (k1,k5) (k2,k6) (k3,k7), the
-// order in which the nibbles of a weight word pair up.
+__device__ __forceinline__ float lds_f32(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint16_t lds_u16(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// The x types: bytes of a channel, the MMA type, where 16-byte piece i of token
+// row r lies in a panel, and a thread's operands of one 32-wide step: its eight
+// channels k0 .. k7 as the words (k0,k4) (k1,k5) (k2,k6) (k3,k7), the order in
+// which the nibbles of a weight word pair up.
 struct XBf16 {
   using Mma = MmaBf16;
   static constexpr int kBytes = 2;
-  static constexpr int kStride = kW4Panel * 2 + 64;  // rows 64 bytes apart modulo the banks
-  static __device__ __forceinline__ void pairs(const unsigned char* p, uint32_t (&b)[4]) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    b[0] = __byte_perm(v.x, v.z, 0x5410);
-    b[1] = __byte_perm(v.x, v.z, 0x7632);
-    b[2] = __byte_perm(v.y, v.w, 0x5410);
-    b[3] = __byte_perm(v.y, v.w, 0x7632);
+  static constexpr int kRow = kW4Panel * 2;
+  // every second row has its 64-byte halves swapped: two rows cover the banks
+  static __device__ __forceinline__ uint32_t piece(int r, int i) {
+    return r * kRow + ((i ^ ((r & 1) * 4)) * 16);
+  }
+  static __device__ __forceinline__ void operands(uint32_t panel, int r, int c, int step,
+                                                  uint32_t (&b)[4]) {
+    uint32_t x, y, z, w;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x), "=r"(y), "=r"(z), "=r"(w)
+                 : "r"(panel + piece(r, step * 4 + c))
+                 : "memory");
+    b[0] = __byte_perm(x, z, 0x5410);
+    b[1] = __byte_perm(x, z, 0x7632);
+    b[2] = __byte_perm(y, w, 0x5410);
+    b[3] = __byte_perm(y, w, 0x7632);
   }
 };
 struct XFp16 : XBf16 {
@@ -130,10 +173,17 @@ struct XFp16 : XBf16 {
 struct XInt8 {
   using Mma = MmaFp16;
   static constexpr int kBytes = 1;
-  static constexpr int kStride = kW4Panel + 32;
-  static __device__ __forceinline__ void pairs(const unsigned char* p, uint32_t (&b)[4]) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    const uint32_t lo = v.x ^ 0x80808080u, hi = v.y ^ 0x80808080u;
+  static constexpr int kRow = kW4Panel + 32;  // four rows cover the banks
+  static __device__ __forceinline__ uint32_t piece(int r, int i) { return r * kRow + i * 16; }
+  static __device__ __forceinline__ void operands(uint32_t panel, int r, int c, int step,
+                                                  uint32_t (&b)[4]) {
+    uint32_t lo, hi;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                 : "=r"(lo), "=r"(hi)
+                 : "r"(panel + r * kRow + step * 32 + c * 8)
+                 : "memory");
+    lo ^= 0x80808080u;
+    hi ^= 0x80808080u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       // bytes (k_i, k_{i+4}) into the low bytes of two halves under 0x64
@@ -147,311 +197,427 @@ struct XInt8 {
 // (q(k_i) - z, q(k_{i+4}) - z) in 16 bits each, exact.
 template <typename M>
 __device__ __forceinline__ uint32_t dequant_pair(uint32_t w, int i, uint32_t zero) {
-  const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | M::kMagic;
+  // (shifted & mask) | magic in one instruction; the compiler alone makes it two
+  uint32_t v;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;"
+      : "=r"(v)
+      : "r"(w >> (4 * i)), "r"(0x000f000fu), "r"(M::kMagic));
   return M::sub(v, zero);
 }
 
-__device__ __forceinline__ float load_scale(const void* s, int dtype, int64_t i) {
-  if (dtype == MOE_DT_BF16) return to_f(static_cast<const __nv_bfloat16*>(s)[i]);
-  if (dtype == MOE_DT_FP16) return to_f(static_cast<const __half*>(s)[i]);
-  return static_cast<const float*>(s)[i];
+// Shared memory: the warps' rings, then two panels of x, scales and zero points;
+// the parts of a sum lie over the rings once those are drained.  With 128 rows of
+// 16-bit scales two CTAs fit an SM for every group size.
+constexpr int kW4Stages = 4;
+constexpr int kW4Ring = kW4Warps * kW4Stages * kW4StageBytes;
+static_assert(kW4MaxRows * kW4RedStride * 4 <= kW4Ring, "the parts fit over the rings");
+template <typename X>
+constexpr int x_panel() {
+  return kW4MaxRows * X::kRow;
 }
 
-__host__ __device__ constexpr int panel_groups(int group, int K) {
-  return group == K || group >= kW4Panel ? 1 : kW4Panel / group;
-}
-
-template <typename X, int NB>
-struct W4Smem {
-  static constexpr int kRing = kW4Warps * kW4Stages * kW4StageBytes;
-  static constexpr int kX = NB * 8 * X::kStride;
-  static constexpr int kRed = NB * 8 * kW4RedStride * 4;
-  static int bytes(int pgroups, bool zeros) {
-    return kRing + 2 * kX + 2 * pgroups * kW4Rows * (zeros ? 8 : 4) + kRed;
-  }
+// What a CTA works on.
+struct W4Tile {
+  int e, n0, rank, split;
+  int p0, p1;  // panels of K
 };
 
-// NB: blocks of eight token rows per pass over the weights.  GS: 32-wide K steps
-// after which a group's sum is scaled (group 32: 1, 64: 2, else 4).
+// One pass over the tile's weights for m <= 8 * NB token rows from `row` on.
+// GS: 32-wide K steps that share a scale (group 32: 1, 64: 2, 128 or a whole
+// row: 4).
 template <typename X, int NB, int GS, bool ZEROS>
-__global__ void __launch_bounds__(kW4Threads, 2) w4_gemv_kernel(W4Args a) {
-  pdl_enter();
+__device__ __forceinline__ void w4_pass(const W4Args& a, const W4Tile& t, int row, int m,
+                                        unsigned char* smem) {
   using M = typename X::Mma;
-  using S = W4Smem<X, NB>;
-  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int kGroups = 16 / GS;  // of a panel
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int nw = warp % 4, kw = warp / 4;
   const int g = lane / 4, c = lane % 4;
-  const int e = blockIdx.z, split = gridDim.x, rank = blockIdx.x;
-  int row0 = 0, row1 = a.R;
-  if (a.offsets) {  // offsets are data: stay inside the R rows whatever they hold
-    row0 = min(max(a.offsets[e], 0), a.R);
-    row1 = min(max(a.offsets[e + 1], row0), a.R);
-  }
-  if (row0 == row1) return;  // the whole cluster
+  const uint32_t base = smem_u32(smem);
+  const uint32_t xs = base + kW4Ring;
+  const uint32_t scales = xs + 2 * x_panel<X>();
+  const uint32_t zeros = scales + 2 * kW4Rows * a.sstride;
+  const uint32_t ring = base + warp * kW4Stages * kW4StageBytes;
 
-  const int pg = panel_groups(a.group, a.K);
-  unsigned char* xs = smem + S::kRing;
-  float* scales = reinterpret_cast<float*>(xs + 2 * S::kX);          // [2][pg][128]
-  uint32_t* zeros = reinterpret_cast<uint32_t*>(scales + 2 * pg * kW4Rows);
-  float* red = reinterpret_cast<float*>(zeros + (ZEROS ? 2 * pg * kW4Rows : 0));
-  const uint32_t ring = smem_u32(smem) + warp * kW4Stages * kW4StageBytes;
-
-  // weight row i (0 .. 127) of the CTA: warp tile i / 32; with a second matrix
-  // rows 0-15 of a tile are the first's, 16-31 the second's, of 16 channels
-  const int n0 = blockIdx.y * a.channels;
+  // Weight row i (0 .. 127) of the CTA belongs to warp tile i / 32; with a second
+  // matrix rows 0-15 of a warp tile are the first's, 16-31 the second's, of 16
+  // channels.  Rows past N stand for channel N - 1: they are not stored.
   auto row_channel = [&](int i) {
-    return a.up ? n0 + (i / 32) * 16 + i % 16 : n0 + i;
+    return min(a.up ? t.n0 + (i / 32) * 16 + i % 16 : t.n0 + i, a.N - 1);
   };
-  auto row_matrix = [&](int i) { return a.up ? (i / 16) % 2 : 0; };
 
-  const int panels = (a.K + kW4Panel - 1) / kW4Panel;
-  const int per = (panels + split - 1) / split;
-  const int p0 = min(panels, rank * per), p1 = min(panels, p0 + per);
+  // Stage q of this warp: 128 channels from p0 * 512 + q * 256 + kw * 128 on, two
+  // stages a panel.  The lane copies 16-byte piece lane % 4 of rows i * 8 +
+  // lane / 4; pieces of a row are swizzled so that neither these writes nor
+  // ldmatrix meet a bank twice.  Pieces past K read the row's last one instead
+  // (x is zero there).
+  const int half = a.K / 2;  // bytes of a weight row
+  const uint8_t* wbase[2];
+  uint32_t wrow[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) wbase[i] = a.w[a.up ? i : 0] + (int64_t)t.e * a.N * half;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    wrow[i] = (uint32_t)row_channel(nw * 32 + i * 8 + lane / 4) * (uint32_t)half;
+  int left = 2 * (t.p1 - t.p0);  // stages still to be loaded
+  uint32_t piece = (t.p0 * kW4Panel + kw * kW4Stage) / 2 + (lane % 4) * 16;
+  const uint32_t last = half - 16;
+  const uint32_t fill0 = ring + (lane / 4) * kW4RowBytes + (((lane % 4) ^ ((lane / 8) % 4)) * 16);
+  uint32_t fill = 0;
+  auto load_stage = [&]() {
+    if (left > 0) {
+      const uint32_t off = min(piece, last);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        cp_async16(fill0 + fill + i * 8 * kW4RowBytes, wbase[i / 2] + (wrow[i] + off));
+    }
+    cp_async_commit();
+    --left;
+    piece += kW4Panel / 4;
+    fill = (fill + kW4StageBytes) % (kW4Stages * kW4StageBytes);
+  };
 
-  // this lane's four weight rows of every stage (rows i * 8 + lane / 4), 16-byte
-  // piece lane % 4
-  const uint8_t* wrow[4];
-  bool wreal[4];
+  // A panel of x, scales and zero points into buffer (p - p0) % 2, by all threads.
+  // x: 16-byte pieces of the present token rows, zeros past K.  Scales: thread
+  // tid takes row tid % 128, in units of sunit bytes from the last unit boundary
+  // at or before the row's first group (rows of odd lengths start inside one).
+  constexpr int kPieces = kW4Panel * X::kBytes / 16;  // of a token row
+  constexpr int kTokStep = kW4Threads / kPieces;
+  const int tok0 = tid / kPieces, kx = (tid % kPieces) * (16 / X::kBytes);
+  const unsigned char* xp =
+      static_cast<const unsigned char*>(a.x) + ((int64_t)(row + tok0) * a.K + kx) * X::kBytes;
+  const int es = a.scale_dtype == MOE_DT_FP32 ? 4 : 2;
+  auto first_group = [&](int i) {  // row i's first group
+    return ((int64_t)t.e * a.N + row_channel(i)) * a.groups;
+  };
+  struct Groups {
+    const unsigned char* from;  // the unit that holds the row's first group, then
+                                // this thread's half of the units
+    int end;                    // the row's end and the tensor's, from there
+    int whole;
+  };
+  const int srow0 = tid % kW4Rows, shalf = tid / kW4Rows;
+  const int smat = a.up ? (srow0 / 16) % 2 : 0;
+  auto groups_of = [&](const void* src, int bytes, int unit, int64_t tensor) {
+    const int64_t first = first_group(srow0) * bytes, at = first & ~(int64_t)(unit - 1);
+    Groups r;
+    r.from = static_cast<const unsigned char*>(src) + at;
+    r.end = (int)(first - at) + a.groups * bytes;
+    r.whole = (int)min(tensor - at, (int64_t)INT32_MAX);
+    return r;
+  };
+  auto load_groups = [&](const Groups& r, int off, int seg, int unit, uint32_t dst) {
+    const int end = min(r.end, off + seg);
+    for (int i = off + shalf * unit; i < end; i += 2 * unit) {
+      if (i + unit <= r.whole) {
+        cp_async_unit(dst + (i - off), r.from + i, unit);
+      } else {  // the tensor ends inside its last word
+        for (int j = i; j < r.whole; ++j)
+          asm volatile("st.shared.u8 [%0], %1;" ::"r"(dst + (j - off)), "r"((uint32_t)r.from[j])
+                       : "memory");
+      }
+    }
+  };
+  const Groups sg = groups_of(a.s[smat], es, a.sunit, a.sbytes);
+  const int sseg = a.groups > 1 ? kGroups * es : 0, smis = sg.end - a.groups * es;
+  Groups zg{};
+  int zmis = 0;
+  if constexpr (ZEROS) {
+    zg = groups_of(a.z[smat], 1, a.zunit, a.zbytes);
+    zmis = zg.end - a.groups;
+  }
+  auto load_panel = [&](int p) {
+    const uint32_t buf = (p - t.p0) & 1;
+    const bool in = p * kW4Panel + kx < a.K;
+#pragma unroll
+    for (int i = 0; i < NB * 8 / kTokStep; ++i)
+      if (tok0 + i * kTokStep < m)
+        cp_async16_or_zero(xs + buf * x_panel<X>() + X::piece(tok0 + i * kTokStep, tid % kPieces),
+                           in ? xp + (int64_t)i * kTokStep * a.K * X::kBytes +
+                                    p * (kW4Panel * X::kBytes)
+                              : static_cast<const unsigned char*>(a.x),
+                           in);
+    load_groups(sg, p * sseg, kGroups * es + smis, a.sunit,
+                scales + (buf * kW4Rows + srow0) * a.sstride);
+    if constexpr (ZEROS)
+      load_groups(zg, a.groups > 1 ? p * kGroups : 0, kGroups + zmis, a.zunit,
+                  zeros + (buf * kW4Rows + srow0) * a.zstride);
+  };
+  // where this thread's four weight rows have their scales and zero points
+  uint32_t srow[4], zrow[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = nw * 32 + i * 8 + lane / 4, n = row_channel(r);
-    wreal[i] = n < a.N;
-    wrow[i] = a.w[row_matrix(r)] + ((int64_t)e * a.N + (wreal[i] ? n : 0)) * (a.K / 2);
+    const int r = nw * 32 + g + i * 8;
+    srow[i] = scales + r * a.sstride + ((uint32_t)first_group(r) * es & (a.sunit - 1));
+    if constexpr (ZEROS) zrow[i] = zeros + r * a.zstride + ((uint32_t)first_group(r) & (a.zunit - 1));
   }
-  // stage q of this warp covers K from p0's panel on: two stages a panel
-  auto load_stage = [&](int q) {
-    const int k = (p0 + q / 2) * kW4Panel + kw * (kW4Panel / 2) + (q % 2) * kW4Stage +
-                  (lane % 4) * 32;
-    const bool in = q < 2 * (p1 - p0) && k < a.K;
-    const uint32_t dst = ring + (q % kW4Stages) * kW4StageBytes + (lane % 4) * 16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      cp_async16(dst + (i * 8 + lane / 4) * kW4RowBytes, wrow[i] + (in ? k / 2 : 0),
-                 in && wreal[i]);
-    cp_async_commit();
-  };
+  const uint32_t gstep = a.groups > 1 ? es : 0;  // one scale a row: always the first
+  const uint32_t gstep_z = a.groups > 1 ? 1 : 0;
 
-  // x: 16-byte pieces of a panel, a thread takes every 256th; scales: one of
-  // the CTA's rows and every second group a thread
-  constexpr int kPieces = kW4Panel * X::kBytes / 16;  // of a row
-  constexpr int kXPer = NB * 8 * kPieces / kW4Threads;
-  const unsigned char* xg = static_cast<const unsigned char*>(a.x);
-  const int srow = tid % kW4Rows, sn = row_channel(srow);
-  const bool sreal = sn < a.N;
-  const int64_t sbase = ((int64_t)e * a.N + (sreal ? sn : 0)) * a.groups;
-  const void* sptr = a.s[row_matrix(srow)];
-  const uint8_t* zptr = a.z[row_matrix(srow)];
+  // absent token rows are zero in both panels
+  for (int i = m * kPieces + tid; i < NB * 8 * kPieces; i += kW4Threads)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      *reinterpret_cast<uint4*>(smem + kW4Ring + b * x_panel<X>() +
+                                X::piece(i / kPieces, i % kPieces)) = make_uint4(0u, 0u, 0u, 0u);
 
-  for (int chunk = row0; chunk < row1; chunk += NB * 8) {
-    const int m = min(NB * 8, row1 - chunk);
-    uint4 xr[kXPer];
-    auto fetch_x = [&](int p) {
+  float acc[2][NB][4] = {};
+  if (t.p0 < t.p1) load_panel(t.p0);  // completes with the first stage
 #pragma unroll
-      for (int i = 0; i < kXPer; ++i) {
-        const int u = tid + i * kW4Threads, tok = u / kPieces;
-        const int k = p * kW4Panel + (u % kPieces) * (16 / X::kBytes);
-        xr[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (tok < m && k < a.K)
-          xr[i] = *reinterpret_cast<const uint4*>(xg + ((int64_t)(chunk + tok) * a.K + k) *
-                                                           X::kBytes);
-      }
-    };
-    auto put_panel = [&](int p) {
-      unsigned char* xb = xs + (p & 1) * S::kX;
+  for (int q = 0; q < kW4Stages - 1; ++q) load_stage();
+  uint32_t use = 0;  // the ring stage in use
+  for (int p = t.p0; p < t.p1; ++p) {
+    const uint32_t buf = (p - t.p0) & 1;
+    const uint32_t xb = xs + buf * x_panel<X>();
 #pragma unroll
-      for (int i = 0; i < kXPer; ++i) {
-        const int u = tid + i * kW4Threads;
-        *reinterpret_cast<uint4*>(xb + (u / kPieces) * X::kStride + (u % kPieces) * 16) = xr[i];
-      }
-      for (int j = tid / kW4Rows; j < pg; j += kW4Threads / kW4Rows) {
-        const int grp = (p * kW4Panel) / a.group + j;
-        const bool in = sreal && grp < a.groups;
-        scales[((p & 1) * pg + j) * kW4Rows + srow] =
-            in ? load_scale(sptr, a.scale_dtype, sbase + grp) : 0.f;
-        if constexpr (ZEROS)
-          zeros[((p & 1) * pg + j) * kW4Rows + srow] =
-              M::kMagic + (in ? (zptr[sbase + grp] & 31u) * 0x00010001u : 0u);
-      }
-    };
-
-#pragma unroll
-    for (int q = 0; q < kW4Stages - 1; ++q) load_stage(q);
-    float acc[2][NB][4] = {};
-    if (p0 < p1) {
-      fetch_x(p0);
-      put_panel(p0);
-    }
-    __syncthreads();
-    for (int p = p0; p < p1; ++p) {
-      if (p + 1 < p1) fetch_x(p + 1);
-      const unsigned char* xb = xs + (p & 1) * S::kX + g * X::kStride;
-      const float* sb = scales + (p & 1) * pg * kW4Rows + nw * 32 + g;
-      const uint32_t* zb = zeros + (p & 1) * pg * kW4Rows + nw * 32 + g;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int q = 2 * (p - p0) + h;
+    for (int h = 0; h < 2; ++h) {
+      if (h == 0) {
+        // the panel came with the stage after this one (the first panel with the
+        // first); everybody is done with the panel before, whose buffer the next
+        // one takes
+        cp_async_wait<kW4Stages - 3>();
+        __syncthreads();
+        if (p + 1 < t.p1) load_panel(p + 1);
+      } else {
         cp_async_wait<kW4Stages - 2>();
         __syncwarp();
-        load_stage(q + kW4Stages - 1);
-        const uint32_t st = ring + (q % kW4Stages) * kW4StageBytes + lane * kW4RowBytes;
-        const int kp = kw * (kW4Panel / 2) + h * kW4Stage;  // K inside the panel
+      }
+      load_stage();
+      const uint32_t st = ring + use + lane * kW4RowBytes;
+      use = (use + kW4StageBytes) % (kW4Stages * kW4StageBytes);
+      const int k0 = p * kW4Panel + h * (kW4Panel / 2) + kw * kW4Stage;
 #pragma unroll
-        for (int s0 = 0; s0 < 4; s0 += GS) {
-          const int grp = pg == 1 ? 0 : (kp + s0 * 32) / a.group;
-          uint32_t zc[4];
+      for (int s0 = 0; s0 < 4; s0 += GS) {
+        if (k0 + s0 * 32 >= a.K) break;  // warp-uniform; no scales there
+        const uint32_t grp = (h * 8 + kw * 4 + s0) / GS;
+        uint32_t zc[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            zc[i] = ZEROS ? zb[grp * kW4Rows + i * 8] : M::kMagic + 0x00080008u;
-          float part[2][NB][4] = {};
-#pragma unroll
-          for (int s = s0; s < s0 + GS; ++s) {
-            uint32_t wv[4];  // first tile rows g, g + 8; second tile rows g, g + 8
-            ldmatrix_x4(st + s * 16, wv);
-            uint32_t af[2][2][4];
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                af[t][i][0] = dequant_pair<M>(wv[2 * t], 2 * i, zc[2 * t]);
-                af[t][i][1] = dequant_pair<M>(wv[2 * t + 1], 2 * i, zc[2 * t + 1]);
-                af[t][i][2] = dequant_pair<M>(wv[2 * t], 2 * i + 1, zc[2 * t]);
-                af[t][i][3] = dequant_pair<M>(wv[2 * t + 1], 2 * i + 1, zc[2 * t + 1]);
-              }
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              uint32_t bf[4];
-              X::pairs(xb + b * 8 * X::kStride + (kp + s * 32 + c * 8) * X::kBytes, bf);
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                M::mma(part[t][b], af[t][0], bf[0], bf[1]);
-                M::mma(part[t][b], af[t][1], bf[2], bf[3]);
-              }
-            }
-          }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const float s_lo = sb[grp * kW4Rows + t * 16], s_hi = sb[grp * kW4Rows + t * 16 + 8];
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              acc[t][b][0] = fmaf(s_lo, part[t][b][0], acc[t][b][0]);
-              acc[t][b][1] = fmaf(s_lo, part[t][b][1], acc[t][b][1]);
-              acc[t][b][2] = fmaf(s_hi, part[t][b][2], acc[t][b][2]);
-              acc[t][b][3] = fmaf(s_hi, part[t][b][3], acc[t][b][3]);
-            }
-          }
+        for (int i = 0; i < 4; ++i) {
+          zc[i] = M::kMagic + 0x00080008u;
+          if constexpr (ZEROS)
+            zc[i] = M::kMagic +
+                    (lds_u8(zrow[i] + buf * kW4Rows * a.zstride + grp * gstep_z) & 31u) *
+                        0x00010001u;
         }
+        float part[2][NB][4] = {};
+#pragma unroll
+        for (int s = s0; s < s0 + GS; ++s) {
+          uint32_t wv[4];  // first tile rows g, g + 8; second tile rows g, g + 8
+          ldmatrix_x4(st + ((s ^ ((lane / 2) % 4)) * 16), wv);
+          uint32_t bf[NB][4];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) X::operands(xb, b * 8 + g, c, h * 8 + kw * 4 + s, bf[b]);
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t af[4] = {dequant_pair<M>(wv[2 * u], 2 * i, zc[2 * u]),
+                                      dequant_pair<M>(wv[2 * u + 1], 2 * i, zc[2 * u + 1]),
+                                      dequant_pair<M>(wv[2 * u], 2 * i + 1, zc[2 * u]),
+                                      dequant_pair<M>(wv[2 * u + 1], 2 * i + 1, zc[2 * u + 1])};
+#pragma unroll
+              for (int b = 0; b < NB; ++b) M::mma(part[u][b], af, bf[b][2 * i], bf[b][2 * i + 1]);
+            }
+        }
+        float sv[4];
+        const uint32_t so = buf * kW4Rows * a.sstride + grp * gstep;
+        if (a.scale_dtype == MOE_DT_BF16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sv[i] = bf16_to_f(lds_u16(srow[i] + so));
+        } else if (a.scale_dtype == MOE_DT_FP16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sv[i] = __half2float(__ushort_as_half(lds_u16(srow[i] + so)));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sv[i] = lds_f32(srow[i] + so);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[u][b][j] = fmaf(sv[2 * u + j / 2], part[u][b][j], acc[u][b][j]);
       }
-      if (p + 1 < p1) put_panel(p + 1);
-      __syncthreads();
     }
-    cp_async_wait<0>();
+  }
+  cp_async_wait<0>();
+  __syncthreads();
 
-    // add the two K halves, then the cluster's parts, in a fixed order
-    auto red_at = [&](int t, int b, int j) -> float& {
-      const int tok = b * 8 + 2 * c + (j & 1), r = nw * 32 + t * 16 + g + (j >> 1) * 8;
-      return red[tok * kW4RedStride + r];
-    };
-    if (kw == 1) {
+  // add the two K halves, then the cluster's parts, in a fixed order
+  float* red = reinterpret_cast<float*>(smem);
+  auto red_at = [&](int u, int b, int j) -> float& {
+    const int tok = b * 8 + 2 * c + (j & 1), r = nw * 32 + u * 16 + g + (j >> 1) * 8;
+    return red[tok * kW4RedStride + r];
+  };
+  if (kw == 1) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) red_at(t, b, j) = acc[t][b][j];
-    }
+        for (int j = 0; j < 4; ++j) red_at(u, b, j) = acc[u][b][j];
+  }
+  __syncthreads();
+  if (kw == 0) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) red_at(u, b, j) += acc[u][b][j];
+  }
+  if (t.split > 1)
+    cluster_sync_all();
+  else
     __syncthreads();
-    if (kw == 0) {
+  auto total = [&](int tok, int r) {
+    if (t.split == 1) return red[tok * kW4RedStride + r];
+    const uint32_t at = base + (tok * kW4RedStride + r) * 4;
+    float v[kW4MaxSplit], sum = 0.f;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+    for (int q = 0; q < kW4MaxSplit; ++q)
+      if (q < t.split) v[q] = ld_cluster_f32(mapa_shared(at, q));
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) red_at(t, b, j) += acc[t][b][j];
+    for (int q = 0; q < kW4MaxSplit; ++q)
+      if (q < t.split) sum += v[q];
+    return sum;
+  };
+  for (int i = tid + t.rank * kW4Threads; i < m * a.channels; i += t.split * kW4Threads) {
+    const int tok = i / a.channels, ch = i % a.channels, n = t.n0 + ch;
+    if (n >= a.N) continue;
+    const float xsc = a.x_scale ? a.x_scale[row + tok] : 1.f;
+    float v;
+    if (a.up) {
+      const int r = (ch / 16) * 32 + ch % 16;
+      const float gate = total(tok, r) * xsc, up = total(tok, r + 16) * xsc;
+      v = gate / (1.f + expf(-gate)) * up;
+    } else {
+      v = total(tok, ch) * xsc;
     }
-    if (split > 1)
-      cluster_sync_all();
+    const int64_t at = (int64_t)(row + tok) * a.N + n;
+    if (a.out_dtype == MOE_DT_BF16)
+      static_cast<__nv_bfloat16*>(a.out)[at] = from_f<__nv_bfloat16>(v);
+    else if (a.out_dtype == MOE_DT_FP16)
+      static_cast<__half*>(a.out)[at] = from_f<__half>(v);
     else
-      __syncthreads();
-    const uint32_t red_sh = smem_u32(red);
-    auto total = [&](int tok, int r) {
-      if (split == 1) return red[tok * kW4RedStride + r];
-      float v = 0.f;
-      for (int q = 0; q < split; ++q)
-        v += ld_cluster_f32(mapa_shared(red_sh + (tok * kW4RedStride + r) * 4, q));
-      return v;
-    };
-    for (int i = tid + rank * kW4Threads; i < m * a.channels; i += split * kW4Threads) {
-      const int tok = i / a.channels, ch = i % a.channels, n = n0 + ch;
-      if (n >= a.N) continue;
-      const float xsc = a.x_scale ? a.x_scale[chunk + tok] : 1.f;
-      float v;
-      if (a.up) {
-        const int r = (ch / 16) * 32 + ch % 16;
-        const float gate = total(tok, r) * xsc, up = total(tok, r + 16) * xsc;
-        v = gate / (1.f + expf(-gate)) * up;
-      } else {
-        v = total(tok, ch) * xsc;
-      }
-      const int64_t at = (int64_t)(chunk + tok) * a.N + n;
-      if (a.out_dtype == MOE_DT_BF16)
-        static_cast<__nv_bfloat16*>(a.out)[at] = from_f<__nv_bfloat16>(v);
-      else if (a.out_dtype == MOE_DT_FP16)
-        static_cast<__half*>(a.out)[at] = from_f<__half>(v);
-      else
-        static_cast<float*>(a.out)[at] = v;
-    }
-    // the next chunk (or the exit) must not overtake a reader of this part
-    if (split > 1)
-      cluster_sync_all();
+      static_cast<float*>(a.out)[at] = v;
+  }
+  // the next pass (or the exit) must not overtake a reader of these parts
+  if (t.split > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
+}
+
+template <typename X, int GS, bool ZEROS>
+__global__ void __launch_bounds__(kW4Threads, 2) w4_gemv_kernel(W4Args a) {
+  pdl_enter();
+  extern __shared__ __align__(128) unsigned char smem[];
+  W4Tile t;
+  t.e = blockIdx.z;
+  t.n0 = blockIdx.y * a.channels;
+  t.rank = blockIdx.x;
+  t.split = gridDim.x;
+  int row0 = 0, row1 = a.R;
+  if (a.offsets) {  // offsets are data: stay inside the R rows whatever they hold
+    row0 = min(max(a.offsets[t.e], 0), a.R);
+    row1 = min(max(a.offsets[t.e + 1], row0), a.R);
+  }
+  const int panels = (a.K + kW4Panel - 1) / kW4Panel;
+  const int per = (panels + t.split - 1) / t.split;
+  t.p0 = min(panels, t.rank * per);
+  t.p1 = min(panels, t.p0 + per);
+  // the whole cluster sees the same rows, so its barriers match
+  while (row0 < row1) {
+    const int m = min(row1 - row0, kW4MaxRows);
+    if (m > 8)
+      w4_pass<X, 2, GS, ZEROS>(a, t, row0, m, smem);
     else
-      __syncthreads();
+      w4_pass<X, 1, GS, ZEROS>(a, t, row0, m, smem);
+    row0 += m;
   }
 }
 
-template <typename X, int NB, int GS, bool ZEROS>
-void launch_as(const Launch& L, const W4Args& a, int split) {
-  const int smem = W4Smem<X, NB>::bytes(panel_groups(a.group, a.K), ZEROS);
-  // the kernel's largest shared memory on any call: groups of 32 with zeros
+// The copy unit of rows of `row` bytes whose panels hold `panel` bytes: the
+// widest that both are multiples of, or 4 with rows that start inside a unit.
+int copy_unit(int64_t row, int panel) {
+  for (int u = 16; u > 4; u /= 2)
+    if (row % u == 0 && panel % u == 0) return u;
+  return 4;
+}
+
+template <typename X, int GS, bool ZEROS>
+void launch_as(const Launch& L, W4Args a, int split) {
+  constexpr int kGroups = 16 / GS;
+  const int es = a.scale_dtype == MOE_DT_FP32 ? 4 : 2;
+  // a row's panel, one word more where rows may start inside a unit, and an odd
+  // number of copy units where that costs little, against bank conflicts
+  auto stride = [](int bytes, int unit, bool inside) {
+    const int n = (bytes + (inside ? unit : 0) + unit - 1) / unit;
+    return (n > 1 && n % 2 == 0 ? n + 1 : n) * unit;
+  };
+  a.sunit = copy_unit((int64_t)a.groups * es, kGroups * es);
+  a.sstride = stride(kGroups * es, a.sunit, (int64_t)a.groups * es % a.sunit != 0);
+  a.sbytes = (int64_t)a.E * a.N * a.groups * es;
+  if (ZEROS) {
+    a.zunit = copy_unit(a.groups, kGroups);
+    a.zstride = stride(kGroups, a.zunit, a.groups % a.zunit != 0);
+    a.zbytes = (int64_t)a.E * a.N * a.groups;
+  }
+  const int smem = kW4Ring + 2 * x_panel<X>() + 2 * kW4Rows * (a.sstride + a.zstride);
+  // at most: fp32 scales of groups of 32 and their zero points
+  constexpr int kMost = kW4Ring + 2 * x_panel<X>() + 2 * kW4Rows * (96 + 48);
   constexpr int kSlotX = std::is_same<X, XBf16>::value ? 0 : std::is_same<X, XFp16>::value ? 1 : 2;
-  constexpr int kSlotIndex = ((kSlotX * 2 + NB - 1) * 3 + GS / 2) * 2 + ZEROS;
+  constexpr int kSlotIndex = (kSlotX * 3 + GS / 2) * 2 + ZEROS;
   static_assert(kSlotIndex < kAttrW4Slots, "one slot for each variant");
-  set_smem_attr_once(reinterpret_cast<const void*>(w4_gemv_kernel<X, NB, GS, ZEROS>),
-                     W4Smem<X, NB>::bytes(kW4Panel / (32 * GS), ZEROS), kAttrW4Base + kSlotIndex);
+  set_smem_attr_once(reinterpret_cast<const void*>(w4_gemv_kernel<X, GS, ZEROS>), kMost,
+                     kAttrW4Base + kSlotIndex);
   const dim3 grid(split, (a.N + a.channels - 1) / a.channels, a.E);
   launch_begin(L, MOE_K_W4);
-  launch_kernel_cluster(w4_gemv_kernel<X, NB, GS, ZEROS>, grid, dim3(split), dim3(kW4Threads), smem,
+  launch_kernel_cluster(w4_gemv_kernel<X, GS, ZEROS>, grid, dim3(split), dim3(kW4Threads), smem,
                         L.stream, a);
   launch_end(L, MOE_K_W4);
 }
-template <typename X, int NB, int GS>
+
+// How many CTAs share a row tile's K: the split with the least time by a count
+// of panels.  A CTA takes the time of its panels and of about two more to start
+// and to add the parts.  Two CTAs fit an SM, and a cluster stays inside a GPC
+// of 16 to 20 SMs, so larger clusters leave some slots empty.
+int choose_split(const W4Args& a, int num_sms) {
+  const int64_t tiles = (int64_t)((a.N + a.channels - 1) / a.channels) *
+                        std::min(a.E, a.R);  // experts with rows, at most
+  const int panels = (a.K + kW4Panel - 1) / kW4Panel;
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int split = 1; split <= std::min(kW4MaxSplit, panels); split *= 2) {
+    const int64_t slots = split == 1 ? 2 * num_sms : num_sms / 19 * (36 / split * split);
+    const int64_t rounds = (tiles * split + slots - 1) / slots;
+    const int64_t cost = rounds * ((panels + split - 1) / split + 2);
+    if (cost < least) {
+      least = cost;
+      best = split;
+    }
+  }
+  return best;
+}
+
+template <typename X, int GS>
 void launch_zeros(const Launch& L, const W4Args& a, int split) {
   if (a.z[0])
-    launch_as<X, NB, GS, true>(L, a, split);
+    launch_as<X, GS, true>(L, a, split);
   else
-    launch_as<X, NB, GS, false>(L, a, split);
-}
-template <typename X, int NB>
-void launch_group(const Launch& L, const W4Args& a, int split) {
-  if (a.group == 32)
-    launch_zeros<X, NB, 1>(L, a, split);
-  else if (a.group == 64)
-    launch_zeros<X, NB, 2>(L, a, split);
-  else
-    launch_zeros<X, NB, 4>(L, a, split);
+    launch_as<X, GS, false>(L, a, split);
 }
 template <typename X>
 void launch_w4(const Launch& L, const W4Args& a) {
-  const int tiles = (a.N + a.channels - 1) / a.channels;
-  const int panels = (a.K + kW4Panel - 1) / kW4Panel;
-  const int64_t ctas = (int64_t)tiles * std::min(a.E, a.R);  // experts with rows, at most
-  int split = 1;
-  while (2 * split <= std::min(kW4MaxSplit, panels) && ctas * split < 2 * L.num_sms) split *= 2;
-  // rows an expert has on average; more than eight go as two blocks a pass
-  if ((int64_t)a.R > 8LL * a.E)
-    launch_group<X, 2>(L, a, split);
+  const int split = choose_split(a, L.num_sms);
+  if (a.group == 32)
+    launch_zeros<X, 1>(L, a, split);
+  else if (a.group == 64)
+    launch_zeros<X, 2>(L, a, split);
   else
-    launch_group<X, 1>(L, a, split);
+    launch_zeros<X, 4>(L, a, split);
 }
 
 }  // namespace
@@ -478,7 +644,10 @@ extern "C" moe_status moe_w4_gemv(int32_t n_experts, int32_t N, int32_t K, int32
   if ((w_up != nullptr) != (scales_up != nullptr) || (zeros_up && !w_up) ||
       (w_up && (zeros != nullptr) != (zeros_up != nullptr)))
     return MOE_ERR_INVALID_ARG;
-  if (n_experts > kW4MaxExperts || N > (1 << 22) || K > (1 << 22)) return MOE_ERR_UNSUPPORTED;
+  // 32-bit offsets inside one expert's matrix
+  if (n_experts > kW4MaxExperts || N > (1 << 22) || K > (1 << 22) ||
+      (int64_t)N * (K / 2) > INT32_MAX)
+    return MOE_ERR_UNSUPPORTED;
   if (R == 0) return MOE_OK;
   if (!x || !w || !scales || !out) return MOE_ERR_INVALID_ARG;
   if ((x_dtype == MOE_DT_INT8) != (x_scale != nullptr)) return MOE_ERR_INVALID_ARG;
@@ -499,8 +668,8 @@ extern "C" moe_status moe_w4_gemv(int32_t n_experts, int32_t N, int32_t K, int32
   a.N = N;
   a.K = K;
   a.R = R;
-  a.group = group > 0 ? group : K;
-  a.groups = K / a.group;
+  a.group = group;
+  a.groups = group > 0 ? K / group : 1;
   a.up = w_up != nullptr;
   a.channels = a.up ? kW4Rows / 2 : kW4Rows;
   a.scale_dtype = scale_dtype;
