@@ -11,59 +11,86 @@ import ctypes
 
 import torch
 
-from . import MoeError, _check, _ptr, _stream, lib  # noqa: F401
+from . import _check, lib
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int8: 3,
           torch.float8_e4m3fn: 4}
-_FLOATS = (torch.bfloat16, torch.float16, torch.float32)
+_FLOATS = frozenset((torch.bfloat16, torch.float16, torch.float32))
+_CODES = frozenset((torch.int8, torch.float8_e4m3fn))
+_ANY = frozenset(DTYPES)
+_F32 = frozenset((torch.float32,))
+_I32 = frozenset((torch.int32,))
+_U8 = frozenset((torch.uint8,))
+
+_W4_X = frozenset((torch.bfloat16, torch.float16, torch.int8))
+
+_add_rmsnorm = lib.moe_add_rmsnorm
+_sort_tokens = lib.moe_sort_tokens
+_sort_tokens_backward = lib.moe_sort_tokens_backward
+_unsort_tokens = lib.moe_unsort_tokens
+_unsort_tokens_backward = lib.moe_unsort_tokens_backward
+_w4_gemv = lib.moe_w4_gemv
 
 
-def _tensor(t, name, dtype, shape, like=None):
-    """t is a contiguous tensor of the given dtype (one, or several to choose
-    from) and shape, on the device of `like` (None: the current CUDA device)."""
+# A call's checks are on the path of every decoded token: the common case is a few
+# attribute reads, and what is wrong with an argument is worked out only then.
+def _tensor(t, name, dtypes, shape, device):
+    """Address of a contiguous tensor of one of the given types and the shape, on
+    CUDA device `device`."""
+    try:
+        if t.dtype in dtypes and t.shape == shape and t.is_contiguous() \
+                and t.get_device() == device:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtypes, shape, device)
+    raise ValueError(f"{name}: not contiguous")
+
+
+def _rows(t, name, dtypes, shape, device):
+    """(address, row stride) of a matrix whose rows are contiguous."""
+    try:
+        if t.dtype in dtypes and t.shape == shape and t.get_device() == device:
+            if t.is_contiguous():
+                return t.data_ptr(), shape[1]
+            row, step = t.stride()
+            if shape[0] <= 1:
+                row = shape[1]
+            if (step == 1 or shape[1] <= 1) and row >= shape[1]:
+                return t.data_ptr(), row
+    except AttributeError:
+        pass
+    _refuse(t, name, dtypes, shape, device)
+    raise ValueError(f"{name}: rows are not contiguous or overlap (strides {t.stride()})")
+
+
+def _refuse(t, name, dtypes, shape, device):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
-    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
-        raise TypeError(f"{name}: {t.dtype} is not {dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} is not {shape}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: not contiguous")
-    _device(t, name, like)
-    return t.data_ptr()
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {t.dtype} is not one of {sorted(map(str, dtypes))}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} is not {tuple(shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, not on CUDA device {device}")
 
 
-def _rows(t, name, dtype, shape, like=None):
-    """(pointer, row stride) of a matrix whose rows are contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
-    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
-        raise TypeError(f"{name}: {t.dtype} is not {dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} is not {shape}")
-    row, step = t.stride()
-    if shape[1] > 1 and step != 1:
-        raise ValueError(f"{name}: channels are not contiguous")
-    if shape[0] <= 1:
-        row = shape[1]
-    elif row < shape[1]:
-        raise ValueError(f"{name}: rows overlap (stride {row})")
-    _device(t, name, like)
-    return t.data_ptr(), row
-
-
-def _device(t, name, like):
-    if like is None:
-        if not t.is_cuda or t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name}: not on the current CUDA device ({t.device})")
-    elif t.device != like.device:
-        raise ValueError(f"{name}: on {t.device}, not {like.device}")
-
-
-def _matrix_shape(t, name):
+def _matrix(t, name, dtypes):
+    """(shape, device index) of the matrix that sets a call's sizes."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise TypeError(f"{name}: expected a matrix")
-    return tuple(t.shape)
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {t.dtype} is not one of {sorted(map(str, dtypes))}")
+    return t.shape, t.get_device()
+
+
+def _stream(stream, device):
+    """The handle of the stream to launch on (None: the current one)."""
+    if device < 0 or device != torch._C._cuda_getDevice():
+        raise ValueError("the tensors are not on the current CUDA device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def moe_add_rmsnorm(x, residual, gamma, eps, sum_out, y=None, q=None, q_scale=None, q_group=0,
@@ -73,27 +100,31 @@ def moe_add_rmsnorm(x, residual, gamma, eps, sum_out, y=None, q=None, q_scale=No
 
     x, residual, sum_out, y [T, H] and gamma [H] share one type (bf16, fp16,
     fp32) and may have row strides; q [T, H] is int8 or float8_e4m3fn, q_scale
-    fp32 [T, groups].  residual, gamma and each output may be None; sum_out may
+    fp32 [T, groups] ([T, 1] for q_group 0).  residual, gamma and each output may be None; sum_out may
     be x or residual itself.
     """
-    T, H = shape = _matrix_shape(x, "x")
-    dt = x.dtype
-    px, ldx = _rows(x, "x", _FLOATS, shape)
-    pr, ldr = (None, 0) if residual is None else _rows(residual, "residual", dt, shape, x)
-    pg = None if gamma is None else _tensor(gamma, "gamma", dt, (H,), x)
-    ps, lds = (None, 0) if sum_out is None else _rows(sum_out, "sum_out", dt, shape, x)
-    py, ldy = (None, 0) if y is None else _rows(y, "y", dt, shape, x)
-    pq = psc = None
-    qdt = 0
+    shape, dev = _matrix(x, "x", _FLOATS)
+    T, H = shape
+    same = (x.dtype,)
+    px, ldx = _rows(x, "x", same, shape, dev)
+    pr = pg = ps = py = pq = psc = None
+    ldr = lds = ldy = qdt = 0
+    if residual is not None:
+        pr, ldr = _rows(residual, "residual", same, shape, dev)
+    if gamma is not None:
+        pg = _tensor(gamma, "gamma", same, (H,), dev)
+    if sum_out is not None:
+        ps, lds = _rows(sum_out, "sum_out", same, shape, dev)
+    if y is not None:
+        py, ldy = _rows(y, "y", same, shape, dev)
     if q is not None:
-        pq = _tensor(q, "q", (torch.int8, torch.float8_e4m3fn), shape, x)
+        pq = _tensor(q, "q", _CODES, shape, dev)
         qdt = DTYPES[q.dtype]
-        groups = (T, -(-H // q_group) if q_group else 1)
-        if q_scale is None or (tuple(q_scale.shape) != groups and (q_group or q_scale.shape != (T,))):
-            raise ValueError(f"q_scale: expected shape {groups}")
-        psc = _tensor(q_scale, "q_scale", torch.float32, tuple(q_scale.shape), x)
-    _check(lib.moe_add_rmsnorm(T, H, DTYPES[dt], px, ldx, pr, ldr, pg, eps, ps, lds, py, ldy, qdt,
-                               q_group, pq, psc, _stream(stream)), "moe_add_rmsnorm")
+        psc = _tensor(q_scale, "q_scale", _F32, (T, -(-H // q_group) if q_group else 1), dev)
+    st = _add_rmsnorm(T, H, DTYPES[x.dtype], px, ldx, pr, ldr, pg, eps, ps, lds, py, ldy, qdt,
+                      q_group, pq, psc, _stream(stream, dev))
+    if st:
+        _check(st, "moe_add_rmsnorm")
 
 
 def moe_sort_workspace_size(T, k, n_experts) -> int:
@@ -115,78 +146,88 @@ def moe_sort_tokens(n_experts, ids, x, x_scale, counts, offsets, sorted_to_expan
     """Stable order of the picks ids [T, k] by expert (dropped picks last) and the
     tokens' rows x [T, H] (and fp32 scales x_scale [T]) in it.  x and x_sorted may
     be None together: only the order is wanted."""
-    T, k = _matrix_shape(ids, "ids")
+    (T, k), dev = _matrix(ids, "ids", _I32)
     R = T * k
-    i32 = torch.int32
-    pi = _tensor(ids, "ids", i32, (T, k))
-    pc = _tensor(counts, "counts", i32, (n_experts,), ids)
-    po = _tensor(offsets, "offsets", i32, (n_experts + 1,), ids)
-    p1 = _tensor(sorted_to_expanded, "sorted_to_expanded", i32, (R,), ids)
-    p2 = _tensor(expanded_to_sorted, "expanded_to_sorted", i32, (R,), ids)
-    H, ldx, dt, px, pxs, psc, pso = 0, 0, 0, None, None, None, None
-    if (x is None) != (x_sorted is None):
-        raise ValueError("x and x_sorted go together")
+    pi = _tensor(ids, "ids", _I32, (T, k), dev)
+    pc = _tensor(counts, "counts", _I32, (n_experts,), dev)
+    po = _tensor(offsets, "offsets", _I32, (n_experts + 1,), dev)
+    p1 = _tensor(sorted_to_expanded, "sorted_to_expanded", _I32, (R,), dev)
+    p2 = _tensor(expanded_to_sorted, "expanded_to_sorted", _I32, (R,), dev)
+    H = ldx = dt = nws = 0
+    px = pxs = psc = pso = pw = None
     if x is not None:
-        H = _matrix_shape(x, "x")[1]
-        px, ldx = _rows(x, "x", tuple(DTYPES), (T, H), ids)
-        pxs = _tensor(x_sorted, "x_sorted", x.dtype, (R, H), ids)
+        if x.dim() != 2:
+            raise ValueError("x: expected a matrix")
+        H = x.shape[1]
+        px, ldx = _rows(x, "x", _ANY, (T, H), dev)
+        pxs = _tensor(x_sorted, "x_sorted", (x.dtype,), (R, H), dev)
         dt = DTYPES[x.dtype]
-    if (x_scale is None) != (scale_sorted is None):
-        raise ValueError("x_scale and scale_sorted go together")
+    elif x_sorted is not None:
+        raise ValueError("x_sorted: given without x")
     if x_scale is not None:
-        psc = _tensor(x_scale, "x_scale", torch.float32, tuple(x_scale.shape), ids)
-        if x_scale.numel() != T:
-            raise ValueError(f"x_scale: expected {T} values")
-        pso = _tensor(scale_sorted, "scale_sorted", torch.float32, (R,), ids)
-    pw = None if ws is None else _tensor(ws, "ws", torch.uint8, tuple(ws.shape), ids)
-    _check(lib.moe_sort_tokens(T, k, n_experts, H, dt, pi, px, ldx, psc, pc, po, p1, p2, pxs, pso,
-                               int(zero_dropped), pw, 0 if ws is None else ws.numel(),
-                               _stream(stream)), "moe_sort_tokens")
+        psc = _tensor(x_scale, "x_scale", _F32, (T, 1) if x_scale.dim() == 2 else (T,), dev)
+        pso = _tensor(scale_sorted, "scale_sorted", _F32, (R,), dev)
+    elif scale_sorted is not None:
+        raise ValueError("scale_sorted: given without x_scale")
+    if ws is not None:
+        nws = ws.numel()
+        pw = _tensor(ws, "ws", _U8, (nws,), dev)
+    st = _sort_tokens(T, k, n_experts, H, dt, pi, px, ldx, psc, pc, po, p1, p2, pxs, pso,
+                      1 if zero_dropped else 0, pw, nws, _stream(stream, dev))
+    if st:
+        _check(st, "moe_sort_tokens")
+
+
+def _plan(offsets, expanded_to_sorted, R, dev):
+    """(experts, addresses) of the plan that moe_sort_tokens wrote."""
+    E = offsets.numel() - 1
+    return E, _tensor(offsets, "offsets", _I32, (E + 1,), dev), \
+        _tensor(expanded_to_sorted, "expanded_to_sorted", _I32, (R,), dev)
 
 
 def moe_sort_tokens_backward(dx_sorted, offsets, expanded_to_sorted, k, dx, stream=None):
     """dx [T, H] = each token's kept rows of dx_sorted [T*k, H], added up."""
-    T, H = _matrix_shape(dx, "dx")
-    pd, ld = _rows(dx, "dx", _FLOATS, (T, H))
-    pr = _tensor(dx_sorted, "dx_sorted", _FLOATS, (T * k, H), dx)
-    po = _tensor(offsets, "offsets", torch.int32, tuple(offsets.shape), dx)
-    p2 = _tensor(expanded_to_sorted, "expanded_to_sorted", torch.int32, (T * k,), dx)
-    _check(lib.moe_sort_tokens_backward(T, k, offsets.numel() - 1, H, DTYPES[dx_sorted.dtype], pr,
-                                        po, p2, DTYPES[dx.dtype], pd, ld, _stream(stream)),
-           "moe_sort_tokens_backward")
+    (T, H), dev = _matrix(dx, "dx", _FLOATS)
+    pd, ld = _rows(dx, "dx", _FLOATS, (T, H), dev)
+    pr = _tensor(dx_sorted, "dx_sorted", _FLOATS, (T * k, H), dev)
+    E, po, p2 = _plan(offsets, expanded_to_sorted, T * k, dev)
+    st = _sort_tokens_backward(T, k, E, H, DTYPES[dx_sorted.dtype], pr, po, p2, DTYPES[dx.dtype],
+                               pd, ld, _stream(stream, dev))
+    if st:
+        _check(st, "moe_sort_tokens_backward")
 
 
 def moe_unsort_tokens(y_sorted, offsets, expanded_to_sorted, topk_w, out, stream=None):
     """out [T, H] = sum over each token's kept picks of topk_w [T, k] times its
     row of y_sorted [T*k, H]."""
-    T, k = _matrix_shape(topk_w, "topk_w")
-    H = _matrix_shape(out, "out")[1]
-    pd, ld = _rows(out, "out", _FLOATS, (T, H))
-    pr = _tensor(y_sorted, "y_sorted", _FLOATS, (T * k, H), out)
-    po = _tensor(offsets, "offsets", torch.int32, tuple(offsets.shape), out)
-    p2 = _tensor(expanded_to_sorted, "expanded_to_sorted", torch.int32, (T * k,), out)
-    pw = _tensor(topk_w, "topk_w", torch.float32, (T, k), out)
-    _check(lib.moe_unsort_tokens(T, k, offsets.numel() - 1, H, DTYPES[y_sorted.dtype], pr, po, p2,
-                                 pw, DTYPES[out.dtype], pd, ld, _stream(stream)),
-           "moe_unsort_tokens")
+    (T, H), dev = _matrix(out, "out", _FLOATS)
+    k = topk_w.shape[-1]
+    pd, ld = _rows(out, "out", _FLOATS, (T, H), dev)
+    pr = _tensor(y_sorted, "y_sorted", _FLOATS, (T * k, H), dev)
+    E, po, p2 = _plan(offsets, expanded_to_sorted, T * k, dev)
+    pw = _tensor(topk_w, "topk_w", _F32, (T, k), dev)
+    st = _unsort_tokens(T, k, E, H, DTYPES[y_sorted.dtype], pr, po, p2, pw, DTYPES[out.dtype], pd,
+                        ld, _stream(stream, dev))
+    if st:
+        _check(st, "moe_unsort_tokens")
 
 
 def moe_unsort_tokens_backward(dout, y_sorted, offsets, expanded_to_sorted, topk_w, dy_sorted,
                                dtopk_w, zero_dropped=True, stream=None):
     """Gradients of moe_unsort_tokens: dy_sorted [T*k, H] and dtopk_w [T, k]."""
-    T, k = _matrix_shape(topk_w, "topk_w")
-    H = _matrix_shape(dout, "dout")[1]
-    pd, ld = _rows(dout, "dout", _FLOATS, (T, H))
-    py = _tensor(y_sorted, "y_sorted", _FLOATS, (T * k, H), dout)
-    po = _tensor(offsets, "offsets", torch.int32, tuple(offsets.shape), dout)
-    p2 = _tensor(expanded_to_sorted, "expanded_to_sorted", torch.int32, (T * k,), dout)
-    pw = _tensor(topk_w, "topk_w", torch.float32, (T, k), dout)
-    pg = _tensor(dy_sorted, "dy_sorted", y_sorted.dtype, (T * k, H), dout)
-    pdw = _tensor(dtopk_w, "dtopk_w", torch.float32, (T, k), dout)
-    _check(lib.moe_unsort_tokens_backward(T, k, offsets.numel() - 1, H, DTYPES[y_sorted.dtype],
-                                          DTYPES[dout.dtype], pd, ld, py, po, p2, pw, pg, pdw,
-                                          int(zero_dropped), _stream(stream)),
-           "moe_unsort_tokens_backward")
+    (T, H), dev = _matrix(dout, "dout", _FLOATS)
+    k = topk_w.shape[-1]
+    pd, ld = _rows(dout, "dout", _FLOATS, (T, H), dev)
+    py = _tensor(y_sorted, "y_sorted", _FLOATS, (T * k, H), dev)
+    E, po, p2 = _plan(offsets, expanded_to_sorted, T * k, dev)
+    pw = _tensor(topk_w, "topk_w", _F32, (T, k), dev)
+    pg = _tensor(dy_sorted, "dy_sorted", (y_sorted.dtype,), (T * k, H), dev)
+    pdw = _tensor(dtopk_w, "dtopk_w", _F32, (T, k), dev)
+    st = _unsort_tokens_backward(T, k, E, H, DTYPES[y_sorted.dtype], DTYPES[dout.dtype], pd, ld, py,
+                                 po, p2, pw, pg, pdw, 1 if zero_dropped else 0,
+                                 _stream(stream, dev))
+    if st:
+        _check(st, "moe_unsort_tokens_backward")
 
 
 def pack_w4(codes):
@@ -203,28 +244,35 @@ def moe_w4_gemv(x, x_scale, offsets, w, scales, zeros, out, w_up=None, scales_up
     None (one expert); w, w_up uint8 [E, N, K / 2]; scales [E, N, groups] bf16,
     fp16 or fp32; zeros uint8 of their shape or None (8); out [R, N].
     """
-    R, K = _matrix_shape(x, "x")
+    (R, K), dev = _matrix(x, "x", _W4_X)
     if not isinstance(w, torch.Tensor) or w.dim() != 3:
         raise TypeError("w: expected [experts, N, K / 2]")
     E, N, _ = w.shape
-    px = _tensor(x, "x", (torch.bfloat16, torch.float16, torch.int8), (R, K))
-    pw = _tensor(w, "w", torch.uint8, (E, N, K // 2), x)
     if not isinstance(scales, torch.Tensor) or scales.dim() != 3:
         raise TypeError("scales: expected [experts, N, groups]")
     G = scales.shape[2]
     if G < 1 or K % G:
         raise ValueError(f"scales: {G} groups do not divide K = {K}")
-    ps = _tensor(scales, "scales", _FLOATS, (E, N, G), x)
-    pxs = None if x_scale is None else _tensor(x_scale, "x_scale", torch.float32,
-                                               tuple(x_scale.shape), x)
-    if pxs is not None and x_scale.numel() != R:
-        raise ValueError(f"x_scale: expected {R} values")
-    pof = None if offsets is None else _tensor(offsets, "offsets", torch.int32, (E + 1,), x)
-    pz = None if zeros is None else _tensor(zeros, "zeros", torch.uint8, (E, N, G), x)
-    pwu = None if w_up is None else _tensor(w_up, "w_up", torch.uint8, (E, N, K // 2), x)
-    psu = None if scales_up is None else _tensor(scales_up, "scales_up", scales.dtype, (E, N, G), x)
-    pzu = None if zeros_up is None else _tensor(zeros_up, "zeros_up", torch.uint8, (E, N, G), x)
-    po = _tensor(out, "out", _FLOATS, (R, N), x)
-    _check(lib.moe_w4_gemv(E, N, K, K // G if G > 1 else 0, R, pof, DTYPES[x.dtype], px, pxs, pw,
-                           pwu, DTYPES[scales.dtype], ps, psu, pz, pzu, DTYPES[out.dtype], po,
-                           _stream(stream)), "moe_w4_gemv")
+    wshape, gshape = (E, N, K // 2), (E, N, G)
+    px = _tensor(x, "x", _W4_X, (R, K), dev)
+    pw = _tensor(w, "w", _U8, wshape, dev)
+    ps = _tensor(scales, "scales", _FLOATS, gshape, dev)
+    pxs = pof = pz = pwu = psu = pzu = None
+    if x_scale is not None:
+        pxs = _tensor(x_scale, "x_scale", _F32, (R, 1) if x_scale.dim() == 2 else (R,), dev)
+    if offsets is not None:
+        pof = _tensor(offsets, "offsets", _I32, (E + 1,), dev)
+    if zeros is not None:
+        pz = _tensor(zeros, "zeros", _U8, gshape, dev)
+    if w_up is not None:
+        pwu = _tensor(w_up, "w_up", _U8, wshape, dev)
+    if scales_up is not None:
+        psu = _tensor(scales_up, "scales_up", (scales.dtype,), gshape, dev)
+    if zeros_up is not None:
+        pzu = _tensor(zeros_up, "zeros_up", _U8, gshape, dev)
+    po = _tensor(out, "out", _FLOATS, (R, N), dev)
+    st = _w4_gemv(E, N, K, K // G if G > 1 else 0, R, pof, DTYPES[x.dtype], px, pxs, pw, pwu,
+                  DTYPES[scales.dtype], ps, psu, pz, pzu, DTYPES[out.dtype], po,
+                  _stream(stream, dev))
+    if st:
+        _check(st, "moe_w4_gemv")

@@ -685,3 +685,76 @@ def test_w4_weights_past_32_bits(m):
         q *= float(s[0, 0, 0])
         rel = (8 * 17 + K // 32 + 20) * 2.0**-23
         within(out[r], q @ x[r].double(), rel * (q.abs() @ x[r].abs().double()) + TINY[FP32])
+
+
+# ----------------------------------------------------- together, as used ----
+def test_autograd_functions_against_torch(m):
+    from sparse_expert_layer_gb300 import autograd
+
+    T, k, E, H = 50, 3, 8, 120
+    g = gen(12)
+    ids = draw_ids(g, T, k, E, 3)
+    x, w, c = randn(g, T, H), torch.rand(T, k, generator=g, device="cuda"), randn(g, T * k, H)
+    grad_out = randn(g, H, T).T  # not contiguous: taken as a copy
+
+    def plain(x, w, c):
+        order, inverse, _, offsets = plan_exact(ids, E)
+        src = torch.from_numpy(order // k).cuda()
+        kept = (torch.arange(T * k, device="cuda") < int(offsets[-1]))[:, None]
+        xs = x[src] * kept
+        y = torch.tanh(xs) * c
+        rows = (y * kept)[torch.from_numpy(inverse).cuda()].view(T, k, H)
+        return (rows * w[..., None]).sum(1)
+
+    a = [t.clone().requires_grad_() for t in (x, w, c)]
+    xs, plan = autograd.sort_tokens(a[0], ids, E)
+    out = autograd.unsort_tokens(torch.tanh(xs) * a[2], a[1], plan)
+    out.backward(grad_out)
+    b = [t.double().requires_grad_() for t in (x, w, c)]
+    want = plain(*b)
+    want.backward(grad_out.double())
+    # sums of a few products near 1 in size (dw: 120 of them), fp32 throughout
+    out, want = out.detach(), want.detach()
+    assert torch.allclose(out.double(), want, rtol=0, atol=64 * U * float(want.abs().max()))
+    for p, q in zip(a, b):
+        assert torch.allclose(p.grad.double(), q.grad, rtol=0,
+                              atol=256 * U * float(q.grad.abs().max()))
+
+
+def test_example_block_against_64_bits(m):
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "w4_block.py")
+    spec = importlib.util.spec_from_file_location("w4_block", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    us, block, x, start, residual = ex.decode()
+    assert us > 0
+    T, H = x.shape
+    r, y = norm_exact(x, start, block.gamma, 1e-6)
+    within(residual, r, half_step(r, BF16) + U * r.abs(), "residual")
+    within(block.y, y, half_step(y, BF16) + NORM_REL * y.abs(), "y")
+    # from the codes and the routing on, every step is checked on its inputs
+    xq = block.q.double() * block.q_scale.double()
+    assert float((xq - y).abs().max()) <= 0.51 * float(block.q_scale.max())
+
+    def dequant(packed, scales):
+        q = torch.stack([packed & 15, packed >> 4], -1).view(*packed.shape[:2], -1).double() - 8
+        return q * scales.double().repeat_interleave(q.shape[2] // scales.shape[2], 2)
+
+    wg, wu, wd = (dequant(*p) for p in (block.gate, block.up, block.down))
+    want = torch.zeros(T, H, dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(want)
+    for j in range(block.k):
+        e = block.ids[:, j].long()
+        gate = torch.einsum("th,tih->ti", xq, wg[e])
+        h = gate * torch.sigmoid(gate) * torch.einsum("th,tih->ti", xq, wu[e])
+        w = block.weights[:, j, None].double()
+        want += w * torch.einsum("ti,thi->th", h, wd[e])
+        size += w * torch.einsum("ti,thi->th", h.abs(), wd[e].abs())
+    # h is rounded to bf16 between the products, the output once more
+    within(block.out, want, half_step(want, BF16) + (2.0**-8) * size, "block output")
+    losses = ex.train()
+    assert losses[-1] < 0.9 * losses[0]
