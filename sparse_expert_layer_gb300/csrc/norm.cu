@@ -36,7 +36,7 @@ struct NormArgs {
   int q_e4m3;         // codes are e4m3 instead of int8
   int q_group;        // channels per scale, 0 = the row
   int groups;
-  float eps;
+  float eps, inv_h;
 };
 
 // The factor from v to its code's value, `most` / amax, as pre * inv: where amax
@@ -44,35 +44,39 @@ struct NormArgs {
 __device__ __forceinline__ void code_factor(float amax, float most, float* pre, float* inv) {
   *pre = amax < 0x1p-96f ? 0x1p64f : 1.f;
   const float a = amax * *pre;
-  *inv = a > 0.f ? most / a : 0.f;
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(a));
+  *inv = a > 0.f ? most * r : 0.f;
+}
+
+// Four int8 codes of v * factor, rounded half to even: adding 1.5 * 2^23 leaves
+// the rounded integer in the sum's low bits.  |v * factor| is at most 127 +
+// rounding, so it needs no clamp; a row with a NaN or an infinity has a NaN (or
+// zero) scale, whatever its codes.
+__device__ __forceinline__ uint32_t int8_codes(const float* v, float factor) {
+  uint32_t u[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) u[j] = __float_as_uint(fmaf(v[j], factor, 12582912.f));
+  return __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+}
+__device__ __forceinline__ uint32_t e4m3_codes(const float* v, float factor) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * factor, v[1] * factor),
+                                               __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * factor, v[3] * factor),
+                                               __NV_SATFINITE, __NV_E4M3);
+  return (lo & 0xffffu) | (hi << 16);
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store_codes(const NormArgs& a, size_t at, int n,
-                                            const float (&v)[kSlot], float pre, float inv) {
-  uint32_t w[2];
-  if (a.q_e4m3) {
+__device__ __forceinline__ void store_codes(const NormArgs& a, size_t at, int n, float (&v)[kSlot],
+                                            float pre, float inv) {
+  if (pre != 1.f) {  // the same for the whole row or group
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-          make_float2(v[4 * i] * pre * inv, v[4 * i + 1] * pre * inv), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-          make_float2(v[4 * i + 2] * pre * inv, v[4 * i + 3] * pre * inv), __NV_SATFINITE,
-          __NV_E4M3);
-      w[i] = (lo & 0xffffu) | (hi << 16);
-    }
-  } else {
-    // |v * inv| is at most 127 + rounding, so rounding to nearest needs no clamp;
-    // a row with a NaN or infinity has a NaN scale, whatever its codes
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t u = 0u;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        u |= (uint32_t)(__float2int_rn(v[4 * i + j] * pre * inv) & 0xff) << (8 * j);
-      w[i] = u;
-    }
+    for (int j = 0; j < kSlot; ++j) v[j] *= pre;
   }
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) w[i] = a.q_e4m3 ? e4m3_codes(v + 4 * i, inv) : int8_codes(v + 4 * i, inv);
   uint8_t* q = static_cast<uint8_t*>(a.q) + at;
   if constexpr (VEC) {
     *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
@@ -83,15 +87,101 @@ __device__ __forceinline__ void store_codes(const NormArgs& a, size_t at, int n,
   }
 }
 
+// Where the threads' sums and maxima of a row meet: per warp, two rows alternate.
+struct NormParts {
+  float2 part[2][32];
+};
+
+// One row from its raw slots on: the new residual, the reduction, y and codes.
+// The slots of x (and of the residual) are in rx (rr); `turn` alternates from
+// row to row, so that one barrier a row is enough.
+template <typename T, int VPT, bool VEC>
+__device__ __forceinline__ void norm_row(const NormArgs& a, int t, const Raw8<T> (&rx)[VPT],
+                                         const Raw8<T> (&rr)[VPT], NormParts& sh, int& turn) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int nwarps = blockDim.x / 32;
+  const float most = a.q_e4m3 ? 448.f : 127.f, unit = a.q_e4m3 ? 1.f / 448.f : 1.f / 127.f;
+  float v[VPT][kSlot];
+  float ss = 0.f, amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int s = threadIdx.x + i * blockDim.x, n = min(kSlot, a.H - s * kSlot);
+#pragma unroll
+    for (int j = 0; j < kSlot; ++j) v[i][j] = 0.f;
+    if (s < a.nslots) {
+      unpack8<T>(rx[i], v[i]);
+      if (a.res) {
+        float r[kSlot];
+        unpack8<T>(rr[i], r);
+#pragma unroll
+        for (int j = 0; j < kSlot; ++j) v[i][j] += r[j];
+      }
+      if (a.sum)
+        store8<T, VEC>(static_cast<T*>(a.sum) + (int64_t)t * a.lds + s * kSlot, n, v[i]);
+#pragma unroll
+      for (int j = 0; j < kSlot; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+      if (a.gamma) {
+        float g[kSlot];
+        load8<T, VEC>(static_cast<const T*>(a.gamma) + s * kSlot, n, g);
+#pragma unroll
+        for (int j = 0; j < kSlot; ++j) v[i][j] *= g[j];
+      }
+      amax = max_abs8(amax, v[i]);
+    }
+  }
+  // values >= 0 compare as their bits do; a NaN shows in the sum of squares
+  auto all_max = [](float m) {
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+  };
+  ss = warp_sum(ss);
+  amax = all_max(amax);
+  if (nwarps > 1) {
+    if (lane == 0) sh.part[turn][warp] = make_float2(ss, amax);
+    __syncthreads();
+    // every warp adds the warps' parts in the same order
+    const float2 p = lane < nwarps ? sh.part[turn][lane] : make_float2(0.f, 0.f);
+    ss = warp_sum(p.x);
+    amax = all_max(p.y);
+    turn ^= 1;
+  }
+  const float rstd = rsqrtf(fmaf(ss, a.inv_h, a.eps));
+  float pre = 1.f, inv = 0.f;
+  if (a.q && a.q_group == 0) {
+    code_factor(amax, most, &pre, &inv);
+    if (threadIdx.x == 0) a.scale[t] = rstd * amax * unit;
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int s = threadIdx.x + i * blockDim.x, n = min(kSlot, a.H - s * kSlot);
+    if (a.y && s < a.nslots) {
+      float o[kSlot];
+#pragma unroll
+      for (int j = 0; j < kSlot; ++j) o[j] = v[i][j] * rstd;
+      store8<T, VEC>(static_cast<T*>(a.y) + (int64_t)t * a.ldy + s * kSlot, n, o);
+    }
+    if (!a.q) continue;
+    if (a.q_group > 0) {
+      // a group's slots lie in consecutive lanes of one warp (slots past the
+      // row hold zeros)
+      const int lanes = a.q_group / kSlot;
+      float m = max_abs8(0.f, v[i]);
+      for (int o = lanes / 2; o > 0; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      code_factor(m, most, &pre, &inv);
+      if (s < a.nslots && lane % lanes == 0)
+        a.scale[(size_t)t * a.groups + s / lanes] = rstd * m * unit;
+    }
+    if (s < a.nslots)
+      store_codes<VEC>(a, (size_t)t * a.H + (size_t)s * kSlot, n, v[i], pre, inv);
+  }
+}
+
 // blockDim.x threads work on one row, blockDim.y rows at a time; slot i of a
 // row belongs to thread i % blockDim.x.
 template <typename T, int VPT, bool VEC, int MAXT>
-__global__ void __launch_bounds__(MAXT) add_rmsnorm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(MAXT, VPT == 2 && sizeof(T) == 2 ? 2 : 1) add_rmsnorm_kernel(NormArgs a) {
   pdl_enter();
-  __shared__ float2 part[2][32];  // per warp: sum of squares, largest |v|; two rows alternate
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int nwarps = blockDim.x / 32;
-  const float most = a.q_e4m3 ? 448.f : 127.f;
+  __shared__ NormParts sh;
   int turn = 0;
   for (int t = blockIdx.x * blockDim.y + threadIdx.y; t < a.T; t += gridDim.x * blockDim.y) {
     const T* x = static_cast<const T*>(a.x) + (int64_t)t * a.ldx;
@@ -105,78 +195,7 @@ __global__ void __launch_bounds__(MAXT) add_rmsnorm_kernel(NormArgs a) {
         if (a.res) rr[i] = load_raw8<T, VEC>(res + s * kSlot, n);
       }
     }
-    float v[VPT][kSlot];
-    float ss = 0.f, amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int s = threadIdx.x + i * blockDim.x, n = min(kSlot, a.H - s * kSlot);
-#pragma unroll
-      for (int j = 0; j < kSlot; ++j) v[i][j] = 0.f;
-      if (s < a.nslots) {
-        unpack8<T>(rx[i], v[i]);
-        if (a.res) {
-          float r[kSlot];
-          unpack8<T>(rr[i], r);
-#pragma unroll
-          for (int j = 0; j < kSlot; ++j) v[i][j] += r[j];
-        }
-        if (a.sum)
-          store8<T, VEC>(static_cast<T*>(a.sum) + (int64_t)t * a.lds + s * kSlot, n, v[i]);
-#pragma unroll
-        for (int j = 0; j < kSlot; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-        if (a.gamma) {
-          float g[kSlot];
-          load8<T, VEC>(static_cast<const T*>(a.gamma) + s * kSlot, n, g);
-#pragma unroll
-          for (int j = 0; j < kSlot; ++j) v[i][j] *= g[j];
-        }
-#pragma unroll
-        for (int j = 0; j < kSlot; ++j) amax = fmaxf(amax, fabsf(v[i][j]));
-      }
-    }
-    ss = warp_sum(ss);
-    amax = warp_max(amax);
-    if (nwarps > 1) {
-      if (lane == 0) part[turn][warp] = make_float2(ss, amax);
-      __syncthreads();
-      // every warp adds the warps' parts in the same order
-      const float2 p = lane < nwarps ? part[turn][lane] : make_float2(0.f, 0.f);
-      ss = warp_sum(p.x);
-      amax = warp_max(p.y);
-      turn ^= 1;  // the next row's parts go elsewhere, so one barrier a row is enough
-    }
-    const float rstd = 1.f / sqrtf(ss / (float)a.H + a.eps);
-    float pre = 1.f, inv = 0.f;
-    if (a.q && a.q_group == 0) {
-      code_factor(amax, most, &pre, &inv);
-      if (threadIdx.x == 0) a.scale[t] = rstd * amax / most;
-    }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int s = threadIdx.x + i * blockDim.x, n = min(kSlot, a.H - s * kSlot);
-      if (a.q && a.q_group > 0) {
-        // a group's slots lie in consecutive lanes of one warp (slots past the
-        // row hold zeros)
-        const int lanes = a.q_group / kSlot;
-        float m = 0.f;
-#pragma unroll
-        for (int j = 0; j < kSlot; ++j) m = fmaxf(m, fabsf(v[i][j]));
-        for (int o = lanes / 2; o > 0; o >>= 1)
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        code_factor(m, most, &pre, &inv);
-        if (s < a.nslots && lane % lanes == 0)
-          a.scale[(size_t)t * a.groups + s / lanes] = rstd * m / most;
-      }
-      if (s < a.nslots) {
-        if (a.q) store_codes<VEC>(a, (size_t)t * a.H + (size_t)s * kSlot, n, v[i], pre, inv);
-        if (a.y) {
-          float o[kSlot];
-#pragma unroll
-          for (int j = 0; j < kSlot; ++j) o[j] = v[i][j] * rstd;
-          store8<T, VEC>(static_cast<T*>(a.y) + (int64_t)t * a.ldy + s * kSlot, n, o);
-        }
-      }
-    }
+    norm_row<T, VPT, VEC>(a, t, rx, rr, sh, turn);
   }
 }
 
@@ -194,13 +213,17 @@ void launch_as(const Launch& L, const NormArgs& a, int threads, int rows) {
 template <typename T, bool VEC>
 void launch_norm(const Launch& L, const NormArgs& a) {
   const int slots32 = (a.nslots + 31) / 32;  // warps at one slot a thread
-  if (slots32 <= 4 && a.T > L.num_sms) {
-    // short rows of a large batch: a warp holds a row, four rows a CTA
-    launch_as<T, 4, VEC, 128>(L, a, 32, 4);
-  } else if (slots32 <= 32 && a.T <= L.num_sms) {
+  const bool wide = sizeof(T) == 4;
+  if (slots32 <= 32 && (a.T <= L.num_sms || (wide && slots32 <= 16))) {
     // few rows: one slot a thread, the shortest chain from load to store
+    // (64 rows of 7168 in bf16: 3.2 us, with two slots 3.6); fp32 rows of up to
+    // 4096 fill the SMs that way too (48 against 52 us for 4096 x 4096)
     launch_as<T, 1, VEC, 1024>(L, a, 32 * slots32, 1);
-  } else if (slots32 <= 32) {
+  } else if (slots32 <= 2) {
+    // short rows: a warp holds a row, four rows a CTA
+    launch_as<T, 2, VEC, 512>(L, a, 32, 4);
+  } else if (slots32 <= 32 && !wide) {
+    // two slots: several rows an SM in different phases (8192 x 7168: 89 us)
     launch_as<T, 2, VEC, 512>(L, a, 32 * ((slots32 + 1) / 2), 1);
   } else if (slots32 <= 64) {
     launch_as<T, 4, VEC, 512>(L, a, 32 * ((slots32 + 3) / 4), 1);
@@ -260,6 +283,7 @@ extern "C" moe_status moe_add_rmsnorm(int32_t T, int32_t H, int32_t dtype, const
   a.q_group = q_group;
   a.groups = q_group > 0 ? (H + q_group - 1) / q_group : 1;
   a.eps = eps;
+  a.inv_h = 1.f / (float)H;
   // whole slots at 16-byte aligned addresses in every row
   auto whole = [&](const void* p, int64_t ld) { return !p || T == 1 || ld * es % 16 == 0; };
   const bool vec = H % kSlot == 0 && whole(x, ldx) && whole(residual, ldr) && whole(sum, lds) &&

@@ -1,5 +1,6 @@
 // Row access shared by the operators around the layer (norm.cu, token_sort.cu,
-// w4_gemv.cu): a thread owns slots of eight consecutive channels, held in fp32.
+// w4_gemv.cu): a thread owns slots of eight consecutive channels, held in fp32;
+// and copies that run ahead of their use.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -52,12 +53,59 @@ __device__ __forceinline__ Raw8<T> load_raw8(const T* p, int n) {
   }
   return r;
 }
+// Two 16-bit values of one word to fp32 and back (rounded to nearest even).
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+  return make_float2(bf16lo(w), bf16hi(w));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+  __half2 h;
+  memcpy(&h, &w, 4);
+  return __half22float2(h);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  uint32_t w;
+  memcpy(&w, &h, 4);
+  return w;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  uint32_t w;
+  memcpy(&w, &h, 4);
+  return w;
+}
+
 template <typename T>
 __device__ __forceinline__ void unpack8(const Raw8<T>& r, float (&f)[kSlot]) {
-  T v[kSlot];
-  memcpy(v, &r, sizeof r);
+  if constexpr (sizeof(T) == 4) {
+    memcpy(f, &r, sizeof r);
+  } else {
+    const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
 #pragma unroll
-  for (int i = 0; i < kSlot; ++i) f[i] = to_f(v[i]);
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = unpack2<T>(w[i]);
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ Raw8<T> pack8(const float (&f)[kSlot]) {
+  Raw8<T> r;
+  if constexpr (sizeof(T) == 4)
+    memcpy(&r, f, sizeof r);
+  else
+    r.q[0] = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]),
+                        pack2<T>(f[6], f[7]));
+  return r;
 }
 template <typename T, bool VEC>
 __device__ __forceinline__ void load8(const T* p, int n, float (&f)[kSlot]) {
@@ -66,19 +114,51 @@ __device__ __forceinline__ void load8(const T* p, int n, float (&f)[kSlot]) {
 // Rounds to nearest even once, here.
 template <typename T, bool VEC>
 __device__ __forceinline__ void store8(T* p, int n, const float (&f)[kSlot]) {
-  T v[kSlot];
-#pragma unroll
-  for (int i = 0; i < kSlot; ++i) v[i] = from_f<T>(f[i]);
+  const Raw8<T> r = pack8<T>(f);
   if constexpr (VEC) {
-    Raw8<T> r;
-    memcpy(&r, v, sizeof r);
 #pragma unroll
     for (int i = 0; i < (int)(sizeof(r.q) / 16); ++i) reinterpret_cast<uint4*>(p)[i] = r.q[i];
   } else {
+    T v[kSlot];
+    memcpy(v, &r, sizeof r);
 #pragma unroll
     for (int i = 0; i < kSlot; ++i)
       if (i < n) p[i] = v[i];
   }
 }
 
+// max(m, |f[0]|, ..., |f[7]|), two values an instruction.
+__device__ __forceinline__ float max_abs8(float m, const float (&f)[kSlot]) {
+#pragma unroll
+  for (int i = 0; i < kSlot; i += 2)
+    asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(f[i]), "f"(f[i + 1]));
+  return m;
+}
+
+// ------------------------------------------------ asynchronous row copies ----
+// Global -> shared by the calling thread, past the L1; waited for by groups.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// real false: the 16 bytes become zeros, src is not read
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_unit(uint32_t dst, const void* src, int bytes) {
+  if (bytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else if (bytes == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 }  // namespace moe

@@ -59,30 +59,6 @@ struct W4Args {
   int64_t sbytes, zbytes;  // of the whole tensors
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-// real false: the 16 bytes become zeros, src is not read
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(real ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_unit(uint32_t dst, const void* src, int bytes) {
-  if (bytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else if (bytes == 8)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -137,6 +113,55 @@ __device__ __forceinline__ uint16_t lds_u16(uint32_t at) {
 __device__ __forceinline__ uint32_t lds_u8(uint32_t at) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// N consecutive 16-bit values from shared memory, in one load where they are
+// aligned to their size: two a word.
+template <int N>
+__device__ __forceinline__ void load_halves(bool whole, uint32_t at, uint32_t (&w)[(N + 1) / 2]) {
+  if (N > 1 && whole) {
+    if constexpr (N == 4)
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+    else
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+      w[i / 2] = lds_u16(at + 2 * i) | (i + 1 < N ? (uint32_t)lds_u16(at + 2 * i + 2) << 16 : 0u);
+  }
+}
+// N consecutive scales of four rows each, as fp32.
+template <typename T, int N>
+__device__ __forceinline__ void load_scales(bool whole, const uint32_t (&at)[4], uint32_t off,
+                                            float (&v)[4][N]) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[r][i] = lds_f32(at[r] + off + 4 * i);
+    } else {
+      uint32_t w[(N + 1) / 2];
+      load_halves<N>(whole, at[r] + off, w);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const float2 f = unpack2<T>(w[i / 2]);
+        v[r][i] = f.x;
+        if (i + 1 < N) v[r][i + 1] = f.y;
+      }
+    }
+  }
+}
+// N consecutive zero points, one a byte.
+template <int N>
+__device__ __forceinline__ uint32_t load_zeros(bool whole, uint32_t at) {
+  uint32_t v = 0u;
+  if (N == 4 && whole) {
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v |= lds_u8(at + i) << (8 * i);
+  }
   return v;
 }
 
@@ -216,6 +241,14 @@ constexpr int x_panel() {
   return kW4MaxRows * X::kRow;
 }
 
+// One thread's part in copying the scales (or zero points) of a weight row.
+struct W4Groups {
+  const unsigned char* from;  // its first unit of the next panel
+  uint32_t dst;               // where that goes in the first buffer
+  int unit, step;             // bytes of a unit, and from panel to panel
+  int panel, end, whole;      // bytes from `from` to the panel's, row's, tensor's end
+};
+
 // What a CTA works on.
 struct W4Tile {
   int e, n0, rank, split;
@@ -249,110 +282,111 @@ __device__ __forceinline__ void w4_pass(const W4Args& a, const W4Tile& t, int ro
   // Stage q of this warp: 128 channels from p0 * 512 + q * 256 + kw * 128 on, two
   // stages a panel.  The lane copies 16-byte piece lane % 4 of rows i * 8 +
   // lane / 4; pieces of a row are swizzled so that neither these writes nor
-  // ldmatrix meet a bank twice.  Pieces past K read the row's last one instead
-  // (x is zero there).
+  // ldmatrix meet a bank twice.  Pieces past K are left as they are: whatever codes
+  // lie there meet zeros of x.
   const int half = a.K / 2;  // bytes of a weight row
-  const uint8_t* wbase[2];
-  uint32_t wrow[4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) wbase[i] = a.w[a.up ? i : 0] + (int64_t)t.e * a.N * half;
+  const uint8_t* wp[4];      // the lane's pieces of the next stage to load
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    wrow[i] = (uint32_t)row_channel(nw * 32 + i * 8 + lane / 4) * (uint32_t)half;
-  int left = 2 * (t.p1 - t.p0);  // stages still to be loaded
-  uint32_t piece = (t.p0 * kW4Panel + kw * kW4Stage) / 2 + (lane % 4) * 16;
-  const uint32_t last = half - 16;
-  const uint32_t fill0 = ring + (lane / 4) * kW4RowBytes + (((lane % 4) ^ ((lane / 8) % 4)) * 16);
-  uint32_t fill = 0;
-  auto load_stage = [&]() {
-    if (left > 0) {
-      const uint32_t off = min(piece, last);
+    wp[i] = a.w[a.up ? i / 2 : 0] +
+            ((int64_t)t.e * a.N + row_channel(nw * 32 + i * 8 + lane / 4)) * half +
+            (t.p0 * kW4Panel + kw * kW4Stage) / 2 + (lane % 4) * 16;
+  // bytes of a row from this lane's piece of stage 0 to the row's (or the range's) end
+  const int wend = min(half, t.p1 * (kW4Panel / 2)) -
+                   ((t.p0 * kW4Panel + kw * kW4Stage) / 2 + (lane % 4) * 16);
+  const uint32_t fill = ring + (lane / 4) * kW4RowBytes + (((lane % 4) ^ ((lane / 8) % 4)) * 16);
+  // stage q into ring slot SLOT = q % kW4Stages; wp stands AHEAD stages before it
+  auto load_stage = [&](auto slot, auto ahead, int q) {
+    constexpr int kSlotAt = decltype(slot)::value * kW4StageBytes;
+    constexpr int kAhead = decltype(ahead)::value * (kW4Panel / 4);
+    if (q * (kW4Panel / 4) < wend)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        cp_async16(fill0 + fill + i * 8 * kW4RowBytes, wbase[i / 2] + (wrow[i] + off));
-    }
+        cp_async16(fill + kSlotAt + i * 8 * kW4RowBytes, wp[i] + kAhead);
     cp_async_commit();
-    --left;
-    piece += kW4Panel / 4;
-    fill = (fill + kW4StageBytes) % (kW4Stages * kW4StageBytes);
   };
 
-  // A panel of x, scales and zero points into buffer (p - p0) % 2, by all threads.
-  // x: 16-byte pieces of the present token rows, zeros past K.  Scales: thread
-  // tid takes row tid % 128, in units of sunit bytes from the last unit boundary
-  // at or before the row's first group (rows of odd lengths start inside one).
+  // A panel of x, scales and zero points into buffer BUF, by all threads; the
+  // pointers go on from panel to panel.  x: 16-byte pieces of the present token
+  // rows, zeros past K.  Scales and zero points: thread tid takes every second
+  // copy unit of row tid % 128, from the last unit boundary at or before the
+  // row's first group (rows of odd lengths start inside a unit).
   constexpr int kPieces = kW4Panel * X::kBytes / 16;  // of a token row
   constexpr int kTokStep = kW4Threads / kPieces;
-  const int tok0 = tid / kPieces, kx = (tid % kPieces) * (16 / X::kBytes);
+  const int tok0 = tid / kPieces;
+  int kx = t.p0 * kW4Panel + (tid % kPieces) * (16 / X::kBytes);
   const unsigned char* xp =
       static_cast<const unsigned char*>(a.x) + ((int64_t)(row + tok0) * a.K + kx) * X::kBytes;
   const int es = a.scale_dtype == MOE_DT_FP32 ? 4 : 2;
   auto first_group = [&](int i) {  // row i's first group
     return ((int64_t)t.e * a.N + row_channel(i)) * a.groups;
   };
-  struct Groups {
-    const unsigned char* from;  // the unit that holds the row's first group, then
-                                // this thread's half of the units
-    int end;                    // the row's end and the tensor's, from there
-    int whole;
-  };
-  const int srow0 = tid % kW4Rows, shalf = tid / kW4Rows;
-  const int smat = a.up ? (srow0 / 16) % 2 : 0;
-  auto groups_of = [&](const void* src, int bytes, int unit, int64_t tensor) {
-    const int64_t first = first_group(srow0) * bytes, at = first & ~(int64_t)(unit - 1);
-    Groups r;
-    r.from = static_cast<const unsigned char*>(src) + at;
-    r.end = (int)(first - at) + a.groups * bytes;
-    r.whole = (int)min(tensor - at, (int64_t)INT32_MAX);
+  auto groups_of = [&](const void* src, int bytes, int unit, int64_t tensor, uint32_t dst) {
+    W4Groups r;
+    const int64_t first = first_group(tid % kW4Rows) * bytes, at = first & ~(int64_t)(unit - 1);
+    const int64_t skip = a.groups > 1 ? (int64_t)t.p0 * kGroups * bytes : 0;
+    const int mine = tid / kW4Rows * unit;  // every second unit of the row
+    r.from = static_cast<const unsigned char*>(src) + at + skip + mine;
+    r.dst = dst + mine;
+    r.unit = unit;
+    r.step = a.groups > 1 ? kGroups * bytes : 0;
+    r.panel = (int)(first - at) + kGroups * bytes - mine;
+    r.end = (int)(first - at) + (int)(a.groups * bytes - skip) - mine;
+    r.whole = (int)min(tensor - at - skip - mine, (int64_t)INT32_MAX);
     return r;
   };
-  auto load_groups = [&](const Groups& r, int off, int seg, int unit, uint32_t dst) {
-    const int end = min(r.end, off + seg);
-    for (int i = off + shalf * unit; i < end; i += 2 * unit) {
-      if (i + unit <= r.whole) {
-        cp_async_unit(dst + (i - off), r.from + i, unit);
+  auto load_groups = [&](W4Groups& r, uint32_t off) {
+    const int end = min(r.end, r.panel);
+    for (int i = 0; i < end; i += 2 * r.unit) {
+      if (i + r.unit <= r.whole) {
+        cp_async_unit(r.dst + off + i, r.from + i, r.unit);
       } else {  // the tensor ends inside its last word
         for (int j = i; j < r.whole; ++j)
-          asm volatile("st.shared.u8 [%0], %1;" ::"r"(dst + (j - off)), "r"((uint32_t)r.from[j])
+          asm volatile("st.shared.u8 [%0], %1;" ::"r"(r.dst + off + j), "r"((uint32_t)r.from[j])
                        : "memory");
       }
     }
+    r.from += r.step;
+    r.end -= r.step;
+    r.whole -= r.step;
   };
-  const Groups sg = groups_of(a.s[smat], es, a.sunit, a.sbytes);
-  const int sseg = a.groups > 1 ? kGroups * es : 0, smis = sg.end - a.groups * es;
-  Groups zg{};
-  int zmis = 0;
-  if constexpr (ZEROS) {
-    zg = groups_of(a.z[smat], 1, a.zunit, a.zbytes);
-    zmis = zg.end - a.groups;
-  }
-  auto load_panel = [&](int p) {
-    const uint32_t buf = (p - t.p0) & 1;
-    const bool in = p * kW4Panel + kx < a.K;
+  const int smat = a.up ? (tid % kW4Rows / 16) % 2 : 0;
+  W4Groups sg = groups_of(a.s[smat], es, a.sunit, a.sbytes, scales + tid % kW4Rows * a.sstride);
+  W4Groups zg{};
+  if constexpr (ZEROS)
+    zg = groups_of(a.z[smat], 1, a.zunit, a.zbytes, zeros + tid % kW4Rows * a.zstride);
+  auto load_panel = [&](auto buf) {
+    constexpr int kBuf = decltype(buf)::value;
+    const bool in = kx < a.K;
 #pragma unroll
     for (int i = 0; i < NB * 8 / kTokStep; ++i)
       if (tok0 + i * kTokStep < m)
-        cp_async16_or_zero(xs + buf * x_panel<X>() + X::piece(tok0 + i * kTokStep, tid % kPieces),
-                           in ? xp + (int64_t)i * kTokStep * a.K * X::kBytes +
-                                    p * (kW4Panel * X::kBytes)
-                              : static_cast<const unsigned char*>(a.x),
-                           in);
-    load_groups(sg, p * sseg, kGroups * es + smis, a.sunit,
-                scales + (buf * kW4Rows + srow0) * a.sstride);
-    if constexpr (ZEROS)
-      load_groups(zg, a.groups > 1 ? p * kGroups : 0, kGroups + zmis, a.zunit,
-                  zeros + (buf * kW4Rows + srow0) * a.zstride);
+        cp_async16_or_zero(
+            xs + kBuf * x_panel<X>() + X::piece(tok0 + i * kTokStep, tid % kPieces),
+            in ? xp + (int64_t)i * kTokStep * a.K * X::kBytes
+               : static_cast<const unsigned char*>(a.x),
+            in);
+    kx += kW4Panel;
+    xp += kW4Panel * X::kBytes;
+    load_groups(sg, kBuf * kW4Rows * a.sstride);
+    if constexpr (ZEROS) load_groups(zg, kBuf * kW4Rows * a.zstride);
   };
-  // where this thread's four weight rows have their scales and zero points
+  // Where this thread's four weight rows have the scales and zero points of its
+  // first stage of a panel.  kGps groups a stage, in one load where rows are whole
+  // numbers of them.
+  constexpr int kGps = 4 / GS;
+  const bool one = a.groups == 1;
+  const bool whole = a.groups % kGps == 0;
   uint32_t srow[4], zrow[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = nw * 32 + g + i * 8;
-    srow[i] = scales + r * a.sstride + ((uint32_t)first_group(r) * es & (a.sunit - 1));
-    if constexpr (ZEROS) zrow[i] = zeros + r * a.zstride + ((uint32_t)first_group(r) & (a.zunit - 1));
+    srow[i] = scales + r * a.sstride + ((uint32_t)first_group(r) * es & (a.sunit - 1)) +
+              (one ? 0 : kw * kGps * es);
+    if constexpr (ZEROS)
+      zrow[i] = zeros + r * a.zstride + ((uint32_t)first_group(r) & (a.zunit - 1)) +
+                (one ? 0 : kw * kGps);
   }
-  const uint32_t gstep = a.groups > 1 ? es : 0;  // one scale a row: always the first
-  const uint32_t gstep_z = a.groups > 1 ? 1 : 0;
 
   // absent token rows are zero in both panels
   for (int i = m * kPieces + tid; i < NB * 8 * kPieces; i += kW4Threads)
@@ -362,84 +396,99 @@ __device__ __forceinline__ void w4_pass(const W4Args& a, const W4Tile& t, int ro
                                 X::piece(i / kPieces, i % kPieces)) = make_uint4(0u, 0u, 0u, 0u);
 
   float acc[2][NB][4] = {};
-  if (t.p0 < t.p1) load_panel(t.p0);  // completes with the first stage
+  auto c0 = std::integral_constant<int, 0>{};
+  auto c1 = std::integral_constant<int, 1>{};
+  auto c2 = std::integral_constant<int, 2>{};
+  auto c3 = std::integral_constant<int, 3>{};
+  if (t.p0 < t.p1) load_panel(c0);  // completes with the first stage
+  load_stage(c0, c0, 0);
+  load_stage(c1, c1, 1);
+  load_stage(c2, c2, 2);
+
+  // Stage SLOT of four: panel SLOT / 2 of the two at hand, its half SLOT % 2.
+  auto stage = [&](auto slot, int p) {
+    constexpr int kSlotN = decltype(slot)::value, kBuf = kSlotN / 2, kHalf = kSlotN % 2;
+    const int q = 2 * (p - t.p0) + kHalf;
+    if constexpr (kHalf == 0) {
+      // the panel came with the stage after this one (the first panel with the
+      // first); everybody is done with the panel before, whose buffer the next
+      // one takes
+      cp_async_wait<kW4Stages - 3>();
+      __syncthreads();
+      if (p + 1 < t.p1) load_panel(std::integral_constant<int, kBuf ^ 1>{});
+    } else {
+      cp_async_wait<kW4Stages - 2>();
+      __syncwarp();
+    }
+    load_stage(std::integral_constant<int, (kSlotN + 3) % 4>{},
+               std::integral_constant<int, kSlotN + 3>{}, q + 3);
+    const int k0 = p * kW4Panel + kHalf * (kW4Panel / 2) + kw * kW4Stage;
+    if (k0 >= a.K) return;  // warp-uniform; no scales there
+    const uint32_t st = ring + kSlotN * kW4StageBytes + lane * kW4RowBytes;
+    const uint32_t xb = xs + kBuf * x_panel<X>();
+
+    // the stage's scales and zero points, as they are
+    float sv[4][kGps];
+    uint32_t zv[4];
+    const uint32_t so = kBuf * kW4Rows * a.sstride + (one ? 0 : kHalf * 2 * kGps * es);
+    if (a.scale_dtype == MOE_DT_BF16)
+      load_scales<__nv_bfloat16, kGps>(whole, srow, so, sv);
+    else if (a.scale_dtype == MOE_DT_FP16)
+      load_scales<__half, kGps>(whole, srow, so, sv);
+    else
+      load_scales<float, kGps>(whole, srow, so, sv);
+    if constexpr (ZEROS)
 #pragma unroll
-  for (int q = 0; q < kW4Stages - 1; ++q) load_stage();
-  uint32_t use = 0;  // the ring stage in use
-  for (int p = t.p0; p < t.p1; ++p) {
-    const uint32_t buf = (p - t.p0) & 1;
-    const uint32_t xb = xs + buf * x_panel<X>();
+      for (int i = 0; i < 4; ++i)
+        zv[i] = load_zeros<kGps>(whole, zrow[i] + kBuf * kW4Rows * a.zstride +
+                                            (one ? 0 : kHalf * 2 * kGps)) & 0x1f1f1f1fu;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h == 0) {
-        // the panel came with the stage after this one (the first panel with the
-        // first); everybody is done with the panel before, whose buffer the next
-        // one takes
-        cp_async_wait<kW4Stages - 3>();
-        __syncthreads();
-        if (p + 1 < t.p1) load_panel(p + 1);
-      } else {
-        cp_async_wait<kW4Stages - 2>();
-        __syncwarp();
-      }
-      load_stage();
-      const uint32_t st = ring + use + lane * kW4RowBytes;
-      use = (use + kW4StageBytes) % (kW4Stages * kW4StageBytes);
-      const int k0 = p * kW4Panel + h * (kW4Panel / 2) + kw * kW4Stage;
+    for (int s0 = 0; s0 < 4; s0 += GS) {
+      if (k0 + s0 * 32 >= a.K) break;
+      uint32_t zc[4];
 #pragma unroll
-      for (int s0 = 0; s0 < 4; s0 += GS) {
-        if (k0 + s0 * 32 >= a.K) break;  // warp-uniform; no scales there
-        const uint32_t grp = (h * 8 + kw * 4 + s0) / GS;
-        uint32_t zc[4];
+      for (int i = 0; i < 4; ++i)
+        zc[i] = ZEROS ? __byte_perm(zv[i], M::kMagic >> 8, 0x4040 + (s0 / GS) * 0x0101)
+                      : M::kMagic + 0x00080008u;
+      float part[2][NB][4] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          zc[i] = M::kMagic + 0x00080008u;
-          if constexpr (ZEROS)
-            zc[i] = M::kMagic +
-                    (lds_u8(zrow[i] + buf * kW4Rows * a.zstride + grp * gstep_z) & 31u) *
-                        0x00010001u;
-        }
-        float part[2][NB][4] = {};
+      for (int s = s0; s < s0 + GS; ++s) {
+        uint32_t wv[4];  // first tile rows g, g + 8; second tile rows g, g + 8
+        ldmatrix_x4(st + ((s ^ ((lane / 2) % 4)) * 16), wv);
+        uint32_t bf[NB][4];
 #pragma unroll
-        for (int s = s0; s < s0 + GS; ++s) {
-          uint32_t wv[4];  // first tile rows g, g + 8; second tile rows g, g + 8
-          ldmatrix_x4(st + ((s ^ ((lane / 2) % 4)) * 16), wv);
-          uint32_t bf[NB][4];
-#pragma unroll
-          for (int b = 0; b < NB; ++b) X::operands(xb, b * 8 + g, c, h * 8 + kw * 4 + s, bf[b]);
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t af[4] = {dequant_pair<M>(wv[2 * u], 2 * i, zc[2 * u]),
-                                      dequant_pair<M>(wv[2 * u + 1], 2 * i, zc[2 * u + 1]),
-                                      dequant_pair<M>(wv[2 * u], 2 * i + 1, zc[2 * u]),
-                                      dequant_pair<M>(wv[2 * u + 1], 2 * i + 1, zc[2 * u + 1])};
-#pragma unroll
-              for (int b = 0; b < NB; ++b) M::mma(part[u][b], af, bf[b][2 * i], bf[b][2 * i + 1]);
-            }
-        }
-        float sv[4];
-        const uint32_t so = buf * kW4Rows * a.sstride + grp * gstep;
-        if (a.scale_dtype == MOE_DT_BF16) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sv[i] = bf16_to_f(lds_u16(srow[i] + so));
-        } else if (a.scale_dtype == MOE_DT_FP16) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sv[i] = __half2float(__ushort_as_half(lds_u16(srow[i] + so)));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sv[i] = lds_f32(srow[i] + so);
-        }
+        for (int b = 0; b < NB; ++b)
+          X::operands(xb, b * 8 + g, c, kHalf * 8 + kw * 4 + s, bf[b]);
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t af[4] = {dequant_pair<M>(wv[2 * u], 2 * i, zc[2 * u]),
+                                    dequant_pair<M>(wv[2 * u + 1], 2 * i, zc[2 * u + 1]),
+                                    dequant_pair<M>(wv[2 * u], 2 * i + 1, zc[2 * u]),
+                                    dequant_pair<M>(wv[2 * u + 1], 2 * i + 1, zc[2 * u + 1])};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              acc[u][b][j] = fmaf(sv[2 * u + j / 2], part[u][b][j], acc[u][b][j]);
+            for (int b = 0; b < NB; ++b) M::mma(part[u][b], af, bf[b][2 * i], bf[b][2 * i + 1]);
+          }
       }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[u][b][j] = fmaf(sv[2 * u + j / 2][s0 / GS], part[u][b][j], acc[u][b][j]);
     }
+  };
+  for (int p = t.p0; p < t.p1; p += 2) {
+    stage(c0, p);
+    stage(c1, p);
+    if (p + 1 < t.p1) {
+      stage(c2, p + 1);
+      stage(c3, p + 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wp[i] += 4 * (kW4Panel / 4);
   }
   cp_async_wait<0>();
   __syncthreads();
