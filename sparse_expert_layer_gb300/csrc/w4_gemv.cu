@@ -34,7 +34,6 @@ constexpr int kW4Threads = 32 * kW4Warps;
 constexpr int kW4Rows = 128;               // weight rows of a CTA
 constexpr int kW4Panel = 512;              // K of a panel of x and scales
 constexpr int kW4Stage = 128;              // K of a ring stage
-constexpr int kW4MaxRows = 16;              // token rows of one pass over the weights
 constexpr int kW4RowBytes = kW4Stage / 2;  // 64: four 16-byte pieces, swizzled
 constexpr int kW4StageBytes = 32 * kW4RowBytes;
 constexpr int kW4XStride = kW4Panel * 2 + 64;  // token rows 64 bytes apart modulo the banks
@@ -85,6 +84,12 @@ struct MmaBf16 {
 };
 struct MmaFp16 {
   static constexpr uint32_t kMagic = 0x64006400u;  // 1024
+  // a / 16 + b
+  static __device__ __forceinline__ uint32_t sixteenth(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(0x2c002c00u), "r"(b));
+    return d;
+  }
   static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -218,28 +223,42 @@ struct XInt8 {
   }
 };
 
-// A weight word holds channels k0 .. k7, a nibble each, k0 lowest: pair i is
-// (q(k_i) - z, q(k_{i+4}) - z) in 16 bits each, exact.
-template <typename M>
-__device__ __forceinline__ uint32_t dequant_pair(uint32_t w, int i, uint32_t zero) {
-  // (shifted & mask) | magic in one instruction; the compiler alone makes it two
+// (w & mask) | magic in one instruction; the compiler alone makes it two.
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
   uint32_t v;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;"
-      : "=r"(v)
-      : "r"(w >> (4 * i)), "r"(0x000f000fu), "r"(M::kMagic));
-  return M::sub(v, zero);
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(w), "r"(mask), "r"(magic));
+  return v;
+}
+// A weight word holds channels k0 .. k7, a nibble each, k0 lowest.  Pair i is
+// (q(k_i) - z, q(k_{i+4}) - z) in 16 bits each, exact.  zero[0] holds magic + z;
+// fp16 has room for a nibble four bits up as well (1024 + 16 q, exact), which
+// saves two of three shifts: zero[1] holds -(64 + z) for those.
+template <typename M>
+__device__ __forceinline__ void dequant(uint32_t w, const uint32_t (&zero)[2], uint32_t (&p)[4]) {
+  if constexpr (std::is_same<M, MmaFp16>::value) {
+    const uint32_t v = w >> 8;
+    p[0] = M::sub(and_or(w, 0x000f000fu, M::kMagic), zero[0]);
+    p[1] = M::sixteenth(and_or(w, 0x00f000f0u, M::kMagic), zero[1]);
+    p[2] = M::sub(and_or(v, 0x000f000fu, M::kMagic), zero[0]);
+    p[3] = M::sixteenth(and_or(v, 0x00f000f0u, M::kMagic), zero[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i] = M::sub(and_or(w >> (4 * i), 0x000f000fu, M::kMagic), zero[0]);
+  }
 }
 
 // Shared memory: the warps' rings, then two panels of x, scales and zero points;
-// the parts of a sum lie over the rings once those are drained.  With 128 rows of
-// 16-bit scales two CTAs fit an SM for every group size.
+// the parts of a sum lie over the rings once those are drained.  With 16-bit
+// scales two CTAs fit an SM for every group size.  (A variant for eight token
+// rows with 80 registers and three CTAs an SM was no faster: 32.0 against 30.3 us
+// for 38912 x 6144.)
+constexpr int kW4MaxRows = 16;  // token rows of one pass over the weights
 constexpr int kW4Stages = 4;
 constexpr int kW4Ring = kW4Warps * kW4Stages * kW4StageBytes;
 static_assert(kW4MaxRows * kW4RedStride * 4 <= kW4Ring, "the parts fit over the rings");
 template <typename X>
-constexpr int x_panel() {
-  return kW4MaxRows * X::kRow;
-}
+constexpr int kW4XPanel = kW4MaxRows* X::kRow;
 
 // One thread's part in copying the scales (or zero points) of a weight row.
 struct W4Groups {
@@ -263,14 +282,15 @@ __device__ __forceinline__ void w4_pass(const W4Args& a, const W4Tile& t, int ro
                                         unsigned char* smem) {
   using M = typename X::Mma;
   constexpr int kGroups = 16 / GS;  // of a panel
+  constexpr int kStages = kW4Stages, kRing = kW4Ring, kXPanel = kW4XPanel<X>;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int nw = warp % 4, kw = warp / 4;
   const int g = lane / 4, c = lane % 4;
   const uint32_t base = smem_u32(smem);
-  const uint32_t xs = base + kW4Ring;
-  const uint32_t scales = xs + 2 * x_panel<X>();
+  const uint32_t xs = base + kRing;
+  const uint32_t scales = xs + 2 * kXPanel;
   const uint32_t zeros = scales + 2 * kW4Rows * a.sstride;
-  const uint32_t ring = base + warp * kW4Stages * kW4StageBytes;
+  const uint32_t ring = base + warp * kStages * kW4StageBytes;
 
   // Weight row i (0 .. 127) of the CTA belongs to warp tile i / 32; with a second
   // matrix rows 0-15 of a warp tile are the first's, 16-31 the second's, of 16
@@ -285,28 +305,32 @@ __device__ __forceinline__ void w4_pass(const W4Args& a, const W4Tile& t, int ro
   // ldmatrix meet a bank twice.  Pieces past K are left as they are: whatever codes
   // lie there meet zeros of x.
   const int half = a.K / 2;  // bytes of a weight row
-  const uint8_t* wp[4];      // the lane's pieces of the next stage to load
+  const uint8_t* wp[4];      // the lane's pieces of the next stage to be loaded
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     wp[i] = a.w[a.up ? i / 2 : 0] +
             ((int64_t)t.e * a.N + row_channel(nw * 32 + i * 8 + lane / 4)) * half +
             (t.p0 * kW4Panel + kw * kW4Stage) / 2 + (lane % 4) * 16;
-  // bytes of a row from this lane's piece of stage 0 to the row's (or the range's) end
-  const int wend = min(half, t.p1 * (kW4Panel / 2)) -
-                   ((t.p0 * kW4Panel + kw * kW4Stage) / 2 + (lane % 4) * 16);
-  const uint32_t fill = ring + (lane / 4) * kW4RowBytes + (((lane % 4) ^ ((lane / 8) % 4)) * 16);
-  // stage q into ring slot SLOT = q % kW4Stages; wp stands AHEAD stages before it
-  auto load_stage = [&](auto slot, auto ahead, int q) {
-    constexpr int kSlotAt = decltype(slot)::value * kW4StageBytes;
-    constexpr int kAhead = decltype(ahead)::value * (kW4Panel / 4);
-    if (q * (kW4Panel / 4) < wend)
+  // bytes from there to the end of the row, or of this CTA's range
+  int wleft = min(half, t.p1 * (kW4Panel / 2)) -
+              ((t.p0 * kW4Panel + kw * kW4Stage) / 2 + (lane % 4) * 16);
+  const uint32_t fill0 = ring + (lane / 4) * kW4RowBytes + (((lane % 4) ^ ((lane / 8) % 4)) * 16);
+  uint32_t fill = 0, use = 0;  // the ring stages to be filled and to be used next
+  auto next = [](uint32_t& at) {
+    at = at == (kStages - 1) * kW4StageBytes ? 0 : at + kW4StageBytes;
+  };
+  auto load_stage = [&]() {
+    if (wleft > 0)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        cp_async16(fill + kSlotAt + i * 8 * kW4RowBytes, wp[i] + kAhead);
+      for (int i = 0; i < 4; ++i) cp_async16(fill0 + fill + i * 8 * kW4RowBytes, wp[i]);
     cp_async_commit();
+    wleft -= kW4Panel / 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wp[i] += kW4Panel / 4;
+    next(fill);
   };
 
-  // A panel of x, scales and zero points into buffer BUF, by all threads; the
+  // A panel of x, scales and zero points into buffer `buf`, by all threads; the
   // pointers go on from panel to panel.  x: 16-byte pieces of the present token
   // rows, zeros past K.  Scales and zero points: thread tid takes every second
   // copy unit of row tid % 128, from the last unit boundary at or before the
@@ -355,21 +379,20 @@ __device__ __forceinline__ void w4_pass(const W4Args& a, const W4Tile& t, int ro
   W4Groups zg{};
   if constexpr (ZEROS)
     zg = groups_of(a.z[smat], 1, a.zunit, a.zbytes, zeros + tid % kW4Rows * a.zstride);
-  auto load_panel = [&](auto buf) {
-    constexpr int kBuf = decltype(buf)::value;
+  auto load_panel = [&](int buf) {
     const bool in = kx < a.K;
 #pragma unroll
     for (int i = 0; i < NB * 8 / kTokStep; ++i)
       if (tok0 + i * kTokStep < m)
         cp_async16_or_zero(
-            xs + kBuf * x_panel<X>() + X::piece(tok0 + i * kTokStep, tid % kPieces),
+            xs + buf * kXPanel + X::piece(tok0 + i * kTokStep, tid % kPieces),
             in ? xp + (int64_t)i * kTokStep * a.K * X::kBytes
                : static_cast<const unsigned char*>(a.x),
             in);
     kx += kW4Panel;
     xp += kW4Panel * X::kBytes;
-    load_groups(sg, kBuf * kW4Rows * a.sstride);
-    if constexpr (ZEROS) load_groups(zg, kBuf * kW4Rows * a.zstride);
+    load_groups(sg, buf * kW4Rows * a.sstride);
+    if constexpr (ZEROS) load_groups(zg, buf * kW4Rows * a.zstride);
   };
   // Where this thread's four weight rows have the scales and zero points of its
   // first stage of a panel.  kGps groups a stage, in one load where rows are whole
@@ -392,45 +415,40 @@ __device__ __forceinline__ void w4_pass(const W4Args& a, const W4Tile& t, int ro
   for (int i = m * kPieces + tid; i < NB * 8 * kPieces; i += kW4Threads)
 #pragma unroll
     for (int b = 0; b < 2; ++b)
-      *reinterpret_cast<uint4*>(smem + kW4Ring + b * x_panel<X>() +
+      *reinterpret_cast<uint4*>(smem + kRing + b * kXPanel +
                                 X::piece(i / kPieces, i % kPieces)) = make_uint4(0u, 0u, 0u, 0u);
 
   float acc[2][NB][4] = {};
-  auto c0 = std::integral_constant<int, 0>{};
-  auto c1 = std::integral_constant<int, 1>{};
-  auto c2 = std::integral_constant<int, 2>{};
-  auto c3 = std::integral_constant<int, 3>{};
-  if (t.p0 < t.p1) load_panel(c0);  // completes with the first stage
-  load_stage(c0, c0, 0);
-  load_stage(c1, c1, 1);
-  load_stage(c2, c2, 2);
+  if (t.p0 < t.p1) load_panel(0);  // completes with the first stage
+#pragma unroll
+  for (int q = 0; q < kStages - 1; ++q) load_stage();
 
-  // Stage SLOT of four: panel SLOT / 2 of the two at hand, its half SLOT % 2.
-  auto stage = [&](auto slot, int p) {
-    constexpr int kSlotN = decltype(slot)::value, kBuf = kSlotN / 2, kHalf = kSlotN % 2;
-    const int q = 2 * (p - t.p0) + kHalf;
+  // One stage: half HALF of panel p, whose x and scales are in buffer `buf`.
+  auto stage = [&](auto which, int p, int buf) {
+    constexpr int kHalf = decltype(which)::value;
     if constexpr (kHalf == 0) {
-      // the panel came with the stage after this one (the first panel with the
+      // The panel came with the stage after this one (the first panel with the
       // first); everybody is done with the panel before, whose buffer the next
-      // one takes
-      cp_async_wait<kW4Stages - 3>();
+      // one takes.
+      cp_async_wait<kStages - 3>();
       __syncthreads();
-      if (p + 1 < t.p1) load_panel(std::integral_constant<int, kBuf ^ 1>{});
+      if (p + 1 < t.p1) load_panel(buf ^ 1);
     } else {
-      cp_async_wait<kW4Stages - 2>();
+      cp_async_wait<kStages - 2>();
       __syncwarp();
     }
-    load_stage(std::integral_constant<int, (kSlotN + 3) % 4>{},
-               std::integral_constant<int, kSlotN + 3>{}, q + 3);
+    load_stage();
+    const uint32_t at = use;
+    next(use);
     const int k0 = p * kW4Panel + kHalf * (kW4Panel / 2) + kw * kW4Stage;
     if (k0 >= a.K) return;  // warp-uniform; no scales there
-    const uint32_t st = ring + kSlotN * kW4StageBytes + lane * kW4RowBytes;
-    const uint32_t xb = xs + kBuf * x_panel<X>();
+    const uint32_t st = ring + at + lane * kW4RowBytes;
+    const uint32_t xb = xs + buf * kXPanel;
 
     // the stage's scales and zero points, as they are
     float sv[4][kGps];
     uint32_t zv[4];
-    const uint32_t so = kBuf * kW4Rows * a.sstride + (one ? 0 : kHalf * 2 * kGps * es);
+    const uint32_t so = buf * kW4Rows * a.sstride + (one ? 0 : kHalf * 2 * kGps * es);
     if (a.scale_dtype == MOE_DT_BF16)
       load_scales<__nv_bfloat16, kGps>(whole, srow, so, sv);
     else if (a.scale_dtype == MOE_DT_FP16)
@@ -440,16 +458,19 @@ __device__ __forceinline__ void w4_pass(const W4Args& a, const W4Tile& t, int ro
     if constexpr (ZEROS)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        zv[i] = load_zeros<kGps>(whole, zrow[i] + kBuf * kW4Rows * a.zstride +
+        zv[i] = load_zeros<kGps>(whole, zrow[i] + buf * kW4Rows * a.zstride +
                                             (one ? 0 : kHalf * 2 * kGps)) & 0x1f1f1f1fu;
 #pragma unroll
     for (int s0 = 0; s0 < 4; s0 += GS) {
       if (k0 + s0 * 32 >= a.K) break;
-      uint32_t zc[4];
+      uint32_t zc[4][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        zc[i] = ZEROS ? __byte_perm(zv[i], M::kMagic >> 8, 0x4040 + (s0 / GS) * 0x0101)
-                      : M::kMagic + 0x00080008u;
+      for (int i = 0; i < 4; ++i) {
+        zc[i][0] = ZEROS ? __byte_perm(zv[i], M::kMagic >> 8, 0x4040 + (s0 / GS) * 0x0101)
+                         : M::kMagic + 0x00080008u;
+        // fp16: 960 - (1024 + z); bf16 has no use for it
+        zc[i][1] = ZEROS ? M::sub(0x63806380u, zc[i][0]) : 0xd480d480u;
+      }
       float part[2][NB][4] = {};
 #pragma unroll
       for (int s = s0; s < s0 + GS; ++s) {
@@ -460,16 +481,17 @@ __device__ __forceinline__ void w4_pass(const W4Args& a, const W4Tile& t, int ro
         for (int b = 0; b < NB; ++b)
           X::operands(xb, b * 8 + g, c, kHalf * 8 + kw * 4 + s, bf[b]);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+          uint32_t lo[4], hi[4];  // rows g and g + 8
+          dequant<M>(wv[2 * u], zc[2 * u], lo);
+          dequant<M>(wv[2 * u + 1], zc[2 * u + 1], hi);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t af[4] = {dequant_pair<M>(wv[2 * u], 2 * i, zc[2 * u]),
-                                    dequant_pair<M>(wv[2 * u + 1], 2 * i, zc[2 * u + 1]),
-                                    dequant_pair<M>(wv[2 * u], 2 * i + 1, zc[2 * u]),
-                                    dequant_pair<M>(wv[2 * u + 1], 2 * i + 1, zc[2 * u + 1])};
+            const uint32_t af[4] = {lo[2 * i], hi[2 * i], lo[2 * i + 1], hi[2 * i + 1]};
 #pragma unroll
             for (int b = 0; b < NB; ++b) M::mma(part[u][b], af, bf[b][2 * i], bf[b][2 * i + 1]);
           }
+        }
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -480,15 +502,9 @@ __device__ __forceinline__ void w4_pass(const W4Args& a, const W4Tile& t, int ro
             acc[u][b][j] = fmaf(sv[2 * u + j / 2][s0 / GS], part[u][b][j], acc[u][b][j]);
     }
   };
-  for (int p = t.p0; p < t.p1; p += 2) {
-    stage(c0, p);
-    stage(c1, p);
-    if (p + 1 < t.p1) {
-      stage(c2, p + 1);
-      stage(c3, p + 1);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) wp[i] += 4 * (kW4Panel / 4);
+  for (int p = t.p0; p < t.p1; ++p) {
+    stage(std::integral_constant<int, 0>{}, p, (p - t.p0) & 1);
+    stage(std::integral_constant<int, 1>{}, p, (p - t.p0) & 1);
   }
   cp_async_wait<0>();
   __syncthreads();
@@ -614,9 +630,10 @@ void launch_as(const Launch& L, W4Args a, int split) {
     a.zstride = stride(kGroups, a.zunit, a.groups % a.zunit != 0);
     a.zbytes = (int64_t)a.E * a.N * a.groups;
   }
-  const int smem = kW4Ring + 2 * x_panel<X>() + 2 * kW4Rows * (a.sstride + a.zstride);
+  constexpr int kFixed = kW4Ring + 2 * kW4XPanel<X>;
+  const int smem = kFixed + 2 * kW4Rows * (a.sstride + a.zstride);
   // at most: fp32 scales of groups of 32 and their zero points
-  constexpr int kMost = kW4Ring + 2 * x_panel<X>() + 2 * kW4Rows * (96 + 48);
+  constexpr int kMost = kFixed + 2 * kW4Rows * (96 + 48);
   constexpr int kSlotX = std::is_same<X, XBf16>::value ? 0 : std::is_same<X, XFp16>::value ? 1 : 2;
   constexpr int kSlotIndex = (kSlotX * 3 + GS / 2) * 2 + ZEROS;
   static_assert(kSlotIndex < kAttrW4Slots, "one slot for each variant");
@@ -624,8 +641,8 @@ void launch_as(const Launch& L, W4Args a, int split) {
                      kAttrW4Base + kSlotIndex);
   const dim3 grid(split, (a.N + a.channels - 1) / a.channels, a.E);
   launch_begin(L, MOE_K_W4);
-  launch_kernel_cluster(w4_gemv_kernel<X, GS, ZEROS>, grid, dim3(split), dim3(kW4Threads), smem,
-                        L.stream, a);
+  launch_kernel_cluster(w4_gemv_kernel<X, GS, ZEROS>, grid, dim3(split), dim3(kW4Threads),
+                        smem, L.stream, a);
   launch_end(L, MOE_K_W4);
 }
 
