@@ -67,23 +67,33 @@ __device__ __forceinline__ uint32_t e4m3_codes(const float* v, float factor) {
   return (lo & 0xffffu) | (hi << 16);
 }
 
+// The codes of a slot; factor[j] belongs to its channel j.
 template <bool VEC>
-__device__ __forceinline__ void store_codes(const NormArgs& a, size_t at, int n, float (&v)[kSlot],
-                                            float pre, float inv) {
-  if (pre != 1.f) {  // the same for the whole row or group
+__device__ __forceinline__ void store_codes(const NormArgs& a, int t, int s, float (&v)[kSlot],
+                                            const float (&pre)[kSlot], const float (&inv)[kSlot]) {
+  uint8_t* q = static_cast<uint8_t*>(a.q) + (size_t)t * a.H;
+  if constexpr (VEC) {  // one factor: a slot lies inside its group
+    if (pre[0] != 1.f) {
 #pragma unroll
-    for (int j = 0; j < kSlot; ++j) v[j] *= pre;
-  }
-  uint32_t w[2];
+      for (int j = 0; j < kSlot; ++j) v[j] *= pre[0];
+    }
+    uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) w[i] = a.q_e4m3 ? e4m3_codes(v + 4 * i, inv) : int8_codes(v + 4 * i, inv);
-  uint8_t* q = static_cast<uint8_t*>(a.q) + at;
-  if constexpr (VEC) {
-    *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+    for (int i = 0; i < 2; ++i)
+      w[i] = a.q_e4m3 ? e4m3_codes(v + 4 * i, inv[0]) : int8_codes(v + 4 * i, inv[0]);
+    *reinterpret_cast<uint2*>(q + s * kSlot) = make_uint2(w[0], w[1]);
   } else {
 #pragma unroll
-    for (int i = 0; i < kSlot; ++i)
-      if (i < n) q[i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+    for (int j = 0; j < kSlot; ++j) v[j] *= pre[j] * inv[j];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w = a.q_e4m3 ? e4m3_codes(v + 4 * i, 1.f) : int8_codes(v + 4 * i, 1.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = slot_channel<!VEC>(s, 4 * i + j);
+        if (c < a.H) q[c] = (uint8_t)(w >> (8 * j));
+      }
+    }
   }
 }
 
@@ -105,10 +115,10 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int t, const Raw8<T>
   float ss = 0.f, amax = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int s = threadIdx.x + i * blockDim.x, n = min(kSlot, a.H - s * kSlot);
+    const int s = threadIdx.x + i * blockDim.x;
 #pragma unroll
     for (int j = 0; j < kSlot; ++j) v[i][j] = 0.f;
-    if (s < a.nslots) {
+    if (slot_inside<!VEC>(s, a.nslots)) {
       unpack8<T>(rx[i], v[i]);
       if (a.res) {
         float r[kSlot];
@@ -116,13 +126,12 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int t, const Raw8<T>
 #pragma unroll
         for (int j = 0; j < kSlot; ++j) v[i][j] += r[j];
       }
-      if (a.sum)
-        store8<T, VEC>(static_cast<T*>(a.sum) + (int64_t)t * a.lds + s * kSlot, n, v[i]);
+      if (a.sum) store8<T, VEC>(static_cast<T*>(a.sum) + (int64_t)t * a.lds, s, a.H, v[i]);
 #pragma unroll
       for (int j = 0; j < kSlot; ++j) ss = fmaf(v[i][j], v[i][j], ss);
       if (a.gamma) {
         float g[kSlot];
-        load8<T, VEC>(static_cast<const T*>(a.gamma) + s * kSlot, n, g);
+        load8<T, VEC>(static_cast<const T*>(a.gamma), s, a.H, g);
 #pragma unroll
         for (int j = 0; j < kSlot; ++j) v[i][j] *= g[j];
       }
@@ -145,39 +154,65 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int t, const Raw8<T>
     turn ^= 1;
   }
   const float rstd = rsqrtf(fmaf(ss, a.inv_h, a.eps));
-  float pre = 1.f, inv = 0.f;
+  float pre[kSlot], inv[kSlot];
   if (a.q && a.q_group == 0) {
-    code_factor(amax, most, &pre, &inv);
+    code_factor(amax, most, &pre[0], &inv[0]);
+#pragma unroll
+    for (int j = 1; j < kSlot; ++j) {
+      pre[j] = pre[0];
+      inv[j] = inv[0];
+    }
     if (threadIdx.x == 0) a.scale[t] = rstd * amax * unit;
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int s = threadIdx.x + i * blockDim.x, n = min(kSlot, a.H - s * kSlot);
-    if (a.y && s < a.nslots) {
+    const int s = threadIdx.x + i * blockDim.x;
+    const bool inside = slot_inside<!VEC>(s, a.nslots);
+    if (a.y && inside) {
       float o[kSlot];
 #pragma unroll
       for (int j = 0; j < kSlot; ++j) o[j] = v[i][j] * rstd;
-      store8<T, VEC>(static_cast<T*>(a.y) + (int64_t)t * a.ldy + s * kSlot, n, o);
+      store8<T, VEC>(static_cast<T*>(a.y) + (int64_t)t * a.ldy, s, a.H, o);
     }
     if (!a.q) continue;
-    if (a.q_group > 0) {
-      // a group's slots lie in consecutive lanes of one warp (slots past the
-      // row hold zeros)
+    // a group lies inside a warp's 256 channels (channels past the row are zero)
+    if (VEC && a.q_group > 0) {  // the slots of consecutive lanes
       const int lanes = a.q_group / kSlot;
       float m = max_abs8(0.f, v[i]);
       for (int o = lanes / 2; o > 0; o >>= 1)
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      code_factor(m, most, &pre, &inv);
-      if (s < a.nslots && lane % lanes == 0)
+      code_factor(m, most, &pre[0], &inv[0]);
+      if (inside && lane % lanes == 0)
         a.scale[(size_t)t * a.groups + s / lanes] = rstd * m * unit;
     }
-    if (s < a.nslots)
-      store_codes<VEC>(a, (size_t)t * a.H + (size_t)s * kSlot, n, v[i], pre, inv);
+    if (!VEC && a.q_group > 0) {  // channels j of all lanes, for q_group / 32 values of j
+      const int each = a.q_group / 32;
+      float m[kSlot];
+#pragma unroll
+      for (int j = 0; j < kSlot; ++j) m[j] = all_max(fabsf(v[i][j]));
+#pragma unroll
+      for (int o = 1; o < kSlot; o <<= 1)  // over aligned runs of `each`
+        if (o < each) {
+          float n[kSlot];
+#pragma unroll
+          for (int j = 0; j < kSlot; ++j) n[j] = fmaxf(m[j], m[j ^ o]);
+#pragma unroll
+          for (int j = 0; j < kSlot; ++j) m[j] = n[j];
+        }
+#pragma unroll
+      for (int j = 0; j < kSlot; ++j) {
+        code_factor(m[j], most, &pre[j], &inv[j]);
+        const int c = slot_channel<!VEC>(s, j);
+        if (inside && lane == 0 && j % each == 0 && c < a.H)
+          a.scale[(size_t)t * a.groups + c / a.q_group] = rstd * m[j] * unit;
+      }
+    }
+    if (inside) store_codes<VEC>(a, t, s, v[i], pre, inv);
   }
 }
 
-// blockDim.x threads work on one row, blockDim.y rows at a time; slot i of a
-// row belongs to thread i % blockDim.x.
+// blockDim.x threads work on one row, blockDim.y rows at a time; slot s of a
+// row belongs to thread s % blockDim.x.
 template <typename T, int VPT, bool VEC, int MAXT>
 __global__ void __launch_bounds__(MAXT, VPT == 2 && sizeof(T) == 2 ? 2 : 1) add_rmsnorm_kernel(NormArgs a) {
   pdl_enter();
@@ -189,10 +224,10 @@ __global__ void __launch_bounds__(MAXT, VPT == 2 && sizeof(T) == 2 ? 2 : 1) add_
     Raw8<T> rx[VPT], rr[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int s = threadIdx.x + i * blockDim.x, n = min(kSlot, a.H - s * kSlot);
-      if (s < a.nslots) {
-        rx[i] = load_raw8<T, VEC>(x + s * kSlot, n);
-        if (a.res) rr[i] = load_raw8<T, VEC>(res + s * kSlot, n);
+      const int s = threadIdx.x + i * blockDim.x;
+      if (slot_inside<!VEC>(s, a.nslots)) {
+        rx[i] = load_raw8<T, VEC>(x, s, a.H);
+        if (a.res) rr[i] = load_raw8<T, VEC>(res, s, a.H);
       }
     }
     norm_row<T, VPT, VEC>(a, t, rx, rr, sh, turn);

@@ -12,9 +12,21 @@ namespace moe {
 
 constexpr int kSlot = 8;  // channels of one slot
 
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+// Slot s of a row of H channels, s = lane modulo 32: channels 8 s .. 8 s + 7, one
+// vector access where rows are whole slots at 16-byte boundaries (VEC).  SPREAD,
+// for other rows: the 32 slots of a warp share 256 channels and a slot takes every
+// 32nd of them, so that a warp's element-wise accesses lie side by side (4096 rows
+// of 7161 through the norm: 191 us with eight neighbours a thread).
+template <bool SPREAD>
+__device__ __forceinline__ int slot_channel(int s, int j) {
+  return SPREAD ? (s & ~31) * kSlot + j * 32 + (s & 31) : s * kSlot + j;
+}
+// Whether slot s has any channel of the row's nslots slots.
+template <bool SPREAD>
+__device__ __forceinline__ bool slot_inside(int s, int nslots) {
+  return (SPREAD ? s & ~31 : s) < nslots;
+}
+
 template <typename T>
 __device__ __forceinline__ T from_f(float v);
 template <>
@@ -37,18 +49,21 @@ struct alignas(16) Raw8 {
   uint4 q[sizeof(T) * kSlot / 16];
 };
 
-// The slot's raw words.  VEC: the slot is whole and 16-byte aligned.  Otherwise
-// its first n (1 .. 8) channels are loaded one by one and the rest are zero.
-template <typename T, bool VEC>
-__device__ __forceinline__ Raw8<T> load_raw8(const T* p, int n) {
+// The raw words of slot s of a row (channels past H are zero).
+template <typename T, bool VEC, bool SPREAD = !VEC>
+__device__ __forceinline__ Raw8<T> load_raw8(const T* row, int s, int H) {
   Raw8<T> r;
   if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < (int)(sizeof(r.q) / 16); ++i) r.q[i] = reinterpret_cast<const uint4*>(p)[i];
+    for (int i = 0; i < (int)(sizeof(r.q) / 16); ++i)
+      r.q[i] = reinterpret_cast<const uint4*>(row + s * kSlot)[i];
   } else {
     T v[kSlot];
 #pragma unroll
-    for (int i = 0; i < kSlot; ++i) v[i] = i < n ? p[i] : from_f<T>(0.f);
+    for (int j = 0; j < kSlot; ++j) {
+      const int c = slot_channel<SPREAD>(s, j);
+      v[j] = c < H ? row[c] : from_f<T>(0.f);
+    }
     memcpy(&r, v, sizeof r);
   }
   return r;
@@ -107,23 +122,26 @@ __device__ __forceinline__ Raw8<T> pack8(const float (&f)[kSlot]) {
                         pack2<T>(f[6], f[7]));
   return r;
 }
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, int n, float (&f)[kSlot]) {
-  unpack8<T>(load_raw8<T, VEC>(p, n), f);
+template <typename T, bool VEC, bool SPREAD = !VEC>
+__device__ __forceinline__ void load8(const T* row, int s, int H, float (&f)[kSlot]) {
+  unpack8<T>(load_raw8<T, VEC, SPREAD>(row, s, H), f);
 }
 // Rounds to nearest even once, here.
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* p, int n, const float (&f)[kSlot]) {
+template <typename T, bool VEC, bool SPREAD = !VEC>
+__device__ __forceinline__ void store8(T* row, int s, int H, const float (&f)[kSlot]) {
   const Raw8<T> r = pack8<T>(f);
   if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < (int)(sizeof(r.q) / 16); ++i) reinterpret_cast<uint4*>(p)[i] = r.q[i];
+    for (int i = 0; i < (int)(sizeof(r.q) / 16); ++i)
+      reinterpret_cast<uint4*>(row + s * kSlot)[i] = r.q[i];
   } else {
     T v[kSlot];
     memcpy(v, &r, sizeof r);
 #pragma unroll
-    for (int i = 0; i < kSlot; ++i)
-      if (i < n) p[i] = v[i];
+    for (int j = 0; j < kSlot; ++j) {
+      const int c = slot_channel<SPREAD>(s, j);
+      if (c < H) row[c] = v[j];
+    }
   }
 }
 
