@@ -75,8 +75,7 @@ struct MmaBf16 {
   }
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                              uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -97,8 +96,7 @@ struct MmaFp16 {
   }
   static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                              uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -445,6 +443,16 @@ __device__ __forceinline__ void w4_pass(const W4Args& a, const W4Tile& t, int ro
     const uint32_t st = ring + at + lane * kW4RowBytes;
     const uint32_t xb = xs + buf * kXPanel;
 
+    // the operands of a 32-wide step, loaded a step ahead of their use: weights of
+    // the first tile's rows g, g + 8 and the second's, and x
+    uint32_t wn[4], bn[NB][4];
+    auto load_step = [&](int s) {
+      ldmatrix_x4(st + ((s ^ ((lane / 2) % 4)) * 16), wn);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) X::operands(xb, b * 8 + g, c, kHalf * 8 + kw * 4 + s, bn[b]);
+    };
+    load_step(0);
+
     // the stage's scales and zero points, as they are
     float sv[4][kGps];
     uint32_t zv[4];
@@ -474,12 +482,14 @@ __device__ __forceinline__ void w4_pass(const W4Args& a, const W4Tile& t, int ro
       float part[2][NB][4] = {};
 #pragma unroll
       for (int s = s0; s < s0 + GS; ++s) {
-        uint32_t wv[4];  // first tile rows g, g + 8; second tile rows g, g + 8
-        ldmatrix_x4(st + ((s ^ ((lane / 2) % 4)) * 16), wv);
-        uint32_t bf[NB][4];
+        uint32_t wv[4], bf[NB][4];
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          X::operands(xb, b * 8 + g, c, kHalf * 8 + kw * 4 + s, bf[b]);
+        for (int i = 0; i < 4; ++i) {
+          wv[i] = wn[i];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) bf[b][i] = bn[b][i];
+        }
+        if (s < 3) load_step(s + 1);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           uint32_t lo[4], hi[4];  // rows g and g + 8
