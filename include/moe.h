@@ -378,7 +378,7 @@ moe_status moe_unsort_tokens_backward(int32_t T, int32_t k, int32_t n_experts, i
  * times x and their sums over a group are exact products added in fp32; scales
  * are applied in fp32; out is rounded once.  Any number of rows is taken; an
  * expert's weights are read once for every 16 rows.
- *  K            a multiple of 32 and of group; N * K < 2^32
+ *  N, K         K a multiple of 32 and of group; N <= 2^21, K <= 2^22, N * K < 2^32
  *  group        channels that share a scale: 32, 64, 128, or 0 (one scale a row)
  *  offsets      int32 [n_experts + 1], device; NULL: one expert, all R rows
  *  x_dtype      MOE_DT_BF16, MOE_DT_FP16, or MOE_DT_INT8 (codes, with x_scale)

@@ -291,12 +291,11 @@ extern "C" moe_status moe_add_rmsnorm(int32_t T, int32_t H, int32_t dtype, const
   if (q && q_dtype != MOE_DT_INT8 && q_dtype != MOE_DT_E4M3) return MOE_ERR_INVALID_ARG;
   if (q && q_group != 0 && q_group != 32 && q_group != 64 && q_group != 128 && q_group != 256)
     return MOE_ERR_INVALID_ARG;
-  if (!sum && !y && !q) return MOE_ERR_INVALID_ARG;
   if (H > kNormMaxHidden) return MOE_ERR_UNSUPPORTED;
   if (ldx < H || (residual && ldr < H) || (sum && lds < H) || (y && ldy < H))
     return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
-  if (!x || (q && !q_scale)) return MOE_ERR_INVALID_ARG;
+  if (!x || (q && !q_scale) || (!sum && !y && !q)) return MOE_ERR_INVALID_ARG;
   if (misaligned16(x, residual, gamma, sum, y, q, q ? q_scale : nullptr)) return MOE_ERR_ALIGNMENT;
   const int es = dtype == MOE_DT_FP32 ? 4 : 2;
   NormArgs a{};

@@ -25,10 +25,10 @@ constexpr int kSortThreads = 256;
 constexpr int kSortBlockPicks = 256;  // most picks one CTA of the counting passes takes
 // Small batches: every CTA finds its token's positions by itself, reading all
 // ids; T CTAs compare R picks each, so the limit is on T * R too.  One launch
-// against four: 256 tokens x 8 picks 5.8 against 8.7 us, but 512 x 8 12.3 against
-// 9.7 and 4096 x 1 25 against 12 us.
+// against four: 512 tokens x 8 picks 7.5 against 9.7 us, 1400 x 1 7.9 against 9.7,
+// but 1024 x 4 11.3 against 10.1 (rows of 1024 bf16 channels).
 constexpr int kSortDirectPicks = 4096;
-constexpr int64_t kSortDirectWork = 1 << 20;
+constexpr int64_t kSortDirectWork = 1 << 21;
 bool sort_direct(int64_t T, int64_t k) {
   return T * k <= kSortDirectPicks && T * T * k <= kSortDirectWork;
 }

@@ -720,8 +720,8 @@ extern "C" moe_status moe_w4_gemv(int32_t n_experts, int32_t N, int32_t K, int32
   if ((w_up != nullptr) != (scales_up != nullptr) || (zeros_up && !w_up) ||
       (w_up && (zeros != nullptr) != (zeros_up != nullptr)))
     return MOE_ERR_INVALID_ARG;
-  // 32-bit offsets inside one expert's matrix
-  if (n_experts > kW4MaxExperts || N > (1 << 22) || K > (1 << 22) ||
+  // 32-bit offsets inside one expert's matrix; at most 65535 row tiles
+  if (n_experts > kW4MaxExperts || N > (1 << 21) || K > (1 << 22) ||
       (int64_t)N * (K / 2) > INT32_MAX)
     return MOE_ERR_UNSUPPORTED;
   if (R == 0) return MOE_OK;

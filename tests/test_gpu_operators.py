@@ -758,3 +758,50 @@ def test_example_block_against_64_bits(m):
     within(block.out, want, half_step(want, BF16) + (2.0**-8) * size, "block output")
     losses = ex.train()
     assert losses[-1] < 0.9 * losses[0]
+
+
+def test_empty_batches_on_the_device(m):
+    i32 = dict(dtype=torch.int32, device="cuda")
+    x = torch.empty(0, 64, device="cuda", dtype=BF16)
+    m.moe_add_rmsnorm(x, None, None, 1e-6, x.clone())
+    ids = torch.empty(0, 2, **i32)
+    p, xs, _ = run_sort(m, ids, 5, x)
+    assert (p["counts"] == 0).all() and (p["offsets"] == 0).all() and xs.shape == (0, 64)
+    m.moe_unsort_tokens(xs, p["offsets"], p["e2s"], torch.empty(0, 2, device="cuda"), x)
+    out = torch.empty(0, 8, device="cuda")
+    m.moe_w4_gemv(x, None, torch.zeros(3, **i32), torch.zeros(2, 8, 32, dtype=torch.uint8,
+                                                              device="cuda"),
+                  torch.ones(2, 8, 1, device="cuda"), None, out)
+    torch.cuda.synchronize()
+
+
+def test_refused_sizes_raise_and_leave_the_context_usable(m):
+    x = torch.zeros(4, 64, device="cuda", dtype=BF16)
+    with pytest.raises(m.MoeError, match="misaligned"):
+        m.moe_add_rmsnorm(torch.zeros(300, device="cuda", dtype=BF16)[4:260].view(4, 64), None, None,
+                          1e-6, x)
+    with pytest.raises(ValueError, match="shape"):
+        m.moe_add_rmsnorm(x, x[:2], None, 1e-6, x)
+    with pytest.raises(ValueError, match="not on CUDA device"):
+        m.moe_add_rmsnorm(x, x.cpu(), None, 1e-6, x)
+    with pytest.raises(TypeError, match="gamma"):
+        m.moe_add_rmsnorm(x, None, torch.ones(64, device="cuda"), 1e-6, x)
+    ids = torch.zeros(9000, 4, dtype=torch.int32, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    plan = (torch.empty(8, **i32), torch.empty(9, **i32), torch.empty(36000, **i32),
+            torch.empty(36000, **i32))
+    with pytest.raises(m.MoeError, match="invalid"):
+        m.moe_sort_tokens(8, ids, None, None, *plan, None)  # no workspace
+    m.moe_add_rmsnorm(x, None, None, 1e-6, x)
+    torch.cuda.synchronize()
+
+
+def test_launches_are_counted(m):
+    before = m.launch_counts()
+    x = torch.zeros(4, 64, device="cuda", dtype=BF16)
+    m.moe_add_rmsnorm(x, None, None, 1e-6, x)
+    run_sort(m, torch.zeros(4, 2, dtype=torch.int32, device="cuda"), 4, x)
+    after = m.launch_counts()
+    assert after["norm"] == before["norm"] + 1
+    assert after["sort_rows"] == before["sort_rows"] + 1
+    assert after["sort_plan"] == before["sort_plan"]
