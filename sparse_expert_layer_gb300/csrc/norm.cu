@@ -91,8 +91,9 @@ __device__ __forceinline__ void store_codes(const NormArgs& a, int t, int s, flo
       w[i] = a.q_e4m3 ? e4m3_codes(v + 4 * i, inv[0]) : int8_codes(v + 4 * i, inv[0]);
     *reinterpret_cast<uint2*>(q + s * kSlot) = make_uint2(w[0], w[1]);
   } else {
+    // one after the other: the product of the factors may overflow
 #pragma unroll
-    for (int j = 0; j < kSlot; ++j) v[j] *= pre[j] * inv[j];
+    for (int j = 0; j < kSlot; ++j) v[j] = v[j] * pre[j] * inv[j];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t w = a.q_e4m3 ? e4m3_codes(v + 4 * i, 1.f) : int8_codes(v + 4 * i, 1.f);

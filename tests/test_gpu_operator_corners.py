@@ -1,0 +1,78 @@
+"""Corners of the operators around the layer: values at the ends of the fp32
+range, tensors that autograd watches, plans and ids of any layout."""
+import pytest
+import torch
+
+from tests import gpu_support as gs
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0**-24
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+INT8, E4M3 = torch.int8, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def m():
+    return gs.lib()
+
+
+def gen(seed=0):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def strided(t, extra):
+    """The same matrix with `extra` further channels between its rows."""
+    wide = torch.full((t.shape[0], t.shape[1] + extra), 5.0, device=t.device, dtype=t.dtype)
+    wide[:, :t.shape[1]] = t
+    return wide[:, :t.shape[1]]
+
+
+def norm_codes(m, x, qdt, group, eps=1e-6, gamma=None):
+    """(y, codes as fp32, scale) of a norm without a residual."""
+    T, H = x.shape
+    y = torch.full((T, H), 7.0, device="cuda", dtype=x.dtype)
+    q = torch.full((T, H), 7, device="cuda", dtype=INT8).view(qdt)
+    scale = torch.full((T, -(-H // group) if group else 1), -1.0, device="cuda")
+    m.moe_add_rmsnorm(x, None, gamma, eps, None, y, q, scale, group)
+    torch.cuda.synchronize()
+    return y, q.to(FP32), scale
+
+
+# ------------------------------------------------- norm: rows of tiny values --
+# Whole numbers p of at most 127 times 2^e, 127 in every group and zeros between:
+# the codes are known without rounding.  int8: p itself.  e4m3: p * 448 / 127,
+# which lies at least 2^-10 of itself away from the middle of two codes unless it
+# is one of them, so an fp32 error does not change it.
+TINY = [(FP32, -149), (FP32, -133), (BF16, -133), (FP32, -103), (FP32, -102), (FP32, -60),
+        (BF16, -60)]
+
+
+@pytest.mark.parametrize("dtype,e", TINY)
+@pytest.mark.parametrize("H,extra", [(256, 0), (256, 8), (256, 3), (255, 0), (257, 0), (33, 0),
+                                     (2056, 0), (2051, 0)])
+@pytest.mark.parametrize("qdt", [INT8, E4M3])
+@pytest.mark.parametrize("group", [0, 32, 256])
+def test_codes_of_tiny_rows(m, dtype, e, H, extra, qdt, group):
+    g = gen(H + group)
+    p = torch.randint(-127, 128, (3, H), generator=g, device="cuda").double()
+    p[torch.rand(3, H, generator=g, device="cuda") < 0.2] = 0
+    p[:, ::32] = 127
+    p[1, ::32] = -127
+    p[2] = 0
+    p[2, H - 1] = 127  # one channel alone; its row has groups of zeros
+    x = (p * 2.0**e).to(dtype)
+    assert torch.equal(x.double(), p * 2.0**e)
+    if extra:
+        x = strided(x, extra)
+    _, code, scale = norm_codes(m, x, qdt, group)
+    want = p if qdt == INT8 else (p * 448 / 127).to(FP32).to(E4M3).double()
+    assert torch.equal(code.double(), want)
+    # scale = max|y| / most: the mean and its root within 32 u (halved), two
+    # products and the rounded 1 / most, each a step of the subnormals at worst
+    width = group or H
+    G = scale.shape[1]
+    rms = torch.sqrt((x.double() ** 2).mean(-1, keepdim=True) + 1e-6)
+    amax = torch.nn.functional.pad(x.double().abs(), (0, G * width - H)).view(3, G, width).amax(-1)
+    want = amax / rms / (127 if qdt == INT8 else 448)
+    assert ((scale.double() - want).abs() <= 36 * U * want + 2.0**-149).all()
