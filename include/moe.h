@@ -288,8 +288,11 @@ typedef enum {
  *   e4m3:  scale = max|y| / 448, code = y / scale rounded to e4m3
  * r, y and the code's quotient are fp32, each rounded once where it is stored
  * (the norm takes r before that rounding).  A row (group) of zeros has scale 0
- * and codes 0; where r holds a NaN or an infinity the scale is NaN, or the
- * group's codes stand for zeros (a finite group beside an infinity).
+ * and codes 0 (with eps = 0 too; its y is 0 then); where r holds a NaN or an
+ * infinity the scale is NaN, or the group's codes stand for zeros (a finite group
+ * beside an infinity).  Squares are summed in fp32: a finite row whose sum is
+ * 2^128 or more has NaN y and scales, and without eps squares below 2^-126 lose
+ * their precision, down to infinite y and scales where none is left.
  *  dtype     MOE_DT_BF16, MOE_DT_FP16 or MOE_DT_FP32: x, residual, gamma, sum, y
  *  x         [T, H], row stride ldx; 1 <= H <= 32768
  *  residual  [T, H], row stride ldr, or NULL (r = x)

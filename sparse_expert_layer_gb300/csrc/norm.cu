@@ -162,7 +162,12 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int t, const Raw8<T>
     amax = all_max(p.y);
     turn ^= 1;
   }
-  const float rstd = rsqrtf(fmaf(ss, a.inv_h, a.eps));
+  const float mean = fmaf(ss, a.inv_h, a.eps);
+  float rstd = rsqrtf(mean);
+  // a row of zeros without eps is zeros, not 0 * inf; a finite row whose squares
+  // overflowed shows as NaN instead of passing for zeros
+  if (mean == 0.f && amax == 0.f) rstd = 0.f;
+  if (isinf(mean) && !isinf(amax)) rstd = __int_as_float(0x7fffffff);
   float pre[kSlot], inv[kSlot];
   if (a.q && a.q_group == 0) {
     code_factor(amax, most, &pre[0], &inv[0]);

@@ -76,3 +76,48 @@ def test_codes_of_tiny_rows(m, dtype, e, H, extra, qdt, group):
     amax = torch.nn.functional.pad(x.double().abs(), (0, G * width - H)).view(3, G, width).amax(-1)
     want = amax / rms / (127 if qdt == INT8 else 448)
     assert ((scale.double() - want).abs() <= 36 * U * want + 2.0**-149).all()
+
+
+# ------------------------------------- norm: the ends of the fp32 statistics --
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("H", [64, 256, 257, 1000, 7161])
+@pytest.mark.parametrize("qdt", [INT8, E4M3])
+@pytest.mark.parametrize("group", [0, 32])
+def test_zero_rows_without_eps(m, dtype, H, qdt, group):
+    x = torch.randn(4, H, generator=gen(H), device="cuda").to(dtype)
+    rest = [norm_codes(m, x, qdt, group, eps=0.0)]
+    x[1] = 0
+    x[3] = -0.0
+    y, code, scale = norm_codes(m, x, qdt, group, eps=0.0)
+    for t in (y, code, scale):
+        assert (t[[1, 3]] == 0).all()
+    for got, before in zip((y, code, scale), rest[0]):
+        assert torch.equal(got[[0, 2]], before[[0, 2]]) and torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("H", [256, 257, 4100])
+@pytest.mark.parametrize("group", [0, 32])
+def test_rows_past_the_range_of_the_squares_show(m, dtype, H, group):
+    x = torch.ones(5, H, device="cuda", dtype=dtype)
+    x[1] = 2.0**66
+    x[2, 7] = -(2.0**64)
+    x[4] = 2.0**56  # squares of 2^112: inside
+    y, _, scale = norm_codes(m, x, INT8, group)
+    assert torch.isnan(y[[1, 2]]).all() and torch.isnan(scale[[1, 2]]).all()
+    for r in (0, 3, 4):
+        assert ((y[r].double() - 1).abs() <= 2.0**-8 + 32 * U).all()
+        assert ((scale[r].double() * 127 - 1).abs() <= 2.0**-19).all()
+
+
+@pytest.mark.parametrize("H", [256, 257])
+def test_rows_whose_squares_vanish_show_without_eps(m, H):
+    # 2^-90 squared is below fp32: nothing is left to divide by
+    x = torch.full((2, H), 2.0**-90, device="cuda")
+    x[:, 3] = 0
+    y, code, scale = norm_codes(m, x, INT8, 0, eps=0.0)
+    assert torch.isinf(scale).all() and not torch.isfinite(y).any()
+    y, code, scale = norm_codes(m, x, INT8, 0, eps=1e-20)
+    want = x.double() * 1e10
+    assert ((y.double() - want).abs() <= 32 * U * want).all()
+    assert torch.equal(code, 127 * (x > 0).float())
