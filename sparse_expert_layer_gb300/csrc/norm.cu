@@ -232,7 +232,8 @@ __global__ void __launch_bounds__(MAXT, VPT == 2 && sizeof(T) == 2 ? 2 : 1) add_
   pdl_enter();
   __shared__ NormParts sh;
   int turn = 0;
-  for (int t = blockIdx.x * blockDim.y + threadIdx.y; t < a.T; t += gridDim.x * blockDim.y) {
+  const int step = gridDim.x * blockDim.y;
+  for (int t = blockIdx.x * blockDim.y + threadIdx.y; t < a.T; t += step) {
     const T* x = static_cast<const T*>(a.x) + (int64_t)t * a.ldx;
     const T* res = static_cast<const T*>(a.res) + (int64_t)t * a.ldr;
     Raw8<T> rx[VPT], rr[VPT];
@@ -245,6 +246,7 @@ __global__ void __launch_bounds__(MAXT, VPT == 2 && sizeof(T) == 2 ? 2 : 1) add_
       }
     }
     norm_row<T, VPT, VEC>(a, t, rx, rr, sh, turn);
+    if (t >= a.T - step) break;  // of 2^31 - 1 rows, t + step may lie past an int
   }
 }
 

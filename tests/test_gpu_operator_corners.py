@@ -121,3 +121,14 @@ def test_rows_whose_squares_vanish_show_without_eps(m, H):
     want = x.double() * 1e10
     assert ((y.double() - want).abs() <= 32 * U * want).all()
     assert torch.equal(code, 127 * (x > 0).float())
+
+
+def test_norm_of_as_many_rows_as_an_int_counts(m):
+    # the last rows' successors lie past 2^31 - 1
+    T = 2**31 - 1
+    x = torch.zeros(T, 1, device="cuda", dtype=BF16)
+    x[-30000:] = torch.randn(30000, 1, generator=gen(), device="cuda").to(BF16)
+    out = torch.full((T, 1), 7.0, device="cuda", dtype=BF16)
+    m.moe_add_rmsnorm(x, None, None, 1e-6, out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, x)
