@@ -264,23 +264,23 @@ void launch_as(const Launch& L, const NormArgs& a, int threads, int rows) {
 template <typename T, bool VEC>
 void launch_norm(const Launch& L, const NormArgs& a) {
   const int slots32 = (a.nslots + 31) / 32;  // warps at one slot a thread
-  const bool wide = sizeof(T) == 4;
+  constexpr bool wide = sizeof(T) == 4;
   if (slots32 <= 32 && (a.T <= L.num_sms || (wide && slots32 <= 16))) {
     // few rows: one slot a thread, the shortest chain from load to store
     // (64 rows of 7168 in bf16: 3.2 us, with two slots 3.6); fp32 rows of up to
     // 4096 fill the SMs that way too (48 against 52 us for 4096 x 4096)
-    launch_as<T, 1, VEC, 1024>(L, a, 32 * slots32, 1);
-  } else if (slots32 <= 2) {
-    // short rows: a warp holds a row, four rows a CTA
-    launch_as<T, 2, VEC, 512>(L, a, 32, 4);
-  } else if (slots32 <= 32 && !wide) {
-    // two slots: several rows an SM in different phases (8192 x 7168: 89 us)
-    launch_as<T, 2, VEC, 512>(L, a, 32 * ((slots32 + 1) / 2), 1);
-  } else if (slots32 <= 64) {
-    launch_as<T, 4, VEC, 512>(L, a, 32 * ((slots32 + 3) / 4), 1);
-  } else {
-    launch_as<T, 4, VEC, 1024>(L, a, 32 * ((slots32 + 3) / 4), 1);
+    return launch_as<T, 1, VEC, 1024>(L, a, 32 * slots32, 1);
   }
+  if constexpr (!wide) {
+    // short rows: a warp holds a row, four rows a CTA
+    if (slots32 <= 2) return launch_as<T, 2, VEC, 512>(L, a, 32, 4);
+    // two slots: several rows an SM in different phases (8192 x 7168: 89 us)
+    if (slots32 <= 32) return launch_as<T, 2, VEC, 512>(L, a, 32 * ((slots32 + 1) / 2), 1);
+  }
+  if (slots32 <= 64)
+    launch_as<T, 4, VEC, 512>(L, a, 32 * ((slots32 + 3) / 4), 1);
+  else
+    launch_as<T, 4, VEC, 1024>(L, a, 32 * ((slots32 + 3) / 4), 1);
 }
 
 template <typename T>
