@@ -32,6 +32,7 @@
 #include <algorithm>
 
 #include "rows.cuh"
+#include "w4_plan.h"
 
 namespace moe {
 
@@ -47,7 +48,6 @@ constexpr int kW4RowBytes = kW4Stage / 2;  // 64: four 16-byte pieces, swizzled
 constexpr int kW4StageBytes = 32 * kW4RowBytes;
 constexpr int kW4XStride = kW4Panel * 2 + 64;  // token rows 64 bytes apart modulo the banks
 constexpr int kW4RedStride = kW4Rows + 4;
-constexpr int kW4MaxSplit = 8;
 
 struct W4Args {
   const int32_t* offsets;  // [E + 1], nullptr: one expert with all R rows
@@ -665,26 +665,10 @@ void launch_as(const Launch& L, W4Args a, int split) {
   launch_end(L, MOE_K_W4);
 }
 
-// How many CTAs share a row tile's K: the split with the least time by a count
-// of panels.  A CTA takes the time of its panels and of about two more to start
-// and to add the parts.  Two CTAs fit an SM, and a cluster stays inside a GPC
-// of 16 to 20 SMs, so larger clusters leave some slots empty.
 int choose_split(const W4Args& a, int num_sms) {
   const int64_t tiles = (int64_t)((a.N + a.channels - 1) / a.channels) *
                         std::min(a.E, a.R);  // experts with rows, at most
-  const int panels = (a.K + kW4Panel - 1) / kW4Panel;
-  int best = 1;
-  int64_t least = INT64_MAX;
-  for (int split = 1; split <= std::min(kW4MaxSplit, panels); split *= 2) {
-    const int64_t slots = split == 1 ? 2 * num_sms : num_sms / 19 * (36 / split * split);
-    const int64_t rounds = (tiles * split + slots - 1) / slots;
-    const int64_t cost = rounds * ((panels + split - 1) / split + 2);
-    if (cost < least) {
-      least = cost;
-      best = split;
-    }
-  }
-  return best;
+  return w4_choose_split(tiles, (a.K + kW4Panel - 1) / kW4Panel, num_sms);
 }
 
 template <typename X, int GS>
