@@ -41,7 +41,6 @@ namespace {
 constexpr int kW4MaxExperts = 4096;
 constexpr int kW4Warps = 8;
 constexpr int kW4Threads = 32 * kW4Warps;
-constexpr int kW4Rows = 128;               // weight rows of a CTA
 constexpr int kW4Panel = 512;              // K of a panel of x and scales
 constexpr int kW4Stage = 128;              // K of a ring stage
 constexpr int kW4RowBytes = kW4Stage / 2;  // 64: four 16-byte pieces, swizzled
@@ -256,10 +255,10 @@ __device__ __forceinline__ void dequant(uint32_t w, const uint32_t (&zero)[2], u
 }
 
 // Shared memory: the warps' rings, then two panels of x, scales and zero points;
-// the parts of a sum lie over the rings once those are drained.  With 16-bit
-// scales two CTAs fit an SM for every group size.  (A variant for eight token
-// rows with 80 registers and three CTAs an SM was no faster: 32.0 against 30.3 us
-// for 38912 x 6144.)
+// the parts of a sum lie over the rings once those are drained.  Two CTAs fit an
+// SM, except for 16-bit x with fp32 scales of groups of 32 (w4_memory).  (A variant
+// for eight token rows with 80 registers and three CTAs an SM was no faster: 32.0
+// against 30.3 us for 38912 x 6144.)
 constexpr int kW4MaxRows = 16;  // token rows of one pass over the weights
 constexpr int kW4Stages = 4;
 constexpr int kW4Ring = kW4Warps * kW4Stages * kW4StageBytes;
@@ -623,34 +622,23 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_gemv_kernel(W4Args a) {
   }
 }
 
-// The copy unit of rows of `row` bytes whose panels hold `panel` bytes: the
-// widest that both are multiples of, or 4 with rows that start inside a unit.
-int copy_unit(int64_t row, int panel) {
-  for (int u = 16; u > 4; u /= 2)
-    if (row % u == 0 && panel % u == 0) return u;
-  return 4;
-}
-
 template <typename X, int GS, bool ZEROS>
-void launch_as(const Launch& L, W4Args a, int split) {
-  constexpr int kGroups = 16 / GS;
+void launch_as(const Launch& L, W4Args a) {
   const int es = a.scale_dtype == MOE_DT_FP32 ? 4 : 2;
-  // a row's panel, one word more where rows may start inside a unit, and an odd
-  // number of copy units where that costs little, against bank conflicts
-  auto stride = [](int bytes, int unit, bool inside) {
-    const int n = (bytes + (inside ? unit : 0) + unit - 1) / unit;
-    return (n > 1 && n % 2 == 0 ? n + 1 : n) * unit;
-  };
-  a.sunit = copy_unit((int64_t)a.groups * es, kGroups * es);
-  a.sstride = stride(kGroups * es, a.sunit, (int64_t)a.groups * es % a.sunit != 0);
+  constexpr int kFixed = kW4Ring + 2 * kW4XPanel<X>;
+  const W4Memory mem = w4_memory(kFixed, a.groups, 16 / GS, es, ZEROS);
+  a.sunit = mem.sunit;
+  a.sstride = mem.sstride;
   a.sbytes = (int64_t)a.E * a.N * a.groups * es;
   if (ZEROS) {
-    a.zunit = copy_unit(a.groups, kGroups);
-    a.zstride = stride(kGroups, a.zunit, a.groups % a.zunit != 0);
+    a.zunit = mem.zunit;
+    a.zstride = mem.zstride;
     a.zbytes = (int64_t)a.E * a.N * a.groups;
   }
-  constexpr int kFixed = kW4Ring + 2 * kW4XPanel<X>;
-  const int smem = kFixed + 2 * kW4Rows * (a.sstride + a.zstride);
+  const int row_tiles = (a.N + a.channels - 1) / a.channels;
+  const int experts = std::min(a.E, a.R);  // with rows, at most
+  const int split = w4_choose_split((int64_t)row_tiles * experts,
+                                    (a.K + kW4Panel - 1) / kW4Panel, L.num_sms, mem.per_sm);
   // at most: fp32 scales of groups of 32 and their zero points
   constexpr int kMost = kFixed + 2 * kW4Rows * (96 + 48);
   constexpr int kSlotX = std::is_same<X, XBf16>::value ? 0 : std::is_same<X, XFp16>::value ? 1 : 2;
@@ -658,35 +646,28 @@ void launch_as(const Launch& L, W4Args a, int split) {
   static_assert(kSlotIndex < kAttrW4Slots, "one slot for each variant");
   set_smem_attr_once(reinterpret_cast<const void*>(w4_gemv_kernel<X, GS, ZEROS>), kMost,
                      kAttrW4Base + kSlotIndex);
-  const dim3 grid(split, (a.N + a.channels - 1) / a.channels, a.E);
+  const dim3 grid(split, row_tiles, a.E);
   launch_begin(L, MOE_K_W4);
   launch_kernel_cluster(w4_gemv_kernel<X, GS, ZEROS>, grid, dim3(split), dim3(kW4Threads),
-                        smem, L.stream, a);
+                        mem.bytes, L.stream, a);
   launch_end(L, MOE_K_W4);
 }
 
-int choose_split(const W4Args& a, int num_sms) {
-  const int64_t tiles = (int64_t)((a.N + a.channels - 1) / a.channels) *
-                        std::min(a.E, a.R);  // experts with rows, at most
-  return w4_choose_split(tiles, (a.K + kW4Panel - 1) / kW4Panel, num_sms);
-}
-
 template <typename X, int GS>
-void launch_zeros(const Launch& L, const W4Args& a, int split) {
+void launch_zeros(const Launch& L, const W4Args& a) {
   if (a.z[0])
-    launch_as<X, GS, true>(L, a, split);
+    launch_as<X, GS, true>(L, a);
   else
-    launch_as<X, GS, false>(L, a, split);
+    launch_as<X, GS, false>(L, a);
 }
 template <typename X>
 void launch_w4(const Launch& L, const W4Args& a) {
-  const int split = choose_split(a, L.num_sms);
   if (a.group == 32)
-    launch_zeros<X, 1>(L, a, split);
+    launch_zeros<X, 1>(L, a);
   else if (a.group == 64)
-    launch_zeros<X, 2>(L, a, split);
+    launch_zeros<X, 2>(L, a);
   else
-    launch_zeros<X, 4>(L, a, split);
+    launch_zeros<X, 4>(L, a);
 }
 
 }  // namespace

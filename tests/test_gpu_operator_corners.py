@@ -132,3 +132,16 @@ def test_norm_of_as_many_rows_as_an_int_counts(m):
     m.moe_add_rmsnorm(x, None, None, 1e-6, out)
     torch.cuda.synchronize()
     assert torch.equal(out, x)
+
+
+# ------------------------------------ 4 bits: rows of scales of every alignment --
+@pytest.mark.parametrize("K,group", [(256, 32), (768, 32), (2304, 32), (128, 32), (1152, 64),
+                                     (768, 64), (1088, 64), (512, 64), (256, 128), (768, 128),
+                                     (1920, 128), (96, 0)])
+@pytest.mark.parametrize("xdt,sdt", [(FP16, FP16), (BF16, FP32), (INT8, FP32), (INT8, BF16)])
+def test_w4_groups_of_every_alignment(m, K, group, xdt, sdt):
+    from tests.test_gpu_operators import check_w4, w4_case
+
+    g = gen(K + group)
+    check_w4(m, w4_case(g, 3, 13, 137, K, group, xdt, sdt, False, True), FP32)
+    check_w4(m, w4_case(g, 2, 5, 70, K, group, xdt, sdt, True, True), BF16)
