@@ -4,6 +4,10 @@ Functions carry the C names and write into tensors that the caller gives, on
 torch's current stream unless one is passed.  Shapes, types and strides are
 checked here, before the pointers reach the library: a TypeError or ValueError
 names the argument; what the library refuses raises MoeError.
+
+The functions record no graph (autograd.py has those that do).  As with torch's
+own calls, what they write counts as changed for tensors that autograd has saved,
+and may not require a gradient while gradients are recorded.
 """
 from __future__ import annotations
 
@@ -30,6 +34,8 @@ _sort_tokens_backward = lib.moe_sort_tokens_backward
 _unsort_tokens = lib.moe_unsort_tokens
 _unsort_tokens_backward = lib.moe_unsort_tokens_backward
 _w4_gemv = lib.moe_w4_gemv
+# torch.autograd.graph.increment_version for several tensors, without its type checks
+_changed = torch._C._increment_version
 
 
 # A call's checks are on the path of every decoded token: the common case is a few
@@ -62,6 +68,12 @@ def _rows(t, name, dtypes, shape, device):
         pass
     _refuse(t, name, dtypes, shape, device)
     raise ValueError(f"{name}: rows are not contiguous or overlap (strides {t.stride()})")
+
+
+def _refuse_grad(name):
+    if torch.is_grad_enabled():
+        raise ValueError(f"{name}: requires a gradient, and the call would write it without "
+                         "recording one (use torch.no_grad() where that is meant)")
 
 
 def _refuse(t, name, dtypes, shape, device):
@@ -109,22 +121,33 @@ def moe_add_rmsnorm(x, residual, gamma, eps, sum_out, y=None, q=None, q_scale=No
     px, ldx = _rows(x, "x", same, shape, dev)
     pr = pg = ps = py = pq = psc = None
     ldr = lds = ldy = qdt = 0
+    written = []
     if residual is not None:
         pr, ldr = _rows(residual, "residual", same, shape, dev)
     if gamma is not None:
         pg = _tensor(gamma, "gamma", same, (H,), dev)
     if sum_out is not None:
         ps, lds = _rows(sum_out, "sum_out", same, shape, dev)
+        if sum_out.requires_grad:
+            _refuse_grad("sum_out")
+        written.append(sum_out)
     if y is not None:
         py, ldy = _rows(y, "y", same, shape, dev)
+        if y.requires_grad:
+            _refuse_grad("y")
+        written.append(y)
     if q is not None:
         pq = _tensor(q, "q", _CODES, shape, dev)
         qdt = DTYPES[q.dtype]
         psc = _tensor(q_scale, "q_scale", _F32, (T, -(-H // q_group) if q_group else 1), dev)
+        if q.requires_grad or q_scale.requires_grad:
+            _refuse_grad("q_scale" if q_scale.requires_grad else "q")
+        written += (q, q_scale)
     st = _add_rmsnorm(T, H, DTYPES[x.dtype], px, ldx, pr, ldr, pg, eps, ps, lds, py, ldy, qdt,
                       q_group, pq, psc, _stream(stream, dev))
     if st:
         _check(st, "moe_add_rmsnorm")
+    _changed(written)
 
 
 def moe_sort_workspace_size(T, k, n_experts) -> int:
@@ -153,6 +176,7 @@ def moe_sort_tokens(n_experts, ids, x, x_scale, counts, offsets, sorted_to_expan
     po = _tensor(offsets, "offsets", _I32, (n_experts + 1,), dev)
     p1 = _tensor(sorted_to_expanded, "sorted_to_expanded", _I32, (R,), dev)
     p2 = _tensor(expanded_to_sorted, "expanded_to_sorted", _I32, (R,), dev)
+    written = [counts, offsets, sorted_to_expanded, expanded_to_sorted]
     H = ldx = dt = nws = 0
     px = pxs = psc = pso = pw = None
     if x is not None:
@@ -161,12 +185,18 @@ def moe_sort_tokens(n_experts, ids, x, x_scale, counts, offsets, sorted_to_expan
         H = x.shape[1]
         px, ldx = _rows(x, "x", _ANY, (T, H), dev)
         pxs = _tensor(x_sorted, "x_sorted", (x.dtype,), (R, H), dev)
+        if x_sorted.requires_grad:
+            _refuse_grad("x_sorted")
+        written.append(x_sorted)
         dt = DTYPES[x.dtype]
     elif x_sorted is not None:
         raise ValueError("x_sorted: given without x")
     if x_scale is not None:
         psc = _tensor(x_scale, "x_scale", _F32, (T, 1) if x_scale.dim() == 2 else (T,), dev)
         pso = _tensor(scale_sorted, "scale_sorted", _F32, (R,), dev)
+        if scale_sorted.requires_grad:
+            _refuse_grad("scale_sorted")
+        written.append(scale_sorted)
     elif scale_sorted is not None:
         raise ValueError("scale_sorted: given without x_scale")
     if ws is not None:
@@ -176,6 +206,7 @@ def moe_sort_tokens(n_experts, ids, x, x_scale, counts, offsets, sorted_to_expan
                       1 if zero_dropped else 0, pw, nws, _stream(stream, dev))
     if st:
         _check(st, "moe_sort_tokens")
+    _changed(written)
 
 
 def _plan(offsets, expanded_to_sorted, R, dev):
@@ -189,12 +220,15 @@ def moe_sort_tokens_backward(dx_sorted, offsets, expanded_to_sorted, k, dx, stre
     """dx [T, H] = each token's kept rows of dx_sorted [T*k, H], added up."""
     (T, H), dev = _matrix(dx, "dx", _FLOATS)
     pd, ld = _rows(dx, "dx", _FLOATS, (T, H), dev)
+    if dx.requires_grad:
+        _refuse_grad("dx")
     pr = _tensor(dx_sorted, "dx_sorted", _FLOATS, (T * k, H), dev)
     E, po, p2 = _plan(offsets, expanded_to_sorted, T * k, dev)
     st = _sort_tokens_backward(T, k, E, H, DTYPES[dx_sorted.dtype], pr, po, p2, DTYPES[dx.dtype],
                                pd, ld, _stream(stream, dev))
     if st:
         _check(st, "moe_sort_tokens_backward")
+    _changed((dx,))
 
 
 def moe_unsort_tokens(y_sorted, offsets, expanded_to_sorted, topk_w, out, stream=None):
@@ -203,6 +237,8 @@ def moe_unsort_tokens(y_sorted, offsets, expanded_to_sorted, topk_w, out, stream
     (T, H), dev = _matrix(out, "out", _FLOATS)
     k = topk_w.shape[-1]
     pd, ld = _rows(out, "out", _FLOATS, (T, H), dev)
+    if out.requires_grad:
+        _refuse_grad("out")
     pr = _tensor(y_sorted, "y_sorted", _FLOATS, (T * k, H), dev)
     E, po, p2 = _plan(offsets, expanded_to_sorted, T * k, dev)
     pw = _tensor(topk_w, "topk_w", _F32, (T, k), dev)
@@ -210,6 +246,7 @@ def moe_unsort_tokens(y_sorted, offsets, expanded_to_sorted, topk_w, out, stream
                         ld, _stream(stream, dev))
     if st:
         _check(st, "moe_unsort_tokens")
+    _changed((out,))
 
 
 def moe_unsort_tokens_backward(dout, y_sorted, offsets, expanded_to_sorted, topk_w, dy_sorted,
@@ -223,11 +260,14 @@ def moe_unsort_tokens_backward(dout, y_sorted, offsets, expanded_to_sorted, topk
     pw = _tensor(topk_w, "topk_w", _F32, (T, k), dev)
     pg = _tensor(dy_sorted, "dy_sorted", (y_sorted.dtype,), (T * k, H), dev)
     pdw = _tensor(dtopk_w, "dtopk_w", _F32, (T, k), dev)
+    if dy_sorted.requires_grad or dtopk_w.requires_grad:
+        _refuse_grad("dy_sorted" if dy_sorted.requires_grad else "dtopk_w")
     st = _unsort_tokens_backward(T, k, E, H, DTYPES[y_sorted.dtype], DTYPES[dout.dtype], pd, ld, py,
                                  po, p2, pw, pg, pdw, 1 if zero_dropped else 0,
                                  _stream(stream, dev))
     if st:
         _check(st, "moe_unsort_tokens_backward")
+    _changed((dy_sorted, dtopk_w))
 
 
 def pack_w4(codes):
@@ -271,8 +311,11 @@ def moe_w4_gemv(x, x_scale, offsets, w, scales, zeros, out, w_up=None, scales_up
     if zeros_up is not None:
         pzu = _tensor(zeros_up, "zeros_up", _U8, gshape, dev)
     po = _tensor(out, "out", _FLOATS, (R, N), dev)
+    if out.requires_grad:
+        _refuse_grad("out")
     st = _w4_gemv(E, N, K, K // G if G > 1 else 0, R, pof, DTYPES[x.dtype], px, pxs, pw, pwu,
                   DTYPES[scales.dtype], ps, psu, pz, pzu, DTYPES[out.dtype], po,
                   _stream(stream, dev))
     if st:
         _check(st, "moe_w4_gemv")
+    _changed((out,))

@@ -145,3 +145,75 @@ def test_w4_groups_of_every_alignment(m, K, group, xdt, sdt):
     g = gen(K + group)
     check_w4(m, w4_case(g, 3, 13, 137, K, group, xdt, sdt, False, True), FP32)
     check_w4(m, w4_case(g, 2, 5, 70, K, group, xdt, sdt, True, True), BF16)
+
+
+# ------------------------------------------------ tensors that autograd watches --
+def raw_calls(m, g, T=20, k=2, E=4, H=64):
+    """name -> (call, the tensors that it writes)."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, res, y, out, dx = (rand(T, H) for _ in range(5))
+    q, qs = torch.zeros(T, H, device="cuda", dtype=INT8), rand(T, 1)
+    ids = torch.randint(0, E, (T, k), generator=g, **i32)
+    plan = [torch.zeros(n, **i32) for n in (E, E + 1, T * k, T * k)]
+    rows, dy, xsc = rand(T * k, H), rand(T * k, H), rand(T)
+    ss, w, dw = rand(T * k), rand(T, k), rand(T, k)
+    wq = torch.zeros(E, 8, H // 2, device="cuda", dtype=torch.uint8)
+    wide, xw, one = rand(T * k, 8), rand(T * k, H).to(BF16), torch.ones(E, 8, 1, device="cuda")
+    m.moe_sort_tokens(E, ids, None, None, *plan, None)
+    return {
+        "norm": (lambda: m.moe_add_rmsnorm(x, res, None, 1e-6, res, y, q, qs), (res, y, q, qs)),
+        "sort": (lambda: m.moe_sort_tokens(E, ids, x, xsc, *plan, rows, ss), (*plan, rows, ss)),
+        "sort_backward": (lambda: m.moe_sort_tokens_backward(rows, plan[1], plan[3], k, dx), (dx,)),
+        "unsort": (lambda: m.moe_unsort_tokens(rows, plan[1], plan[3], w, out), (out,)),
+        "unsort_backward": (lambda: m.moe_unsort_tokens_backward(out, rows, plan[1], plan[3], w, dy,
+                                                                 dw), (dy, dw)),
+        "w4": (lambda: m.moe_w4_gemv(xw, None, plan[1], wq, one, None, wide), (wide,)),
+    }
+
+
+CALLS = ["norm", "sort", "sort_backward", "unsort", "unsort_backward", "w4"]
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_written_tensors_count_as_changed(m, name):
+    call, written = raw_calls(m, gen(1))[name]
+    before = [t._version for t in written]
+    call()
+    torch.cuda.synchronize()
+    assert all(t._version > v for t, v in zip(written, before))
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_written_tensors_may_not_require_a_gradient(m, name):
+    call, written = raw_calls(m, gen(2))[name]
+    for t in (t for t in written if t.is_floating_point() and t.dtype == FP32):
+        before = t.clone()
+        t.requires_grad_()
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call()
+        torch.cuda.synchronize()
+        assert torch.equal(t.detach(), before)
+        with torch.no_grad():  # as torch's own in-place calls
+            call()
+        t.requires_grad_(False)
+    torch.cuda.synchronize()
+
+
+def test_a_saved_residual_written_in_place_is_noticed(m):
+    g = gen(3)
+    x, res = (torch.randn(4, 64, generator=g, device="cuda") for _ in range(2))
+    w = torch.ones(64, device="cuda", requires_grad=True)
+    loss = (res * w).sum()  # keeps res for w's gradient
+    m.moe_add_rmsnorm(x, res, None, 1e-6, res)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_inference_tensors_may_be_written(m):
+    with torch.inference_mode():
+        x = torch.ones(4, 64, device="cuda")
+        m.moe_add_rmsnorm(x, None, None, 1e-6, None, x)
+    m.moe_add_rmsnorm(x, None, None, 1e-6, None, x)
+    torch.cuda.synchronize()
+    assert (x.double() - 1).abs().max() <= 1e-6

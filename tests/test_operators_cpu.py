@@ -171,3 +171,18 @@ def test_binding_checks_tensors_before_the_library(moe):
     ids = torch.zeros(4, 2, dtype=torch.int64)
     with pytest.raises(TypeError, match="ids"):
         moe.moe_sort_tokens(8, ids, None, None, None, None, None, None, None)
+
+
+def test_binding_refuses_to_write_what_requires_a_gradient(moe):
+    # before anything is launched, and whatever the device
+    x, out = torch.zeros(4, 64), torch.zeros(4, 64, requires_grad=True)
+    with pytest.raises(ValueError, match="sum_out: requires a gradient"):
+        moe.moe_add_rmsnorm(x, None, None, 1e-6, out)
+    with pytest.raises(ValueError, match="y: requires a gradient"):
+        moe.moe_add_rmsnorm(x, None, None, 1e-6, x, out)
+    i32 = dict(dtype=torch.int32)
+    with pytest.raises(ValueError, match="out: requires a gradient"):
+        moe.moe_unsort_tokens(torch.zeros(8, 64), torch.zeros(9, **i32), torch.zeros(8, **i32),
+                              torch.zeros(4, 2), out)
+    with torch.no_grad(), pytest.raises(ValueError, match="current CUDA device"):
+        moe.moe_add_rmsnorm(x, None, None, 1e-6, out)
