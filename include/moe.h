@@ -364,7 +364,8 @@ moe_status moe_unsort_tokens(int32_t T, int32_t k, int32_t n_experts, int32_t H,
  *   dy_sorted[p] = topk_w[r] * dout[t];   dtopk_w[r] = sum_h dout[t, h] * y_sorted[p, h]
  * A dropped pick has dtopk_w = 0, and its dy_sorted row is zeroed
  * (zero_dropped = 1) or not written (0).
- *  dout  [T, H] of out_dtype, row stride ldd; y_sorted, dy_sorted [T*k, H] of dtype */
+ *  dout  [T, H] of out_dtype, row stride ldd; y_sorted, dy_sorted [T*k, H] of dtype
+ *  dy_sorted  may be NULL: only dtopk_w is wanted */
 moe_status moe_unsort_tokens_backward(int32_t T, int32_t k, int32_t n_experts, int32_t H,
                                       int32_t dtype, int32_t out_dtype, const void* dout,
                                       int64_t ldd, const void* y_sorted, const int32_t* offsets,

@@ -75,9 +75,11 @@ class _Unsort(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout):
         y, w, offsets, expanded_to_sorted = ctx.saved_tensors
-        dy, dw = torch.empty_like(y), torch.empty_like(w)
+        # frozen experts' outputs have no gradient to fill
+        dy = torch.empty_like(y) if ctx.needs_input_grad[0] else None
+        dw = torch.empty_like(w)
         ops.moe_unsort_tokens_backward(_ready(dout), y, offsets, expanded_to_sorted, w, dy, dw)
-        return dy, dw, None, None, None
+        return dy, dw if ctx.needs_input_grad[1] else None, None, None, None
 
 
 def sort_tokens(x, topk_ids, n_experts):

@@ -251,23 +251,29 @@ def moe_unsort_tokens(y_sorted, offsets, expanded_to_sorted, topk_w, out, stream
 
 def moe_unsort_tokens_backward(dout, y_sorted, offsets, expanded_to_sorted, topk_w, dy_sorted,
                                dtopk_w, zero_dropped=True, stream=None):
-    """Gradients of moe_unsort_tokens: dy_sorted [T*k, H] and dtopk_w [T, k]."""
+    """Gradients of moe_unsort_tokens: dy_sorted [T*k, H] (None: not wanted) and
+    dtopk_w [T, k]."""
     (T, H), dev = _matrix(dout, "dout", _FLOATS)
     k = topk_w.shape[-1]
     pd, ld = _rows(dout, "dout", _FLOATS, (T, H), dev)
     py = _tensor(y_sorted, "y_sorted", _FLOATS, (T * k, H), dev)
     E, po, p2 = _plan(offsets, expanded_to_sorted, T * k, dev)
     pw = _tensor(topk_w, "topk_w", _F32, (T, k), dev)
-    pg = _tensor(dy_sorted, "dy_sorted", (y_sorted.dtype,), (T * k, H), dev)
     pdw = _tensor(dtopk_w, "dtopk_w", _F32, (T, k), dev)
-    if dy_sorted.requires_grad or dtopk_w.requires_grad:
-        _refuse_grad("dy_sorted" if dy_sorted.requires_grad else "dtopk_w")
+    if dtopk_w.requires_grad:
+        _refuse_grad("dtopk_w")
+    written, pg = [dtopk_w], None
+    if dy_sorted is not None:
+        pg = _tensor(dy_sorted, "dy_sorted", (y_sorted.dtype,), (T * k, H), dev)
+        if dy_sorted.requires_grad:
+            _refuse_grad("dy_sorted")
+        written.append(dy_sorted)
     st = _unsort_tokens_backward(T, k, E, H, DTYPES[y_sorted.dtype], DTYPES[dout.dtype], pd, ld, py,
                                  po, p2, pw, pg, pdw, 1 if zero_dropped else 0,
                                  _stream(stream, dev))
     if st:
         _check(st, "moe_unsort_tokens_backward")
-    _changed((dy_sorted, dtopk_w))
+    _changed(written)
 
 
 def pack_w4(codes):

@@ -217,3 +217,44 @@ def test_inference_tensors_may_be_written(m):
     m.moe_add_rmsnorm(x, None, None, 1e-6, None, x)
     torch.cuda.synchronize()
     assert (x.double() - 1).abs().max() <= 1e-6
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("T", [40, 700])
+def test_frozen_expert_outputs_get_no_gradient(m, dtype, T):
+    from sparse_expert_layer_gb300 import autograd
+
+    k, E, H = 4, 8, 1024
+    g = gen(T)
+    ids = torch.randint(-1, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    _, plan = autograd.sort_tokens(torch.zeros(T, H, device="cuda", dtype=dtype), ids, E)
+    y = torch.randn(T * k, H, generator=g, device="cuda").to(dtype)
+    w = torch.rand(T, k, generator=g, device="cuda")
+    grad = torch.randn(T, H, generator=g, device="cuda").to(dtype)
+    grads, peaks = [], []
+    for frozen in (False, True):
+        yi, wi = y.clone().requires_grad_(not frozen), w.clone().requires_grad_()
+        out = autograd.unsort_tokens(yi, wi, plan)
+        torch.cuda.synchronize()
+        start = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        out.backward(grad)
+        torch.cuda.synchronize()
+        peaks.append(torch.cuda.max_memory_allocated() - start)
+        grads.append(wi.grad)
+        assert (yi.grad is None) == frozen
+    assert torch.equal(*grads)
+    rows = T * k * H * y.element_size()
+    assert peaks[1] < rows <= peaks[0]
+
+
+def test_the_gradient_of_the_rows_may_be_left_out(m):
+    from tests.test_gpu_operators import back_case
+
+    t, _, _, _ = back_case(gen(5), 50, 4, 8, 333, FP32, BF16, 4)
+    args = t["dout"], t["y"], t["offsets"], t["e2s"], t["w"]
+    dy, dw, alone = torch.empty_like(t["y"]), torch.empty_like(t["w"]), torch.empty_like(t["w"])
+    m.moe_unsort_tokens_backward(*args, dy, dw)
+    m.moe_unsort_tokens_backward(*args, None, alone)
+    torch.cuda.synchronize()
+    assert torch.equal(dw, alone)
