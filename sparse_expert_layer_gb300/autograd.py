@@ -40,6 +40,7 @@ class _Sort(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, ids, n_experts):
         T, k = ids.shape
+        ids = _ready(ids).contiguous()
         i32 = dict(dtype=torch.int32, device=ids.device)
         plan = (torch.empty(n_experts, **i32), torch.empty(n_experts + 1, **i32),
                 torch.empty(T * k, **i32), torch.empty(T * k, **i32))
@@ -84,7 +85,8 @@ class _Unsort(torch.autograd.Function):
 
 def sort_tokens(x, topk_ids, n_experts):
     """(x_sorted [T*k, H], SortPlan) of x [T, H] (bf16, fp16 or fp32) and int32
-    topk_ids [T, k]; ids outside [0, n_experts) are dropped picks."""
+    topk_ids [T, k]; ids outside [0, n_experts) are dropped picks.  x and topk_ids
+    of other layouts are copied first."""
     if x.dtype not in (torch.bfloat16, torch.float16, torch.float32):
         raise TypeError(f"x: {x.dtype} has no gradient here")
     x_sorted, *plan = _Sort.apply(x, topk_ids, n_experts)

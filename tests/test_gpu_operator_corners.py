@@ -258,3 +258,22 @@ def test_the_gradient_of_the_rows_may_be_left_out(m):
     m.moe_unsort_tokens_backward(*args, None, alone)
     torch.cuda.synchronize()
     assert torch.equal(dw, alone)
+
+
+@pytest.mark.parametrize("layout", ["columns", "transposed", "start", "expanded"])
+def test_ids_of_any_layout_are_sorted(m, layout):
+    from sparse_expert_layer_gb300 import autograd
+
+    T, k, E, H = 30, 2, 8, 64
+    g = gen(4)
+    x = torch.randn(T, H, generator=g, device="cuda")
+    draw = lambda *s: torch.randint(-1, E, s, generator=g, device="cuda",  # noqa: E731
+                                    dtype=torch.int32)
+    ids = {"columns": lambda: draw(T, k + 3)[:, 1:1 + k], "transposed": lambda: draw(k, T).T,
+           "start": lambda: draw(T * k + 1)[1:].view(T, k),
+           "expanded": lambda: draw(T, 1).expand(T, k)}[layout]()
+    want, plan = autograd.sort_tokens(x, ids.clone(memory_format=torch.contiguous_format), E)
+    got, other = autograd.sort_tokens(x, ids, E)
+    assert torch.equal(got, want)
+    assert torch.equal(plan.expanded_to_sorted, other.expanded_to_sorted)
+    assert torch.equal(plan.offsets, other.offsets)
