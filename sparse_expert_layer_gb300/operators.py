@@ -77,8 +77,7 @@ def _refuse_grad(name):
 
 
 def _refuse(t, name, dtypes, shape, device):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
+    _a_tensor(t, name)
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: {t.dtype} is not one of {sorted(map(str, dtypes))}")
     if t.shape != shape:
@@ -87,13 +86,29 @@ def _refuse(t, name, dtypes, shape, device):
         raise ValueError(f"{name}: on {t.device}, not on CUDA device {device}")
 
 
-def _matrix(t, name, dtypes):
-    """(shape, device index) of the matrix that sets a call's sizes."""
+def _a_tensor(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
+
+
+def _row_scales(t, rows, device):
+    """Address of x_scale, [rows] or [rows, 1]."""
+    _a_tensor(t, "x_scale")
+    return _tensor(t, "x_scale", _F32, (rows, 1) if t.dim() == 2 else (rows,), device)
+
+
+def _matrix(t, name, dtypes, strided=True):
+    """(shape, device index, address, row stride) of the matrix that sets a call's sizes."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise TypeError(f"{name}: expected a matrix")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: {t.dtype} is not one of {sorted(map(str, dtypes))}")
-    return t.shape, t.get_device()
+    shape, device = t.shape, t.get_device()
+    if t.is_contiguous():
+        return shape, device, t.data_ptr(), shape[1]
+    if not strided:
+        raise ValueError(f"{name}: not contiguous")
+    return shape, device, *_rows(t, name, dtypes, shape, device)
 
 
 def _stream(stream, device):
@@ -115,10 +130,9 @@ def moe_add_rmsnorm(x, residual, gamma, eps, sum_out, y=None, q=None, q_scale=No
     fp32 [T, groups] ([T, 1] for q_group 0).  residual, gamma and each output may be None; sum_out may
     be x or residual itself.
     """
-    shape, dev = _matrix(x, "x", _FLOATS)
+    shape, dev, px, ldx = _matrix(x, "x", _FLOATS)
     T, H = shape
     same = (x.dtype,)
-    px, ldx = _rows(x, "x", same, shape, dev)
     pr = pg = ps = py = pq = psc = None
     ldr = lds = ldy = qdt = 0
     written = []
@@ -169,9 +183,8 @@ def moe_sort_tokens(n_experts, ids, x, x_scale, counts, offsets, sorted_to_expan
     """Stable order of the picks ids [T, k] by expert (dropped picks last) and the
     tokens' rows x [T, H] (and fp32 scales x_scale [T]) in it.  x and x_sorted may
     be None together: only the order is wanted."""
-    (T, k), dev = _matrix(ids, "ids", _I32)
+    (T, k), dev, pi, _ = _matrix(ids, "ids", _I32, strided=False)
     R = T * k
-    pi = _tensor(ids, "ids", _I32, (T, k), dev)
     pc = _tensor(counts, "counts", _I32, (n_experts,), dev)
     po = _tensor(offsets, "offsets", _I32, (n_experts + 1,), dev)
     p1 = _tensor(sorted_to_expanded, "sorted_to_expanded", _I32, (R,), dev)
@@ -180,8 +193,12 @@ def moe_sort_tokens(n_experts, ids, x, x_scale, counts, offsets, sorted_to_expan
     H = ldx = dt = nws = 0
     px = pxs = psc = pso = pw = None
     if x is not None:
-        if x.dim() != 2:
-            raise ValueError("x: expected a matrix")
+        try:
+            if x.dim() != 2:
+                raise ValueError("x: expected a matrix")
+        except AttributeError:
+            _a_tensor(x, "x")
+            raise
         H = x.shape[1]
         px, ldx = _rows(x, "x", _ANY, (T, H), dev)
         pxs = _tensor(x_sorted, "x_sorted", (x.dtype,), (R, H), dev)
@@ -192,7 +209,7 @@ def moe_sort_tokens(n_experts, ids, x, x_scale, counts, offsets, sorted_to_expan
     elif x_sorted is not None:
         raise ValueError("x_sorted: given without x")
     if x_scale is not None:
-        psc = _tensor(x_scale, "x_scale", _F32, (T, 1) if x_scale.dim() == 2 else (T,), dev)
+        psc = _row_scales(x_scale, T, dev)
         pso = _tensor(scale_sorted, "scale_sorted", _F32, (R,), dev)
         if scale_sorted.requires_grad:
             _refuse_grad("scale_sorted")
@@ -200,6 +217,7 @@ def moe_sort_tokens(n_experts, ids, x, x_scale, counts, offsets, sorted_to_expan
     elif scale_sorted is not None:
         raise ValueError("scale_sorted: given without x_scale")
     if ws is not None:
+        _a_tensor(ws, "ws")
         nws = ws.numel()
         pw = _tensor(ws, "ws", _U8, (nws,), dev)
     st = _sort_tokens(T, k, n_experts, H, dt, pi, px, ldx, psc, pc, po, p1, p2, pxs, pso,
@@ -209,17 +227,28 @@ def moe_sort_tokens(n_experts, ids, x, x_scale, counts, offsets, sorted_to_expan
     _changed(written)
 
 
+def _picks(topk_w):
+    try:
+        return topk_w.shape[1]
+    except (AttributeError, IndexError):
+        _matrix(topk_w, "topk_w", _F32)  # says what is wrong
+        raise
+
+
 def _plan(offsets, expanded_to_sorted, R, dev):
     """(experts, addresses) of the plan that moe_sort_tokens wrote."""
-    E = offsets.numel() - 1
+    try:
+        E = offsets.numel() - 1
+    except AttributeError:
+        _a_tensor(offsets, "offsets")
+        raise
     return E, _tensor(offsets, "offsets", _I32, (E + 1,), dev), \
         _tensor(expanded_to_sorted, "expanded_to_sorted", _I32, (R,), dev)
 
 
 def moe_sort_tokens_backward(dx_sorted, offsets, expanded_to_sorted, k, dx, stream=None):
     """dx [T, H] = each token's kept rows of dx_sorted [T*k, H], added up."""
-    (T, H), dev = _matrix(dx, "dx", _FLOATS)
-    pd, ld = _rows(dx, "dx", _FLOATS, (T, H), dev)
+    (T, H), dev, pd, ld = _matrix(dx, "dx", _FLOATS)
     if dx.requires_grad:
         _refuse_grad("dx")
     pr = _tensor(dx_sorted, "dx_sorted", _FLOATS, (T * k, H), dev)
@@ -234,9 +263,8 @@ def moe_sort_tokens_backward(dx_sorted, offsets, expanded_to_sorted, k, dx, stre
 def moe_unsort_tokens(y_sorted, offsets, expanded_to_sorted, topk_w, out, stream=None):
     """out [T, H] = sum over each token's kept picks of topk_w [T, k] times its
     row of y_sorted [T*k, H]."""
-    (T, H), dev = _matrix(out, "out", _FLOATS)
-    k = topk_w.shape[-1]
-    pd, ld = _rows(out, "out", _FLOATS, (T, H), dev)
+    (T, H), dev, pd, ld = _matrix(out, "out", _FLOATS)
+    k = _picks(topk_w)
     if out.requires_grad:
         _refuse_grad("out")
     pr = _tensor(y_sorted, "y_sorted", _FLOATS, (T * k, H), dev)
@@ -253,9 +281,8 @@ def moe_unsort_tokens_backward(dout, y_sorted, offsets, expanded_to_sorted, topk
                                dtopk_w, zero_dropped=True, stream=None):
     """Gradients of moe_unsort_tokens: dy_sorted [T*k, H] (None: not wanted) and
     dtopk_w [T, k]."""
-    (T, H), dev = _matrix(dout, "dout", _FLOATS)
-    k = topk_w.shape[-1]
-    pd, ld = _rows(dout, "dout", _FLOATS, (T, H), dev)
+    (T, H), dev, pd, ld = _matrix(dout, "dout", _FLOATS)
+    k = _picks(topk_w)
     py = _tensor(y_sorted, "y_sorted", _FLOATS, (T * k, H), dev)
     E, po, p2 = _plan(offsets, expanded_to_sorted, T * k, dev)
     pw = _tensor(topk_w, "topk_w", _F32, (T, k), dev)
@@ -290,7 +317,7 @@ def moe_w4_gemv(x, x_scale, offsets, w, scales, zeros, out, w_up=None, scales_up
     None (one expert); w, w_up uint8 [E, N, K / 2]; scales [E, N, groups] bf16,
     fp16 or fp32; zeros uint8 of their shape or None (8); out [R, N].
     """
-    (R, K), dev = _matrix(x, "x", _W4_X)
+    (R, K), dev, px, _ = _matrix(x, "x", _W4_X, strided=False)
     if not isinstance(w, torch.Tensor) or w.dim() != 3:
         raise TypeError("w: expected [experts, N, K / 2]")
     E, N, _ = w.shape
@@ -300,12 +327,11 @@ def moe_w4_gemv(x, x_scale, offsets, w, scales, zeros, out, w_up=None, scales_up
     if G < 1 or K % G:
         raise ValueError(f"scales: {G} groups do not divide K = {K}")
     wshape, gshape = (E, N, K // 2), (E, N, G)
-    px = _tensor(x, "x", _W4_X, (R, K), dev)
     pw = _tensor(w, "w", _U8, wshape, dev)
     ps = _tensor(scales, "scales", _FLOATS, gshape, dev)
     pxs = pof = pz = pwu = psu = pzu = None
     if x_scale is not None:
-        pxs = _tensor(x_scale, "x_scale", _F32, (R, 1) if x_scale.dim() == 2 else (R,), dev)
+        pxs = _row_scales(x_scale, R, dev)
     if offsets is not None:
         pof = _tensor(offsets, "offsets", _I32, (E + 1,), dev)
     if zeros is not None:

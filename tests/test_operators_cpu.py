@@ -186,3 +186,29 @@ def test_binding_refuses_to_write_what_requires_a_gradient(moe):
                               torch.zeros(4, 2), out)
     with torch.no_grad(), pytest.raises(ValueError, match="current CUDA device"):
         moe.moe_add_rmsnorm(x, None, None, 1e-6, out)
+
+
+def test_binding_names_what_is_not_a_tensor(moe):
+    i32 = dict(dtype=torch.int32)
+    x, rows, w, bad = torch.zeros(4, 64), torch.zeros(8, 64), torch.zeros(4, 2), [1.0]
+    ids = torch.zeros(4, 2, **i32)
+    plan = [torch.zeros(n, **i32) for n in (8, 9, 8, 8)]
+    u8 = torch.zeros(1, 8, 32, dtype=torch.uint8)
+    calls = [
+        ("x", lambda: moe.moe_sort_tokens(8, ids, bad, None, *plan, rows)),
+        ("x_sorted", lambda: moe.moe_sort_tokens(8, ids, x, None, *plan, bad)),
+        ("x_scale", lambda: moe.moe_sort_tokens(8, ids, x, bad, *plan, rows, w)),
+        ("scale_sorted", lambda: moe.moe_sort_tokens(8, ids, x, x[:, 0].clone(), *plan, rows, bad)),
+        ("ws", lambda: moe.moe_sort_tokens(8, ids, x, None, *plan, rows, None, bad)),
+        ("offsets", lambda: moe.moe_sort_tokens_backward(rows, bad, plan[3], 2, x)),
+        ("expanded_to_sorted", lambda: moe.moe_sort_tokens_backward(rows, plan[1], bad, 2, x)),
+        ("topk_w", lambda: moe.moe_unsort_tokens(rows, plan[1], plan[3], bad, x)),
+        ("topk_w", lambda: moe.moe_unsort_tokens(rows, plan[1], plan[3], w[0, 0], x)),
+        ("topk_w", lambda: moe.moe_unsort_tokens_backward(x, rows, plan[1], plan[3], bad, rows, w)),
+        ("offsets", lambda: moe.moe_unsort_tokens_backward(x, rows, None, plan[3], w, rows, w)),
+        ("x_scale", lambda: moe.moe_w4_gemv(x.bfloat16(), bad, None, u8, torch.ones(1, 8, 1), None,
+                                            torch.zeros(4, 8))),
+    ]
+    for name, call in calls:
+        with pytest.raises(TypeError, match=f"^{name}: "):
+            call()
