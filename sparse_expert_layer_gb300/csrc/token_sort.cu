@@ -355,7 +355,9 @@ constexpr int kGradThreads = 256;
 // drows[p] = w * dout[t], dw = <dout[t], rows[p]>: a CTA takes `picks` picks of
 // one token; a slot of dout is loaded once for all of them.  A thread's channels
 // are neighbours in rows of any alignment: dw has the same bits whatever the row
-// strides.  ROWS false: drows is not wanted (4096 x 8 of 5120 bf16 channels take
+// strides.  Rows of odd lengths pay for that with accesses of one channel, eight
+// channels apart in a warp: 2048 x 8 of 5121 bf16 channels take 161 us (33% of the
+// copy rate), of 5120 63 us.  ROWS false: drows is not wanted (4096 x 8 of 5120 bf16 channels take
 // 68 us instead of 119).  A test at run time instead cost rows of odd lengths 7%.
 template <typename TI, typename TO, bool VEC, bool ROWS>
 __global__ void __launch_bounds__(kGradThreads) unsort_grad_kernel(GradArgs a, int parts) {

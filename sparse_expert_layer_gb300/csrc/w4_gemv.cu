@@ -19,14 +19,21 @@
 // panels of x and scales are shared.  With few row tiles a cluster of CTAs
 // splits K and adds the parts through distributed shared memory in rank order.
 //
-// Taking the nibbles apart bounds it: eleven instructions for eight weights in
-// bf16 (nine in fp16), seven of them on the half-rate integer pipe.  56 experts'
-// gate and up (5120 -> 1536, groups of 128, 192 rows) take 109 us, 4.2 TB/s, 62%
-// of the copy rate; the same loads without the arithmetic take 78 us, and the
-// arithmetic of a dense matrix without its loads 27 of 30 us.  Groups of 32 with
-// zero points add loads and instructions a step: 14 experts' down (2048 -> 7168)
-// 45 us, 40%.  Leaving the subtraction of z to a sum of x by another MMA was no
-// faster (111 us) and less exact.
+// 56 experts' gate and up (5120 -> 1536, groups of 128, 192 rows) take 109 us,
+// 4.2 TB/s, 62% of the copy rate.  No unit is full: the schedulers issue in 62% of
+// the cycles, the half-rate integer pipe is busy in 57%, the tensor pipe in 24%,
+// with four warps a scheduler (128 registers a thread).  The same loads without
+// the arithmetic take 78 us, so what is lost is overlap of the two.  Half of the
+// instructions take nibbles apart: eleven for eight weights in bf16 (nine in
+// fp16), seven of them on the integer pipe; the rest permutes x, forms addresses
+// and applies scales.  Leaving the subtraction of z to a sum of x by another MMA
+// was no faster (111 us) and less exact.
+//
+// 14 experts' down (2048 -> 7168, groups of 32 with zero points, 37 rows) take 45
+// us, 40%, and fill less still (issue 50%, integer pipe 37%, tensor pipe 12%): a
+// CTA has four panels beside its start and the adding of its parts, and 784 CTAs on
+// 304 slots are 2.6 rounds that run as three.  With zero points the registers do
+// not suffice and 56 to 104 bytes a thread are spilled, up to 24 without.
 #include <math.h>
 
 #include <algorithm>
