@@ -400,6 +400,32 @@ moe_status moe_w4_gemv(int32_t n_experts, int32_t N, int32_t K, int32_t group, i
                        const void* scales, const void* scales_up, const uint8_t* zeros,
                        const uint8_t* zeros_up, int32_t out_dtype, void* out, moe_stream_t stream);
 
+/* Global norm of many tensors, and the tensors scaled so that it is at most max_norm:
+ *   norm = sqrt(sum of the squares of all elements);  c = min(1, max_norm / (norm + eps))
+ *   out = in * c for each tensor that has an out
+ * A tensor's squares are added in fp32 for at most 64 elements, then in fp64 in a
+ * fixed order (the same bits on every call on one device); norm and c are fp32, each
+ * product is rounded once.  Where the norm is infinite c is 0 (infinite elements
+ * become NaN), where it is NaN everything does; an element of 2^64 or more makes the
+ * norm infinite, squares below 2^-126 lose their precision.  With c = 1 a tensor
+ * whose out is its in is not written.
+ *  tensors   HOST array of n entries, read before the call returns; n >= 0
+ *            in, out: contiguous, aligned to an element; out NULL (only counted), in
+ *            itself, or memory that overlaps no in and no other out
+ *            n elements >= 0 of dtype MOE_DT_BF16, MOE_DT_FP16 or MOE_DT_FP32
+ *  max_norm, eps  finite, >= 0 (0 / 0 is NaN)
+ *  norm      fp32 [1] out, or NULL; norm or some out is required
+ *  ws        moe_clip_workspace_size bytes, 256-byte aligned; need not be initialised */
+typedef struct {
+  const void* in;
+  void* out;
+  int64_t n;
+  int32_t dtype; /* moe_dtype */
+} moe_tensor;
+moe_status moe_clip_workspace_size(size_t* bytes);
+moe_status moe_clip_grad_norm(int32_t n, const moe_tensor* tensors, float max_norm, float eps,
+                              float* norm, void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* Synchronises `stream`, reads and clears the device status word in `ws`.
  * MOE_OK, MOE_ERR_DEVICE_CHECK or MOE_ERR_DEVICE_TIMEOUT (or MOE_ERR_CUDA). */
 moe_status moe_check_device_status(void* ws, moe_stream_t stream);
@@ -437,6 +463,8 @@ typedef enum {
   MOE_K_UNSORT,      /* moe_unsort_tokens, moe_sort_tokens_backward */
   MOE_K_UNSORT_GRAD, /* moe_unsort_tokens_backward */
   MOE_K_W4,          /* moe_w4_gemv */
+  MOE_K_GRAD_NORM,   /* moe_clip_grad_norm: sums of squares */
+  MOE_K_CLIP,        /* moe_clip_grad_norm: products */
   MOE_K_COUNT
 } moe_kernel_kind;
 

@@ -1,0 +1,293 @@
+// Global norm of many tensors, and the tensors times min(1, max_norm / (norm + eps)).
+//
+// Two kernels: the sums of squares, then the products.  Both walk the same list of
+// chunks of 32 KB, the first forwards and the second backwards, so that what the
+// first read last is still in L2 when the second starts there.
+//
+// The squares of a thread's 64 elements of a chunk (fp32: 32) are added in fp32, its
+// chunks and the threads in fp64, each CTA's sum in a slot of its own, and the slots
+// in order: the same bits on every call on one device.
+#include <math.h>
+
+#include <algorithm>
+
+#include "rows.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kClipThreads = 256;
+constexpr int kClipCtasPerSm = 4;
+constexpr int kClipMaxCtas = 4096;   // slots of the workspace
+constexpr int kClipUnroll = 8;       // 16-byte words of a thread in a chunk
+constexpr int kClipChunk = kClipThreads * kClipUnroll;  // words
+constexpr int kClipMost = 512;       // tensors of one launch
+constexpr int kClipFew = 48;         // the same, for a short parameter block
+constexpr int64_t kClipMaxElems = 1LL << 42;
+
+struct ClipTensor {
+  const unsigned char* in;   // down to a 16-byte boundary
+  unsigned char* out;        // the byte that belongs to `in` (nullptr: not wanted)
+  int64_t n;                 // bytes from `in` to the tensor's end
+  int32_t skip;              // bytes from `in` to the tensor's first element
+  int32_t dtype;
+};
+
+template <int N>
+struct ClipList {
+  ClipTensor t[N];
+  int32_t first[N + 1];  // each tensor's first chunk
+  int32_t count;
+};
+
+template <int N>
+__device__ __forceinline__ int clip_find(const ClipList<N>& l, int chunk) {
+  int lo = 0, hi = l.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (l.first[mid] <= chunk)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// f(word, its elements as fp32) for the thread's words of a chunk; elements
+// outside the tensor are zeros.  Loads of the chunk's words are issued together.
+template <typename T, typename F>
+__device__ __forceinline__ void clip_words(const ClipTensor& t, int64_t word0, F f) {
+  constexpr int kPer = 16 / sizeof(T);
+  const int64_t words = (t.n + 15) / 16;
+  uint4 v[kClipUnroll];
+#pragma unroll
+  for (int i = 0; i < kClipUnroll; ++i) {
+    const int64_t w = word0 + threadIdx.x + i * kClipThreads, at = w * 16;
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (w >= words) continue;
+    if (at >= t.skip && at + 16 <= t.n) {
+      v[i] = *reinterpret_cast<const uint4*>(t.in + at);
+    } else {  // a tensor's first or last word
+      T e[kPer];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int64_t b = at + j * (int)sizeof(T);
+        e[j] = b >= t.skip && b < t.n ? *reinterpret_cast<const T*>(t.in + b) : from_f<T>(0.f);
+      }
+      memcpy(&v[i], e, 16);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kClipUnroll; ++i) {
+    const int64_t w = word0 + threadIdx.x + i * kClipThreads;
+    if (w >= words) continue;
+    float x[kPer];
+    if constexpr (sizeof(T) == 4) {
+      memcpy(x, &v[i], 16);
+    } else {
+      const uint32_t p[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 q = unpack2<T>(p[j]);
+        x[2 * j] = q.x;
+        x[2 * j + 1] = q.y;
+      }
+    }
+    f(w, x);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float clip_square(const ClipTensor& t, int64_t word0) {
+  constexpr int kPer = 16 / sizeof(T);
+  float s[4] = {};
+  clip_words<T>(t, word0, [&](int64_t, const float(&x)[kPer]) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) s[j % 4] = fmaf(x[j], x[j], s[j % 4]);
+  });
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+template <typename T>
+__device__ __forceinline__ void clip_scale(const ClipTensor& t, int64_t word0, float c) {
+  constexpr int kPer = 16 / sizeof(T);
+  const bool together = (reinterpret_cast<uintptr_t>(t.out) & 15u) == 0;
+  clip_words<T>(t, word0, [&](int64_t w, const float(&x)[kPer]) {
+    const int64_t at = w * 16;
+    T y[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) y[j] = from_f<T>(x[j] * c);
+    if (together && at >= t.skip && at + 16 <= t.n) {
+      uint4 q;
+      memcpy(&q, y, 16);
+      *reinterpret_cast<uint4*>(t.out + at) = q;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int64_t b = at + j * (int)sizeof(T);
+        if (b >= t.skip && b < t.n) *reinterpret_cast<T*>(t.out + b) = y[j];
+      }
+    }
+  });
+}
+
+// The block's sum of v, in every thread; added in a fixed order.
+__device__ __forceinline__ double clip_block_sum(double v) {
+  __shared__ double part[kClipThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+  __syncthreads();
+  double s = 0.;
+#pragma unroll
+  for (int i = 0; i < kClipThreads / 32; ++i) s += part[i];
+  __syncthreads();
+  return s;
+}
+
+// more: a list after the first one, added to what the slots hold.
+template <int N>
+__global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
+    clip_norm_kernel(const __grid_constant__ ClipList<N> l, double* slots, int more) {
+  pdl_enter();
+  double sum = 0.;
+  const int chunks = l.first[l.count];
+  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const int i = clip_find(l, c);
+    const ClipTensor& t = l.t[i];
+    const int64_t w = (int64_t)(c - l.first[i]) * kClipChunk;
+    sum += (double)(t.dtype == MOE_DT_BF16   ? clip_square<__nv_bfloat16>(t, w)
+                    : t.dtype == MOE_DT_FP16 ? clip_square<__half>(t, w)
+                                             : clip_square<float>(t, w));
+  }
+  sum = clip_block_sum(sum);
+  if (threadIdx.x == 0) slots[blockIdx.x] = more ? slots[blockIdx.x] + sum : sum;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
+    clip_scale_kernel(const __grid_constant__ ClipList<N> l, const double* slots, int nslots,
+                      float max_norm, float eps, float* norm_out) {
+  pdl_enter();
+  double sum = 0.;
+  for (int i = threadIdx.x; i < nslots; i += kClipThreads) sum += slots[i];
+  const float norm = (float)sqrt(clip_block_sum(sum));
+  if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
+  const float q = max_norm / (norm + eps);
+  const float c = q >= 1.f ? 1.f : q;  // a NaN stays one
+  const int chunks = l.first[l.count];
+  for (int k = blockIdx.x; k < chunks; k += gridDim.x) {
+    const int chunk = chunks - 1 - k, i = clip_find(l, chunk);
+    const ClipTensor& t = l.t[i];
+    if (!t.out || (c == 1.f && t.out == t.in)) continue;
+    const int64_t w = (int64_t)(chunk - l.first[i]) * kClipChunk;
+    if (t.dtype == MOE_DT_BF16)
+      clip_scale<__nv_bfloat16>(t, w, c);
+    else if (t.dtype == MOE_DT_FP16)
+      clip_scale<__half>(t, w, c);
+    else
+      clip_scale<float>(t, w, c);
+  }
+}
+
+int clip_size(int dtype) { return dtype == MOE_DT_FP32 ? 4 : 2; }
+
+// Tensors [i, i + count) of the call; false: more chunks than an int counts.
+template <int N>
+bool clip_list(const moe_tensor* ts, int count, ClipList<N>* l) {
+  int64_t chunks = 0;
+  l->count = 0;
+  for (int i = 0; i < count; ++i) {
+    const moe_tensor& s = ts[i];
+    if (s.n == 0) continue;
+    ClipTensor& t = l->t[l->count];
+    const uintptr_t at = reinterpret_cast<uintptr_t>(s.in);
+    t.skip = (int32_t)(at & 15u);
+    t.in = reinterpret_cast<const unsigned char*>(at - t.skip);
+    t.out = s.out ? static_cast<unsigned char*>(s.out) - t.skip : nullptr;
+    t.n = t.skip + s.n * clip_size(s.dtype);
+    t.dtype = s.dtype;
+    l->first[l->count++] = (int32_t)chunks;
+    chunks += (t.n + kClipChunk * 16LL - 1) / (kClipChunk * 16LL);
+    if (chunks > INT32_MAX - kClipMaxCtas) return false;
+  }
+  l->first[l->count] = (int32_t)chunks;
+  return true;
+}
+
+template <int N>
+moe_status clip_run(const Launch& L, int n, const moe_tensor* ts, float max_norm, float eps,
+                    float* norm, double* slots) {
+  const int most = std::min(kClipMaxCtas, kClipCtasPerSm * L.num_sms);
+  ClipList<N> l;
+  // every list has the slots of all CTAs, so that later lists add to what is there
+  int used = 0;
+  for (int i = 0; i < n; i += N) {
+    if (!clip_list<N>(ts + i, std::min(N, n - i), &l)) return MOE_ERR_UNSUPPORTED;
+    used = std::max(used, std::min(most, l.first[l.count]));
+  }
+  used = std::max(used, 1);
+  for (int pass = 0; pass < 2; ++pass) {
+    bool scaled = pass == 0 || norm != nullptr;
+    for (int i = 0; i < n && !scaled; ++i) scaled = ts[i].out != nullptr && ts[i].n > 0;
+    if (!scaled) break;
+    for (int i = 0; i < std::max(n, 1); i += N) {
+      // the second pass goes backwards
+      const int last = (std::max(n, 1) - 1) / N * N, at = pass ? last - i : i;
+      clip_list<N>(ts + at, std::min(N, n - at), &l);
+      launch_begin(L, pass ? MOE_K_CLIP : MOE_K_GRAD_NORM);
+      if (pass == 0)
+        launch_kernel(clip_norm_kernel<N>, dim3(used), dim3(kClipThreads), 0, L.stream, l, slots,
+                      at > 0 ? 1 : 0);
+      else
+        launch_kernel(clip_scale_kernel<N>, dim3(used), dim3(kClipThreads), 0, L.stream, l,
+                      static_cast<const double*>(slots), used, max_norm, eps,
+                      i == 0 ? norm : nullptr);
+      launch_end(L, pass ? MOE_K_CLIP : MOE_K_GRAD_NORM);
+    }
+  }
+  return launch_status_take();
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_clip_workspace_size(size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = kClipMaxCtas * sizeof(double);
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_clip_grad_norm(int32_t n, const moe_tensor* tensors, float max_norm,
+                                         float eps, float* norm, void* ws, size_t ws_bytes,
+                                         moe_stream_t stream) {
+  if (n < 0 || (n > 0 && !tensors) || !isfinite(max_norm) || max_norm < 0.f || !isfinite(eps) ||
+      eps < 0.f)
+    return MOE_ERR_INVALID_ARG;
+  bool outputs = norm != nullptr;
+  for (int i = 0; i < n; ++i) {
+    const moe_tensor& t = tensors[i];
+    if (t.n < 0 || t.dtype < MOE_DT_BF16 || t.dtype > MOE_DT_FP32) return MOE_ERR_INVALID_ARG;
+    if (t.n > kClipMaxElems) return MOE_ERR_UNSUPPORTED;
+    if (t.n > 0 && !t.in) return MOE_ERR_INVALID_ARG;
+    const uintptr_t mask = clip_size(t.dtype) - 1;
+    if ((reinterpret_cast<uintptr_t>(t.in) & mask) || (reinterpret_cast<uintptr_t>(t.out) & mask))
+      return MOE_ERR_ALIGNMENT;
+    outputs = outputs || t.out;
+  }
+  if (!outputs) return MOE_ERR_INVALID_ARG;
+  if (!ws) return MOE_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) || (reinterpret_cast<uintptr_t>(norm) & 3u))
+    return MOE_ERR_ALIGNMENT;
+  if (ws_bytes < kClipMaxCtas * sizeof(double)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  Launch L;
+  const moe_status s = open_launch(stream, &L);
+  if (s != MOE_OK) return s;
+  double* slots = static_cast<double*>(ws);
+  return n <= kClipFew ? clip_run<kClipFew>(L, n, tensors, max_norm, eps, norm, slots)
+                       : clip_run<kClipMost>(L, n, tensors, max_norm, eps, norm, slots);
+}

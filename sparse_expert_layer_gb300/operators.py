@@ -15,7 +15,7 @@ import ctypes
 
 import torch
 
-from . import _check, lib
+from . import MoeTensor, _check, lib
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int8: 3,
           torch.float8_e4m3fn: 4}
@@ -34,6 +34,7 @@ _sort_tokens_backward = lib.moe_sort_tokens_backward
 _unsort_tokens = lib.moe_unsort_tokens
 _unsort_tokens_backward = lib.moe_unsort_tokens_backward
 _w4_gemv = lib.moe_w4_gemv
+_clip_grad_norm = lib.moe_clip_grad_norm
 # torch.autograd.graph.increment_version for several tensors, without its type checks
 _changed = torch._C._increment_version
 
@@ -351,3 +352,87 @@ def moe_w4_gemv(x, x_scale, offsets, w, scales, zeros, out, w_up=None, scales_up
     if st:
         _check(st, "moe_w4_gemv")
     _changed((out,))
+
+
+def moe_clip_workspace_size() -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib.moe_clip_workspace_size(ctypes.byref(n)), "moe_clip_workspace_size")
+    return n.value
+
+
+def clip_workspace(device="cuda"):
+    """A uint8 tensor of moe_clip_workspace_size bytes."""
+    return torch.empty(moe_clip_workspace_size(), dtype=torch.uint8, device=device)
+
+
+class TensorList:
+    """Tensors as moe_clip_grad_norm takes them, checked once: a program whose
+    gradients stay where they are makes one list and calls with it every step.
+
+    tensors: contiguous bf16, fp16 or fp32 tensors of any shapes on one CUDA device.
+    outs: None (in place), or for each tensor one of its shape and type, the tensor
+    itself, or None (only counted).  What is written may not overlap anything else.
+    """
+
+    def __init__(self, tensors, outs=None):
+        self.tensors = list(tensors)
+        self.outs = self.tensors if outs is None else list(outs)
+        if len(self.outs) != len(self.tensors):
+            raise ValueError(f"outs: {len(self.outs)} for {len(self.tensors)} tensors")
+        self.device = -1
+        self.entries = (MoeTensor * len(self.tensors))()
+        spans = []
+        for i, (t, o) in enumerate(zip(self.tensors, self.outs)):
+            _a_tensor(t, f"tensors[{i}]")
+            if i == 0:
+                self.device = t.get_device()
+            e = self.entries[i]
+            e.in_ = _tensor(t, f"tensors[{i}]", _FLOATS, t.shape, self.device)
+            e.n, e.dtype = t.numel(), DTYPES[t.dtype]
+            size = e.n * t.element_size()
+            if o is not None:
+                e.out = _tensor(o, f"outs[{i}]", (t.dtype,), t.shape, self.device)
+            if size:
+                spans.append((e.in_, e.in_ + size, o is not None and e.out == e.in_, i))
+                if o is not None and e.out != e.in_:
+                    spans.append((e.out, e.out + size, True, i))
+        spans.sort(key=lambda s: s[:2])
+        end, wrote = 0, False  # of the span that reaches furthest, and of any that reaches there
+        for start, stop, written, i in spans:
+            if start < end and (written or wrote):
+                raise ValueError(f"tensors[{i}]: memory that is written overlaps another tensor")
+            wrote = written or (wrote and start < end)
+            end = max(end, stop)
+        self.written = [o for o in self.outs if o is not None]
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def moe_clip_grad_norm(tensors, max_norm, norm, ws, eps=1e-6, stream=None):
+    """norm (fp32 [1] or None) = the square root of the sum of all squares; each
+    tensor times min(1, max_norm / (norm + eps)) goes to its out.
+
+    tensors: a TensorList, or tensors that are scaled in place; ws: clip_workspace.
+    """
+    if not isinstance(tensors, TensorList):
+        tensors = TensorList(tensors)
+    n = len(tensors)
+    dev = tensors.device if n else ws.get_device()
+    written = tensors.written
+    for i, t in enumerate(written):
+        if t.requires_grad:
+            _refuse_grad(f"outs[{i}]")
+    pn = None
+    if norm is not None:
+        pn = _tensor(norm, "norm", _F32, (1,), dev)
+        if norm.requires_grad:
+            _refuse_grad("norm")
+        written = written + [norm]
+    _a_tensor(ws, "ws")
+    nws = ws.numel()
+    st = _clip_grad_norm(n, tensors.entries, max_norm, eps, pn, _tensor(ws, "ws", _U8, (nws,), dev),
+                         nws, _stream(stream, dev))
+    if st:
+        _check(st, "moe_clip_grad_norm")
+    _changed(written)
