@@ -279,7 +279,8 @@ typedef enum {
   MOE_DT_FP16 = 1,
   MOE_DT_FP32 = 2,
   MOE_DT_INT8 = 3,
-  MOE_DT_E4M3 = 4
+  MOE_DT_E4M3 = 4,
+  MOE_DT_U4 = 5 /* two 4-bit codes a byte: only as weights, where said */
 } moe_dtype;
 
 /* Residual addition, RMS norm and 8-bit codes, in one pass:
@@ -400,6 +401,44 @@ moe_status moe_w4_gemv(int32_t n_experts, int32_t N, int32_t K, int32_t group, i
                        const void* scales, const void* scales_up, const uint8_t* zeros,
                        const uint8_t* zeros_up, int32_t out_dtype, void* out, moe_stream_t stream);
 
+/* The whole layer for a few tokens: at most eight, in two kernels, with 16-bit or
+ * 4-bit weights.  moe_layer_forward's result,
+ *   out[t] = sum over picks of w * (expert's FFN, or x_t for zero-computation experts)
+ *            + shared expert,
+ * for decode steps and short drafts, where that call's launches would take longer than
+ * the picked experts' weights.  Logits and statistics are fp32; 16-bit weights meet x
+ * as it is and h as a sum of two 16-bit numbers, 4-bit weights meet x exactly (elements
+ * below 2^-23 of a token's largest are rounded at 2^-33 of it) and h with 11 bits; all
+ * sums and scales are fp32 and out is rounded once.  The same bits on every call.
+ *  cfg       wdtype MOE_W_BF16 whatever the weights are; out_fp32, gemv_max_rows,
+ *            combine and ffn_launch are not read
+ *  T         <= 8, T * hidden <= 65536 (MOE_ERR_UNSUPPORTED otherwise, and where one
+ *            SM's shared memory has no room for the tokens beside two stages of weights)
+ *  dtype     MOE_DT_BF16 or MOE_DT_FP16: x and out, [T, H] with row strides ldx, ldo
+ *  w_router, bias  as for moe_route
+ *  topk_ids, topk_w  as written by moe_route, or NULL: not wanted
+ *  ws        moe_few_tokens_workspace_size bytes, 256-byte aligned, zeroed once before its
+ *            first use; its head is the status block of moe_check_device_status
+ * Weights: gate and up [E_r, I, H], down [E_r, H, I], the shared expert's without E_r. */
+typedef struct {
+  const void* w[3];       /* gate, up, down */
+  const void* scales[3];  /* MOE_DT_U4: [.., K / group], else NULL */
+  const uint8_t* zeros[3]; /* MOE_DT_U4: zero points 0 .. 31 as moe_w4_gemv's, or NULL (8):
+                             for all of the call's matrices or for none */
+} moe_few_expert;
+typedef struct {
+  int32_t w_dtype;     /* x's dtype, or MOE_DT_U4: codes packed as moe_w4_gemv's; H, I and
+                          the shared expert's I multiples of 32 and of group */
+  int32_t group;       /* MOE_DT_U4: 32, 64, 128, or 0 (one scale a row) */
+  int32_t scale_dtype; /* MOE_DT_U4: MOE_DT_BF16, MOE_DT_FP16 or MOE_DT_FP32 */
+  moe_few_expert routed, shared;
+} moe_few_weights;
+moe_status moe_few_tokens_workspace_size(const moe_config* cfg, int32_t T, size_t* bytes);
+moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weights* weights, int32_t T,
+                          int32_t dtype, const void* x, int64_t ldx, const float* w_router,
+                          const float* bias, int32_t* topk_ids, float* topk_w, void* out,
+                          int64_t ldo, void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* Global norm of many tensors, and the tensors scaled so that it is at most max_norm:
  *   norm = sqrt(sum of the squares of all elements);  c = min(1, max_norm / (norm + eps))
  *   out = in * c for each tensor that has an out
@@ -463,6 +502,8 @@ typedef enum {
   MOE_K_UNSORT,      /* moe_unsort_tokens, moe_sort_tokens_backward */
   MOE_K_UNSORT_GRAD, /* moe_unsort_tokens_backward */
   MOE_K_W4,          /* moe_w4_gemv */
+  MOE_K_FEW_ROUTE,   /* moe_few_tokens: router and top-k */
+  MOE_K_FEW_FFN,     /* moe_few_tokens: experts and combine */
   MOE_K_GRAD_NORM,   /* moe_clip_grad_norm: sums of squares */
   MOE_K_CLIP,        /* moe_clip_grad_norm: products */
   MOE_K_COUNT

@@ -44,7 +44,7 @@ FFN_LAUNCH_DEFAULT, FFN_LAUNCH_TWO, FFN_LAUNCH_ONE, FFN_LAUNCH_ONE_WIDE = 0, 1, 
 KERNELS = ["router", "topk", "perm_count", "perm_scan", "perm_scatter", "perm_gather",
            "worklist", "gemv_gate_up", "gemv_down", "tc_gate_up", "tc_down", "quant_h", "combine",
            "w8_exact", "sort", "norm", "sort_plan", "sort_rows", "unsort", "unsort_grad", "w4",
-           "grad_norm", "clip"]
+           "few_route", "few_ffn", "grad_norm", "clip"]
 N_KERNELS = len(KERNELS)
 
 
@@ -56,6 +56,17 @@ class MoeConfig(ctypes.Structure):
         (n, ctypes.c_int32) for n in (
             "bias_mode", "shared_inter", "wdtype", "out_fp32", "gemv_max_rows", "combine",
             "ffn_launch")]
+
+
+class MoeFewExpert(ctypes.Structure):
+    """Mirror of moe_few_expert in include/moe.h."""
+    _fields_ = [(n, ctypes.c_void_p * 3) for n in ("w", "scales", "zeros")]
+
+
+class MoeFewWeights(ctypes.Structure):
+    """Mirror of moe_few_weights in include/moe.h."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("w_dtype", "group", "scale_dtype")] + [
+        (n, MoeFewExpert) for n in ("routed", "shared")]
 
 
 class MoeTensor(ctypes.Structure):
@@ -103,6 +114,9 @@ _SIGS = {
     "moe_unsort_tokens_backward": [_I, _I, _I, _I, _I, _I, _P, _L, _P, _P, _P, _P, _P, _P, _I,
                                    _P],
     "moe_w4_gemv": [_I, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _I, _P, _P, _P, _P, _I, _P, _P],
+    "moe_few_tokens_workspace_size": [_C, _I, ctypes.POINTER(_SZ)],
+    "moe_few_tokens": [_C, ctypes.POINTER(MoeFewWeights), _I, _I, _P, _L, _P, _P, _P, _P, _P, _L,
+                       _P, _SZ, _P],
     "moe_clip_workspace_size": [ctypes.POINTER(_SZ)],
     "moe_clip_grad_norm": [_I, ctypes.POINTER(MoeTensor), _F, _F, _P, _P, _SZ, _P],
     "moe_selftest_wait_timeout": [_P, ctypes.c_int64, _P],
@@ -123,7 +137,8 @@ EXPORTS = sorted(list(_SIGS) + ["moe_status_string", "moe_kernel_name"])
 _OPERATORS = ("moe_add_rmsnorm", "moe_sort_workspace_size", "sort_workspace", "moe_sort_tokens",
               "moe_sort_tokens_backward", "moe_unsort_tokens", "moe_unsort_tokens_backward",
               "moe_w4_gemv", "pack_w4", "moe_clip_workspace_size", "clip_workspace", "TensorList",
-              "moe_clip_grad_norm")
+              "moe_clip_grad_norm", "FewTokenExperts", "moe_few_tokens_workspace_size",
+              "few_tokens_workspace", "moe_few_tokens")
 
 
 def __getattr__(name):

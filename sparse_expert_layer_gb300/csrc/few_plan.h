@@ -1,0 +1,68 @@
+// Shared-memory plan of the layer for a few tokens (few_tokens.cu), host code only.
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+
+namespace moe {
+
+constexpr int kFewMaxT = 8;
+constexpr int kFewWarps = 16;
+constexpr int kFewTeamWarps = 4;  // warps that share the K of one gate/up tile
+constexpr int kFewTeams = kFewWarps / kFewTeamWarps;
+constexpr int kFewSub = 2048;     // bytes of the weights of a ring stage: 16 rows of 128
+constexpr int kFewMaxStages = 8;
+constexpr int kFewSmem = 226 * 1024;  // dynamic; the kernel has a few words besides
+constexpr int kFewUnitBytes = 40;
+
+// Layout of a CTA's shared memory: x, its block sums, units, parts, rings.
+struct FewPlan {
+  int step_k;          // K of a stage: 256 four-bit or 64 sixteen-bit weights a row
+  int xpitch;          // bytes between two tokens
+  int block;           // K that shares a scale: 32, 64 or 128
+  int sum_at, unit_at, red_at, queue_at, ring_at;
+  int swords, zwords;  // 4-byte words of scales and zero points a row has in a stage
+  int sub_bytes;       // of a stage
+  int stages;
+  int bytes;           // of the CTA; stages < 2: does not fit
+};
+
+inline int few_round(int v, int to) { return (v + to - 1) / to * to; }
+
+// The 4-byte words that hold n items of `size` bytes which start `size`-aligned in rows
+// of `row` bytes.
+inline int few_words(int n, int size, int64_t row) {
+  const int bytes = n * size;
+  return row % 4 == 0 && bytes % 4 == 0 ? bytes / 4 : (bytes + 4 - size + 3) / 4;
+}
+
+// mt: 16-row tiles of a gate/up tile; group: 0 (a row), 32, 64, 128; longest: the
+// largest K of the layer's matrices
+inline FewPlan few_plan(int T, int H, int units, bool four_bits, int group, int scale_bytes,
+                        bool zeros, bool rows_aligned_scales, bool rows_aligned_zeros, int mt) {
+  FewPlan p{};
+  p.step_k = four_bits ? 256 : 64;
+  p.block = four_bits ? (group ? group : 128) : 0;
+  // two tokens' 64-byte pieces cover the banks
+  p.xpitch = few_round(H, p.step_k) * 2 + 64;
+  p.sum_at = T * p.xpitch;
+  const int blocks = four_bits ? few_round(H, p.step_k) / p.block : 0;
+  p.unit_at = p.sum_at + blocks * kFewMaxT * 4;
+  p.red_at = few_round(p.unit_at + units * kFewUnitBytes, 16);
+  p.queue_at = p.red_at + kFewTeams * kFewTeamWarps * mt * 16 * 8 * 4;
+  p.ring_at = few_round(p.queue_at + kFewTeams * 16 * 4, 128);
+  p.sub_bytes = kFewSub;
+  if (four_bits) {
+    const int n = group ? p.step_k / group : 1;
+    p.swords = few_words(n, scale_bytes, rows_aligned_scales ? 4 : scale_bytes);
+    p.zwords = zeros ? few_words(n, 1, rows_aligned_zeros ? 4 : 1) : 0;
+    p.sub_bytes += few_round(16 * 4 * (p.swords + p.zwords), 16);
+  }
+  p.stages = std::min(kFewMaxStages, (kFewSmem - p.ring_at) / (kFewWarps * p.sub_bytes));
+  p.bytes = p.ring_at + kFewWarps * p.stages * p.sub_bytes;
+  // the parts of the down projection lie over the rings: 16 warps of 64 channels
+  if (p.stages * p.sub_bytes < 64 * kFewMaxT * 4) p.stages = 0;
+  return p;
+}
+
+}  // namespace moe

@@ -427,7 +427,9 @@ enum {
   kAttrRouteSmall,
   kAttrW4Base,                   // x type x group x zero points
   kAttrW4Slots = 3 * 3 * 2,
-  kAttrSlots = kAttrW4Base + kAttrW4Slots
+  kAttrFewRoute = kAttrW4Base + kAttrW4Slots,  // 4 slots: tokens 1, 2, 4, 8
+  kAttrFewFfn = kAttrFewRoute + 4,             // 16 slots: weights x gate/up tile
+  kAttrSlots = kAttrFewFfn + 16
 };
 void set_smem_attr_once(const void* func, int bytes, int slot);
 

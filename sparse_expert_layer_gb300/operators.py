@@ -15,7 +15,7 @@ import ctypes
 
 import torch
 
-from . import MoeTensor, _check, lib
+from . import MoeConfig, MoeFewWeights, MoeTensor, _check, lib
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int8: 3,
           torch.float8_e4m3fn: 4}
@@ -25,6 +25,7 @@ _ANY = frozenset(DTYPES)
 _F32 = frozenset((torch.float32,))
 _I32 = frozenset((torch.int32,))
 _U8 = frozenset((torch.uint8,))
+_U4 = 5  # MOE_DT_U4
 
 _W4_X = frozenset((torch.bfloat16, torch.float16, torch.int8))
 
@@ -35,6 +36,7 @@ _unsort_tokens = lib.moe_unsort_tokens
 _unsort_tokens_backward = lib.moe_unsort_tokens_backward
 _w4_gemv = lib.moe_w4_gemv
 _clip_grad_norm = lib.moe_clip_grad_norm
+_few_tokens = lib.moe_few_tokens
 # torch.autograd.graph.increment_version for several tensors, without its type checks
 _changed = torch._C._increment_version
 
@@ -435,4 +437,133 @@ def moe_clip_grad_norm(tensors, max_norm, norm, ws, eps=1e-6, stream=None):
                          nws, _stream(stream, dev))
     if st:
         _check(st, "moe_clip_grad_norm")
+    _changed(written)
+
+
+class FewTokenExperts:
+    """A layer's description and weights as moe_few_tokens takes them, checked once.
+
+    cfg: MoeConfig with the wdtype of a bf16 layer, whatever the weights are.
+    weights: w_gate, w_up [E, I, H] and w_down [E, H, I], with a shared expert also
+    shared_gate, shared_up [I_s, H] and shared_down [H, I_s]: all bf16, all fp16 (the
+    type of x), or all uint8 codes of pack_w4 (half the last dimension).  4-bit weights
+    have scales s_gate, ..., s_shared_down [.., groups] of one type, and may have uint8
+    zero points z_gate, ... of the same shapes (all or none).
+    w_router [E + zero experts, H] and bias fp32 as for moe_route.
+    """
+
+    def __init__(self, cfg, weights, w_router, bias=None):
+        if not isinstance(cfg, MoeConfig):
+            raise TypeError(f"cfg: expected a MoeConfig, got {type(cfg).__name__}")
+        _a_tensor(w_router, "w_router")
+        self.cfg, self.device = cfg, w_router.get_device()
+        self.kept = dict(weights), w_router, bias  # what the addresses below belong to
+        H, E = cfg.hidden, cfg.n_routed
+        total = E + cfg.n_zero
+        self.w_router = _tensor(w_router, "w_router", _F32, (total, H), self.device)
+        self.bias = None if bias is None else _tensor(bias, "bias", _F32, (total,), self.device)
+        self.c = MoeFewWeights()
+        first = weights.get("w_gate" if E else "shared_gate")
+        self.dtype = None  # of x: any 16-bit type with 4-bit weights
+        four, scale_type, groups0 = False, None, None
+        if E or cfg.shared_inter:
+            _a_tensor(first, "w_gate" if E else "shared_gate")
+            four = first.dtype == torch.uint8
+            if not four and first.dtype not in (torch.bfloat16, torch.float16):
+                raise TypeError(f"weights: {first.dtype} is none of bf16, fp16 and uint8")
+            self.dtype = None if four else first.dtype
+            self.c.w_dtype = _U4 if four else DTYPES[first.dtype]
+        names = []
+        if E:
+            names.append((self.c.routed, "w_", "", (E,), cfg.inter))
+        if cfg.shared_inter:
+            names.append((self.c.shared, "shared_", "shared_", (), cfg.shared_inter))
+        self.zeros = None
+        for part, prefix, infix, lead, inter in names:
+            for i, (m, n, k) in enumerate((("gate", inter, H), ("up", inter, H),
+                                           ("down", H, inter))):
+                name = prefix + m
+                shape = (*lead, n, k // 2 if four else k)
+                part.w[i] = _tensor(weights.get(name), name, (first.dtype,), shape, self.device)
+                if not four:
+                    continue
+                sname, zname = "s_" + infix + m, "z_" + infix + m
+                s, z = weights.get(sname), weights.get(zname)
+                _a_tensor(s, sname)
+                if s.dim() != len(shape):
+                    raise ValueError(f"{sname}: shape {tuple(s.shape)}")
+                groups = s.shape[-1]
+                if groups < 1 or k % groups:
+                    raise ValueError(f"{sname}: {groups} groups do not divide K = {k}")
+                width = k // groups if groups > 1 else 0
+                # one group a row is `0` unless the other matrices say how wide it is
+                if groups0 is None or groups0 == 0:
+                    groups0 = width
+                if width != groups0 and not (width == 0 and k == groups0):
+                    raise ValueError(f"{sname}: groups of {k // groups}, others of {groups0}")
+                scale_type = scale_type or s.dtype
+                part.scales[i] = _tensor(s, sname, (scale_type,) if scale_type in _FLOATS else
+                                         _FLOATS, (*lead, n, groups), self.device)
+                if self.zeros is None:
+                    self.zeros = z is not None
+                if self.zeros != (z is not None):
+                    raise ValueError(f"{zname}: zero points for all matrices or for none")
+                if z is not None:
+                    part.zeros[i] = _tensor(z, zname, _U8, (*lead, n, groups), self.device)
+        if four:
+            if groups0:  # rows that hold one group of that width
+                for _, _, infix, _, inter in names:
+                    for m, k in (("gate", H), ("up", H), ("down", inter)):
+                        if k // weights["s_" + infix + m].shape[-1] != groups0:
+                            raise ValueError(f"s_{infix}{m}: not in groups of {groups0}")
+            self.c.group, self.c.scale_dtype = groups0, DTYPES[scale_type]
+
+
+def moe_few_tokens_workspace_size(cfg, T) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib.moe_few_tokens_workspace_size(ctypes.byref(cfg), T, ctypes.byref(n)),
+           "moe_few_tokens_workspace_size")
+    return n.value
+
+
+def few_tokens_workspace(experts, T):
+    """Zeroed uint8 tensor of moe_few_tokens_workspace_size bytes on the experts' device."""
+    dev = f"cuda:{experts.device}" if experts.device >= 0 else "cpu"
+    return torch.zeros(moe_few_tokens_workspace_size(experts.cfg, T), dtype=torch.uint8,
+                       device=dev)
+
+
+_HALVES = frozenset((torch.bfloat16, torch.float16))
+
+
+def moe_few_tokens(experts, x, out, ws, topk_ids=None, topk_w=None, stream=None):
+    """out [T, H] = the layer of a FewTokenExperts for x [T, H], T <= 8 (bf16 or fp16,
+    the weights' type where those have 16 bits; both may have row strides).  ws:
+    few_tokens_workspace; topk_ids int32 and topk_w fp32 [T, k] are written if given."""
+    shape, dev, px, ldx = _matrix(x, "x", _HALVES if experts.dtype is None else (experts.dtype,))
+    T, H = shape
+    cfg = experts.cfg
+    if H != cfg.hidden:
+        raise ValueError(f"x: {H} channels, the layer has {cfg.hidden}")
+    if dev != experts.device:
+        raise ValueError(f"x: on {x.device}, the experts on CUDA device {experts.device}")
+    po, ldo = _rows(out, "out", (x.dtype,), shape, dev)
+    if out.requires_grad:
+        _refuse_grad("out")
+    written, pi, pw = [out], None, None
+    if topk_ids is not None:
+        pi = _tensor(topk_ids, "topk_ids", _I32, (T, cfg.top_k), dev)
+        written.append(topk_ids)
+    if topk_w is not None:
+        pw = _tensor(topk_w, "topk_w", _F32, (T, cfg.top_k), dev)
+        if topk_w.requires_grad:
+            _refuse_grad("topk_w")
+        written.append(topk_w)
+    _a_tensor(ws, "ws")
+    nws = ws.numel()
+    st = _few_tokens(cfg, experts.c, T, DTYPES[x.dtype], px, ldx, experts.w_router, experts.bias,
+                     pi, pw, po, ldo, _tensor(ws, "ws", _U8, (nws,), dev), nws,
+                     _stream(stream, dev))
+    if st:
+        _check(st, "moe_few_tokens")
     _changed(written)

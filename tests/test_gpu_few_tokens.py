@@ -1,0 +1,420 @@
+"""moe_few_tokens against its definition: picks and weights from the fp64 oracle's
+router, the experts in 64 bits on the GPU.
+
+Tolerance, element by element, u = 2^-24.  A sum of K products leaves at most
+(K / 8 + 64) u times the sum of the magnitudes that were added: each MMA of sixteen
+products rounds within two u of what it holds, and the few additions that join blocks,
+warps and scales follow (4 bits: the magnitudes are those of q x and z x).  h carries
+the errors of gate and up (|silu'| <= 1.1) and its own rounding: 2^-12 of it and 2^-34
+of the row's largest with 4-bit weights, 2^-17 as two bf16 numbers, 2^-22 as two fp16
+ones.  Routing weights are within 1e-5, and out is rounded once.
+"""
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import synth
+from tests import gpu_support as gs
+from tests import support
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0**-24
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+TINY = {BF16: 2.0**-134, FP16: 2.0**-25}
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def m():
+    return gs.lib()
+
+
+def gen(seed=0):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+# description overrides of a small softmax layer
+LAYERS = {
+    "flat": dict(hidden=512, inter=256, n_routed=16, top_k=4, renormalize=True),
+    "groups": dict(hidden=1024, inter=320, n_routed=64, top_k=8, n_group=8, topk_group=4,
+                   score="sigmoid", renormalize=True, routed_scale=2.5, shared_inter=384),
+    "per_group": dict(hidden=640, inter=384, n_routed=64, top_k=8, n_group=8, per_group_k=1,
+                      shared_inter=512),
+    "zero": dict(hidden=1024, inter=384, n_routed=96, n_zero=48, top_k=12, bias_mode="logit",
+                 bias_kind="iid", renormalize=False),
+    "select": dict(hidden=288, inter=96, n_routed=24, top_k=3, score="sigmoid",
+                   bias_mode="select", bias_kind="iid", renormalize=True),
+    "only_zero": dict(hidden=256, inter=32, n_routed=0, n_zero=8, top_k=2, renormalize=True),
+    "only_shared": dict(hidden=256, inter=32, n_routed=0, n_zero=4, top_k=1, shared_inter=160),
+    "all": dict(hidden=160, inter=64, n_routed=32, top_k=32, renormalize=True),
+    "one": dict(hidden=32, inter=32, n_routed=1, top_k=1),
+    "wide": dict(hidden=64, inter=32, n_routed=2048, top_k=6),
+    "deep": dict(hidden=7168, inter=2048, n_routed=12, top_k=4, shared_inter=2048),
+    # 16-bit weights only
+    "ragged": dict(hidden=1000, inter=200, n_routed=24, n_zero=8, top_k=5, bias_mode="logit",
+                   bias_kind="iid", shared_inter=136),
+    "eight": dict(hidden=8, inter=8, n_routed=4, top_k=2, shared_inter=8),
+    "more_channels": dict(hidden=13104, inter=48, n_routed=4, top_k=2),
+}
+
+
+def make(name, T, dtype, bits, group=0, zeros=False, sdt=None, seed=0):
+    """A layer's inputs: description, x, router, bias and weights on the GPU."""
+    spec = synth.spec("tiny", T=T, name=f"few_{name}", **dict(
+        dict(n_zero=0, renormalize=False), **LAYERS[name]))
+    x, w_r, bias, _ = support.make_inputs(spec, seed)
+    # values that both 16-bit types hold
+    x = torch.where(x.abs() < 2.0**-16, torch.zeros_like(x), x)
+    g = gen(seed + T)
+    E, H, I, Is = spec["n_routed"], spec["hidden"], spec["inter"], spec["shared_inter"]
+    w = {}
+
+    def stack(key, infix, mat, shape):
+        K = shape[-1]
+        if bits == 16:
+            w[key] = (torch.randn(*shape, generator=g, device="cuda") / K**0.5).to(dtype)
+            return
+        groups = K // group if group else 1
+        codes = torch.randint(0, 16, shape, generator=g, device="cuda", dtype=torch.uint8)
+        w[key] = gs.lib().pack_w4(codes)
+        w[f"s_{infix}{mat}"] = ((0.3 + torch.rand(*shape[:-1], groups, generator=g, device="cuda"))
+                                / (4.6 * K**0.5)).to(sdt or dtype)
+        if zeros:
+            w[f"z_{infix}{mat}"] = torch.randint(0, 32, (*shape[:-1], groups), generator=g,
+                                                 device="cuda", dtype=torch.uint8)
+
+    for mat, n, k in (("gate", I, H), ("up", I, H), ("down", H, I)):
+        if E:
+            stack("w_" + mat, "", mat, (E, n, k))
+        if Is:
+            n, k = (Is if mat != "down" else H), (H if mat != "down" else Is)
+            stack("shared_" + mat, "shared_", mat, (n, k))
+    return dict(spec=spec, x16=x, x=x.to(dtype).cuda(), w_r=w_r, bias=bias, w=w, bits=bits,
+                dtype=dtype)
+
+
+def exact_matrix(w, key, infix, mat, e):
+    """(values, magnitudes that the kernel adds) of one matrix in 64 bits."""
+    t = w[key] if e is None else w[key][e]
+    if t.dtype != torch.uint8:
+        v = t.double()
+        return v, v.abs()
+    s = w[f"s_{infix}{mat}"]
+    z = w.get(f"z_{infix}{mat}")
+    s, z = (s, z) if e is None else (s[e], None if z is None else z[e])
+    q = torch.stack([t & 15, t >> 4], -1).view(t.shape[0], -1).double()
+    width = q.shape[1] // s.shape[1]
+    z = torch.full_like(s, 8.0, dtype=torch.float64) if z is None else z.double()
+    z, s = z.repeat_interleave(width, 1), s.double().repeat_interleave(width, 1)
+    return (q - z) * s, (q + z) * s
+
+
+def exact_ffn(c, prefix, infix, e, x):
+    """(y, bound of its error) of one expert for one token, in 64 bits."""
+    four = c["bits"] == 4
+
+    def product(mat, v, mag):
+        a, b = exact_matrix(c["w"], prefix + mat, infix, mat, e)
+        return a @ v, (a.shape[1] / 8 + 64) * U * (b @ mag), a
+
+    xa = x.abs()
+    # 4 bits: x below 2^-23 of its largest is rounded at 2^-33 of that
+    round_x = 2.0**-33 * xa.max() if four else 0.0
+    g, dg, ga = product("gate", x, xa)
+    u, du, ua = product("up", x, xa)
+    dg = dg + round_x * ga.abs().sum(1)
+    du = du + round_x * ua.abs().sum(1)
+    silu = g * torch.sigmoid(g)
+    h = silu * u
+    dh = 1.1 * dg * u.abs() + (silu.abs() + 1.1 * dg) * du + 16 * U * h.abs()
+    top = (h.abs() + dh).max()
+    rel = 2.0**-12 if four else 2.0**-17 if c["dtype"] == BF16 else 2.0**-22
+    dh = dh + rel * (h.abs() + dh) + 2.0**-34 * top
+    y, dy, da = product("down", h, h.abs() + dh)
+    return y, dy + da.abs() @ dh
+
+
+def exact(c, ids, wts):
+    """(out, bound) of the whole layer; ids, wts [T, k] in 64 bits."""
+    spec = c["spec"]
+    E = spec["n_routed"]
+    T = ids.shape[0]
+    out = torch.zeros(T, spec["hidden"], dtype=torch.float64, device="cuda")
+    tol = torch.zeros_like(out)
+    for t in range(T):
+        x = c["x"][t].double()
+        for e, p in zip(ids[t].tolist(), wts[t].tolist()):
+            y, dy = exact_ffn(c, "w_", "", e, x) if e < E else (x, torch.zeros_like(x))
+            out[t] += p * y
+            tol[t] += abs(p) * (dy + (1e-5 + 64 * U) * y.abs())
+        if spec["shared_inter"]:
+            y, dy = exact_ffn(c, "shared_", "shared_", None, x)
+            out[t] += y
+            tol[t] += dy + 64 * U * y.abs()
+    return out, tol + torch.finfo(c["dtype"]).eps / 2 * (out.abs() + tol) + TINY[c["dtype"]]
+
+
+def experts_of(m, c):
+    cfg = m.config_from_spec(c["spec"])
+    bias = None if c["bias"] is None else c["bias"].cuda()
+    return m.FewTokenExperts(cfg, c["w"], c["w_r"].cuda(), bias)
+
+
+def routed(c):
+    spec = c["spec"]
+    ids, w, _, _ = oracle.route(spec, synth.bf16_bits(c["x16"]), c["w_r"].numpy(),
+                                support.np_bias(c["bias"]))
+    return torch.from_numpy(np.asarray(ids)), torch.from_numpy(np.asarray(w, dtype=np.float64))
+
+
+def check(m, c, x=None, extra=0):
+    spec = c["spec"]
+    T, H, k = spec["T"], spec["hidden"], spec["top_k"]
+    experts = experts_of(m, c)
+    ws = m.few_tokens_workspace(experts, T)
+    guard = torch.full((ws.numel() + 512,), 0, dtype=torch.uint8, device="cuda")
+    guard[ws.numel():] = 99
+    x = c["x"] if x is None else x
+    wide = torch.full((T, H + extra), 7.0, dtype=c["dtype"], device="cuda")
+    ids = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    w = torch.full((T, k), -1.0, device="cuda")
+    m.moe_few_tokens(experts, x, wide[:, :H], guard[:ws.numel()], ids, w)
+    torch.cuda.synchronize()
+    assert m.moe_check_device_status(guard) == m.MOE_OK
+    assert (guard[ws.numel():] == 99).all() and (wide[:, H:] == 7).all()
+    ids_o, w_o = routed(c)
+    assert torch.equal(ids.cpu().long(), ids_o.long())
+    assert np.allclose(w.cpu().numpy(), w_o.numpy(), rtol=1e-5, atol=1e-7)
+    want, tol = exact(c, ids_o, w_o)
+    over = (wide[:, :H].double() - want).abs() - tol
+    assert float(over.max()) <= 0, f"off by {float((wide[:, :H].double() - want).abs().max()):.3e}, " \
+        f"{float(over.max()):.3e} more than allowed"
+    return wide[:, :H]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("T", [1, 2, 3, 8])
+@pytest.mark.parametrize("name", list(LAYERS))
+def test_sixteen_bit_weights(m, name, T, dtype):
+    if T * LAYERS[name]["hidden"] > 65536:
+        T = 65536 // LAYERS[name]["hidden"]
+    check(m, make(name, T, dtype, 16))
+
+
+FOUR = ["flat", "groups", "per_group", "zero", "select", "only_zero", "only_shared", "all", "one",
+        "wide", "deep"]
+
+
+@pytest.mark.parametrize("T", [1, 2, 5, 8])
+@pytest.mark.parametrize("name", FOUR)
+@pytest.mark.parametrize("dtype,group,zeros,sdt", [(BF16, 32, False, BF16), (BF16, 0, True, FP32),
+                                                   (FP16, 32, True, FP16), (FP16, 0, False, BF16)])
+def test_four_bit_weights(m, name, T, dtype, group, zeros, sdt):
+    check(m, make(name, T, dtype, 4, group, zeros, sdt))
+
+
+@pytest.mark.parametrize("T", [1, 4, 8])
+@pytest.mark.parametrize("name,group", [("flat", 64), ("flat", 128), ("per_group", 128),
+                                        ("groups", 64), ("zero", 64), ("zero", 128),
+                                        ("deep", 64), ("deep", 128), ("deep", 32)])
+@pytest.mark.parametrize("zeros,sdt", [(False, BF16), (True, FP16), (True, FP32)])
+def test_four_bit_groups(m, name, T, group, zeros, sdt):
+    check(m, make(name, T, BF16, 4, group, zeros, sdt))
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("T", [2, 3, 7])
+def test_all_tokens_alike(m, bits, T):
+    # every expert has all tokens
+    c = make("groups", T, BF16, bits, 32)
+    c["x16"][:] = c["x16"][0].clone()
+    c["x"][:] = c["x"][0].clone()
+    out = check(m, c)
+    assert (out == out[0]).all()
+
+
+@pytest.mark.parametrize("extra", [8, 3])
+@pytest.mark.parametrize("bits", [4, 16])
+def test_row_strides(m, extra, bits):
+    c = make("flat", 5, BF16, bits, 64)
+    wide = torch.full((5, 512 + extra), float("nan"), dtype=BF16, device="cuda")
+    wide[:, :512] = c["x"]
+    check(m, c, wide[:, :512], extra)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("bits", [4, 16])
+def test_a_loud_channel(m, dtype, bits):
+    # x spans many binades; its largest value sets the scale of a 4-bit product's x
+    c = make("flat", 3, dtype, bits, 32)
+    scale = torch.exp2(torch.randint(-12, 1, c["x"].shape, generator=gen(1), device="cuda").float())
+    x = (c["x"].float() * scale).to(BF16)
+    x[:, 17] *= 64
+    x = torch.where(x.abs() < 2.0**-16, torch.zeros_like(x), x)
+    c["x16"], c["x"] = x.cpu(), x.to(dtype)
+    if not support.margin_rows(c["spec"], c["x16"], c["w_r"], c["bias"], 1e-4).all():
+        pytest.skip("the picks are not clear")
+    check(m, c)
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_token_that_is_not_finite_stays_alone(m, bits, bad):
+    c = make("flat", 4, BF16, bits, 32)
+    experts = experts_of(m, c)
+    ws = m.few_tokens_workspace(experts, 4)
+    good, out = torch.empty_like(c["x"]), torch.empty_like(c["x"])
+    m.moe_few_tokens(experts, c["x"], good, ws)
+    x = c["x"].clone()
+    x[2, 5] = bad
+    m.moe_few_tokens(experts, x, out, ws)
+    torch.cuda.synchronize()
+    rest = [0, 1, 3]
+    # (the other token's picks may differ, and with them the order of the sums)
+    assert torch.isfinite(out[rest]).all()
+    assert ((out[rest].double() - good[rest].double()).abs()
+            <= 2.0**-7 * good[rest].double().abs() + 1e-3).all()
+    assert not torch.isfinite(out[2]).all()
+    m.moe_few_tokens(experts, c["x"], out, ws)
+    assert torch.equal(out, good)
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+def test_zero_tokens_and_tiny_ones(m, bits):
+    c = make("flat", 3, BF16, bits, 32)
+    experts = experts_of(m, c)
+    ws = m.few_tokens_workspace(experts, 3)
+    x, out = c["x"].clone(), torch.empty_like(c["x"])
+    x[0] = 0
+    x[1] = (x[1].float() * 2.0**-60).to(BF16)  # gate and up survive, h underflows to nothing
+    m.moe_few_tokens(experts, x, out, ws)
+    assert (out[0] == 0).all() and torch.isfinite(out).all() and float(out[1].abs().max()) < 1e-30
+    assert m.moe_check_device_status(ws) == m.MOE_OK
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+def test_the_same_bits_on_every_call_and_in_a_graph(m, bits):
+    c = make("groups", 8, BF16, bits, 32)
+    experts = experts_of(m, c)
+    ws = m.few_tokens_workspace(experts, 8)
+    out = torch.empty_like(c["x"])
+    m.moe_few_tokens(experts, c["x"], out, ws)
+    first = out.clone()
+    for _ in range(20):
+        out.fill_(7)
+        m.moe_few_tokens(experts, c["x"], out, ws)
+        assert torch.equal(out, first)
+    graph = torch.cuda.CUDAGraph()
+    x = c["x"].clone()
+    with torch.cuda.graph(graph):
+        m.moe_few_tokens(experts, x, out, ws)
+        m.moe_few_tokens(experts, out, x, ws)  # back to back: the second reads the first's output
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first)
+    again = torch.empty_like(x)
+    m.moe_few_tokens(experts, first, again, ws)
+    assert torch.equal(x, again)
+    assert m.moe_check_device_status(ws) == m.MOE_OK
+
+
+def test_one_workspace_for_batches_of_any_size(m):
+    c = make("groups", 8, BF16, 4, 32)
+    experts = experts_of(m, c)
+    ws = m.few_tokens_workspace(experts, 8)
+    want = torch.empty_like(c["x"])
+    m.moe_few_tokens(experts, c["x"], want, ws)
+    for T in (1, 8, 3, 2, 7):
+        out = torch.empty_like(c["x"][:T])
+        m.moe_few_tokens(experts, c["x"][:T], out, ws)
+        assert ((out.double() - want[:T].double()).abs()
+                <= 2.0**-7 * want[:T].double().abs() + 1e-3).all()
+    m.moe_few_tokens(experts, c["x"][:0], c["x"][:0], ws)  # no tokens: nothing to do
+    small = m.few_tokens_workspace(experts, 1)
+    with pytest.raises(m.MoeError, match="workspace too small"):
+        m.moe_few_tokens(experts, c["x"], want, small)
+
+
+def test_two_streams_at_once(m):
+    c = [make("deep", T, BF16, 4, 128, seed=T) for T in (1, 4)]
+    experts = [experts_of(m, v) for v in c]
+    streams = [torch.cuda.Stream() for _ in c]
+    ws = [m.few_tokens_workspace(e, v["spec"]["T"]) for e, v in zip(experts, c)]
+    want = [torch.empty_like(v["x"]) for v in c]
+    outs = [torch.empty_like(v["x"]) for v in c]
+    for e, v, w, o in zip(experts, c, ws, want):
+        m.moe_few_tokens(e, v["x"], o, w)
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for e, v, w, o, s in zip(experts, c, ws, outs, streams):
+            m.moe_few_tokens(e, v["x"], o, w, stream=s)
+    torch.cuda.synchronize()
+    for o, w, v in zip(outs, ws, want):
+        assert torch.equal(o, v)
+        assert m.moe_check_device_status(w) == m.MOE_OK
+
+
+def test_launches_and_arguments(m):
+    c = make("flat", 4, BF16, 16)
+    experts = experts_of(m, c)
+    ws = m.few_tokens_workspace(experts, 4)
+    out = torch.empty_like(c["x"])
+    before = m.launch_counts()
+    m.moe_few_tokens(experts, c["x"], out, ws)
+    after = m.launch_counts()
+    assert {k: after[k] - before[k] for k in after if after[k] != before[k]} == \
+        {"few_route": 1, "few_ffn": 1}
+    for bad, error in ((dict(x=c["x"].half()), TypeError), (dict(x=c["x"][:, :256]), ValueError),
+                       (dict(out=out.half()), TypeError), (dict(out=out[:2]), ValueError),
+                       (dict(ws=None), TypeError), (dict(x=c["x"].cpu()), ValueError),
+                       (dict(topk_ids=torch.empty(4, 4, device="cuda")), TypeError),
+                       (dict(topk_w=torch.empty(4, 3, device="cuda")), ValueError)):
+        a = dict(dict(x=c["x"], out=out, ws=ws), **bad)
+        with pytest.raises(error):
+            m.moe_few_tokens(experts, **a)
+    with pytest.raises(m.MoeError, match="unsupported"):
+        nine = torch.zeros(9, 512, dtype=BF16, device="cuda")
+        m.moe_few_tokens(experts, nine, torch.empty_like(nine), ws)
+    with pytest.raises(ValueError, match="requires a gradient"):
+        m.moe_few_tokens(experts, c["x"], torch.empty_like(c["x"]).requires_grad_(), ws)
+
+
+def test_as_the_layer_itself(m):
+    """The same weights through moe_layer_forward, within both calls' roundings."""
+    c = make("groups", 8, BF16, 16)
+    got = check(m, c)
+    spec, w = c["spec"], c["w"]
+    cfg = m.config_from_spec(spec)
+    out = torch.empty_like(got)
+    ws = m.workspace(cfg, 8)
+    m.moe_layer_forward(cfg, 8, c["x"], c["w_r"].cuda(), None, w["w_gate"], w["w_up"], w["w_down"],
+                        None, None, None, w["shared_gate"], w["shared_up"], w["shared_down"], out,
+                        ws)
+    torch.cuda.synchronize()
+    assert float((out.double() - got.double()).norm() / got.double().norm()) <= gs.REL_L2
+
+
+def test_plain_launches_give_the_same_bits(m, tmp_path):
+    """MOE_PDL=0 in another process: the second kernel then starts after the first."""
+    code = (
+        "import sys, torch\n"
+        "from tests import test_gpu_few_tokens as t, gpu_support as gs\n"
+        "m = gs.lib()\n"
+        "c = t.make('groups', 8, torch.bfloat16, 4, 32)\n"
+        "e = t.experts_of(m, c)\n"
+        "o = torch.empty_like(c['x'])\n"
+        "m.moe_few_tokens(e, c['x'], o, m.few_tokens_workspace(e, 8))\n"
+        "torch.save(o.cpu(), sys.argv[1])\n")
+    outs = []
+    for pdl in ("0", "1"):
+        at = str(tmp_path / pdl)
+        subprocess.run([sys.executable, "-c", code, at], check=True, cwd=ROOT,
+                       env=dict(os.environ, MOE_PDL=pdl), timeout=300)
+        outs.append(torch.load(at))
+    assert torch.equal(*outs)
