@@ -439,6 +439,50 @@ moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weights* weights,
                           const float* bias, int32_t* topk_ids, float* topk_w, void* out,
                           int64_t ldo, void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/* Low-rank adapters of many requests at once, beside a projection that they share
+ * (whose output is `base`): for the positions p = offsets[j] .. offsets[j+1]-1 of adapter j,
+ * t = order[p],
+ *   v[p] = x[t] A_j^T;   y[t] = base[t] + scale[j] * v[p] B_j
+ * A row without an adapter (positions from offsets[n_adapters] on) is its base.  offsets
+ * and order are moe_sort_tokens' offsets and sorted_to_expanded for ids [T, 1], one sort
+ * for all projections of a step.  Sums are fp32; v enters the second product as two
+ * 16-bit numbers (2^-17 of it is lost in bf16, 2^-22 in fp16; exactly where each row has
+ * its own CTAs); y is rounded once.  The same bits on every call.
+ *  r, T      1 <= r <= 128; T <= 2^21, n_adapters <= 4096, K, N <= 2^21
+ *  dtype     MOE_DT_BF16 or MOE_DT_FP16: x [T, K], a [n_adapters, r, K],
+ *            b [n_adapters, r, N], base and y [T, N]; row strides ldx, ldb, ldy
+ *  scale     fp32 [n_adapters], or NULL (1)
+ *  order     int32 [T], a permutation, or NULL: rows are sorted already.  Positions whose
+ *            row lies outside [0, T) are skipped
+ *  base      NULL: zeros; may be y itself (the same stride): rows without an adapter are
+ *            then not written
+ *  v         fp32 [T, r] out, what moe_adapters_backward needs (positions without an
+ *            adapter are not written), or NULL
+ *  ws        moe_adapters_workspace_size bytes, 256-byte aligned; need not be initialised */
+moe_status moe_adapters_workspace_size(int32_t T, int32_t r, int32_t K, int32_t N, size_t* bytes);
+moe_status moe_adapters(int32_t T, int32_t n_adapters, int32_t r, int32_t K, int32_t N,
+                        int32_t dtype, const void* x, int64_t ldx, const void* a, const void* b,
+                        const float* scale, const int32_t* offsets, const int32_t* order,
+                        const void* base, int64_t ldb, void* y, int64_t ldy, float* v, void* ws,
+                        size_t ws_bytes, moe_stream_t stream);
+
+/* Gradients through moe_adapters (that of base is dy itself): with u[p] = scale[j] *
+ * dy[t] B_j^T,
+ *   dx[t] = u[p] A_j (zeros without an adapter);  dA_j = sum over p of u[p]^T x[t];
+ *   dB_j = scale[j] * sum over p of v[p]^T dy[t]  (zeros for an adapter without rows)
+ * u and v enter the sums over p as three bf16 or two fp16 numbers (24 or 22 bits; fp16:
+ * relative to the largest of the call).  The same bits on every call.
+ *  v          as moe_adapters wrote it
+ *  dx         [T, K] of dtype, row stride lddx, or NULL
+ *  da, db     of grad_dtype (MOE_DT_FP32 or dtype), as a and b, or both NULL (x and v are
+ *             then not read); dx or da is required */
+moe_status moe_adapters_backward(int32_t T, int32_t n_adapters, int32_t r, int32_t K, int32_t N,
+                                 int32_t dtype, const void* dy, int64_t lddy, const void* x,
+                                 int64_t ldx, const float* v, const void* a, const void* b,
+                                 const float* scale, const int32_t* offsets, const int32_t* order,
+                                 void* dx, int64_t lddx, int32_t grad_dtype, void* da, void* db,
+                                 void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* Global norm of many tensors, and the tensors scaled so that it is at most max_norm:
  *   norm = sqrt(sum of the squares of all elements);  c = min(1, max_norm / (norm + eps))
  *   out = in * c for each tensor that has an out
@@ -504,6 +548,8 @@ typedef enum {
   MOE_K_W4,          /* moe_w4_gemv */
   MOE_K_FEW_ROUTE,   /* moe_few_tokens: router and top-k */
   MOE_K_FEW_FFN,     /* moe_few_tokens: experts and combine */
+  MOE_K_ADAPTERS,    /* moe_adapters, moe_adapters_backward: products of rows */
+  MOE_K_ADAPTERS_GRAD, /* moe_adapters_backward: sums over positions */
   MOE_K_GRAD_NORM,   /* moe_clip_grad_norm: sums of squares */
   MOE_K_CLIP,        /* moe_clip_grad_norm: products */
   MOE_K_COUNT

@@ -44,7 +44,7 @@ FFN_LAUNCH_DEFAULT, FFN_LAUNCH_TWO, FFN_LAUNCH_ONE, FFN_LAUNCH_ONE_WIDE = 0, 1, 
 KERNELS = ["router", "topk", "perm_count", "perm_scan", "perm_scatter", "perm_gather",
            "worklist", "gemv_gate_up", "gemv_down", "tc_gate_up", "tc_down", "quant_h", "combine",
            "w8_exact", "sort", "norm", "sort_plan", "sort_rows", "unsort", "unsort_grad", "w4",
-           "few_route", "few_ffn", "grad_norm", "clip"]
+           "few_route", "few_ffn", "adapters", "adapters_grad", "grad_norm", "clip"]
 N_KERNELS = len(KERNELS)
 
 
@@ -117,6 +117,11 @@ _SIGS = {
     "moe_few_tokens_workspace_size": [_C, _I, ctypes.POINTER(_SZ)],
     "moe_few_tokens": [_C, ctypes.POINTER(MoeFewWeights), _I, _I, _P, _L, _P, _P, _P, _P, _P, _L,
                        _P, _SZ, _P],
+    "moe_adapters_workspace_size": [_I, _I, _I, _I, ctypes.POINTER(_SZ)],
+    "moe_adapters": [_I, _I, _I, _I, _I, _I, _P, _L, _P, _P, _P, _P, _P, _P, _L, _P, _L, _P, _P,
+                     _SZ, _P],
+    "moe_adapters_backward": [_I, _I, _I, _I, _I, _I, _P, _L, _P, _L, _P, _P, _P, _P, _P, _P, _P,
+                              _L, _I, _P, _P, _P, _SZ, _P],
     "moe_clip_workspace_size": [ctypes.POINTER(_SZ)],
     "moe_clip_grad_norm": [_I, ctypes.POINTER(MoeTensor), _F, _F, _P, _P, _SZ, _P],
     "moe_selftest_wait_timeout": [_P, ctypes.c_int64, _P],
@@ -138,7 +143,8 @@ _OPERATORS = ("moe_add_rmsnorm", "moe_sort_workspace_size", "sort_workspace", "m
               "moe_sort_tokens_backward", "moe_unsort_tokens", "moe_unsort_tokens_backward",
               "moe_w4_gemv", "pack_w4", "moe_clip_workspace_size", "clip_workspace", "TensorList",
               "moe_clip_grad_norm", "FewTokenExperts", "moe_few_tokens_workspace_size",
-              "few_tokens_workspace", "moe_few_tokens")
+              "few_tokens_workspace", "moe_few_tokens", "moe_adapters_workspace_size",
+              "adapters_workspace", "moe_adapters", "moe_adapters_backward")
 
 
 def __getattr__(name):

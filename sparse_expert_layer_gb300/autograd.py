@@ -1,4 +1,4 @@
-"""Sorting tokens by expert and back inside a torch graph.
+"""Sorting tokens by expert and back, and low-rank adapters, inside a torch graph.
 
     x_sorted, plan = sort_tokens(x, topk_ids, n_experts)
     y_sorted = experts(x_sorted, plan.offsets)
@@ -8,6 +8,12 @@ Forward and backward are the kernels of moe_sort_tokens, moe_unsort_tokens and
 their gradients (include/moe.h): sums in fp32 in slot order, the same bits on
 every call.  Gradients reach x, y_sorted and topk_w; rows of dropped picks are
 zero in x_sorted and in the gradient of y_sorted.  First derivatives only.
+
+    plan = plan_adapters(adapter_ids, n_adapters)      # one for all projections of a step
+    y = adapters(x @ w.T, x, a, b, scale, plan)
+
+adds each row's adapter to a shared projection (moe_adapters, moe_adapters_backward);
+gradients reach the projection, x, a and b.
 """
 from __future__ import annotations
 
@@ -98,3 +104,60 @@ def unsort_tokens(y_sorted, topk_w, plan, dtype=None):
     (fp32), in `dtype` (None: y_sorted's)."""
     return _Unsort.apply(y_sorted, topk_w, plan.offsets, plan.expanded_to_sorted,
                          dtype or y_sorted.dtype)
+
+
+class _Adapters(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, base, x, a, b, scale, offsets, order):
+        x, a, b = _ready(x), _dense(a), _dense(b)
+        T, (_, r, K), N = x.shape[0], a.shape, b.shape[2]
+        y = torch.empty(T, N, dtype=x.dtype, device=x.device)
+        v = torch.empty(T, r, device=x.device)
+        ws = ops.adapters_workspace(T, r, K, N, x.device)
+        ops.moe_adapters(x, a, b, scale, offsets, order, None if base is None else _ready(base),
+                         y, v, ws)
+        ctx.save_for_backward(x, v, a, b, scale, offsets, order)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, v, a, b, scale, offsets, order = ctx.saved_tensors
+        want = ctx.needs_input_grad
+        dx = da = db = None
+        if any(want[1:4]):
+            T, (_, r, K), N = x.shape[0], a.shape, b.shape[2]
+            if want[1]:
+                dx = torch.empty(T, K, dtype=x.dtype, device=x.device)
+            if want[2] or want[3]:
+                da, db = torch.empty_like(a), torch.empty_like(b)
+            ops.moe_adapters_backward(_ready(dy), x, v, a, b, scale, offsets, order, dx, da, db,
+                                      ops.adapters_workspace(T, r, K, N, x.device))
+        return (dy if want[0] else None, dx, da if want[2] else None, db if want[3] else None,
+                None, None, None)
+
+
+def _dense(t):
+    """t itself where it is contiguous from a 16-byte boundary on, else a copy."""
+    return t if t.is_contiguous() and t.data_ptr() % 16 == 0 else \
+        t.clone(memory_format=torch.contiguous_format)
+
+
+def plan_adapters(adapter_ids, n_adapters):
+    """SortPlan of the rows by adapter: int32 adapter_ids [T], those outside
+    [0, n_adapters) without one."""
+    T = adapter_ids.shape[0]
+    ids = _dense(adapter_ids).view(T, 1)
+    i32 = dict(dtype=torch.int32, device=ids.device)
+    plan = SortPlan(torch.empty(n_adapters, **i32), torch.empty(n_adapters + 1, **i32),
+                    torch.empty(T, **i32), torch.empty(T, **i32))
+    ops.moe_sort_tokens(n_adapters, ids, None, None, plan.counts, plan.offsets,
+                        plan.sorted_to_expanded, plan.expanded_to_sorted, None,
+                        ws=ops.sort_workspace(T, 1, n_adapters, ids.device))
+    return plan
+
+
+def adapters(base, x, a, b, scale, plan):
+    """base [T, N] (None: zeros) + each row's adapter applied to x [T, K]: a [J, r, K],
+    b [J, r, N] (bf16 or fp16, all alike), scale fp32 [J] or None (a constant)."""
+    return _Adapters.apply(base, x, a, b, scale, plan.offsets, plan.sorted_to_expanded)

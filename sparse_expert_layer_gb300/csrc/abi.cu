@@ -867,7 +867,7 @@ const char* moe_kernel_name(int32_t kind) {
       "router", "topk", "perm_count", "perm_scan", "perm_scatter", "perm_gather", "worklist",
       "gemv_gate_up", "gemv_down", "tc_gate_up", "tc_down", "quant_h", "combine", "w8_exact",
       "sort", "norm", "sort_plan", "sort_rows", "unsort", "unsort_grad", "w4",
-      "few_route", "few_ffn", "grad_norm", "clip"};
+      "few_route", "few_ffn", "adapters", "adapters_grad", "grad_norm", "clip"};
   return (kind >= 0 && kind < MOE_K_COUNT) ? names[kind] : "unknown";
 }
 

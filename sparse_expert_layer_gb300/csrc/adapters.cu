@@ -1,0 +1,936 @@
+// Low-rank adapters of many requests at once, beside a projection that they share.
+//
+//   v[p] = x[row p] A_j^T;   y[row p] = base[row p] + s_j v[p] B_j        (forward)
+//   u[p] = s_j dy[row p] B_j^T;   dx[row p] = u[p] A_j;                   (backward)
+//   dA_j = sum_p u[p]^T x[row p];   dB_j = s_j sum_p v[p]^T dy[row p]
+//
+// for the positions p of adapter j in the sorted order of moe_sort_tokens.  A and B lie
+// as [rank][channel], so both directions are the same three products: rows times a
+// matrix over its channels (shrink), a few numbers times its rows (expand), and sums
+// over positions (outer).
+//
+// Bound by memory: the rank is small beside the channels.  Few rows: a cluster of up to
+// eight CTAs takes one position from x to y, each CTA a slice of the channels on CUDA
+// cores, and v is exchanged through distributed shared memory: one launch, and the
+// adapters are read once.  Many rows: warp-level MMAs with x and the rows of A through
+// cp.async rings; the K of a block of positions may be split over a cluster whose parts
+// are added in order.  v, u are fp32; where they meet 16-bit factors they are split into
+// two 16-bit terms (three bf16 ones for dA and dB, whose results may be fp32): 2^-17
+// (bf16) or 2^-22 (fp16) of them is lost, which a rounded output does not show.
+#include <math.h>
+
+#include <algorithm>
+
+#include "mma.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMaxRank = 128;
+constexpr int kMaxAdapters = 4096;
+constexpr int kMaxCluster = 8;
+
+struct Segments {
+  const int32_t* offsets;  // [J + 1]
+  const int32_t* order;    // position -> row, or nullptr
+  int T, J;
+  // offsets are data: stay inside the T positions whatever they hold
+  __device__ __forceinline__ int at(int j) const { return min(max(offsets[j], 0), T); }
+  // the row of position p, -1: none
+  __device__ __forceinline__ int row(int p) const {
+    const int r = order ? order[p] : p;
+    return r >= 0 && r < T ? r : -1;
+  }
+  // the first adapter whose positions end after p, by all threads of the block
+  __device__ __forceinline__ int first_after(int p) const {
+    int n = 0;
+    for (int j = threadIdx.x; j - (int)threadIdx.x < J; j += blockDim.x)
+      n += __syncthreads_count(j < J && at(j + 1) <= p);
+    return n;
+  }
+};
+
+// Piece i (channels 8 i ..) of a row of n channels, zeros past its end.
+template <typename T>
+__device__ __forceinline__ uint4 load_piece(const T* row, int i, int n, bool vec) {
+  if (vec) return 8 * i < n ? *reinterpret_cast<const uint4*>(row + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+  T v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 8 * i + j < n ? row[8 * i + j] : from_f<T>(0.f);
+  uint4 q;
+  memcpy(&q, v, 16);
+  return q;
+}
+template <typename T>
+__device__ __forceinline__ void unpack_piece(const uint4& q, float (&f)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = unpack2<T>(w[i]);
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_piece(T* row, int i, int n, bool vec, const float (&f)[8]) {
+  const Raw8<T> r = pack8<T>(f);
+  if (vec) {
+    if (8 * i < n) *reinterpret_cast<uint4*>(row + 8 * i) = r.q[0];
+    return;
+  }
+  T v[8];
+  memcpy(v, &r, 16);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (8 * i + j < n) row[8 * i + j] = v[j];
+}
+// The same into shared memory: asynchronous where rows are whole pieces.
+template <typename T>
+__device__ __forceinline__ void stage_piece(uint32_t dst, const T* row, int i, int n, bool vec,
+                                            bool real) {
+  if (vec) {
+    const bool in = real && 8 * i < n;
+    cp_async16_or_zero(dst, row + (in ? 8 * i : 0), in);
+  } else {
+    const uint4 q = real ? load_piece<T>(row, i, n, false) : make_uint4(0u, 0u, 0u, 0u);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(q.x), "r"(q.y),
+                 "r"(q.z), "r"(q.w)
+                 : "memory");
+  }
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+
+// The largest |v| that a block has seen, for the range of fp16 terms: one word a block.
+__device__ __forceinline__ uint32_t block_max(uint32_t bits) {
+  __shared__ uint32_t most[32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) most[threadIdx.x / 32] = bits;
+  __syncthreads();
+  for (int i = 0; i < (int)blockDim.x / 32; ++i) bits = max(bits, most[i]);
+  return bits;
+}
+
+struct AdapterArgs {
+  Segments seg;
+  const void* x;  // shrink: rows [T, K] times m1 [J, r, K]
+  int64_t ldx;
+  const void* m1;
+  const float* scale1;  // of v, or nullptr
+  float* v;             // [T, r], by position
+  const void* m2;       // expand: v times m2 [J, r, N]
+  const float* scale2;
+  const void* base;     // [T, N], or nullptr: zeros
+  int64_t ldb;
+  void* y;
+  int64_t ldy;
+  const float* other;   // backward: the v of the forward pass
+  uint32_t* max_v;      // backward: largest |v|, |other| of each block
+  uint32_t* max_other;
+  int r, K, N;
+  int xvec, m1vec, m2vec, yvec;
+};
+
+// ---------------------------------------------------------------- few rows ----
+constexpr int kRowThreads = 128;
+constexpr int kRowWarps = kRowThreads / 32;
+
+// One position: a cluster's CTAs take slices of K, then slices of N.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(AdapterArgs a) {
+  pdl_enter();
+  __shared__ float part[kMaxRank], total[kMaxRank];
+  __shared__ float columns[kRowWarps][32 * 8];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int rank = blockIdx.x, C = gridDim.x, p = blockIdx.y, r = a.r;
+  const int j = a.seg.first_after(p);
+  const int row = a.seg.row(p);
+  const bool has = j < a.seg.J && a.seg.at(j) <= p && row >= 0;
+  const int n8 = (a.N + 7) / 8, np = (n8 + C - 1) / C;
+  const int n0 = min(n8, rank * np), n1 = min(n8, n0 + np);
+  T* yrow = static_cast<T*>(a.y) + row * a.ldy;
+  const T* brow = a.base ? static_cast<const T*>(a.base) + row * a.ldb : nullptr;
+  if (!has) {  // the whole cluster; the row is its base
+    if (row >= 0 && a.y != a.base)
+      for (int i = n0 + tid; i < n1; i += kRowThreads) {
+        float f[8] = {};
+        if (brow) unpack_piece<T>(load_piece<T>(brow, i, a.N, a.yvec), f);
+        store_piece<T>(yrow, i, a.N, a.yvec, f);
+      }
+    if (a.max_v && tid == 0) {
+      a.max_v[p * C + rank] = 0u;
+      a.max_other[p * C + rank] = 0u;
+    }
+    return;
+  }
+  const T* m2 = static_cast<const T*>(a.m2) + (int64_t)j * r * a.N;
+  // the second matrix's slice on its way to L2 while the first is read
+  if (a.y && a.m2vec)
+    for (int i = tid; i < r * (n1 - n0); i += kRowThreads)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(m2 + (int64_t)(i / (n1 - n0)) * a.N +
+                                                    8 * (n0 + i % (n1 - n0))));
+  const T* xrow = static_cast<const T*>(a.x) + row * a.ldx;
+  const T* m1 = static_cast<const T*>(a.m1) + (int64_t)j * r * a.K;
+  const int k8 = (a.K + 7) / 8, kp = (k8 + C - 1) / C;
+  const int k0 = min(k8, rank * kp), k1 = min(k8, k0 + kp);
+  constexpr int kRanks = 4;  // of a warp at once
+  for (int i0 = warp * kRanks; i0 < r; i0 += kRowWarps * kRanks) {
+    float acc[kRanks] = {};
+    for (int k = k0 + lane; k < k1; k += 32) {
+      const uint4 xq = load_piece<T>(xrow, k, a.K, a.xvec);
+      uint4 mq[kRanks];
+#pragma unroll
+      for (int i = 0; i < kRanks; ++i)
+        mq[i] = i0 + i < r ? load_piece<T>(m1 + (int64_t)(i0 + i) * a.K, k, a.K, a.m1vec)
+                           : make_uint4(0u, 0u, 0u, 0u);
+      float xf[8], mf[8];
+      unpack_piece<T>(xq, xf);
+#pragma unroll
+      for (int i = 0; i < kRanks; ++i) {
+        unpack_piece<T>(mq[i], mf);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[i] = fmaf(xf[c], mf[c], acc[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRanks; ++i) {
+      const float s = warp_sum(acc[i]);
+      if (lane == 0 && i0 + i < r) part[i0 + i] = s;
+    }
+  }
+  cluster_sync_all();
+  const float s1 = a.scale1 ? a.scale1[j] : 1.f, s2 = a.scale2 ? a.scale2[j] : 1.f;
+  uint32_t most = 0u, most_other = 0u;
+  for (int i = tid; i < r; i += kRowThreads) {
+    float s = 0.f;
+    for (int q = 0; q < C; ++q) s += ld_cluster_f32(mapa_shared(smem_u32(&part[i]), q));
+    s *= s1;
+    total[i] = s;
+    if (rank == 0) {
+      a.v[(int64_t)p * r + i] = s;
+      most = max(most, __float_as_uint(fabsf(s)));
+      if (a.other)
+        most_other = max(most_other, __float_as_uint(fabsf(a.other[(int64_t)p * r + i])));
+    }
+  }
+  if (a.max_v) {
+    most = block_max(most);
+    most_other = block_max(most_other);
+    if (tid == 0) {
+      a.max_v[p * C + rank] = most;
+      a.max_other[p * C + rank] = most_other;
+    }
+  }
+  cluster_sync_all();  // (also: no CTA leaves while another reads its part)
+  if (!a.y) return;
+  for (int c0 = n0; c0 < n1; c0 += 32) {
+    const int i = c0 + lane;
+    float acc[8] = {};
+    if (i < n1)
+#pragma unroll 4
+      for (int q = warp; q < r; q += kRowWarps) {
+        float f[8];
+        unpack_piece<T>(load_piece<T>(m2 + (int64_t)q * a.N, i, a.N, a.m2vec), f);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] = fmaf(total[q], f[c], acc[c]);
+      }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 8; ++c) columns[warp][c * 32 + lane] = acc[c];
+    __syncthreads();
+    if (warp == 0 && i < n1) {
+      float f[8] = {};
+      if (brow) unpack_piece<T>(load_piece<T>(brow, i, a.N, a.yvec), f);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) s += columns[w][c * 32 + lane];
+        f[c] = fmaf(s2, s, f[c]);
+      }
+      store_piece<T>(yrow, i, a.N, a.yvec, f);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ shrink ----
+constexpr int kShrinkRows = 64;
+constexpr int kShrinkThreads = 128;
+constexpr int kShrinkStages = 4;
+
+// v of 64 positions: x rows and the adapter's rows in 128-byte slices of K.  Slice c of
+// row i lies at 16-byte piece c ^ (i % 8), so that neither copies nor ldmatrix meet a
+// bank twice.
+template <typename T, int RT>
+__global__ void __launch_bounds__(kShrinkThreads) adapters_shrink_kernel(AdapterArgs a) {
+  pdl_enter();
+  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int kX = kShrinkRows * 128, kStage = kX + RT * 128;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int rank = blockIdx.x, S = gridDim.x, p0 = blockIdx.y * kShrinkRows, r = a.r;
+  const uint32_t base = smem_u32(smem);
+  const int kept = a.seg.at(a.seg.J), p_end = min(p0 + kShrinkRows, kept);
+  const int slices = (a.K + 63) / 64;
+  const int c0 = (int)((int64_t)slices * rank / S), c1 = (int)((int64_t)slices * (rank + 1) / S);
+  float* red = reinterpret_cast<float*>(smem);
+  uint32_t most = 0u;
+  for (int j = a.seg.first_after(p0); j < a.seg.J && a.seg.at(j) < p_end; ++j) {
+    const int lo = max(a.seg.at(j), p0), hi = min(a.seg.at(j + 1), p_end);
+    if (lo >= hi) continue;
+    const T* xr[4];
+    bool real[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = p0 + tid / 8 + 16 * i;
+      const int row = p >= lo && p < hi ? a.seg.row(p) : -1;
+      real[i] = row >= 0;
+      xr[i] = static_cast<const T*>(a.x) + (real[i] ? row * a.ldx : 0);
+    }
+    const T* m = static_cast<const T*>(a.m1) + ((int64_t)j * r) * a.K;
+    auto load = [&](int c, int slot) {
+      const uint32_t st = base + slot * kStage;
+      const int piece = tid % 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = tid / 8 + 16 * i;
+        stage_piece<T>(st + row * 128 + ((piece ^ (row % 8)) * 16), xr[i], c * 8 + piece, a.K,
+                       a.xvec, real[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < RT / 16; ++i) {
+        const int row = tid / 8 + 16 * i;
+        const bool in = row < r;
+        stage_piece<T>(st + kX + row * 128 + ((piece ^ (row % 8)) * 16),
+                       m + (in ? (int64_t)row * a.K : 0), c * 8 + piece, a.K, a.m1vec, in);
+      }
+    };
+    float acc[RT / 8][4] = {};
+#pragma unroll
+    for (int q = 0; q < kShrinkStages - 1; ++q) {
+      if (c0 + q < c1) load(c0 + q, q);
+      cp_async_commit();
+    }
+    for (int c = c0; c < c1; ++c) {
+      cp_async_wait<kShrinkStages - 2>();
+      __syncthreads();
+      const int ahead = c + kShrinkStages - 1;
+      if (ahead < c1) load(ahead, (ahead - c0) % kShrinkStages);
+      cp_async_commit();
+      const uint32_t st = base + (c - c0) % kShrinkStages * kStage;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        uint32_t af[4];
+        const int row = warp * 16 + lane % 16;
+        ldsm4(st + row * 128 + (((kk * 2 + lane / 16) ^ (row % 8)) * 16), af);
+#pragma unroll
+        for (int n = 0; n < RT / 16; ++n) {
+          uint32_t bf[4];
+          const int i = n * 16 + lane % 8 + lane / 16 * 8;
+          ldsm4(st + kX + i * 128 + (((kk * 2 + lane / 8 % 2) ^ (i % 8)) * 16), bf);
+          mma16816<T>(acc[2 * n], af[0], af[1], af[2], af[3], bf[0], bf[1]);
+          mma16816<T>(acc[2 * n + 1], af[0], af[1], af[2], af[3], bf[2], bf[3]);
+        }
+      }
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < RT / 8; ++n) {
+      float* at = red + (warp * 16 + lane / 4) * RT + n * 8 + lane % 4 * 2;
+      *reinterpret_cast<float2*>(at) = make_float2(acc[n][0], acc[n][1]);
+      *reinterpret_cast<float2*>(at + 8 * RT) = make_float2(acc[n][2], acc[n][3]);
+    }
+    cluster_sync_all();
+    const float s1 = a.scale1 ? a.scale1[j] : 1.f;
+    for (int e = rank * kShrinkThreads + tid; e < kShrinkRows * RT; e += S * kShrinkThreads) {
+      const int p = p0 + e / RT, i = e % RT;
+      if (p < lo || p >= hi || i >= r) continue;
+      float s = 0.f;
+      for (int q = 0; q < S; ++q) s += ld_cluster_f32(mapa_shared(base + e * 4, q));
+      s *= s1;
+      a.v[(int64_t)p * r + i] = s;
+      most = max(most, __float_as_uint(fabsf(s)));
+    }
+    cluster_sync_all();
+  }
+  if (a.max_v) {
+    uint32_t other = 0u;
+    const int64_t first = (int64_t)p0 * r, last = (int64_t)max(p_end, p0) * r;
+    for (int64_t i = first + rank * kShrinkThreads + tid; i < last; i += S * kShrinkThreads)
+      other = max(other, __float_as_uint(fabsf(a.other[i])));
+    most = block_max(most);
+    other = block_max(other);
+    if (tid == 0) {
+      a.max_v[blockIdx.y * S + rank] = most;
+      a.max_other[blockIdx.y * S + rank] = other;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ expand ----
+constexpr int kExpandRows = 128;
+constexpr int kExpandThreads = 256;
+constexpr int kExpandTile = 256;  // columns of the second matrix in shared memory
+
+// y of 128 positions and a range of columns.  The columns of 32 are dealt to the four
+// n-tiles of MMAs so that a lane's results are eight neighbours: pair t of 16-byte piece
+// q belongs to n-tile t, columns 2 (q % 4) and the next.
+template <typename T, int RT>
+__global__ void __launch_bounds__(kExpandThreads) adapters_expand_kernel(AdapterArgs a, int range) {
+  pdl_enter();
+  extern __shared__ __align__(128) unsigned char smem[];
+  const uint32_t mt = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g = lane / 4, tg = lane % 4;
+  const int p0 = blockIdx.y * kExpandRows, r = a.r;
+  const int n_begin = blockIdx.x * range, n_end = min(a.N, n_begin + range);
+  const int kept = a.seg.at(a.seg.J), p_end = min(p0 + kExpandRows, kept);
+  const int pa = p0 + warp * 16 + g, pb = pa + 8;
+  const int ra = pa < a.seg.T ? a.seg.row(pa) : -1, rb = pb < a.seg.T ? a.seg.row(pb) : -1;
+  T* ya = static_cast<T*>(a.y) + ra * a.ldy;
+  T* yb = static_cast<T*>(a.y) + rb * a.ldy;
+  const T* ba = static_cast<const T*>(a.base) + ra * a.ldb;
+  const T* bb = static_cast<const T*>(a.base) + rb * a.ldb;
+  for (int j = a.seg.first_after(p0); j < a.seg.J && a.seg.at(j) < p_end; ++j) {
+    const int lo = max(a.seg.at(j), p0), hi = min(a.seg.at(j + 1), p_end);
+    if (lo >= hi) continue;
+    const bool ina = pa >= lo && pa < hi && ra >= 0, inb = pb >= lo && pb < hi && rb >= 0;
+    const bool mine = __any_sync(0xffffffffu, ina || inb);
+    // the rows' v as two 16-bit terms
+    uint32_t hi_t[RT / 16][4], lo_t[RT / 16][4];
+    float sa = a.scale2 ? a.scale2[j] : 1.f, sb = sa;
+    {
+      float f[RT / 16][8];
+      float ma = 0.f, mb = 0.f;
+#pragma unroll
+      for (int k = 0; k < RT / 16; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int i = k * 16 + tg * 2 + (q & 1) + (q >> 1) * 8;
+          const bool in = i < r;
+          f[k][q] = ina && in ? a.v[(int64_t)pa * r + i] : 0.f;
+          f[k][4 + q] = inb && in ? a.v[(int64_t)pb * r + i] : 0.f;
+          ma = fmaxf(ma, fabsf(f[k][q]));
+          mb = fmaxf(mb, fabsf(f[k][4 + q]));
+        }
+      float upa = 1.f, upb = 1.f;
+      if constexpr (std::is_same<T, __half>::value) {  // into fp16's range, row by row
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+          mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+        }
+        const uint32_t ua = fp16_range_bits(__float_as_uint(ma));
+        const uint32_t ub = fp16_range_bits(__float_as_uint(mb));
+        upa = __uint_as_float(ua);
+        upb = __uint_as_float(ub);
+        sa *= inverse_pow2(ua);
+        sb *= inverse_pow2(ub);
+      }
+#pragma unroll
+      for (int k = 0; k < RT / 16; ++k)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          split2<T>(f[k][2 * q] * upa, f[k][2 * q + 1] * upa, hi_t[k][2 * q], lo_t[k][2 * q]);
+          split2<T>(f[k][4 + 2 * q] * upb, f[k][5 + 2 * q] * upb, hi_t[k][2 * q + 1],
+                    lo_t[k][2 * q + 1]);
+        }
+    }
+    const T* m = static_cast<const T*>(a.m2) + (int64_t)j * r * a.N;
+    for (int n0 = n_begin; n0 < n_end; n0 += kExpandTile) {
+      __syncthreads();
+      for (int e = tid; e < RT * (kExpandTile / 8); e += kExpandThreads) {
+        const int i = e / (kExpandTile / 8), q = e % (kExpandTile / 8);
+        const uint4 v = i < r ? load_piece<T>(m + (int64_t)i * a.N, n0 / 8 + q, a.N, a.m2vec)
+                              : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(mt + i * (kExpandTile * 2) +
+                                                       (((q / 4 * 4 + t) ^ (i % 8)) * 16) +
+                                                       (q % 4) * 4),
+                       "r"(w[t])
+                       : "memory");
+      }
+      __syncthreads();
+      if (!mine) continue;
+#pragma unroll 2
+      for (int c = 0; c < kExpandTile / 32; ++c) {
+        if (n0 + c * 32 >= n_end) break;
+        const int piece = n0 / 8 + c * 4 + tg;
+        uint4 qa = make_uint4(0u, 0u, 0u, 0u), qb = qa;
+        if (a.base) {
+          if (ina) qa = load_piece<T>(ba, piece, a.N, a.yvec);
+          if (inb) qb = load_piece<T>(bb, piece, a.N, a.yvec);
+        }
+        float d[4][4] = {};
+#pragma unroll
+        for (int k = 0; k < RT / 16; ++k) {
+          const int i = k * 16 + lane % 16;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t bf[4];
+            ldsm4_trans(mt + i * (kExpandTile * 2) + (((c * 4 + h * 2 + lane / 16) ^ (i % 8)) * 16),
+                        bf);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              mma16816<T>(d[2 * h + t], hi_t[k][0], hi_t[k][1], hi_t[k][2], hi_t[k][3], bf[2 * t],
+                          bf[2 * t + 1]);
+              mma16816<T>(d[2 * h + t], lo_t[k][0], lo_t[k][1], lo_t[k][2], lo_t[k][3], bf[2 * t],
+                          bf[2 * t + 1]);
+            }
+          }
+        }
+        float fa[8], fb[8];
+        unpack_piece<T>(qa, fa);
+        unpack_piece<T>(qb, fb);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            fa[2 * t + h] = fmaf(sa, d[t][h], fa[2 * t + h]);
+            fb[2 * t + h] = fmaf(sb, d[t][2 + h], fb[2 * t + h]);
+          }
+        if (ina) store_piece<T>(ya, piece, a.N, a.yvec, fa);
+        if (inb) store_piece<T>(yb, piece, a.N, a.yvec, fb);
+      }
+    }
+  }
+  // rows without an adapter are their base
+  if (a.y == a.base) return;
+  for (int p = max(kept, p0) + warp; p < min(p0 + kExpandRows, a.seg.T); p += kExpandThreads / 32) {
+    const int row = a.seg.row(p);
+    if (row < 0) continue;
+    for (int i = n_begin / 8 + lane; 8 * i < n_end; i += 32) {
+      float f[8] = {};
+      if (a.base)
+        unpack_piece<T>(load_piece<T>(static_cast<const T*>(a.base) + row * a.ldb, i, a.N, a.yvec),
+                        f);
+      store_piece<T>(static_cast<T*>(a.y) + row * a.ldy, i, a.N, a.yvec, f);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- outer ----
+struct OuterSide {
+  const float* v;        // [T, r] by position
+  const uint32_t* max;   // its largest magnitudes, one a block
+  const void* x;         // [T, n] rows
+  int64_t ldx;
+  const float* scale;    // of the result, or nullptr
+  void* out;             // [J, r, n]
+  int n, vec, tiles;
+};
+struct OuterArgs {
+  Segments seg;
+  OuterSide side[2];
+  int r, blocks, out_dtype;
+};
+
+constexpr int kOuterThreads = 256;
+constexpr int kOuterRows = 32;  // positions of a stage
+constexpr int kOuterStages = 3;
+template <int RT>
+constexpr int kOuterCols = RT <= 64 ? 256 : 128;
+// 16-bit terms of v: bf16 three (24 bits), fp16 two (22 bits)
+template <typename T>
+constexpr int kTerms = std::is_same<T, __half>::value ? 2 : 3;
+
+// Sums over the positions of an adapter, a tile of columns for all ranks.  The MMAs' rows
+// are the ranks, their K the positions: v and x are both read transposed.
+template <typename T, int RT>
+__global__ void __launch_bounds__(kOuterThreads) adapters_outer_kernel(OuterArgs a) {
+  pdl_enter();
+  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int kCols = kOuterCols<RT>, kPieces = kCols / 8;
+  constexpr int kX = kOuterRows * kCols * 2;
+  constexpr int kVRow = RT * 2, kPlane = kOuterRows * kVRow, kTerm = kTerms<T>;
+  constexpr int kWarpCols = kCols / 8;  // of each of the eight warps
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int rank = blockIdx.x, S = gridDim.x, j = blockIdx.z, r = a.r;
+  const bool second = (int)blockIdx.y >= a.side[0].tiles;
+  const OuterSide& s = a.side[second];
+  const int n0 = (blockIdx.y - (second ? a.side[0].tiles : 0)) * kCols;
+  const uint32_t base = smem_u32(smem), planes = base + kOuterStages * kX;
+  const int lo = a.seg.at(j), hi = max(lo, a.seg.at(j + 1));
+  // this rank's positions: whole stages
+  const int stages = (hi - lo + kOuterRows - 1) / kOuterRows;
+  const int q0 = (int)((int64_t)stages * rank / S), q1 = (int)((int64_t)stages * (rank + 1) / S);
+  float up = 1.f, down = s.scale ? s.scale[j] : 1.f;
+  if constexpr (kTerm == 2) {
+    uint32_t most = 0u;
+    for (int i = tid; i < a.blocks; i += kOuterThreads) most = max(most, s.max[i]);
+    const uint32_t bits = fp16_range_bits(block_max(most));
+    up = __uint_as_float(bits);
+    down *= inverse_pow2(bits);
+  }
+  auto load_x = [&](int q, int slot) {
+    for (int e = tid; e < kOuterRows * kPieces; e += kOuterThreads) {
+      const int i = e / kPieces, c = e % kPieces, p = lo + q * kOuterRows + i;
+      const int row = p < hi ? a.seg.row(p) : -1;
+      stage_piece<T>(base + slot * kX + i * (kCols * 2) + ((c ^ (i % 8)) * 16),
+                     static_cast<const T*>(s.x) + (row >= 0 ? row * s.ldx : 0), n0 / 8 + c, s.n,
+                     s.vec, row >= 0);
+    }
+  };
+  // pairs of ranks of v, two a thread of the first RT * 16 pairs
+  constexpr int kPairs = kOuterRows * RT / 2, kMine = (kPairs + kOuterThreads - 1) / kOuterThreads;
+  float2 v[kMine];
+  auto load_v = [&](int q) {
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+      const int e = tid + m * kOuterThreads, i = e / (RT / 2), k = e % (RT / 2) * 2;
+      const int p = lo + q * kOuterRows + i;
+      const bool in = e < kPairs && p < hi && a.seg.row(p) >= 0;
+      v[m].x = in && k < r ? s.v[(int64_t)p * r + k] * up : 0.f;
+      v[m].y = in && k + 1 < r ? s.v[(int64_t)p * r + k + 1] * up : 0.f;
+    }
+  };
+  auto store_v = [&](int buf) {
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+      const int e = tid + m * kOuterThreads, i = e / (RT / 2), k = e % (RT / 2) * 2;
+      if (e >= kPairs) break;
+      // 16-byte pieces swizzled by position, as far as a row has them
+      const uint32_t at = planes + buf * kTerm * kPlane + i * kVRow +
+                          (((k / 8) ^ (i % (RT / 8 < 8 ? RT / 8 : 8))) * 16) + k % 8 * 2;
+      float x = v[m].x, y = v[m].y;
+#pragma unroll
+      for (int t = 0; t < kTerm; ++t) {
+        const uint32_t w = pack2<T>(x, y);
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + t * kPlane), "r"(w) : "memory");
+        const float2 f = unpack2<T>(w);
+        x -= f.x;
+        y -= f.y;
+      }
+    }
+  };
+  float acc[RT / 16][kWarpCols / 8][4] = {};
+  if (q0 < q1) load_v(q0);
+#pragma unroll
+  for (int i = 0; i < kOuterStages - 1; ++i) {
+    if (q0 + i < q1) load_x(q0 + i, i);
+    cp_async_commit();
+  }
+  for (int q = q0; q < q1; ++q) {
+    const int buf = (q - q0) & 1;
+    store_v(buf);
+    cp_async_wait<kOuterStages - 2>();
+    __syncthreads();
+    const int ahead = q + kOuterStages - 1;
+    if (ahead < q1) load_x(ahead, (ahead - q0) % kOuterStages);
+    cp_async_commit();
+    if (q + 1 < q1) load_v(q + 1);
+    const uint32_t xs = base + (q - q0) % kOuterStages * kX;
+    const uint32_t vs = planes + buf * kTerm * kPlane;
+#pragma unroll
+    for (int kk = 0; kk < kOuterRows / 16; ++kk) {
+      uint32_t bf[kWarpCols / 16][4];
+#pragma unroll
+      for (int c = 0; c < kWarpCols / 16; ++c) {
+        const int i = kk * 16 + lane % 16, piece = warp * (kWarpCols / 8) + c * 2 + lane / 16;
+        ldsm4_trans(xs + i * (kCols * 2) + ((piece ^ (i % 8)) * 16), bf[c]);
+      }
+#pragma unroll
+      for (int m = 0; m < RT / 16; ++m)
+#pragma unroll
+        for (int t = 0; t < kTerm; ++t) {
+          uint32_t af[4];
+          // (ranks 0-7, positions 0-7) (8-15, 0-7) (0-7, 8-15) (8-15, 8-15)
+          const int i = kk * 16 + lane % 8 + lane / 16 * 8, piece = m * 2 + lane / 8 % 2;
+          ldsm4_trans(vs + t * kPlane + i * kVRow +
+                          ((piece ^ (i % (RT / 8 < 8 ? RT / 8 : 8))) * 16),
+                      af);
+#pragma unroll
+          for (int c = 0; c < kWarpCols / 16; ++c) {
+            mma16816<T>(acc[m][2 * c], af[0], af[1], af[2], af[3], bf[c][0], bf[c][1]);
+            mma16816<T>(acc[m][2 * c + 1], af[0], af[1], af[2], af[3], bf[c][2], bf[c][3]);
+          }
+        }
+    }
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+  // parts [rank][column], added in the order of the cluster's ranks
+  float* red = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int m = 0; m < RT / 16; ++m)
+#pragma unroll
+    for (int c = 0; c < kWarpCols / 8; ++c) {
+      float* at = red + (m * 16 + lane / 4) * kCols + warp * kWarpCols + c * 8 + lane % 4 * 2;
+      *reinterpret_cast<float2*>(at) = make_float2(acc[m][c][0], acc[m][c][1]);
+      *reinterpret_cast<float2*>(at + 8 * kCols) = make_float2(acc[m][c][2], acc[m][c][3]);
+    }
+  cluster_sync_all();
+  for (int e = rank * kOuterThreads + tid; e < r * kCols; e += S * kOuterThreads) {
+    const int i = e / kCols, n = n0 + e % kCols;
+    if (n >= s.n) continue;
+    float f = 0.f;
+    for (int q = 0; q < S; ++q) f += ld_cluster_f32(mapa_shared(base + e * 4, q));
+    f *= down;
+    const int64_t at = ((int64_t)j * r + i) * s.n + n;
+    if (a.out_dtype == MOE_DT_FP32)
+      static_cast<float*>(s.out)[at] = f;
+    else
+      static_cast<T*>(s.out)[at] = from_f<T>(f);
+  }
+  cluster_sync_all();
+}
+
+// ------------------------------------------------------------------ launch --
+template <typename T, int RT>
+constexpr int outer_smem() {
+  const int rings = kOuterStages * kOuterRows * kOuterCols<RT> * 2 +
+                    2 * kTerms<T> * kOuterRows * RT * 2;
+  return std::max(rings, RT * kOuterCols<RT> * 4);
+}
+template <int RT>
+constexpr int shrink_smem() {
+  return std::max(kShrinkStages * (kShrinkRows + RT) * 128, kShrinkRows * RT * 4);
+}
+
+// The most CTAs of a power of two, up to eight, that share `units` of work while there
+// are at most `most` CTAs in all and each has at least `least` units.
+int adapters_split(int64_t clusters, int64_t units, int64_t most, int64_t least) {
+  int s = 1;
+  while (s < kMaxCluster && clusters * 2 * s <= most && units >= 2 * s * least) s *= 2;
+  return s;
+}
+
+// One position a cluster for as many positions as this, or where adapters have few.
+constexpr int kRowPositions = 64;
+bool adapters_by_rows(int T, int J) { return T <= kRowPositions || T <= 2 * J; }
+
+int row_cluster(const AdapterArgs& a) {
+  // slices of at least 256 channels
+  return adapters_split(1, std::max(a.K, a.N), kMaxCluster, 256);
+}
+int shrink_cluster(const AdapterArgs& a, int num_sms) {
+  const int blocks = (a.seg.T + kShrinkRows - 1) / kShrinkRows;
+  return adapters_split(blocks, (a.K + 63) / 64, 3LL * num_sms, 4);
+}
+
+template <typename T, int RT>
+void launch_tiles(const Launch& L, const AdapterArgs& a, int rt_slot) {
+  const int type = std::is_same<T, __half>::value ? 1 : 0;
+  const int S = shrink_cluster(a, L.num_sms);
+  set_smem_attr_once(reinterpret_cast<const void*>(adapters_shrink_kernel<T, RT>),
+                     shrink_smem<RT>(), kAttrAdapters + 8 * type + rt_slot);
+  launch_begin(L, MOE_K_ADAPTERS);
+  launch_kernel_cluster(adapters_shrink_kernel<T, RT>,
+                        dim3(S, (a.seg.T + kShrinkRows - 1) / kShrinkRows), dim3(S),
+                        dim3(kShrinkThreads), shrink_smem<RT>(), L.stream, a);
+  launch_end(L, MOE_K_ADAPTERS);
+  if (!a.y) return;
+  // ranges of whole tiles: about two CTAs an SM
+  const int blocks = (a.seg.T + kExpandRows - 1) / kExpandRows;
+  const int tiles = (a.N + kExpandTile - 1) / kExpandTile;
+  const int per = std::max(1, (int)((int64_t)tiles * blocks / (3LL * L.num_sms)));
+  set_smem_attr_once(reinterpret_cast<const void*>(adapters_expand_kernel<T, RT>),
+                     RT * kExpandTile * 2, kAttrAdapters + 8 * type + 4 + rt_slot);
+  launch_begin(L, MOE_K_ADAPTERS);
+  launch_kernel(adapters_expand_kernel<T, RT>, dim3((tiles + per - 1) / per, blocks),
+                dim3(kExpandThreads), RT * kExpandTile * 2, L.stream, a, per * kExpandTile);
+  launch_end(L, MOE_K_ADAPTERS);
+}
+template <typename T, int RT>
+void launch_outer(const Launch& L, OuterArgs a, int rt_slot) {
+  const int type = std::is_same<T, __half>::value ? 1 : 0;
+  int tiles = 0;
+  for (OuterSide& s : a.side) {
+    s.tiles = (s.n + kOuterCols<RT> - 1) / kOuterCols<RT>;
+    tiles += s.tiles;
+  }
+  const int S = adapters_split((int64_t)tiles * a.seg.J,
+                               std::max(1, a.seg.T / a.seg.J / kOuterRows), 4LL * L.num_sms, 4);
+  set_smem_attr_once(reinterpret_cast<const void*>(adapters_outer_kernel<T, RT>),
+                     outer_smem<T, RT>(), kAttrAdapters + 16 + 4 * type + rt_slot);
+  launch_begin(L, MOE_K_ADAPTERS_GRAD);
+  launch_kernel_cluster(adapters_outer_kernel<T, RT>, dim3(S, tiles, a.seg.J), dim3(S),
+                        dim3(kOuterThreads), outer_smem<T, RT>(), L.stream, a);
+  launch_end(L, MOE_K_ADAPTERS_GRAD);
+}
+
+// Shrink and expand, then (outer not nullptr) the sums over positions.
+template <typename T>
+void launch_adapters(const Launch& L, const AdapterArgs& a, OuterArgs* outer) {
+  const int slot = a.r <= 16 ? 0 : a.r <= 32 ? 1 : a.r <= 64 ? 2 : 3;
+  if (a.seg.T == 0) {
+  } else if (adapters_by_rows(a.seg.T, a.seg.J)) {
+    const int C = row_cluster(a);
+    launch_begin(L, MOE_K_ADAPTERS);
+    launch_kernel_cluster(adapters_row_kernel<T>, dim3(C, a.seg.T), dim3(C), dim3(kRowThreads), 0,
+                          L.stream, a);
+    launch_end(L, MOE_K_ADAPTERS);
+    if (outer) outer->blocks = C * a.seg.T;
+  } else {
+    switch (slot) {
+      case 0: launch_tiles<T, 16>(L, a, 0); break;
+      case 1: launch_tiles<T, 32>(L, a, 1); break;
+      case 2: launch_tiles<T, 64>(L, a, 2); break;
+      default: launch_tiles<T, 128>(L, a, 3); break;
+    }
+    if (outer)
+      outer->blocks =
+          shrink_cluster(a, L.num_sms) * ((a.seg.T + kShrinkRows - 1) / kShrinkRows);
+  }
+  if (!outer) return;
+  switch (slot) {
+    case 0: launch_outer<T, 16>(L, *outer, 0); break;
+    case 1: launch_outer<T, 32>(L, *outer, 1); break;
+    case 2: launch_outer<T, 64>(L, *outer, 2); break;
+    default: launch_outer<T, 128>(L, *outer, 3); break;
+  }
+}
+
+struct AdapterLayout {
+  size_t v, max_v, max_other, total;
+};
+AdapterLayout adapters_layout(int64_t T, int64_t r) {
+  auto up = [](int64_t n) { return ((size_t)n + 255) & ~(size_t)255; };
+  AdapterLayout l;
+  l.v = 0;
+  l.max_v = up(T * r * 4);
+  l.max_other = l.max_v + up(T * kMaxCluster * 4);
+  l.total = l.max_other + up(T * kMaxCluster * 4);
+  return l;
+}
+
+moe_status check_adapters(int32_t T, int32_t J, int32_t r, int32_t K, int32_t N, int32_t dtype) {
+  if (T < 0 || J < 1 || r < 1 || K < 1 || N < 1) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_DT_BF16 && dtype != MOE_DT_FP16) return MOE_ERR_INVALID_ARG;
+  if (r > kMaxRank || J > kMaxAdapters || T > (1 << 21) || K > (1 << 21) || N > (1 << 21))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_adapters_workspace_size(int32_t T, int32_t r, int32_t K,
+                                                  int32_t N, size_t* bytes) {
+  const moe_status s = check_adapters(T, 1, r, K, N, MOE_DT_BF16);
+  if (s != MOE_OK) return s;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = adapters_layout(T, r).total;
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_adapters(int32_t T, int32_t n_adapters, int32_t r, int32_t K, int32_t N,
+                                   int32_t dtype, const void* x, int64_t ldx, const void* a,
+                                   const void* b, const float* scale, const int32_t* offsets,
+                                   const int32_t* order, const void* base, int64_t ldb, void* y,
+                                   int64_t ldy, float* v, void* ws, size_t ws_bytes,
+                                   moe_stream_t stream) {
+  const moe_status cs = check_adapters(T, n_adapters, r, K, N, dtype);
+  if (cs != MOE_OK) return cs;
+  if (ldx < K || (base && ldb < N) || ldy < N) return MOE_ERR_INVALID_ARG;
+  if (base && base == y && ldb != ldy) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !a || !b || !offsets || !y || !ws) return MOE_ERR_INVALID_ARG;
+  if (misaligned16(x, a, b, scale, offsets, order, base, y, v) ||
+      (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return MOE_ERR_ALIGNMENT;
+  const AdapterLayout l = adapters_layout(T, r);
+  if (ws_bytes < l.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  Launch L;
+  const moe_status s = open_launch(stream, &L);
+  if (s != MOE_OK) return s;
+  AdapterArgs g{};
+  g.seg = {offsets, order, T, n_adapters};
+  g.x = x;
+  g.ldx = ldx;
+  g.m1 = a;
+  g.v = v ? v : reinterpret_cast<float*>(static_cast<char*>(ws) + l.v);
+  g.m2 = b;
+  g.scale2 = scale;
+  g.base = base;
+  g.ldb = ldb;
+  g.y = y;
+  g.ldy = ldy;
+  g.r = r;
+  g.K = K;
+  g.N = N;
+  g.xvec = K % 8 == 0 && ldx % 8 == 0;
+  g.m1vec = K % 8 == 0;
+  g.m2vec = N % 8 == 0;
+  g.yvec = N % 8 == 0 && ldy % 8 == 0 && (!base || ldb % 8 == 0);
+  if (dtype == MOE_DT_BF16)
+    launch_adapters<__nv_bfloat16>(L, g, nullptr);
+  else
+    launch_adapters<__half>(L, g, nullptr);
+  return launch_status_take();
+}
+
+extern "C" moe_status moe_adapters_backward(
+    int32_t T, int32_t n_adapters, int32_t r, int32_t K, int32_t N, int32_t dtype, const void* dy,
+    int64_t lddy, const void* x, int64_t ldx, const float* v, const void* a, const void* b,
+    const float* scale, const int32_t* offsets, const int32_t* order, void* dx, int64_t lddx,
+    int32_t grad_dtype, void* da, void* db, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  const moe_status cs = check_adapters(T, n_adapters, r, K, N, dtype);
+  if (cs != MOE_OK) return cs;
+  if (lddy < N || ldx < K || (dx && lddx < K)) return MOE_ERR_INVALID_ARG;
+  if ((da != nullptr) != (db != nullptr) || (!dx && !da)) return MOE_ERR_INVALID_ARG;
+  if (da && grad_dtype != MOE_DT_FP32 && grad_dtype != dtype) return MOE_ERR_INVALID_ARG;
+  if (!offsets || !a || !b) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!dy || !ws || (da && (!x || !v)))) return MOE_ERR_INVALID_ARG;
+  if (misaligned16(dy, x, v, a, b, scale, offsets, order, dx, da, db) ||
+      (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return MOE_ERR_ALIGNMENT;
+  const AdapterLayout l = adapters_layout(T, r);
+  if (ws_bytes < l.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (T == 0 && !da) return MOE_OK;
+  Launch L;
+  const moe_status s = open_launch(stream, &L);
+  if (s != MOE_OK) return s;
+  char* at = static_cast<char*>(ws);
+  AdapterArgs g{};
+  g.seg = {offsets, order, T, n_adapters};
+  g.x = dy;
+  g.ldx = lddy;
+  g.m1 = b;
+  g.scale1 = scale;
+  g.v = reinterpret_cast<float*>(at + l.v);
+  g.m2 = a;
+  g.y = dx;
+  g.ldy = lddx;
+  g.r = r;
+  g.K = N;
+  g.N = K;
+  g.xvec = N % 8 == 0 && lddy % 8 == 0;
+  g.m1vec = N % 8 == 0;
+  g.m2vec = K % 8 == 0;
+  g.yvec = K % 8 == 0 && lddx % 8 == 0;
+  OuterArgs o{};
+  if (da) {
+    g.other = v;
+    g.max_v = reinterpret_cast<uint32_t*>(at + l.max_v);
+    g.max_other = reinterpret_cast<uint32_t*>(at + l.max_other);
+    o.seg = g.seg;
+    o.side[0] = {g.v, g.max_v, x, ldx, nullptr, da, K, K % 8 == 0 && ldx % 8 == 0, 0};
+    o.side[1] = {v, g.max_other, dy, lddy, scale, db, N, g.xvec, 0};
+    o.r = r;
+    o.out_dtype = grad_dtype;
+  }
+  if (dtype == MOE_DT_BF16)
+    launch_adapters<__nv_bfloat16>(L, g, da ? &o : nullptr);
+  else
+    launch_adapters<__half>(L, g, da ? &o : nullptr);
+  return launch_status_take();
+}

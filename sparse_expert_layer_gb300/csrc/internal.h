@@ -429,7 +429,8 @@ enum {
   kAttrW4Slots = 3 * 3 * 2,
   kAttrFewRoute = kAttrW4Base + kAttrW4Slots,  // 4 slots: tokens 1, 2, 4, 8
   kAttrFewFfn = kAttrFewRoute + 4,             // 16 slots: weights x gate/up tile
-  kAttrSlots = kAttrFewFfn + 16
+  kAttrAdapters = kAttrFewFfn + 16,            // 24 slots: three kernels x types x ranks
+  kAttrSlots = kAttrAdapters + 24
 };
 void set_smem_attr_once(const void* func, int bytes, int slot);
 

@@ -26,6 +26,7 @@ _F32 = frozenset((torch.float32,))
 _I32 = frozenset((torch.int32,))
 _U8 = frozenset((torch.uint8,))
 _U4 = 5  # MOE_DT_U4
+_HALVES = frozenset((torch.bfloat16, torch.float16))
 
 _W4_X = frozenset((torch.bfloat16, torch.float16, torch.int8))
 
@@ -37,6 +38,8 @@ _unsort_tokens_backward = lib.moe_unsort_tokens_backward
 _w4_gemv = lib.moe_w4_gemv
 _clip_grad_norm = lib.moe_clip_grad_norm
 _few_tokens = lib.moe_few_tokens
+_adapters = lib.moe_adapters
+_adapters_backward = lib.moe_adapters_backward
 # torch.autograd.graph.increment_version for several tensors, without its type checks
 _changed = torch._C._increment_version
 
@@ -431,10 +434,8 @@ def moe_clip_grad_norm(tensors, max_norm, norm, ws, eps=1e-6, stream=None):
         if norm.requires_grad:
             _refuse_grad("norm")
         written = written + [norm]
-    _a_tensor(ws, "ws")
-    nws = ws.numel()
-    st = _clip_grad_norm(n, tensors.entries, max_norm, eps, pn, _tensor(ws, "ws", _U8, (nws,), dev),
-                         nws, _stream(stream, dev))
+    pws, nws = _bytes(ws, dev)
+    st = _clip_grad_norm(n, tensors.entries, max_norm, eps, pn, pws, nws, _stream(stream, dev))
     if st:
         _check(st, "moe_clip_grad_norm")
     _changed(written)
@@ -533,9 +534,6 @@ def few_tokens_workspace(experts, T):
                        device=dev)
 
 
-_HALVES = frozenset((torch.bfloat16, torch.float16))
-
-
 def moe_few_tokens(experts, x, out, ws, topk_ids=None, topk_w=None, stream=None):
     """out [T, H] = the layer of a FewTokenExperts for x [T, H], T <= 8 (bf16 or fp16,
     the weights' type where those have 16 bits; both may have row strides).  ws:
@@ -559,11 +557,113 @@ def moe_few_tokens(experts, x, out, ws, topk_ids=None, topk_w=None, stream=None)
         if topk_w.requires_grad:
             _refuse_grad("topk_w")
         written.append(topk_w)
-    _a_tensor(ws, "ws")
-    nws = ws.numel()
+    pws, nws = _bytes(ws, dev)
     st = _few_tokens(cfg, experts.c, T, DTYPES[x.dtype], px, ldx, experts.w_router, experts.bias,
-                     pi, pw, po, ldo, _tensor(ws, "ws", _U8, (nws,), dev), nws,
-                     _stream(stream, dev))
+                     pi, pw, po, ldo, pws, nws, _stream(stream, dev))
     if st:
         _check(st, "moe_few_tokens")
+    _changed(written)
+
+
+def moe_adapters_workspace_size(T, r, K, N) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib.moe_adapters_workspace_size(T, r, K, N, ctypes.byref(n)),
+           "moe_adapters_workspace_size")
+    return n.value
+
+
+def adapters_workspace(T, r, K, N, device="cuda"):
+    """A uint8 tensor of moe_adapters_workspace_size bytes, for T rows or fewer."""
+    return torch.empty(moe_adapters_workspace_size(T, r, K, N), dtype=torch.uint8, device=device)
+
+
+def _adapter_parts(a, b, scale, offsets, order, T, same, dev):
+    """(adapters, rank, K, N) and the addresses of a, b, scale, offsets and order."""
+    for t, name in ((a, "a"), (b, "b")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise TypeError(f"{name}: expected [adapters, rank, channels]")
+    J, r, K = a.shape
+    N = b.shape[2]
+    return (J, r, K, N), (
+        _tensor(a, "a", same, (J, r, K), dev), _tensor(b, "b", same, (J, r, N), dev),
+        None if scale is None else _tensor(scale, "scale", _F32, (J,), dev),
+        _tensor(offsets, "offsets", _I32, (J + 1,), dev),
+        None if order is None else _tensor(order, "order", _I32, (T,), dev))
+
+
+def _bytes(ws, dev):
+    """(address, size) of a workspace."""
+    _a_tensor(ws, "ws")
+    n = ws.numel()
+    return _tensor(ws, "ws", _U8, (n,), dev), n
+
+
+def moe_adapters(x, a, b, scale, offsets, order, base, y, v, ws, stream=None):
+    """y[t] = base[t] + scale[j] * (x[t] @ a[j].T) @ b[j] for the rows t = order[p] at the
+    positions offsets[j] <= p < offsets[j + 1]; other rows are their base.
+
+    x [T, K], base and y [T, N] (row strides allowed), a [J, r, K] and b [J, r, N] share
+    one type (bf16, fp16); scale fp32 [J] or None (1); offsets int32 [J + 1] and order
+    int32 [T] as moe_sort_tokens' offsets and sorted_to_expanded of ids [T, 1], order None
+    where rows are sorted; base None (zeros) or y itself; v fp32 [T, r] or None: x a^T by
+    position, for moe_adapters_backward; ws: adapters_workspace.
+    """
+    (T, _), dev, px, ldx = _matrix(x, "x", _HALVES)
+    same = (x.dtype,)
+    (J, r, K, N), (pa, pb, psc, po, pord) = _adapter_parts(a, b, scale, offsets, order, T, same,
+                                                           dev)
+    if x.shape[1] != K:
+        raise ValueError(f"x: {x.shape[1]} channels, a has {K}")
+    py, ldy = _rows(y, "y", same, (T, N), dev)
+    if y.requires_grad:
+        _refuse_grad("y")
+    written, pbase, ldb, pv = [y], None, 0, None
+    if base is not None:
+        pbase, ldb = _rows(base, "base", same, (T, N), dev)
+    if v is not None:
+        pv = _tensor(v, "v", _F32, (T, r), dev)
+        if v.requires_grad:
+            _refuse_grad("v")
+        written.append(v)
+    pw, nws = _bytes(ws, dev)
+    st = _adapters(T, J, r, K, N, DTYPES[x.dtype], px, ldx, pa, pb, psc, po, pord, pbase, ldb, py,
+                   ldy, pv, pw, nws, _stream(stream, dev))
+    if st:
+        _check(st, "moe_adapters")
+    _changed(written)
+
+
+def moe_adapters_backward(dy, x, v, a, b, scale, offsets, order, dx, da, db, ws, stream=None):
+    """Gradients of moe_adapters: dx [T, K] of x's type (None: not wanted), da and db as a
+    and b in fp32 or their type (None together: not wanted, x and v may then be None)."""
+    (T, N0), dev, pdy, lddy = _matrix(dy, "dy", _HALVES)
+    same = (dy.dtype,)
+    (J, r, K, N), (pa, pb, psc, po, pord) = _adapter_parts(a, b, scale, offsets, order, T, same,
+                                                           dev)
+    if N0 != N:
+        raise ValueError(f"dy: {N0} channels, b has {N}")
+    if (da is None) != (db is None) or (dx is None and da is None):
+        raise ValueError("da, db: wanted together; dx or both of them")
+    px = pv = pdx = pda = pdb = None
+    ldx = lddx = K
+    gdt = DTYPES[torch.float32]
+    written = []
+    if dx is not None:
+        pdx, lddx = _rows(dx, "dx", same, (T, K), dev)
+        written.append(dx)
+    if da is not None:
+        px, ldx = _rows(x, "x", same, (T, K), dev)
+        pv = _tensor(v, "v", _F32, (T, r), dev)
+        pda = _tensor(da, "da", (torch.float32, dy.dtype), (J, r, K), dev)
+        pdb = _tensor(db, "db", (da.dtype,), (J, r, N), dev)
+        gdt = DTYPES[da.dtype]
+        written += (da, db)
+    for t, name in ((dx, "dx"), (da, "da"), (db, "db")):
+        if t is not None and t.requires_grad:
+            _refuse_grad(name)
+    pw, nws = _bytes(ws, dev)
+    st = _adapters_backward(T, J, r, K, N, DTYPES[dy.dtype], pdy, lddy, px, ldx, pv, pa, pb, psc,
+                            po, pord, pdx, lddx, gdt, pda, pdb, pw, nws, _stream(stream, dev))
+    if st:
+        _check(st, "moe_adapters_backward")
     _changed(written)
