@@ -11,7 +11,7 @@ constexpr int kFewWarps = 16;
 constexpr int kFewTeamWarps = 4;  // warps that share the K of one gate/up tile
 constexpr int kFewTeams = kFewWarps / kFewTeamWarps;
 constexpr int kFewSub = 2048;     // bytes of the weights of a ring stage: 16 rows of 128
-constexpr int kFewMaxStages = 8;
+constexpr int kFewMaxStages = 4;
 constexpr int kFewSmem = 226 * 1024;  // dynamic; the kernel has a few words besides
 constexpr int kFewUnitBytes = 40;
 
@@ -36,10 +36,10 @@ inline int few_words(int n, int size, int64_t row) {
   return row % 4 == 0 && bytes % 4 == 0 ? bytes / 4 : (bytes + 4 - size + 3) / 4;
 }
 
-// mt: 16-row tiles of a gate/up tile; group: 0 (a row), 32, 64, 128; longest: the
-// largest K of the layer's matrices
+// group: 0 (a row), 32, 64, 128; rows_aligned: every row's scales (zero points) begin at a
+// multiple of four bytes
 inline FewPlan few_plan(int T, int H, int units, bool four_bits, int group, int scale_bytes,
-                        bool zeros, bool rows_aligned_scales, bool rows_aligned_zeros, int mt) {
+                        bool zeros, bool rows_aligned_scales, bool rows_aligned_zeros) {
   FewPlan p{};
   p.step_k = four_bits ? 256 : 64;
   p.block = four_bits ? (group ? group : 128) : 0;
@@ -49,7 +49,7 @@ inline FewPlan few_plan(int T, int H, int units, bool four_bits, int group, int 
   const int blocks = four_bits ? few_round(H, p.step_k) / p.block : 0;
   p.unit_at = p.sum_at + blocks * kFewMaxT * 4;
   p.red_at = few_round(p.unit_at + units * kFewUnitBytes, 16);
-  p.queue_at = p.red_at + kFewTeams * kFewTeamWarps * mt * 16 * 8 * 4;
+  p.queue_at = p.red_at + kFewTeams * kFewTeamWarps * 16 * 8 * 4;
   p.ring_at = few_round(p.queue_at + kFewTeams * 16 * 4, 128);
   p.sub_bytes = kFewSub;
   if (four_bits) {

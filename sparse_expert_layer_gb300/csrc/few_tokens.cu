@@ -12,8 +12,8 @@
 // token that is not finite stays in its column.
 //
 // The second kernel has one CTA an SM.  Gate and up: teams of four warps claim tiles of
-// 8 or 16 channels of an expert (8 gate and 8 up rows an MMA tile), a quarter of K a
-// warp; their parts are added in order, SwiGLU gives h in fp32.  Down: a CTA owns a
+// 8 channels of an expert (8 gate and 8 up rows, one MMA tile), a quarter of K a warp;
+// their parts are added in order, SwiGLU gives h in fp32.  Down: a CTA owns a
 // range of output channels of all experts; its 16 warps split the (expert, K) steps
 // evenly, apply the routing weights to their own sums, and add them in order: one
 // rounded store, no atomics, the same bits on every call.  Between the two a CTA waits
@@ -26,9 +26,9 @@
 // q * 2^-24 (four bits up: q * 2^-20, its x is divided by 16), so a weight costs part of
 // one AND.  x (and h) are scaled by a power of two for each token that brings their
 // largest value to 2^13, which makes them fp16 exactly (bf16 values: down to 2^-26 of
-// the largest), h rounded to 11 bits.  A block's sum of (q - z) x is 2^24 times the
-// MMA's sum minus z times the sum of x, which a further MMA of ones gives for h; scales
-// are applied in fp32.  16-bit weights: x as it is, h as a sum of two 16-bit numbers.
+// the largest), h rounded to 11 bits.  A block's MMAs start from -z times its sum of
+// x (of h: another MMA gives it), so they hold 2^-24 times the sum of (q - z) x; scales are
+// applied in fp32.  16-bit weights: x as it is, h as a sum of two 16-bit numbers.
 #include <math.h>
 
 #include "few_plan.h"
@@ -84,6 +84,7 @@ struct FewArgs {
   int T, H, I, Is, inter;
   int fp16, vec;  // type of x and out; rows of x in 16-byte pieces
   int group, scale_dtype;
+  int zstep;  // groups of a row in a stage, 0 where a row has one
   FewPlan p;
 };
 
@@ -278,52 +279,73 @@ __device__ __forceinline__ void cp_async_word(uint32_t dst, const void* src, int
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
                : "memory");
 }
+// 16 bytes of a weight row.  Past its end (in false) codes are left as they are: whatever
+// lies there is finite and meets zeros of x; 16-bit weights become zeros (src is not read).
+template <bool FOUR>
+__device__ __forceinline__ void copy_piece(uint32_t dst, const unsigned char* src, bool in,
+                                           const void* safe) {
+  if constexpr (FOUR) {
+    if (in)
+      asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src)
+                   : "memory");
+  } else {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst),
+                 "l"(in ? static_cast<const void*>(src) : safe), "r"(in ? 16 : 0)
+                 : "memory");
+  }
+}
 __device__ __forceinline__ void team_barrier(int team) {
   asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * kFewTeamWarps) : "memory");
 }
 // All but the `stages - 2` groups committed last have arrived.
 __device__ __forceinline__ void wait_stage(int stages) {
-  switch (stages) {
-    case 2: cp_async_wait<0>(); break;
-    case 3: cp_async_wait<1>(); break;
-    case 4: cp_async_wait<2>(); break;
-    case 5: cp_async_wait<3>(); break;
-    case 6: cp_async_wait<4>(); break;
-    case 7: cp_async_wait<5>(); break;
-    default: cp_async_wait<6>(); break;
-  }
+  if (stages == 4)
+    cp_async_wait<2>();
+  else if (stages == 3)
+    cp_async_wait<1>();
+  else
+    cp_async_wait<0>();
 }
+static_assert(kFewMaxStages == 4, "wait_stage knows up to four");
 
-__device__ __forceinline__ float read_scale(uint32_t at, int dtype) {
-  if (dtype == MOE_DT_FP32) {
+template <typename T>
+__device__ __forceinline__ float read_scale(uint32_t at) {
+  if constexpr (sizeof(T) == 4) {
     float v;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
     return v;
+  } else {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+    if constexpr (std::is_same<T, __half>::value)
+      return __half2float(__ushort_as_half(v));
+    else
+      return bf16_to_f(v);
   }
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
-  return dtype == MOE_DT_BF16 ? bf16_to_f(v) : __half2float(__ushort_as_half(v));
 }
 __device__ __forceinline__ float read_zero(uint32_t at) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
   return (float)(v & 31u);
 }
-
-// Where a lane's two weight rows of a 16-row tile have their groups: the byte of a
-// stage's first group inside its first word (bits 0-1 of the row's address).
-struct FewSkew {
-  uint32_t s, z;  // address of the first row's first group, modulo 4
-  uint32_t s8, z8;
-};
+// d = a b + (c0, c1, c2, c3)
+__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
+                                         float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
 
 // The kinds of weights.  kWords: granules of eight K that a lane supplies in a stage;
-// granule i is x's 16-byte piece granule(i, tg) of the stage.
-template <int BLOCK, bool ZEROS>
+// granule i is x's 16-byte piece piece(i, tg) of the stage.
+template <int BLOCK, bool ZEROS, typename SCALE>
 struct Four {
   using Mma = __half;
+  using Scale = SCALE;
   static constexpr bool kFour = true, kZeros = ZEROS, kScaled = true, kRest = false;
-  static constexpr int kStepK = 256, kWords = 8;
+  static constexpr int kStepK = 256, kWords = 8, kScaleBytes = sizeof(SCALE);
   static constexpr int kBlock = BLOCK, kBlocks = 256 / BLOCK, kPer = BLOCK / 32;
   // first K of granule i of quad lane tg
   static __device__ __forceinline__ int k_of(int i, int tg) {
@@ -355,76 +377,86 @@ struct Sixteen {
   using Mma = T;
   static constexpr bool kFour = false, kRest = true;
   static constexpr bool kScaled = std::is_same<T, __half>::value;  // h needs fp16's range
-  static constexpr int kStepK = 64, kWords = 2;
-  static constexpr int kBlocks = 1;
+  static constexpr int kStepK = 64, kWords = 2, kBlocks = 1;
   static __device__ __forceinline__ int k_of(int i, int tg) { return i * 32 + tg * 8; }
   static __device__ __forceinline__ int piece(int i, int tg) { return i * 4 + tg; }
   static __device__ __forceinline__ int piece_of_k8(int j) { return j; }
   static __device__ __forceinline__ int swizzle(int r, int c) { return c ^ ((r & 1) << 2); }
 };
 
-// acc += a stage's 16 rows times b.  xs: sums of x over the stage's blocks for the
-// lane's columns 2 tg and 2 tg + 1.
+// Where a lane finds the groups of its rows g and g + 8 in a stage: their offset from the
+// stage, with the byte of the first group inside its word.  (Eight rows further on that byte
+// is the same.)
+struct FewGroups {
+  uint32_t s;  // scales of row g
+  uint32_t z;  // zero points of row g, less the byte
+  uint32_t zbyte;
+};
+
+// acc += the sum over a stage's K of its 16 rows times b: 2^-24 of it with 4-bit weights.
+// xs: minus 8 x 2^-24 times the sums of x over the stage's blocks (with zero points: minus
+// 2^-24 times them), for the lane's columns 2 tg and 2 tg + 1.
 template <typename K>
 __device__ __forceinline__ void multiply(uint32_t st, const uint32_t (&b)[K::kWords][4],
                                          const uint32_t (&rest)[K::kRest ? K::kWords : 1][4],
                                          const float2 (&xs)[K::kBlocks], bool with_rest,
-                                         const FewArgs& a, const FewSkew& skew, int step,
+                                         const FewArgs& a, const FewGroups& at, int step,
                                          float (&acc)[4]) {
   const int lane = threadIdx.x % 32, g = lane / 4, tg = lane % 4;
   const uint32_t row = st + g * 128;
   if constexpr (K::kFour) {
-    const uint32_t sbase = st + kFewSub, zbase = sbase + 64 * a.p.swords;
-    const int es = a.scale_dtype == MOE_DT_FP32 ? 4 : 2;
-    // groups of a stage; 0: one for the whole row
-    const int gs = a.group ? K::kBlocks : 0;
-    const uint32_t s0 = sbase + g * 4 * a.p.swords + ((skew.s + step * gs * es) & 3u);
-    const uint32_t s8 = sbase + (g + 8) * 4 * a.p.swords + ((skew.s8 + step * gs * es) & 3u);
-    const uint32_t z0 = zbase + g * 4 * a.p.zwords + ((skew.z + step * gs) & 3u);
-    const uint32_t z8 = zbase + (g + 8) * 4 * a.p.zwords + ((skew.z8 + step * gs) & 3u);
+    const uint32_t s0 = st + at.s, s8 = s0 + 32 * a.p.swords;
+    const uint32_t z0 = st + at.z + ((at.zbyte + step * a.zstep) & 3u), z8 = z0 + 32 * a.p.zwords;
 #pragma unroll
     for (int blk = 0; blk < K::kBlocks; ++blk) {
       uint32_t lo[K::kPer], hi[K::kPer];
       const int byte = blk * (K::kBlock / 2) + tg * (K::kBlock / 8);
-      const uint32_t at = row + K::swizzle(g, byte / 16) * 16 + byte % 16;
+      const uint32_t from = row + K::swizzle(g, byte / 16) * 16 + byte % 16;
       if constexpr (K::kPer == 4) {
-        const uint4 u = lds128(at), v = lds128(at + 8 * 128);
+        const uint4 u = lds128(from), v = lds128(from + 8 * 128);
         lo[0] = u.x, lo[1] = u.y, lo[2] = u.z, lo[3] = u.w;
         hi[0] = v.x, hi[1] = v.y, hi[2] = v.z, hi[3] = v.w;
       } else if constexpr (K::kPer == 2) {
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(lo[0]), "=r"(lo[1]) : "r"(at) : "memory");
         asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                     : "=r"(hi[0]), "=r"(hi[1]) : "r"(at + 8 * 128) : "memory");
+                     : "=r"(lo[0]), "=r"(lo[1]) : "r"(from) : "memory");
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                     : "=r"(hi[0]), "=r"(hi[1]) : "r"(from + 8 * 128) : "memory");
       } else {
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(lo[0]) : "r"(at) : "memory");
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(hi[0]) : "r"(at + 8 * 128) : "memory");
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(lo[0]) : "r"(from) : "memory");
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(hi[0]) : "r"(from + 8 * 128) : "memory");
       }
-      float d[4] = {};
+      const int j = a.group ? blk : 0;
+      float c0 = xs[blk].x, c1 = xs[blk].y, c2 = c0, c3 = c1;
+      if constexpr (K::kZeros) {
+        const float za = read_zero(z0 + j), zb = read_zero(z8 + j);
+        c2 = c0 * zb, c3 = c1 * zb, c0 *= za, c1 *= za;
+      }
+      float d[4];
 #pragma unroll
       for (int i = 0; i < K::kPer; ++i) {
         const int w = blk * K::kPer + i;
         const uint32_t l = lo[i], h = hi[i], l8 = l >> 8, h8 = h >> 8;
-        mma16816<__half>(d, l & 0x000f000fu, h & 0x000f000fu, l & 0x00f000f0u, h & 0x00f000f0u,
-                         b[w][0], b[w][1]);
+        if (i == 0)
+          mma_from(d, l & 0x000f000fu, h & 0x000f000fu, l & 0x00f000f0u, h & 0x00f000f0u, b[w][0],
+                   b[w][1], c0, c1, c2, c3);
+        else
+          mma16816<__half>(d, l & 0x000f000fu, h & 0x000f000fu, l & 0x00f000f0u, h & 0x00f000f0u,
+                           b[w][0], b[w][1]);
         mma16816<__half>(d, l8 & 0x000f000fu, h8 & 0x000f000fu, l8 & 0x00f000f0u,
                          h8 & 0x00f000f0u, b[w][2], b[w][3]);
       }
-      const int j = gs ? blk : 0;
-      const float sa = read_scale(s0 + j * es, a.scale_dtype);
-      const float sb = read_scale(s8 + j * es, a.scale_dtype);
-      const float za = K::kZeros ? read_zero(z0 + j) : 8.f;
-      const float zb = K::kZeros ? read_zero(z8 + j) : 8.f;
-      constexpr float kUp = 16777216.f;
-      acc[0] = fmaf(sa, fmaf(d[0], kUp, -za * xs[blk].x), acc[0]);
-      acc[1] = fmaf(sa, fmaf(d[1], kUp, -za * xs[blk].y), acc[1]);
-      acc[2] = fmaf(sb, fmaf(d[2], kUp, -zb * xs[blk].x), acc[2]);
-      acc[3] = fmaf(sb, fmaf(d[3], kUp, -zb * xs[blk].y), acc[3]);
+      const float sa = read_scale<typename K::Scale>(s0 + j * K::kScaleBytes);
+      const float sb = read_scale<typename K::Scale>(s8 + j * K::kScaleBytes);
+      acc[0] = fmaf(sa, d[0], acc[0]);
+      acc[1] = fmaf(sa, d[1], acc[1]);
+      acc[2] = fmaf(sb, d[2], acc[2]);
+      acc[3] = fmaf(sb, d[3], acc[3]);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < K::kWords; ++i) {
-      const uint32_t at = row + K::swizzle(g, i * 4 + tg) * 16;
-      const uint4 u = lds128(at), v = lds128(at + 8 * 128);
+      const uint32_t from = row + K::swizzle(g, i * 4 + tg) * 16;
+      const uint4 u = lds128(from), v = lds128(from + 8 * 128);
       mma16816<typename K::Mma>(acc, u.x, v.x, u.y, v.y, b[i][0], b[i][1]);
       mma16816<typename K::Mma>(acc, u.z, v.z, u.w, v.w, b[i][2], b[i][3]);
       if (with_rest) {
@@ -449,42 +481,39 @@ __device__ __forceinline__ FewShape shape_of(const FewArgs& a, int k) {
   return s;
 }
 
-// Copies a stage: 16 rows of 128 bytes (zeros past the row's end), and their scales and
-// zero points.  wp[i]: the lane's row lane / 8 + 4 i of the tile; sp, zp: the scales of row
-// lane / 2, up to send, zend.
+// The scales and zero points of a stage's row lane / 2, whose groups begin at sp and zp:
+// words lane % 2, + 2, .. of each, up to the row's end.
 template <typename K>
-__device__ __forceinline__ void copy_stage(const FewArgs& a, const FewShape& sh, uint32_t st,
-                                           int step, const unsigned char* const (&wp)[4],
-                                           const unsigned char* sp, const unsigned char* zp) {
+__device__ __forceinline__ void copy_groups(const FewArgs& a, const FewShape& sh, uint32_t st,
+                                            int step, const unsigned char* sp,
+                                            const unsigned char* zp) {
   const int lane = threadIdx.x % 32;
-  const int byte = step * 128 + (lane % 8) * 16;
-  const bool in = byte < sh.row;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = lane / 8 + 4 * i;
-    cp_async16_or_zero(st + r * 128 + K::swizzle(r, lane % 8) * 16, wp[i] + (in ? byte : 0), in);
-  }
+  auto words = [&](const unsigned char* row, int first, int end, int n, uint32_t dst) {
+    const uint32_t byte = (uint32_t)(reinterpret_cast<uintptr_t>(row + first) & 3u);
+    const unsigned char* const first_word = row + first - byte;
+    const unsigned char* from = first_word + 4 * (lane % 2);
+    int left = end - first + (int)byte - 4 * (lane % 2);
+    dst += lane / 2 * 4 * n + 4 * (lane % 2);
+    for (int i = lane % 2; i < n; i += 2, from += 8, left -= 8, dst += 8)
+      cp_async_word(dst, left > 0 ? from : first_word, max(0, min(4, left)));
+  };
+  words(sp, step * a.zstep * K::kScaleBytes, sh.groups * K::kScaleBytes, a.p.swords, st + kFewSub);
+  if constexpr (K::kZeros)
+    words(zp, step * a.zstep, sh.groups, a.p.zwords, st + kFewSub + 64 * a.p.swords);
+}
+template <typename K>
+__device__ __forceinline__ FewGroups groups_at(const FewArgs& a, const FewShape& sh, int64_t row) {
+  const int g = threadIdx.x % 32 / 4;
+  FewGroups at{};
   if constexpr (K::kFour) {
-    const int es = a.scale_dtype == MOE_DT_FP32 ? 4 : 2;
-    const int gs = a.group ? K::kBlocks : 0;
-    auto words = [&](const unsigned char* row, int first, int end, int n, uint32_t dst) {
-      const uintptr_t at = reinterpret_cast<uintptr_t>(row + first) & ~(uintptr_t)3;
-      const uintptr_t stop = reinterpret_cast<uintptr_t>(row + end);
-      for (int i = lane % 2; i < n; i += 2) {
-        const uintptr_t p = at + 4 * i;
-        const int left = p < stop ? (int)min((uintptr_t)4, stop - p) : 0;
-        cp_async_word(dst + (lane / 2) * 4 * n + 4 * i,
-                      reinterpret_cast<const void*>(left ? p : (at & ~(uintptr_t)3)), left);
-      }
-    };
-    words(sp, min(step * gs, sh.groups - 1) * es, sh.groups * es, a.p.swords, st + kFewSub);
-    if constexpr (K::kZeros)
-      words(zp, min(step * gs, sh.groups - 1), sh.groups, a.p.zwords,
-            st + kFewSub + 64 * a.p.swords);
+    at.s = kFewSub + g * 4 * a.p.swords + ((uint32_t)(row * sh.groups * K::kScaleBytes) & 3u);
+    at.z = kFewSub + 64 * a.p.swords + g * 4 * a.p.zwords;
+    at.zbyte = (uint32_t)(row * sh.groups);
   }
+  return at;
 }
 
-// Parts of the gate/up tiles' numbering.
+// The numbering of the gate/up tiles.
 struct FewTiles {
   int routed, shared;  // tiles of one routed expert, of the shared one
   int units, total;
@@ -499,7 +528,7 @@ __device__ __forceinline__ void tile_at(const FewTiles& n, int tile, int* unit, 
   }
 }
 
-template <typename K, int MT>
+template <typename K>
 __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, const FewUnit* units,
                                         const FewTiles& n, const float* x_inverse) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -508,13 +537,13 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, c
   const FewShape sh = shape_of<K>(a, a.H);
   const int per = (sh.steps + kFewTeamWarps - 1) / kFewTeamWarps;
   const int k0 = min(sh.steps, kw * per), k1 = min(sh.steps, k0 + per);
-  const int S = a.p.stages;
+  const int S = a.p.stages, sub = a.p.sub_bytes;
   // tiles a team knows beyond the one it works on: as many as its rings reach into
   const int least = sh.steps - (sh.steps - 1) / per * per;  // the last busy warp's steps
-  const int ahead = (S - 1 + least * MT - 1) / (least * MT);
+  const int ahead = (S - 1 + least - 1) / least;
   volatile int* queue = reinterpret_cast<int*>(smem + a.p.queue_at) + team * 16;
-  float* red = reinterpret_cast<float*>(smem + a.p.red_at) + team * kFewTeamWarps * MT * 128;
-  const uint32_t ring = smem_u32(smem) + a.p.ring_at + warp * S * a.p.sub_bytes;
+  float* red = reinterpret_cast<float*>(smem + a.p.red_at) + team * kFewTeamWarps * 128;
+  const uint32_t ring = smem_u32(smem) + a.p.ring_at + warp * S * sub;
   FewHead* head = a.head;
   if (tt == 0) {
     const int base = atomicAdd(&head->claim, ahead + 1);
@@ -522,17 +551,18 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, c
   }
   team_barrier(team);
 
-  // what is copied next: stage (step, m) of tile queue[seq]
+  // What is copied next: stage `step` of tile queue[seq].  gate, up: the lane's piece of rows
+  // lane / 8 of both, 4 rows more for the second; left: bytes from there to the rows' end.
   struct {
-    int seq, step, m;
+    int seq, step, left;
     bool fresh, done;
-    const unsigned char* gate;  // the lane's row lane / 8 of the tile's first gate rows
-    const unsigned char* up;
-    const unsigned char* s;     // scales and zero points of the lane's row lane / 2
-    const unsigned char* z;
-    int last;  // the most eight-row blocks the tile may go on
-  } next{0, k0, 0, true, k0 == k1, nullptr, nullptr, nullptr, nullptr, 0};
-  uint32_t fill = 0;
+    const unsigned char *gate, *up, *s, *z;
+  } next{0, k0, 0, true, k0 == k1, nullptr, nullptr, nullptr, nullptr};
+  const int dst = lane / 8 * 128, four_rows = 4 * sh.row;
+  const int d0 = dst + K::swizzle(lane / 8, lane % 8) * 16;
+  const int d1 = dst + 4 * 128 + K::swizzle(lane / 8 + 4, lane % 8) * 16;
+  uint32_t fill = ring;
+  const uint32_t ring_end = ring + S * sub;
   auto issue = [&]() {
     if (!next.done && next.fresh) {
       const int tile = queue[next.seq % 16];
@@ -540,45 +570,44 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, c
       if (!next.done) {
         int u, f;
         tile_at(n, tile, &u, &f);
-        const int e = units[u].expert, N = e < 0 ? a.Is : a.I;
+        const int e = units[u].expert;
         const FewMatrix* m = e < 0 ? a.shared : a.m;
-        const int64_t row = (e < 0 ? 0 : (int64_t)e * N) + f * 8 * MT;
-        next.last = (N - f * 8 * MT) / 8 - 1;
-        next.gate = m[0].w + (row + lane / 8) * sh.row;
-        next.up = m[1].w + (row + lane / 8) * sh.row;
+        const int64_t row = (e < 0 ? 0 : (int64_t)e * a.I) + f * 8;
+        const int64_t at = (row + lane / 8) * sh.row + k0 * 128 + (lane % 8) * 16;
+        next.gate = m[0].w + at;
+        next.up = m[1].w + at;
+        next.left = sh.row - k0 * 128 - (lane % 8) * 16;
         if constexpr (K::kFour) {
-          const FewMatrix& mine = m[lane / 16];  // rows 0-7 of a tile are gate's
-          const int es = a.scale_dtype == MOE_DT_FP32 ? 4 : 2;
-          next.s = mine.s + (row + lane / 2 % 8) * sh.groups * es;
-          if constexpr (K::kZeros) next.z = mine.z + (row + lane / 2 % 8) * sh.groups;
+          const int64_t first = (row + lane / 2 % 8) * sh.groups;  // rows 0-7 are gate's
+          next.s = (lane < 16 ? m[0].s : m[1].s) + first * K::kScaleBytes;
+          if constexpr (K::kZeros) next.z = (lane < 16 ? m[0].z : m[1].z) + first;
         }
         next.fresh = false;
       }
     }
     if (!next.done) {
-      const int64_t skip = min(next.m, next.last) * 8;
-      const unsigned char* const wp[4] = {
-          next.gate + skip * sh.row, next.gate + (skip + 4) * sh.row, next.up + skip * sh.row,
-          next.up + (skip + 4) * sh.row};
-      const int es = a.scale_dtype == MOE_DT_FP32 ? 4 : 2;
-      copy_stage<K>(a, sh, ring + fill, next.step, wp, next.s + skip * sh.groups * es,
-                    next.z + skip * sh.groups);
-      if (++next.m == MT) {
-        next.m = 0;
-        if (++next.step == k1) {
-          next.step = k0;
-          ++next.seq;
-          next.fresh = true;
-        }
+      const bool in = next.left > 0;
+      copy_piece<K::kFour>(fill + d0, next.gate, in, a.x);
+      copy_piece<K::kFour>(fill + d1, next.gate + four_rows, in, a.x);
+      copy_piece<K::kFour>(fill + d0 + 8 * 128, next.up, in, a.x);
+      copy_piece<K::kFour>(fill + d1 + 8 * 128, next.up + four_rows, in, a.x);
+      if constexpr (K::kFour) copy_groups<K>(a, sh, fill, next.step, next.s, next.z);
+      next.gate += 128;
+      next.up += 128;
+      next.left -= 128;
+      if (++next.step == k1) {
+        next.step = k0;
+        ++next.seq;
+        next.fresh = true;
       }
     }
     cp_async_commit();
-    fill = fill == (uint32_t)(S - 1) * a.p.sub_bytes ? 0u : fill + a.p.sub_bytes;
+    fill = fill + sub == ring_end ? ring : fill + sub;
   };
   for (int i = 0; i < S - 1; ++i) issue();
 
-  uint32_t use = 0;
-  const uint32_t xrow = smem_u32(smem) + min(g, a.T - 1) * a.p.xpitch;
+  uint32_t use = ring;
+  const uint32_t xrow = smem_u32(smem) + min(g, a.T - 1) * a.p.xpitch + tg * 16;
   const uint32_t sums = smem_u32(smem) + a.p.sum_at + tg * 8;
   for (int seq = 0;; ++seq) {
     const int tile = queue[seq % 16];
@@ -587,16 +616,18 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, c
     if (tt == 0) claimed = atomicAdd(&head->claim, 1);
     int u, f;
     tile_at(n, tile, &u, &f);
-    const int e = units[u].expert, N = e < 0 ? a.Is : a.I;
-    const int64_t row0 = (e < 0 ? 0 : (int64_t)e * N) + f * 8 * MT + g;
-    const uint32_t es = a.scale_dtype == MOE_DT_FP32 ? 4 : 2;
-    float acc[MT][4] = {};
+    const int e = units[u].expert;
+    const FewGroups at = groups_at<K>(a, sh, (e < 0 ? 0 : (int64_t)e * a.I) + f * 8 + g);
+    float acc[4] = {};
     for (int step = k0; step < k1; ++step) {
+      wait_stage(S);
+      __syncwarp();
+      issue();
       uint32_t b[K::kWords][4];
       float2 xs[K::kBlocks];
 #pragma unroll
       for (int i = 0; i < K::kWords; ++i) {
-        const uint4 v = lds128(xrow + (step * (K::kStepK / 8) + K::piece(i, tg)) * 16);
+        const uint4 v = lds128(xrow + (step * (K::kStepK / 8) + K::piece(i, 0)) * 16);
         b[i][0] = v.x, b[i][1] = v.y, b[i][2] = v.z, b[i][3] = v.w;
       }
       if constexpr (K::kFour) {
@@ -608,47 +639,31 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, c
                        : "memory");
       }
       const uint32_t none[K::kRest ? K::kWords : 1][4] = {};
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        wait_stage(S);
-        __syncwarp();
-        issue();
-        const int64_t row = row0 + min(m, (N - f * 8 * MT) / 8 - 1) * 8;
-        FewSkew skew{};
-        if constexpr (K::kFour) {
-          skew.s = skew.s8 = (uint32_t)(row * sh.groups * es);
-          skew.z = skew.z8 = (uint32_t)(row * sh.groups);
-        }
-        multiply<K>(ring + use, b, none, xs, false, a, skew, step, acc[m]);
-        use = use == (uint32_t)(S - 1) * a.p.sub_bytes ? 0u : use + a.p.sub_bytes;
-      }
+      multiply<K>(use, b, none, xs, false, a, at, step, acc);
+      use = use + sub == ring_end ? ring : use + sub;
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      float* r = red + (kw * MT + m) * 128 + g * 8 + 2 * tg;
-      *reinterpret_cast<float2*>(r) = make_float2(acc[m][0], acc[m][1]);
-      *reinterpret_cast<float2*>(r + 64) = make_float2(acc[m][2], acc[m][3]);
-    }
+    float* r = red + kw * 128 + g * 8 + 2 * tg;
+    *reinterpret_cast<float2*>(r) = make_float2(acc[0], acc[1]);
+    *reinterpret_cast<float2*>(r + 64) = make_float2(acc[2], acc[3]);
     if (tt == 0) queue[(seq + ahead + 1) % 16] = claimed;
     team_barrier(team);
-    if (tt < 64 * MT) {
-      const int ch = tt % 8, t = tt / 8 % 8, m = tt / 64;
-      const int c = f * 8 * MT + m * 8 + ch;
+    if (tt < 64) {
+      const int ch = tt % 8, t = tt / 8;
       float gate = 0.f, up = 0.f;
 #pragma unroll
       for (int i = 0; i < kFewTeamWarps; ++i) {
-        gate += red[(i * MT + m) * 128 + ch * 8 + t];
-        up += red[(i * MT + m) * 128 + (ch + 8) * 8 + t];
+        gate += red[i * 128 + ch * 8 + t];
+        up += red[i * 128 + (ch + 8) * 8 + t];
       }
-      const bool mine = c < N && ((units[u].tokens >> t) & 1u);
+      const bool mine = (units[u].tokens >> t) & 1u;
       float h = 0.f;
       if (mine) {
         if constexpr (K::kFour) {
-          gate *= x_inverse[t];
-          up *= x_inverse[t];
+          gate = gate * 16777216.f * x_inverse[t];
+          up = up * 16777216.f * x_inverse[t];
         }
         h = gate / (1.f + expf(-gate)) * up;
-        __stcg(a.h + ((int64_t)u * a.T + t) * a.inter + c, h);
+        __stcg(a.h + ((int64_t)u * a.T + t) * a.inter + f * 8 + ch, h);
       }
       if constexpr (K::kScaled) {
         uint32_t most = __float_as_uint(fabsf(h));
@@ -674,57 +689,76 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int g = lane / 4, tg = lane % 4;
   const FewShape rs = shape_of<K>(a, a.I), ss = shape_of<K>(a, a.Is);
-  const int S = a.p.stages;
-  const uint32_t ring = smem_u32(smem) + a.p.ring_at + warp * S * a.p.sub_bytes;
+  const int S = a.p.stages, sub = a.p.sub_bytes;
+  const uint32_t ring = smem_u32(smem) + a.p.ring_at + warp * S * sub, ring_end = ring + S * sub;
   float* sums = reinterpret_cast<float*>(smem + a.p.ring_at);
   const int share = (a.H + gridDim.x - 1) / gridDim.x;
   const int c_begin = min(a.H, (int)blockIdx.x * share), c_end = min(a.H, c_begin + share);
-  const int flat = n.units * rs.steps + (shared ? ss.steps : 0);
+  const int routed = n.units * rs.steps, flat = routed + (shared ? ss.steps : 0);
   const int f0 = (int)((int64_t)flat * warp / kFewWarps);
   const int f1 = (int)((int64_t)flat * (warp + 1) / kFewWarps);
-  const uint32_t es = a.scale_dtype == MOE_DT_FP32 ? 4 : 2;
+  const int dst = lane / 8 * 128;
+  const int d0 = dst + K::swizzle(lane / 8, lane % 8) * 16;
+  const int d1 = dst + 4 * 128 + K::swizzle(lane / 8 + 4, lane % 8) * 16;
   bool waited = false;
 
   for (int c0 = c_begin; c0 < c_end; c0 += 16 * kFewDownTiles) {
     const int channels = min(c_end - c0, 16 * kFewDownTiles);
     const int tiles = (channels + 15) / 16;
-    auto unit_at = [&](int f, int* u, int* step) {
-      if (f < n.units * rs.steps) {
-        *u = f / rs.steps;
-        *step = f % rs.steps;
-      } else {
-        *u = n.units;
-        *step = f - n.units * rs.steps;
+    // What is copied next: tile m of step `step` of unit u.
+    struct {
+      int f, u, step, m, steps;
+      const FewShape* sh;
+      const unsigned char *w, *s, *z;  // the lane's piece of the first row, its row's groups
+    } next{f0, f0 < routed ? f0 / max(1, rs.steps) : n.units, 0, 0, 0, &rs, nullptr, nullptr,
+           nullptr};
+    next.step = f0 - next.u * rs.steps;
+    auto enter = [&]() {  // a unit's pointers
+      const int e = units[next.u].expert;
+      const FewMatrix& m = e < 0 ? a.shared[2] : a.m[2];
+      next.sh = e < 0 ? &ss : &rs;
+      next.steps = next.sh->steps;
+      const int64_t first = (e < 0 ? 0 : (int64_t)e * a.H) + c0;
+      next.w = m.w + (first + lane / 8) * next.sh->row + (lane % 8) * 16;
+      if constexpr (K::kFour) {
+        const int64_t groups = (first + lane / 2) * next.sh->groups;
+        next.s = m.s + groups * K::kScaleBytes;
+        if constexpr (K::kZeros) next.z = m.z + groups;
       }
     };
-    int next_f = f0, next_m = 0;
-    uint32_t fill = 0, use = 0;
+    if (f0 < f1) enter();
+    uint32_t fill = ring, use = ring;
     auto issue = [&]() {
-      if (next_f < f1) {
-        int u, step;
-        unit_at(next_f, &u, &step);
-        const int e = units[u].expert;
-        const FewMatrix& m = e < 0 ? a.shared[2] : a.m[2];
-        const FewShape& sh = e < 0 ? ss : rs;
-        const int64_t first = e < 0 ? 0 : (int64_t)e * a.H;
-        auto row = [&](int r) { return first + min(c0 + next_m * 16 + r, c_end - 1); };
-        const unsigned char* wp[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) wp[i] = m.w + row(lane / 8 + 4 * i) * sh.row;
-        const unsigned char *sp = nullptr, *zp = nullptr;
+      if (next.f < f1) {
+        const FewShape& sh = *next.sh;
+        const int byte = next.step * 128;
+        // rows past the range are not stored, whatever they hold
+        const int rows = byte + (lane % 8) * 16 < sh.row ? channels - next.m * 16 - lane / 8 : 0;
+        const unsigned char* w = next.w + (int64_t)next.m * 16 * sh.row + byte;
+        const int64_t four = 4 * (int64_t)sh.row;
+        copy_piece<K::kFour>(fill + d0, w, rows > 0, a.x);
+        copy_piece<K::kFour>(fill + d1, w + four, rows > 4, a.x);
+        copy_piece<K::kFour>(fill + d0 + 8 * 128, w + 2 * four, rows > 8, a.x);
+        copy_piece<K::kFour>(fill + d1 + 8 * 128, w + 3 * four, rows > 12, a.x);
         if constexpr (K::kFour) {
-          sp = m.s + row(lane / 2) * sh.groups * es;
-          if constexpr (K::kZeros) zp = m.z + row(lane / 2) * sh.groups;
+          // (a row past the range takes the last one's)
+          const int r = min(next.m * 16, channels - 1 - lane / 2) * sh.groups;
+          const unsigned char* z = nullptr;
+          if constexpr (K::kZeros) z = next.z + r;
+          copy_groups<K>(a, sh, fill, next.step, next.s + r * K::kScaleBytes, z);
         }
-        const unsigned char* const wc[4] = {wp[0], wp[1], wp[2], wp[3]};
-        copy_stage<K>(a, sh, ring + fill, step, wc, sp, zp);
-        if (++next_m == tiles) {
-          next_m = 0;
-          ++next_f;
+        if (++next.m == tiles) {
+          next.m = 0;
+          ++next.f;
+          if (++next.step == next.steps) {
+            next.step = 0;
+            ++next.u;
+            if (next.f < f1) enter();
+          }
         }
       }
       cp_async_commit();
-      fill = fill == (uint32_t)(S - 1) * a.p.sub_bytes ? 0u : fill + a.p.sub_bytes;
+      fill = fill + sub == ring_end ? ring : fill + sub;
     };
     for (int i = 0; i < S - 1; ++i) issue();
     if (!waited) {
@@ -736,9 +770,11 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
     }
 
     float acc[kFewDownTiles][4] = {}, total[kFewDownTiles][4] = {};
-    int unit = -1;
     float w0 = 0.f, w1 = 0.f, up = 1.f;
     const float* hrow = nullptr;
+    FewGroups at[kFewDownTiles];
+    int u = f0 < routed ? f0 / max(1, rs.steps) : n.units;
+    int step = f0 - u * rs.steps, steps = 0, kmax = 0;
     auto flush = [&]() {
 #pragma unroll
       for (int m = 0; m < kFewDownTiles; ++m) {
@@ -750,30 +786,38 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
       }
     };
     for (int f = f0; f < f1; ++f) {
-      int u, step;
-      unit_at(f, &u, &step);
-      if (u != unit) {
-        if (unit >= 0) flush();
-        unit = u;
+      if (f == f0 || step == steps) {
+        if (f > f0) {
+          flush();
+          step = 0;
+          ++u;
+        }
+        const int e = units[u].expert;
+        const FewShape& sh = e < 0 ? ss : rs;
+        steps = sh.steps;
+        kmax = sh.K;
         const uint32_t tokens = units[u].tokens;
         hrow = g < a.T && ((tokens >> g) & 1u) ? a.h + ((int64_t)u * a.T + g) * a.inter : nullptr;
-        w0 = units[u].w[2 * tg];
-        w1 = units[u].w[2 * tg + 1];
+        w0 = units[u].w[2 * tg] * (K::kFour ? 16777216.f : 1.f);
+        w1 = units[u].w[2 * tg + 1] * (K::kFour ? 16777216.f : 1.f);
         if constexpr (K::kScaled) {
           up = __uint_as_float(fp16_range_bits(__ldcg(&a.head->hmax[u][g])));
           w0 *= inverse_pow2(fp16_range_bits(__ldcg(&a.head->hmax[u][2 * tg])));
           w1 *= inverse_pow2(fp16_range_bits(__ldcg(&a.head->hmax[u][2 * tg + 1])));
         }
+        if constexpr (K::kFour) {
+#pragma unroll
+          for (int m = 0; m < kFewDownTiles; ++m)
+            at[m] = groups_at<K>(a, sh, (e < 0 ? 0 : (int64_t)e * a.H) + c0 + m * 16 + g);
+        }
       }
-      const int e = units[u].expert;
-      const FewShape& sh = e < 0 ? ss : rs;
       // the lane's h of this step, as MMA operands
       uint32_t b[K::kWords][4], rest[K::kRest ? K::kWords : 1][4];
 #pragma unroll
       for (int i = 0; i < K::kWords; ++i) {
         const int k = step * K::kStepK + K::k_of(i, tg);
         float4 p = make_float4(0.f, 0.f, 0.f, 0.f), q = p;
-        if (hrow && k < sh.K) {
+        if (hrow && k < kmax) {
           p = __ldcg(reinterpret_cast<const float4*>(hrow + k));
           q = __ldcg(reinterpret_cast<const float4*>(hrow + k + 4));
         }
@@ -792,38 +836,31 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
 #pragma unroll
         for (int blk = 0; blk < K::kBlocks; ++blk) {
           float d[4] = {};
+          // sums: twos and thirty-twos (for what was divided by 16) of -2^-22, or -2^-25
+          constexpr uint32_t kOne = K::kZeros ? 0x80018001u : 0x80088008u;   // -2^-24, -2^-21
+          constexpr uint32_t kMany = K::kZeros ? 0x80108010u : 0x80808080u;  // 16 times that
 #pragma unroll
           for (int i = 0; i < K::kPer; ++i) {
-            // ones, and sixteens for what was divided by 16
-            mma16816<__half>(d, 0x3c003c00u, 0x3c003c00u, 0x4c004c00u, 0x4c004c00u,
-                             b[blk * K::kPer + i][0], b[blk * K::kPer + i][1]);
-            mma16816<__half>(d, 0x3c003c00u, 0x3c003c00u, 0x4c004c00u, 0x4c004c00u,
-                             b[blk * K::kPer + i][2], b[blk * K::kPer + i][3]);
+            mma16816<__half>(d, kOne, kOne, kMany, kMany, b[blk * K::kPer + i][0],
+                             b[blk * K::kPer + i][1]);
+            mma16816<__half>(d, kOne, kOne, kMany, kMany, b[blk * K::kPer + i][2],
+                             b[blk * K::kPer + i][3]);
           }
           xs[blk] = make_float2(d[0], d[1]);
         }
       }
-      const int64_t first = (e < 0 ? 0 : (int64_t)e * a.H);
 #pragma unroll
       for (int m = 0; m < kFewDownTiles; ++m) {
         if (m >= tiles) break;
         wait_stage(S);
         __syncwarp();
         issue();
-        FewSkew skew{};
-        if constexpr (K::kFour) {
-          const int64_t r0 = first + min(c0 + m * 16 + g, c_end - 1);
-          const int64_t r8 = first + min(c0 + m * 16 + g + 8, c_end - 1);
-          skew.s = (uint32_t)(r0 * sh.groups * es);
-          skew.s8 = (uint32_t)(r8 * sh.groups * es);
-          skew.z = (uint32_t)(r0 * sh.groups);
-          skew.z8 = (uint32_t)(r8 * sh.groups);
-        }
-        multiply<K>(ring + use, b, rest, xs, true, a, skew, step, acc[m]);
-        use = use == (uint32_t)(S - 1) * a.p.sub_bytes ? 0u : use + a.p.sub_bytes;
+        multiply<K>(use, b, rest, xs, true, a, at[m], step, acc[m]);
+        use = use + sub == ring_end ? ring : use + sub;
       }
+      ++step;
     }
-    if (unit >= 0) flush();
+    flush();
     cp_async_wait<0>();
     __syncthreads();
     // [warp][channel][token], added in the order of the warps
@@ -839,16 +876,16 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < kFewWarps; ++w) v += sums[(w * 16 * kFewDownTiles + c) * 8 + t];
-      const int64_t at = c0 + c;
+      const int64_t col = c0 + c;
       const float zw = zero_w[t];
       if (zw != 0.f) {
-        const uint16_t x = static_cast<const uint16_t*>(a.x)[t * a.ldx + at];
+        const uint16_t x = static_cast<const uint16_t*>(a.x)[t * a.ldx + col];
         v = fmaf(zw, a.fp16 ? __half2float(__ushort_as_half(x)) : bf16_to_f(x), v);
       }
       if (a.fp16)
-        static_cast<__half*>(a.out)[t * a.ldo + at] = from_f<__half>(v);
+        static_cast<__half*>(a.out)[t * a.ldo + col] = from_f<__half>(v);
       else
-        static_cast<__nv_bfloat16*>(a.out)[t * a.ldo + at] = from_f<__nv_bfloat16>(v);
+        static_cast<__nv_bfloat16*>(a.out)[t * a.ldo + col] = from_f<__nv_bfloat16>(v);
     }
     __syncthreads();
   }
@@ -926,13 +963,15 @@ __device__ __forceinline__ void stage_x(const FewArgs& a, unsigned char* smem, f
         s += (b0.x + b0.y) + (b2.x + b2.y);
         s16 += (b1.x + b1.y) + (b3.x + b3.y);
       }
-      sums[i] = fmaf(16.f, s16, s);
+      // what a block's sum starts from, in its unit of 2^-24: minus z x, z = 8 where the
+      // zero points are not given
+      sums[i] = fmaf(16.f, s16, s) * (K::kZeros ? -1.f : -8.f) * 0x1p-24f;
     }
     __syncthreads();
   }
 }
 
-template <typename K, int MT>
+template <typename K>
 __global__ void __launch_bounds__(kFewThreads, 1) few_ffn_kernel(const __grid_constant__ FewArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float x_inverse[kFewMaxT], zero_w[kFewMaxT];
@@ -945,14 +984,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_ffn_kernel(const __grid_co
   const bool shared = a.Is > 0;
   FewTiles n;
   n.units = __ldcg(&a.head->units);
-  n.routed = (a.I + 8 * MT - 1) / (8 * MT);
-  n.shared = shared ? (a.Is + 8 * MT - 1) / (8 * MT) : 0;
+  n.routed = a.I / 8;
+  n.shared = a.Is / 8;
   n.total = n.units * n.routed + n.shared;
   for (int i = tid; i < (n.units + shared) * (kFewUnitBytes / 4); i += kFewThreads)
     reinterpret_cast<uint32_t*>(units)[i] = __ldcg(reinterpret_cast<const uint32_t*>(a.head->unit) + i);
   if (tid < kFewMaxT) zero_w[tid] = __ldcg(&a.head->zero_w[tid]);
   __syncthreads();
-  gate_up<K, MT>(a, smem, units, n, x_inverse);
+  gate_up<K>(a, smem, units, n, x_inverse);
   __syncthreads();
   pdl_trigger();
   down<K>(a, smem, units, n, shared, zero_w);
@@ -973,20 +1012,28 @@ void launch_route(const Launch& L, const RouteArgs& r) {
   launch_end(L, MOE_K_FEW_ROUTE);
 }
 
-template <typename K, int MT>
-void launch_ffn_as(const Launch& L, const FewArgs& a, int slot) {
-  set_smem_attr_once(reinterpret_cast<const void*>(few_ffn_kernel<K, MT>), kFewSmem,
-                     kAttrFewFfn + 2 * slot + MT - 1);
+template <typename K>
+void launch_ffn(const Launch& L, const FewArgs& a, int slot) {
+  set_smem_attr_once(reinterpret_cast<const void*>(few_ffn_kernel<K>), kFewSmem, kAttrFewFfn + slot);
   launch_begin(L, MOE_K_FEW_FFN);
-  launch_kernel(few_ffn_kernel<K, MT>, dim3(L.num_sms), dim3(kFewThreads), a.p.bytes, L.stream, a);
+  launch_kernel(few_ffn_kernel<K>, dim3(L.num_sms), dim3(kFewThreads), a.p.bytes, L.stream, a);
   launch_end(L, MOE_K_FEW_FFN);
 }
-template <typename K>
-void launch_ffn(const Launch& L, const FewArgs& a, int mt, int slot) {
-  if (mt == 1)
-    launch_ffn_as<K, 1>(L, a, slot);
+template <int BLOCK, bool ZEROS>
+void launch_four_as(const Launch& L, const FewArgs& a, int slot) {
+  if (a.scale_dtype == MOE_DT_BF16)
+    launch_ffn<Four<BLOCK, ZEROS, __nv_bfloat16>>(L, a, slot);
+  else if (a.scale_dtype == MOE_DT_FP16)
+    launch_ffn<Four<BLOCK, ZEROS, __half>>(L, a, slot + 1);
   else
-    launch_ffn_as<K, 2>(L, a, slot);
+    launch_ffn<Four<BLOCK, ZEROS, float>>(L, a, slot + 2);
+}
+template <int BLOCK>
+void launch_four(const Launch& L, const FewArgs& a, bool zeros, int slot) {
+  if (zeros)
+    launch_four_as<BLOCK, true>(L, a, slot);
+  else
+    launch_four_as<BLOCK, false>(L, a, slot + 3);
 }
 
 struct FewLayout {
@@ -1004,10 +1051,6 @@ FewLayout few_layout(const moe_config& c, int T) {
   l.total = l.h + up((size_t)units * T * std::max(c.inter, c.shared_inter) * 4);
   return l;
 }
-
-// Gate/up tiles of 8 channels where few tokens leave few tiles; of 16, which read x
-// once for twice the weights, otherwise.
-int few_tiles(int T) { return T <= 2 ? 1 : 2; }
 
 moe_status check_few(const moe_config* c, int T) {
   // the layer's own checks of the description; the batch's limits are this file's
@@ -1087,11 +1130,8 @@ extern "C" moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weight
 
   FewArgs a{};
   const int units = std::min(c.n_routed, T * c.top_k) + (c.shared_inter > 0);
-  int mt = few_tiles(T);
   const int es = wt->scale_dtype == MOE_DT_FP32 ? 4 : 2;
-  a.p = few_plan(T, c.hidden, units, four, wt->group, es, zeros, aligned_s, aligned_z, mt);
-  if (a.p.stages < 3 && mt > 1)
-    a.p = few_plan(T, c.hidden, units, four, wt->group, es, zeros, aligned_s, aligned_z, mt = 1);
+  a.p = few_plan(T, c.hidden, units, four, wt->group, es, zeros, aligned_s, aligned_z);
   if (a.p.stages < 2) return MOE_ERR_UNSUPPORTED;
   Launch L;
   const moe_status s = open_launch(stream, &L);
@@ -1139,6 +1179,7 @@ extern "C" moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weight
   a.vec = r.vec;
   a.group = four ? wt->group : 0;
   a.scale_dtype = four ? wt->scale_dtype : MOE_DT_FP32;
+  a.zstep = a.group ? a.p.step_k / a.group : 0;
 
   if (T == 1)
     launch_route<1>(L, r);
@@ -1148,17 +1189,15 @@ extern "C" moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weight
     launch_route<4>(L, r);
   else
     launch_route<8>(L, r);
-  if (!four) {
-    if (a.fp16)
-      launch_ffn<Sixteen<__half>>(L, a, mt, 0);
-    else
-      launch_ffn<Sixteen<__nv_bfloat16>>(L, a, mt, 1);
-  } else if (a.p.block == 32) {
-    zeros ? launch_ffn<Four<32, true>>(L, a, mt, 2) : launch_ffn<Four<32, false>>(L, a, mt, 3);
-  } else if (a.p.block == 64) {
-    zeros ? launch_ffn<Four<64, true>>(L, a, mt, 4) : launch_ffn<Four<64, false>>(L, a, mt, 5);
-  } else {
-    zeros ? launch_ffn<Four<128, true>>(L, a, mt, 6) : launch_ffn<Four<128, false>>(L, a, mt, 7);
-  }
+  if (!four && a.fp16)
+    launch_ffn<Sixteen<__half>>(L, a, 0);
+  else if (!four)
+    launch_ffn<Sixteen<__nv_bfloat16>>(L, a, 1);
+  else if (a.p.block == 32)
+    launch_four<32>(L, a, zeros, 2);
+  else if (a.p.block == 64)
+    launch_four<64>(L, a, zeros, 8);
+  else
+    launch_four<128>(L, a, zeros, 14);
   return launch_status_take();
 }
