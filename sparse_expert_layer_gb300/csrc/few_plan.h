@@ -11,7 +11,7 @@ constexpr int kFewWarps = 16;
 constexpr int kFewTeamWarps = 4;  // warps that share the K of one gate/up tile
 constexpr int kFewTeams = kFewWarps / kFewTeamWarps;
 constexpr int kFewSub = 2048;     // bytes of the weights of a ring stage: 16 rows of 128
-constexpr int kFewMaxStages = 4;
+constexpr int kFewMaxStages = 3;
 constexpr int kFewSmem = 226 * 1024;  // dynamic; the kernel has a few words besides
 constexpr int kFewUnitBytes = 40;
 
@@ -22,7 +22,10 @@ struct FewPlan {
   int block;           // K that shares a scale: 32, 64 or 128
   int sum_at, unit_at, red_at, queue_at, ring_at;
   int swords, zwords;  // 4-byte words of scales and zero points a row has in a stage
-  int sub_bytes;       // of a stage
+  int s_eight, z_eight;  // bytes from a row's groups to those eight rows on
+  int s_next, z_next;    // bytes from a block's scale (zero point) to the next one's, or 0
+  int whole;             // rows are whole stages, so a stage's scales are aligned copies
+  int sub_bytes;         // of a stage
   int stages;
   int bytes;           // of the CTA; stages < 2: does not fit
 };
@@ -39,7 +42,7 @@ inline int few_words(int n, int size, int64_t row) {
 // group: 0 (a row), 32, 64, 128; rows_aligned: every row's scales (zero points) begin at a
 // multiple of four bytes
 inline FewPlan few_plan(int T, int H, int units, bool four_bits, int group, int scale_bytes,
-                        bool zeros, bool rows_aligned_scales, bool rows_aligned_zeros) {
+                        bool zeros, bool rows_aligned_scales, bool rows_aligned_zeros, bool whole) {
   FewPlan p{};
   p.step_k = four_bits ? 256 : 64;
   p.block = four_bits ? (group ? group : 128) : 0;
@@ -56,6 +59,11 @@ inline FewPlan few_plan(int T, int H, int units, bool four_bits, int group, int 
     const int n = group ? p.step_k / group : 1;
     p.swords = few_words(n, scale_bytes, rows_aligned_scales ? 4 : scale_bytes);
     p.zwords = zeros ? few_words(n, 1, rows_aligned_zeros ? 4 : 1) : 0;
+    p.s_eight = 32 * p.swords;
+    p.z_eight = 32 * p.zwords;
+    p.s_next = group ? scale_bytes : 0;
+    p.z_next = group ? 1 : 0;
+    p.whole = whole;
     p.sub_bytes += few_round(16 * 4 * (p.swords + p.zwords), 16);
   }
   p.stages = std::min(kFewMaxStages, (kFewSmem - p.ring_at) / (kFewWarps * p.sub_bytes));

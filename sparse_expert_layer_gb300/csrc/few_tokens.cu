@@ -299,14 +299,12 @@ __device__ __forceinline__ void team_barrier(int team) {
 }
 // All but the `stages - 2` groups committed last have arrived.
 __device__ __forceinline__ void wait_stage(int stages) {
-  if (stages == 4)
-    cp_async_wait<2>();
-  else if (stages == 3)
+  if (stages == 3)
     cp_async_wait<1>();
   else
     cp_async_wait<0>();
 }
-static_assert(kFewMaxStages == 4, "wait_stage knows up to four");
+static_assert(kFewMaxStages == 3, "wait_stage knows two and three");
 
 template <typename T>
 __device__ __forceinline__ float read_scale(uint32_t at) {
@@ -384,29 +382,32 @@ struct Sixteen {
   static __device__ __forceinline__ int swizzle(int r, int c) { return c ^ ((r & 1) << 2); }
 };
 
-// Where a lane finds the groups of its rows g and g + 8 in a stage: their offset from the
-// stage, with the byte of the first group inside its word.  (Eight rows further on that byte
-// is the same.)
+// Where a lane finds the groups of its row g in a stage (row g + 8: `eight` bytes on; the
+// byte inside the first word is the same there).
 struct FewGroups {
-  uint32_t s;  // scales of row g
-  uint32_t z;  // zero points of row g, less the byte
+  uint32_t s;  // scales
+  uint32_t z;  // zero points, less the byte inside their first word
   uint32_t zbyte;
 };
 
 // acc += the sum over a stage's K of its 16 rows times b: 2^-24 of it with 4-bit weights.
 // xs: minus 8 x 2^-24 times the sums of x over the stage's blocks (with zero points: minus
-// 2^-24 times them), for the lane's columns 2 tg and 2 tg + 1.
-template <typename K>
+// 2^-24 times them), for the lane's columns 2 tg and 2 tg + 1.  row: the stage and the lane's
+// row g in it.
+template <typename K, bool REST>
 __device__ __forceinline__ void multiply(uint32_t st, const uint32_t (&b)[K::kWords][4],
-                                         const uint32_t (&rest)[K::kRest ? K::kWords : 1][4],
-                                         const float2 (&xs)[K::kBlocks], bool with_rest,
-                                         const FewArgs& a, const FewGroups& at, int step,
-                                         float (&acc)[4]) {
+                                         const uint32_t (&rest)[REST ? K::kWords : 1][4],
+                                         const float2 (&xs)[K::kBlocks], const FewArgs& a,
+                                         const FewGroups& at, int step, float (&acc)[4]) {
   const int lane = threadIdx.x % 32, g = lane / 4, tg = lane % 4;
   const uint32_t row = st + g * 128;
   if constexpr (K::kFour) {
-    const uint32_t s0 = st + at.s, s8 = s0 + 32 * a.p.swords;
-    const uint32_t z0 = st + at.z + ((at.zbyte + step * a.zstep) & 3u), z8 = z0 + 32 * a.p.zwords;
+    const uint32_t s0 = st + at.s, s8 = s0 + a.p.s_eight;
+    uint32_t z0 = 0, z8 = 0;
+    if constexpr (K::kZeros) {
+      z0 = st + at.z + ((at.zbyte + step * a.zstep) & 3u);
+      z8 = z0 + a.p.z_eight;
+    }
 #pragma unroll
     for (int blk = 0; blk < K::kBlocks; ++blk) {
       uint32_t lo[K::kPer], hi[K::kPer];
@@ -425,12 +426,15 @@ __device__ __forceinline__ void multiply(uint32_t st, const uint32_t (&b)[K::kWo
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(lo[0]) : "r"(from) : "memory");
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(hi[0]) : "r"(from + 8 * 128) : "memory");
       }
-      const int j = a.group ? blk : 0;
+      // (one scale for the whole row: every block reads the first)
+      const uint32_t js = blk * a.p.s_next, jz = blk * a.p.z_next;
       float c0 = xs[blk].x, c1 = xs[blk].y, c2 = c0, c3 = c1;
       if constexpr (K::kZeros) {
-        const float za = read_zero(z0 + j), zb = read_zero(z8 + j);
+        const float za = read_zero(z0 + jz), zb = read_zero(z8 + jz);
         c2 = c0 * zb, c3 = c1 * zb, c0 *= za, c1 *= za;
       }
+      const float sa = read_scale<typename K::Scale>(s0 + js);
+      const float sb = read_scale<typename K::Scale>(s8 + js);
       float d[4];
 #pragma unroll
       for (int i = 0; i < K::kPer; ++i) {
@@ -445,8 +449,6 @@ __device__ __forceinline__ void multiply(uint32_t st, const uint32_t (&b)[K::kWo
         mma16816<__half>(d, l8 & 0x000f000fu, h8 & 0x000f000fu, l8 & 0x00f000f0u,
                          h8 & 0x00f000f0u, b[w][2], b[w][3]);
       }
-      const float sa = read_scale<typename K::Scale>(s0 + j * K::kScaleBytes);
-      const float sb = read_scale<typename K::Scale>(s8 + j * K::kScaleBytes);
       acc[0] = fmaf(sa, d[0], acc[0]);
       acc[1] = fmaf(sa, d[1], acc[1]);
       acc[2] = fmaf(sb, d[2], acc[2]);
@@ -459,7 +461,7 @@ __device__ __forceinline__ void multiply(uint32_t st, const uint32_t (&b)[K::kWo
       const uint4 u = lds128(from), v = lds128(from + 8 * 128);
       mma16816<typename K::Mma>(acc, u.x, v.x, u.y, v.y, b[i][0], b[i][1]);
       mma16816<typename K::Mma>(acc, u.z, v.z, u.w, v.w, b[i][2], b[i][3]);
-      if (with_rest) {
+      if constexpr (REST) {
         mma16816<typename K::Mma>(acc, u.x, v.x, u.y, v.y, rest[i][0], rest[i][1]);
         mma16816<typename K::Mma>(acc, u.z, v.z, u.w, v.w, rest[i][2], rest[i][3]);
       }
@@ -481,12 +483,12 @@ __device__ __forceinline__ FewShape shape_of(const FewArgs& a, int k) {
   return s;
 }
 
-// The scales and zero points of a stage's row lane / 2, whose groups begin at sp and zp:
-// words lane % 2, + 2, .. of each, up to the row's end.
+// The scales and zero points of a stage's row lane / 2, whose groups begin at sp and zp.
+// Where all rows are whole stages (a.p.whole) the scales of a stage are one aligned copy (or
+// two); otherwise words lane % 2, + 2, .. of each, up to the row's end.
 template <typename K>
-__device__ __forceinline__ void copy_groups(const FewArgs& a, const FewShape& sh, uint32_t st,
-                                            int step, const unsigned char* sp,
-                                            const unsigned char* zp) {
+__device__ __forceinline__ void copy_groups(const FewArgs& a, int groups, uint32_t st, int step,
+                                            const unsigned char* sp, const unsigned char* zp) {
   const int lane = threadIdx.x % 32;
   auto words = [&](const unsigned char* row, int first, int end, int n, uint32_t dst) {
     const uint32_t byte = (uint32_t)(reinterpret_cast<uintptr_t>(row + first) & 3u);
@@ -497,9 +499,27 @@ __device__ __forceinline__ void copy_groups(const FewArgs& a, const FewShape& sh
     for (int i = lane % 2; i < n; i += 2, from += 8, left -= 8, dst += 8)
       cp_async_word(dst, left > 0 ? from : first_word, max(0, min(4, left)));
   };
-  words(sp, step * a.zstep * K::kScaleBytes, sh.groups * K::kScaleBytes, a.p.swords, st + kFewSub);
-  if constexpr (K::kZeros)
-    words(zp, step * a.zstep, sh.groups, a.p.zwords, st + kFewSub + 64 * a.p.swords);
+  constexpr int kRun = K::kBlocks * K::kScaleBytes;  // of a row
+  if (a.p.whole) {
+    const unsigned char* from = sp + step * kRun;
+    const uint32_t dst = st + kFewSub + lane / 2 * kRun;
+    if constexpr (kRun == 32) {
+      cp_async16(dst + lane % 2 * 16, from + lane % 2 * 16);
+    } else if (lane % 2 == 0) {
+      cp_async_unit(dst, from, kRun);
+    }
+  } else {
+    words(sp, step * a.zstep * K::kScaleBytes, groups * K::kScaleBytes, a.p.swords, st + kFewSub);
+  }
+  if constexpr (K::kZeros) {
+    if (a.p.whole && K::kBlocks >= 4) {
+      if (lane % 2 == 0)
+        cp_async_unit(st + kFewSub + 64 * a.p.swords + lane / 2 * K::kBlocks, zp + step * K::kBlocks,
+                      K::kBlocks);
+    } else {
+      words(zp, step * a.zstep, groups, a.p.zwords, st + kFewSub + 64 * a.p.swords);
+    }
+  }
 }
 template <typename K>
 __device__ __forceinline__ FewGroups groups_at(const FewArgs& a, const FewShape& sh, int64_t row) {
@@ -551,64 +571,64 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, c
   }
   team_barrier(team);
 
-  // What is copied next: stage `step` of tile queue[seq].  gate, up: the lane's piece of rows
-  // lane / 8 of both, 4 rows more for the second; left: bytes from there to the rows' end.
-  struct {
-    int seq, step, left;
-    bool fresh, done;
-    const unsigned char *gate, *up, *s, *z;
-  } next{0, k0, 0, true, k0 == k1, nullptr, nullptr, nullptr, nullptr};
-  const int dst = lane / 8 * 128, four_rows = 4 * sh.row;
-  const int d0 = dst + K::swizzle(lane / 8, lane % 8) * 16;
-  const int d1 = dst + 4 * 128 + K::swizzle(lane / 8 + 4, lane % 8) * 16;
-  uint32_t fill = ring;
-  const uint32_t ring_end = ring + S * sub;
-  auto issue = [&]() {
-    if (!next.done && next.fresh) {
-      const int tile = queue[next.seq % 16];
-      next.done = tile >= n.total;
-      if (!next.done) {
+  // What is copied next: the tile of queue[seq], `togo` stages of it.  The lane copies its
+  // piece of rows lane / 8 and four on of both matrices, and groups of row lane / 2.
+  int seq_next = 0, togo = 0, step_next = 0, left = 0;
+  bool done = k0 == k1;
+  const unsigned char *gate0 = nullptr, *gate1 = nullptr, *up0 = nullptr, *up1 = nullptr;
+  const unsigned char *sp = nullptr, *zp = nullptr;
+  const int dst = lane / 8 * 128;
+  const uint32_t d0 = dst + K::swizzle(lane / 8, lane % 8) * 16;
+  const uint32_t d1 = dst + 4 * 128 + K::swizzle(lane / 8 + 4, lane % 8) * 16;
+  const uint32_t ring_last = ring + (S - 1) * sub;
+  auto issue = [&](uint32_t slot) {
+    if (togo == 0 && !done) {
+      const int tile = queue[seq_next++ % 16];
+      done = tile >= n.total;
+      if (!done) {
         int u, f;
         tile_at(n, tile, &u, &f);
         const int e = units[u].expert;
         const FewMatrix* m = e < 0 ? a.shared : a.m;
         const int64_t row = (e < 0 ? 0 : (int64_t)e * a.I) + f * 8;
         const int64_t at = (row + lane / 8) * sh.row + k0 * 128 + (lane % 8) * 16;
-        next.gate = m[0].w + at;
-        next.up = m[1].w + at;
-        next.left = sh.row - k0 * 128 - (lane % 8) * 16;
+        gate0 = m[0].w + at;
+        gate1 = gate0 + 4 * sh.row;
+        up0 = m[1].w + at;
+        up1 = up0 + 4 * sh.row;
+        left = sh.row - k0 * 128 - (lane % 8) * 16;
         if constexpr (K::kFour) {
           const int64_t first = (row + lane / 2 % 8) * sh.groups;  // rows 0-7 are gate's
-          next.s = (lane < 16 ? m[0].s : m[1].s) + first * K::kScaleBytes;
-          if constexpr (K::kZeros) next.z = (lane < 16 ? m[0].z : m[1].z) + first;
+          sp = (lane < 16 ? m[0].s : m[1].s) + first * K::kScaleBytes;
+          if constexpr (K::kZeros) zp = (lane < 16 ? m[0].z : m[1].z) + first;
         }
-        next.fresh = false;
+        togo = k1 - k0;
+        step_next = k0;
       }
     }
-    if (!next.done) {
-      const bool in = next.left > 0;
-      copy_piece<K::kFour>(fill + d0, next.gate, in, a.x);
-      copy_piece<K::kFour>(fill + d1, next.gate + four_rows, in, a.x);
-      copy_piece<K::kFour>(fill + d0 + 8 * 128, next.up, in, a.x);
-      copy_piece<K::kFour>(fill + d1 + 8 * 128, next.up + four_rows, in, a.x);
-      if constexpr (K::kFour) copy_groups<K>(a, sh, fill, next.step, next.s, next.z);
-      next.gate += 128;
-      next.up += 128;
-      next.left -= 128;
-      if (++next.step == k1) {
-        next.step = k0;
-        ++next.seq;
-        next.fresh = true;
-      }
+    if (togo) {
+      const bool in = left > 0;
+      copy_piece<K::kFour>(slot + d0, gate0, in, a.x);
+      copy_piece<K::kFour>(slot + d1, gate1, in, a.x);
+      copy_piece<K::kFour>(slot + d0 + 8 * 128, up0, in, a.x);
+      copy_piece<K::kFour>(slot + d1 + 8 * 128, up1, in, a.x);
+      if constexpr (K::kFour) copy_groups<K>(a, sh.groups, slot, step_next, sp, zp);
+      gate0 += 128;
+      gate1 += 128;
+      up0 += 128;
+      up1 += 128;
+      left -= 128;
+      ++step_next;
+      --togo;
     }
     cp_async_commit();
-    fill = fill + sub == ring_end ? ring : fill + sub;
   };
-  for (int i = 0; i < S - 1; ++i) issue();
+  for (int i = 0; i < S - 1; ++i) issue(ring + i * sub);
 
-  uint32_t use = ring;
-  const uint32_t xrow = smem_u32(smem) + min(g, a.T - 1) * a.p.xpitch + tg * 16;
-  const uint32_t sums = smem_u32(smem) + a.p.sum_at + tg * 8;
+  uint32_t use = ring, before = ring_last;  // the stage to be used, the one used last
+  const uint32_t x0 = smem_u32(smem) + min(g, a.T - 1) * a.p.xpitch + tg * 16 +
+                      k0 * (K::kStepK * 2);
+  const uint32_t sum0 = smem_u32(smem) + a.p.sum_at + tg * 8 + k0 * (K::kBlocks * kFewMaxT * 4);
   for (int seq = 0;; ++seq) {
     const int tile = queue[seq % 16];
     if (tile >= n.total) break;
@@ -619,28 +639,32 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, c
     const int e = units[u].expert;
     const FewGroups at = groups_at<K>(a, sh, (e < 0 ? 0 : (int64_t)e * a.I) + f * 8 + g);
     float acc[4] = {};
+    uint32_t xat = x0, sum_at = sum0;
     for (int step = k0; step < k1; ++step) {
       wait_stage(S);
       __syncwarp();
-      issue();
+      issue(before);
       uint32_t b[K::kWords][4];
       float2 xs[K::kBlocks];
 #pragma unroll
       for (int i = 0; i < K::kWords; ++i) {
-        const uint4 v = lds128(xrow + (step * (K::kStepK / 8) + K::piece(i, 0)) * 16);
+        const uint4 v = lds128(xat + K::piece(i, 0) * 16);
         b[i][0] = v.x, b[i][1] = v.y, b[i][2] = v.z, b[i][3] = v.w;
       }
+      xat += K::kStepK * 2;
       if constexpr (K::kFour) {
 #pragma unroll
         for (int i = 0; i < K::kBlocks; ++i)
           asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
                        : "=f"(xs[i].x), "=f"(xs[i].y)
-                       : "r"(sums + (step * K::kBlocks + i) * kFewMaxT * 4)
+                       : "r"(sum_at + i * kFewMaxT * 4)
                        : "memory");
+        sum_at += K::kBlocks * kFewMaxT * 4;
       }
-      const uint32_t none[K::kRest ? K::kWords : 1][4] = {};
-      multiply<K>(use, b, none, xs, false, a, at, step, acc);
-      use = use + sub == ring_end ? ring : use + sub;
+      const uint32_t none[1][4] = {};
+      multiply<K, false>(use, b, none, xs, a, at, step, acc);
+      before = use;
+      use = use == ring_last ? ring : use + sub;
     }
     float* r = red + kw * 128 + g * 8 + 2 * tg;
     *reinterpret_cast<float2*>(r) = make_float2(acc[0], acc[1]);
@@ -690,77 +714,77 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
   const int g = lane / 4, tg = lane % 4;
   const FewShape rs = shape_of<K>(a, a.I), ss = shape_of<K>(a, a.Is);
   const int S = a.p.stages, sub = a.p.sub_bytes;
-  const uint32_t ring = smem_u32(smem) + a.p.ring_at + warp * S * sub, ring_end = ring + S * sub;
+  const uint32_t ring = smem_u32(smem) + a.p.ring_at + warp * S * sub;
+  const uint32_t ring_last = ring + (S - 1) * sub;
   float* sums = reinterpret_cast<float*>(smem + a.p.ring_at);
   const int share = (a.H + gridDim.x - 1) / gridDim.x;
   const int c_begin = min(a.H, (int)blockIdx.x * share), c_end = min(a.H, c_begin + share);
   const int routed = n.units * rs.steps, flat = routed + (shared ? ss.steps : 0);
   const int f0 = (int)((int64_t)flat * warp / kFewWarps);
   const int f1 = (int)((int64_t)flat * (warp + 1) / kFewWarps);
+  const int u0 = f0 < routed ? f0 / max(1, rs.steps) : n.units;
   const int dst = lane / 8 * 128;
-  const int d0 = dst + K::swizzle(lane / 8, lane % 8) * 16;
-  const int d1 = dst + 4 * 128 + K::swizzle(lane / 8 + 4, lane % 8) * 16;
+  const uint32_t d0 = dst + K::swizzle(lane / 8, lane % 8) * 16;
+  const uint32_t d1 = dst + 4 * 128 + K::swizzle(lane / 8 + 4, lane % 8) * 16;
   bool waited = false;
 
   for (int c0 = c_begin; c0 < c_end; c0 += 16 * kFewDownTiles) {
     const int channels = min(c_end - c0, 16 * kFewDownTiles);
     const int tiles = (channels + 15) / 16;
-    // What is copied next: tile m of step `step` of unit u.
-    struct {
-      int f, u, step, m, steps;
-      const FewShape* sh;
-      const unsigned char *w, *s, *z;  // the lane's piece of the first row, its row's groups
-    } next{f0, f0 < routed ? f0 / max(1, rs.steps) : n.units, 0, 0, 0, &rs, nullptr, nullptr,
-           nullptr};
-    next.step = f0 - next.u * rs.steps;
-    auto enter = [&]() {  // a unit's pointers
-      const int e = units[next.u].expert;
+    // What is copied next: tile m of step next_step of unit next_u; the lane's piece of the
+    // tile's row lane / 8, and the groups of the range's row lane / 2.
+    int togo = f1 - f0, next_u = u0, next_step = f0 - u0 * rs.steps, m_next = 0;
+    int next_steps = 0, next_groups = 0, next_row = 0;
+    const unsigned char *w = nullptr, *sp = nullptr, *zp = nullptr;
+    int64_t four = 0;  // bytes of four rows
+    auto enter = [&]() {
+      const int e = units[next_u].expert;
       const FewMatrix& m = e < 0 ? a.shared[2] : a.m[2];
-      next.sh = e < 0 ? &ss : &rs;
-      next.steps = next.sh->steps;
+      next_steps = e < 0 ? ss.steps : rs.steps;
+      next_groups = e < 0 ? ss.groups : rs.groups;
+      next_row = e < 0 ? ss.row : rs.row;
+      four = 4 * (int64_t)next_row;
       const int64_t first = (e < 0 ? 0 : (int64_t)e * a.H) + c0;
-      next.w = m.w + (first + lane / 8) * next.sh->row + (lane % 8) * 16;
+      w = m.w + (first + lane / 8) * next_row + next_step * 128 + (lane % 8) * 16;
       if constexpr (K::kFour) {
-        const int64_t groups = (first + lane / 2) * next.sh->groups;
-        next.s = m.s + groups * K::kScaleBytes;
-        if constexpr (K::kZeros) next.z = m.z + groups;
+        const int64_t groups = (first + lane / 2) * next_groups;
+        sp = m.s + groups * K::kScaleBytes;
+        if constexpr (K::kZeros) zp = m.z + groups;
       }
     };
-    if (f0 < f1) enter();
-    uint32_t fill = ring, use = ring;
-    auto issue = [&]() {
-      if (next.f < f1) {
-        const FewShape& sh = *next.sh;
-        const int byte = next.step * 128;
+    if (togo) enter();
+    auto issue = [&](uint32_t slot) {
+      if (togo) {
         // rows past the range are not stored, whatever they hold
-        const int rows = byte + (lane % 8) * 16 < sh.row ? channels - next.m * 16 - lane / 8 : 0;
-        const unsigned char* w = next.w + (int64_t)next.m * 16 * sh.row + byte;
-        const int64_t four = 4 * (int64_t)sh.row;
-        copy_piece<K::kFour>(fill + d0, w, rows > 0, a.x);
-        copy_piece<K::kFour>(fill + d1, w + four, rows > 4, a.x);
-        copy_piece<K::kFour>(fill + d0 + 8 * 128, w + 2 * four, rows > 8, a.x);
-        copy_piece<K::kFour>(fill + d1 + 8 * 128, w + 3 * four, rows > 12, a.x);
+        int rows = channels - m_next * 16 - lane / 8;
+        if (next_step * 128 + (lane % 8) * 16 >= next_row) rows = 0;
+        copy_piece<K::kFour>(slot + d0, w, rows > 0, a.x);
+        copy_piece<K::kFour>(slot + d1, w + four, rows > 4, a.x);
+        copy_piece<K::kFour>(slot + d0 + 8 * 128, w + 2 * four, rows > 8, a.x);
+        copy_piece<K::kFour>(slot + d1 + 8 * 128, w + 3 * four, rows > 12, a.x);
         if constexpr (K::kFour) {
           // (a row past the range takes the last one's)
-          const int r = min(next.m * 16, channels - 1 - lane / 2) * sh.groups;
+          const int r = min(m_next * 16, channels - 1 - lane / 2) * next_groups;
           const unsigned char* z = nullptr;
-          if constexpr (K::kZeros) z = next.z + r;
-          copy_groups<K>(a, sh, fill, next.step, next.s + r * K::kScaleBytes, z);
+          if constexpr (K::kZeros) z = zp + r;
+          copy_groups<K>(a, next_groups, slot, next_step, sp + r * K::kScaleBytes, z);
         }
-        if (++next.m == tiles) {
-          next.m = 0;
-          ++next.f;
-          if (++next.step == next.steps) {
-            next.step = 0;
-            ++next.u;
-            if (next.f < f1) enter();
+        w += 4 * four;
+        if (++m_next == tiles) {
+          w += 128 - tiles * 4 * four;
+          m_next = 0;
+          --togo;
+          if (++next_step == next_steps) {
+            next_step = 0;
+            ++next_u;
+            if (togo) enter();
           }
         }
       }
       cp_async_commit();
-      fill = fill + sub == ring_end ? ring : fill + sub;
     };
-    for (int i = 0; i < S - 1; ++i) issue();
+    for (int i = 0; i < S - 1; ++i) issue(ring + i * sub);
+    uint32_t use = ring, before = ring_last;
     if (!waited) {
       // every tile's h is stored (bounded: a tile belongs to a running team)
       if (tid == 0 && !wait_rows_done(&a.head->done, n.total))
@@ -772,9 +796,8 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
     float acc[kFewDownTiles][4] = {}, total[kFewDownTiles][4] = {};
     float w0 = 0.f, w1 = 0.f, up = 1.f;
     const float* hrow = nullptr;
-    FewGroups at[kFewDownTiles];
-    int u = f0 < routed ? f0 / max(1, rs.steps) : n.units;
-    int step = f0 - u * rs.steps, steps = 0, kmax = 0;
+    FewGroups at{};  // of every tile: sixteen rows on, groups lie alike
+    int u = u0, step = f0 - u0 * rs.steps, steps = 0, kmax = 0;
     auto flush = [&]() {
 #pragma unroll
       for (int m = 0; m < kFewDownTiles; ++m) {
@@ -805,11 +828,7 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
           w0 *= inverse_pow2(fp16_range_bits(__ldcg(&a.head->hmax[u][2 * tg])));
           w1 *= inverse_pow2(fp16_range_bits(__ldcg(&a.head->hmax[u][2 * tg + 1])));
         }
-        if constexpr (K::kFour) {
-#pragma unroll
-          for (int m = 0; m < kFewDownTiles; ++m)
-            at[m] = groups_at<K>(a, sh, (e < 0 ? 0 : (int64_t)e * a.H) + c0 + m * 16 + g);
-        }
+        at = groups_at<K>(a, sh, (e < 0 ? 0 : (int64_t)e * a.H) + c0 + g);
       }
       // the lane's h of this step, as MMA operands
       uint32_t b[K::kWords][4], rest[K::kRest ? K::kWords : 1][4];
@@ -854,9 +873,10 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
         if (m >= tiles) break;
         wait_stage(S);
         __syncwarp();
-        issue();
-        multiply<K>(use, b, rest, xs, true, a, at[m], step, acc[m]);
-        use = use + sub == ring_end ? ring : use + sub;
+        issue(before);
+        multiply<K, K::kRest>(use, b, rest, xs, a, at, step, acc[m]);
+        before = use;
+        use = use == ring_last ? ring : use + sub;
       }
       ++step;
     }
@@ -1089,7 +1109,7 @@ extern "C" moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weight
   const bool any = c.n_routed > 0 || c.shared_inter > 0;  // weights at all
   const bool four = any && wt->w_dtype == MOE_DT_U4;
   if (any && !four && wt->w_dtype != dtype) return MOE_ERR_INVALID_ARG;
-  bool aligned_s = true, aligned_z = true, zeros = false;
+  bool aligned_s = true, aligned_z = true, whole = true, zeros = false;
   if (four) {
     const int group = wt->group;
     if (group != 0 && group != 32 && group != 64 && group != 128) return MOE_ERR_INVALID_ARG;
@@ -1101,6 +1121,7 @@ extern "C" moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weight
       const int groups = group > 0 ? k / group : 1;
       aligned_s = aligned_s && (k == 0 || groups * es % 4 == 0);
       aligned_z = aligned_z && (k == 0 || groups % 4 == 0);
+      whole = whole && group > 0 && k % 256 == 0;
     }
   }
   const moe_few_expert* part[2] = {&wt->routed, &wt->shared};
@@ -1131,7 +1152,7 @@ extern "C" moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weight
   FewArgs a{};
   const int units = std::min(c.n_routed, T * c.top_k) + (c.shared_inter > 0);
   const int es = wt->scale_dtype == MOE_DT_FP32 ? 4 : 2;
-  a.p = few_plan(T, c.hidden, units, four, wt->group, es, zeros, aligned_s, aligned_z);
+  a.p = few_plan(T, c.hidden, units, four, wt->group, es, zeros, aligned_s, aligned_z, whole);
   if (a.p.stages < 2) return MOE_ERR_UNSUPPORTED;
   Launch L;
   const moe_status s = open_launch(stream, &L);
