@@ -11,9 +11,9 @@ constexpr int kFewWarps = 16;
 constexpr int kFewTeamWarps = 4;  // warps that share the K of one gate/up tile
 constexpr int kFewTeams = kFewWarps / kFewTeamWarps;
 constexpr int kFewSub = 2048;     // bytes of the weights of a ring stage: 16 rows of 128
-constexpr int kFewMaxStages = 3;
+constexpr int kFewMaxStages = 6;
 constexpr int kFewSmem = 226 * 1024;  // dynamic; the kernel has a few words besides
-constexpr int kFewUnitBytes = 40;
+constexpr int kFewUnitBytes = 8;
 
 // Layout of a CTA's shared memory: x, its block sums, units, parts, rings.
 struct FewPlan {
@@ -52,7 +52,7 @@ inline FewPlan few_plan(int T, int H, int units, bool four_bits, int group, int 
   const int blocks = four_bits ? few_round(H, p.step_k) / p.block : 0;
   p.unit_at = p.sum_at + blocks * kFewMaxT * 4;
   p.red_at = few_round(p.unit_at + units * kFewUnitBytes, 16);
-  p.queue_at = p.red_at + kFewTeams * kFewTeamWarps * 16 * 8 * 4;
+  p.queue_at = p.red_at + 2 * kFewTeams * kFewTeamWarps * 16 * 8 * 4;
   p.ring_at = few_round(p.queue_at + kFewTeams * 16 * 4, 128);
   p.sub_bytes = kFewSub;
   if (four_bits) {

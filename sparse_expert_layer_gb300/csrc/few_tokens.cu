@@ -40,18 +40,16 @@ namespace moe {
 namespace {
 
 constexpr int kFewThreads = 32 * kFewWarps;
-constexpr int kRouteThreads = 256;
+constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kFewMaxPicks = kFewMaxT * 32;
 constexpr int kFewMaxTH = 65536;           // tokens x hidden
 constexpr int kRouteScratch = 96 * 1024;   // top-k scratch in shared memory, at most
-constexpr int kRouteSmem = 212 * 1024;     // eight rows for five tokens of kFewMaxTH / 5
 
 // One expert with rows (expert -1: the shared one).
 struct FewUnit {
   int expert;
-  uint32_t tokens;    // bit t: token t picked it
-  float w[kFewMaxT];  // its routing weight, 0 for other tokens
+  uint32_t tokens;  // bit t: token t picked it
 };
 static_assert(sizeof(FewUnit) == kFewUnitBytes, "the plan's size");
 
@@ -63,6 +61,7 @@ struct FewHead {
   int units;        // without the shared one
   float zero_w[kFewMaxT];  // weights of the tokens' zero-computation picks
   FewUnit unit[kFewMaxPicks + 1];
+  float w[kFewMaxPicks + 1][kFewMaxT];        // a unit's routing weights, 0 for other tokens
   uint32_t hmax[kFewMaxPicks + 1][kFewMaxT];  // largest |h| of a unit's token, fp32 bits
 };
 
@@ -102,10 +101,23 @@ struct RouteArgs {
 };
 
 // ---------------------------------------------------------------- routing ----
+// Top-k without groups in registers; other kinds by topk_token, whose logits and scratch (4 E
+// floats a token) lie in shared memory where they fit.
+__host__ __device__ inline bool route_flat(const TopkArgs& a) {
+  return a.n_group <= 1 && a.E <= 1024;
+}
+__host__ __device__ inline bool route_scratch_inside(const TopkArgs& a) {
+  return !route_flat(a) && a.T * a.E * 16 <= kRouteScratch;
+}
 __device__ __forceinline__ float2 unpack_x(uint32_t w, int fp16) {
   return fp16 ? unpack2<__half>(w) : unpack2<__nv_bfloat16>(w);
 }
-// Eight channels of a 16-bit row.
+// Four, eight channels of a 16-bit row.
+__device__ __forceinline__ uint2 load_x4(const void* x, int64_t at, bool vec) {
+  const uint16_t* p = static_cast<const uint16_t*>(x) + at;
+  if (vec) return *reinterpret_cast<const uint2*>(p);
+  return make_uint2(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16);
+}
 __device__ __forceinline__ uint4 load_x8(const void* x, int64_t at, bool vec) {
   const uint16_t* p = static_cast<const uint16_t*>(x) + at;
   if (vec) return *reinterpret_cast<const uint4*>(p);
@@ -117,96 +129,207 @@ __device__ __forceinline__ uint4 load_x8(const void* x, int64_t at, bool vec) {
   return q;
 }
 
-// Logits of the CTA's experts for all TT >= T tokens; the last CTA picks.
+// The sums of N values over the warp, N a power of two up to 32: lane i * 32 / N (and the
+// lanes that follow it, up to the next one) ends up with that of v[i].
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N]) {
+  const int lane = threadIdx.x % 32;
+  int o = 16;
+#pragma unroll
+  for (int n = N / 2; n > 0; n /= 2, o /= 2) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float mine = upper ? v[i + n] : v[i], theirs = upper ? v[i] : v[i + n];
+      v[i] = mine + __shfl_xor_sync(0xffffffffu, theirs, o);
+    }
+  }
+  float s = v[0];
+  for (; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+// Larger floats are larger numbers; what can not be picked (-inf, NaN) is 0.
+__device__ __forceinline__ uint32_t pick_key(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return v > -INFINITY ? b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u) : 0u;
+}
+
+// topk_token (topk.cuh) without groups for at most 32 * N experts: a lane keeps those of every
+// 32nd expert in registers, a pick is a maximum over the warp by redux.  The same scores, order
+// and weights.
+template <int N>
+__device__ __forceinline__ void pick_flat(const TopkArgs& a, int t, const float* row) {
+  const int lane = threadIdx.x % 32;
+  float score[N], bias[N];
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = lane + 32 * i;
+    score[i] = e < a.E ? __ldcg(row + e) : -INFINITY;
+    bias[i] = e < a.E && a.bias_mode != MOE_BIAS_NONE ? a.bias[e] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (a.bias_mode == MOE_BIAS_LOGIT) score[i] += bias[i];
+    m = fmaxf(m, score[i]);
+  }
+  if (a.score == MOE_SCORE_SOFTMAX) {
+    m = warp_max(m);
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      score[i] = lane + 32 * i < a.E ? expf(score[i] - m) : 0.f;
+      z += score[i];
+    }
+    z = warp_sum(z);
+#pragma unroll
+    for (int i = 0; i < N; ++i) score[i] = score[i] / z;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) score[i] = 1.f / (1.f + expf(-score[i]));
+  }
+  uint32_t key[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    key[i] = lane + 32 * i >= a.E                ? 0u
+             : a.bias_mode == MOE_BIAS_SELECT ? pick_key(score[i] + bias[i])
+                                              : pick_key(score[i]);
+  int my_id = 0;
+  float my_w = 0.f;
+  for (int j = 0; j < a.k; ++j) {
+    uint32_t best = 0u;
+    int at = 0;
+    float w = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = i;
+        w = score[i];
+      }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const uint32_t mine = best == top ? (uint32_t)(lane + 32 * at) : 0xffffffffu;
+    uint32_t id = __reduce_min_sync(0xffffffffu, mine);
+    if (top == 0u) {  // fewer eligible experts than k (non-finite keys)
+      if (lane == 0) raise_status(a.status, kStInternal, MOE_K_FEW_ROUTE);
+      id = 0u;
+      w = score[0];
+    }
+    w = __shfl_sync(0xffffffffu, w, id % 32);
+    if (lane == j) {
+      my_id = (int)id;
+      my_w = w;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (id == (uint32_t)(lane + 32 * i)) key[i] = 0u;
+  }
+  const float sum = warp_sum(lane < a.k ? my_w : 0.f);
+  if (lane < a.k) {
+    a.ids[t * a.k + lane] = my_id;
+    a.w[t * a.k + lane] = (a.renorm ? my_w / sum : my_w) * a.scale;
+  }
+}
+
+// Logits of the CTA's experts for all TT >= T tokens; the last CTA picks.  A thread keeps its
+// columns of all tokens in registers and meets two rows of W_r at a time with them; the first
+// rows are on their way while x arrives.
 template <int TT>
 __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(RouteArgs a) {
   pdl_enter();
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float part[kRouteWarps][2][TT];
+  __shared__ float part[kRouteWarps][2 * TT];
   __shared__ int32_t ids[kFewMaxPicks];
   __shared__ float wts[kFewMaxPicks];
   __shared__ int warp_units[kRouteWarps];
   __shared__ int last;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int T = a.tk.T, H = a.H, E = a.tk.E, k = a.tk.k;
-  for (int i = tid; i < TT * (H / 8); i += kRouteThreads) {
-    const int t = i / (H / 8), c = i % (H / 8);
-    reinterpret_cast<uint4*>(smem)[i] =
-        t < T ? load_x8(a.x, t * a.ldx + 8 * c, a.vec) : make_uint4(0u, 0u, 0u, 0u);
-  }
-  __syncthreads();
-  constexpr int kCols = 4;  // float4 of each row in flight
-  for (int r = blockIdx.x; r < E; r += 2 * gridDim.x) {
-    const bool two = r + gridDim.x < E;
+  const int T = a.tk.T, H = a.H, E = a.tk.E, k = a.tk.k, G = gridDim.x;
+  constexpr int kCols = 4;  // float4 of a row that a thread holds at once
+  constexpr int kSpan = kCols * kRouteThreads;
+  for (int r = blockIdx.x; r < E; r += 2 * G) {
+    const bool two = r + G < E;
     const float4* w0 = reinterpret_cast<const float4*>(a.w_r + (size_t)r * H);
-    const float4* w1 = reinterpret_cast<const float4*>(
-        a.w_r + (size_t)(two ? r + gridDim.x : r) * H);
-    float acc[2][TT] = {};
-    for (int c0 = tid; c0 < H / 4; c0 += kCols * kRouteThreads) {
+    const float4* w1 = reinterpret_cast<const float4*>(a.w_r + (size_t)(two ? r + G : r) * H);
+    float acc[2 * TT] = {};
+    for (int c0 = tid; c0 - tid < H / 4; c0 += kSpan) {
       float4 v0[kCols], v1[kCols];
 #pragma unroll
       for (int i = 0; i < kCols; ++i) {
         const int c = c0 + i * kRouteThreads;
-        v0[i] = c < H / 4 ? __ldg(w0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-        v1[i] = c < H / 4 && two ? __ldg(w1 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const bool in = c < H / 4;
+        v0[i] = in ? __ldg(w0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v1[i] = in && two ? __ldg(w1 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
+      uint2 x[TT][kCols];
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) {
-        const int c = c0 + i * kRouteThreads;
-        if (c >= H / 4) break;
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) {
+          const int c = c0 + i * kRouteThreads;
+          x[t][i] = t < T && c < H / 4 ? load_x4(a.x, t * a.ldx + 4 * c, a.vec) : make_uint2(0u, 0u);
+        }
+#pragma unroll
+      for (int i = 0; i < kCols; ++i)
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-          const uint2 q = reinterpret_cast<const uint2*>(smem)[t * (H / 4) + c];
-          const float2 x0 = unpack_x(q.x, a.fp16), x1 = unpack_x(q.y, a.fp16);
-          acc[0][t] = fmaf(v0[i].x, x0.x, acc[0][t]);
-          acc[0][t] = fmaf(v0[i].y, x0.y, acc[0][t]);
-          acc[0][t] = fmaf(v0[i].z, x1.x, acc[0][t]);
-          acc[0][t] = fmaf(v0[i].w, x1.y, acc[0][t]);
-          acc[1][t] = fmaf(v1[i].x, x0.x, acc[1][t]);
-          acc[1][t] = fmaf(v1[i].y, x0.y, acc[1][t]);
-          acc[1][t] = fmaf(v1[i].z, x1.x, acc[1][t]);
-          acc[1][t] = fmaf(v1[i].w, x1.y, acc[1][t]);
+          const float2 x0 = unpack_x(x[t][i].x, a.fp16), x1 = unpack_x(x[t][i].y, a.fp16);
+          acc[t] = fmaf(v0[i].x, x0.x, acc[t]);
+          acc[t] = fmaf(v0[i].y, x0.y, acc[t]);
+          acc[t] = fmaf(v0[i].z, x1.x, acc[t]);
+          acc[t] = fmaf(v0[i].w, x1.y, acc[t]);
+          acc[TT + t] = fmaf(v1[i].x, x0.x, acc[TT + t]);
+          acc[TT + t] = fmaf(v1[i].y, x0.y, acc[TT + t]);
+          acc[TT + t] = fmaf(v1[i].z, x1.x, acc[TT + t]);
+          acc[TT + t] = fmaf(v1[i].w, x1.y, acc[TT + t]);
         }
-      }
     }
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const float v = warp_sum(acc[j][t]);
-        if (lane == 0) part[warp][j][t] = v;
-      }
+    const float s = warp_sums<2 * TT>(acc);
+    constexpr int kEach = 32 / (2 * TT);  // lanes with the same sum
+    if (lane % kEach == 0) part[warp][lane / kEach] = s;
     __syncthreads();
     if (tid < 2 * TT) {
       const int j = tid / TT, t = tid % TT;
       float v = 0.f;
 #pragma unroll
-      for (int i = 0; i < kRouteWarps; ++i) v += part[i][j][t];
-      if (t < T && (j == 0 || two)) a.logits[(size_t)t * E + r + j * gridDim.x] = v;
+      for (int i = 0; i < kRouteWarps; ++i) v += part[i][tid];
+      if (t < T && (j == 0 || two)) a.logits[(size_t)t * E + r + j * G] = v;
     }
     __syncthreads();
   }
-  if (tid == 0) {
-    __threadfence();
-    last = atomicAdd(&a.head->ticket, 1) == (int)gridDim.x - 1;
-    __threadfence();
+  if (warp == 0) {  // (the warp that stored the logits)
+    __syncwarp();
+    if (lane == 0) {
+      __threadfence();
+      last = atomicAdd(&a.head->ticket, 1) == G - 1;
+      __threadfence();
+    }
   }
   __syncthreads();
   if (!last) return;
 
   // Picks of all tokens, a warp each.
+  const bool flat = route_flat(a.tk), inside = route_scratch_inside(a.tk);
   float* lg = reinterpret_cast<float*>(smem);
-  const bool inside = T * E * 16 <= kRouteScratch;
   for (int i = tid; i < T * E && inside; i += kRouteThreads) lg[i] = __ldcg(a.logits + i);
-  for (int i = tid; i < T * k; i += kRouteThreads) ids[i] = -1;
-  __syncthreads();
+  if (inside) __syncthreads();
   if (warp < T) {
     TopkArgs tk = a.tk;
     tk.ids = ids;
     tk.w = wts;
     const float* row = inside ? lg + warp * E : a.logits + (size_t)warp * E;
-    float* scratch = inside ? lg + T * E + warp * 3 * E : a.scratch + (size_t)warp * 3 * E;
-    topk_token(tk, warp, row, scratch);
+    if (!flat)
+      topk_token(tk, warp, row,
+                 inside ? lg + T * E + warp * 3 * E : a.scratch + (size_t)warp * 3 * E);
+    else if (E <= 256)
+      pick_flat<8>(tk, warp, row);
+    else if (E <= 512)
+      pick_flat<16>(tk, warp, row);
+    else if (E <= 768)
+      pick_flat<24>(tk, warp, row);
+    else
+      pick_flat<32>(tk, warp, row);
   }
   __syncthreads();
 
@@ -225,19 +348,19 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(RouteArgs a) {
     units += warp_units[i];
   }
   if (first) {
-    FewUnit u;
-    u.expert = e;
-    u.tokens = 0u;
-#pragma unroll
-    for (int t = 0; t < kFewMaxT; ++t) u.w[t] = 0.f;
+    FewUnit u{e, 0u};
+    float w[kFewMaxT] = {};
     for (int i = tid; i < picks; ++i)
       if (ids[i] == e) {
         u.tokens |= 1u << (i / k);
 #pragma unroll
         for (int t = 0; t < kFewMaxT; ++t)
-          if (t == i / k) u.w[t] += wts[i];
+          if (t == i / k) w[t] += wts[i];
       }
-    head->unit[before + __popc(ballot & ((1u << lane) - 1u))] = u;
+    const int at = before + __popc(ballot & ((1u << lane) - 1u));
+    head->unit[at] = u;
+#pragma unroll
+    for (int t = 0; t < kFewMaxT; ++t) head->w[at][t] = w[t];
   }
   if (tid < kFewMaxT) {
     float z = 0.f;
@@ -247,12 +370,9 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(RouteArgs a) {
   }
   if (tid == 0) {
     if (a.shared) {
-      FewUnit u;
-      u.expert = -1;
-      u.tokens = (1u << T) - 1u;
+      head->unit[units] = {-1, (1u << T) - 1u};
 #pragma unroll
-      for (int t = 0; t < kFewMaxT; ++t) u.w[t] = t < T ? 1.f : 0.f;
-      head->unit[units] = u;
+      for (int t = 0; t < kFewMaxT; ++t) head->w[units][t] = t < T ? 1.f : 0.f;
     }
     head->units = units;
     head->ticket = head->claim = head->done = 0;
@@ -299,12 +419,16 @@ __device__ __forceinline__ void team_barrier(int team) {
 }
 // All but the `stages - 2` groups committed last have arrived.
 __device__ __forceinline__ void wait_stage(int stages) {
-  if (stages == 3)
+  if (stages >= 6)
+    cp_async_wait<4>();
+  else if (stages >= 4)
+    cp_async_wait<2>();
+  else if (stages == 3)
     cp_async_wait<1>();
   else
     cp_async_wait<0>();
 }
-static_assert(kFewMaxStages == 3, "wait_stage knows two and three");
+static_assert(kFewMaxStages == 6, "wait_stage knows 2, 3, 4 and 6 (5 waits like 4)");
 
 template <typename T>
 __device__ __forceinline__ float read_scale(uint32_t at) {
@@ -562,7 +686,7 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, c
   const int least = sh.steps - (sh.steps - 1) / per * per;  // the last busy warp's steps
   const int ahead = (S - 1 + least - 1) / least;
   volatile int* queue = reinterpret_cast<int*>(smem + a.p.queue_at) + team * 16;
-  float* red = reinterpret_cast<float*>(smem + a.p.red_at) + team * kFewTeamWarps * 128;
+  float* red = reinterpret_cast<float*>(smem + a.p.red_at) + team * 2 * kFewTeamWarps * 128;
   const uint32_t ring = smem_u32(smem) + a.p.ring_at + warp * S * sub;
   FewHead* head = a.head;
   if (tt == 0) {
@@ -666,40 +790,47 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, c
       before = use;
       use = use == ring_last ? ring : use + sub;
     }
-    float* r = red + kw * 128 + g * 8 + 2 * tg;
+    // The parts meet in one of two buffers; one warp of the team, another each time, adds them
+    // and stores h while the others go on.  (The buffer's next use is past the next barrier,
+    // which that warp reaches when it is done.)
+    float* parts = red + (seq & 1) * kFewTeamWarps * 128;
+    float* r = parts + kw * 128 + g * 8 + 2 * tg;
     *reinterpret_cast<float2*>(r) = make_float2(acc[0], acc[1]);
     *reinterpret_cast<float2*>(r + 64) = make_float2(acc[2], acc[3]);
     if (tt == 0) queue[(seq + ahead + 1) % 16] = claimed;
     team_barrier(team);
-    if (tt < 64) {
-      const int ch = tt % 8, t = tt / 8;
-      float gate = 0.f, up = 0.f;
+    if (kw == seq % kFewTeamWarps) {
+      const int ch = lane % 8;
+      const uint32_t tokens = units[u].tokens;
+      for (int t = lane / 8; t - lane / 8 < a.T; t += 4) {
+        float gate = 0.f, up = 0.f;
 #pragma unroll
-      for (int i = 0; i < kFewTeamWarps; ++i) {
-        gate += red[i * 128 + ch * 8 + t];
-        up += red[i * 128 + (ch + 8) * 8 + t];
-      }
-      const bool mine = (units[u].tokens >> t) & 1u;
-      float h = 0.f;
-      if (mine) {
-        if constexpr (K::kFour) {
-          gate = gate * 16777216.f * x_inverse[t];
-          up = up * 16777216.f * x_inverse[t];
+        for (int i = 0; i < kFewTeamWarps; ++i) {
+          gate += parts[i * 128 + ch * 8 + t];
+          up += parts[i * 128 + (ch + 8) * 8 + t];
         }
-        h = gate / (1.f + expf(-gate)) * up;
-        __stcg(a.h + ((int64_t)u * a.T + t) * a.inter + f * 8 + ch, h);
-      }
-      if constexpr (K::kScaled) {
-        uint32_t most = __float_as_uint(fabsf(h));
+        const bool mine = (tokens >> t) & 1u;
+        float h = 0.f;
+        if (mine) {
+          if constexpr (K::kFour) {
+            gate = gate * 16777216.f * x_inverse[t];
+            up = up * 16777216.f * x_inverse[t];
+          }
+          h = gate / (1.f + expf(-gate)) * up;
+          __stcg(a.h + ((int64_t)u * a.T + t) * a.inter + f * 8 + ch, h);
+        }
+        if constexpr (K::kScaled) {
+          uint32_t most = __float_as_uint(fabsf(h));
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-        if (ch == 0 && mine) atomicMax(&head->hmax[u][t], most);
+          for (int o = 4; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+          if (ch == 0 && mine) atomicMax(&head->hmax[u][t], most);
+        }
       }
-    }
-    team_barrier(team);
-    if (tt == 0) {
-      __threadfence();
-      atomicAdd(&head->done, 1);
+      __syncwarp();
+      if (lane == 0) {
+        __threadfence();
+        atomicAdd(&head->done, 1);
+      }
     }
   }
   cp_async_wait<0>();
@@ -821,8 +952,8 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
         kmax = sh.K;
         const uint32_t tokens = units[u].tokens;
         hrow = g < a.T && ((tokens >> g) & 1u) ? a.h + ((int64_t)u * a.T + g) * a.inter : nullptr;
-        w0 = units[u].w[2 * tg] * (K::kFour ? 16777216.f : 1.f);
-        w1 = units[u].w[2 * tg + 1] * (K::kFour ? 16777216.f : 1.f);
+        w0 = __ldcg(&a.head->w[u][2 * tg]) * (K::kFour ? 16777216.f : 1.f);
+        w1 = __ldcg(&a.head->w[u][2 * tg + 1]) * (K::kFour ? 16777216.f : 1.f);
         if constexpr (K::kScaled) {
           up = __uint_as_float(fp16_range_bits(__ldcg(&a.head->hmax[u][g])));
           w0 *= inverse_pow2(fp16_range_bits(__ldcg(&a.head->hmax[u][2 * tg])));
@@ -1021,10 +1152,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_ffn_kernel(const __grid_co
 template <int TT>
 void launch_route(const Launch& L, const RouteArgs& r) {
   const int E = r.tk.E;
-  const size_t need = std::max<size_t>((size_t)TT * r.H * 2,
-                                       r.tk.T * E * 16 <= kRouteScratch ? (size_t)r.tk.T * E * 16 : 0);
-  set_smem_attr_once(reinterpret_cast<const void*>(few_route_kernel<TT>),
-                     kRouteSmem,
+  const size_t need = route_scratch_inside(r.tk) ? (size_t)r.tk.T * E * 16 : 0;
+  set_smem_attr_once(reinterpret_cast<const void*>(few_route_kernel<TT>), kRouteScratch,
                      kAttrFewRoute + (TT == 1 ? 0 : TT == 2 ? 1 : TT == 4 ? 2 : 3));
   launch_begin(L, MOE_K_FEW_ROUTE);
   launch_kernel(few_route_kernel<TT>, dim3(std::min(E, L.num_sms)), dim3(kRouteThreads), need,

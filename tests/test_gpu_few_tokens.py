@@ -54,6 +54,13 @@ LAYERS = {
     "only_shared": dict(hidden=256, inter=32, n_routed=0, n_zero=4, top_k=1, shared_inter=160),
     "all": dict(hidden=160, inter=64, n_routed=32, top_k=32, renormalize=True),
     "one": dict(hidden=32, inter=32, n_routed=1, top_k=1),
+    "flat256": dict(hidden=64, inter=32, n_routed=250, top_k=9, renormalize=True),
+    "flat512": dict(hidden=96, inter=32, n_routed=300, n_zero=200, top_k=32, bias_mode="logit",
+                    bias_kind="iid"),
+    "flat768": dict(hidden=64, inter=32, n_routed=513, top_k=7, score="sigmoid",
+                    bias_mode="select", bias_kind="iid"),
+    "flat1024": dict(hidden=64, inter=32, n_routed=1024, top_k=5, routed_scale=1.5),
+    "groups_wide": dict(hidden=64, inter=32, n_routed=1600, top_k=4, n_group=8, topk_group=3),
     "wide": dict(hidden=64, inter=32, n_routed=2048, top_k=6),
     "deep": dict(hidden=7168, inter=2048, n_routed=12, top_k=4, shared_inter=2048),
     # 16-bit weights only
@@ -207,7 +214,7 @@ def test_sixteen_bit_weights(m, name, T, dtype):
     check(m, make(name, T, dtype, 16))
 
 
-FOUR = ["flat", "groups", "per_group", "zero", "select", "only_zero", "only_shared", "all", "one",
+FOUR = ["flat", "flat512", "flat768", "groups", "per_group", "zero", "select", "only_zero", "only_shared", "all", "one",
         "wide", "deep"]
 
 
