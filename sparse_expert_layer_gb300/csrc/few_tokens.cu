@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(RouteArgs a) {
   __shared__ float part[kRouteWarps][2 * TT];
   __shared__ int32_t ids[kFewMaxPicks];
   __shared__ float wts[kFewMaxPicks];
-  __shared__ int warp_units[kRouteWarps];
+  __shared__ bool first[kFewMaxPicks];
   __shared__ int last;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int T = a.tk.T, H = a.H, E = a.tk.E, k = a.tk.k, G = gridDim.x;
@@ -333,34 +333,37 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(RouteArgs a) {
   }
   __syncthreads();
 
-  // Units: the distinct experts with weights, in order of their first pick.
+  // Units: the distinct experts with weights, in order of their first pick; a warp a pick,
+  // lanes compare it with the others.
   FewHead* head = a.head;
   const int picks = T * k;
-  const int e = tid < picks ? ids[tid] : -1;
-  bool first = e >= 0 && e < a.E_r;
-  for (int i = 0; i < tid && first; ++i) first = ids[i] != e;
-  const uint32_t ballot = __ballot_sync(0xffffffffu, first);
-  if (lane == 0) warp_units[warp] = __popc(ballot);
-  __syncthreads();
-  int before = 0, units = 0;
-  for (int i = 0; i < kRouteWarps; ++i) {
-    before += i < warp ? warp_units[i] : 0;
-    units += warp_units[i];
+  for (int p = warp; p < picks; p += kRouteWarps) {
+    const int e = ids[p];
+    bool earlier = e < 0 || e >= a.E_r;
+    for (int i = lane; i < p; i += 32) earlier = earlier || ids[i] == e;
+    earlier = __any_sync(0xffffffffu, earlier);
+    if (lane == 0) first[p] = !earlier;
   }
-  if (first) {
-    FewUnit u{e, 0u};
-    float w[kFewMaxT] = {};
-    for (int i = tid; i < picks; ++i)
+  __syncthreads();
+  int units = 0;
+  for (int i0 = 0; i0 < picks; i0 += 32)
+    units += __popc(__ballot_sync(0xffffffffu, i0 + lane < picks && first[i0 + lane]));
+  for (int p = warp; p < picks; p += kRouteWarps) {
+    if (!first[p]) continue;
+    const int e = ids[p];
+    int at = 0;
+    for (int i0 = 0; i0 < p; i0 += 32)
+      at += __popc(__ballot_sync(0xffffffffu, i0 + lane < p && first[i0 + lane]));
+    uint32_t tokens = 0u;
+    if (lane < kFewMaxT) head->w[at][lane] = 0.f;
+    __syncwarp();
+    for (int i = p + lane; i < picks; i += 32)
       if (ids[i] == e) {
-        u.tokens |= 1u << (i / k);
-#pragma unroll
-        for (int t = 0; t < kFewMaxT; ++t)
-          if (t == i / k) w[t] += wts[i];
+        tokens |= 1u << (i / k);
+        head->w[at][i / k] = wts[i];
       }
-    const int at = before + __popc(ballot & ((1u << lane) - 1u));
-    head->unit[at] = u;
-#pragma unroll
-    for (int t = 0; t < kFewMaxT; ++t) head->w[at][t] = w[t];
+    tokens = __reduce_or_sync(0xffffffffu, tokens);
+    if (lane == 0) head->unit[at] = {e, tokens};
   }
   if (tid < kFewMaxT) {
     float z = 0.f;
