@@ -49,6 +49,44 @@ struct Segments {
       n += __syncthreads_count(j < J && at(j + 1) <= p);
     return n;
   }
+  // Tile `tile` when each adapter's positions (and those without one, adapter J) are cut into
+  // tiles of `rows`: its adapter and positions lo .. hi.  lo >= hi: there are not so many.  By
+  // all threads of the block; at most T / rows + J + 1 tiles have positions.
+  __device__ __forceinline__ void tile(int index, int rows, int* adapter, int* lo, int* hi) const {
+    __shared__ int sums[32], found[3];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    if (threadIdx.x == 0) found[0] = -1;
+    int before = 0;
+    for (int j0 = 0; j0 <= J; j0 += blockDim.x) {
+      const int j = j0 + threadIdx.x;
+      const int a = j <= J ? at(j) : 0, b = j < J ? at(j + 1) : T;
+      const int n = j <= J && b > a ? (b - a + rows - 1) / rows : 0;
+      int sum = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
+      }
+      if (lane == 31) sums[warp] = sum;
+      __syncthreads();
+      int total = 0;
+      for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+        if (w < warp) sum += sums[w];
+        total += sums[w];
+      }
+      const int first = before + sum - n;
+      if (n > 0 && index >= first && index < first + n) {
+        found[0] = j;
+        found[1] = a + (index - first) * rows;
+        found[2] = min(b, found[1] + rows);
+      }
+      before += total;
+      __syncthreads();
+    }
+    *adapter = found[0];
+    *lo = found[0] >= 0 ? found[1] : 0;
+    *hi = found[0] >= 0 ? found[2] : 0;
+  }
 };
 
 // Piece i (channels 8 i ..) of a row of n channels, zeros past its end.
@@ -268,109 +306,114 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(AdapterArgs a
 }
 
 // ------------------------------------------------------------------ shrink ----
-constexpr int kShrinkRows = 64;
-constexpr int kShrinkThreads = 128;
 constexpr int kShrinkStages = 4;
+// positions of a tile: more where the adapter's rows are many beside them
+template <int RT>
+constexpr int kShrinkRows = RT <= 32 ? 64 : 128;
+int shrink_rows(int r) { return r <= 32 ? 64 : 128; }
 
-// v of 64 positions: x rows and the adapter's rows in 128-byte slices of K.  Slice c of
-// row i lies at 16-byte piece c ^ (i % 8), so that neither copies nor ldmatrix meet a
-// bank twice.
+// v of a tile of one adapter's positions: x rows and the adapter's rows in 128-byte slices of
+// K.  Slice c of row i lies at 16-byte piece c ^ (i % 8), so that neither copies nor ldmatrix
+// meet a bank twice.  A warp has 16 positions and all ranks.
 template <typename T, int RT>
-__global__ void __launch_bounds__(kShrinkThreads) adapters_shrink_kernel(AdapterArgs a) {
+__global__ void __launch_bounds__(2 * kShrinkRows<RT>) adapters_shrink_kernel(AdapterArgs a) {
   pdl_enter();
   extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int kX = kShrinkRows * 128, kStage = kX + RT * 128;
+  constexpr int kRows = kShrinkRows<RT>, kThreads = 2 * kRows;
+  constexpr int kX = kRows * 128, kStage = kX + RT * 128;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int rank = blockIdx.x, S = gridDim.x, p0 = blockIdx.y * kShrinkRows, r = a.r;
+  const int rank = blockIdx.x, S = gridDim.x, r = a.r;
   const uint32_t base = smem_u32(smem);
-  const int kept = a.seg.at(a.seg.J), p_end = min(p0 + kShrinkRows, kept);
+  int j, lo, hi;
+  a.seg.tile(blockIdx.y, kRows, &j, &lo, &hi);
+  if (lo >= hi || j >= a.seg.J) {  // the whole cluster
+    if (a.max_v && tid == 0) a.max_v[blockIdx.y * S + rank] = a.max_other[blockIdx.y * S + rank] = 0u;
+    return;
+  }
   const int slices = (a.K + 63) / 64;
   const int c0 = (int)((int64_t)slices * rank / S), c1 = (int)((int64_t)slices * (rank + 1) / S);
-  float* red = reinterpret_cast<float*>(smem);
-  uint32_t most = 0u;
-  for (int j = a.seg.first_after(p0); j < a.seg.J && a.seg.at(j) < p_end; ++j) {
-    const int lo = max(a.seg.at(j), p0), hi = min(a.seg.at(j + 1), p_end);
-    if (lo >= hi) continue;
-    const T* xr[4];
-    bool real[4];
+  constexpr int kStep = kThreads / 8;  // rows that the threads copy at once
+  const int piece = tid % 8;
+  const T* xr[kRows / kStep];
+  bool real[kRows / kStep];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int p = p0 + tid / 8 + 16 * i;
-      const int row = p >= lo && p < hi ? a.seg.row(p) : -1;
-      real[i] = row >= 0;
-      xr[i] = static_cast<const T*>(a.x) + (real[i] ? row * a.ldx : 0);
+  for (int i = 0; i < kRows / kStep; ++i) {
+    const int p = lo + tid / 8 + kStep * i;
+    const int row = p < hi ? a.seg.row(p) : -1;
+    real[i] = row >= 0;
+    xr[i] = static_cast<const T*>(a.x) + (real[i] ? row * a.ldx : 0);
+  }
+  const T* m = static_cast<const T*>(a.m1) + ((int64_t)j * r) * a.K;
+  auto load = [&](int c, int slot) {
+    const uint32_t st = base + slot * kStage;
+#pragma unroll
+    for (int i = 0; i < kRows / kStep; ++i) {
+      const int row = tid / 8 + kStep * i;
+      stage_piece<T>(st + row * 128 + ((piece ^ (row % 8)) * 16), xr[i], c * 8 + piece, a.K, a.xvec,
+                     real[i]);
     }
-    const T* m = static_cast<const T*>(a.m1) + ((int64_t)j * r) * a.K;
-    auto load = [&](int c, int slot) {
-      const uint32_t st = base + slot * kStage;
-      const int piece = tid % 8;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = tid / 8 + 16 * i;
-        stage_piece<T>(st + row * 128 + ((piece ^ (row % 8)) * 16), xr[i], c * 8 + piece, a.K,
-                       a.xvec, real[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < RT / 16; ++i) {
-        const int row = tid / 8 + 16 * i;
-        const bool in = row < r;
+    for (int i = 0; i < (RT + kStep - 1) / kStep; ++i) {
+      const int row = tid / 8 + kStep * i;
+      const bool in = row < r;
+      if (row < RT)
         stage_piece<T>(st + kX + row * 128 + ((piece ^ (row % 8)) * 16),
                        m + (in ? (int64_t)row * a.K : 0), c * 8 + piece, a.K, a.m1vec, in);
-      }
-    };
-    float acc[RT / 8][4] = {};
-#pragma unroll
-    for (int q = 0; q < kShrinkStages - 1; ++q) {
-      if (c0 + q < c1) load(c0 + q, q);
-      cp_async_commit();
     }
-    for (int c = c0; c < c1; ++c) {
-      cp_async_wait<kShrinkStages - 2>();
-      __syncthreads();
-      const int ahead = c + kShrinkStages - 1;
-      if (ahead < c1) load(ahead, (ahead - c0) % kShrinkStages);
-      cp_async_commit();
-      const uint32_t st = base + (c - c0) % kShrinkStages * kStage;
+  };
+  float acc[RT / 8][4] = {};
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        uint32_t af[4];
-        const int row = warp * 16 + lane % 16;
-        ldsm4(st + row * 128 + (((kk * 2 + lane / 16) ^ (row % 8)) * 16), af);
-#pragma unroll
-        for (int n = 0; n < RT / 16; ++n) {
-          uint32_t bf[4];
-          const int i = n * 16 + lane % 8 + lane / 16 * 8;
-          ldsm4(st + kX + i * 128 + (((kk * 2 + lane / 8 % 2) ^ (i % 8)) * 16), bf);
-          mma16816<T>(acc[2 * n], af[0], af[1], af[2], af[3], bf[0], bf[1]);
-          mma16816<T>(acc[2 * n + 1], af[0], af[1], af[2], af[3], bf[2], bf[3]);
-        }
-      }
-    }
-    cp_async_wait<0>();
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < RT / 8; ++n) {
-      float* at = red + (warp * 16 + lane / 4) * RT + n * 8 + lane % 4 * 2;
-      *reinterpret_cast<float2*>(at) = make_float2(acc[n][0], acc[n][1]);
-      *reinterpret_cast<float2*>(at + 8 * RT) = make_float2(acc[n][2], acc[n][3]);
-    }
-    cluster_sync_all();
-    const float s1 = a.scale1 ? a.scale1[j] : 1.f;
-    for (int e = rank * kShrinkThreads + tid; e < kShrinkRows * RT; e += S * kShrinkThreads) {
-      const int p = p0 + e / RT, i = e % RT;
-      if (p < lo || p >= hi || i >= r) continue;
-      float s = 0.f;
-      for (int q = 0; q < S; ++q) s += ld_cluster_f32(mapa_shared(base + e * 4, q));
-      s *= s1;
-      a.v[(int64_t)p * r + i] = s;
-      most = max(most, __float_as_uint(fabsf(s)));
-    }
-    cluster_sync_all();
+  for (int q = 0; q < kShrinkStages - 1; ++q) {
+    if (c0 + q < c1) load(c0 + q, q);
+    cp_async_commit();
   }
+  for (int c = c0; c < c1; ++c) {
+    cp_async_wait<kShrinkStages - 2>();
+    __syncthreads();
+    const int ahead = c + kShrinkStages - 1;
+    if (ahead < c1) load(ahead, (ahead - c0) % kShrinkStages);
+    cp_async_commit();
+    const uint32_t st = base + (c - c0) % kShrinkStages * kStage;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      uint32_t af[4];
+      const int row = warp * 16 + lane % 16;
+      ldsm4(st + row * 128 + (((kk * 2 + lane / 16) ^ (row % 8)) * 16), af);
+#pragma unroll
+      for (int n = 0; n < RT / 16; ++n) {
+        uint32_t bf[4];
+        const int i = n * 16 + lane % 8 + lane / 16 * 8;
+        ldsm4(st + kX + i * 128 + (((kk * 2 + lane / 8 % 2) ^ (i % 8)) * 16), bf);
+        mma16816<T>(acc[2 * n], af[0], af[1], af[2], af[3], bf[0], bf[1]);
+        mma16816<T>(acc[2 * n + 1], af[0], af[1], af[2], af[3], bf[2], bf[3]);
+      }
+    }
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int n = 0; n < RT / 8; ++n) {
+    float* at = red + (warp * 16 + lane / 4) * RT + n * 8 + lane % 4 * 2;
+    *reinterpret_cast<float2*>(at) = make_float2(acc[n][0], acc[n][1]);
+    *reinterpret_cast<float2*>(at + 8 * RT) = make_float2(acc[n][2], acc[n][3]);
+  }
+  cluster_sync_all();
+  const float s1 = a.scale1 ? a.scale1[j] : 1.f;
+  uint32_t most = 0u;
+  for (int e = rank * kThreads + tid; e < kRows * RT; e += S * kThreads) {
+    const int p = lo + e / RT, i = e % RT;
+    if (p >= hi || i >= r) continue;
+    float s = 0.f;
+    for (int q = 0; q < S; ++q) s += ld_cluster_f32(mapa_shared(base + e * 4, q));
+    s *= s1;
+    a.v[(int64_t)p * r + i] = s;
+    most = max(most, __float_as_uint(fabsf(s)));
+  }
+  cluster_sync_all();
   if (a.max_v) {
     uint32_t other = 0u;
-    const int64_t first = (int64_t)p0 * r, last = (int64_t)max(p_end, p0) * r;
-    for (int64_t i = first + rank * kShrinkThreads + tid; i < last; i += S * kShrinkThreads)
+    for (int64_t i = (int64_t)lo * r + rank * kThreads + tid; i < (int64_t)hi * r; i += S * kThreads)
       other = max(other, __float_as_uint(fabsf(a.other[i])));
     most = block_max(most);
     other = block_max(other);
@@ -384,142 +427,166 @@ __global__ void __launch_bounds__(kShrinkThreads) adapters_shrink_kernel(Adapter
 // ------------------------------------------------------------------ expand ----
 constexpr int kExpandRows = 128;
 constexpr int kExpandThreads = 256;
-constexpr int kExpandTile = 256;  // columns of the second matrix in shared memory
+constexpr int kExpandTile = 256;  // columns of the second matrix in shared memory at once
 
-// y of 128 positions and a range of columns.  The columns of 32 are dealt to the four
-// n-tiles of MMAs so that a lane's results are eight neighbours: pair t of 16-byte piece
-// q belongs to n-tile t, columns 2 (q % 4) and the next.
+// y of a tile of one adapter's positions and a range of columns; a warp has 16 positions.  The
+// columns of 32 are dealt to the four n-tiles of MMAs so that a lane's results are eight
+// neighbours: pair t of 16-byte piece q belongs to n-tile t, columns 2 (q % 4) and the next.
+// Tiles of the second matrix are copied one ahead, base is read two chunks of 32 ahead.
 template <typename T, int RT>
 __global__ void __launch_bounds__(kExpandThreads) adapters_expand_kernel(AdapterArgs a, int range) {
   pdl_enter();
   extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int kTile = RT * kExpandTile * 2, kChunks = kExpandTile / 32;
   const uint32_t mt = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g = lane / 4, tg = lane % 4;
-  const int p0 = blockIdx.y * kExpandRows, r = a.r;
-  const int n_begin = blockIdx.x * range, n_end = min(a.N, n_begin + range);
-  const int kept = a.seg.at(a.seg.J), p_end = min(p0 + kExpandRows, kept);
-  const int pa = p0 + warp * 16 + g, pb = pa + 8;
-  const int ra = pa < a.seg.T ? a.seg.row(pa) : -1, rb = pb < a.seg.T ? a.seg.row(pb) : -1;
-  T* ya = static_cast<T*>(a.y) + ra * a.ldy;
-  T* yb = static_cast<T*>(a.y) + rb * a.ldy;
-  const T* ba = static_cast<const T*>(a.base) + ra * a.ldb;
-  const T* bb = static_cast<const T*>(a.base) + rb * a.ldb;
-  for (int j = a.seg.first_after(p0); j < a.seg.J && a.seg.at(j) < p_end; ++j) {
-    const int lo = max(a.seg.at(j), p0), hi = min(a.seg.at(j + 1), p_end);
-    if (lo >= hi) continue;
-    const bool ina = pa >= lo && pa < hi && ra >= 0, inb = pb >= lo && pb < hi && rb >= 0;
-    const bool mine = __any_sync(0xffffffffu, ina || inb);
-    // the rows' v as two 16-bit terms
-    uint32_t hi_t[RT / 16][4], lo_t[RT / 16][4];
-    float sa = a.scale2 ? a.scale2[j] : 1.f, sb = sa;
-    {
-      float f[RT / 16][8];
-      float ma = 0.f, mb = 0.f;
-#pragma unroll
-      for (int k = 0; k < RT / 16; ++k)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int i = k * 16 + tg * 2 + (q & 1) + (q >> 1) * 8;
-          const bool in = i < r;
-          f[k][q] = ina && in ? a.v[(int64_t)pa * r + i] : 0.f;
-          f[k][4 + q] = inb && in ? a.v[(int64_t)pb * r + i] : 0.f;
-          ma = fmaxf(ma, fabsf(f[k][q]));
-          mb = fmaxf(mb, fabsf(f[k][4 + q]));
-        }
-      float upa = 1.f, upb = 1.f;
-      if constexpr (std::is_same<T, __half>::value) {  // into fp16's range, row by row
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
-          mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-        }
-        const uint32_t ua = fp16_range_bits(__float_as_uint(ma));
-        const uint32_t ub = fp16_range_bits(__float_as_uint(mb));
-        upa = __uint_as_float(ua);
-        upb = __uint_as_float(ub);
-        sa *= inverse_pow2(ua);
-        sb *= inverse_pow2(ub);
-      }
-#pragma unroll
-      for (int k = 0; k < RT / 16; ++k)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          split2<T>(f[k][2 * q] * upa, f[k][2 * q + 1] * upa, hi_t[k][2 * q], lo_t[k][2 * q]);
-          split2<T>(f[k][4 + 2 * q] * upb, f[k][5 + 2 * q] * upb, hi_t[k][2 * q + 1],
-                    lo_t[k][2 * q + 1]);
-        }
-    }
-    const T* m = static_cast<const T*>(a.m2) + (int64_t)j * r * a.N;
-    for (int n0 = n_begin; n0 < n_end; n0 += kExpandTile) {
-      __syncthreads();
-      for (int e = tid; e < RT * (kExpandTile / 8); e += kExpandThreads) {
-        const int i = e / (kExpandTile / 8), q = e % (kExpandTile / 8);
-        const uint4 v = i < r ? load_piece<T>(m + (int64_t)i * a.N, n0 / 8 + q, a.N, a.m2vec)
-                              : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(mt + i * (kExpandTile * 2) +
-                                                       (((q / 4 * 4 + t) ^ (i % 8)) * 16) +
-                                                       (q % 4) * 4),
-                       "r"(w[t])
-                       : "memory");
-      }
-      __syncthreads();
-      if (!mine) continue;
-#pragma unroll 2
-      for (int c = 0; c < kExpandTile / 32; ++c) {
-        if (n0 + c * 32 >= n_end) break;
-        const int piece = n0 / 8 + c * 4 + tg;
-        uint4 qa = make_uint4(0u, 0u, 0u, 0u), qb = qa;
-        if (a.base) {
-          if (ina) qa = load_piece<T>(ba, piece, a.N, a.yvec);
-          if (inb) qb = load_piece<T>(bb, piece, a.N, a.yvec);
-        }
-        float d[4][4] = {};
-#pragma unroll
-        for (int k = 0; k < RT / 16; ++k) {
-          const int i = k * 16 + lane % 16;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t bf[4];
-            ldsm4_trans(mt + i * (kExpandTile * 2) + (((c * 4 + h * 2 + lane / 16) ^ (i % 8)) * 16),
-                        bf);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              mma16816<T>(d[2 * h + t], hi_t[k][0], hi_t[k][1], hi_t[k][2], hi_t[k][3], bf[2 * t],
-                          bf[2 * t + 1]);
-              mma16816<T>(d[2 * h + t], lo_t[k][0], lo_t[k][1], lo_t[k][2], lo_t[k][3], bf[2 * t],
-                          bf[2 * t + 1]);
-            }
-          }
-        }
-        float fa[8], fb[8];
-        unpack_piece<T>(qa, fa);
-        unpack_piece<T>(qb, fb);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            fa[2 * t + h] = fmaf(sa, d[t][h], fa[2 * t + h]);
-            fb[2 * t + h] = fmaf(sb, d[t][2 + h], fb[2 * t + h]);
-          }
-        if (ina) store_piece<T>(ya, piece, a.N, a.yvec, fa);
-        if (inb) store_piece<T>(yb, piece, a.N, a.yvec, fb);
+  const int r = a.r, n_begin = blockIdx.x * range, n_end = min(a.N, n_begin + range);
+  int j, lo, hi;
+  a.seg.tile(blockIdx.y, kExpandRows, &j, &lo, &hi);
+  if (lo >= hi) return;
+  if (j >= a.seg.J) {  // rows without an adapter are their base
+    if (a.y == a.base) return;
+    for (int p = lo + warp; p < hi; p += kExpandThreads / 32) {
+      const int row = a.seg.row(p);
+      if (row < 0) continue;
+      for (int i = n_begin / 8 + lane; 8 * i < n_end; i += 32) {
+        float f[8] = {};
+        if (a.base)
+          unpack_piece<T>(
+              load_piece<T>(static_cast<const T*>(a.base) + row * a.ldb, i, a.N, a.yvec), f);
+        store_piece<T>(static_cast<T*>(a.y) + row * a.ldy, i, a.N, a.yvec, f);
       }
     }
+    return;
   }
-  // rows without an adapter are their base
-  if (a.y == a.base) return;
-  for (int p = max(kept, p0) + warp; p < min(p0 + kExpandRows, a.seg.T); p += kExpandThreads / 32) {
-    const int row = a.seg.row(p);
-    if (row < 0) continue;
-    for (int i = n_begin / 8 + lane; 8 * i < n_end; i += 32) {
-      float f[8] = {};
-      if (a.base)
-        unpack_piece<T>(load_piece<T>(static_cast<const T*>(a.base) + row * a.ldb, i, a.N, a.yvec),
-                        f);
-      store_piece<T>(static_cast<T*>(a.y) + row * a.ldy, i, a.N, a.yvec, f);
+  const T* m = static_cast<const T*>(a.m2) + (int64_t)j * r * a.N;
+  auto load_tile = [&](int n0, int buf) {
+    for (int e = tid; e < RT * (kExpandTile / 8); e += kExpandThreads) {
+      const int i = e / (kExpandTile / 8), q = e % (kExpandTile / 8), c = n0 / 8 + q;
+      const bool in = i < r && 8 * c < a.N;
+      const T* from = m + (int64_t)i * a.N + 8 * c;
+      const uint32_t to = mt + buf * kTile + i * (kExpandTile * 2) + (q % 4) * 4;
+      uint32_t w[4] = {};
+      if (in && !a.m2vec) {
+        const uint4 v = load_piece<T>(m + (int64_t)i * a.N, c, a.N, false);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t dst = to + (((q / 4 * 4 + t) ^ (i % 8)) * 16);
+        if (in && a.m2vec)
+          cp_async_unit(dst, from + 2 * t, 4);
+        else
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(w[t]) : "memory");
+      }
+    }
+  };
+  load_tile(n_begin, 0);
+  cp_async_commit();
+  const int pa = lo + warp * 16 + g, pb = pa + 8;
+  const int ra = pa < hi ? a.seg.row(pa) : -1, rb = pb < hi ? a.seg.row(pb) : -1;
+  const bool ina = ra >= 0, inb = rb >= 0, mine = lo + warp * 16 < hi;
+  T* ya = static_cast<T*>(a.y) + (ina ? ra * a.ldy : 0);
+  T* yb = static_cast<T*>(a.y) + (inb ? rb * a.ldy : 0);
+  const T* ba = static_cast<const T*>(a.base) + (ina ? ra * a.ldb : 0);
+  const T* bb = static_cast<const T*>(a.base) + (inb ? rb * a.ldb : 0);
+  // the base of chunk c (columns n_begin + 32 c ..)
+  auto load_base = [&](int c, uint4 (&q)[2]) {
+    const int piece = n_begin / 8 + c * 4 + tg;
+    q[0] = q[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (a.base && 8 * piece < n_end) {
+      if (ina) q[0] = load_piece<T>(ba, piece, a.N, a.yvec);
+      if (inb) q[1] = load_piece<T>(bb, piece, a.N, a.yvec);
+    }
+  };
+  uint4 next[2][2];
+  load_base(0, next[0]);
+  load_base(1, next[1]);
+  // the rows' v as two 16-bit terms
+  uint32_t hi_t[RT / 16][4], lo_t[RT / 16][4];
+  float sa = a.scale2 ? a.scale2[j] : 1.f, sb = sa;
+  {
+    float f[RT / 16][8];
+    float ma = 0.f, mb = 0.f;
+#pragma unroll
+    for (int k = 0; k < RT / 16; ++k)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = k * 16 + tg * 2 + (q & 1) + (q >> 1) * 8;
+        const bool in = i < r;
+        f[k][q] = ina && in ? a.v[(int64_t)pa * r + i] : 0.f;
+        f[k][4 + q] = inb && in ? a.v[(int64_t)pb * r + i] : 0.f;
+        ma = fmaxf(ma, fabsf(f[k][q]));
+        mb = fmaxf(mb, fabsf(f[k][4 + q]));
+      }
+    float upa = 1.f, upb = 1.f;
+    if constexpr (std::is_same<T, __half>::value) {  // into fp16's range, row by row
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+        mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+      }
+      const uint32_t ua = fp16_range_bits(__float_as_uint(ma));
+      const uint32_t ub = fp16_range_bits(__float_as_uint(mb));
+      upa = __uint_as_float(ua);
+      upb = __uint_as_float(ub);
+      sa *= inverse_pow2(ua);
+      sb *= inverse_pow2(ub);
+    }
+#pragma unroll
+    for (int k = 0; k < RT / 16; ++k)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        split2<T>(f[k][2 * q] * upa, f[k][2 * q + 1] * upa, hi_t[k][2 * q], lo_t[k][2 * q]);
+        split2<T>(f[k][4 + 2 * q] * upb, f[k][5 + 2 * q] * upb, hi_t[k][2 * q + 1],
+                  lo_t[k][2 * q + 1]);
+      }
+  }
+  int buf = 0;
+  for (int n0 = n_begin; n0 < n_end; n0 += kExpandTile, buf ^= 1) {
+    cp_async_wait<0>();
+    __syncthreads();  // the tile is there, and nobody reads the one before
+    if (n0 + kExpandTile < n_end) load_tile(n0 + kExpandTile, buf ^ 1);
+    cp_async_commit();
+    if (!mine) continue;
+    const uint32_t tile = mt + buf * kTile;
+#pragma unroll 2
+    for (int c = 0; c < kChunks; ++c) {
+      const int piece = n0 / 8 + c * 4 + tg;
+      const uint4 qa = next[0][0], qb = next[0][1];
+      next[0][0] = next[1][0], next[0][1] = next[1][1];
+      load_base((n0 - n_begin) / 32 + c + 2, next[1]);
+      if (n0 + c * 32 >= n_end) break;
+      float d[4][4] = {};
+#pragma unroll
+      for (int k = 0; k < RT / 16; ++k) {
+        const int i = k * 16 + lane % 16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t bf[4];
+          ldsm4_trans(tile + i * (kExpandTile * 2) + (((c * 4 + h * 2 + lane / 16) ^ (i % 8)) * 16),
+                      bf);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            mma16816<T>(d[2 * h + t], hi_t[k][0], hi_t[k][1], hi_t[k][2], hi_t[k][3], bf[2 * t],
+                        bf[2 * t + 1]);
+            mma16816<T>(d[2 * h + t], lo_t[k][0], lo_t[k][1], lo_t[k][2], lo_t[k][3], bf[2 * t],
+                        bf[2 * t + 1]);
+          }
+        }
+      }
+      float fa[8], fb[8];
+      unpack_piece<T>(qa, fa);
+      unpack_piece<T>(qb, fb);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          fa[2 * t + h] = fmaf(sa, d[t][h], fa[2 * t + h]);
+          fb[2 * t + h] = fmaf(sb, d[t][2 + h], fb[2 * t + h]);
+        }
+      if (ina) store_piece<T>(ya, piece, a.N, a.yvec, fa);
+      if (inb) store_piece<T>(yb, piece, a.N, a.yvec, fb);
     }
   }
 }
@@ -699,7 +766,7 @@ constexpr int outer_smem() {
 }
 template <int RT>
 constexpr int shrink_smem() {
-  return std::max(kShrinkStages * (kShrinkRows + RT) * 128, kShrinkRows * RT * 4);
+  return std::max(kShrinkStages * (kShrinkRows<RT> + RT) * 128, kShrinkRows<RT> * RT * 4);
 }
 
 // The most CTAs of a power of two, up to eight, that share `units` of work while there
@@ -718,9 +785,15 @@ int row_cluster(const AdapterArgs& a) {
   // slices of at least 256 channels
   return adapters_split(1, std::max(a.K, a.N), kMaxCluster, 256);
 }
+// Tiles of `rows` positions that may have any: see Segments::tile.
+int adapter_tiles(const AdapterArgs& a, int rows) {
+  return a.seg.T / rows + std::min(a.seg.J + 1, a.seg.T) + (a.seg.T % rows ? 1 : 0);
+}
 int shrink_cluster(const AdapterArgs& a, int num_sms) {
-  const int blocks = (a.seg.T + kShrinkRows - 1) / kShrinkRows;
-  return adapters_split(blocks, (a.K + 63) / 64, 3LL * num_sms, 4);
+  const int rows = shrink_rows(a.r);
+  // two (three) CTAs an SM hold the tiles of 128 (64) positions
+  return adapters_split((a.seg.T + rows - 1) / rows, (a.K + 63) / 64,
+                        (rows == 64 ? 3LL : 2LL) * num_sms, 4);
 }
 
 template <typename T, int RT>
@@ -730,20 +803,21 @@ void launch_tiles(const Launch& L, const AdapterArgs& a, int rt_slot) {
   set_smem_attr_once(reinterpret_cast<const void*>(adapters_shrink_kernel<T, RT>),
                      shrink_smem<RT>(), kAttrAdapters + 8 * type + rt_slot);
   launch_begin(L, MOE_K_ADAPTERS);
-  launch_kernel_cluster(adapters_shrink_kernel<T, RT>,
-                        dim3(S, (a.seg.T + kShrinkRows - 1) / kShrinkRows), dim3(S),
-                        dim3(kShrinkThreads), shrink_smem<RT>(), L.stream, a);
+  launch_kernel_cluster(adapters_shrink_kernel<T, RT>, dim3(S, adapter_tiles(a, kShrinkRows<RT>)),
+                        dim3(S), dim3(2 * kShrinkRows<RT>), shrink_smem<RT>(), L.stream, a);
   launch_end(L, MOE_K_ADAPTERS);
   if (!a.y) return;
-  // ranges of whole tiles: about two CTAs an SM
+  // ranges of whole tiles of columns, for about two rounds of CTAs
   const int blocks = (a.seg.T + kExpandRows - 1) / kExpandRows;
   const int tiles = (a.N + kExpandTile - 1) / kExpandTile;
-  const int per = std::max(1, (int)((int64_t)tiles * blocks / (3LL * L.num_sms)));
-  set_smem_attr_once(reinterpret_cast<const void*>(adapters_expand_kernel<T, RT>),
-                     RT * kExpandTile * 2, kAttrAdapters + 8 * type + 4 + rt_slot);
+  const int per = std::max(1, (int)((int64_t)tiles * blocks / (4LL * L.num_sms)));
+  constexpr int kSmem = 2 * RT * kExpandTile * 2;
+  set_smem_attr_once(reinterpret_cast<const void*>(adapters_expand_kernel<T, RT>), kSmem,
+                     kAttrAdapters + 8 * type + 4 + rt_slot);
   launch_begin(L, MOE_K_ADAPTERS);
-  launch_kernel(adapters_expand_kernel<T, RT>, dim3((tiles + per - 1) / per, blocks),
-                dim3(kExpandThreads), RT * kExpandTile * 2, L.stream, a, per * kExpandTile);
+  launch_kernel(adapters_expand_kernel<T, RT>,
+                dim3((tiles + per - 1) / per, adapter_tiles(a, kExpandRows)), dim3(kExpandThreads),
+                kSmem, L.stream, a, per * kExpandTile);
   launch_end(L, MOE_K_ADAPTERS);
 }
 template <typename T, int RT>
@@ -784,8 +858,7 @@ void launch_adapters(const Launch& L, const AdapterArgs& a, OuterArgs* outer) {
       default: launch_tiles<T, 128>(L, a, 3); break;
     }
     if (outer)
-      outer->blocks =
-          shrink_cluster(a, L.num_sms) * ((a.seg.T + kShrinkRows - 1) / kShrinkRows);
+      outer->blocks = shrink_cluster(a, L.num_sms) * adapter_tiles(a, shrink_rows(a.r));
   }
   if (!outer) return;
   switch (slot) {
