@@ -209,6 +209,8 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(AdapterArgs a
         if (brow) unpack_piece<T>(load_piece<T>(brow, i, a.N, a.yvec), f);
         store_piece<T>(yrow, i, a.N, a.yvec, f);
       }
+    if (rank == 0 && row < 0 && j < a.seg.J && a.seg.at(j) <= p)
+      for (int i = tid; i < r; i += kRowThreads) a.v[(int64_t)p * r + i] = 0.f;
     if (a.max_v && tid == 0) {
       a.max_v[p * C + rank] = 0u;
       a.max_other[p * C + rank] = 0u;
@@ -609,7 +611,7 @@ struct OuterArgs {
 
 constexpr int kOuterThreads = 256;
 constexpr int kOuterRows = 32;  // positions of a stage
-constexpr int kOuterStages = 3;
+constexpr int kOuterStages = 4;
 template <int RT>
 constexpr int kOuterCols = RT <= 64 ? 256 : 128;
 // 16-bit terms of v: bf16 three (24 bits), fp16 two (22 bits)
@@ -644,16 +646,28 @@ __global__ void __launch_bounds__(kOuterThreads) adapters_outer_kernel(OuterArgs
     up = __uint_as_float(bits);
     down *= inverse_pow2(bits);
   }
-  auto load_x = [&](int q, int slot) {
-    for (int e = tid; e < kOuterRows * kPieces; e += kOuterThreads) {
-      const int i = e / kPieces, c = e % kPieces, p = lo + q * kOuterRows + i;
-      const int row = p < hi ? a.seg.row(p) : -1;
-      stage_piece<T>(base + slot * kX + i * (kCols * 2) + ((c ^ (i % 8)) * 16),
-                     static_cast<const T*>(s.x) + (row >= 0 ? row * s.ldx : 0), n0 / 8 + c, s.n,
-                     s.vec, row >= 0);
+  // The rows of a stage's positions that this thread copies a piece of: read a stage before
+  // their copies are made.
+  constexpr int kCopies = kOuterRows * kPieces / kOuterThreads, kApart = kOuterThreads / kPieces;
+  const int piece = tid % kPieces;
+  int rows[kCopies];
+  auto load_rows = [&](int q) {
+#pragma unroll
+    for (int m = 0; m < kCopies; ++m) {
+      const int p = lo + q * kOuterRows + tid / kPieces + m * kApart;
+      rows[m] = p < hi ? a.seg.row(p) : -1;
     }
   };
-  // pairs of ranks of v, two a thread of the first RT * 16 pairs
+  auto load_x = [&](int slot) {
+#pragma unroll
+    for (int m = 0; m < kCopies; ++m) {
+      const int i = tid / kPieces + m * kApart;
+      stage_piece<T>(base + slot * kX + i * (kCols * 2) + ((piece ^ (i % 8)) * 16),
+                     static_cast<const T*>(s.x) + (rows[m] >= 0 ? rows[m] * s.ldx : 0),
+                     n0 / 8 + piece, s.n, s.vec, rows[m] >= 0);
+    }
+  };
+  // pairs of ranks of v (that of a position without a row is zero)
   constexpr int kPairs = kOuterRows * RT / 2, kMine = (kPairs + kOuterThreads - 1) / kOuterThreads;
   float2 v[kMine];
   auto load_v = [&](int q) {
@@ -661,7 +675,7 @@ __global__ void __launch_bounds__(kOuterThreads) adapters_outer_kernel(OuterArgs
     for (int m = 0; m < kMine; ++m) {
       const int e = tid + m * kOuterThreads, i = e / (RT / 2), k = e % (RT / 2) * 2;
       const int p = lo + q * kOuterRows + i;
-      const bool in = e < kPairs && p < hi && a.seg.row(p) >= 0;
+      const bool in = e < kPairs && p < hi;
       v[m].x = in && k < r ? s.v[(int64_t)p * r + k] * up : 0.f;
       v[m].y = in && k + 1 < r ? s.v[(int64_t)p * r + k + 1] * up : 0.f;
     }
@@ -687,9 +701,11 @@ __global__ void __launch_bounds__(kOuterThreads) adapters_outer_kernel(OuterArgs
   };
   float acc[RT / 16][kWarpCols / 8][4] = {};
   if (q0 < q1) load_v(q0);
+  if (q0 < q1) load_rows(q0);
 #pragma unroll
   for (int i = 0; i < kOuterStages - 1; ++i) {
-    if (q0 + i < q1) load_x(q0 + i, i);
+    if (q0 + i < q1) load_x(i);
+    if (q0 + i + 1 < q1) load_rows(q0 + i + 1);
     cp_async_commit();
   }
   for (int q = q0; q < q1; ++q) {
@@ -698,8 +714,9 @@ __global__ void __launch_bounds__(kOuterThreads) adapters_outer_kernel(OuterArgs
     cp_async_wait<kOuterStages - 2>();
     __syncthreads();
     const int ahead = q + kOuterStages - 1;
-    if (ahead < q1) load_x(ahead, (ahead - q0) % kOuterStages);
+    if (ahead < q1) load_x((ahead - q0) % kOuterStages);
     cp_async_commit();
+    if (ahead + 1 < q1) load_rows(ahead + 1);
     if (q + 1 < q1) load_v(q + 1);
     const uint32_t xs = base + (q - q0) % kOuterStages * kX;
     const uint32_t vs = planes + buf * kTerm * kPlane;
@@ -791,9 +808,9 @@ int adapter_tiles(const AdapterArgs& a, int rows) {
 }
 int shrink_cluster(const AdapterArgs& a, int num_sms) {
   const int rows = shrink_rows(a.r);
-  // two (three) CTAs an SM hold the tiles of 128 (64) positions
+  // two CTAs of 128 positions fit an SM, four of 64
   return adapters_split((a.seg.T + rows - 1) / rows, (a.K + 63) / 64,
-                        (rows == 64 ? 3LL : 2LL) * num_sms, 4);
+                        (rows == 64 ? 4LL : 2LL) * num_sms, 4);
 }
 
 template <typename T, int RT>
@@ -807,10 +824,12 @@ void launch_tiles(const Launch& L, const AdapterArgs& a, int rt_slot) {
                         dim3(S), dim3(2 * kShrinkRows<RT>), shrink_smem<RT>(), L.stream, a);
   launch_end(L, MOE_K_ADAPTERS);
   if (!a.y) return;
-  // ranges of whole tiles of columns, for about two rounds of CTAs
-  const int blocks = (a.seg.T + kExpandRows - 1) / kExpandRows;
+  // ranges of whole tiles of columns, for one round of two CTAs an SM: a CTA has about as long
+  // to start (tile, rows, v) as for two tiles of columns
+  const int blocks = (a.seg.T + kExpandRows - 1) / kExpandRows + std::min(a.seg.J, a.seg.T) / 2;
   const int tiles = (a.N + kExpandTile - 1) / kExpandTile;
-  const int per = std::max(1, (int)((int64_t)tiles * blocks / (4LL * L.num_sms)));
+  const int ranges = std::max(1, std::min(tiles, 2 * L.num_sms / blocks));
+  const int per = (tiles + ranges - 1) / ranges;
   constexpr int kSmem = 2 * RT * kExpandTile * 2;
   set_smem_attr_once(reinterpret_cast<const void*>(adapters_expand_kernel<T, RT>), kSmem,
                      kAttrAdapters + 8 * type + 4 + rt_slot);
@@ -828,8 +847,19 @@ void launch_outer(const Launch& L, OuterArgs a, int rt_slot) {
     s.tiles = (s.n + kOuterCols<RT> - 1) / kOuterCols<RT>;
     tiles += s.tiles;
   }
-  const int S = adapters_split((int64_t)tiles * a.seg.J,
-                               std::max(1, a.seg.T / a.seg.J / kOuterRows), 4LL * L.num_sms, 4);
+  // the split of an adapter's positions with the least time by a count of stages: rounds of
+  // two CTAs an SM, each of its stages and about four more to start and to add the parts
+  const int64_t clusters = (int64_t)tiles * a.seg.J, slots = 2LL * L.num_sms;
+  const int64_t stages = std::max(1, a.seg.T / a.seg.J / kOuterRows);
+  int S = 1;
+  int64_t least = INT64_MAX;
+  for (int q = 1; q <= kMaxCluster; q *= 2) {
+    const int64_t cost = (clusters * q + slots - 1) / slots * ((stages + q - 1) / q + 4);
+    if (cost < least) {
+      least = cost;
+      S = q;
+    }
+  }
   set_smem_attr_once(reinterpret_cast<const void*>(adapters_outer_kernel<T, RT>),
                      outer_smem<T, RT>(), kAttrAdapters + 16 + 4 * type + rt_slot);
   launch_begin(L, MOE_K_ADAPTERS_GRAD);
