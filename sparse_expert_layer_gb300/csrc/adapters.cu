@@ -429,6 +429,8 @@ __global__ void __launch_bounds__(2 * kShrinkRows<RT>) adapters_shrink_kernel(Ad
 // ------------------------------------------------------------------ expand ----
 constexpr int kExpandRows = 128;
 constexpr int kExpandThreads = 256;
+template <int RT>
+constexpr int kExpandPerSm = RT <= 32 ? 3 : RT == 64 ? 2 : 1;  // CTAs
 constexpr int kExpandTile = 256;  // columns of the second matrix in shared memory at once
 
 // y of a tile of one adapter's positions and a range of columns; a warp has 16 positions.  The
@@ -436,10 +438,12 @@ constexpr int kExpandTile = 256;  // columns of the second matrix in shared memo
 // neighbours: pair t of 16-byte piece q belongs to n-tile t, columns 2 (q % 4) and the next.
 // Tiles of the second matrix are copied one ahead, base is read two chunks of 32 ahead.
 template <typename T, int RT>
-__global__ void __launch_bounds__(kExpandThreads) adapters_expand_kernel(AdapterArgs a, int range) {
+__global__ void __launch_bounds__(kExpandThreads, kExpandPerSm<RT>)
+    adapters_expand_kernel(AdapterArgs a, int range) {
   pdl_enter();
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int kTile = RT * kExpandTile * 2, kChunks = kExpandTile / 32;
+  constexpr bool kHalf = std::is_same<T, __half>::value;
   const uint32_t mt = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g = lane / 4, tg = lane % 4;
   const int r = a.r, n_begin = blockIdx.x * range, n_end = min(a.N, n_begin + range);
@@ -521,8 +525,8 @@ __global__ void __launch_bounds__(kExpandThreads) adapters_expand_kernel(Adapter
         ma = fmaxf(ma, fabsf(f[k][q]));
         mb = fmaxf(mb, fabsf(f[k][4 + q]));
       }
-    float upa = 1.f, upb = 1.f;
-    if constexpr (std::is_same<T, __half>::value) {  // into fp16's range, row by row
+    float upa = sa, upb = sb;  // bf16: the MMAs add scale * v * b to the base themselves
+    if constexpr (kHalf) {     // into fp16's range, row by row; scaled back afterwards
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) {
         ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
@@ -559,7 +563,18 @@ __global__ void __launch_bounds__(kExpandThreads) adapters_expand_kernel(Adapter
       next[0][0] = next[1][0], next[0][1] = next[1][1];
       load_base((n0 - n_begin) / 32 + c + 2, next[1]);
       if (n0 + c * 32 >= n_end) break;
-      float d[4][4] = {};
+      float fa[8], fb[8], d[4][4] = {};
+      unpack_piece<T>(qa, fa);
+      unpack_piece<T>(qb, fb);
+      if constexpr (!kHalf) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            d[t][h] = fa[2 * t + h];
+            d[t][2 + h] = fb[2 * t + h];
+          }
+      }
 #pragma unroll
       for (int k = 0; k < RT / 16; ++k) {
         const int i = k * 16 + lane % 16;
@@ -577,15 +592,12 @@ __global__ void __launch_bounds__(kExpandThreads) adapters_expand_kernel(Adapter
           }
         }
       }
-      float fa[8], fb[8];
-      unpack_piece<T>(qa, fa);
-      unpack_piece<T>(qb, fb);
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          fa[2 * t + h] = fmaf(sa, d[t][h], fa[2 * t + h]);
-          fb[2 * t + h] = fmaf(sb, d[t][2 + h], fb[2 * t + h]);
+          fa[2 * t + h] = kHalf ? fmaf(sa, d[t][h], fa[2 * t + h]) : d[t][h];
+          fb[2 * t + h] = kHalf ? fmaf(sb, d[t][2 + h], fb[2 * t + h]) : d[t][2 + h];
         }
       if (ina) store_piece<T>(ya, piece, a.N, a.yvec, fa);
       if (inb) store_piece<T>(yb, piece, a.N, a.yvec, fb);
@@ -614,6 +626,8 @@ constexpr int kOuterRows = 32;  // positions of a stage
 constexpr int kOuterStages = 4;
 template <int RT>
 constexpr int kOuterCols = RT <= 64 ? 256 : 128;
+template <int RT>
+constexpr int kOuterPerSm = RT == 16 ? 3 : RT <= 64 ? 2 : 1;  // CTAs
 // 16-bit terms of v: bf16 three (24 bits), fp16 two (22 bits)
 template <typename T>
 constexpr int kTerms = std::is_same<T, __half>::value ? 2 : 3;
@@ -621,7 +635,7 @@ constexpr int kTerms = std::is_same<T, __half>::value ? 2 : 3;
 // Sums over the positions of an adapter, a tile of columns for all ranks.  The MMAs' rows
 // are the ranks, their K the positions: v and x are both read transposed.
 template <typename T, int RT>
-__global__ void __launch_bounds__(kOuterThreads) adapters_outer_kernel(OuterArgs a) {
+__global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer_kernel(OuterArgs a) {
   pdl_enter();
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int kCols = kOuterCols<RT>, kPieces = kCols / 8;
@@ -669,15 +683,15 @@ __global__ void __launch_bounds__(kOuterThreads) adapters_outer_kernel(OuterArgs
   };
   // pairs of ranks of v (that of a position without a row is zero)
   constexpr int kPairs = kOuterRows * RT / 2, kMine = (kPairs + kOuterThreads - 1) / kOuterThreads;
-  float2 v[kMine];
-  auto load_v = [&](int q) {
+  float2 v[kMine] = {};
+  auto load_v = [&](int q, float2 (&to)[kMine]) {
 #pragma unroll
     for (int m = 0; m < kMine; ++m) {
       const int e = tid + m * kOuterThreads, i = e / (RT / 2), k = e % (RT / 2) * 2;
       const int p = lo + q * kOuterRows + i;
       const bool in = e < kPairs && p < hi;
-      v[m].x = in && k < r ? s.v[(int64_t)p * r + k] * up : 0.f;
-      v[m].y = in && k + 1 < r ? s.v[(int64_t)p * r + k + 1] * up : 0.f;
+      to[m].x = in && k < r ? s.v[(int64_t)p * r + k] : 0.f;
+      to[m].y = in && k + 1 < r ? s.v[(int64_t)p * r + k + 1] : 0.f;
     }
   };
   auto store_v = [&](int buf) {
@@ -688,7 +702,7 @@ __global__ void __launch_bounds__(kOuterThreads) adapters_outer_kernel(OuterArgs
       // 16-byte pieces swizzled by position, as far as a row has them
       const uint32_t at = planes + buf * kTerm * kPlane + i * kVRow +
                           (((k / 8) ^ (i % (RT / 8 < 8 ? RT / 8 : 8))) * 16) + k % 8 * 2;
-      float x = v[m].x, y = v[m].y;
+      float x = v[m].x * up, y = v[m].y * up;
 #pragma unroll
       for (int t = 0; t < kTerm; ++t) {
         const uint32_t w = pack2<T>(x, y);
@@ -700,7 +714,10 @@ __global__ void __launch_bounds__(kOuterThreads) adapters_outer_kernel(OuterArgs
     }
   };
   float acc[RT / 16][kWarpCols / 8][4] = {};
-  if (q0 < q1) load_v(q0);
+  // v two stages ahead: `later` is that of the stage after the next
+  float2 later[kMine] = {};
+  if (q0 < q1) load_v(q0, v);
+  if (q0 + 1 < q1) load_v(q0 + 1, later);
   if (q0 < q1) load_rows(q0);
 #pragma unroll
   for (int i = 0; i < kOuterStages - 1; ++i) {
@@ -717,7 +734,9 @@ __global__ void __launch_bounds__(kOuterThreads) adapters_outer_kernel(OuterArgs
     if (ahead < q1) load_x((ahead - q0) % kOuterStages);
     cp_async_commit();
     if (ahead + 1 < q1) load_rows(ahead + 1);
-    if (q + 1 < q1) load_v(q + 1);
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) v[m] = later[m];
+    if (q + 2 < q1) load_v(q + 2, later);
     const uint32_t xs = base + (q - q0) % kOuterStages * kX;
     const uint32_t vs = planes + buf * kTerm * kPlane;
 #pragma unroll
@@ -824,11 +843,11 @@ void launch_tiles(const Launch& L, const AdapterArgs& a, int rt_slot) {
                         dim3(S), dim3(2 * kShrinkRows<RT>), shrink_smem<RT>(), L.stream, a);
   launch_end(L, MOE_K_ADAPTERS);
   if (!a.y) return;
-  // ranges of whole tiles of columns, for one round of two CTAs an SM: a CTA has about as long
+  // ranges of whole tiles of columns, for one round of CTAs: a CTA has about as long
   // to start (tile, rows, v) as for two tiles of columns
   const int blocks = (a.seg.T + kExpandRows - 1) / kExpandRows + std::min(a.seg.J, a.seg.T) / 2;
   const int tiles = (a.N + kExpandTile - 1) / kExpandTile;
-  const int ranges = std::max(1, std::min(tiles, 2 * L.num_sms / blocks));
+  const int ranges = std::max(1, std::min(tiles, kExpandPerSm<RT> * L.num_sms / blocks));
   const int per = (tiles + ranges - 1) / ranges;
   constexpr int kSmem = 2 * RT * kExpandTile * 2;
   set_smem_attr_once(reinterpret_cast<const void*>(adapters_expand_kernel<T, RT>), kSmem,
@@ -848,8 +867,8 @@ void launch_outer(const Launch& L, OuterArgs a, int rt_slot) {
     tiles += s.tiles;
   }
   // the split of an adapter's positions with the least time by a count of stages: rounds of
-  // two CTAs an SM, each of its stages and about four more to start and to add the parts
-  const int64_t clusters = (int64_t)tiles * a.seg.J, slots = 2LL * L.num_sms;
+  // CTAs, each of its stages and about four more to start and to add the parts
+  const int64_t clusters = (int64_t)tiles * a.seg.J, slots = (int64_t)kOuterPerSm<RT> * L.num_sms;
   const int64_t stages = std::max(1, a.seg.T / a.seg.J / kOuterRows);
   int S = 1;
   int64_t least = INT64_MAX;
