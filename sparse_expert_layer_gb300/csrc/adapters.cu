@@ -436,7 +436,7 @@ constexpr int kExpandTile = 256;  // columns of the second matrix in shared memo
 // y of a tile of one adapter's positions and a range of columns; a warp has 16 positions.  The
 // columns of 32 are dealt to the four n-tiles of MMAs so that a lane's results are eight
 // neighbours: pair t of 16-byte piece q belongs to n-tile t, columns 2 (q % 4) and the next.
-// Tiles of the second matrix are copied one ahead, base is read two chunks of 32 ahead.
+// Tiles of the second matrix are copied one ahead, base is read two or four chunks ahead.
 template <typename T, int RT>
 __global__ void __launch_bounds__(kExpandThreads, kExpandPerSm<RT>)
     adapters_expand_kernel(AdapterArgs a, int range) {
@@ -505,9 +505,10 @@ __global__ void __launch_bounds__(kExpandThreads, kExpandPerSm<RT>)
       if (inb) q[1] = load_piece<T>(bb, piece, a.N, a.yvec);
     }
   };
-  uint4 next[2][2];
-  load_base(0, next[0]);
-  load_base(1, next[1]);
+  constexpr int kAhead = RT <= 32 ? 2 : 4;
+  uint4 next[kAhead][2];
+#pragma unroll
+  for (int c = 0; c < kAhead; ++c) load_base(c, next[c]);
   // the rows' v as two 16-bit terms
   uint32_t hi_t[RT / 16][4], lo_t[RT / 16][4];
   float sa = a.scale2 ? a.scale2[j] : 1.f, sb = sa;
@@ -556,12 +557,11 @@ __global__ void __launch_bounds__(kExpandThreads, kExpandPerSm<RT>)
     cp_async_commit();
     if (!mine) continue;
     const uint32_t tile = mt + buf * kTile;
-#pragma unroll 2
+#pragma unroll kAhead
     for (int c = 0; c < kChunks; ++c) {
       const int piece = n0 / 8 + c * 4 + tg;
-      const uint4 qa = next[0][0], qb = next[0][1];
-      next[0][0] = next[1][0], next[0][1] = next[1][1];
-      load_base((n0 - n_begin) / 32 + c + 2, next[1]);
+      const uint4 qa = next[c % kAhead][0], qb = next[c % kAhead][1];
+      load_base((n0 - n_begin) / 32 + c + kAhead, next[c % kAhead]);
       if (n0 + c * 32 >= n_end) break;
       float fa[8], fb[8], d[4][4] = {};
       unpack_piece<T>(qa, fa);
@@ -623,7 +623,8 @@ struct OuterArgs {
 
 constexpr int kOuterThreads = 256;
 constexpr int kOuterRows = 32;  // positions of a stage
-constexpr int kOuterStages = 4;
+constexpr int kOuterStages = 3;
+constexpr int kOuterAhead = 32;  // stages whose rows are looked up at once
 template <int RT>
 constexpr int kOuterCols = RT <= 64 ? 256 : 128;
 template <int RT>
@@ -640,14 +641,18 @@ __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int kCols = kOuterCols<RT>, kPieces = kCols / 8;
   constexpr int kX = kOuterRows * kCols * 2;
-  constexpr int kVRow = RT * 2, kPlane = kOuterRows * kVRow, kTerm = kTerms<T>;
+  // rows of v 16 bytes longer than they are: eight lie side by side in the banks
+  constexpr int kVRow = RT * 2 + 16, kPlane = kOuterRows * kVRow, kTerm = kTerms<T>;
   constexpr int kWarpCols = kCols / 8;  // of each of the eight warps
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int rank = blockIdx.x, S = gridDim.x, j = blockIdx.z, r = a.r;
   const bool second = (int)blockIdx.y >= a.side[0].tiles;
   const OuterSide& s = a.side[second];
   const int n0 = (blockIdx.y - (second ? a.side[0].tiles : 0)) * kCols;
-  const uint32_t base = smem_u32(smem), planes = base + kOuterStages * kX;
+  constexpr int kV = kOuterRows * RT * 4;
+  const uint32_t base = smem_u32(smem), vring = base + kOuterStages * kX;
+  const uint32_t planes = vring + kOuterStages * kV;
+  int* rows = reinterpret_cast<int*>(smem + kOuterStages * (kX + kV) + 2 * kTerm * kPlane);
   const int lo = a.seg.at(j), hi = max(lo, a.seg.at(j + 1));
   // this rank's positions: whole stages
   const int stages = (hi - lo + kOuterRows - 1) / kOuterRows;
@@ -660,84 +665,93 @@ __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer
     up = __uint_as_float(bits);
     down *= inverse_pow2(bits);
   }
-  // The rows of a stage's positions that this thread copies a piece of: read a stage before
-  // their copies are made.
-  constexpr int kCopies = kOuterRows * kPieces / kOuterThreads, kApart = kOuterThreads / kPieces;
-  const int piece = tid % kPieces;
-  int rows[kCopies];
-  auto load_rows = [&](int q) {
-#pragma unroll
-    for (int m = 0; m < kCopies; ++m) {
-      const int p = lo + q * kOuterRows + tid / kPieces + m * kApart;
-      rows[m] = p < hi ? a.seg.row(p) : -1;
+  // The rows of the positions, kOuterAhead stages at once, in two buffers.
+  auto look_up = [&](int q) {
+    int* to = rows + (q - q0) / kOuterAhead % 2 * kOuterAhead * kOuterRows;
+    for (int e = tid; e < kOuterAhead * kOuterRows; e += kOuterThreads) {
+      const int p = lo + q * kOuterRows + e;
+      to[e] = p < hi ? a.seg.row(p) : -1;
     }
   };
-  auto load_x = [&](int slot) {
+  // A stage's pieces of x, and four ranks of v at once by the threads that split them (those
+  // of a position without a row are zero).
+  constexpr int kQuads = kOuterRows * RT / 4, kMine = (kQuads + kOuterThreads - 1) / kOuterThreads;
+  const bool vvec = r % 4 == 0;
+  auto load = [&](int q, int slot) {
+    const int* from = rows + (q - q0) % (2 * kOuterAhead) * kOuterRows;
 #pragma unroll
-    for (int m = 0; m < kCopies; ++m) {
-      const int i = tid / kPieces + m * kApart;
+    for (int m = 0; m < kOuterRows * kPieces / kOuterThreads; ++m) {
+      const int i = tid / kPieces + m * (kOuterThreads / kPieces), piece = tid % kPieces;
+      const int row = from[i];
       stage_piece<T>(base + slot * kX + i * (kCols * 2) + ((piece ^ (i % 8)) * 16),
-                     static_cast<const T*>(s.x) + (rows[m] >= 0 ? rows[m] * s.ldx : 0),
-                     n0 / 8 + piece, s.n, s.vec, rows[m] >= 0);
+                     static_cast<const T*>(s.x) + (row >= 0 ? row * s.ldx : 0), n0 / 8 + piece, s.n,
+                     s.vec, row >= 0);
     }
-  };
-  // pairs of ranks of v (that of a position without a row is zero)
-  constexpr int kPairs = kOuterRows * RT / 2, kMine = (kPairs + kOuterThreads - 1) / kOuterThreads;
-  float2 v[kMine] = {};
-  auto load_v = [&](int q, float2 (&to)[kMine]) {
 #pragma unroll
     for (int m = 0; m < kMine; ++m) {
-      const int e = tid + m * kOuterThreads, i = e / (RT / 2), k = e % (RT / 2) * 2;
+      const int e = tid + m * kOuterThreads, i = e / (RT / 4), k = e % (RT / 4) * 4;
+      if (e >= kQuads) break;
       const int p = lo + q * kOuterRows + i;
-      const bool in = e < kPairs && p < hi;
-      to[m].x = in && k < r ? s.v[(int64_t)p * r + k] : 0.f;
-      to[m].y = in && k + 1 < r ? s.v[(int64_t)p * r + k + 1] : 0.f;
+      const uint32_t to = vring + slot * kV + e * 16;
+      const float* at = s.v + (int64_t)p * r + k;
+      if (vvec) {
+        const bool in = p < hi && k < r;
+        cp_async16_or_zero(to, in ? at : s.v, in);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const bool in = p < hi && k + c < r;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + 4 * c),
+                       "l"(in ? at + c : s.v), "r"(in ? 4 : 0)
+                       : "memory");
+        }
+      }
     }
   };
-  auto store_v = [&](int buf) {
+  auto split_v = [&](int slot, int buf) {
 #pragma unroll
     for (int m = 0; m < kMine; ++m) {
-      const int e = tid + m * kOuterThreads, i = e / (RT / 2), k = e % (RT / 2) * 2;
-      if (e >= kPairs) break;
-      // 16-byte pieces swizzled by position, as far as a row has them
-      const uint32_t at = planes + buf * kTerm * kPlane + i * kVRow +
-                          (((k / 8) ^ (i % (RT / 8 < 8 ? RT / 8 : 8))) * 16) + k % 8 * 2;
-      float x = v[m].x * up, y = v[m].y * up;
+      const int e = tid + m * kOuterThreads, i = e / (RT / 4), k = e % (RT / 4) * 4;
+      if (e >= kQuads) break;
+      float f[4];
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
+                   : "r"(vring + slot * kV + e * 16)
+                   : "memory");
+#pragma unroll
+      for (int c = 0; c < 4; ++c) f[c] *= up;
+      const uint32_t at = planes + buf * kTerm * kPlane + i * kVRow + k * 2;
 #pragma unroll
       for (int t = 0; t < kTerm; ++t) {
-        const uint32_t w = pack2<T>(x, y);
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + t * kPlane), "r"(w) : "memory");
-        const float2 f = unpack2<T>(w);
-        x -= f.x;
-        y -= f.y;
+        const uint32_t w0 = pack2<T>(f[0], f[1]), w1 = pack2<T>(f[2], f[3]);
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + t * kPlane), "r"(w0), "r"(w1)
+                     : "memory");
+        const float2 g0 = unpack2<T>(w0), g1 = unpack2<T>(w1);
+        f[0] -= g0.x;
+        f[1] -= g0.y;
+        f[2] -= g1.x;
+        f[3] -= g1.y;
       }
     }
   };
   float acc[RT / 16][kWarpCols / 8][4] = {};
-  // v two stages ahead: `later` is that of the stage after the next
-  float2 later[kMine] = {};
-  if (q0 < q1) load_v(q0, v);
-  if (q0 + 1 < q1) load_v(q0 + 1, later);
-  if (q0 < q1) load_rows(q0);
+  look_up(q0);
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < kOuterStages - 1; ++i) {
-    if (q0 + i < q1) load_x(i);
-    if (q0 + i + 1 < q1) load_rows(q0 + i + 1);
+    if (q0 + i < q1) load(q0 + i, i);
     cp_async_commit();
   }
   for (int q = q0; q < q1; ++q) {
-    const int buf = (q - q0) & 1;
-    store_v(buf);
+    const int buf = (q - q0) & 1, slot = (q - q0) % kOuterStages;
     cp_async_wait<kOuterStages - 2>();
+    split_v(slot, buf);  // what this thread copied
     __syncthreads();
     const int ahead = q + kOuterStages - 1;
-    if (ahead < q1) load_x((ahead - q0) % kOuterStages);
+    if (ahead < q1) load(ahead, (ahead - q0) % kOuterStages);
     cp_async_commit();
-    if (ahead + 1 < q1) load_rows(ahead + 1);
-#pragma unroll
-    for (int m = 0; m < kMine; ++m) v[m] = later[m];
-    if (q + 2 < q1) load_v(q + 2, later);
-    const uint32_t xs = base + (q - q0) % kOuterStages * kX;
+    if ((q - q0) % kOuterAhead == 0 && q + kOuterAhead < q1) look_up(q + kOuterAhead);
+    const uint32_t xs = base + slot * kX;
     const uint32_t vs = planes + buf * kTerm * kPlane;
 #pragma unroll
     for (int kk = 0; kk < kOuterRows / 16; ++kk) {
@@ -754,9 +768,7 @@ __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer
           uint32_t af[4];
           // (ranks 0-7, positions 0-7) (8-15, 0-7) (0-7, 8-15) (8-15, 8-15)
           const int i = kk * 16 + lane % 8 + lane / 16 * 8, piece = m * 2 + lane / 8 % 2;
-          ldsm4_trans(vs + t * kPlane + i * kVRow +
-                          ((piece ^ (i % (RT / 8 < 8 ? RT / 8 : 8))) * 16),
-                      af);
+          ldsm4_trans(vs + t * kPlane + i * kVRow + piece * 16, af);
 #pragma unroll
           for (int c = 0; c < kWarpCols / 16; ++c) {
             mma16816<T>(acc[m][2 * c], af[0], af[1], af[2], af[3], bf[c][0], bf[c][1]);
@@ -796,8 +808,8 @@ __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer
 // ------------------------------------------------------------------ launch --
 template <typename T, int RT>
 constexpr int outer_smem() {
-  const int rings = kOuterStages * kOuterRows * kOuterCols<RT> * 2 +
-                    2 * kTerms<T> * kOuterRows * RT * 2;
+  const int rings = kOuterStages * kOuterRows * (kOuterCols<RT> * 2 + RT * 4) +
+                    2 * kTerms<T> * kOuterRows * (RT * 2 + 16) + 2 * kOuterAhead * kOuterRows * 4;
   return std::max(rings, RT * kOuterCols<RT> * 4);
 }
 template <int RT>
@@ -872,7 +884,7 @@ void launch_outer(const Launch& L, OuterArgs a, int rt_slot) {
   const int64_t stages = std::max(1, a.seg.T / a.seg.J / kOuterRows);
   int S = 1;
   int64_t least = INT64_MAX;
-  for (int q = 1; q <= kMaxCluster; q *= 2) {
+  for (int q = 1; q <= kMaxCluster; ++q) {
     const int64_t cost = (clusters * q + slots - 1) / slots * ((stages + q - 1) / q + 4);
     if (cost < least) {
       least = cost;
