@@ -192,7 +192,6 @@ template <typename T>
 __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(AdapterArgs a) {
   pdl_enter();
   __shared__ float part[kMaxRank], total[kMaxRank];
-  __shared__ float columns[kRowWarps][32 * 8];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int rank = blockIdx.x, C = gridDim.x, p = blockIdx.y, r = a.r;
   const int j = a.seg.first_after(p);
@@ -227,23 +226,32 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(AdapterArgs a
   const T* m1 = static_cast<const T*>(a.m1) + (int64_t)j * r * a.K;
   const int k8 = (a.K + 7) / 8, kp = (k8 + C - 1) / C;
   const int k0 = min(k8, rank * kp), k1 = min(k8, k0 + kp);
-  constexpr int kRanks = 4;  // of a warp at once
+  constexpr int kRanks = 4, kAtOnce = 4;  // ranks of a warp, pieces of a lane in flight
   for (int i0 = warp * kRanks; i0 < r; i0 += kRowWarps * kRanks) {
     float acc[kRanks] = {};
-    for (int k = k0 + lane; k < k1; k += 32) {
-      const uint4 xq = load_piece<T>(xrow, k, a.K, a.xvec);
-      uint4 mq[kRanks];
+    for (int kb = k0; kb < k1; kb += 32 * kAtOnce) {
+      uint4 xq[kAtOnce], mq[kAtOnce][kRanks];
 #pragma unroll
-      for (int i = 0; i < kRanks; ++i)
-        mq[i] = i0 + i < r ? load_piece<T>(m1 + (int64_t)(i0 + i) * a.K, k, a.K, a.m1vec)
-                           : make_uint4(0u, 0u, 0u, 0u);
-      float xf[8], mf[8];
-      unpack_piece<T>(xq, xf);
+      for (int q = 0; q < kAtOnce; ++q) {
+        const int k = kb + q * 32 + lane;
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+        xq[q] = k < k1 ? load_piece<T>(xrow, k, a.K, a.xvec) : none;
 #pragma unroll
-      for (int i = 0; i < kRanks; ++i) {
-        unpack_piece<T>(mq[i], mf);
+        for (int i = 0; i < kRanks; ++i)
+          mq[q][i] = k < k1 && i0 + i < r
+                         ? load_piece<T>(m1 + (int64_t)(i0 + i) * a.K, k, a.K, a.m1vec)
+                         : none;
+      }
 #pragma unroll
-        for (int c = 0; c < 8; ++c) acc[i] = fmaf(xf[c], mf[c], acc[i]);
+      for (int q = 0; q < kAtOnce; ++q) {
+        float xf[8], mf[8];
+        unpack_piece<T>(xq[q], xf);
+#pragma unroll
+        for (int i = 0; i < kRanks; ++i) {
+          unpack_piece<T>(mq[q][i], mf);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) acc[i] = fmaf(xf[c], mf[c], acc[i]);
+        }
       }
     }
 #pragma unroll
@@ -275,36 +283,35 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(AdapterArgs a
       a.max_other[p * C + rank] = most_other;
     }
   }
-  cluster_sync_all();  // (also: no CTA leaves while another reads its part)
-  if (!a.y) return;
-  for (int c0 = n0; c0 < n1; c0 += 32) {
-    const int i = c0 + lane;
-    float acc[8] = {};
-    if (i < n1)
-#pragma unroll 4
-      for (int q = warp; q < r; q += kRowWarps) {
-        float f[8];
-        unpack_piece<T>(load_piece<T>(m2 + (int64_t)q * a.N, i, a.N, a.m2vec), f);
+  __syncthreads();
+  // (no CTA leaves while another reads its part: waited for at the end)
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  // a lane has eight columns and adds up all ranks
+  for (int i = n0 + tid; i < n1 && a.y; i += kRowThreads) {
+    float f[8] = {}, acc[8] = {};
+    const uint4 bq = brow ? load_piece<T>(brow, i, a.N, a.yvec) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+    for (int q0 = 0; q0 < r; q0 += 8) {
+      uint4 mq[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) acc[c] = fmaf(total[q], f[c], acc[c]);
+      for (int q = 0; q < 8; ++q)
+        mq[q] = q0 + q < r ? load_piece<T>(m2 + (int64_t)(q0 + q) * a.N, i, a.N, a.m2vec)
+                           : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        float m[8];
+        unpack_piece<T>(mq[q], m);
+        const float v = q0 + q < r ? total[q0 + q] : 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] = fmaf(v, m[c], acc[c]);
       }
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < 8; ++c) columns[warp][c * 32 + lane] = acc[c];
-    __syncthreads();
-    if (warp == 0 && i < n1) {
-      float f[8] = {};
-      if (brow) unpack_piece<T>(load_piece<T>(brow, i, a.N, a.yvec), f);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < kRowWarps; ++w) s += columns[w][c * 32 + lane];
-        f[c] = fmaf(s2, s, f[c]);
-      }
-      store_piece<T>(yrow, i, a.N, a.yvec, f);
     }
+    unpack_piece<T>(bq, f);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) f[c] = fmaf(s2, acc[c], f[c]);
+    store_piece<T>(yrow, i, a.N, a.yvec, f);
   }
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ shrink ----
@@ -825,9 +832,15 @@ int adapters_split(int64_t clusters, int64_t units, int64_t most, int64_t least)
   return s;
 }
 
-// One position a cluster for as many positions as this, or where adapters have few.
-constexpr int kRowPositions = 64;
-bool adapters_by_rows(int T, int J) { return T <= kRowPositions || T <= 2 * J; }
+// One position a cluster, or tiles of positions.  By rows every row reads its adapter again
+// (from L2): cheap while that is little, or where adapters have about a row each.  Rank 16,
+// 5120 to 5120 channels: 64 rows 9 us; 128 rows (21 M products) 15.6 us against 15.3 in tiles;
+// 256 rows 28.8 against 16.1.  100 rows, 1000 to 1000 channels (3.2 M): 7.1 against 12.0.
+constexpr int64_t kRowWork = 18 << 20;
+bool adapters_by_rows(const AdapterArgs& a) {
+  const int64_t T = a.seg.T;
+  return T <= 2 * a.seg.J || (T <= 4096 && T * a.r * (a.K + a.N) <= kRowWork);
+}
 
 int row_cluster(const AdapterArgs& a) {
   // slices of at least 256 channels
@@ -904,7 +917,7 @@ template <typename T>
 void launch_adapters(const Launch& L, const AdapterArgs& a, OuterArgs* outer) {
   const int slot = a.r <= 16 ? 0 : a.r <= 32 ? 1 : a.r <= 64 ? 2 : 3;
   if (a.seg.T == 0) {
-  } else if (adapters_by_rows(a.seg.T, a.seg.J)) {
+  } else if (adapters_by_rows(a)) {
     const int C = row_cluster(a);
     launch_begin(L, MOE_K_ADAPTERS);
     launch_kernel_cluster(adapters_row_kernel<T>, dim3(C, a.seg.T), dim3(C), dim3(kRowThreads), 0,
