@@ -54,82 +54,134 @@ __device__ __forceinline__ int clip_find(const ClipList<N>& l, int chunk) {
   return lo;
 }
 
-// f(word, its elements as fp32) for the thread's words of a chunk; elements
-// outside the tensor are zeros.  Loads of the chunk's words are issued together.
-template <typename T, typename F>
-__device__ __forceinline__ void clip_words(const ClipTensor& t, int64_t word0, F f) {
-  constexpr int kPer = 16 / sizeof(T);
-  const int64_t words = (t.n + 15) / 16;
-  uint4 v[kClipUnroll];
+template <typename T>
+__device__ __forceinline__ void clip_unpack(const uint4& q, float (&x)[16 / sizeof(T)]) {
+  if constexpr (sizeof(T) == 4) {
+    memcpy(x, &q, 16);
+  } else {
+    const uint32_t p[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int i = 0; i < kClipUnroll; ++i) {
-    const int64_t w = word0 + threadIdx.x + i * kClipThreads, at = w * 16;
-    v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (w >= words) continue;
-    if (at >= t.skip && at + 16 <= t.n) {
-      v[i] = *reinterpret_cast<const uint4*>(t.in + at);
-    } else {  // a tensor's first or last word
-      T e[kPer];
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int64_t b = at + j * (int)sizeof(T);
-        e[j] = b >= t.skip && b < t.n ? *reinterpret_cast<const T*>(t.in + b) : from_f<T>(0.f);
-      }
-      memcpy(&v[i], e, 16);
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack2<T>(p[j]);
+      x[2 * j] = f.x;
+      x[2 * j + 1] = f.y;
     }
   }
+}
+// The product with c, as it is stored.
+template <typename T>
+__device__ __forceinline__ uint4 clip_product(const uint4& q, float c) {
+  constexpr int kPer = 16 / sizeof(T);
+  float x[kPer];
+  clip_unpack<T>(q, x);
+  uint4 r;
+  if constexpr (sizeof(T) == 4) {
+    r = make_uint4(__float_as_uint(x[0] * c), __float_as_uint(x[1] * c), __float_as_uint(x[2] * c),
+                   __float_as_uint(x[3] * c));
+  } else {
+    r = make_uint4(pack2<T>(x[0] * c, x[1] * c), pack2<T>(x[2] * c, x[3] * c),
+                   pack2<T>(x[4] * c, x[5] * c), pack2<T>(x[6] * c, x[7] * c));
+  }
+  return r;
+}
+
+// The whole words of a chunk, as indexes into it, and an element in a word that a tensor begins
+// or ends in, by the first threads.
+struct ClipRange {
+  int lo, hi;
+  int64_t at;  // the element's byte
+  bool edge;
+  __device__ __forceinline__ ClipRange(const ClipTensor& t, int64_t word0) {
+    const int64_t first = (t.skip + 15) / 16, last = t.n / 16;
+    lo = (int)max((int64_t)0, first - word0);
+    hi = (int)max((int64_t)0, min((int64_t)kClipChunk, last - word0));
+    // threads 0 .. : elements of the first word, then of the last
+    const int size = t.dtype == MOE_DT_FP32 ? 4 : 2, per = 16 / size;
+    const bool front = threadIdx.x < per;
+    const int64_t word = front ? 0 : last;
+    at = word * 16 + (int)threadIdx.x % per * size;
+    edge = threadIdx.x < 2 * per && at >= t.skip && at < t.n && word >= word0 &&
+           word < word0 + kClipChunk && (front ? t.skip > 0 : last > 0 || t.skip == 0);
+  }
+};
+__device__ __forceinline__ float clip_element(const unsigned char* p, int dtype) {
+  if (dtype == MOE_DT_FP32) return *reinterpret_cast<const float*>(p);
+  const uint16_t v = *reinterpret_cast<const uint16_t*>(p);
+  return dtype == MOE_DT_BF16 ? bf16_to_f(v) : __half2float(__ushort_as_half(v));
+}
+__device__ __forceinline__ void clip_store(unsigned char* p, int dtype, float v) {
+  if (dtype == MOE_DT_FP32)
+    *reinterpret_cast<float*>(p) = v;
+  else if (dtype == MOE_DT_BF16)
+    *reinterpret_cast<__nv_bfloat16*>(p) = from_f<__nv_bfloat16>(v);
+  else
+    *reinterpret_cast<__half*>(p) = from_f<__half>(v);
+}
+// A thread's words of a chunk, all loads in flight (words outside are zeros).
+__device__ __forceinline__ void clip_load(const ClipTensor& t, int64_t word0, const ClipRange& r,
+                                          uint4 (&v)[kClipUnroll]) {
+  const uint4* p = reinterpret_cast<const uint4*>(t.in) + word0;
 #pragma unroll
   for (int i = 0; i < kClipUnroll; ++i) {
-    const int64_t w = word0 + threadIdx.x + i * kClipThreads;
-    if (w >= words) continue;
-    float x[kPer];
-    if constexpr (sizeof(T) == 4) {
-      memcpy(x, &v[i], 16);
-    } else {
-      const uint32_t p[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 q = unpack2<T>(p[j]);
-        x[2 * j] = q.x;
-        x[2 * j + 1] = q.y;
-      }
-    }
-    f(w, x);
+    const int w = threadIdx.x + i * kClipThreads;
+    v[i] = w >= r.lo && w < r.hi ? p[w] : make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
 template <typename T>
-__device__ __forceinline__ float clip_square(const ClipTensor& t, int64_t word0) {
+__device__ __forceinline__ float clip_squares(const uint4 (&v)[kClipUnroll]) {
   constexpr int kPer = 16 / sizeof(T);
   float s[4] = {};
-  clip_words<T>(t, word0, [&](int64_t, const float(&x)[kPer]) {
+#pragma unroll
+  for (int i = 0; i < kClipUnroll; ++i) {
+    float x[kPer];
+    clip_unpack<T>(v[i], x);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) s[j % 4] = fmaf(x[j], x[j], s[j % 4]);
-  });
+  }
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
-
 template <typename T>
+__device__ __forceinline__ void clip_products(uint4* o, const ClipRange& r,
+                                              const uint4 (&v)[kClipUnroll], float c) {
+#pragma unroll
+  for (int i = 0; i < kClipUnroll; ++i) {
+    const int w = threadIdx.x + i * kClipThreads;
+    if (w >= r.lo && w < r.hi) o[w] = clip_product<T>(v[i], c);
+  }
+}
+
+__device__ __forceinline__ float clip_square(const ClipTensor& t, int64_t word0) {
+  const ClipRange r(t, word0);
+  uint4 v[kClipUnroll];
+  clip_load(t, word0, r, v);
+  float x = 0.f;
+  if (r.edge) x = clip_element(t.in + r.at, t.dtype);
+  const float s = t.dtype == MOE_DT_BF16   ? clip_squares<__nv_bfloat16>(v)
+                  : t.dtype == MOE_DT_FP16 ? clip_squares<__half>(v)
+                                           : clip_squares<float>(v);
+  return fmaf(x, x, s);
+}
+
 __device__ __forceinline__ void clip_scale(const ClipTensor& t, int64_t word0, float c) {
-  constexpr int kPer = 16 / sizeof(T);
-  const bool together = (reinterpret_cast<uintptr_t>(t.out) & 15u) == 0;
-  clip_words<T>(t, word0, [&](int64_t w, const float(&x)[kPer]) {
-    const int64_t at = w * 16;
-    T y[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) y[j] = from_f<T>(x[j] * c);
-    if (together && at >= t.skip && at + 16 <= t.n) {
-      uint4 q;
-      memcpy(&q, y, 16);
-      *reinterpret_cast<uint4*>(t.out + at) = q;
-    } else {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int64_t b = at + j * (int)sizeof(T);
-        if (b >= t.skip && b < t.n) *reinterpret_cast<T*>(t.out + b) = y[j];
-      }
-    }
-  });
+  const ClipRange r(t, word0);
+  if ((reinterpret_cast<uintptr_t>(t.out) & 15u) == 0) {
+    uint4* o = reinterpret_cast<uint4*>(t.out) + word0;
+    uint4 v[kClipUnroll];
+    clip_load(t, word0, r, v);
+    if (t.dtype == MOE_DT_BF16)
+      clip_products<__nv_bfloat16>(o, r, v, c);
+    else if (t.dtype == MOE_DT_FP16)
+      clip_products<__half>(o, r, v, c);
+    else
+      clip_products<float>(o, r, v, c);
+  } else {  // out begins at another byte of a word than in
+    const int size = t.dtype == MOE_DT_FP32 ? 4 : 2;
+    for (int64_t b = (word0 + r.lo) * 16 + threadIdx.x * size; b < (word0 + r.hi) * 16;
+         b += kClipThreads * size)
+      clip_store(t.out + b, t.dtype, clip_element(t.in + b, t.dtype) * c);
+  }
+  if (r.edge) clip_store(t.out + r.at, t.dtype, clip_element(t.in + r.at, t.dtype) * c);
 }
 
 // The block's sum of v, in every thread; added in a fixed order.
@@ -157,9 +209,7 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
     const int i = clip_find(l, c);
     const ClipTensor& t = l.t[i];
     const int64_t w = (int64_t)(c - l.first[i]) * kClipChunk;
-    sum += (double)(t.dtype == MOE_DT_BF16   ? clip_square<__nv_bfloat16>(t, w)
-                    : t.dtype == MOE_DT_FP16 ? clip_square<__half>(t, w)
-                                             : clip_square<float>(t, w));
+    sum += (double)clip_square(t, w);
   }
   sum = clip_block_sum(sum);
   if (threadIdx.x == 0) slots[blockIdx.x] = more ? slots[blockIdx.x] + sum : sum;
@@ -182,12 +232,7 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
     const ClipTensor& t = l.t[i];
     if (!t.out || (c == 1.f && t.out == t.in)) continue;
     const int64_t w = (int64_t)(chunk - l.first[i]) * kClipChunk;
-    if (t.dtype == MOE_DT_BF16)
-      clip_scale<__nv_bfloat16>(t, w, c);
-    else if (t.dtype == MOE_DT_FP16)
-      clip_scale<__half>(t, w, c);
-    else
-      clip_scale<float>(t, w, c);
+    clip_scale(t, w, c);
   }
 }
 
