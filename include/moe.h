@@ -486,11 +486,11 @@ moe_status moe_adapters_backward(int32_t T, int32_t n_adapters, int32_t r, int32
 /* Global norm of many tensors, and the tensors scaled so that it is at most max_norm:
  *   norm = sqrt(sum of the squares of all elements);  c = min(1, max_norm / (norm + eps))
  *   out = in * c for each tensor that has an out
- * A tensor's squares are added in fp32 for at most 64 elements, then in fp64 in a
- * fixed order (the same bits on every call on one device); norm and c are fp32, each
- * product is rounded once.  Where the norm is infinite c is 0 (infinite elements
- * become NaN), where it is NaN everything does; an element of 2^64 or more makes the
- * norm infinite, squares below 2^-126 lose their precision.  With c = 1 a tensor
+ * A tensor's squares are added in fp32 for at most 64 elements, then as pairs of fp32
+ * in a fixed order (the same bits on every call on one device); norm and c are fp32, each
+ * product is rounded once.  Where the norm is infinite c is 0 (infinite elements become
+ * NaN), where it is NaN everything does; a norm of 2^64 or more is infinite, squares
+ * below 2^-126 lose their precision.  With c = 1 a tensor
  * whose out is its in is not written.
  *  tensors   HOST array of n entries, read before the call returns; n >= 0
  *            in, out: contiguous, aligned to an element; out NULL (only counted), in

@@ -1,11 +1,11 @@
 // Global norm of many tensors, and the tensors times min(1, max_norm / (norm + eps)).
 //
-// Two kernels: the sums of squares, then the products.  Both walk the same list of
-// chunks of 32 KB, the first forwards and the second backwards, so that what the
-// first read last is still in L2 when the second starts there.
+// Two kernels: the sums of squares, then the products.  Each CTA has a contiguous part
+// of the list of chunks of 32 KB; the first kernel goes through it forwards and the second
+// backwards, so that what the first read last is still in L2 when the second starts there.
 //
 // The squares of a thread's 64 elements of a chunk (fp32: 32) are added in fp32, its
-// chunks and the threads in fp64, each CTA's sum in a slot of its own, and the slots
+// chunks and the threads as pairs of fp32, each CTA's sum in a slot of its own, and the slots
 // in order: the same bits on every call on one device.
 #include <math.h>
 
@@ -151,10 +151,8 @@ __device__ __forceinline__ void clip_products(uint4* o, const ClipRange& r,
   }
 }
 
-__device__ __forceinline__ float clip_square(const ClipTensor& t, int64_t word0) {
-  const ClipRange r(t, word0);
-  uint4 v[kClipUnroll];
-  clip_load(t, word0, r, v);
+__device__ __forceinline__ float clip_square(const ClipTensor& t, const ClipRange& r,
+                                             const uint4 (&v)[kClipUnroll]) {
   float x = 0.f;
   if (r.edge) x = clip_element(t.in + r.at, t.dtype);
   const float s = t.dtype == MOE_DT_BF16   ? clip_squares<__nv_bfloat16>(v)
@@ -163,12 +161,10 @@ __device__ __forceinline__ float clip_square(const ClipTensor& t, int64_t word0)
   return fmaf(x, x, s);
 }
 
-__device__ __forceinline__ void clip_scale(const ClipTensor& t, int64_t word0, float c) {
-  const ClipRange r(t, word0);
+__device__ __forceinline__ void clip_scale(const ClipTensor& t, int64_t word0, const ClipRange& r,
+                                           const uint4 (&v)[kClipUnroll], float c) {
   if ((reinterpret_cast<uintptr_t>(t.out) & 15u) == 0) {
     uint4* o = reinterpret_cast<uint4*>(t.out) + word0;
-    uint4 v[kClipUnroll];
-    clip_load(t, word0, r, v);
     if (t.dtype == MOE_DT_BF16)
       clip_products<__nv_bfloat16>(o, r, v, c);
     else if (t.dtype == MOE_DT_FP16)
@@ -184,55 +180,99 @@ __device__ __forceinline__ void clip_scale(const ClipTensor& t, int64_t word0, f
   if (r.edge) clip_store(t.out + r.at, t.dtype, clip_element(t.in + r.at, t.dtype) * c);
 }
 
+// A CTA's chunks, a contiguous part of the list, forwards or backwards.  The tensor that they
+// belong to is looked up once, kept in registers and then followed: indexed reads of the
+// parameters are slow (read for every chunk they took longer than 20 MB of data).
+template <int N, bool BACK>
+struct ClipWalk {
+  const ClipList<N>& l;
+  ClipTensor t;
+  int chunk, left, i, begin, end;  // begin, end: the tensor's chunks
+  __device__ __forceinline__ ClipWalk(const ClipList<N>& list) : l(list) {
+    const int64_t chunks = l.first[l.count];
+    const int c0 = (int)(chunks * blockIdx.x / gridDim.x);
+    const int c1 = (int)(chunks * (blockIdx.x + 1) / gridDim.x);
+    left = c1 - c0;
+    chunk = BACK ? c1 - 1 : c0;
+    i = left > 0 ? clip_find(l, chunk) : 0;
+    enter();
+  }
+  __device__ __forceinline__ void enter() {
+    t = l.t[i];
+    begin = l.first[i];
+    end = l.first[i + 1];
+  }
+  __device__ __forceinline__ int64_t word() const { return (int64_t)(chunk - begin) * kClipChunk; }
+  __device__ __forceinline__ void next() {
+    --left;
+    chunk += BACK ? -1 : 1;
+    if (left > 0 && (BACK ? chunk < begin : chunk >= end)) {
+      i += BACK ? -1 : 1;
+      enter();
+    }
+  }
+};
+
+// A sum as hi + lo, lo the rounding errors of hi's additions (Knuth's exact addition).  fp64
+// would do it shorter, but its rate here is so low that the additions of 608 CTAs' threads took
+// longer than 20 MB of data.  hi is inf or NaN where the sum is; lo means nothing then.
+struct ClipSum {
+  float hi, lo;
+};
+__device__ __forceinline__ ClipSum clip_add(const ClipSum& a, const ClipSum& b) {
+  const float s = a.hi + b.hi, t = s - a.hi;
+  return {s, ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo)};
+}
+__device__ __forceinline__ float clip_value(const ClipSum& a) {
+  return fabsf(a.hi) < INFINITY ? a.hi + a.lo : a.hi;
+}
 // The block's sum of v, in every thread; added in a fixed order.
-__device__ __forceinline__ double clip_block_sum(double v) {
-  __shared__ double part[kClipThreads / 32];
+__device__ __forceinline__ ClipSum clip_block_sum(ClipSum v) {
+  __shared__ ClipSum part[kClipThreads / 32];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1)
+    v = clip_add(v, {__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
   if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
   __syncthreads();
-  double s = 0.;
+  ClipSum s = part[0];
 #pragma unroll
-  for (int i = 0; i < kClipThreads / 32; ++i) s += part[i];
-  __syncthreads();
+  for (int i = 1; i < kClipThreads / 32; ++i) s = clip_add(s, part[i]);
   return s;
 }
 
 // more: a list after the first one, added to what the slots hold.
 template <int N>
 __global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
-    clip_norm_kernel(const __grid_constant__ ClipList<N> l, double* slots, int more) {
+    clip_norm_kernel(const __grid_constant__ ClipList<N> l, ClipSum* slots, int more) {
   pdl_enter();
-  double sum = 0.;
-  const int chunks = l.first[l.count];
-  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int i = clip_find(l, c);
-    const ClipTensor& t = l.t[i];
-    const int64_t w = (int64_t)(c - l.first[i]) * kClipChunk;
-    sum += (double)clip_square(t, w);
+  ClipSum sum{0.f, 0.f};
+  for (ClipWalk<N, false> walk(l); walk.left > 0; walk.next()) {
+    const ClipRange r(walk.t, walk.word());
+    uint4 v[kClipUnroll];
+    clip_load(walk.t, walk.word(), r, v);
+    sum = clip_add(sum, {clip_square(walk.t, r, v), 0.f});
   }
   sum = clip_block_sum(sum);
-  if (threadIdx.x == 0) slots[blockIdx.x] = more ? slots[blockIdx.x] + sum : sum;
+  if (threadIdx.x == 0) slots[blockIdx.x] = more ? clip_add(slots[blockIdx.x], sum) : sum;
 }
 
 template <int N>
 __global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
-    clip_scale_kernel(const __grid_constant__ ClipList<N> l, const double* slots, int nslots,
+    clip_scale_kernel(const __grid_constant__ ClipList<N> l, const ClipSum* slots, int nslots,
                       float max_norm, float eps, float* norm_out) {
   pdl_enter();
-  double sum = 0.;
-  for (int i = threadIdx.x; i < nslots; i += kClipThreads) sum += slots[i];
-  const float norm = (float)sqrt(clip_block_sum(sum));
+  ClipSum sum{0.f, 0.f};
+  for (int i = threadIdx.x; i < nslots; i += kClipThreads) sum = clip_add(sum, slots[i]);
+  const float norm = sqrtf(clip_value(clip_block_sum(sum)));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
   const float q = max_norm / (norm + eps);
   const float c = q >= 1.f ? 1.f : q;  // a NaN stays one
-  const int chunks = l.first[l.count];
-  for (int k = blockIdx.x; k < chunks; k += gridDim.x) {
-    const int chunk = chunks - 1 - k, i = clip_find(l, chunk);
-    const ClipTensor& t = l.t[i];
-    if (!t.out || (c == 1.f && t.out == t.in)) continue;
-    const int64_t w = (int64_t)(chunk - l.first[i]) * kClipChunk;
-    clip_scale(t, w, c);
+  for (ClipWalk<N, true> walk(l); walk.left > 0; walk.next()) {
+    if (!walk.t.out || (c == 1.f && walk.t.out == walk.t.in)) continue;
+    const ClipRange r(walk.t, walk.word());
+    uint4 v[kClipUnroll];
+    clip_load(walk.t, walk.word(), r, v);
+    clip_scale(walk.t, walk.word(), r, v, c);
   }
 }
 
@@ -263,7 +303,7 @@ bool clip_list(const moe_tensor* ts, int count, ClipList<N>* l) {
 
 template <int N>
 moe_status clip_run(const Launch& L, int n, const moe_tensor* ts, float max_norm, float eps,
-                    float* norm, double* slots) {
+                    float* norm, ClipSum* slots) {
   const int most = std::min(kClipMaxCtas, kClipCtasPerSm * L.num_sms);
   ClipList<N> l;
   // every list has the slots of all CTAs, so that later lists add to what is there
@@ -287,7 +327,7 @@ moe_status clip_run(const Launch& L, int n, const moe_tensor* ts, float max_norm
                       at > 0 ? 1 : 0);
       else
         launch_kernel(clip_scale_kernel<N>, dim3(used), dim3(kClipThreads), 0, L.stream, l,
-                      static_cast<const double*>(slots), used, max_norm, eps,
+                      static_cast<const ClipSum*>(slots), used, max_norm, eps,
                       i == 0 ? norm : nullptr);
       launch_end(L, pass ? MOE_K_CLIP : MOE_K_GRAD_NORM);
     }
@@ -303,7 +343,7 @@ using namespace moe;
 
 extern "C" moe_status moe_clip_workspace_size(size_t* bytes) {
   if (!bytes) return MOE_ERR_INVALID_ARG;
-  *bytes = kClipMaxCtas * sizeof(double);
+  *bytes = kClipMaxCtas * sizeof(ClipSum);
   return MOE_OK;
 }
 
@@ -328,11 +368,11 @@ extern "C" moe_status moe_clip_grad_norm(int32_t n, const moe_tensor* tensors, f
   if (!ws) return MOE_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) || (reinterpret_cast<uintptr_t>(norm) & 3u))
     return MOE_ERR_ALIGNMENT;
-  if (ws_bytes < kClipMaxCtas * sizeof(double)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < kClipMaxCtas * sizeof(ClipSum)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   Launch L;
   const moe_status s = open_launch(stream, &L);
   if (s != MOE_OK) return s;
-  double* slots = static_cast<double*>(ws);
+  ClipSum* slots = static_cast<ClipSum*>(ws);
   return n <= kClipFew ? clip_run<kClipFew>(L, n, tensors, max_norm, eps, norm, slots)
                        : clip_run<kClipMost>(L, n, tensors, max_norm, eps, norm, slots);
 }

@@ -1,9 +1,9 @@
 """moe_clip_grad_norm against its definition in 64 bits.
 
 Norm: a thread adds at most 16 squares in each of four fp32 accumulators, which two
-additions join (18 u of a sum of positive terms, u = 2^-24), the rest is fp64; the
-root halves that and is rounded once: 10 u.  Products: c adds a sum, a quotient and
-the product, 13 u, and the rounding to the type.
+additions join (18 u of a sum of positive terms, u = 2^-24), the rest is added as pairs of
+fp32 (2^-44) and rounded once; the root halves that and is rounded once: 10.5 u.  Products: c adds a sum, a quotient and
+the product, 14 u, and the rounding to the type.
 """
 import math
 
@@ -45,7 +45,7 @@ def check(m, tensors, max_norm, outs=None, what=""):
     m.moe_clip_grad_norm(lst, max_norm, norm, m.clip_workspace(), EPS)
     torch.cuda.synchronize()
     want = norm_of(kept)
-    assert abs(float(norm) - want) <= 10 * U * want, (what, float(norm), want)
+    assert abs(float(norm) - want) <= 11 * U * want, (what, float(norm), want)
     c = min(1.0, max_norm / (want + EPS))
     for t, k, o in zip(tensors, kept, lst.outs):
         if o is None or k.numel() == 0:
@@ -54,7 +54,7 @@ def check(m, tensors, max_norm, outs=None, what=""):
             assert torch.equal(o, k), what
         else:
             y = k.double() * c
-            tol = (torch.finfo(o.dtype).eps / 2 + 13 * U) * y.abs() + TINY[o.dtype]
+            tol = (torch.finfo(o.dtype).eps / 2 + 14 * U) * y.abs() + TINY[o.dtype]
             assert ((o.double() - y).abs() <= tol).all(), what
         if o is not t:
             assert torch.equal(t, k), what
@@ -138,13 +138,13 @@ def test_what_is_not_finite(m, dtype):
 
 
 def test_ends_of_the_range(m):
-    big = torch.full((50,), 2.0**63, device="cuda")  # squares of 2^126, sums past fp32 in fp64
+    big = torch.full((50,), 2.0**63, device="cuda")  # squares of 2^126
     big[1:] = 2.0**60
     check(m, [big], 1.0)
     small = torch.full((5000,), 2.0**-62, device="cuda")
     norm = torch.empty(1, device="cuda")
     m.moe_clip_grad_norm(m.TensorList([small], [None]), 1.0, norm, m.clip_workspace())
-    assert abs(float(norm) / norm_of([small]) - 1) <= 10 * U
+    assert abs(float(norm) / norm_of([small]) - 1) <= 11 * U
 
 
 def test_the_same_bits_on_every_call_and_in_a_graph(m):
@@ -170,7 +170,7 @@ def test_the_same_bits_on_every_call_and_in_a_graph(m):
     src[1].mul_(2)  # a replay reads what the gradients hold then
     graph.replay()
     torch.cuda.synchronize()
-    assert abs(float(norm) - norm_of(src)) <= 10 * U * norm_of(src)
+    assert abs(float(norm) - norm_of(src)) <= 11 * U * norm_of(src)
 
 
 def test_two_streams_at_once(m):
@@ -186,7 +186,7 @@ def test_two_streams_at_once(m):
             m.moe_clip_grad_norm(lst, 1.0, norm, ws, stream=st)
     torch.cuda.synchronize()
     for (lst, norm, _), w in zip(state, want):
-        assert abs(float(norm) - w) <= 10 * U * w
+        assert abs(float(norm) - w) <= 11 * U * w
         assert abs(norm_of(lst.outs) - 1) < 1e-5
 
 
