@@ -404,16 +404,18 @@ __device__ __forceinline__ void cp_async_word(uint32_t dst, const void* src, int
 }
 // 16 bytes of a weight row.  Past its end (in false) codes are left as they are: whatever
 // lies there is finite and meets zeros of x; 16-bit weights become zeros (src is not read).
+// Weights leave L2 first: they pass once, and what stays is the kernel's own instructions and h.
 template <bool FOUR>
 __device__ __forceinline__ void copy_piece(uint32_t dst, const unsigned char* src, bool in,
-                                           const void* safe) {
+                                           const void* safe, uint64_t policy) {
   if constexpr (FOUR) {
     if (in)
-      asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src)
+      asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::256B [%0], [%1], 16, %2;" ::"r"(dst),
+                   "l"(src), "l"(policy)
                    : "memory");
   } else {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst),
-                 "l"(in ? static_cast<const void*>(src) : safe), "r"(in ? 16 : 0)
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::256B [%0], [%1], 16, %2, %3;" ::"r"(dst),
+                 "l"(in ? static_cast<const void*>(src) : safe), "r"(in ? 16 : 0), "l"(policy)
                  : "memory");
   }
 }
@@ -422,16 +424,14 @@ __device__ __forceinline__ void team_barrier(int team) {
 }
 // All but the `stages - 2` groups committed last have arrived.
 __device__ __forceinline__ void wait_stage(int stages) {
-  if (stages >= 6)
-    cp_async_wait<4>();
-  else if (stages >= 4)
+  if (stages == 4)
     cp_async_wait<2>();
   else if (stages == 3)
     cp_async_wait<1>();
   else
     cp_async_wait<0>();
 }
-static_assert(kFewMaxStages == 6, "wait_stage knows 2, 3, 4 and 6 (5 waits like 4)");
+static_assert(kFewMaxStages == 4, "wait_stage knows up to four");
 
 template <typename T>
 __device__ __forceinline__ float read_scale(uint32_t at) {
@@ -708,6 +708,7 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, c
   const uint32_t d0 = dst + K::swizzle(lane / 8, lane % 8) * 16;
   const uint32_t d1 = dst + 4 * 128 + K::swizzle(lane / 8 + 4, lane % 8) * 16;
   const uint32_t ring_last = ring + (S - 1) * sub;
+  const uint64_t policy = policy_evict_first();
   auto issue = [&](uint32_t slot) {
     if (togo == 0 && !done) {
       const int tile = queue[seq_next++ % 16];
@@ -735,10 +736,10 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, c
     }
     if (togo) {
       const bool in = left > 0;
-      copy_piece<K::kFour>(slot + d0, gate0, in, a.x);
-      copy_piece<K::kFour>(slot + d1, gate1, in, a.x);
-      copy_piece<K::kFour>(slot + d0 + 8 * 128, up0, in, a.x);
-      copy_piece<K::kFour>(slot + d1 + 8 * 128, up1, in, a.x);
+      copy_piece<K::kFour>(slot + d0, gate0, in, a.x, policy);
+      copy_piece<K::kFour>(slot + d1, gate1, in, a.x, policy);
+      copy_piece<K::kFour>(slot + d0 + 8 * 128, up0, in, a.x, policy);
+      copy_piece<K::kFour>(slot + d1 + 8 * 128, up1, in, a.x, policy);
       if constexpr (K::kFour) copy_groups<K>(a, sh.groups, slot, step_next, sp, zp);
       gate0 += 128;
       gate1 += 128;
@@ -756,6 +757,7 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, c
   const uint32_t x0 = smem_u32(smem) + min(g, a.T - 1) * a.p.xpitch + tg * 16 +
                       k0 * (K::kStepK * 2);
   const uint32_t sum0 = smem_u32(smem) + a.p.sum_at + tg * 8 + k0 * (K::kBlocks * kFewMaxT * 4);
+  int stored = 0;
   for (int seq = 0;; ++seq) {
     const int tile = queue[seq % 16];
     if (tile >= n.total) break;
@@ -829,17 +831,76 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, c
           if (ch == 0 && mine) atomicMax(&head->hmax[u][t], most);
         }
       }
-      __syncwarp();
-      if (lane == 0) {
-        __threadfence();
-        atomicAdd(&head->done, 1);
-      }
     }
+    ++stored;
   }
   cp_async_wait<0>();
+  // The team's tiles are stored: one fence for all of them (one a tile held up the warp that
+  // finished it by a microsecond).
+  team_barrier(team);
+  if (tt == 0) {
+    __threadfence();
+    atomicAdd(&head->done, stored);
+  }
 }
 
 constexpr int kFewDownTiles = 4;  // 16-row tiles of one pass of the down projection
+
+// Eight values of h as MMA operands, scaled by `up`; rest: what 16-bit operands leave of them.
+template <typename K>
+__device__ __forceinline__ void h_operands(const float4& p, const float4& q, float up,
+                                           uint32_t (&b)[4], uint32_t (&rest)[4]) {
+  const float v[8] = {p.x * up, p.y * up, p.z * up, p.w * up,
+                      q.x * up, q.y * up, q.z * up, q.w * up};
+  if constexpr (K::kFour) {
+    K::operands(v, b);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      split2<typename K::Mma>(v[2 * j], v[2 * j + 1], b[j], rest[j]);
+  }
+}
+
+// All rows of h as operands in shared memory, over x: where they fit, each CTA turns them into
+// operands once and not for every tile of channels.  row[r]: unit * 8 + token.
+template <typename K>
+__device__ __forceinline__ void stage_h(const FewArgs& a, unsigned char* smem,
+                                        const FewUnit* units, int rows, const int* row) {
+  const int pieces = (a.p.hpitch - 64) / 16, n = rows * pieces;
+  constexpr int kAtOnce = 4;
+  for (int e0 = threadIdx.x; e0 < n; e0 += kAtOnce * kFewThreads) {
+    float4 p[kAtOnce], q[kAtOnce];
+    uint32_t most[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int e = e0 + i * kFewThreads, r = e / pieces, j = e % pieces;
+      p[i] = q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      most[i] = 0u;
+      if (e >= n) continue;
+      const int u = row[r] / kFewMaxT, t = row[r] % kFewMaxT;
+      if (8 * j < (units[u].expert < 0 ? a.Is : a.I)) {
+        const float* from = a.h + ((int64_t)u * a.T + t) * a.inter + 8 * j;
+        p[i] = __ldcg(reinterpret_cast<const float4*>(from));
+        q[i] = __ldcg(reinterpret_cast<const float4*>(from + 4));
+      }
+      if constexpr (K::kScaled) most[i] = __ldcg(&a.head->hmax[u][t]);
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int e = e0 + i * kFewThreads, r = e / pieces, j = e % pieces;
+      if (e >= n) break;
+      const float up = K::kScaled ? __uint_as_float(fp16_range_bits(most[i])) : 1.f;
+      uint32_t b[4], rest[4] = {};
+      h_operands<K>(p[i], q[i], up, b, rest);
+      const int step = j / (K::kStepK / 8);
+      unsigned char* to = smem + r * a.p.hpitch +
+                          (step * (K::kStepK / 8) + K::piece_of_k8(j % (K::kStepK / 8))) * 16;
+      *reinterpret_cast<uint4*>(to) = make_uint4(b[0], b[1], b[2], b[3]);
+      if constexpr (K::kRest)
+        *reinterpret_cast<uint4*>(to + a.p.hrest) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+    }
+  }
+}
 
 template <typename K>
 __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, const FewUnit* units,
@@ -850,6 +911,7 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
   const int S = a.p.stages, sub = a.p.sub_bytes;
   const uint32_t ring = smem_u32(smem) + a.p.ring_at + warp * S * sub;
   const uint32_t ring_last = ring + (S - 1) * sub;
+  const uint64_t policy = policy_evict_first();
   float* sums = reinterpret_cast<float*>(smem + a.p.ring_at);
   const int share = (a.H + gridDim.x - 1) / gridDim.x;
   const int c_begin = min(a.H, (int)blockIdx.x * share), c_end = min(a.H, c_begin + share);
@@ -860,6 +922,10 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
   const int dst = lane / 8 * 128;
   const uint32_t d0 = dst + K::swizzle(lane / 8, lane % 8) * 16;
   const uint32_t d1 = dst + 4 * 128 + K::swizzle(lane / 8 + 4, lane % 8) * 16;
+  // units' first rows of h, and behind the last their number; then the rows' units and tokens
+  const int* row0 = reinterpret_cast<const int*>(smem + a.p.row_at);
+  const int nunits = n.units + shared;
+  const bool inside = a.p.hpitch > 0;
   bool waited = false;
 
   for (int c0 = c_begin; c0 < c_end; c0 += 16 * kFewDownTiles) {
@@ -892,10 +958,10 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
         // rows past the range are not stored, whatever they hold
         int rows = channels - m_next * 16 - lane / 8;
         if (next_step * 128 + (lane % 8) * 16 >= next_row) rows = 0;
-        copy_piece<K::kFour>(slot + d0, w, rows > 0, a.x);
-        copy_piece<K::kFour>(slot + d1, w + four, rows > 4, a.x);
-        copy_piece<K::kFour>(slot + d0 + 8 * 128, w + 2 * four, rows > 8, a.x);
-        copy_piece<K::kFour>(slot + d1 + 8 * 128, w + 3 * four, rows > 12, a.x);
+        copy_piece<K::kFour>(slot + d0, w, rows > 0, a.x, policy);
+        copy_piece<K::kFour>(slot + d1, w + four, rows > 4, a.x, policy);
+        copy_piece<K::kFour>(slot + d0 + 8 * 128, w + 2 * four, rows > 8, a.x, policy);
+        copy_piece<K::kFour>(slot + d1 + 8 * 128, w + 3 * four, rows > 12, a.x, policy);
         if constexpr (K::kFour) {
           // (a row past the range takes the last one's)
           const int r = min(m_next * 16, channels - 1 - lane / 2) * next_groups;
@@ -925,11 +991,16 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
         raise_status(a.status, kStTimeout, MOE_K_FEW_FFN);
       __syncthreads();
       waited = true;
+      if (inside) {
+        stage_h<K>(a, smem, units, row0[nunits], row0 + nunits + 1);
+        __syncthreads();
+      }
     }
 
     float acc[kFewDownTiles][4] = {}, total[kFewDownTiles][4] = {};
     float w0 = 0.f, w1 = 0.f, up = 1.f;
     const float* hrow = nullptr;
+    uint32_t hat = 0;  // the row in shared memory
     FewGroups at{};  // of every tile: sixteen rows on, groups lie alike
     int u = u0, step = f0 - u0 * rs.steps, steps = 0, kmax = 0;
     auto flush = [&]() {
@@ -954,7 +1025,9 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
         steps = sh.steps;
         kmax = sh.K;
         const uint32_t tokens = units[u].tokens;
-        hrow = g < a.T && ((tokens >> g) & 1u) ? a.h + ((int64_t)u * a.T + g) * a.inter : nullptr;
+        hrow = (tokens >> g) & 1u ? a.h + ((int64_t)u * a.T + g) * a.inter : nullptr;
+        if (inside)
+          hat = smem_u32(smem) + (row0[u] + __popc(tokens & ((1u << g) - 1u))) * a.p.hpitch + tg * 16;
         w0 = __ldcg(&a.head->w[u][2 * tg]) * (K::kFour ? 16777216.f : 1.f);
         w1 = __ldcg(&a.head->w[u][2 * tg + 1]) * (K::kFour ? 16777216.f : 1.f);
         if constexpr (K::kScaled) {
@@ -966,22 +1039,28 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
       }
       // the lane's h of this step, as MMA operands
       uint32_t b[K::kWords][4], rest[K::kRest ? K::kWords : 1][4];
+      if (inside) {
 #pragma unroll
-      for (int i = 0; i < K::kWords; ++i) {
-        const int k = step * K::kStepK + K::k_of(i, tg);
-        float4 p = make_float4(0.f, 0.f, 0.f, 0.f), q = p;
-        if (hrow && k < kmax) {
-          p = __ldcg(reinterpret_cast<const float4*>(hrow + k));
-          q = __ldcg(reinterpret_cast<const float4*>(hrow + k + 4));
+        for (int i = 0; i < K::kWords; ++i) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u), q = v;
+          if (hrow) {
+            v = lds128(hat + (step * (K::kStepK / 8) + K::piece(i, 0)) * 16);
+            if constexpr (K::kRest)
+              q = lds128(hat + a.p.hrest + (step * (K::kStepK / 8) + K::piece(i, 0)) * 16);
+          }
+          b[i][0] = v.x, b[i][1] = v.y, b[i][2] = v.z, b[i][3] = v.w;
+          if constexpr (K::kRest) rest[i][0] = q.x, rest[i][1] = q.y, rest[i][2] = q.z, rest[i][3] = q.w;
         }
-        const float v[8] = {p.x * up, p.y * up, p.z * up, p.w * up,
-                            q.x * up, q.y * up, q.z * up, q.w * up};
-        if constexpr (K::kFour) {
-          K::operands(v, b[i]);
-        } else {
+      } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            split2<typename K::Mma>(v[2 * j], v[2 * j + 1], b[i][j], rest[i][j]);
+        for (int i = 0; i < K::kWords; ++i) {
+          const int k = step * K::kStepK + K::k_of(i, tg);
+          float4 p = make_float4(0.f, 0.f, 0.f, 0.f), q = p;
+          if (hrow && k < kmax) {
+            p = __ldcg(reinterpret_cast<const float4*>(hrow + k));
+            q = __ldcg(reinterpret_cast<const float4*>(hrow + k + 4));
+          }
+          h_operands<K>(p, q, up, b[i], rest[K::kRest ? i : 0]);
         }
       }
       float2 xs[K::kBlocks];
@@ -1145,6 +1224,18 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_ffn_kernel(const __grid_co
     reinterpret_cast<uint32_t*>(units)[i] = __ldcg(reinterpret_cast<const uint32_t*>(a.head->unit) + i);
   if (tid < kFewMaxT) zero_w[tid] = __ldcg(&a.head->zero_w[tid]);
   __syncthreads();
+  if (a.p.hpitch > 0) {  // the rows of h (read after the next barrier)
+    int* row0 = reinterpret_cast<int*>(smem + a.p.row_at);
+    const int nunits = n.units + shared;
+    for (int u = tid; u <= nunits; u += kFewThreads) {
+      int first = 0;
+      for (int i = 0; i < u; ++i) first += __popc(units[i].tokens);
+      row0[u] = first;
+      if (u < nunits)
+        for (int t = 0; t < kFewMaxT; ++t)
+          if ((units[u].tokens >> t) & 1u) row0[nunits + 1 + first++] = u * kFewMaxT + t;
+    }
+  }
   gate_up<K>(a, smem, units, n, x_inverse);
   __syncthreads();
   pdl_trigger();
@@ -1284,7 +1375,9 @@ extern "C" moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weight
   FewArgs a{};
   const int units = std::min(c.n_routed, T * c.top_k) + (c.shared_inter > 0);
   const int es = wt->scale_dtype == MOE_DT_FP32 ? 4 : 2;
-  a.p = few_plan(T, c.hidden, units, four, wt->group, es, zeros, aligned_s, aligned_z, whole);
+  a.p = few_plan(T, c.hidden, std::max(c.n_routed > 0 ? c.inter : 0, c.shared_inter), units,
+                 T * (std::min(c.n_routed, c.top_k) + (c.shared_inter > 0)), four, wt->group, es,
+                 zeros, aligned_s, aligned_z, whole);
   if (a.p.stages < 2) return MOE_ERR_UNSUPPORTED;
   Launch L;
   const moe_status s = open_launch(stream, &L);
