@@ -473,24 +473,23 @@ __global__ void __launch_bounds__(kExpandThreads, kExpandPerSm<RT>)
     return;
   }
   const T* m = static_cast<const T*>(a.m2) + (int64_t)j * r * a.N;
+  // (a warp's 32 pairs of columns are 128 bytes there and here)
   auto load_tile = [&](int n0, int buf) {
-    for (int e = tid; e < RT * (kExpandTile / 8); e += kExpandThreads) {
-      const int i = e / (kExpandTile / 8), q = e % (kExpandTile / 8), c = n0 / 8 + q;
-      const bool in = i < r && 8 * c < a.N;
-      const T* from = m + (int64_t)i * a.N + 8 * c;
-      const uint32_t to = mt + buf * kTile + i * (kExpandTile * 2) + (q % 4) * 4;
-      uint32_t w[4] = {};
-      if (in && !a.m2vec) {
-        const uint4 v = load_piece<T>(m + (int64_t)i * a.N, c, a.N, false);
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-      }
+    for (int e = tid; e < RT * (kExpandTile / 2); e += kExpandThreads) {
+      const int i = e / (kExpandTile / 2), w = e % (kExpandTile / 2), q = w / 4, t = w % 4;
+      const int n = n0 + 2 * w;
+      const uint32_t dst = mt + buf * kTile + i * (kExpandTile * 2) +
+                           (((q / 4 * 4 + t) ^ (i % 8)) * 16) + (q % 4) * 4;
+      const T* from = m + (int64_t)i * a.N + n;
+      if (i < r && n < a.N && a.m2vec) {
+        cp_async_unit(dst, from, 4);
+      } else {
+        T v[2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint32_t dst = to + (((q / 4 * 4 + t) ^ (i % 8)) * 16);
-        if (in && a.m2vec)
-          cp_async_unit(dst, from + 2 * t, 4);
-        else
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(w[t]) : "memory");
+        for (int c = 0; c < 2; ++c) v[c] = i < r && n + c < a.N ? from[c] : from_f<T>(0.f);
+        uint32_t pair;
+        memcpy(&pair, v, 4);
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(pair) : "memory");
       }
     }
   };
