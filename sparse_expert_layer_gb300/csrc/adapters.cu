@@ -370,7 +370,19 @@ __global__ void __launch_bounds__(2 * kShrinkRows<RT>) adapters_shrink_kernel(Ad
                        m + (in ? (int64_t)row * a.K : 0), c * 8 + piece, a.K, a.m1vec, in);
     }
   };
-  float acc[RT / 8][4] = {};
+  // MMAs cut their sums off where fp32 ends, each time the same way: after every kFlush slices
+  // (sixteen MMAs) what they hold is added, rounded, to the sum.
+  constexpr int kFlush = 4;
+  float acc[RT / 8][4] = {}, sum[RT / 8][4] = {};
+  auto flush = [&]() {
+#pragma unroll
+    for (int n = 0; n < RT / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sum[n][i] += acc[n][i];
+        acc[n][i] = 0.f;
+      }
+  };
 #pragma unroll
   for (int q = 0; q < kShrinkStages - 1; ++q) {
     if (c0 + q < c1) load(c0 + q, q);
@@ -397,15 +409,17 @@ __global__ void __launch_bounds__(2 * kShrinkRows<RT>) adapters_shrink_kernel(Ad
         mma16816<T>(acc[2 * n + 1], af[0], af[1], af[2], af[3], bf[2], bf[3]);
       }
     }
+    if ((c - c0) % kFlush == kFlush - 1) flush();
   }
+  flush();
   cp_async_wait<0>();
   __syncthreads();
   float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (int n = 0; n < RT / 8; ++n) {
     float* at = red + (warp * 16 + lane / 4) * RT + n * 8 + lane % 4 * 2;
-    *reinterpret_cast<float2*>(at) = make_float2(acc[n][0], acc[n][1]);
-    *reinterpret_cast<float2*>(at + 8 * RT) = make_float2(acc[n][2], acc[n][3]);
+    *reinterpret_cast<float2*>(at) = make_float2(sum[n][0], sum[n][1]);
+    *reinterpret_cast<float2*>(at + 8 * RT) = make_float2(sum[n][2], sum[n][3]);
   }
   cluster_sync_all();
   const float s1 = a.scale1 ? a.scale1[j] : 1.f;
@@ -632,7 +646,7 @@ constexpr int kOuterRows = 32;  // positions of a stage
 constexpr int kOuterStages = 3;
 constexpr int kOuterAhead = 32;  // stages whose rows are looked up at once
 template <int RT>
-constexpr int kOuterCols = RT <= 64 ? 256 : 128;
+constexpr int kOuterCols = RT <= 32 ? 256 : 128;
 template <int RT>
 constexpr int kOuterPerSm = RT == 16 ? 3 : RT <= 64 ? 2 : 1;  // CTAs
 // 16-bit terms of v: bf16 three (24 bits), fp16 two (22 bits)
@@ -740,7 +754,20 @@ __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer
       }
     }
   };
-  float acc[RT / 16][kWarpCols / 8][4] = {};
+  // as in the shrink: sums of kFlush stages' MMAs (two or three terms of v, two steps each)
+  constexpr int kFlush = 2;
+  float acc[RT / 16][kWarpCols / 8][4] = {}, sum[RT / 16][kWarpCols / 8][4] = {};
+  auto flush = [&]() {
+#pragma unroll
+    for (int m = 0; m < RT / 16; ++m)
+#pragma unroll
+      for (int c = 0; c < kWarpCols / 8; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[m][c][i] += acc[m][c][i];
+          acc[m][c][i] = 0.f;
+        }
+  };
   look_up(q0);
   __syncthreads();
 #pragma unroll
@@ -782,7 +809,9 @@ __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer
           }
         }
     }
+    if ((q - q0) % kFlush == kFlush - 1) flush();
   }
+  flush();
   cp_async_wait<0>();
   __syncthreads();
   // parts [rank][column], added in the order of the cluster's ranks
@@ -792,8 +821,8 @@ __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer
 #pragma unroll
     for (int c = 0; c < kWarpCols / 8; ++c) {
       float* at = red + (m * 16 + lane / 4) * kCols + warp * kWarpCols + c * 8 + lane % 4 * 2;
-      *reinterpret_cast<float2*>(at) = make_float2(acc[m][c][0], acc[m][c][1]);
-      *reinterpret_cast<float2*>(at + 8 * kCols) = make_float2(acc[m][c][2], acc[m][c][3]);
+      *reinterpret_cast<float2*>(at) = make_float2(sum[m][c][0], sum[m][c][1]);
+      *reinterpret_cast<float2*>(at + 8 * kCols) = make_float2(sum[m][c][2], sum[m][c][3]);
     }
   cluster_sync_all();
   for (int e = rank * kOuterThreads + tid; e < r * kCols; e += S * kOuterThreads) {
