@@ -412,9 +412,11 @@ moe_status moe_w4_gemv(int32_t n_experts, int32_t N, int32_t K, int32_t group, i
  * sums and scales are fp32 and out is rounded once.  The same bits on every call.
  *  cfg       wdtype MOE_W_BF16 whatever the weights are; out_fp32, gemv_max_rows,
  *            combine and ffn_launch are not read
- *  T         <= 8, T * hidden <= 65536 (MOE_ERR_UNSUPPORTED otherwise, and where one
- *            SM's shared memory has no room for the tokens beside two stages of weights)
- *  dtype     MOE_DT_BF16 or MOE_DT_FP16: x and out, [T, H] with row strides ldx, ldo
+ *  T         <= 8, T * hidden <= 65536, inter and shared_inter <= 2^20
+ *            (MOE_ERR_UNSUPPORTED otherwise, and where one SM's shared memory has no room
+ *            for the tokens beside two stages of weights)
+ *  dtype     MOE_DT_BF16 or MOE_DT_FP16: x and out, [T, H] with row strides ldx, ldo; out
+ *            overlaps nothing that is read
  *  w_router, bias  as for moe_route
  *  topk_ids, topk_w  as written by moe_route, or NULL: not wanted
  *  ws        moe_few_tokens_workspace_size bytes, 256-byte aligned, zeroed once before its

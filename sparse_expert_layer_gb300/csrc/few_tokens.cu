@@ -44,6 +44,7 @@ constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kFewMaxPicks = kFewMaxT * 32;
 constexpr int kFewMaxTH = 65536;           // tokens x hidden
+constexpr int kFewMaxInter = 1 << 20;      // rows and tiles are counted in 32 bits
 constexpr int kRouteScratch = 96 * 1024;   // top-k scratch in shared memory, at most
 
 // One expert with rows (expert -1: the shared one).
@@ -999,6 +1000,7 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
 
     float acc[kFewDownTiles][4] = {}, total[kFewDownTiles][4] = {};
     float w0 = 0.f, w1 = 0.f, up = 1.f;
+    bool in0 = false, in1 = false;  // the lane's columns have picked the unit
     const float* hrow = nullptr;
     uint32_t hat = 0;  // the row in shared memory
     FewGroups at{};  // of every tile: sixteen rows on, groups lie alike
@@ -1006,10 +1008,15 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
     auto flush = [&]() {
 #pragma unroll
       for (int m = 0; m < kFewDownTiles; ++m) {
-        total[m][0] = fmaf(w0, acc[m][0], total[m][0]);
-        total[m][1] = fmaf(w1, acc[m][1], total[m][1]);
-        total[m][2] = fmaf(w0, acc[m][2], total[m][2]);
-        total[m][3] = fmaf(w1, acc[m][3], total[m][3]);
+        // (other columns' sums are zeros, but NaN where a weight is not finite)
+        if (in0) {
+          total[m][0] = fmaf(w0, acc[m][0], total[m][0]);
+          total[m][2] = fmaf(w0, acc[m][2], total[m][2]);
+        }
+        if (in1) {
+          total[m][1] = fmaf(w1, acc[m][1], total[m][1]);
+          total[m][3] = fmaf(w1, acc[m][3], total[m][3]);
+        }
         acc[m][0] = acc[m][1] = acc[m][2] = acc[m][3] = 0.f;
       }
     };
@@ -1028,6 +1035,8 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
         hrow = (tokens >> g) & 1u ? a.h + ((int64_t)u * a.T + g) * a.inter : nullptr;
         if (inside)
           hat = smem_u32(smem) + (row0[u] + __popc(tokens & ((1u << g) - 1u))) * a.p.hpitch + tg * 16;
+        in0 = (tokens >> (2 * tg)) & 1u;
+        in1 = (tokens >> (2 * tg + 1)) & 1u;
         w0 = __ldcg(&a.head->w[u][2 * tg]) * (K::kFour ? 16777216.f : 1.f);
         w1 = __ldcg(&a.head->w[u][2 * tg + 1]) * (K::kFour ? 16777216.f : 1.f);
         if constexpr (K::kScaled) {
@@ -1301,7 +1310,9 @@ moe_status check_few(const moe_config* c, int T) {
   const moe_status s = moe_workspace_size(c, T < 0 ? T : std::min(T, 1), &bytes);
   if (s != MOE_OK) return s;
   if (c->wdtype != MOE_W_BF16) return MOE_ERR_UNSUPPORTED;
-  if (T > kFewMaxT || (int64_t)T * c->hidden > kFewMaxTH) return MOE_ERR_UNSUPPORTED;
+  if (T > kFewMaxT || (int64_t)T * c->hidden > kFewMaxTH || c->inter > kFewMaxInter ||
+      c->shared_inter > kFewMaxInter)
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -1371,6 +1382,7 @@ extern "C" moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weight
     return MOE_ERR_ALIGNMENT;
   const FewLayout l = few_layout(c, T);
   if (ws_bytes < l.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (out == x) return MOE_ERR_INVALID_ARG;
 
   FewArgs a{};
   const int units = std::min(c.n_routed, T * c.top_k) + (c.shared_inter > 0);

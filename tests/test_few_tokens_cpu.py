@@ -45,14 +45,16 @@ def weights(moe, four, **kw):
 
 def call(moe, four=False, cfg=None, wt=None, **kw):
     a = dict(T=4, dtype=BF16, x=FAKE, ldx=256, w_router=FAKE, bias=FAKE, ids=None, w=None,
-             out=FAKE, ldo=256, ws=FAKE, ws_bytes=1 << 40)
+             out=FAKE + 4096, ldo=256, ws=FAKE, ws_bytes=1 << 40)
     a.update(kw)
     return moe.lib.moe_few_tokens(ctypes.byref(config(moe, **(cfg or {}))),
                                   ctypes.byref(weights(moe, four, **(wt or {}))), *a.values(), None)
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(T=-1), INVALID), (dict(T=9), UNSUPPORTED), (dict(dtype=FP32), INVALID),
+    (dict(T=-1), INVALID), (dict(out=FAKE), INVALID),
+    (dict(cfg=dict(inter=(1 << 20) + 32)), UNSUPPORTED),
+    (dict(cfg=dict(shared_inter=(1 << 20) + 32)), UNSUPPORTED), (dict(T=9), UNSUPPORTED), (dict(dtype=FP32), INVALID),
     (dict(dtype=FP16), INVALID), (dict(x=None), INVALID), (dict(ldx=255), INVALID),
     (dict(w_router=None), INVALID), (dict(bias=None), INVALID), (dict(out=None), INVALID),
     (dict(ldo=100), INVALID), (dict(ws=None), INVALID), (dict(ws_bytes=1000), WS),

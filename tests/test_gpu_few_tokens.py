@@ -425,3 +425,23 @@ def test_plain_launches_give_the_same_bits(m, tmp_path):
                        env=dict(os.environ, MOE_PDL=pdl), timeout=300)
         outs.append(torch.load(at))
     assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("dtype,bits", [(BF16, 16), (FP16, 16), (BF16, 4)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_weights_that_are_not_finite_reach_their_tokens_only(m, dtype, bits, bad):
+    c = make("deep", 6, dtype, bits, 64)
+    experts = experts_of(m, c)
+    ws = m.few_tokens_workspace(experts, 6)
+    good, out = torch.empty_like(c["x"]), torch.empty_like(c["x"])
+    ids = torch.empty(6, 4, dtype=torch.int32, device="cuda")
+    m.moe_few_tokens(experts, c["x"], good, ws, ids)
+    e = int(ids[2, 1])
+    picked = (ids == e).any(1)
+    assert picked.any() and not picked.all()
+    for key in ("w_gate", "w_down") if bits == 16 else ("s_gate", "s_down"):
+        c["w"][key][e].fill_(bad)
+    m.moe_few_tokens(experts, c["x"], out, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(out[~picked], good[~picked])
+    assert not torch.isfinite(out[picked]).any()
