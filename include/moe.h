@@ -457,7 +457,7 @@ moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weights* weights,
  *  order     int32 [T], a permutation, or NULL: rows are sorted already.  Positions whose
  *            row lies outside [0, T) are skipped
  *  base      NULL: zeros; may be y itself (the same stride): rows without an adapter are
- *            then not written
+ *            then not written.  y overlaps nothing else that is read
  *  v         fp32 [T, r] out, what moe_adapters_backward needs (positions without an
  *            adapter are not written), or NULL
  *  ws        moe_adapters_workspace_size bytes, 256-byte aligned; need not be initialised */
@@ -472,10 +472,11 @@ moe_status moe_adapters(int32_t T, int32_t n_adapters, int32_t r, int32_t K, int
  * dy[t] B_j^T,
  *   dx[t] = u[p] A_j (zeros without an adapter);  dA_j = sum over p of u[p]^T x[t];
  *   dB_j = scale[j] * sum over p of v[p]^T dy[t]  (zeros for an adapter without rows)
- * u and v enter the sums over p as three bf16 or two fp16 numbers (24 or 22 bits; fp16:
- * relative to the largest of the call).  The same bits on every call.
+ * u and v enter the sums over p as three bf16 or two fp16 numbers (24 or 22 bits; fp16: or
+ * 2^-38 of the adapter's largest, where that is more).  What an adapter's rows hold, NaN
+ * too, changes no other adapter's gradients.  The same bits on every call.
  *  v          as moe_adapters wrote it
- *  dx         [T, K] of dtype, row stride lddx, or NULL
+ *  dx         [T, K] of dtype, row stride lddx, or NULL; overlaps nothing that is read
  *  da, db     of grad_dtype (MOE_DT_FP32 or dtype), as a and b, or both NULL (x and v are
  *             then not read); dx or da is required */
 moe_status moe_adapters_backward(int32_t T, int32_t n_adapters, int32_t r, int32_t K, int32_t N,

@@ -87,7 +87,26 @@ struct Segments {
     *lo = found[0] >= 0 ? found[1] : 0;
     *hi = found[0] >= 0 ? found[2] : 0;
   }
+  // The tiles of the adapters before j, by all threads of the block.
+  __device__ __forceinline__ int tiles_before(int j, int rows) const {
+    __shared__ int parts[32];
+    int n = 0;
+    for (int i = threadIdx.x; i < j; i += blockDim.x)
+      n += (max(0, at(i + 1) - at(i)) + rows - 1) / rows;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (threadIdx.x % 32 == 0) parts[threadIdx.x / 32] = n;
+    __syncthreads();
+    n = 0;
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) n += parts[w];
+    return n;
+  }
 };
+
+// The fp32 bits of |v| as they count towards a largest magnitude: what is not finite does not.
+__device__ __forceinline__ uint32_t magnitude(float v) {
+  const uint32_t bits = __float_as_uint(fabsf(v));
+  return bits < 0x7f800000u ? bits : 0u;
+}
 
 // Piece i (channels 8 i ..) of a row of n channels, zeros past its end.
 template <typename T>
@@ -270,9 +289,8 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(AdapterArgs a
     total[i] = s;
     if (rank == 0) {
       a.v[(int64_t)p * r + i] = s;
-      most = max(most, __float_as_uint(fabsf(s)));
-      if (a.other)
-        most_other = max(most_other, __float_as_uint(fabsf(a.other[(int64_t)p * r + i])));
+      most = max(most, magnitude(s));
+      if (a.other) most_other = max(most_other, magnitude(a.other[(int64_t)p * r + i]));
     }
   }
   if (a.max_v) {
@@ -431,13 +449,13 @@ __global__ void __launch_bounds__(2 * kShrinkRows<RT>) adapters_shrink_kernel(Ad
     for (int q = 0; q < S; ++q) s += ld_cluster_f32(mapa_shared(base + e * 4, q));
     s *= s1;
     a.v[(int64_t)p * r + i] = s;
-    most = max(most, __float_as_uint(fabsf(s)));
+    most = max(most, magnitude(s));
   }
   cluster_sync_all();
   if (a.max_v) {
     uint32_t other = 0u;
     for (int64_t i = (int64_t)lo * r + rank * kThreads + tid; i < (int64_t)hi * r; i += S * kThreads)
-      other = max(other, __float_as_uint(fabsf(a.other[i])));
+      other = max(other, magnitude(a.other[i]));
     most = block_max(most);
     other = block_max(other);
     if (tid == 0) {
@@ -639,6 +657,7 @@ struct OuterArgs {
   Segments seg;
   OuterSide side[2];
   int r, blocks, out_dtype;
+  int tile, each;  // the blocks of `max`: `each` for every tile of so many positions
 };
 
 constexpr int kOuterThreads = 256;
@@ -680,7 +699,10 @@ __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer
   float up = 1.f, down = s.scale ? s.scale[j] : 1.f;
   if constexpr (kTerm == 2) {
     uint32_t most = 0u;
-    for (int i = tid; i < a.blocks; i += kOuterThreads) most = max(most, s.max[i]);
+    // of the adapter's own positions: what the others hold changes nothing
+    const int first = (a.tile == 1 ? lo : a.seg.tiles_before(j, a.tile)) * a.each;
+    const int end = min(a.blocks, first + (hi - lo + a.tile - 1) / a.tile * a.each);
+    for (int i = first + tid; i < end; i += kOuterThreads) most = max(most, s.max[i]);
     const uint32_t bits = fp16_range_bits(block_max(most));
     up = __uint_as_float(bits);
     down *= inverse_pow2(bits);
@@ -951,7 +973,11 @@ void launch_adapters(const Launch& L, const AdapterArgs& a, OuterArgs* outer) {
     launch_kernel_cluster(adapters_row_kernel<T>, dim3(C, a.seg.T), dim3(C), dim3(kRowThreads), 0,
                           L.stream, a);
     launch_end(L, MOE_K_ADAPTERS);
-    if (outer) outer->blocks = C * a.seg.T;
+    if (outer) {
+      outer->tile = 1;
+      outer->each = C;
+      outer->blocks = C * a.seg.T;
+    }
   } else {
     switch (slot) {
       case 0: launch_tiles<T, 16>(L, a, 0); break;
@@ -959,8 +985,11 @@ void launch_adapters(const Launch& L, const AdapterArgs& a, OuterArgs* outer) {
       case 2: launch_tiles<T, 64>(L, a, 2); break;
       default: launch_tiles<T, 128>(L, a, 3); break;
     }
-    if (outer)
-      outer->blocks = shrink_cluster(a, L.num_sms) * adapter_tiles(a, shrink_rows(a.r));
+    if (outer) {
+      outer->tile = shrink_rows(a.r);
+      outer->each = shrink_cluster(a, L.num_sms);
+      outer->blocks = outer->each * adapter_tiles(a, outer->tile);
+    }
   }
   if (!outer) return;
   switch (slot) {
@@ -1024,6 +1053,7 @@ extern "C" moe_status moe_adapters(int32_t T, int32_t n_adapters, int32_t r, int
     return MOE_ERR_ALIGNMENT;
   const AdapterLayout l = adapters_layout(T, r);
   if (ws_bytes < l.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (y == x) return MOE_ERR_INVALID_ARG;
   Launch L;
   const moe_status s = open_launch(stream, &L);
   if (s != MOE_OK) return s;
@@ -1071,6 +1101,7 @@ extern "C" moe_status moe_adapters_backward(
   const AdapterLayout l = adapters_layout(T, r);
   if (ws_bytes < l.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (T == 0 && !da) return MOE_OK;
+  if (T > 0 && dx && (dx == dy || dx == x)) return MOE_ERR_INVALID_ARG;
   Launch L;
   const moe_status s = open_launch(stream, &L);
   if (s != MOE_OK) return s;

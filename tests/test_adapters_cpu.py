@@ -29,7 +29,7 @@ def forward(moe, **kw):
 
 def backward(moe, **kw):
     a = dict(T=4, J=2, r=16, K=64, N=128, dtype=BF16, dy=FAKE, lddy=128, x=FAKE, ldx=64, v=FAKE,
-             a=FAKE, b=FAKE, scale=FAKE, offsets=FAKE, order=FAKE, dx=FAKE, lddx=64,
+             a=FAKE, b=FAKE, scale=FAKE, offsets=FAKE, order=FAKE, dx=FAKE + 4096, lddx=64,
              grad_dtype=FP32, da=FAKE, db=FAKE, ws=FAKE, ws_bytes=1 << 30)
     a.update(kw)
     return moe.lib.moe_adapters_backward(*a.values(), None)
@@ -49,7 +49,7 @@ COMMON = [(dict(T=-1), INVALID), (dict(J=0), INVALID), (dict(r=0), INVALID), (di
 @pytest.mark.parametrize("kw,status", COMMON + [
     (dict(x=None), INVALID), (dict(y=None), INVALID), (dict(ldy=127), INVALID),
     (dict(ldb=127), INVALID), (dict(y=FAKE, ldy=136), INVALID), (dict(y=FAKE + 2), ALIGNMENT),
-    (dict(base=FAKE + 2), ALIGNMENT), (dict(K=(1 << 21) + 1, ldx=1 << 22), UNSUPPORTED),
+    (dict(base=FAKE + 2), ALIGNMENT), (dict(x=FAKE + 4096), INVALID), (dict(K=(1 << 21) + 1, ldx=1 << 22), UNSUPPORTED),
     (dict(N=(1 << 21) + 1, ldb=1 << 22, ldy=1 << 22), UNSUPPORTED)])
 def test_refusals(moe, kw, status):
     assert forward(moe, **kw) == status
@@ -59,7 +59,7 @@ def test_refusals(moe, kw, status):
     (dict(dy=None), INVALID), (dict(x=None), INVALID), (dict(v=None), INVALID),
     (dict(lddy=127), INVALID), (dict(lddx=63), INVALID), (dict(da=None), INVALID),
     (dict(db=None), INVALID), (dict(dx=None, da=None, db=None), INVALID),
-    (dict(grad_dtype=FP16), INVALID), (dict(grad_dtype=INT8), INVALID),
+    (dict(dx=FAKE), INVALID), (dict(dy=FAKE + 4096), INVALID), (dict(grad_dtype=FP16), INVALID), (dict(grad_dtype=INT8), INVALID),
     (dict(da=FAKE + 4), ALIGNMENT), (dict(dx=FAKE + 4), ALIGNMENT), (dict(dy=FAKE + 4), ALIGNMENT)])
 def test_backward_refusals(moe, kw, status):
     assert backward(moe, **kw) == status
@@ -78,3 +78,14 @@ def test_workspace_size(moe):
     assert moe.lib.moe_adapters_workspace_size(4, 129, 64, 64, ctypes.byref(n)) == UNSUPPORTED
     assert moe.lib.moe_adapters_workspace_size(4, 16, 64, 64, None) == INVALID
     assert moe.adapters_workspace(4, 16, 64, 128, "cpu").numel() > 0
+
+
+def test_a_scale_that_wants_a_gradient_is_refused(moe):
+    import torch
+
+    from sparse_expert_layer_gb300 import autograd
+
+    x, a, b = torch.zeros(4, 64), torch.zeros(2, 16, 64), torch.zeros(2, 16, 128)
+    plan = autograd.SortPlan(*(torch.zeros(4, dtype=torch.int32) for _ in range(4)))
+    with pytest.raises(RuntimeError, match="scale"):
+        autograd.adapters(None, x, a, b, torch.ones(2, requires_grad=True), plan)

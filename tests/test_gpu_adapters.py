@@ -6,7 +6,7 @@ Tolerance, element by element, u = 2^-24: a sum of n products leaves at most
 within two u of what it holds; blocks, warps and a cluster's parts follow).  v and u then
 enter the next product as two 16-bit numbers, 2^-17 of them lost in bf16 and 2^-22 in
 fp16, or in the sums over positions as three bf16 (2^-24) or two fp16 numbers (2^-22, and
-2^-36 of the call's largest).  What is stored is rounded once.
+2^-36 of the adapter's largest).  What is stored is rounded once.
 """
 import pytest
 import torch
@@ -95,14 +95,13 @@ def exact(c):
         u, du = s * u, s * du + 2 * U * s * u.abs()
         us[j] = u, du
         out["dx"][0][t], out["dx"][1][t] = product(u, f["a"][j], du + split * u.abs())
-    top_u = max((float((u.abs() + du).max()) for u, du in us.values()), default=0.0)
-    top_v = float((out["v"][0].abs() + out["v"][1]).max()) if T else 0.0
     for j, t in enumerate(rows):
         if not len(t):
             continue
         s = f["scale"][j]
         u, du = us[j]
         v, dv = out["v"][0][t], out["v"][1][t]
+        top_u, top_v = float((u.abs() + du).max()), float((v.abs() + dv).max())
         out["da"][0][j], out["da"][1][j] = product(
             u.T, f["x"][t], (du + term * u.abs() + 2.0**-36 * top_u).T)
         g, dg = product(v.T, f["dy"][t], (dv + term * v.abs() + 2.0**-36 * top_v).T)
@@ -460,3 +459,120 @@ def test_a_training_step_in_a_graph(m):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(grads + [norm], first))
+
+
+# By rows the adapters are read from L2 again for every position; from 18 << 20 products
+# T * r * (K + N) on (and more than two rows an adapter) positions go in tiles.
+def tiled(r=16, K=1000, N=1016, J=5, T=None, **kw):
+    T = T or (18 << 20) // (r * (K + N)) + 70
+    assert T > 2 * J and T * r * (K + N) > 18 << 20
+    return make(T, J, r, K, N, kw.pop("dtype", BF16), **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("r,K,N", [(1, 4000, 9), (15, 9, 3001), (16, 1003, 1001), (17, 1002, 1000),
+                                   (32, 1001, 400), (33, 1000, 402), (64, 72, 1015), (65, 777, 8),
+                                   (128, 1, 600), (127, 260, 255)])
+def test_odd_sizes_in_tiles(m, dtype, r, K, N):
+    check(m, tiled(r, K, N, dtype=dtype))
+
+
+@pytest.mark.parametrize("extra", [8, 3])
+@pytest.mark.parametrize("r", [16, 64])
+def test_row_strides_in_tiles(m, extra, r):
+    check(m, tiled(r), extra)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("r", [8, 48])
+def test_gradients_of_the_16_bit_type_in_tiles(m, dtype, r):
+    check(m, tiled(r, dtype=dtype), grad_dtype=dtype)
+
+
+@pytest.mark.parametrize("r", [16, 128])
+@pytest.mark.parametrize("which", ["none", "one", "ends", "alternating", "all_of_the_last", "sixty",
+                                   "one_each"])
+def test_plans_in_tiles(m, which, r):
+    T = 700 if r == 16 else 160
+    J = 64 if which == "one_each" else 6
+    at = torch.arange(T)
+    ids = {"none": torch.full((T,), J), "one": torch.full((T,), 3),
+           "ends": torch.where(at < T - 1, 0, J - 1), "alternating": at % (J + 1),
+           "all_of_the_last": torch.full((T,), J - 1),
+           "sixty": torch.clamp(at // 64, max=J),  # whole tiles
+           "one_each": torch.where(at < J, at, J)}[which]
+    check(m, tiled(r, J=J, T=T, ids=ids.cuda()))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_loud_and_quiet_rows_in_tiles(m, dtype):
+    c = tiled(dtype=dtype)
+    for k in ("x", "dy"):
+        c[k] = (c[k].float() * torch.exp2(torch.randint(-9, 10, (c["T"], 1), generator=gen(5),
+                                                        device="cuda").float())).to(dtype)
+    c["a"] = (c["a"].float() * 64).to(dtype)
+    c["b"] = (c["b"].float() / 64).to(dtype)
+    check(m, c)
+
+
+def test_offsets_and_rows_out_of_range_are_skipped_in_tiles(m):
+    c = tiled(J=3)
+    T, r, K, N = (c[k] for k in ("T", "r", "K", "N"))
+    ws = m.adapters_workspace(T, r, K, N)
+    v = torch.zeros(T, r, device="cuda")
+    a = c["x"], c["a"], c["b"], None
+    y, good = torch.full_like(c["base"], 7), torch.empty_like(c["base"])
+    order = c["order"].clone()
+    gone = order[::3].long()
+    order[::3] = torch.tensor([-1, T, 2**31 - 1], device="cuda", dtype=torch.int32).repeat(T)[
+        :len(order[::3])]
+    m.moe_adapters(*a, c["offsets"], order, c["base"], y, v, ws)
+    m.moe_adapters(*a, c["offsets"], c["order"], c["base"], good, None, ws)
+    torch.cuda.synchronize()
+    stay = torch.ones(T, dtype=torch.bool, device="cuda")
+    stay[gone] = False
+    assert (y[gone] == 7).all() and torch.equal(y[stay], good[stay])
+    dx, da, db = torch.full_like(c["x"], 7), torch.empty(3, r, K, device="cuda"), \
+        torch.empty(3, r, N, device="cuda")
+    m.moe_adapters_backward(c["dy"], c["x"], v, c["a"], c["b"], None, c["offsets"], order, dx, da,
+                            db, ws)
+    assert (dx[gone] == 7).all() and torch.isfinite(da).all() and torch.isfinite(db).all()
+    for offsets in ([0, T, T + 5, 2**31 - 1], [-9, -5, 3, 2], [5, 5, 5, 5], [T, 0, T, 0]):
+        off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+        m.moe_adapters(*a, off, c["order"], c["base"], y, v, ws)
+        m.moe_adapters_backward(c["dy"], c["x"], v, c["a"], c["b"], None, off, c["order"], dx, da,
+                                db, ws)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("T", [90, 700])
+@pytest.mark.parametrize("what", ["loud", float("nan"), float("inf")])
+def test_an_adapter_changes_no_other_ones_results(m, T, dtype, what):
+    r, K, N, J = 16, 1000, 1016, 5
+    c = make(T, J, r, K, N, dtype)
+    ws = m.adapters_workspace(T, r, K, N)
+
+    def step():
+        y, v = torch.empty_like(c["base"]), torch.zeros(T, r, device="cuda")
+        dx, da, db = torch.empty_like(c["x"]), torch.empty(J, r, K, device="cuda"), \
+            torch.empty(J, r, N, device="cuda")
+        plan = c["scale"], c["offsets"], c["order"]
+        m.moe_adapters(c["x"], c["a"], c["b"], *plan, c["base"], y, v, ws)
+        m.moe_adapters_backward(c["dy"], c["x"], v, c["a"], c["b"], *plan, dx, da, db, ws)
+        torch.cuda.synchronize()
+        return y, dx, da, db
+
+    good = step()
+    one = c["ids"] == 2
+    if what == "loud":
+        c["scale"][2] = 2.0**40
+        c["a"][2] *= 2**9
+    else:
+        c["x"][one], c["dy"][one] = what, what
+    got = step()
+    for p, q in zip(got[:2], good[:2]):
+        assert torch.equal(p[~one], q[~one])
+    rest = [0, 1, 3, 4]
+    for p, q in zip(got[2:], good[2:]):
+        assert torch.equal(p[rest], q[rest])
