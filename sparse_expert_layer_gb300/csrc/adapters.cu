@@ -12,11 +12,16 @@
 // Bound by memory: the rank is small beside the channels.  Few rows: a cluster of up to
 // eight CTAs takes one position from x to y, each CTA a slice of the channels on CUDA
 // cores, and v is exchanged through distributed shared memory: one launch, and the
-// adapters are read once.  Many rows: warp-level MMAs with x and the rows of A through
-// cp.async rings; the K of a block of positions may be split over a cluster whose parts
+// adapters are read once.  Many rows: shrink, then expand, with rows of x and of A through
+// cp.async rings into MMAs; the K of a tile of positions may be split over a cluster whose parts
 // are added in order.  v, u are fp32; where they meet 16-bit factors they are split into
 // two 16-bit terms (three bf16 ones for dA and dB, whose results may be fp32): 2^-17
 // (bf16) or 2^-22 (fp16) of them is lost, which a rounded output does not show.
+//
+// Measured on a GB300, cold, us (at 6.78 TB/s): one row, rank 16, 5120 to 5120 channels 7.6 (a
+// launch and three dependent reads); 64 rows of 48 adapters, 7168 to 2048 9.1 (1.6); 8192 rows,
+// 5120 to 5120, rank 16 65 (37), 64 76 (38), 128 130 (39); gradients of 8192 rows, rank 16, 7168
+// and 5120 channels 107 (48), of which the sums over positions are 54.
 #include <math.h>
 
 #include <algorithm>
@@ -108,6 +113,11 @@ __device__ __forceinline__ uint32_t magnitude(float v) {
   return bits < 0x7f800000u ? bits : 0u;
 }
 
+__device__ __forceinline__ void sts128(uint32_t at, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
 // Piece i (channels 8 i ..) of a row of n channels, zeros past its end.
 template <typename T>
 __device__ __forceinline__ uint4 load_piece(const T* row, int i, int n, bool vec) {
@@ -130,17 +140,20 @@ __device__ __forceinline__ void unpack_piece(const uint4& q, float (&f)[8]) {
   }
 }
 template <typename T>
-__device__ __forceinline__ void store_piece(T* row, int i, int n, bool vec, const float (&f)[8]) {
-  const Raw8<T> r = pack8<T>(f);
+__device__ __forceinline__ void store_words(T* row, int i, int n, bool vec, const uint4& q) {
   if (vec) {
-    if (8 * i < n) *reinterpret_cast<uint4*>(row + 8 * i) = r.q[0];
+    if (8 * i < n) *reinterpret_cast<uint4*>(row + 8 * i) = q;
     return;
   }
   T v[8];
-  memcpy(v, &r, 16);
+  memcpy(v, &q, 16);
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     if (8 * i + j < n) row[8 * i + j] = v[j];
+}
+template <typename T>
+__device__ __forceinline__ void store_piece(T* row, int i, int n, bool vec, const float (&f)[8]) {
+  store_words<T>(row, i, n, vec, pack8<T>(f).q[0]);
 }
 // The same into shared memory: asynchronous where rows are whole pieces.
 template <typename T>
@@ -150,10 +163,7 @@ __device__ __forceinline__ void stage_piece(uint32_t dst, const T* row, int i, i
     const bool in = real && 8 * i < n;
     cp_async16_or_zero(dst, row + (in ? 8 * i : 0), in);
   } else {
-    const uint4 q = real ? load_piece<T>(row, i, n, false) : make_uint4(0u, 0u, 0u, 0u);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(q.x), "r"(q.y),
-                 "r"(q.z), "r"(q.w)
-                 : "memory");
+    sts128(dst, real ? load_piece<T>(row, i, n, false) : make_uint4(0u, 0u, 0u, 0u));
   }
 }
 
@@ -341,7 +351,8 @@ int shrink_rows(int r) { return r <= 32 ? 64 : 128; }
 
 // v of a tile of one adapter's positions: x rows and the adapter's rows in 128-byte slices of
 // K.  Slice c of row i lies at 16-byte piece c ^ (i % 8), so that neither copies nor ldmatrix
-// meet a bank twice.  A warp has 16 positions and all ranks.
+// meet a bank twice.  A warp has 16 positions and all ranks.  Waits for slices: 3.7 TB/s at rank
+// 16 (8192 rows of 5120, 23 us), 2.8 at rank 64 (32 us; shared memory half busy).
 template <typename T, int RT>
 __global__ void __launch_bounds__(2 * kShrinkRows<RT>) adapters_shrink_kernel(AdapterArgs a) {
   pdl_enter();
@@ -465,29 +476,214 @@ __global__ void __launch_bounds__(2 * kShrinkRows<RT>) adapters_shrink_kernel(Ad
   }
 }
 
+// The same for more than 64 ranks through tcgen05, whose operands the slices are as they lie: M is
+// the 128 positions, N the ranks, accumulators in tensor memory.  A thread issues a slice's MMAs,
+// their completion frees its stage.  kAccums accumulators in turn, kFlush slices each, shorten the
+// chains of sums that are cut off.  Of ldmatrix and mma.sync 128 ranks are too many: 8192 rows of
+// 5120 to 5120 in 154 us, here 130; of 64 ranks the call takes 75 us with those and 86 with this.
+template <typename T, int RT>
+__global__ void __launch_bounds__(256, RT <= 64 ? 2 : 1) adapters_shrink_tc_kernel(AdapterArgs a) {
+  extern __shared__ unsigned char raw[];
+  __shared__ uint64_t bars[kShrinkStages];
+  __shared__ uint32_t tmem_slot;
+  constexpr int kRows = 128, kThreads = 256;
+  constexpr int kX = kRows * 128, kStage = kX + RT * 128;
+  constexpr int kAccums = 256 / RT, kFlush = 4;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int rank = blockIdx.x, S = gridDim.x, r = a.r;
+  // (the same offset in every CTA of the cluster)
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  pdl_wait();
+  int j, lo, hi;
+  a.seg.tile(blockIdx.y, kRows, &j, &lo, &hi);
+  if (lo >= hi || j >= a.seg.J) {  // the whole cluster
+    if (a.max_v && tid == 0) a.max_v[blockIdx.y * S + rank] = a.max_other[blockIdx.y * S + rank] = 0u;
+    return;
+  }
+  const int slices = (a.K + 63) / 64;
+  const int c0 = (int)((int64_t)slices * rank / S), c1 = (int)((int64_t)slices * (rank + 1) / S);
+  constexpr int kStep = kThreads / 8;  // rows that the threads copy at once
+  const int piece = tid % 8;
+  const T* xr[kRows / kStep];
+  bool real[kRows / kStep];
+#pragma unroll
+  for (int i = 0; i < kRows / kStep; ++i) {
+    const int p = lo + tid / 8 + kStep * i;
+    const int row = p < hi ? a.seg.row(p) : -1;
+    real[i] = row >= 0;
+    xr[i] = static_cast<const T*>(a.x) + (real[i] ? row * a.ldx : 0);
+  }
+  const T* m = static_cast<const T*>(a.m1) + ((int64_t)j * r) * a.K;
+  auto load = [&](int c, int slot) {
+    const uint32_t st = base + slot * kStage;
+#pragma unroll
+    for (int i = 0; i < kRows / kStep; ++i) {
+      const int row = tid / 8 + kStep * i;
+      stage_piece<T>(st + row * 128 + ((piece ^ (row % 8)) * 16), xr[i], c * 8 + piece, a.K, a.xvec,
+                     real[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < RT / kStep; ++i) {
+      const int row = tid / 8 + kStep * i;
+      const bool in = row < r;
+      stage_piece<T>(st + kX + row * 128 + ((piece ^ (row % 8)) * 16),
+                     m + (in ? (int64_t)row * a.K : 0), c * 8 + piece, a.K, a.m1vec, in);
+    }
+  };
+#pragma unroll
+  for (int q = 0; q < kShrinkStages - 1; ++q) {
+    if (c0 + q < c1) load(c0 + q, q);
+    cp_async_commit();
+  }
+  if (tid == 0) {
+#pragma unroll
+    for (int q = 0; q < kShrinkStages; ++q) mbar_init(smem_u32(&bars[q]), 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), kAccums * RT);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();  // (as in the expand: after every CTA has its tensor memory)
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
+  const uint32_t idesc = std::is_same<T, __half>::value ? idesc_f16_f32(kRows, RT)
+                                                        : idesc_bf16_f32(kRows, RT);
+  bool ok = true;
+  for (int c = c0; c < c1; ++c) {
+    const int n = c - c0, slot = n % kShrinkStages;
+    cp_async_wait<kShrinkStages - 2>();
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      const uint32_t st = base + slot * kStage;
+      const uint32_t d = tmem + n / kFlush % kAccums * RT;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        tc_mma_bf16(d, sdesc_sw128(st + k * 32), sdesc_sw128(st + kX + k * 32), idesc,
+                    n >= kFlush * kAccums || n % kFlush > 0 || k > 0);
+      tc_commit(smem_u32(&bars[slot]));
+    }
+    __syncwarp();
+    // the stage of the slice before is free when its MMAs are done
+    const int ahead = c + kShrinkStages - 1;
+    if (n > 0) ok = warp_wait(smem_u32(&bars[(n - 1) % kShrinkStages]),
+                              (n - 1) / kShrinkStages & 1) && ok;
+    if (ahead < c1) load(ahead, (ahead - c0) % kShrinkStages);
+    cp_async_commit();
+  }
+  const int all = c1 - c0;
+  if (all > 0) ok = warp_wait(smem_u32(&bars[(all - 1) % kShrinkStages]),
+                              (all - 1) / kShrinkStages & 1) && ok;
+  tc_fence_after();
+  cp_async_wait<0>();
+  __syncthreads();
+  // [position][rank]; a warp has 32 positions and half the ranks
+  float* red = reinterpret_cast<float*>(raw + (base - smem_u32(raw)));
+  const int used = min(kAccums, (all + kFlush - 1) / kFlush);
+#pragma unroll
+  for (int h = 0; h < RT / 64; ++h) {
+    const int first = warp / 4 * (RT / 2) + 32 * h;
+    float sum[32] = {};
+    for (int q = 0; q < used; ++q) {
+      uint32_t d[32];
+      tmem_ld32(tmem + ((uint32_t)(warp % 4 * 32) << 16) + q * RT + first, d);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum[i] += __uint_as_float(d[i]);
+    }
+    // (rows of 33 x 4 bytes would be out of step with the other CTAs': turn the columns instead)
+    float* at = red + (warp % 4 * 32 + lane) * RT;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) at[(first + i) ^ lane] = ok ? sum[i] : NAN;
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kAccums * RT);
+  }
+  const float s1 = a.scale1 ? a.scale1[j] : 1.f;
+  uint32_t most = 0u;
+  for (int e = rank * kThreads + tid; e < kRows * RT; e += S * kThreads) {
+    const int row = e / RT, i = e % RT, p = lo + row;
+    if (p >= hi || i >= r) continue;
+    float s = 0.f;
+    for (int q = 0; q < S; ++q)
+      s += ld_cluster_f32(mapa_shared(base + (row * RT + (i ^ (row % 32))) * 4, q));
+    s *= s1;
+    a.v[(int64_t)p * r + i] = s;
+    most = max(most, magnitude(s));
+  }
+  cluster_sync_all();
+  if (a.max_v) {
+    uint32_t other = 0u;
+    for (int64_t i = (int64_t)lo * r + rank * kThreads + tid; i < (int64_t)hi * r; i += S * kThreads)
+      other = max(other, magnitude(a.other[i]));
+    most = block_max(most);
+    other = block_max(other);
+    if (tid == 0) {
+      a.max_v[blockIdx.y * S + rank] = most;
+      a.max_other[blockIdx.y * S + rank] = other;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ expand ----
 constexpr int kExpandRows = 128;
 constexpr int kExpandThreads = 256;
 template <int RT>
-constexpr int kExpandPerSm = RT <= 32 ? 3 : RT == 64 ? 2 : 1;  // CTAs
-constexpr int kExpandTile = 256;  // columns of the second matrix in shared memory at once
+constexpr int kExpandPerSm = RT <= 64 ? 2 : 1;  // CTAs
+constexpr int kExpandTile = 128;  // columns of an accumulator, one of two
+constexpr uint32_t kExpandTmem = 2 * kExpandTile;
 
-// y of a tile of one adapter's positions and a range of columns; a warp has 16 positions.  The
-// columns of 32 are dealt to the four n-tiles of MMAs so that a lane's results are eight
-// neighbours: pair t of 16-byte piece q belongs to n-tile t, columns 2 (q % 4) and the next.
-// Tiles of the second matrix are copied one ahead, base is read two or four chunks ahead.
-template <typename T, int RT>
+// Sixteen lanes x 32 columns of fp32: a lane has columns 8 i + 2 (lane % 4) and the next of rows
+// lane / 4 (r[4 i], r[4 i + 1]) and lane / 4 + 8 (r[4 i + 2], r[4 i + 3]).
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// The second matrix as the MMAs' B operand, whose columns lie side by side: 64 columns of a rank
+// are 128 bytes, eight ranks an atom of the 128-byte swizzle, `chunk` bytes to the next 64 columns.
+__device__ __forceinline__ uint64_t expand_b_desc(uint32_t at, uint32_t chunk) {
+  return sdesc_sw128(at) - ((uint64_t)1u << 16) + ((uint64_t)(chunk >> 4) << 16);
+}
+
+// y of a tile of one adapter's positions and a range of columns through tcgen05: v as two terms of
+// 16 bits in shared memory, times tiles of 128 columns of the second matrix, into one of two
+// accumulators while the other is read.  A warp has 32 positions and 64 columns of a tile; the
+// columns of 32 are dealt to the accumulator so that a lane's results are eight neighbours of a
+// position: pair t of 16-byte piece q lies at columns 8 t + 2 q and the next.  The base of the
+// next tile is in registers.
+// LINES (base and at most 32 ranks): 8192 rows, 5120 to 5120, rank 16 65 us and 73 without, rank
+// 32 70 and 77; rank 64 77 and 75, and without a base 109 and 107 (gradients of 8192 rows).  Through
+// shared memory, a position a lane: 66 and 78 (ranks 16, 64), gradients 120; a lane writing 64
+// columns of a position itself 89 and 81.  With mma.sync and v in registers the same calls took 79
+// and 85, gradients 111.
+template <typename T, int RT, bool LINES>
 __global__ void __launch_bounds__(kExpandThreads, kExpandPerSm<RT>)
     adapters_expand_kernel(AdapterArgs a, int range) {
-  pdl_enter();
-  extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int kTile = RT * kExpandTile * 2, kChunks = kExpandTile / 32;
+  extern __shared__ unsigned char raw[];
+  __shared__ uint64_t bars[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ float row_scale[kExpandRows];
   constexpr bool kHalf = std::is_same<T, __half>::value;
-  const uint32_t mt = smem_u32(smem);
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g = lane / 4, tg = lane % 4;
+  constexpr int kAtoms = (RT + 63) / 64, kTerm = kAtoms * kExpandRows * 128;  // bytes of a term
+  constexpr int kChunk = RT * 128, kTile = kExpandTile / 64 * kChunk;
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t tiles = base + 2 * kTerm;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int r = a.r, n_begin = blockIdx.x * range, n_end = min(a.N, n_begin + range);
+  // (what the kernel before does not write is read before the wait for it: that kernel let this
+  // one start only after its own)
   int j, lo, hi;
   a.seg.tile(blockIdx.y, kExpandRows, &j, &lo, &hi);
+  if (lo >= hi || j >= a.seg.J) pdl_wait();  // no CTA ends before the kernel before has
   if (lo >= hi) return;
   if (j >= a.seg.J) {  // rows without an adapter are their base
     if (a.y == a.base) return;
@@ -505,13 +701,14 @@ __global__ void __launch_bounds__(kExpandThreads, kExpandPerSm<RT>)
     return;
   }
   const T* m = static_cast<const T*>(a.m2) + (int64_t)j * r * a.N;
-  // (a warp's 32 pairs of columns are 128 bytes there and here)
   auto load_tile = [&](int n0, int buf) {
-    for (int e = tid; e < RT * (kExpandTile / 2); e += kExpandThreads) {
-      const int i = e / (kExpandTile / 2), w = e % (kExpandTile / 2), q = w / 4, t = w % 4;
+    constexpr int kWords = kExpandTile / 2;
+#pragma unroll
+    for (int e0 = 0; e0 < RT * kWords; e0 += kExpandThreads) {
+      const int e = e0 + tid, i = e / kWords, w = e % kWords, t = w % 4, q = w / 4 % 4;
       const int n = n0 + 2 * w;
-      const uint32_t dst = mt + buf * kTile + i * (kExpandTile * 2) +
-                           (((q / 4 * 4 + t) ^ (i % 8)) * 16) + (q % 4) * 4;
+      const uint32_t dst = tiles + buf * kTile + w / 32 * kChunk + i * 128 +
+                           (((w / 16 % 2 * 4 + t) ^ (i % 8)) * 16) + 4 * q;
       const T* from = m + (int64_t)i * a.N + n;
       if (i < r && n < a.N && a.m2vec) {
         cp_async_unit(dst, from, 4);
@@ -527,119 +724,186 @@ __global__ void __launch_bounds__(kExpandThreads, kExpandPerSm<RT>)
   };
   load_tile(n_begin, 0);
   cp_async_commit();
-  const int pa = lo + warp * 16 + g, pb = pa + 8;
-  const int ra = pa < hi ? a.seg.row(pa) : -1, rb = pb < hi ? a.seg.row(pb) : -1;
-  const bool ina = ra >= 0, inb = rb >= 0, mine = lo + warp * 16 < hi;
-  T* ya = static_cast<T*>(a.y) + (ina ? ra * a.ldy : 0);
-  T* yb = static_cast<T*>(a.y) + (inb ? rb * a.ldy : 0);
-  const T* ba = static_cast<const T*>(a.base) + (ina ? ra * a.ldb : 0);
-  const T* bb = static_cast<const T*>(a.base) + (inb ? rb * a.ldb : 0);
-  // the base of chunk c (columns n_begin + 32 c ..)
-  auto load_base = [&](int c, uint4 (&q)[2]) {
-    const int piece = n_begin / 8 + c * 4 + tg;
-    q[0] = q[1] = make_uint4(0u, 0u, 0u, 0u);
-    if (a.base && 8 * piece < n_end) {
-      if (ina) q[0] = load_piece<T>(ba, piece, a.N, a.yvec);
-      if (inb) q[1] = load_piece<T>(bb, piece, a.N, a.yvec);
-    }
-  };
-  constexpr int kAhead = RT <= 32 ? 2 : 4;
-  uint4 next[kAhead][2];
-#pragma unroll
-  for (int c = 0; c < kAhead; ++c) load_base(c, next[c]);
-  // the rows' v as two 16-bit terms
-  uint32_t hi_t[RT / 16][4], lo_t[RT / 16][4];
-  float sa = a.scale2 ? a.scale2[j] : 1.f, sb = sa;
-  {
-    float f[RT / 16][8];
-    float ma = 0.f, mb = 0.f;
-#pragma unroll
-    for (int k = 0; k < RT / 16; ++k)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int i = k * 16 + tg * 2 + (q & 1) + (q >> 1) * 8;
-        const bool in = i < r;
-        f[k][q] = ina && in ? a.v[(int64_t)pa * r + i] : 0.f;
-        f[k][4 + q] = inb && in ? a.v[(int64_t)pb * r + i] : 0.f;
-        ma = fmaxf(ma, fabsf(f[k][q]));
-        mb = fmaxf(mb, fabsf(f[k][4 + q]));
-      }
-    float upa = sa, upb = sb;  // bf16: the MMAs add scale * v * b to the base themselves
-    if constexpr (kHalf) {     // into fp16's range, row by row; scaled back afterwards
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
-        mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-      }
-      const uint32_t ua = fp16_range_bits(__float_as_uint(ma));
-      const uint32_t ub = fp16_range_bits(__float_as_uint(mb));
-      upa = __uint_as_float(ua);
-      upb = __uint_as_float(ub);
-      sa *= inverse_pow2(ua);
-      sb *= inverse_pow2(ub);
-    }
-#pragma unroll
-    for (int k = 0; k < RT / 16; ++k)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        split2<T>(f[k][2 * q] * upa, f[k][2 * q + 1] * upa, hi_t[k][2 * q], lo_t[k][2 * q]);
-        split2<T>(f[k][4 + 2 * q] * upb, f[k][5 + 2 * q] * upb, hi_t[k][2 * q + 1],
-                  lo_t[k][2 * q + 1]);
-      }
+  if (n_begin + kExpandTile < n_end) load_tile(n_begin + kExpandTile, 1);
+  cp_async_commit();
+  if (tid == 0) {
+    mbar_init(smem_u32(&bars[0]), 1);
+    mbar_init(smem_u32(&bars[1]), 1);
+    fence_barrier_init();
   }
-  int buf = 0;
-  for (int n0 = n_begin; n0 < n_end; n0 += kExpandTile, buf ^= 1) {
-    cp_async_wait<0>();
-    __syncthreads();  // the tile is there, and nobody reads the one before
-    if (n0 + kExpandTile < n_end) load_tile(n0 + kExpandTile, buf ^ 1);
-    cp_async_commit();
-    if (!mine) continue;
-    const uint32_t tile = mt + buf * kTile;
-#pragma unroll kAhead
-    for (int c = 0; c < kChunks; ++c) {
-      const int piece = n0 / 8 + c * 4 + tg;
-      const uint4 qa = next[c % kAhead][0], qb = next[c % kAhead][1];
-      load_base((n0 - n_begin) / 32 + c + kAhead, next[c % kAhead]);
-      if (n0 + c * 32 >= n_end) break;
-      float fa[8], fb[8], d[4][4] = {};
-      unpack_piece<T>(qa, fa);
-      unpack_piece<T>(qb, fb);
-      if constexpr (!kHalf) {
+  // The lane's four positions are mine + 8 i, and two pieces of each: tg and tg + 4 of a line of 64
+  // columns.  LINES: lanes with the positions beside them (lane ^ 4) pass half of the even one's
+  // line and then half of the odd one's, so that eight lanes read and write whole lines.
+  const int mine = warp % 4 * 32 + lane / 4, col = warp / 4 * 64, tg = lane % 4;
+  const bool odd = lane & 4;
+  int row[4][2];
+  bool any = false;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            d[t][h] = fa[2 * t + h];
-            d[t][2 + h] = fb[2 * t + h];
-          }
-      }
-#pragma unroll
-      for (int k = 0; k < RT / 16; ++k) {
-        const int i = k * 16 + lane % 16;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t bf[4];
-          ldsm4_trans(tile + i * (kExpandTile * 2) + (((c * 4 + h * 2 + lane / 16) ^ (i % 8)) * 16),
-                      bf);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            mma16816<T>(d[2 * h + t], hi_t[k][0], hi_t[k][1], hi_t[k][2], hi_t[k][3], bf[2 * t],
-                        bf[2 * t + 1]);
-            mma16816<T>(d[2 * h + t], lo_t[k][0], lo_t[k][1], lo_t[k][2], lo_t[k][3], bf[2 * t],
-                        bf[2 * t + 1]);
-          }
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          fa[2 * t + h] = kHalf ? fmaf(sa, d[t][h], fa[2 * t + h]) : d[t][h];
-          fb[2 * t + h] = kHalf ? fmaf(sb, d[t][2 + h], fb[2 * t + h]) : d[t][2 + h];
-        }
-      if (ina) store_piece<T>(ya, piece, a.N, a.yvec, fa);
-      if (inb) store_piece<T>(yb, piece, a.N, a.yvec, fb);
+    for (int q = 0; q < 2; ++q) {
+      const int p = lo + (LINES ? (mine & ~1) + q : mine) + 8 * i;
+      row[i][q] = p < hi ? a.seg.row(p) : -1;
+      any = any || row[i][q] >= 0;
     }
+  any = __any_sync(0xffffffffu, any);
+  auto piece = [&](int q) { return tg + (LINES ? (odd ? 4 : 0) : 4 * q); };
+  uint4 next[4][2];
+  auto load_base = [&](int n, int i, int q) {
+    next[i][q] = make_uint4(0u, 0u, 0u, 0u);
+    if (a.base && row[i][q] >= 0 && n + 8 * piece(q) < n_end)
+      next[i][q] = load_piece<T>(static_cast<const T*>(a.base) + row[i][q] * a.ldb,
+                                 n / 8 + piece(q), a.N, a.yvec);
+  };
+  // (even, odd) rows' pieces <-> the own position's pieces tg and tg + 4
+  auto swap_halves = [&](uint4& even, uint4& other) {
+    const uint4 give = odd ? even : other;
+    uint4 got;
+    got.x = __shfl_xor_sync(0xffffffffu, give.x, 4);
+    got.y = __shfl_xor_sync(0xffffffffu, give.y, 4);
+    got.z = __shfl_xor_sync(0xffffffffu, give.z, 4);
+    got.w = __shfl_xor_sync(0xffffffffu, give.w, 4);
+    if (odd)
+      even = got;
+    else
+      other = got;
+  };
+#pragma unroll
+  for (int i = 0; i < 8; ++i) load_base(n_begin + col, i % 4, i / 4);
+  // (no kernel that waits for this one starts, and takes tensor memory, before every CTA of this
+  // one has its own)
+  __syncwarp();
+  if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), kExpandTmem);
+  pdl_wait();
+  // v as two terms: a row's pieces of eight ranks by neighbouring lanes
+  {
+    const float scale = a.scale2 ? a.scale2[j] : 1.f;
+    constexpr int kRowLanes = RT / 8;
+#pragma unroll
+    for (int e0 = 0; e0 < kExpandRows * kRowLanes; e0 += kExpandThreads) {
+      const int e = e0 + tid, i = e / kRowLanes, k8 = e % kRowLanes;
+      const bool in = lo + i < hi;
+      const float* v = a.v + (int64_t)(lo + (in ? i : 0)) * r;
+      float f[8] = {};
+      if (r % 8 == 0) {
+        if (in && k8 * 8 < r) {
+          *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(v + k8 * 8);
+          *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(v + k8 * 8 + 4);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (in && k8 * 8 + c < r) f[c] = v[k8 * 8 + c];
+      }
+      float up = scale;  // bf16: scale * v
+      if constexpr (kHalf) {  // into fp16's range, row by row; scaled back afterwards
+        float most = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) most = fmaxf(most, fabsf(f[c]));
+#pragma unroll
+        for (int o = 1; o < kRowLanes; o <<= 1)
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        const uint32_t bits = fp16_range_bits(__float_as_uint(most));
+        up = __uint_as_float(bits);
+        if (k8 == 0) row_scale[i] = scale * inverse_pow2(bits);
+      }
+      uint32_t first[4], rest[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) split2<T>(f[2 * c] * up, f[2 * c + 1] * up, first[c], rest[c]);
+      const uint32_t at =
+          base + k8 / 8 * (kExpandRows * 128) + i * 128 + (((k8 % 8) ^ (i % 8)) * 16);
+      sts128(at, make_uint4(first[0], first[1], first[2], first[3]));
+      sts128(at + kTerm, make_uint4(rest[0], rest[1], rest[2], rest[3]));
+    }
+  }
+  cp_async_wait<1>();
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
+  const uint32_t idesc = (kHalf ? idesc_f16_f32(kExpandRows, kExpandTile)
+                                : idesc_bf16_f32(kExpandRows, kExpandTile)) |
+                         (1u << 16);  // B's columns side by side
+  auto multiply = [&](int buf) {  // one thread
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int k = 0; k < RT / 16; ++k)
+        tc_mma_bf16(tmem + buf * kExpandTile,
+                    sdesc_sw128(base + t * kTerm + k / 4 * (kExpandRows * 128) + k % 4 * 32),
+                    expand_b_desc(tiles + buf * kTile + k * 2048, kChunk), idesc, t > 0 || k > 0);
+    tc_commit(smem_u32(&bars[buf]));
+  };
+  if (tid == 0) multiply(0);
+  float back[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) back[i] = kHalf ? row_scale[mine + 8 * i] : 1.f;
+  bool ok = true;
+  int use = 0;
+  for (int n0 = n_begin; n0 < n_end; n0 += kExpandTile, ++use) {
+    const int buf = use & 1;
+    const bool more = n0 + kExpandTile < n_end;
+    if (more) {  // the next tile is there, and nobody reads its accumulator
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncthreads();
+      tc_fence_after();
+      if (tid == 0) multiply(buf ^ 1);
+      __syncwarp();
+    }
+    ok = warp_wait(smem_u32(&bars[buf]), (use >> 1) & 1) && ok;
+    tc_fence_after();
+    if (n0 + 2 * kExpandTile < n_end) load_tile(n0 + 2 * kExpandTile, buf);
+    cp_async_commit();
+    if (!any) continue;
+    const int n = n0 + col;
+    // a piece of position i: base plus its part of 16 positions and 32 columns
+    auto finish = [&](uint4 base, const uint32_t (&d)[16], int i) {
+      float f[8];
+      unpack_piece<T>(base, f);
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        f[c] = ok ? fmaf(back[i], __uint_as_float(d[c / 2 * 4 + i % 2 * 2 + c % 2]), f[c]) : NAN;
+      return pack8<T>(f).q[0];
+    };
+    auto store = [&](int i, int q, const uint4& v) {
+      if (row[i][q] >= 0 && n + 8 * piece(q) < n_end)
+        store_words<T>(static_cast<T*>(a.y) + row[i][q] * a.ldy, n / 8 + piece(q), a.N, a.yvec, v);
+      load_base(n + kExpandTile, i, q);
+    };
+    const uint32_t acc = tmem + ((uint32_t)(warp % 4 * 32) << 16) + buf * kExpandTile + col;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {  // 16 positions of a line, or 32 of half of one
+      uint32_t d[2][16];
+#pragma unroll
+      for (int l = 0; l < 2; ++l)
+        tmem_ld_rows(acc + ((uint32_t)(16 * (LINES ? k : l)) << 16) + 32 * (LINES ? l : k), d[l]);
+      tmem_ld_wait();
+      if constexpr (LINES) {
+#pragma unroll
+        for (int i = 2 * k; i < 2 * k + 2; ++i) {
+          uint4 q0 = next[i][0], q1 = next[i][1];
+          swap_halves(q0, q1);
+          q0 = finish(q0, d[0], i);
+          q1 = finish(q1, d[1], i);
+          swap_halves(q0, q1);
+          store(i, 0, q0);
+          store(i, 1, q1);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store(i, k, finish(next[i][k], d[i / 2], i));
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kExpandTmem);
   }
 }
 
@@ -871,7 +1135,8 @@ constexpr int outer_smem() {
 }
 template <int RT>
 constexpr int shrink_smem() {
-  return std::max(kShrinkStages * (kShrinkRows<RT> + RT) * 128, kShrinkRows<RT> * RT * 4);
+  // (on the tensor cores from a 1024-byte boundary on)
+  return kShrinkStages * (kShrinkRows<RT> + RT) * 128 + (RT <= 64 ? 0 : 1024);
 }
 
 // The most CTAs of a power of two, up to eight, that share `units` of work while there
@@ -911,27 +1176,43 @@ template <typename T, int RT>
 void launch_tiles(const Launch& L, const AdapterArgs& a, int rt_slot) {
   const int type = std::is_same<T, __half>::value ? 1 : 0;
   const int S = shrink_cluster(a, L.num_sms);
-  set_smem_attr_once(reinterpret_cast<const void*>(adapters_shrink_kernel<T, RT>),
-                     shrink_smem<RT>(), kAttrAdapters + 8 * type + rt_slot);
-  launch_begin(L, MOE_K_ADAPTERS);
-  launch_kernel_cluster(adapters_shrink_kernel<T, RT>, dim3(S, adapter_tiles(a, kShrinkRows<RT>)),
-                        dim3(S), dim3(2 * kShrinkRows<RT>), shrink_smem<RT>(), L.stream, a);
-  launch_end(L, MOE_K_ADAPTERS);
+  auto shrink = [&](auto kernel) {
+    set_smem_attr_once(reinterpret_cast<const void*>(kernel), shrink_smem<RT>(),
+                       kAttrAdapters + 8 * type + rt_slot);
+    launch_begin(L, MOE_K_ADAPTERS);
+    launch_kernel_cluster(kernel, dim3(S, adapter_tiles(a, kShrinkRows<RT>)), dim3(S),
+                          dim3(2 * kShrinkRows<RT>), shrink_smem<RT>(), L.stream, a);
+    launch_end(L, MOE_K_ADAPTERS);
+  };
+  if constexpr (RT <= 64)
+    shrink(adapters_shrink_kernel<T, RT>);
+  else
+    shrink(adapters_shrink_tc_kernel<T, RT>);
   if (!a.y) return;
-  // ranges of whole tiles of columns, for one round of CTAs: a CTA has about as long
-  // to start (tile, rows, v) as for two tiles of columns
-  const int blocks = (a.seg.T + kExpandRows - 1) / kExpandRows + std::min(a.seg.J, a.seg.T) / 2;
+  // ranges of whole tiles of columns, for one round of CTAs: a CTA has about as long to start
+  // (tile, rows, v) as for several tiles of columns (at most 4 or 6 of them a CTA, 640 or 448 CTAs
+  // where 256 do: 84 us instead of 78 at 8192 rows and rank 64; adapters whose rows are fewer than
+  // a tile's have one each)
+  const int blocks = std::max((a.seg.T + kExpandRows - 1) / kExpandRows +
+                                  std::min(a.seg.J, a.seg.T) / 2, std::min(a.seg.J, a.seg.T));
   const int tiles = (a.N + kExpandTile - 1) / kExpandTile;
   const int ranges = std::max(1, std::min(tiles, kExpandPerSm<RT> * L.num_sms / blocks));
   const int per = (tiles + ranges - 1) / ranges;
-  constexpr int kSmem = 2 * RT * kExpandTile * 2;
-  set_smem_attr_once(reinterpret_cast<const void*>(adapters_expand_kernel<T, RT>), kSmem,
-                     kAttrAdapters + 8 * type + 4 + rt_slot);
-  launch_begin(L, MOE_K_ADAPTERS);
-  launch_kernel(adapters_expand_kernel<T, RT>,
-                dim3((tiles + per - 1) / per, adapter_tiles(a, kExpandRows)), dim3(kExpandThreads),
-                kSmem, L.stream, a, per * kExpandTile);
-  launch_end(L, MOE_K_ADAPTERS);
+  constexpr int kSmem = 1024 + 2 * ((RT + 63) / 64 * kExpandRows * 128 + RT * kExpandTile * 2);
+  auto expand = [&](auto kernel, int slot) {
+    set_smem_attr_once(reinterpret_cast<const void*>(kernel), kSmem, kAttrAdapters + slot);
+    launch_begin(L, MOE_K_ADAPTERS);
+    launch_kernel(kernel, dim3((tiles + per - 1) / per, adapter_tiles(a, kExpandRows)),
+                  dim3(kExpandThreads), kSmem, L.stream, a, per * kExpandTile);
+    launch_end(L, MOE_K_ADAPTERS);
+  };
+  if constexpr (RT <= 32) {
+    if (a.base) {
+      expand(adapters_expand_kernel<T, RT, true>, 24 + 2 * type + rt_slot);
+      return;
+    }
+  }
+  expand(adapters_expand_kernel<T, RT, false>, 8 * type + 4 + rt_slot);
 }
 template <typename T, int RT>
 void launch_outer(const Launch& L, OuterArgs a, int rt_slot) {

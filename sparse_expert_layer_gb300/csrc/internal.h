@@ -429,8 +429,8 @@ enum {
   kAttrW4Slots = 3 * 3 * 2,
   kAttrFewRoute = kAttrW4Base + kAttrW4Slots,  // 4 slots: tokens 1, 2, 4, 8
   kAttrFewFfn = kAttrFewRoute + 4,             // 20 slots: kinds of weights
-  kAttrAdapters = kAttrFewFfn + 20,            // 24 slots: three kernels x types x ranks
-  kAttrSlots = kAttrAdapters + 24
+  kAttrAdapters = kAttrFewFfn + 20,            // 28 slots: kernels x types x ranks
+  kAttrSlots = kAttrAdapters + 28
 };
 void set_smem_attr_once(const void* func, int bytes, int slot);
 

@@ -576,3 +576,36 @@ def test_an_adapter_changes_no_other_ones_results(m, T, dtype, what):
     rest = [0, 1, 3, 4]
     for p, q in zip(got[2:], good[2:]):
         assert torch.equal(p[rest], q[rest])
+
+
+@pytest.mark.parametrize("r", [16, 64, 128])
+def test_beside_the_layer(m, r):
+    """Calls in turn with the layer's on one stream, whose kernels start before the last ones have
+    ended, and beside them on another one: both hold tensor memory."""
+    c = tiled(r, 1024, 1024, T=1500)
+    spec = dict(hidden=1024, inter=512, n_routed=8, top_k=2, renormalize=True)
+    cfg = m.config_from_spec(spec)
+    T, g = c["T"], gen(7)
+    w = [(randn(g, 8, *s) / 32).to(BF16) for s in ((512, 1024), (512, 1024), (1024, 512))]
+    w_r = randn(g, 8, 1024) / 32
+    lws = [m.workspace(cfg, T) for _ in range(2)]
+    ws = [m.adapters_workspace(T, r, 1024, 1024) for _ in range(2)]
+    out = [torch.empty_like(c["x"]) for _ in range(2)]
+    y = [torch.empty_like(c["base"]) for _ in range(2)]
+
+    def step(i, stream=None):
+        m.moe_layer_forward(cfg, T, c["x"], w_r, None, *w, None, None, None, None, None, None,
+                            out[i], lws[i], stream=stream)
+        m.moe_adapters(out[i], c["a"], c["b"], c["scale"], c["offsets"], c["order"], c["base"], y[i],
+                       None, ws[i], stream=stream)
+
+    step(0)
+    torch.cuda.synchronize()
+    first = out[0].clone(), y[0].clone()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            step(i, s)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(out[i], first[0]) and torch.equal(y[i], first[1])
