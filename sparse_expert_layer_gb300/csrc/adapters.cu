@@ -840,7 +840,6 @@ __global__ void __launch_bounds__(kExpandThreads, kExpandPerSm<RT>)
   float back[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) back[i] = kHalf ? row_scale[mine + 8 * i] : 1.f;
-  bool ok = true;
   int use = 0;
   for (int n0 = n_begin; n0 < n_end; n0 += kExpandTile, ++use) {
     const int buf = use & 1;
@@ -854,7 +853,8 @@ __global__ void __launch_bounds__(kExpandThreads, kExpandPerSm<RT>)
       if (tid == 0) multiply(buf ^ 1);
       __syncwarp();
     }
-    ok = warp_wait(smem_u32(&bars[buf]), (use >> 1) & 1) && ok;
+    if (!warp_wait(smem_u32(&bars[buf]), (use >> 1) & 1))  // gave up: no numbers then
+      back[0] = back[1] = back[2] = back[3] = NAN;
     tc_fence_after();
     if (n0 + 2 * kExpandTile < n_end) load_tile(n0 + 2 * kExpandTile, buf);
     cp_async_commit();
@@ -862,11 +862,11 @@ __global__ void __launch_bounds__(kExpandThreads, kExpandPerSm<RT>)
     const int n = n0 + col;
     // a piece of position i: base plus its part of 16 positions and 32 columns
     auto finish = [&](uint4 base, const uint32_t (&d)[16], int i) {
-      float f[8];
-      unpack_piece<T>(base, f);
+      float f[8] = {};
+      if (a.base) unpack_piece<T>(base, f);
 #pragma unroll
       for (int c = 0; c < 8; ++c)
-        f[c] = ok ? fmaf(back[i], __uint_as_float(d[c / 2 * 4 + i % 2 * 2 + c % 2]), f[c]) : NAN;
+        f[c] = fmaf(back[i], __uint_as_float(d[c / 2 * 4 + i % 2 * 2 + c % 2]), f[c]);
       return pack8<T>(f).q[0];
     };
     auto store = [&](int i, int q, const uint4& v) {
