@@ -4,6 +4,11 @@
 // of the list of chunks of 32 KB; the first kernel goes through it forwards and the second
 // backwards, so that what the first read last is still in L2 when the second starts there.
 //
+// Bound by memory: a product needs the norm, so what L2 does not hold is read twice.  48 fp32
+// tensors of 25 MB 12.1 us (read and written once: 7.4 at 6.78 TB/s; two launches and a sum of all
+// slots are the rest); 37 tensors of all types, 40 MB 22; 3 GB of bf16 in three tensors 1370 (two
+// reads and a write: 1335; 7.0 TB/s in the first kernel, 6.5 in the second).
+//
 // The squares of a thread's 64 elements of a chunk (fp32: 32) are added in fp32, its
 // chunks and the threads as pairs of fp32, each CTA's sum in a slot of its own, and the slots
 // in order: the same bits on every call on one device.
