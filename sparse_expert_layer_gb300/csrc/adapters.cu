@@ -173,12 +173,6 @@ __device__ __forceinline__ void ldsm4(uint32_t at, uint32_t (&r)[4]) {
                : "r"(at)
                : "memory");
 }
-__device__ __forceinline__ void ldsm4_trans(uint32_t at, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(at)
-               : "memory");
-}
 
 // The largest |v| that a block has seen, for the range of fp16 terms: one word a block.
 __device__ __forceinline__ uint32_t block_max(uint32_t bits) {
@@ -648,9 +642,9 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[16]) 
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-// The second matrix as the MMAs' B operand, whose columns lie side by side: 64 columns of a rank
-// are 128 bytes, eight ranks an atom of the 128-byte swizzle, `chunk` bytes to the next 64 columns.
-__device__ __forceinline__ uint64_t expand_b_desc(uint32_t at, uint32_t chunk) {
+// An MMA's operand whose rows (of K) have their elements of M or N side by side: 64 of them are 128
+// bytes, eight rows an atom of the 128-byte swizzle, `chunk` bytes to the next 64 elements.
+__device__ __forceinline__ uint64_t sdesc_rows(uint32_t at, uint32_t chunk) {
   return sdesc_sw128(at) - ((uint64_t)1u << 16) + ((uint64_t)(chunk >> 4) << 16);
 }
 
@@ -833,7 +827,7 @@ __global__ void __launch_bounds__(kExpandThreads, kExpandPerSm<RT>)
       for (int k = 0; k < RT / 16; ++k)
         tc_mma_bf16(tmem + buf * kExpandTile,
                     sdesc_sw128(base + t * kTerm + k / 4 * (kExpandRows * 128) + k % 4 * 32),
-                    expand_b_desc(tiles + buf * kTile + k * 2048, kChunk), idesc, t > 0 || k > 0);
+                    sdesc_rows(tiles + buf * kTile + k * 2048, kChunk), idesc, t > 0 || k > 0);
     tc_commit(smem_u32(&bars[buf]));
   };
   if (tid == 0) multiply(0);
@@ -936,26 +930,48 @@ constexpr int kOuterPerSm = RT == 16 ? 3 : RT <= 64 ? 2 : 1;  // CTAs
 template <typename T>
 constexpr int kTerms = std::is_same<T, __half>::value ? 2 : 3;
 
-// Sums over the positions of an adapter, a tile of columns for all ranks.  The MMAs' rows
-// are the ranks, their K the positions: v and x are both read transposed.
+// What the sums over positions of RT ranks need.
+template <typename T, int RT>
+struct OuterShape {
+  static constexpr int kTerm = kTerms<T>;
+  static constexpr int kChunk = kOuterRows * 128;  // 64 columns or ranks of a stage
+  static constexpr int kX = kOuterCols<RT> / 64 * kChunk, kV = kOuterRows * RT * 4;
+  static constexpr int kPlanes = (RT * kTerm + 63) / 64 * kChunk;  // the terms of v
+  // terms side by side in an accumulator, or added up in it
+  static constexpr int kStacked = RT <= 64 ? kTerm : 1, kParts = kTerm / kStacked;
+  static constexpr int kN = RT * kStacked;
+  static constexpr int kUsed = kOuterCols<RT> / 128 * kN;  // columns of tensor memory
+  static constexpr int kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
+  // stages until an accumulator has sixteen MMAs (18 where terms are added up)
+  static constexpr int kFlush = kParts == 1 ? 8 : 9 / kParts;
+  static constexpr int kBytes =
+      1024 + kOuterStages * (kX + kV) + 2 * kPlanes + 2 * kOuterAhead * kOuterRows * 4;
+  static_assert(RT * kOuterCols<RT> * 4 <= kOuterStages * kX + 2 * kPlanes + kOuterStages * kV, "");
+};
+
+// Sums over the positions of an adapter, a tile of columns for all ranks, through tcgen05: M is
+// 128 columns, K the positions, N the ranks of all terms side by side (of 128 ranks: of one term
+// after the other).  Rows of x and terms of v lie as the MMAs read them, both transposed.  After
+// every kFlush stages the accumulators are added, rounded, to sums in registers: MMAs cut theirs
+// off where fp32 ends.
 template <typename T, int RT>
 __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer_kernel(OuterArgs a) {
-  pdl_enter();
-  extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int kCols = kOuterCols<RT>, kPieces = kCols / 8;
-  constexpr int kX = kOuterRows * kCols * 2;
-  // rows of v 16 bytes longer than they are: eight lie side by side in the banks
-  constexpr int kVRow = RT * 2 + 16, kPlane = kOuterRows * kVRow, kTerm = kTerms<T>;
-  constexpr int kWarpCols = kCols / 8;  // of each of the eight warps
+  extern __shared__ unsigned char raw[];
+  __shared__ uint64_t bars[kOuterStages];
+  __shared__ uint32_t tmem_slot;
+  using O = OuterShape<T, RT>;
+  constexpr int kCols = kOuterCols<RT>, kPieces = kCols / 8, kBlocks = kCols / 128;
+  constexpr int kX = O::kX, kV = O::kV, kPlanes = O::kPlanes, kTerm = kTerms<T>;
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  unsigned char* const smem = raw + (base - smem_u32(raw));
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int rank = blockIdx.x, S = gridDim.x, j = blockIdx.z, r = a.r;
   const bool second = (int)blockIdx.y >= a.side[0].tiles;
   const OuterSide& s = a.side[second];
   const int n0 = (blockIdx.y - (second ? a.side[0].tiles : 0)) * kCols;
-  constexpr int kV = kOuterRows * RT * 4;
-  const uint32_t base = smem_u32(smem), vring = base + kOuterStages * kX;
-  const uint32_t planes = vring + kOuterStages * kV;
-  int* rows = reinterpret_cast<int*>(smem + kOuterStages * (kX + kV) + 2 * kTerm * kPlane);
+  const uint32_t planes = base + kOuterStages * kX, vring = planes + 2 * kPlanes;
+  int* rows = reinterpret_cast<int*>(smem + kOuterStages * (kX + kV) + 2 * kPlanes);
+  pdl_wait();
   const int lo = a.seg.at(j), hi = max(lo, a.seg.at(j + 1));
   // this rank's positions: whole stages
   const int stages = (hi - lo + kOuterRows - 1) / kOuterRows;
@@ -989,7 +1005,8 @@ __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer
     for (int m = 0; m < kOuterRows * kPieces / kOuterThreads; ++m) {
       const int i = tid / kPieces + m * (kOuterThreads / kPieces), piece = tid % kPieces;
       const int row = from[i];
-      stage_piece<T>(base + slot * kX + i * (kCols * 2) + ((piece ^ (i % 8)) * 16),
+      stage_piece<T>(base + slot * kX + piece / 8 * O::kChunk + i * 128 +
+                         (((piece % 8) ^ (i % 8)) * 16),
                      static_cast<const T*>(s.x) + (row >= 0 ? row * s.ldx : 0), n0 / 8 + piece, s.n,
                      s.vec, row >= 0);
     }
@@ -1026,12 +1043,13 @@ __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer
                    : "memory");
 #pragma unroll
       for (int c = 0; c < 4; ++c) f[c] *= up;
-      const uint32_t at = planes + buf * kTerm * kPlane + i * kVRow + k * 2;
 #pragma unroll
       for (int t = 0; t < kTerm; ++t) {
         const uint32_t w0 = pack2<T>(f[0], f[1]), w1 = pack2<T>(f[2], f[3]);
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + t * kPlane), "r"(w0), "r"(w1)
-                     : "memory");
+        const int n = t * RT + k;
+        const uint32_t at = planes + buf * kPlanes + n / 64 * O::kChunk + i * 128 +
+                            (((n % 64 / 8) ^ (i % 8)) * 16) + n % 8 * 2;
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(w0), "r"(w1) : "memory");
         const float2 g0 = unpack2<T>(w0), g1 = unpack2<T>(w1);
         f[0] -= g0.x;
         f[1] -= g0.y;
@@ -1040,77 +1058,95 @@ __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer
       }
     }
   };
-  // as in the shrink: sums of kFlush stages' MMAs (two or three terms of v, two steps each)
-  constexpr int kFlush = 2;
-  float acc[RT / 16][kWarpCols / 8][4] = {}, sum[RT / 16][kWarpCols / 8][4] = {};
-  auto flush = [&]() {
-#pragma unroll
-    for (int m = 0; m < RT / 16; ++m)
-#pragma unroll
-      for (int c = 0; c < kWarpCols / 8; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sum[m][c][i] += acc[m][c][i];
-          acc[m][c][i] = 0.f;
-        }
-  };
   look_up(q0);
+  if (tid == 0) {
+#pragma unroll
+    for (int q = 0; q < kOuterStages; ++q) mbar_init(smem_u32(&bars[q]), 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), O::kTmem);
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  pdl_trigger();  // (every CTA has its tensor memory before another kernel's CTAs take theirs)
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
 #pragma unroll
   for (int i = 0; i < kOuterStages - 1; ++i) {
     if (q0 + i < q1) load(q0 + i, i);
     cp_async_commit();
   }
+  const uint32_t idesc = (std::is_same<T, __half>::value ? idesc_f16_f32(128, O::kN)
+                                                         : idesc_bf16_f32(128, O::kN)) |
+                         (1u << 15) | (1u << 16);  // columns, and ranks, side by side
+  // a thread has a column, and half of the ranks where the tile is 128 columns
+  constexpr int kSums = RT * kBlocks / 2;
+  const int block = kBlocks == 2 ? warp / 4 : 0, first = kBlocks == 2 ? 0 : warp / 4 * kSums;
+  float sum[kSums] = {};
+  bool ok = true;
   for (int q = q0; q < q1; ++q) {
-    const int buf = (q - q0) & 1, slot = (q - q0) % kOuterStages;
+    const int n = q - q0, buf = n & 1, slot = n % kOuterStages;
     cp_async_wait<kOuterStages - 2>();
     split_v(slot, buf);  // what this thread copied
+    fence_proxy_async_smem();
+    tc_fence_before();
     __syncthreads();
+    if (tid == 0) {
+      tc_fence_after();
+#pragma unroll
+      for (int m = 0; m < kBlocks; ++m)
+#pragma unroll
+        for (int t = 0; t < O::kParts; ++t)
+#pragma unroll
+          for (int k = 0; k < kOuterRows / 16; ++k)
+            tc_mma_bf16(tmem + m * O::kN,
+                        sdesc_rows(base + slot * kX + m * 2 * O::kChunk + k * 2048, O::kChunk),
+                        sdesc_rows(planes + buf * kPlanes + t * (O::kN / 64 * O::kChunk) + k * 2048,
+                                   O::kChunk),
+                        idesc, n % O::kFlush > 0 || t > 0 || k > 0);
+      tc_commit(smem_u32(&bars[slot]));
+    }
+    __syncwarp();
+    // the stage before is free when its MMAs are done
+    if (n > 0) ok = warp_wait(smem_u32(&bars[(n - 1) % kOuterStages]),
+                              (n - 1) / kOuterStages & 1) && ok;
     const int ahead = q + kOuterStages - 1;
     if (ahead < q1) load(ahead, (ahead - q0) % kOuterStages);
     cp_async_commit();
-    if ((q - q0) % kOuterAhead == 0 && q + kOuterAhead < q1) look_up(q + kOuterAhead);
-    const uint32_t xs = base + slot * kX;
-    const uint32_t vs = planes + buf * kTerm * kPlane;
+    if (n % kOuterAhead == 0 && q + kOuterAhead < q1) look_up(q + kOuterAhead);
+    if (n % O::kFlush == O::kFlush - 1 || q == q1 - 1) {
+      ok = warp_wait(smem_u32(&bars[slot]), n / kOuterStages & 1) && ok;
+      tc_fence_after();
 #pragma unroll
-    for (int kk = 0; kk < kOuterRows / 16; ++kk) {
-      uint32_t bf[kWarpCols / 16][4];
+      for (int c = 0; c < kSums; c += 16) {
+        uint32_t d[kTerm][16];
 #pragma unroll
-      for (int c = 0; c < kWarpCols / 16; ++c) {
-        const int i = kk * 16 + lane % 16, piece = warp * (kWarpCols / 8) + c * 2 + lane / 16;
-        ldsm4_trans(xs + i * (kCols * 2) + ((piece ^ (i % 8)) * 16), bf[c]);
-      }
+        for (int t = 0; t < O::kStacked; ++t)
+          tmem_ld16(tmem + ((uint32_t)(warp % 4 * 32) << 16) + block * O::kN + t * RT + first + c, d[t]);
+        tmem_ld_wait();
 #pragma unroll
-      for (int m = 0; m < RT / 16; ++m)
+        for (int i = 0; i < 16; ++i) {
+          float f = __uint_as_float(d[0][i]);
 #pragma unroll
-        for (int t = 0; t < kTerm; ++t) {
-          uint32_t af[4];
-          // (ranks 0-7, positions 0-7) (8-15, 0-7) (0-7, 8-15) (8-15, 8-15)
-          const int i = kk * 16 + lane % 8 + lane / 16 * 8, piece = m * 2 + lane / 8 % 2;
-          ldsm4_trans(vs + t * kPlane + i * kVRow + piece * 16, af);
-#pragma unroll
-          for (int c = 0; c < kWarpCols / 16; ++c) {
-            mma16816<T>(acc[m][2 * c], af[0], af[1], af[2], af[3], bf[c][0], bf[c][1]);
-            mma16816<T>(acc[m][2 * c + 1], af[0], af[1], af[2], af[3], bf[c][2], bf[c][3]);
-          }
+          for (int t = 1; t < O::kStacked; ++t) f += __uint_as_float(d[t][i]);
+          sum[c + i] += f;
         }
+      }
     }
-    if ((q - q0) % kFlush == kFlush - 1) flush();
   }
-  flush();
+  tc_fence_before();
   cp_async_wait<0>();
   __syncthreads();
   // parts [rank][column], added in the order of the cluster's ranks
   float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int m = 0; m < RT / 16; ++m)
-#pragma unroll
-    for (int c = 0; c < kWarpCols / 8; ++c) {
-      float* at = red + (m * 16 + lane / 4) * kCols + warp * kWarpCols + c * 8 + lane % 4 * 2;
-      *reinterpret_cast<float2*>(at) = make_float2(sum[m][c][0], sum[m][c][1]);
-      *reinterpret_cast<float2*>(at + 8 * kCols) = make_float2(sum[m][c][2], sum[m][c][3]);
-    }
+  for (int i = 0; i < kSums; ++i)
+    red[(first + i) * kCols + block * 128 + warp % 4 * 32 + lane] = ok ? sum[i] : NAN;
   cluster_sync_all();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, O::kTmem);
+  }
   for (int e = rank * kOuterThreads + tid; e < r * kCols; e += S * kOuterThreads) {
     const int i = e / kCols, n = n0 + e % kCols;
     if (n >= s.n) continue;
@@ -1127,12 +1163,6 @@ __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer
 }
 
 // ------------------------------------------------------------------ launch --
-template <typename T, int RT>
-constexpr int outer_smem() {
-  const int rings = kOuterStages * kOuterRows * (kOuterCols<RT> * 2 + RT * 4) +
-                    2 * kTerms<T> * kOuterRows * (RT * 2 + 16) + 2 * kOuterAhead * kOuterRows * 4;
-  return std::max(rings, RT * kOuterCols<RT> * 4);
-}
 template <int RT>
 constexpr int shrink_smem() {
   // (on the tensor cores from a 1024-byte boundary on)
@@ -1236,10 +1266,10 @@ void launch_outer(const Launch& L, OuterArgs a, int rt_slot) {
     }
   }
   set_smem_attr_once(reinterpret_cast<const void*>(adapters_outer_kernel<T, RT>),
-                     outer_smem<T, RT>(), kAttrAdapters + 16 + 4 * type + rt_slot);
+                     OuterShape<T, RT>::kBytes, kAttrAdapters + 16 + 4 * type + rt_slot);
   launch_begin(L, MOE_K_ADAPTERS_GRAD);
   launch_kernel_cluster(adapters_outer_kernel<T, RT>, dim3(S, tiles, a.seg.J), dim3(S),
-                        dim3(kOuterThreads), outer_smem<T, RT>(), L.stream, a);
+                        dim3(kOuterThreads), OuterShape<T, RT>::kBytes, L.stream, a);
   launch_end(L, MOE_K_ADAPTERS_GRAD);
 }
 

@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&maps.b);
     if (MODE == kTcGateUp || MODE == kTcFfn) prefetch_tensormap(&maps.a1);
   }
-  // TMEM touches no global memory either (the kernels of adapters.cu, which hold
-  // TMEM too, let this one start only after all their CTAs have theirs)
+  // TMEM touches no global memory either (no kernel of this library that can
+  // share an SM with this one holds TMEM)
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), G::kTmemCols);
   pdl_wait();
   // the work list's first entries load in the same round as its counts (any
