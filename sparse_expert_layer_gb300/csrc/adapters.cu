@@ -20,8 +20,8 @@
 //
 // Measured on a GB300, cold, us (at 6.78 TB/s): one row, rank 16, 5120 to 5120 channels 7.6 (a
 // launch and three dependent reads); 64 rows of 48 adapters, 7168 to 2048 9.1 (1.6); 8192 rows,
-// 5120 to 5120, rank 16 65 (37), 64 76 (38), 128 130 (39); gradients of 8192 rows, rank 16, 7168
-// and 5120 channels 107 (48), of which the sums over positions are 54.
+// 5120 to 5120, rank 16 65 (37), 64 75 (38), 128 131 (39); gradients of 8192 rows, rank 16, 7168
+// and 5120 channels 104 (48), rank 64, 5120 and 5120 177 (41).
 #include <math.h>
 
 #include <algorithm>
@@ -941,6 +941,8 @@ struct OuterShape {
   static constexpr int kStacked = RT <= 64 ? kTerm : 1, kParts = kTerm / kStacked;
   static constexpr int kN = RT * kStacked;
   static constexpr int kUsed = kOuterCols<RT> / 128 * kN;  // columns of tensor memory
+  // (The CTAs of kernels with clusters that fit an SM's shared memory together never want more than
+  // its 512 columns, whatever their ranks: no CTA waits for columns while its cluster holds others.)
   static constexpr int kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
   // stages until an accumulator has sixteen MMAs (18 where terms are added up)
   static constexpr int kFlush = kParts == 1 ? 8 : 9 / kParts;
@@ -953,7 +955,10 @@ struct OuterShape {
 // 128 columns, K the positions, N the ranks of all terms side by side (of 128 ranks: of one term
 // after the other).  Rows of x and terms of v lie as the MMAs read them, both transposed.  After
 // every kFlush stages the accumulators are added, rounded, to sums in registers: MMAs cut theirs
-// off where fp32 ends.
+// off where fp32 ends.  Waits for stages at 44% issue: 201 MB of x and dy at rank 16 in 51 us, 4.1
+// TB/s.  With mma.sync and ldmatrix the gradients of 8192 rows took 107 us instead of 104 (rank 16,
+// 7168 and 5120 channels), 218 instead of 177 (64, 5120 and 5120) and 260 instead of 203 (128, 2048
+// and 2048); columns in twos of 128 up to 32 ranks, as tensor memory holds two CTAs' sums.
 template <typename T, int RT>
 __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer_kernel(OuterArgs a) {
   extern __shared__ unsigned char raw[];
