@@ -18,8 +18,8 @@
 // two 16-bit terms (three bf16 ones for dA and dB, whose results may be fp32): 2^-17
 // (bf16) or 2^-22 (fp16) of them is lost, which a rounded output does not show.
 //
-// Measured on a GB300, cold, us (at 6.78 TB/s): one row, rank 16, 5120 to 5120 channels 7.6 (a
-// launch and three dependent reads); 64 rows of 48 adapters, 7168 to 2048 9.1 (1.6); 8192 rows,
+// Measured on a GB300, cold, us (at 6.78 TB/s): one row, rank 16, 5120 to 5120 channels 7.1 (a
+// launch and three dependent reads); 64 rows of 48 adapters, 7168 to 2048 8.8 (1.6); 8192 rows,
 // 5120 to 5120, rank 16 65 (37), 64 75 (38), 128 131 (39); gradients of 8192 rows, rank 16, 7168
 // and 5120 channels 104 (48), rank 64, 5120 and 5120 177 (41).
 #include <math.h>
@@ -207,12 +207,14 @@ struct AdapterArgs {
 };
 
 // ---------------------------------------------------------------- few rows ----
-constexpr int kRowThreads = 128;
-constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kRowSide = 128;  // threads side by side along the second product's columns
 
-// One position: a cluster's CTAs take slices of K, then slices of N.
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(AdapterArgs a) {
+// One position: a cluster's CTAs take slices of K, then slices of N.  A warp takes four ranks of
+// the first product at once, 128 threads eight of the second: more WARPS, fewer dependent reads.
+template <typename T, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) adapters_row_kernel(AdapterArgs a) {
+  constexpr int kThreads = 32 * WARPS, kGroups = kThreads / kRowSide;
+  __shared__ float red[kGroups > 1 ? (kGroups - 1) * 8 * kRowSide : 1];
   pdl_enter();
   __shared__ float part[kMaxRank], total[kMaxRank];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -226,13 +228,13 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(AdapterArgs a
   const T* brow = a.base ? static_cast<const T*>(a.base) + row * a.ldb : nullptr;
   if (!has) {  // the whole cluster; the row is its base
     if (row >= 0 && a.y != a.base)
-      for (int i = n0 + tid; i < n1; i += kRowThreads) {
+      for (int i = n0 + tid; i < n1; i += kThreads) {
         float f[8] = {};
         if (brow) unpack_piece<T>(load_piece<T>(brow, i, a.N, a.yvec), f);
         store_piece<T>(yrow, i, a.N, a.yvec, f);
       }
     if (rank == 0 && row < 0 && j < a.seg.J && a.seg.at(j) <= p)
-      for (int i = tid; i < r; i += kRowThreads) a.v[(int64_t)p * r + i] = 0.f;
+      for (int i = tid; i < r; i += kThreads) a.v[(int64_t)p * r + i] = 0.f;
     if (a.max_v && tid == 0) {
       a.max_v[p * C + rank] = 0u;
       a.max_other[p * C + rank] = 0u;
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(AdapterArgs a
   const T* m2 = static_cast<const T*>(a.m2) + (int64_t)j * r * a.N;
   // the second matrix's slice on its way to L2 while the first is read
   if (a.y && a.m2vec)
-    for (int i = tid; i < r * (n1 - n0); i += kRowThreads)
+    for (int i = tid; i < r * (n1 - n0); i += kThreads)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(m2 + (int64_t)(i / (n1 - n0)) * a.N +
                                                     8 * (n0 + i % (n1 - n0))));
   const T* xrow = static_cast<const T*>(a.x) + row * a.ldx;
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(AdapterArgs a
   const int k8 = (a.K + 7) / 8, kp = (k8 + C - 1) / C;
   const int k0 = min(k8, rank * kp), k1 = min(k8, k0 + kp);
   constexpr int kRanks = 4, kAtOnce = 4;  // ranks of a warp, pieces of a lane in flight
-  for (int i0 = warp * kRanks; i0 < r; i0 += kRowWarps * kRanks) {
+  for (int i0 = warp * kRanks; i0 < r; i0 += WARPS * kRanks) {
     float acc[kRanks] = {};
     for (int kb = k0; kb < k1; kb += 32 * kAtOnce) {
       uint4 xq[kAtOnce], mq[kAtOnce][kRanks];
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(AdapterArgs a
   cluster_sync_all();
   const float s1 = a.scale1 ? a.scale1[j] : 1.f, s2 = a.scale2 ? a.scale2[j] : 1.f;
   uint32_t most = 0u, most_other = 0u;
-  for (int i = tid; i < r; i += kRowThreads) {
+  for (int i = tid; i < r; i += kThreads) {
     float s = 0.f;
     for (int q = 0; q < C; ++q) s += ld_cluster_f32(mapa_shared(smem_u32(&part[i]), q));
     s *= s1;
@@ -308,12 +310,16 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(AdapterArgs a
   __syncthreads();
   // (no CTA leaves while another reads its part: waited for at the end)
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  // a lane has eight columns and adds up all ranks
-  for (int i = n0 + tid; i < n1 && a.y; i += kRowThreads) {
+  // a thread has eight columns and adds up the ranks of its group
+  const int group = tid / kRowSide, side = tid % kRowSide;
+  for (int i0 = n0; i0 < n1 && a.y; i0 += kRowSide) {
+    const int i = i0 + side;
+    const bool in = i < n1;
     float f[8] = {}, acc[8] = {};
-    const uint4 bq = brow ? load_piece<T>(brow, i, a.N, a.yvec) : make_uint4(0u, 0u, 0u, 0u);
+    const uint4 bq = brow && in && group == 0 ? load_piece<T>(brow, i, a.N, a.yvec)
+                                              : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
-    for (int q0 = 0; q0 < r; q0 += 8) {
+    for (int q0 = 8 * group; q0 < r && in; q0 += 8 * kGroups) {
       uint4 mq[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q)
@@ -328,10 +334,26 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(AdapterArgs a
         for (int c = 0; c < 8; ++c) acc[c] = fmaf(v, m[c], acc[c]);
       }
     }
-    unpack_piece<T>(bq, f);
+    if constexpr (kGroups > 1) {  // the groups' parts, added in order
+      if (group > 0) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) f[c] = fmaf(s2, acc[c], f[c]);
-    store_piece<T>(yrow, i, a.N, a.yvec, f);
+        for (int c = 0; c < 8; ++c) red[((group - 1) * 8 + c) * kRowSide + side] = acc[c];
+      }
+      __syncthreads();
+      if (group == 0) {
+#pragma unroll
+        for (int q = 0; q < kGroups - 1; ++q)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) acc[c] += red[(q * 8 + c) * kRowSide + side];
+      }
+    }
+    if (group == 0 && in) {
+      unpack_piece<T>(bq, f);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) f[c] = fmaf(s2, acc[c], f[c]);
+      store_piece<T>(yrow, i, a.N, a.yvec, f);
+    }
+    if constexpr (kGroups > 1) __syncthreads();
   }
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -1183,18 +1205,29 @@ int adapters_split(int64_t clusters, int64_t units, int64_t most, int64_t least)
 }
 
 // One position a cluster, or tiles of positions.  By rows every row reads its adapter again
-// (from L2): cheap while that is little, or where adapters have about a row each.  Rank 16,
-// 5120 to 5120 channels: 64 rows 9 us; 128 rows (21 M products) 15.6 us against 15.3 in tiles;
-// 256 rows 28.8 against 16.1.  100 rows, 1000 to 1000 channels (3.2 M): 7.1 against 12.0.
-constexpr int64_t kRowWork = 18 << 20;
+// (from L2): cheap while that is little, or where adapters have about a row each.  us by rows and
+// in tiles: rank 16, 5120 to 5120 channels, 64 rows 9.1 and 15.6, 128 (21 M products) 15.6 and 16.1,
+// 160 21.5 and 16.2; 1000 to 1000, 300 rows 8.5 and 10.0, 1000 rows 25 and 10.7; rank 32, 2048 to
+// 2048, 64 rows (8.4 M) 10.6 and 10.2, 128 19 and 11; rank 64, 40 rows 16.5 and 12.5; 64 rows of 64
+// adapters, rank 64, 2048 to 2048 19 and 29, of 48, rank 16, 7168 to 2048 9.3 and 20.
 bool adapters_by_rows(const AdapterArgs& a) {
   const int64_t T = a.seg.T;
-  return T <= 2 * a.seg.J || (T <= 4096 && T * a.r * (a.K + a.N) <= kRowWork);
+  return T <= 2 * a.seg.J ||
+         (T <= 304 && T * a.r * (a.K + a.N) <= (a.r <= 16 ? 20 << 20 : 8 << 20));
 }
 
 int row_cluster(const AdapterArgs& a) {
   // slices of at least 256 channels
   return adapters_split(1, std::max(a.K, a.N), kMaxCluster, 256);
+}
+// Warps of a CTA: for all ranks at once, where clusters of that many surely find room together (an
+// SM holds sixteen warps; GPCs are not filled evenly).  One row, 5120 to 5120 channels, rank 64: 16.1
+// us with four, 9.0 with sixteen; 128: 27.8 and 13.5; but 64 rows of 64 adapters, 2048 to 2048, rank
+// 64: 19 and 36.
+int row_warps(const AdapterArgs& a, int cluster, int num_sms) {
+  int warps = a.r <= 16 ? 4 : a.r <= 32 ? 8 : 16;
+  while (warps > 4 && (int64_t)a.seg.T * cluster * warps * 2 > 16LL * num_sms) warps /= 2;
+  return warps;
 }
 // Tiles of `rows` positions that may have any: see Segments::tile.
 int adapter_tiles(const AdapterArgs& a, int rows) {
@@ -1286,8 +1319,14 @@ void launch_adapters(const Launch& L, const AdapterArgs& a, OuterArgs* outer) {
   } else if (adapters_by_rows(a)) {
     const int C = row_cluster(a);
     launch_begin(L, MOE_K_ADAPTERS);
-    launch_kernel_cluster(adapters_row_kernel<T>, dim3(C, a.seg.T), dim3(C), dim3(kRowThreads), 0,
-                          L.stream, a);
+    auto rows = [&](auto kernel, int warps) {
+      launch_kernel_cluster(kernel, dim3(C, a.seg.T), dim3(C), dim3(32 * warps), 0, L.stream, a);
+    };
+    switch (row_warps(a, C, L.num_sms)) {
+      case 4: rows(adapters_row_kernel<T, 4>, 4); break;
+      case 8: rows(adapters_row_kernel<T, 8>, 8); break;
+      default: rows(adapters_row_kernel<T, 16>, 16); break;
+    }
     launch_end(L, MOE_K_ADAPTERS);
     if (outer) {
       outer->tile = 1;

@@ -461,11 +461,11 @@ def test_a_training_step_in_a_graph(m):
     assert all(torch.equal(p, q) for p, q in zip(grads + [norm], first))
 
 
-# By rows the adapters are read from L2 again for every position; from 18 << 20 products
-# T * r * (K + N) on (and more than two rows an adapter) positions go in tiles.
+# By rows the adapters are read from L2 again for every position; above 304 rows or 20 << 20 products
+# T * r * (K + N) (8 << 20 above rank 16), and with more than two rows an adapter, positions go in tiles.
 def tiled(r=16, K=1000, N=1016, J=5, T=None, **kw):
     T = T or (18 << 20) // (r * (K + N)) + 70
-    assert T > 2 * J and T * r * (K + N) > 18 << 20
+    assert T > 2 * J and (T > 304 or T * r * (K + N) > (20 << 20 if r <= 16 else 8 << 20))
     return make(T, J, r, K, N, kw.pop("dtype", BF16), **kw)
 
 
