@@ -579,11 +579,13 @@ def adapters_workspace(T, r, K, N, device="cuda"):
 
 def _adapter_parts(a, b, scale, offsets, order, T, same, dev):
     """(adapters, rank, K, N) and the addresses of a, b, scale, offsets and order."""
-    for t, name in ((a, "a"), (b, "b")):
-        if not isinstance(t, torch.Tensor) or t.dim() != 3:
-            raise TypeError(f"{name}: expected [adapters, rank, channels]")
-    J, r, K = a.shape
-    N = b.shape[2]
+    try:
+        (J, r, K), (_, _, N) = a.shape, b.shape
+    except (AttributeError, ValueError):
+        for t, name in ((a, "a"), (b, "b")):
+            if not isinstance(t, torch.Tensor) or t.dim() != 3:
+                raise TypeError(f"{name}: expected [adapters, rank, channels]") from None
+        raise
     return (J, r, K, N), (
         _tensor(a, "a", same, (J, r, K), dev), _tensor(b, "b", same, (J, r, N), dev),
         None if scale is None else _tensor(scale, "scale", _F32, (J,), dev),
@@ -593,8 +595,11 @@ def _adapter_parts(a, b, scale, offsets, order, T, same, dev):
 
 def _bytes(ws, dev):
     """(address, size) of a workspace."""
-    _a_tensor(ws, "ws")
-    n = ws.numel()
+    try:
+        n = ws.numel()
+    except AttributeError:
+        _a_tensor(ws, "ws")
+        raise
     return _tensor(ws, "ws", _U8, (n,), dev), n
 
 
