@@ -21,7 +21,7 @@
 // Measured on a GB300, cold, us (at 6.78 TB/s): one row, rank 16, 5120 to 5120 channels 7.1 (a
 // launch and three dependent reads); 64 rows of 48 adapters, 7168 to 2048 8.8 (1.6); 8192 rows,
 // 5120 to 5120, rank 16 65 (37), 64 75 (38), 128 131 (39); gradients of 8192 rows, rank 16, 7168
-// and 5120 channels 104 (48), rank 64, 5120 and 5120 177 (41).
+// and 5120 channels 104 (48), rank 64, 5120 and 5120 164 (41).
 #include <math.h>
 
 #include <algorithm>
@@ -979,7 +979,7 @@ struct OuterShape {
 // every kFlush stages the accumulators are added, rounded, to sums in registers: MMAs cut theirs
 // off where fp32 ends.  Waits for stages at 44% issue: 201 MB of x and dy at rank 16 in 51 us, 4.1
 // TB/s.  With mma.sync and ldmatrix the gradients of 8192 rows took 107 us instead of 104 (rank 16,
-// 7168 and 5120 channels), 218 instead of 177 (64, 5120 and 5120) and 260 instead of 203 (128, 2048
+// 7168 and 5120 channels), 218 instead of 164 (64, 5120 and 5120) and 260 instead of 177 (128, 2048
 // and 2048); columns in twos of 128 up to 32 ranks, as tensor memory holds two CTAs' sums.
 template <typename T, int RT>
 __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer_kernel(OuterArgs a) {
@@ -1291,13 +1291,14 @@ void launch_outer(const Launch& L, OuterArgs a, int rt_slot) {
     tiles += s.tiles;
   }
   // the split of an adapter's positions with the least time by a count of stages: rounds of
-  // CTAs, each of its stages and about four more to start and to add the parts
+  // CTAs, each of its stages and about eight more to start and to add the parts (with four 8192 rows,
+  // 5120 to 5120, rank 64 177 us instead of 164)
   const int64_t clusters = (int64_t)tiles * a.seg.J, slots = (int64_t)kOuterPerSm<RT> * L.num_sms;
   const int64_t stages = std::max(1, a.seg.T / a.seg.J / kOuterRows);
   int S = 1;
   int64_t least = INT64_MAX;
   for (int q = 1; q <= kMaxCluster; ++q) {
-    const int64_t cost = (clusters * q + slots - 1) / slots * ((stages + q - 1) / q + 4);
+    const int64_t cost = (clusters * q + slots - 1) / slots * ((stages + q - 1) / q + 8);
     if (cost < least) {
       least = cost;
       S = q;
