@@ -1295,6 +1295,9 @@ void launch_four(const Launch& L, const FewArgs& a, bool zeros, int slot) {
     launch_four_as<BLOCK, false>(L, a, slot + 3);
 }
 
+// (without routed experts cfg.inter means nothing: it may be any number)
+int few_inter(const moe_config& c) { return c.n_routed > 0 ? c.inter : 0; }
+
 struct FewLayout {
   size_t head, logits, scratch, h, total;
 };
@@ -1307,7 +1310,7 @@ FewLayout few_layout(const moe_config& c, int T) {
   l.logits = l.head + up(sizeof(FewHead));
   l.scratch = l.logits + up((size_t)T * E * 4);
   l.h = l.scratch + up(T * E * 16 <= kRouteScratch ? 0 : (size_t)T * E * 12);
-  l.total = l.h + up((size_t)units * T * std::max(c.inter, c.shared_inter) * 4);
+  l.total = l.h + up((size_t)units * T * std::max(few_inter(c), c.shared_inter) * 4);
   return l;
 }
 
@@ -1317,7 +1320,7 @@ moe_status check_few(const moe_config* c, int T) {
   const moe_status s = moe_workspace_size(c, T < 0 ? T : std::min(T, 1), &bytes);
   if (s != MOE_OK) return s;
   if (c->wdtype != MOE_W_BF16) return MOE_ERR_UNSUPPORTED;
-  if (T > kFewMaxT || (int64_t)T * c->hidden > kFewMaxTH || c->inter > kFewMaxInter ||
+  if (T > kFewMaxT || (int64_t)T * c->hidden > kFewMaxTH || few_inter(*c) > kFewMaxInter ||
       c->shared_inter > kFewMaxInter)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
@@ -1357,7 +1360,7 @@ extern "C" moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weight
     if (wt->scale_dtype < MOE_DT_BF16 || wt->scale_dtype > MOE_DT_FP32) return MOE_ERR_INVALID_ARG;
     const int es = wt->scale_dtype == MOE_DT_FP32 ? 4 : 2;
     for (int i = 0; i < 3; ++i) {
-      const int k = i == 0 ? c.hidden : i == 1 ? (c.n_routed ? c.inter : 0) : c.shared_inter;
+      const int k = i == 0 ? c.hidden : i == 1 ? few_inter(c) : c.shared_inter;
       if (k % 32 || (group > 0 && k % group)) return MOE_ERR_INVALID_ARG;
       const int groups = group > 0 ? k / group : 1;
       aligned_s = aligned_s && (k == 0 || groups * es % 4 == 0);
@@ -1394,7 +1397,7 @@ extern "C" moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weight
   FewArgs a{};
   const int units = std::min(c.n_routed, T * c.top_k) + (c.shared_inter > 0);
   const int es = wt->scale_dtype == MOE_DT_FP32 ? 4 : 2;
-  a.p = few_plan(T, c.hidden, std::max(c.n_routed > 0 ? c.inter : 0, c.shared_inter), units,
+  a.p = few_plan(T, c.hidden, std::max(few_inter(c), c.shared_inter), units,
                  T * (std::min(c.n_routed, c.top_k) + (c.shared_inter > 0)), four, wt->group, es,
                  zeros, aligned_s, aligned_z, whole);
   if (a.p.stages < 2) return MOE_ERR_UNSUPPORTED;
@@ -1437,9 +1440,9 @@ extern "C" moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weight
   a.h = reinterpret_cast<float*>(base + l.h);
   a.T = T;
   a.H = c.hidden;
-  a.I = c.n_routed > 0 ? c.inter : 0;
+  a.I = few_inter(c);
   a.Is = c.shared_inter;
-  a.inter = std::max(c.inter, c.shared_inter);
+  a.inter = std::max(a.I, a.Is);  // a row of h: whole float4s
   a.fp16 = r.fp16;
   a.vec = r.vec;
   a.group = four ? wt->group : 0;

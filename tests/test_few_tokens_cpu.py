@@ -106,6 +106,18 @@ def test_workspace_size(moe):
     assert moe.lib.moe_few_tokens_workspace_size(ctypes.byref(config(moe)), 1, None) == INVALID
 
 
+@pytest.mark.parametrize("T", [1, 2, 8])
+def test_an_inter_that_no_expert_has_changes_nothing(moe, T):
+    # rows of h are the shared expert's then: whole 16-byte pieces, whatever inter is
+    sizes = {moe.moe_few_tokens_workspace_size(
+        config(moe, n_routed=0, n_zero=4, inter=inter, shared_inter=8), T)
+        for inter in (0, 8, 50, 4097, (1 << 20) + 3)}
+    assert len(sizes) == 1
+    # inter of routed experts is that of h, and checked
+    with pytest.raises(moe.MoeError):
+        moe.moe_few_tokens_workspace_size(config(moe, inter=50), T)
+
+
 def handle(moe, four=False, drop=(), cfg=None, **kw):
     """A FewTokenExperts of CPU tensors (never launched)."""
     c = config(moe, **(cfg or {}))

@@ -52,6 +52,7 @@ LAYERS = {
                    bias_mode="select", bias_kind="iid", renormalize=True),
     "only_zero": dict(hidden=256, inter=32, n_routed=0, n_zero=8, top_k=2, renormalize=True),
     "only_shared": dict(hidden=256, inter=32, n_routed=0, n_zero=4, top_k=1, shared_inter=160),
+    "unused_inter": dict(hidden=256, inter=50, n_routed=0, n_zero=4, top_k=1, shared_inter=32),
     "all": dict(hidden=160, inter=64, n_routed=32, top_k=32, renormalize=True),
     "one": dict(hidden=32, inter=32, n_routed=1, top_k=1),
     "flat256": dict(hidden=64, inter=32, n_routed=250, top_k=9, renormalize=True),
@@ -214,7 +215,7 @@ def test_sixteen_bit_weights(m, name, T, dtype):
     check(m, make(name, T, dtype, 16))
 
 
-FOUR = ["flat", "flat512", "flat768", "groups", "per_group", "zero", "select", "only_zero", "only_shared", "all", "one",
+FOUR = ["flat", "flat512", "flat768", "groups", "per_group", "zero", "select", "only_zero", "only_shared", "unused_inter", "all", "one",
         "wide", "deep"]
 
 
