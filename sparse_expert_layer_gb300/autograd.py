@@ -109,8 +109,6 @@ def unsort_tokens(y_sorted, topk_w, plan, dtype=None):
 class _Adapters(torch.autograd.Function):
     @staticmethod
     def forward(ctx, base, x, a, b, scale, offsets, order):
-        if ctx.needs_input_grad[4]:
-            raise RuntimeError("scale: adapters gives it no gradient; detach it")
         x, a, b = _ready(x), _dense(a), _dense(b)
         T, (_, r, K), N = x.shape[0], a.shape, b.shape[2]
         y = torch.empty(T, N, dtype=x.dtype, device=x.device)
@@ -162,5 +160,7 @@ def plan_adapters(adapter_ids, n_adapters):
 def adapters(base, x, a, b, scale, plan):
     """base [T, N] (None: zeros) + each row's adapter applied to x [T, K]: a [J, r, K],
     b [J, r, N] (bf16 or fp16, all alike), scale fp32 [J] or None (a constant: one that
-    requires a gradient is refused)."""
+    requires a gradient is refused while gradients are recorded)."""
+    if scale is not None and scale.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError("scale: adapters gives it no gradient; detach it")
     return _Adapters.apply(base, x, a, b, scale, plan.offsets, plan.sorted_to_expanded)

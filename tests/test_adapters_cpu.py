@@ -89,3 +89,15 @@ def test_a_scale_that_wants_a_gradient_is_refused(moe):
     plan = autograd.SortPlan(*(torch.zeros(4, dtype=torch.int32) for _ in range(4)))
     with pytest.raises(RuntimeError, match="scale"):
         autograd.adapters(None, x, a, b, torch.ones(2, requires_grad=True), plan)
+
+
+def test_a_scale_that_wants_a_gradient_is_a_constant_under_no_grad(moe):
+    import torch
+
+    from sparse_expert_layer_gb300 import autograd
+
+    x, a, b = (torch.zeros(*s, dtype=torch.bfloat16) for s in ((4, 64), (2, 16, 64), (2, 16, 128)))
+    plan = autograd.SortPlan(*(torch.zeros(n, dtype=torch.int32) for n in (2, 3, 4, 4)))
+    # (as far as the launch, for which these tensors are on the wrong device)
+    with torch.no_grad(), pytest.raises(ValueError, match="not on the current CUDA device"):
+        autograd.adapters(None, x, a, b, torch.ones(2, requires_grad=True), plan)

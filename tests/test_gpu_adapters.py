@@ -424,6 +424,21 @@ def test_autograd_of_parts_and_layouts(m):
         g.sum().backward()
 
 
+@pytest.mark.parametrize("T", [24, 200])
+def test_evaluation_with_a_scale_that_is_a_parameter(m, T):
+    from sparse_expert_layer_gb300 import autograd
+
+    c = make(T, 3, 8, 96, 64, BF16)
+    plan = autograd.plan_adapters(c["ids"].int(), 3)
+    args = c["base"], c["x"], c["a"], c["b"]
+    want = autograd.adapters(*args, c["scale"], plan)
+    scale = torch.nn.Parameter(c["scale"].clone())
+    with torch.no_grad():
+        assert torch.equal(autograd.adapters(*args, scale, plan), want)
+    with pytest.raises(RuntimeError, match="scale"):
+        autograd.adapters(*args, scale, plan)
+
+
 def test_a_training_step_in_a_graph(m):
     """Forward, backward and clipping captured while eager gradients of the same leaves live."""
     from sparse_expert_layer_gb300 import autograd
