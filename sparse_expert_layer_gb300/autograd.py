@@ -110,6 +110,7 @@ class _Adapters(torch.autograd.Function):
     @staticmethod
     def forward(ctx, base, x, a, b, scale, offsets, order):
         x, a, b = _ready(x), _dense(a), _dense(b)
+        scale = None if scale is None else _dense(scale)
         T, (_, r, K), N = x.shape[0], a.shape, b.shape[2]
         y = torch.empty(T, N, dtype=x.dtype, device=x.device)
         v = torch.empty(T, r, device=x.device)

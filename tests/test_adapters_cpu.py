@@ -101,3 +101,19 @@ def test_a_scale_that_wants_a_gradient_is_a_constant_under_no_grad(moe):
     # (as far as the launch, for which these tensors are on the wrong device)
     with torch.no_grad(), pytest.raises(ValueError, match="not on the current CUDA device"):
         autograd.adapters(None, x, a, b, torch.ones(2, requires_grad=True), plan)
+
+
+@pytest.mark.parametrize("layout", ["slice", "column"])
+def test_a_scale_of_another_layout_is_copied(moe, monkeypatch, layout):
+    import torch
+
+    from sparse_expert_layer_gb300 import autograd
+
+    seen = []
+    monkeypatch.setattr(autograd.ops, "moe_adapters", lambda x, a, b, scale, *rest: seen.append(scale))
+    x, a, b = (torch.zeros(*s, dtype=torch.bfloat16) for s in ((4, 64), (2, 16, 64), (2, 16, 128)))
+    plan = autograd.SortPlan(*(torch.zeros(n, dtype=torch.int32) for n in (2, 3, 4, 4)))
+    scale = {"slice": torch.arange(5.0)[1:3], "column": torch.arange(8.0).view(2, 4)[:, 1]}[layout]
+    autograd.adapters(None, x, a, b, scale, plan)
+    (got,) = seen
+    assert torch.equal(got, scale) and got.is_contiguous() and got.data_ptr() % 16 == 0

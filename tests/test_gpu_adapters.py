@@ -439,6 +439,22 @@ def test_evaluation_with_a_scale_that_is_a_parameter(m, T):
         autograd.adapters(*args, scale, plan)
 
 
+@pytest.mark.parametrize("T", [24, 200])
+def test_a_slice_of_a_scale(m, T):
+    from sparse_expert_layer_gb300 import autograd
+
+    c = make(T, 3, 8, 96, 64, BF16)
+    plan = autograd.plan_adapters(c["ids"].int(), 3)
+    scales = torch.cat([torch.full((1,), 9.0, device="cuda"), c["scale"]])
+    got = []
+    for scale in (c["scale"], scales[1:]):
+        leaves = [c[k].clone().requires_grad_() for k in ("x", "a", "b")]
+        y = autograd.adapters(c["base"], *leaves, scale, plan)
+        y.backward(c["dy"])
+        got.append([y.detach()] + [t.grad for t in leaves])
+    assert all(torch.equal(p, q) for p, q in zip(*got))
+
+
 def test_a_training_step_in_a_graph(m):
     """Forward, backward and clipping captured while eager gradients of the same leaves live."""
     from sparse_expert_layer_gb300 import autograd
