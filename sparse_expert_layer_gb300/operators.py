@@ -457,7 +457,8 @@ class FewTokenExperts:
         if not isinstance(cfg, MoeConfig):
             raise TypeError(f"cfg: expected a MoeConfig, got {type(cfg).__name__}")
         _a_tensor(w_router, "w_router")
-        self.cfg, self.device = cfg, w_router.get_device()
+        # a copy: what is checked here has to be what later calls see
+        self.cfg, self.device = MoeConfig.from_buffer_copy(cfg), w_router.get_device()
         self.kept = dict(weights), w_router, bias  # what the addresses below belong to
         H, E = cfg.hidden, cfg.n_routed
         total = E + cfg.n_zero

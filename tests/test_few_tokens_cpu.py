@@ -163,3 +163,16 @@ def test_handles_are_checked(moe):
     x = torch.zeros(2, 256, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="not on the current CUDA device"):
         moe.moe_few_tokens(four, x, x.clone(), torch.zeros(1 << 20, dtype=torch.uint8))
+
+
+def test_a_description_that_changes_later_changes_no_handle(moe, monkeypatch):
+    # the sizes that the weights were checked against stay those of every call
+    made = []
+    monkeypatch.setitem(globals(), "config", lambda *a, _c=config, **kw: made.append(_c(*a, **kw))
+                        or made[-1])
+    experts = handle(moe)
+    size = moe.few_tokens_workspace(experts, 4).numel()
+    made[-1].hidden, made[-1].inter, made[-1].n_routed, made[-1].top_k = 512, 256, 16, 4
+    assert (experts.cfg.hidden, experts.cfg.inter, experts.cfg.n_routed, experts.cfg.top_k) == \
+        (256, 128, 8, 2)
+    assert moe.few_tokens_workspace(experts, 4).numel() == size
