@@ -449,7 +449,9 @@ moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weights* weights,
  * and order are moe_sort_tokens' offsets and sorted_to_expanded for ids [T, 1], one sort
  * for all projections of a step.  Sums are fp32; v enters the second product as two
  * 16-bit numbers (2^-17 of it is lost in bf16, 2^-22 in fp16; exactly where each row has
- * its own CTAs); y is rounded once.  The same bits on every call.
+ * its own CTAs); y is rounded once.  The same bits on every call.  An infinite v is infinite
+ * in y; where b holds infinities (in gradients also x, dy or a), sums that meet them are
+ * infinite or NaN.
  *  r, T      1 <= r <= 128; T <= 2^21, n_adapters <= 4096, K, N <= 2^21
  *  dtype     MOE_DT_BF16 or MOE_DT_FP16: x [T, K], a [n_adapters, r, K],
  *            b [n_adapters, r, N], base and y [T, N]; row strides ldx, ldb, ldy

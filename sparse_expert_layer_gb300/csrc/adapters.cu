@@ -107,12 +107,6 @@ struct Segments {
   }
 };
 
-// The fp32 bits of |v| as they count towards a largest magnitude: what is not finite does not.
-__device__ __forceinline__ uint32_t magnitude(float v) {
-  const uint32_t bits = __float_as_uint(fabsf(v));
-  return bits < 0x7f800000u ? bits : 0u;
-}
-
 __device__ __forceinline__ void sts128(uint32_t at, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z),
                "r"(v.w)
@@ -813,13 +807,13 @@ __global__ void __launch_bounds__(kExpandThreads, kExpandPerSm<RT>)
       }
       float up = scale;  // bf16: scale * v
       if constexpr (kHalf) {  // into fp16's range, row by row; scaled back afterwards
-        float most = 0.f;
+        uint32_t most = 0u;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) most = fmaxf(most, fabsf(f[c]));
+        for (int c = 0; c < 8; ++c) most = max(most, magnitude(f[c]));
 #pragma unroll
         for (int o = 1; o < kRowLanes; o <<= 1)
-          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-        const uint32_t bits = fp16_range_bits(__float_as_uint(most));
+          most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        const uint32_t bits = fp16_range_bits(most);
         up = __uint_as_float(bits);
         if (k8 == 0) row_scale[i] = scale * inverse_pow2(bits);
       }
@@ -1078,10 +1072,10 @@ __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer
                             (((n % 64 / 8) ^ (i % 8)) * 16) + n % 8 * 2;
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(w0), "r"(w1) : "memory");
         const float2 g0 = unpack2<T>(w0), g1 = unpack2<T>(w1);
-        f[0] -= g0.x;
-        f[1] -= g0.y;
-        f[2] -= g1.x;
-        f[3] -= g1.y;
+        f[0] = left_of(f[0], g0.x);
+        f[1] = left_of(f[1], g0.y);
+        f[2] = left_of(f[2], g1.x);
+        f[3] = left_of(f[3], g1.y);
       }
     }
   };

@@ -2,6 +2,8 @@
 // carry fp32 operands through them (few_tokens.cu, adapters.cu).
 #pragma once
 
+#include <math.h>
+
 #include "rows.cuh"
 
 namespace moe {
@@ -42,12 +44,23 @@ __device__ __forceinline__ float inverse_pow2(uint32_t bits) {
   return __uint_as_float((254u << 23) - bits);
 }
 
+// The fp32 bits of |v| as they count towards a largest magnitude: what is not finite does not.
+__device__ __forceinline__ uint32_t magnitude(float v) {
+  const uint32_t bits = __float_as_uint(fabsf(v));
+  return bits < 0x7f800000u ? bits : 0u;
+}
+
+// What a 16-bit term leaves of v: nothing of an infinity, which would be NaN, nor of a NaN.
+__device__ __forceinline__ float left_of(float v, float term) {
+  return fabsf(term) < INFINITY ? v - term : 0.f;
+}
+
 // (lo, hi) rounded to the 16-bit type, and what that rounding left, rounded again.
 template <typename T>
 __device__ __forceinline__ void split2(float lo, float hi, uint32_t& first, uint32_t& rest) {
   first = pack2<T>(lo, hi);
   const float2 f = unpack2<T>(first);
-  rest = pack2<T>(lo - f.x, hi - f.y);
+  rest = pack2<T>(left_of(lo, f.x), left_of(hi, f.y));
 }
 
 }  // namespace moe

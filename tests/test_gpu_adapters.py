@@ -609,6 +609,71 @@ def test_an_adapter_changes_no_other_ones_results(m, T, dtype, what):
         assert torch.equal(p[rest], q[rest])
 
 
+def same_infinities(got, want):
+    """Elements that are not finite are the same infinities or NaN; want is in 64 bits."""
+    got, want = got.double(), want.float().double()  # (what passes fp32's range is infinite)
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.isposinf(got), torch.isposinf(want))
+    assert torch.equal(torch.isneginf(got), torch.isneginf(want))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("T", [20, 1200])
+def test_infinite_rows_give_infinities(m, T, dtype):
+    """One rank, so that a sum has one infinity; by rows and in tiles alike."""
+    K, N = 256, 136
+    c = make(T, 3, 1, K, N, dtype, none=0.0)
+    ws = m.adapters_workspace(T, 1, K, N)
+    plan = c["scale"], c["offsets"], c["order"]
+    f = {k: c[k].double() for k in ("x", "dy", "a", "b", "scale")}
+    a, b, s = f["a"][c["ids"], 0], f["b"][c["ids"], 0], f["scale"][c["ids"], None]
+    x, dy = c["x"].clone(), c["dy"].clone()
+    x[5, 7], dy[9, 3] = float("inf"), float("-inf")
+    y = torch.empty_like(c["base"])
+    v = torch.zeros(T, 1, device="cuda")
+    m.moe_adapters(x, c["a"], c["b"], *plan, c["base"], y, v, ws)
+    want = c["base"].double() + s * (x.double() * a).sum(1, keepdim=True) * b
+    assert torch.isinf(want[5]).sum() > N // 2 and torch.isfinite(want).sum() >= (T - 1) * N
+    same_infinities(y, want)
+    # gradients: u of one position is infinite
+    m.moe_adapters(c["x"], c["a"], c["b"], *plan, c["base"], y, v, ws)
+    dx, da, db = torch.empty_like(x), torch.empty(3, 1, K, device="cuda"), \
+        torch.empty(3, 1, N, device="cuda")
+    m.moe_adapters_backward(dy, c["x"], v, c["a"], c["b"], *plan, dx, da, db, ws)
+    u = s * (dy.double() * b).sum(1, keepdim=True)
+    assert torch.isinf(u).sum() == 1
+    same_infinities(dx, u * a)
+    for j in range(3):
+        at = c["ids"] == j
+        same_infinities(da[j, 0], (u[at] * f["x"][at]).sum(0))
+    # (dy's own infinity meets v's terms: infinite or NaN, in its column only)
+    j = int(c["ids"][9])
+    assert not torch.isfinite(db[j, 0, 3])
+    db[j, 0, 3] = 0
+    assert torch.isfinite(db).all()
+
+
+@pytest.mark.parametrize("r", [16, 100])
+@pytest.mark.parametrize("T", [20, 1200])
+def test_one_infinite_rank_among_finite_ones(m, T, r):
+    K, N = 256, 136
+    c = make(T, 3, r, K, N, BF16, none=0.0)
+    j = int(c["ids"][5])
+    c["x"][5, 7], c["a"][j, 0, 7] = 2.0**100, 2.0**40
+    c["x"][6:, 7] = 0
+    c["x"][:5, 7] = 0
+    ws = m.adapters_workspace(T, r, K, N)
+    y = torch.empty_like(c["base"])
+    v = torch.zeros(T, r, device="cuda")
+    m.moe_adapters(c["x"], c["a"], c["b"], c["scale"], c["offsets"], c["order"], c["base"], y, v, ws)
+    assert torch.isinf(v).sum() == 1 and not torch.isnan(v).any()
+    want = v[torch.argsort(c["order"])[5]].double() @ c["b"][j].double()
+    assert torch.isinf(want).all()
+    same_infinities(y[5], want)
+    rest = torch.arange(T, device="cuda") != 5
+    assert torch.isfinite(y[rest]).all()
+
+
 @pytest.mark.parametrize("r", [16, 64, 128])
 def test_beside_the_layer(m, r):
     """Calls in turn with the layer's on one stream, whose kernels start before the last ones have
