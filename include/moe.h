@@ -409,7 +409,8 @@ moe_status moe_w4_gemv(int32_t n_experts, int32_t N, int32_t K, int32_t group, i
  * the picked experts' weights.  Logits and statistics are fp32; 16-bit weights meet x
  * as it is and h as a sum of two 16-bit numbers, 4-bit weights meet x exactly (elements
  * below 2^-23 of a token's largest are rounded at 2^-33 of it) and h with 11 bits; all
- * sums and scales are fp32 and out is rounded once.  The same bits on every call.
+ * sums and scales are fp32 and out is rounded once.  The same bits on every call.  An
+ * infinite h is infinite in out, NaN with 4-bit weights.
  *  cfg       wdtype MOE_W_BF16 whatever the weights are; out_fp32, gemv_max_rows,
  *            combine and ffn_launch are not read
  *  T         <= 8, T * hidden <= 65536, inter and shared_inter <= 2^20

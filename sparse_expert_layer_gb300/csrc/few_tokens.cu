@@ -70,7 +70,7 @@ struct FewHead {
   float zero_w[kFewMaxT];  // weights of the tokens' zero-computation picks
   FewUnit unit[kFewMaxPicks + 1];
   float w[kFewMaxPicks + 1][kFewMaxT];        // a unit's routing weights, 0 for other tokens
-  uint32_t hmax[kFewMaxPicks + 1][kFewMaxT];  // largest |h| of a unit's token, fp32 bits
+  uint32_t hmax[kFewMaxPicks + 1][kFewMaxT];  // largest finite |h| of a unit's token, fp32 bits
 };
 
 struct FewMatrix {
@@ -833,7 +833,7 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, c
           __stcg(a.h + ((int64_t)u * a.T + t) * a.inter + f * 8 + ch, h);
         }
         if constexpr (K::kScaled) {
-          uint32_t most = __float_as_uint(fabsf(h));
+          uint32_t most = magnitude(h);
 #pragma unroll
           for (int o = 4; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
           if (ch == 0 && mine) atomicMax(&head->hmax[u][t], most);

@@ -446,3 +446,35 @@ def test_weights_that_are_not_finite_reach_their_tokens_only(m, dtype, bits, bad
     torch.cuda.synchronize()
     assert torch.equal(out[~picked], good[~picked])
     assert not torch.isfinite(out[picked]).any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("T", [1, 4])
+@pytest.mark.parametrize("name", ["flat", "deep"])
+def test_an_infinite_h_gives_infinities(m, name, T, dtype):
+    c = make(name, T, dtype, 16)
+    c["x"][0, 0] = 0.5  # its gate becomes +inf: silu is infinite, not NaN
+    spec = c["spec"]
+    experts = experts_of(m, c)
+    ws = m.few_tokens_workspace(experts, T)
+    out = torch.empty_like(c["x"])
+    ids = torch.empty(T, spec["top_k"], dtype=torch.int32, device="cuda")
+    w = torch.empty(T, spec["top_k"], device="cuda")
+    c["w"]["w_gate"][:, 3, 0] = float("inf")
+    m.moe_few_tokens(experts, c["x"], out, ws, ids, w)
+    torch.cuda.synchronize()
+    e = int(ids[0, 0])
+    # one expert alone: of two, infinities could cancel
+    c["w"]["w_gate"][:, 3, 0] = 0.0
+    c["w"]["w_gate"][e, 3, 0] = float("inf")
+    m.moe_few_tokens(experts, c["x"], out, ws)
+    torch.cuda.synchronize()
+    up = c["w"]["w_up"][e, 3].double() @ c["x"][0].double()
+    want = torch.sign(up) * c["w"]["w_down"][e, :, 3].double() * float("inf")
+    assert torch.isinf(want).sum() > spec["hidden"] * 0.9
+    got = out[0].double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got[torch.isinf(want)], want[torch.isinf(want)])
+    rest = [t for t in range(1, T) if e not in ids[t].tolist()]
+    assert torch.isfinite(out[rest]).all()
+    assert m.moe_check_device_status(ws) == m.MOE_OK
