@@ -228,8 +228,19 @@ __device__ __forceinline__ ClipSum clip_add(const ClipSum& a, const ClipSum& b) 
   const float s = a.hi + b.hi, t = s - a.hi;
   return {s, ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo)};
 }
-__device__ __forceinline__ float clip_value(const ClipSum& a) {
-  return fabsf(a.hi) < INFINITY ? a.hi + a.lo : a.hi;
+// The root of a sum, as a pair too: one Newton step from the rounded root.
+__device__ __forceinline__ ClipSum clip_root(const ClipSum& a) {
+  const float r = sqrtf(a.hi), e = (fmaf(-r, r, a.hi) + a.lo) / (2.f * r);
+  return {r, fabsf(e) <= r * 0x1p-20f ? e : 0.f};  // none of 0, inf and NaN
+}
+// min(1, max_norm / (norm + eps)), rounded once: every element's product has its error, which
+// a rounded sum, quotient and root would make three times that.  NaN stays one.
+__device__ __forceinline__ float clip_factor(const ClipSum& norm, float max_norm, float eps) {
+  const ClipSum d = clip_add(norm, {eps, 0.f});
+  const float q = max_norm / d.hi;
+  const float e = (fmaf(-q, d.hi, max_norm) - q * d.lo) / d.hi;
+  const float c = fabsf(e) <= q * 0x1p-20f ? q + e : q;
+  return c >= 1.f ? 1.f : c;
 }
 // The block's sum of v, in every thread; added in a fixed order.
 __device__ __forceinline__ ClipSum clip_block_sum(ClipSum v) {
@@ -268,10 +279,9 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtasPerSm)
   pdl_enter();
   ClipSum sum{0.f, 0.f};
   for (int i = threadIdx.x; i < nslots; i += kClipThreads) sum = clip_add(sum, slots[i]);
-  const float norm = sqrtf(clip_value(clip_block_sum(sum)));
-  if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
-  const float q = max_norm / (norm + eps);
-  const float c = q >= 1.f ? 1.f : q;  // a NaN stays one
+  const ClipSum norm = clip_root(clip_block_sum(sum));
+  if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm.hi + norm.lo;
+  const float c = clip_factor(norm, max_norm, eps);
   for (ClipWalk<N, true> walk(l); walk.left > 0; walk.next()) {
     if (!walk.t.out || (c == 1.f && walk.t.out == walk.t.in)) continue;
     const ClipRange r(walk.t, walk.word());

@@ -221,3 +221,39 @@ def test_launches(m):
     m.moe_clip_grad_norm(t, 1.0, None, m.clip_workspace())
     after = m.launch_counts()
     assert after["grad_norm"] - before["grad_norm"] == 1 and after["clip"] - before["clip"] == 1
+
+
+def test_the_factor_is_rounded_once(m):
+    """Ones whose sums are exact: the norm is the root of their number, an output the factor."""
+    import numpy as np
+
+    ws, norm = m.clip_workspace(), torch.empty(1, device="cuda")
+    for max_norm, eps in ((0.75, EPS), (3.0, 0.0), (0.1, 2.0**-3)):
+        for n in list(range(10, 200)) + [777, 4096, 100003, 999999]:
+            t = torch.ones(n, device="cuda")
+            m.moe_clip_grad_norm([t], max_norm, norm, ws, eps)
+            root = math.sqrt(n)
+            c = float(np.float32(max_norm)) / (root + float(np.float32(eps)))
+            # half a step, and the pair's own error
+            assert abs(float(norm) - root) <= 0.501 * np.spacing(np.float32(root)), n
+            assert abs(float(t[-1]) - c) <= 0.501 * np.spacing(np.float32(c)), n
+            assert (t == t[0]).all()
+
+
+def test_ends_of_the_factor(m):
+    ws, norm = m.clip_workspace(), torch.empty(1, device="cuda")
+    top = torch.finfo(FP32).max
+    for value, max_norm, eps, want in ((2.0**60, 1.0, 0.0, 1.0), (2.0**-60, 2.0**-61, 0.0, 2.0**-61),
+                                       (1.0, top, 0.0, 1.0), (1.0, 0.0, EPS, 0.0),
+                                       (1.0, 1.0, top, 0.0), (4.0, 2.0**-140, 0.0, 2.0**-140)):
+        t = torch.zeros(100, device="cuda")
+        t[17] = value
+        m.moe_clip_grad_norm([t], max_norm, norm, ws, eps)
+        assert abs(float(t[17]) - want) <= 2.0**-23 * want + 2.0**-127, (value, max_norm, eps)
+        assert float(norm) == value and torch.count_nonzero(t) <= 1
+    t = torch.zeros(100, device="cuda")
+    m.moe_clip_grad_norm([t], 0.0, norm, ws, 0.0)
+    assert float(norm) == 0 and torch.isnan(t).all()  # 0 / 0
+    t = torch.zeros(100, device="cuda")
+    m.moe_clip_grad_norm([t], 1.0, norm, ws, 0.0)
+    assert float(norm) == 0 and (t == 0).all()
