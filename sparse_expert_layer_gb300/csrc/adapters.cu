@@ -488,8 +488,9 @@ __global__ void __launch_bounds__(2 * kShrinkRows<RT>) adapters_shrink_kernel(Ad
 
 // The same for more than 64 ranks through tcgen05, whose operands the slices are as they lie: M is
 // the 128 positions, N the ranks, accumulators in tensor memory.  A thread issues a slice's MMAs,
-// their completion frees its stage.  kAccums accumulators in turn, kFlush slices each, shorten the
-// chains of sums that are cut off.  Of ldmatrix and mma.sync 128 ranks are too many: 8192 rows of
+// their completion frees its stage.  Two accumulators in turn: while one has the MMAs of kFlush
+// slices, what the other holds is added, rounded, to sums in registers, as above.  Of ldmatrix and
+// mma.sync 128 ranks are too many: 8192 rows of
 // 5120 to 5120 in 154 us, here 130; of 64 ranks the call takes 75 us with those and 86 with this.
 template <typename T, int RT>
 __global__ void __launch_bounds__(256, RT <= 64 ? 2 : 1) adapters_shrink_tc_kernel(AdapterArgs a) {
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(256, RT <= 64 ? 2 : 1) adapters_shrink_tc_kern
   __shared__ uint32_t tmem_slot;
   constexpr int kRows = 128, kThreads = 256;
   constexpr int kX = kRows * 128, kStage = kX + RT * 128;
-  constexpr int kAccums = 256 / RT, kFlush = 4;
+  constexpr int kAccums = 2, kFlush = 4;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int rank = blockIdx.x, S = gridDim.x, r = a.r;
   // (the same offset in every CTA of the cluster)
@@ -559,6 +560,21 @@ __global__ void __launch_bounds__(256, RT <= 64 ? 2 : 1) adapters_shrink_tc_kern
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
   const uint32_t idesc = std::is_same<T, __half>::value ? idesc_f16_f32(kRows, RT)
                                                         : idesc_bf16_f32(kRows, RT);
+  // a warp has 32 positions, a lane one of them, and half the ranks
+  float sum[RT / 64][32] = {};
+  auto flush = [&](int chunk) {
+    tc_fence_after();
+#pragma unroll
+    for (int h = 0; h < RT / 64; ++h) {
+      uint32_t d[32];
+      tmem_ld32(tmem + ((uint32_t)(warp % 4 * 32) << 16) + chunk % kAccums * RT +
+                    warp / 4 * (RT / 2) + 32 * h, d);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum[h][i] += __uint_as_float(d[i]);
+    }
+    tc_fence_before();
+  };
   bool ok = true;
   for (int c = c0; c < c1; ++c) {
     const int n = c - c0, slot = n % kShrinkStages;
@@ -566,47 +582,40 @@ __global__ void __launch_bounds__(256, RT <= 64 ? 2 : 1) adapters_shrink_tc_kern
     fence_proxy_async_smem();
     __syncthreads();
     if (tid == 0) {
+      tc_fence_after();
       const uint32_t st = base + slot * kStage;
       const uint32_t d = tmem + n / kFlush % kAccums * RT;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         tc_mma_bf16(d, sdesc_sw128(st + k * 32), sdesc_sw128(st + kX + k * 32), idesc,
-                    n >= kFlush * kAccums || n % kFlush > 0 || k > 0);
+                    n % kFlush > 0 || k > 0);
       tc_commit(smem_u32(&bars[slot]));
     }
     __syncwarp();
-    // the stage of the slice before is free when its MMAs are done
+    // the stage of the slice before is free when its MMAs are done, and so are its accumulator's
     const int ahead = c + kShrinkStages - 1;
     if (n > 0) ok = warp_wait(smem_u32(&bars[(n - 1) % kShrinkStages]),
                               (n - 1) / kShrinkStages & 1) && ok;
     if (ahead < c1) load(ahead, (ahead - c0) % kShrinkStages);
     cp_async_commit();
+    if (n > 0 && n % kFlush == 0) flush(n / kFlush - 1);
   }
   const int all = c1 - c0;
-  if (all > 0) ok = warp_wait(smem_u32(&bars[(all - 1) % kShrinkStages]),
-                              (all - 1) / kShrinkStages & 1) && ok;
-  tc_fence_after();
+  if (all > 0) {
+    ok = warp_wait(smem_u32(&bars[(all - 1) % kShrinkStages]), (all - 1) / kShrinkStages & 1) && ok;
+    flush((all - 1) / kFlush);
+  }
   cp_async_wait<0>();
   __syncthreads();
-  // [position][rank]; a warp has 32 positions and half the ranks
+  // [position][rank]; (rows of 33 x 4 bytes would be out of step with the other CTAs': turn the
+  // columns instead)
   float* red = reinterpret_cast<float*>(raw + (base - smem_u32(raw)));
-  const int used = min(kAccums, (all + kFlush - 1) / kFlush);
+  float* at = red + (warp % 4 * 32 + lane) * RT;
 #pragma unroll
-  for (int h = 0; h < RT / 64; ++h) {
-    const int first = warp / 4 * (RT / 2) + 32 * h;
-    float sum[32] = {};
-    for (int q = 0; q < used; ++q) {
-      uint32_t d[32];
-      tmem_ld32(tmem + ((uint32_t)(warp % 4 * 32) << 16) + q * RT + first, d);
-      tmem_ld_wait();
+  for (int h = 0; h < RT / 64; ++h)
 #pragma unroll
-      for (int i = 0; i < 32; ++i) sum[i] += __uint_as_float(d[i]);
-    }
-    // (rows of 33 x 4 bytes would be out of step with the other CTAs': turn the columns instead)
-    float* at = red + (warp % 4 * 32 + lane) * RT;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) at[(first + i) ^ lane] = ok ? sum[i] : NAN;
-  }
+    for (int i = 0; i < 32; ++i)
+      at[(warp / 4 * (RT / 2) + 32 * h + i) ^ lane] = ok ? sum[h][i] : NAN;
   tc_fence_before();
   cluster_sync_all();
   if (warp == 0) {

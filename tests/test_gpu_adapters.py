@@ -674,6 +674,33 @@ def test_one_infinite_rank_among_finite_ones(m, T, r):
     assert torch.isfinite(y[rest]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("r", [16, 64, 65, 128])
+@pytest.mark.parametrize("T,K", [(400, 65536), (2500, 5120)])
+def test_long_sums_are_rounded_on_the_way(m, T, K, r, dtype):
+    """v of positive numbers, whose MMAs all cut off in one direction.
+
+    Sixteen MMAs lose at most 2 u each of what is held then, 17 u of their sum for terms of
+    about one size (16 + 15 + .. + 1 of 16, each 2 u); a CTA adds its chunks of 256 products
+    rounded, u of the growing sum each; eight CTAs' parts and the store follow.  A sixteenth
+    more covers chunks that are not alike.  One chain of MMAs would lose up to K / 16 u."""
+    J, N = 2, 8
+    c = make(T, J, r, K, N, dtype, none=0.0)
+    c["x"], c["a"] = c["x"].abs() + 0.5, (c["a"].float().abs() + 0.5 / K**0.5).to(dtype)
+    v = torch.zeros(T, r, device="cuda")
+    y, ws = torch.empty_like(c["base"]), m.adapters_workspace(T, r, K, N)
+    m.moe_adapters(c["x"], c["a"], c["b"], c["scale"], c["offsets"], c["order"], c["base"], y, v, ws)
+    torch.cuda.synchronize()
+    units = 17 + K / 256 / 2 / 8 + 8 + 1  # of u; the split over eight CTAs
+    if T == 2500:
+        units = 17 + K / 256 / 2 + 8 + 1  # not split, at most
+    for j in range(J):
+        at = torch.nonzero(c["ids"][c["order"].long()] == j)[:, 0]
+        want = c["x"][c["order"][at].long()].double() @ c["a"][j].double().T
+        off = ((v[at].double() - want).abs() / want).max()
+        assert float(off) <= 17 / 16 * units * U, float(off) / U
+
+
 @pytest.mark.parametrize("r", [16, 64, 128])
 def test_beside_the_layer(m, r):
     """Calls in turn with the layer's on one stream, whose kernels start before the last ones have
