@@ -490,8 +490,8 @@ __global__ void __launch_bounds__(2 * kShrinkRows<RT>) adapters_shrink_kernel(Ad
 // the 128 positions, N the ranks, accumulators in tensor memory.  A thread issues a slice's MMAs,
 // their completion frees its stage.  Two accumulators in turn: while one has the MMAs of kFlush
 // slices, what the other holds is added, rounded, to sums in registers, as above.  Of ldmatrix and
-// mma.sync 128 ranks are too many: 8192 rows of
-// 5120 to 5120 in 154 us, here 130; of 64 ranks the call takes 75 us with those and 86 with this.
+// mma.sync 128 ranks are too many: 8192 rows of 5120 to 5120 in 154 us, here 130; of 64 ranks the
+// call takes 75 us with those and 86 with this.
 template <typename T, int RT>
 __global__ void __launch_bounds__(256, RT <= 64 ? 2 : 1) adapters_shrink_tc_kernel(AdapterArgs a) {
   extern __shared__ unsigned char raw[];
@@ -1199,6 +1199,15 @@ constexpr int shrink_smem() {
   return kShrinkStages * (kShrinkRows<RT> + RT) * 128 + (RT <= 64 ? 0 : 1024);
 }
 
+// CTAs of the shrink that an SM's shared memory holds, as the split over K counts them.  Rank 128,
+// 5120 to 5120 channels, where one fits: 8192 rows 130 us, counted as two 138; 4096 rows 81 and 101.
+constexpr int shrink_per_sm(int r) { return r <= 32 ? 4 : r <= 64 ? 2 : 1; }
+static_assert(shrink_per_sm(16) * (shrink_smem<16>() + 1024) <= 228 * 1024 &&
+                  shrink_per_sm(32) * (shrink_smem<32>() + 1024) <= 228 * 1024 &&
+                  shrink_per_sm(64) * (shrink_smem<64>() + 1024) <= 228 * 1024 &&
+                  shrink_per_sm(128) * (shrink_smem<128>() + 1024) <= 228 * 1024,
+              "CTAs of one round");
+
 // The most CTAs of a power of two, up to eight, that share `units` of work while there
 // are at most `most` CTAs in all and each has at least `least` units.
 int adapters_split(int64_t clusters, int64_t units, int64_t most, int64_t least) {
@@ -1238,9 +1247,8 @@ int adapter_tiles(const AdapterArgs& a, int rows) {
 }
 int shrink_cluster(const AdapterArgs& a, int num_sms) {
   const int rows = shrink_rows(a.r);
-  // two CTAs of 128 positions fit an SM, four of 64
   return adapters_split((a.seg.T + rows - 1) / rows, (a.K + 63) / 64,
-                        (rows == 64 ? 4LL : 2LL) * num_sms, 4);
+                        (int64_t)shrink_per_sm(a.r) * num_sms, 4);
 }
 
 template <typename T, int RT>
