@@ -1217,15 +1217,20 @@ int adapters_split(int64_t clusters, int64_t units, int64_t most, int64_t least)
 }
 
 // One position a cluster, or tiles of positions.  By rows every row reads its adapter again
-// (from L2): cheap while that is little, or where adapters have about a row each.  us by rows and
-// in tiles: rank 16, 5120 to 5120 channels, 64 rows 9.1 and 15.6, 128 (21 M products) 15.6 and 16.1,
-// 160 21.5 and 16.2; 1000 to 1000, 300 rows 8.5 and 10.0, 1000 rows 25 and 10.7; rank 32, 2048 to
-// 2048, 64 rows (8.4 M) 10.6 and 10.2, 128 19 and 11; rank 64, 40 rows 16.5 and 12.5; 64 rows of 64
-// adapters, rank 64, 2048 to 2048 19 and 29, of 48, rank 16, 7168 to 2048 9.3 and 20.
-bool adapters_by_rows(const AdapterArgs& a) {
+// (from L2): cheap while that is little, or where adapters have about a row each; the offsets that
+// say how many have rows lie on the device, so many loaded adapters count as that while T is small
+// beside the SMs.  us by rows and in tiles: rank 16, 5120 to 5120 channels, 64 rows 9.1 and 15.6, 128
+// (21 M products) 15.6 and 16.1, 160 21.5 and 16.2; 1000 to 1000, 300 rows 8.5 and 10.0, 1000 rows 25
+// and 10.7; rank 32, 2048 to 2048, 64 rows (8.4 M) 10.6 and 10.2, 128 19 and 11; rank 64, 40 rows 16.5
+// and 12.5; 64 rows of 64 adapters, rank 64, 2048 to 2048 19 and 29, of 48, rank 16, 7168 to 2048 9.3
+// and 20.  1024 loaded adapters, rows of all of them, and of one (captured in a graph): rank 16, 5120
+// to 5120, 512 rows 81 and 199, 71 and 134, 2048 rows 253 and 353, 237 and 159; rank 64, 2048 to 2048,
+// 256 rows 79 and 118, 67 and 73, 512 rows 140 and 207, 120 and 89, 2048 rows 470 and 407, 433 and
+// 128; rank 128, 5120 to 5120, 512 rows 335 and 724, 249 and 245, 2048 rows 1042 and 1515, 945 and 335.
+bool adapters_by_rows(const AdapterArgs& a, int num_sms) {
   const int64_t T = a.seg.T;
-  return T <= 2 * a.seg.J ||
-         (T <= 304 && T * a.r * (a.K + a.N) <= (a.r <= 16 ? 20 << 20 : 8 << 20));
+  return (T <= 2 * a.seg.J && T <= (a.r <= 16 ? 8 : 3) * num_sms) ||
+         (T <= 2 * num_sms && T * a.r * (a.K + a.N) <= (a.r <= 16 ? 20 << 20 : 8 << 20));
 }
 
 int row_cluster(const AdapterArgs& a) {
@@ -1328,7 +1333,7 @@ template <typename T>
 void launch_adapters(const Launch& L, const AdapterArgs& a, OuterArgs* outer) {
   const int slot = a.r <= 16 ? 0 : a.r <= 32 ? 1 : a.r <= 64 ? 2 : 3;
   if (a.seg.T == 0) {
-  } else if (adapters_by_rows(a)) {
+  } else if (adapters_by_rows(a, L.num_sms)) {
     const int C = row_cluster(a);
     launch_begin(L, MOE_K_ADAPTERS);
     auto rows = [&](auto kernel, int warps) {
@@ -1372,11 +1377,14 @@ struct AdapterLayout {
 };
 AdapterLayout adapters_layout(int64_t T, int64_t r) {
   auto up = [](int64_t n) { return ((size_t)n + 255) & ~(size_t)255; };
+  // largest magnitudes: a word for each CTA of a position's cluster or of a tile's, of which there
+  // are at most T / 64 + T + 1 (adapter_tiles)
+  const int64_t words = T > 0 ? kMaxCluster * (T + T / 64 + 2) : 0;
   AdapterLayout l;
   l.v = 0;
   l.max_v = up(T * r * 4);
-  l.max_other = l.max_v + up(T * kMaxCluster * 4);
-  l.total = l.max_other + up(T * kMaxCluster * 4);
+  l.max_other = l.max_v + up(words * 4);
+  l.total = l.max_other + up(words * 4);
   return l;
 }
 

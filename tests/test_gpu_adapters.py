@@ -701,6 +701,24 @@ def test_long_sums_are_rounded_on_the_way(m, T, K, r, dtype):
         assert float(off) <= 17 / 16 * units * U, float(off) / U
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("which", ["all", "one"])
+@pytest.mark.parametrize("T,J,r,K,N", [
+    (500, 4096, 17, 40, 24), (460, 300, 64, 264, 520), (1000, 512, 128, 136, 72),
+    (1300, 700, 16, 256, 264), (700, 400, 16, 256, 264), (450, 1000, 33, 72, 80)])
+def test_many_loaded_adapters(m, T, J, r, K, N, which, dtype):
+    """By rows while they are few beside the SMs, in tiles above, whatever number is loaded."""
+    ids = None if which == "all" else torch.full((T,), J // 3, device="cuda")
+    c = make(T, J, r, K, N, dtype, ids=ids)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    y, ws = torch.empty_like(c["base"]), m.adapters_workspace(T, r, K, N)
+    before = m.launch_counts()["adapters"]
+    m.moe_adapters(c["x"], c["a"], c["b"], c["scale"], c["offsets"], c["order"], c["base"], y, None, ws)
+    by_rows = T <= (8 if r <= 16 else 3) * sms
+    assert m.launch_counts()["adapters"] - before == (1 if by_rows else 2)
+    check(m, c)
+
+
 @pytest.mark.parametrize("r", [16, 64, 128])
 def test_beside_the_layer(m, r):
     """Calls in turn with the layer's on one stream, whose kernels start before the last ones have
