@@ -719,6 +719,38 @@ def test_many_loaded_adapters(m, T, J, r, K, N, which, dtype):
     check(m, c)
 
 
+def row_form(T, J, r, K, N):
+    """(CTAs, warps) of a position where the call goes by rows (adapters.cu: row_cluster, row_warps)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    cluster = 1
+    while cluster < 8 and max(K, N) >= 2 * cluster * 256:
+        cluster *= 2
+    warps = 4 if r <= 16 else 8 if r <= 32 else 16
+    while warps > 4 and T * cluster * warps * 2 > 16 * sms:
+        warps //= 2
+    return cluster, warps
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("extra", [0, 8, 3])
+@pytest.mark.parametrize("T,J,r,K,N,form", [
+    (1, 2, 64, 5120, 1024, (8, 16)), (1, 1, 128, 2048, 2056, (8, 16)), (3, 8, 100, 1001, 515, (2, 16)),
+    (8, 8, 33, 264, 520, (2, 16)), (2, 3, 65, 7, 3000, (8, 16)), (1, 1, 127, 200, 90, (1, 16)),
+    (4, 4, 24, 1000, 1544, (4, 8)), (40, 30, 64, 1032, 600, (4, 4)), (30, 20, 48, 520, 1000, (2, 16)),
+    (60, 50, 40, 600, 72, (2, 8)), (2, 2, 17, 4096, 4104, (8, 8)), (3, 2, 16, 4096, 264, (8, 4))])
+def test_widths_of_a_row(m, T, J, r, K, N, form, extra, dtype):
+    """Four, eight and sixteen warps a CTA, one to eight CTAs a row."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    if sms == 152:
+        assert row_form(T, J, r, K, N) == form
+    c = make(T, J, r, K, N, dtype, none=0.0 if T == 1 else 0.2)
+    y, ws = torch.empty_like(c["base"]), m.adapters_workspace(T, r, K, N)
+    before = m.launch_counts()["adapters"]
+    m.moe_adapters(c["x"], c["a"], c["b"], c["scale"], c["offsets"], c["order"], c["base"], y, None, ws)
+    assert m.launch_counts()["adapters"] - before == 1
+    check(m, c, extra)
+
+
 @pytest.mark.parametrize("r", [16, 64, 128])
 def test_beside_the_layer(m, r):
     """Calls in turn with the layer's on one stream, whose kernels start before the last ones have
