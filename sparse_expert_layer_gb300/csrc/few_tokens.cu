@@ -53,6 +53,9 @@ constexpr int kFewMaxPicks = kFewMaxT * 32;
 constexpr int kFewMaxTH = 65536;           // tokens x hidden
 constexpr int kFewMaxInter = 1 << 20;      // rows and tiles are counted in 32 bits
 constexpr int kRouteScratch = 96 * 1024;   // top-k scratch in shared memory, at most
+// MMAs cut their sums off where fp32 ends, each time the same way: with 16-bit weights what
+// sixteen of them hold is added, rounded, to the sum.  (4-bit ones: a block's are scaled and added.)
+constexpr int kFewChain = 16;
 
 // One expert with rows (expert -1: the shared one).
 struct FewUnit {
@@ -775,7 +778,14 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, c
     tile_at(n, tile, &u, &f);
     const int e = units[u].expert;
     const FewGroups at = groups_at<K>(a, sh, (e < 0 ? 0 : (int64_t)e * a.I) + f * 8 + g);
-    float acc[4] = {};
+    float acc[4] = {}, sum[4] = {};
+    auto flush = [&]() {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sum[i] += acc[i];
+        acc[i] = 0.f;
+      }
+    };
     uint32_t xat = x0, sum_at = sum0;
     for (int step = k0; step < k1; ++step) {
       wait_stage(S);
@@ -800,16 +810,21 @@ __device__ __forceinline__ void gate_up(const FewArgs& a, unsigned char* smem, c
       }
       const uint32_t none[1][4] = {};
       multiply<K, false>(use, b, none, xs, a, at, step, acc);
+      if constexpr (!K::kFour) {
+        constexpr int kSteps = kFewChain / (2 * K::kWords);
+        if ((step - k0) % kSteps == kSteps - 1) flush();
+      }
       before = use;
       use = use == ring_last ? ring : use + sub;
     }
     // The parts meet in one of two buffers; one warp of the team, another each time, adds them
     // and stores h while the others go on.  (The buffer's next use is past the next barrier,
     // which that warp reaches when it is done.)
+    flush();
     float* parts = red + (seq & 1) * kFewTeamWarps * 128;
     float* r = parts + kw * 128 + g * 8 + 2 * tg;
-    *reinterpret_cast<float2*>(r) = make_float2(acc[0], acc[1]);
-    *reinterpret_cast<float2*>(r + 64) = make_float2(acc[2], acc[3]);
+    *reinterpret_cast<float2*>(r) = make_float2(sum[0], sum[1]);
+    *reinterpret_cast<float2*>(r + 64) = make_float2(sum[2], sum[3]);
     if (tt == 0) queue[(seq + ahead + 1) % 16] = claimed;
     team_barrier(team);
     if (kw == seq % kFewTeamWarps) {
@@ -1108,6 +1123,10 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
         use = use == ring_last ? ring : use + sub;
       }
       ++step;
+      if constexpr (!K::kFour) {
+        constexpr int kSteps = kFewChain / (4 * K::kWords);
+        if ((f - f0) % kSteps == kSteps - 1) flush();
+      }
     }
     flush();
     cp_async_wait<0>();

@@ -478,3 +478,46 @@ def test_an_infinite_h_gives_infinities(m, name, T, dtype):
     rest = [t for t in range(1, T) if e not in ids[t].tolist()]
     assert torch.isfinite(out[rest]).all()
     assert m.moe_check_device_status(ws) == m.MOE_OK
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("H,I,T", [(65536, 64, 1), (8192, 64, 8), (1024, 1 << 18, 8)])
+def test_long_sums_are_rounded_on_the_way(m, H, I, T, dtype):
+    """All terms positive, so that MMAs all cut off in one direction and relative errors add up.
+
+    An output is the rounding of a number within d of the value.  Sixteen MMAs lose at most 17 u
+    of their sum (2 u each of what is held then, 16 + 15 + .. + 1 of 16 parts); n such sums added,
+    rounded, n / 2 + 1 u; the parts of four warps (gate and up) or sixteen (down) 4 or 16 u.  h
+    has gate's (times 1.1, for silu') and up's, 16 u of its own, and its split, 2^-17 or 2^-22.
+    A sixteenth more covers parts that are not alike.  A chain of K / 64 MMAs and more would lose
+    hundreds of u, a good part of which shows in fp16's step, 8192 u."""
+    spec = synth.spec("tiny", T=T, name="few_long", n_zero=0, renormalize=True, hidden=H, inter=I,
+                      n_routed=1, top_k=1)
+    g = gen(H + I)
+    x = 0.5 + torch.rand(T, H, generator=g, device="cuda")
+    # (gate's weights, about 24 / H: silu(24) is 24)
+    w = {"w_gate": 0.5 + torch.rand(1, I, H, generator=g, device="cuda"),
+         "w_up": 0.5 + torch.rand(1, I, H, generator=g, device="cuda"),
+         "w_down": 0.5 + torch.rand(1, H, I, generator=g, device="cuda")}
+    for key, scale in (("w_gate", 24 / H), ("w_up", 2 / H), ("w_down", 1 / I)):
+        w[key] = w[key].mul_(scale).mul_(64 if dtype == FP16 and key == "w_down" else 1).to(dtype)
+    x = x.to(dtype)
+    experts = m.FewTokenExperts(m.config_from_spec(spec), w, torch.ones(1, H, device="cuda"))
+    ws = m.few_tokens_workspace(experts, T)
+    out = torch.empty_like(x)
+    m.moe_few_tokens(experts, x, out, ws)
+    torch.cuda.synchronize()
+    assert m.moe_check_device_status(ws) == m.MOE_OK
+    xd = x.double()
+
+    def product(v, key):  # in parts: 64-bit copies of the large weights are too large
+        return torch.cat([v @ part.double().T for part in w[key][0].split(1 << 14)], 1)
+
+    gate, up = product(xd, "w_gate"), product(xd, "w_up")
+    want = product(gate * torch.sigmoid(gate) * up, "w_down")
+    assert float(want.min()) > 2.0**-10 and float(want.max()) < 2.0**15
+    product_of = 17 + H / 256 / 4 / 2 + 1 + 4
+    d = 2.1 * product_of + 16 + 17 + I / 64 / 16 / 2 / 2 + 1 + 16
+    d = 17 / 16 * d * U + (2.0**-17 if dtype == BF16 else 2.0**-22)
+    low, high = (want * (1 - d)).to(dtype), (want * (1 + d)).to(dtype)
+    assert (out >= low).all() and (out <= high).all(), float(((out.double() - want) / want).abs().max())
