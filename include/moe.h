@@ -407,9 +407,11 @@ moe_status moe_w4_gemv(int32_t n_experts, int32_t N, int32_t K, int32_t group, i
  *            + shared expert,
  * for decode steps and short drafts, where that call's launches would take longer than
  * the picked experts' weights.  Logits and statistics are fp32; 16-bit weights meet x
- * as it is and h as a sum of two 16-bit numbers, 4-bit weights meet x exactly (elements
- * below 2^-23 of a token's largest are rounded at 2^-33 of it) and h with 11 bits; all
- * sums and scales are fp32 and out is rounded once.  The same bits on every call.  An
+ * as it is and h as a sum of two 16-bit numbers.  4-bit weights meet x in fp16, scaled so
+ * that elements down to 2^-23 of a token's largest are exact (their MMAs add products cut
+ * off at 2^-15 of the largest x of sixteen), and h as a sum of two fp16 numbers where x is
+ * fp16 (22 bits), as one where it is bf16 (11 bits, of which 8 are left in out).  Other sums
+ * and scales are fp32 and out is rounded once.  The same bits on every call.  An
  * infinite h is infinite in out, NaN with 4-bit weights.
  *  cfg       wdtype MOE_W_BF16 whatever the weights are; out_fp32, gemv_max_rows,
  *            combine and ffn_launch are not read

@@ -33,9 +33,22 @@
 // q * 2^-24 (four bits up: q * 2^-20, its x is divided by 16), so a weight costs part of
 // one AND.  x (and h) are scaled by a power of two for each token that brings their
 // largest value to 2^13, which makes them fp16 exactly (bf16 values: down to 2^-26 of
-// the largest), h rounded to 11 bits.  A block's MMAs start from -z times its sum of
-// x (of h: another MMA gives it), so they hold 2^-24 times the sum of (q - z) x; scales are
-// applied in fp32.  16-bit weights: x as it is, h as a sum of two 16-bit numbers.
+// the largest).  A block's MMAs start from -z times its sum of x (of h: another MMA gives it), so
+// they hold 2^-24 times the sum of (q - z) x; scales are applied in fp32.  16-bit weights: x as it
+// is.
+//
+// An MMA cuts off what it adds at 2^-25 of the largest addend, for which a subnormal counts as 2^-14,
+// the smallest normal number: at 2^-15 of the largest x of sixteen where that meets q * 2^-24.  h is
+// about 1e-6 off by that, 1 to 2e-5 beside channels a thousand times as loud.  With codes brought
+// to q * 2^-18 (three shifts more for eight of them) it was 2 to 4e-7 off, which no output showed,
+// and one token took 4% longer.
+//
+// With 16-bit weights h is a sum of two 16-bit numbers, the second of which has MMAs of its own.
+// With 4-bit ones, whose products are bound by issue and registers, h is one fp16 number where outputs
+// are bf16: these are 1.65e-3 off by their rounding, its 11 bits do not show.  fp16 outputs, 2.1e-4
+// off by theirs, were 2.8 to 3.2e-4 off with it, so there a token's h takes two columns of the MMAs,
+// for its two terms: four tokens fill them, and an expert with more goes through the down projection
+// twice.  That makes calls 5 to 9% longer.
 #include <math.h>
 
 #include "few_plan.h"
@@ -63,6 +76,12 @@ struct FewUnit {
   uint32_t tokens;  // bit t: token t picked it
 };
 static_assert(sizeof(FewUnit) == kFewUnitBytes, "the plan's size");
+// Tokens of a unit that the down projection takes at once.
+struct FewPass {
+  int unit;
+  uint32_t tokens;
+};
+static_assert(sizeof(FewPass) == kFewPassBytes, "the plan's size");
 
 // Workspace after the status block.  `ticket` is zero between calls; the rest is
 // written by the first kernel.
@@ -476,11 +495,13 @@ __device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1
 
 // The kinds of weights.  kWords: granules of eight K that a lane supplies in a stage;
 // granule i is x's 16-byte piece piece(i, tg) of the stage.
-template <int BLOCK, bool ZEROS, typename SCALE>
+template <int BLOCK, bool ZEROS, typename SCALE, bool PAIRED>
 struct Four {
   using Mma = __half;
   using Scale = SCALE;
-  static constexpr bool kFour = true, kZeros = ZEROS, kScaled = true, kRest = false;
+  static constexpr bool kFour = true, kZeros = ZEROS, kScaled = true;
+  // a second term of h has MMAs or columns of its own
+  static constexpr bool kRest = false, kPaired = PAIRED, kTwo = PAIRED;
   static constexpr int kStepK = 256, kWords = 8, kScaleBytes = sizeof(SCALE);
   static constexpr int kBlock = BLOCK, kBlocks = 256 / BLOCK, kPer = BLOCK / 32;
   // first K of granule i of quad lane tg
@@ -501,17 +522,17 @@ struct Four {
     return BLOCK == 128 ? c ^ ((r & 1) << 2) : BLOCK == 64 ? c ^ ((r & 3) << 1) : c ^ (r & 7);
   }
   // (k0, k4) (k1, k5) / 16 (k2, k6) (k3, k7) / 16 of eight values
-  static __device__ __forceinline__ void operands(const float (&v)[8], uint32_t (&b)[4]) {
-    b[0] = pack2<__half>(v[0], v[4]);
-    b[1] = pack2<__half>(v[1] * 0.0625f, v[5] * 0.0625f);
-    b[2] = pack2<__half>(v[2], v[6]);
-    b[3] = pack2<__half>(v[3] * 0.0625f, v[7] * 0.0625f);
+  static __device__ __forceinline__ void order(float (&v)[8]) {
+    const float w[8] = {v[0], v[4], v[1] * 0.0625f, v[5] * 0.0625f,
+                        v[2], v[6], v[3] * 0.0625f, v[7] * 0.0625f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = w[i];
   }
 };
 template <typename T>
 struct Sixteen {
   using Mma = T;
-  static constexpr bool kFour = false, kRest = true;
+  static constexpr bool kFour = false, kRest = true, kPaired = false, kTwo = true;
   static constexpr bool kScaled = std::is_same<T, __half>::value;  // h needs fp16's range
   static constexpr int kStepK = 64, kWords = 2, kBlocks = 1;
   static __device__ __forceinline__ int k_of(int i, int tg) { return i * 32 + tg * 8; }
@@ -873,14 +894,14 @@ constexpr int kFewDownTiles = 4;  // 16-row tiles of one pass of the down projec
 template <typename K>
 __device__ __forceinline__ void h_operands(const float4& p, const float4& q, float up,
                                            uint32_t (&b)[4], uint32_t (&rest)[4]) {
-  const float v[8] = {p.x * up, p.y * up, p.z * up, p.w * up,
-                      q.x * up, q.y * up, q.z * up, q.w * up};
-  if constexpr (K::kFour) {
-    K::operands(v, b);
-  } else {
+  float v[8] = {p.x * up, p.y * up, p.z * up, p.w * up, q.x * up, q.y * up, q.z * up, q.w * up};
+  if constexpr (K::kFour) K::order(v);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (K::kTwo)
       split2<typename K::Mma>(v[2 * j], v[2 * j + 1], b[j], rest[j]);
+    else
+      b[j] = pack2<typename K::Mma>(v[2 * j], v[2 * j + 1]);
   }
 }
 
@@ -913,13 +934,13 @@ __device__ __forceinline__ void stage_h(const FewArgs& a, unsigned char* smem,
       const int e = e0 + i * kFewThreads, r = e / pieces, j = e % pieces;
       if (e >= n) break;
       const float up = K::kScaled ? __uint_as_float(fp16_range_bits(most[i])) : 1.f;
-      uint32_t b[4], rest[4] = {};
+      uint32_t b[4], rest[4];
       h_operands<K>(p[i], q[i], up, b, rest);
       const int step = j / (K::kStepK / 8);
       unsigned char* to = smem + r * a.p.hpitch +
                           (step * (K::kStepK / 8) + K::piece_of_k8(j % (K::kStepK / 8))) * 16;
       *reinterpret_cast<uint4*>(to) = make_uint4(b[0], b[1], b[2], b[3]);
-      if constexpr (K::kRest)
+      if constexpr (K::kTwo)
         *reinterpret_cast<uint4*>(to + a.p.hrest) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
     }
   }
@@ -927,7 +948,8 @@ __device__ __forceinline__ void stage_h(const FewArgs& a, unsigned char* smem,
 
 template <typename K>
 __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, const FewUnit* units,
-                                     const FewTiles& n, bool shared, const float* zero_w) {
+                                     const FewTiles& n, const FewPass* passes, const int* npasses,
+                                     int nunits, const float* zero_w) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int g = lane / 4, tg = lane % 4;
   const FewShape rs = shape_of<K>(a, a.I), ss = shape_of<K>(a, a.Is);
@@ -938,30 +960,31 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
   float* sums = reinterpret_cast<float*>(smem + a.p.ring_at);
   const int share = (a.H + gridDim.x - 1) / gridDim.x;
   const int c_begin = min(a.H, (int)blockIdx.x * share), c_end = min(a.H, c_begin + share);
-  const int routed = n.units * rs.steps, flat = routed + (shared ? ss.steps : 0);
+  // every pass's steps, the routed experts' first
+  const int routed = npasses[0] * rs.steps, flat = routed + npasses[1] * ss.steps;
   const int f0 = (int)((int64_t)flat * warp / kFewWarps);
   const int f1 = (int)((int64_t)flat * (warp + 1) / kFewWarps);
-  const int u0 = f0 < routed ? f0 / max(1, rs.steps) : n.units;
+  const int d0 = f0 < routed ? f0 / rs.steps : npasses[0] + (f0 - routed) / max(1, ss.steps);
+  const int step0 = f0 < routed ? f0 % rs.steps : (f0 - routed) % max(1, ss.steps);
   const int dst = lane / 8 * 128;
-  const uint32_t d0 = dst + K::swizzle(lane / 8, lane % 8) * 16;
-  const uint32_t d1 = dst + 4 * 128 + K::swizzle(lane / 8 + 4, lane % 8) * 16;
+  const uint32_t dst0 = dst + K::swizzle(lane / 8, lane % 8) * 16;
+  const uint32_t dst1 = dst + 4 * 128 + K::swizzle(lane / 8 + 4, lane % 8) * 16;
   // units' first rows of h, and behind the last their number; then the rows' units and tokens
   const int* row0 = reinterpret_cast<const int*>(smem + a.p.row_at);
-  const int nunits = n.units + shared;
   const bool inside = a.p.hpitch > 0;
   bool waited = false;
 
   for (int c0 = c_begin; c0 < c_end; c0 += 16 * kFewDownTiles) {
     const int channels = min(c_end - c0, 16 * kFewDownTiles);
     const int tiles = (channels + 15) / 16;
-    // What is copied next: tile m of step next_step of unit next_u; the lane's piece of the
+    // What is copied next: tile m of step next_step of pass next_d; the lane's piece of the
     // tile's row lane / 8, and the groups of the range's row lane / 2.
-    int togo = f1 - f0, next_u = u0, next_step = f0 - u0 * rs.steps, m_next = 0;
+    int togo = f1 - f0, next_d = d0, next_step = step0, m_next = 0;
     int next_steps = 0, next_groups = 0, next_row = 0;
     const unsigned char *w = nullptr, *sp = nullptr, *zp = nullptr;
     int64_t four = 0;  // bytes of four rows
     auto enter = [&]() {
-      const int e = units[next_u].expert;
+      const int e = units[passes[next_d].unit].expert;
       const FewMatrix& m = e < 0 ? a.shared[2] : a.m[2];
       next_steps = e < 0 ? ss.steps : rs.steps;
       next_groups = e < 0 ? ss.groups : rs.groups;
@@ -981,10 +1004,10 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
         // rows past the range are not stored, whatever they hold
         int rows = channels - m_next * 16 - lane / 8;
         if (next_step * 128 + (lane % 8) * 16 >= next_row) rows = 0;
-        copy_piece<K::kFour>(slot + d0, w, rows > 0, a.x, policy);
-        copy_piece<K::kFour>(slot + d1, w + four, rows > 4, a.x, policy);
-        copy_piece<K::kFour>(slot + d0 + 8 * 128, w + 2 * four, rows > 8, a.x, policy);
-        copy_piece<K::kFour>(slot + d1 + 8 * 128, w + 3 * four, rows > 12, a.x, policy);
+        copy_piece<K::kFour>(slot + dst0, w, rows > 0, a.x, policy);
+        copy_piece<K::kFour>(slot + dst1, w + four, rows > 4, a.x, policy);
+        copy_piece<K::kFour>(slot + dst0 + 8 * 128, w + 2 * four, rows > 8, a.x, policy);
+        copy_piece<K::kFour>(slot + dst1 + 8 * 128, w + 3 * four, rows > 12, a.x, policy);
         if constexpr (K::kFour) {
           // (a row past the range takes the last one's)
           const int r = min(m_next * 16, channels - 1 - lane / 2) * next_groups;
@@ -999,7 +1022,7 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
           --togo;
           if (++next_step == next_steps) {
             next_step = 0;
-            ++next_u;
+            ++next_d;
             if (togo) enter();
           }
         }
@@ -1022,14 +1045,32 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
 
     float acc[kFewDownTiles][4] = {}, total[kFewDownTiles][4] = {};
     float w0 = 0.f, w1 = 0.f, up = 1.f;
-    bool in0 = false, in1 = false;  // the lane's columns have picked the unit
-    const float* hrow = nullptr;
+    bool in0 = false, in1 = false;  // tokens 2 tg and 2 tg + 1 are the pass's
+    int from0 = 0, from1 = 0;       // their columns, where these are paired
+    const float* hrow = nullptr;    // of the lane's column g
     uint32_t hat = 0;  // the row in shared memory
     FewGroups at{};  // of every tile: sixteen rows on, groups lie alike
-    int u = u0, step = f0 - u0 * rs.steps, steps = 0, kmax = 0;
+    int d = d0, step = step0, steps = 0, kmax = 0;
     auto flush = [&]() {
 #pragma unroll
       for (int m = 0; m < kFewDownTiles; ++m) {
+        if constexpr (K::kPaired) {
+          // columns c and c + 4 are the terms of the pass's token c: added, and brought to the
+          // lane that has that token
+          float both[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            both[i] = acc[m][i] + __shfl_xor_sync(0xffffffffu, acc[m][i], 2);
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            const float a0 = __shfl_sync(0xffffffffu, both[i], from0 / 2, 4);
+            const float b0 = __shfl_sync(0xffffffffu, both[i + 1], from0 / 2, 4);
+            const float a1 = __shfl_sync(0xffffffffu, both[i], from1 / 2, 4);
+            const float b1 = __shfl_sync(0xffffffffu, both[i + 1], from1 / 2, 4);
+            acc[m][i] = from0 & 1 ? b0 : a0;
+            acc[m][i + 1] = from1 & 1 ? b1 : a1;
+          }
+        }
         // (other columns' sums are zeros, but NaN where a weight is not finite)
         if (in0) {
           total[m][0] = fmaf(w0, acc[m][0], total[m][0]);
@@ -1047,22 +1088,33 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
         if (f > f0) {
           flush();
           step = 0;
-          ++u;
+          ++d;
         }
-        const int e = units[u].expert;
+        const int u = passes[d].unit, e = units[u].expert;
         const FewShape& sh = e < 0 ? ss : rs;
         steps = sh.steps;
         kmax = sh.K;
-        const uint32_t tokens = units[u].tokens;
-        hrow = (tokens >> g) & 1u ? a.h + ((int64_t)u * a.T + g) * a.inter : nullptr;
-        if (inside)
-          hat = smem_u32(smem) + (row0[u] + __popc(tokens & ((1u << g) - 1u))) * a.p.hpitch + tg * 16;
+        const uint32_t tokens = passes[d].tokens;
         in0 = (tokens >> (2 * tg)) & 1u;
         in1 = (tokens >> (2 * tg + 1)) & 1u;
+        int t = g;  // the token of the lane's column
+        bool has = (tokens >> g) & 1u;
+        if constexpr (K::kPaired) {  // the pass's token g % 4
+          uint32_t left = tokens;
+          for (int i = 0; i < g % kFewPairs; ++i) left &= left - 1u;
+          has = left != 0u;
+          t = has ? __ffs(left) - 1 : 0;
+          from0 = __popc(tokens & ((1u << (2 * tg)) - 1u));
+          from1 = from0 + in0;
+        }
+        hrow = has ? a.h + ((int64_t)u * a.T + t) * a.inter : nullptr;
+        if (inside)
+          hat = smem_u32(smem) + (row0[u] + __popc(units[u].tokens & ((1u << t) - 1u))) * a.p.hpitch +
+                tg * 16 + (K::kPaired && g >= kFewPairs ? a.p.hrest : 0);
         w0 = __ldcg(&a.head->w[u][2 * tg]) * (K::kFour ? 16777216.f : 1.f);
         w1 = __ldcg(&a.head->w[u][2 * tg + 1]) * (K::kFour ? 16777216.f : 1.f);
         if constexpr (K::kScaled) {
-          up = __uint_as_float(fp16_range_bits(__ldcg(&a.head->hmax[u][g])));
+          up = __uint_as_float(fp16_range_bits(__ldcg(&a.head->hmax[u][t])));
           w0 *= inverse_pow2(fp16_range_bits(__ldcg(&a.head->hmax[u][2 * tg])));
           w1 *= inverse_pow2(fp16_range_bits(__ldcg(&a.head->hmax[u][2 * tg + 1])));
         }
@@ -1092,6 +1144,10 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
             q = __ldcg(reinterpret_cast<const float4*>(hrow + k + 4));
           }
           h_operands<K>(p, q, up, b[i], rest[K::kRest ? i : 0]);
+          if (K::kPaired && g >= kFewPairs) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b[i][j] = rest[0][j];
+          }
         }
       }
       float2 xs[K::kBlocks];
@@ -1205,9 +1261,9 @@ __device__ __forceinline__ void stage_x(const FewArgs& a, unsigned char* smem, f
           v[2 * l] = f.x * up;
           v[2 * l + 1] = f.y * up;
         }
-        uint32_t b[4];
-        K::operands(v, b);
-        q = make_uint4(b[0], b[1], b[2], b[3]);
+        K::order(v);
+        q = make_uint4(pack2<__half>(v[0], v[1]), pack2<__half>(v[2], v[3]),
+                       pack2<__half>(v[4], v[5]), pack2<__half>(v[6], v[7]));
       }
     }
     const int step = j / (K::kStepK / 8);
@@ -1243,6 +1299,7 @@ template <typename K>
 __global__ void __launch_bounds__(kFewThreads, 1) few_ffn_kernel(const __grid_constant__ FewArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float x_inverse[kFewMaxT], zero_w[kFewMaxT];
+  __shared__ int npasses[2];  // of routed experts, of the shared one
   const int tid = threadIdx.x;
   // x is complete: the routing kernel let this one start only after its own wait for
   // everything before it.  What the routing kernel writes is read after the wait here.
@@ -1259,12 +1316,28 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_ffn_kernel(const __grid_co
     reinterpret_cast<uint32_t*>(units)[i] = __ldcg(reinterpret_cast<const uint32_t*>(a.head->unit) + i);
   if (tid < kFewMaxT) zero_w[tid] = __ldcg(&a.head->zero_w[tid]);
   __syncthreads();
-  if (a.p.hpitch > 0) {  // the rows of h (read after the next barrier)
+  // the passes of the down projection and, where h is kept here, its rows (read after the next
+  // barrier)
+  const int nunits = n.units + shared;
+  FewPass* passes = reinterpret_cast<FewPass*>(smem + a.p.pass_at);
+  constexpr int kMost = K::kPaired ? kFewPairs : kFewMaxT;  // tokens of a pass
+  for (int u = tid; u <= nunits; u += kFewThreads) {
     int* row0 = reinterpret_cast<int*>(smem + a.p.row_at);
-    const int nunits = n.units + shared;
-    for (int u = tid; u <= nunits; u += kFewThreads) {
-      int first = 0;
-      for (int i = 0; i < u; ++i) first += __popc(units[i].tokens);
+    int first = 0, pass = 0;
+    for (int i = 0; i < u; ++i) {
+      const int tokens = __popc(units[i].tokens);
+      first += tokens;
+      pass += tokens > kMost ? 2 : 1;
+    }
+    if (u == n.units) npasses[0] = pass;
+    if (u == nunits) npasses[1] = shared ? __popc(units[n.units].tokens) > kMost ? 2 : 1 : 0;
+    if (u < nunits) {
+      uint32_t rest = units[u].tokens;
+      for (int i = 0; i < kMost; ++i) rest &= rest - 1u;
+      passes[pass] = {u, units[u].tokens ^ rest};
+      if (rest) passes[pass + 1] = {u, rest};
+    }
+    if (a.p.hpitch > 0) {
       row0[u] = first;
       if (u < nunits)
         for (int t = 0; t < kFewMaxT; ++t)
@@ -1274,7 +1347,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_ffn_kernel(const __grid_co
   gate_up<K>(a, smem, units, n, x_inverse);
   __syncthreads();
   pdl_trigger();
-  down<K>(a, smem, units, n, shared, zero_w);
+  down<K>(a, smem, units, n, passes, npasses, nunits, zero_w);
 }
 
 // ------------------------------------------------------------------ launch --
@@ -1297,21 +1370,27 @@ void launch_ffn(const Launch& L, const FewArgs& a, int slot) {
   launch_kernel(few_ffn_kernel<K>, dim3(L.num_sms), dim3(kFewThreads), a.p.bytes, L.stream, a);
   launch_end(L, MOE_K_FEW_FFN);
 }
-template <int BLOCK, bool ZEROS>
+template <int BLOCK, bool ZEROS, bool PAIRED>
 void launch_four_as(const Launch& L, const FewArgs& a, int slot) {
   if (a.scale_dtype == MOE_DT_BF16)
-    launch_ffn<Four<BLOCK, ZEROS, __nv_bfloat16>>(L, a, slot);
+    launch_ffn<Four<BLOCK, ZEROS, __nv_bfloat16, PAIRED>>(L, a, slot);
   else if (a.scale_dtype == MOE_DT_FP16)
-    launch_ffn<Four<BLOCK, ZEROS, __half>>(L, a, slot + 1);
+    launch_ffn<Four<BLOCK, ZEROS, __half, PAIRED>>(L, a, slot + 1);
   else
-    launch_ffn<Four<BLOCK, ZEROS, float>>(L, a, slot + 2);
+    launch_ffn<Four<BLOCK, ZEROS, float, PAIRED>>(L, a, slot + 2);
 }
 template <int BLOCK>
 void launch_four(const Launch& L, const FewArgs& a, bool zeros, int slot) {
-  if (zeros)
-    launch_four_as<BLOCK, true>(L, a, slot);
-  else
-    launch_four_as<BLOCK, false>(L, a, slot + 3);
+  if (a.fp16) {
+    if (zeros)
+      launch_four_as<BLOCK, true, true>(L, a, slot);
+    else
+      launch_four_as<BLOCK, false, true>(L, a, slot + 3);
+  } else if (zeros) {
+    launch_four_as<BLOCK, true, false>(L, a, slot + 6);
+  } else {
+    launch_four_as<BLOCK, false, false>(L, a, slot + 9);
+  }
 }
 
 // (without routed experts cfg.inter means nothing: it may be any number)
@@ -1418,7 +1497,7 @@ extern "C" moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weight
   const int es = wt->scale_dtype == MOE_DT_FP32 ? 4 : 2;
   a.p = few_plan(T, c.hidden, std::max(few_inter(c), c.shared_inter), units,
                  T * (std::min(c.n_routed, c.top_k) + (c.shared_inter > 0)), four, wt->group, es,
-                 zeros, aligned_s, aligned_z, whole);
+                 zeros, aligned_s, aligned_z, whole, !four || dtype == MOE_DT_FP16);
   if (a.p.stages < 2) return MOE_ERR_UNSUPPORTED;
   Launch L;
   const moe_status s = open_launch(stream, &L);
@@ -1483,8 +1562,8 @@ extern "C" moe_status moe_few_tokens(const moe_config* cfg, const moe_few_weight
   else if (a.p.block == 32)
     launch_four<32>(L, a, zeros, 2);
   else if (a.p.block == 64)
-    launch_four<64>(L, a, zeros, 8);
+    launch_four<64>(L, a, zeros, 14);
   else
-    launch_four<128>(L, a, zeros, 14);
+    launch_four<128>(L, a, zeros, 26);
   return launch_status_take();
 }

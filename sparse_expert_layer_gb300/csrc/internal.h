@@ -428,8 +428,8 @@ enum {
   kAttrW4Base,                   // x type x group x zero points
   kAttrW4Slots = 3 * 3 * 2,
   kAttrFewRoute = kAttrW4Base + kAttrW4Slots,  // 4 slots: tokens 1, 2, 4, 8
-  kAttrFewFfn = kAttrFewRoute + 4,             // 20 slots: kinds of weights
-  kAttrAdapters = kAttrFewFfn + 20,            // 28 slots: kernels x types x ranks
+  kAttrFewFfn = kAttrFewRoute + 4,             // 38 slots: kinds of weights
+  kAttrAdapters = kAttrFewFfn + 38,            // 28 slots: kernels x types x ranks
   kAttrSlots = kAttrAdapters + 28
 };
 void set_smem_attr_once(const void* func, int bytes, int slot);

@@ -521,3 +521,169 @@ def test_long_sums_are_rounded_on_the_way(m, H, I, T, dtype):
     d = 17 / 16 * d * U + (2.0**-17 if dtype == BF16 else 2.0**-22)
     low, high = (want * (1 - d)).to(dtype), (want * (1 + d)).to(dtype)
     assert (out >= low).all() and (out <= high).all(), float(((out.double() - want) / want).abs().max())
+
+
+def cut_product(w, key, infix, mat, e, v, dv=None):
+    """A 4-bit matrix in groups of 32 times v (off by dv) in 64 bits, and the bound of its error.
+
+    A block is four MMAs (two of codes, two of ones for the sum of v), each of sixteen products and
+    what it starts from, cut off at 2^-15 of the largest |v|: 68 of that times the block's scale.
+    Blocks, warps and scales are added and applied in fp32: 15 u of the magnitudes."""
+    a, b = exact_matrix(w, key, infix, mat, e)
+    s = w[f"s_{infix}{mat}"]
+    s = (s if e is None else s[e]).double()
+    top = (v.abs() + (0 if dv is None else dv)).max()
+    tol = 15 * U * (b @ v.abs()) + 68 * 2.0**-15 * top * s.abs().sum(1) + \
+        2.0**-33 * top * a.abs().sum(1)
+    return a @ v, tol if dv is None else tol + a.abs() @ dv
+
+
+def hidden_of(c, prefix, infix, e, x):
+    """(h, bound of its error as the down projection takes it) of one expert for one token."""
+    (g, dg), (u, du) = (cut_product(c["w"], prefix + mat, infix, mat, e, x) for mat in ("gate", "up"))
+    silu = g * torch.sigmoid(g)
+    h = silu * u
+    dh = 1.1 * dg * u.abs() + (silu.abs() + 1.1 * dg) * du + 16 * U * h.abs()
+    # one fp16 number where x is bf16 (half a step: eps / 2 = 2^-11), else two; 2^-34 of the largest
+    rel = 2.0**-11 if c["dtype"] == BF16 else 2.0**-22
+    return h, dh + rel * (h.abs() + dh) + 2.0**-34 * (h.abs() + dh).max()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("T,E,k,Is", [(1, 1, 1, 0), (3, 2, 1, 64), (4, 8, 3, 0), (5, 1, 1, 64),
+                                      (6, 3, 2, 32), (8, 1, 1, 0), (8, 2, 2, 96), (8, 16, 4, 64)])
+@pytest.mark.parametrize("I", [64, 2080])
+def test_differences_of_h_in_four_bit_layers(m, T, E, k, Is, I, dtype):
+    """Rows of the down projection with +1 and -1 at two h of a token that are next to each other in
+    size, for experts with one to eight tokens."""
+    H = 96
+    spec = synth.spec("tiny", T=T, name="few_h", n_zero=0, renormalize=True, hidden=H, inter=I,
+                      n_routed=E, top_k=k, shared_inter=Is)
+    g = gen(T + E + I)
+    x = torch.randn(T, H, generator=g, device="cuda").to(BF16)
+    x = torch.where(x.abs() < 2.0**-9, torch.zeros_like(x), x).to(dtype)
+    c = dict(spec=spec, x=x, dtype=dtype, bits=4, w={})
+    parts = [("w_", "", (E,), I)] + ([("shared_", "shared_", (), Is)] if Is else [])
+    for prefix, infix, lead, inter in parts:
+        for mat, n, kk in (("gate", inter, H), ("up", inter, H), ("down", H, inter)):
+            c["w"][prefix + mat] = m.pack_w4(torch.randint(
+                0, 16, (*lead, n, kk), generator=g, device="cuda", dtype=torch.uint8))
+            c["w"][f"s_{infix}{mat}"] = (0.3 + torch.rand(*lead, n, kk // 32, generator=g,
+                                                          device="cuda")) / (4.6 * H**0.5)
+            c["w"][f"z_{infix}{mat}"] = torch.full((*lead, n, kk // 32), 8 if mat != "down" else 1,
+                                                   dtype=torch.uint8, device="cuda")
+        # down: zero points 1, codes 1 but for 2 and 0 at two neighbours in size among the larger h of
+        # token row % T; scales 1 for their groups, 0 for the others
+        q = torch.ones((*lead, H, inter), dtype=torch.uint8, device="cuda")
+        s = torch.zeros((*lead, H, inter // 32), device="cuda")
+        for e in range(E) if lead else (None,):
+            qe, se = (q, s) if e is None else (q[e], s[e])
+            for t in range(T):
+                h = hidden_of(c, prefix, infix, e, x[t].double())[0]
+                order = torch.argsort(h.abs(), descending=True)[:inter // 2]
+                order = order[torch.argsort(h[order])]
+                gaps = torch.argsort((h[order][1:] - h[order][:-1]).abs())
+                for i, row in enumerate(range(t, H, T)):
+                    j = int(gaps[i % (len(gaps) // 2)])
+                    for at, code in ((int(order[j]), 2), (int(order[j + 1]), 0)):
+                        qe[row, at], se[row, at // 32] = code, 1.0
+        c["w"][prefix + "down"], c["w"][f"s_{infix}down"] = m.pack_w4(q), s
+    w_r = torch.randn(E, H, generator=g, device="cuda")
+    experts = m.FewTokenExperts(m.config_from_spec(spec), c["w"], w_r)
+    ws = m.few_tokens_workspace(experts, T)
+    out = torch.empty_like(x)
+    ids = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, k, device="cuda")
+    m.moe_few_tokens(experts, x, out, ws, ids, w)
+    torch.cuda.synchronize()
+    assert m.moe_check_device_status(ws) == m.MOE_OK
+    for t in range(T):
+        picks = [("w_", "", int(e), float(p)) for e, p in zip(ids[t], w[t])] + \
+            ([("shared_", "shared_", None, 1.0)] if Is else [])
+        want, tol = (torch.zeros(H, dtype=torch.float64, device="cuda") for _ in range(2))
+        for prefix, infix, e, p in picks:
+            y, dy = cut_product(c["w"], prefix + "down", infix, "down", e,
+                                *hidden_of(c, prefix, infix, e, x[t].double()))
+            want += p * y
+            tol += p * (dy + 30 * U * y.abs())  # sixteen warps, picks, weights
+        tol = tol + torch.finfo(dtype).eps / 2 * (want.abs() + tol) + TINY[dtype]
+        over = ((out[t].double() - want).abs() - tol).max()
+        assert float(over) <= 0, (t, float(over), float(tol.median()))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("T,E,k,Is", [(1, 1, 1, 0), (2, 3, 2, 0), (3, 2, 1, 64), (4, 8, 3, 0),
+                                      (5, 1, 1, 64), (6, 3, 2, 32), (7, 4, 4, 0), (8, 1, 1, 0),
+                                      (8, 2, 2, 96), (8, 16, 4, 64)])
+@pytest.mark.parametrize("I,group", [(64, 32), (2080, 32), (128, 64), (2304, 128)])
+def test_h_of_fp16_layers_has_two_terms(m, T, E, k, Is, I, group, zeros, dtype):
+    """The differences of neighbours again, of h that the MMAs add exactly: all between an eighth of
+    the largest and it, so that their 11-bit terms are multiples of what an MMA cuts off at.
+
+    x has one channel, so that gate and up are a code and a scale: exact but for fp32's roundings,
+    16 u of h with silu's.  What is left is h's own rounding, half a step of fp16, eps / 2 = 2^-11 of
+    it, with one term, 2^-22 with two, and 8 u of the magnitudes (q + z) h of its blocks, which z times their sum and the scales
+    round to."""
+    if group > 32:
+        Is = up_to(Is, group)
+    H = 128
+    spec = synth.spec("tiny", T=T, name="few_h", n_zero=0, renormalize=True, hidden=H, inter=I,
+                      n_routed=E, top_k=k, shared_inter=Is)
+    g = gen(T + E + I)
+    x = torch.zeros(T, H, device="cuda", dtype=dtype)
+    x[:, 0] = 1 + torch.randperm(64, generator=g, device="cuda")[:T] / 128
+    w, hs = {}, {}
+    parts = [("w_", "", (E,), I)] + ([("shared_", "shared_", (), Is)] if Is else [])
+    for prefix, infix, lead, inter in parts:
+        for mat, n, kk in (("gate", inter, H), ("up", inter, H), ("down", H, inter)):
+            q = torch.randint(0, 16, (*lead, n, kk), generator=g, device="cuda", dtype=torch.uint8)
+            q[..., 0] = 9
+            w[prefix + mat] = m.pack_w4(q)
+            w[f"s_{infix}{mat}"] = 1 + torch.rand(*lead, n, kk // group, generator=g, device="cuda")
+            if zeros:
+                w[f"z_{infix}{mat}"] = torch.full((*lead, n, kk // group), 8, dtype=torch.uint8,
+                                                  device="cuda")
+        gate, up = (w[f"s_{infix}{mat}"][..., 0].double() for mat in ("gate", "up"))
+        q = torch.full((*lead, H, inter), 8, dtype=torch.uint8, device="cuda")
+        s = torch.zeros((*lead, H, inter // group), device="cuda")
+        for e in range(E) if lead else (None,):
+            qe, se = (q, s) if e is None else (q[e], s[e])
+            for t in range(T):
+                v = gate if e is None else gate[e]
+                v = v * x[t, 0].double()
+                h = v * torch.sigmoid(v) * (up if e is None else up[e]) * x[t, 0].double()
+                assert float(h.min()) >= float(h.max()) / 8
+                hs[e, t] = h
+                order = torch.argsort(h)
+                for i, row in enumerate(range(t, H, T)):
+                    j = (37 * i + 11) % (inter - 1)
+                    for at, code in ((int(order[j]), 9), (int(order[j + 1]), 7)):
+                        qe[row, at], se[row, at // group] = code, 1.0
+        w[prefix + "down"], w[f"s_{infix}down"] = m.pack_w4(q), s
+    w_r = torch.randn(E, H, generator=g, device="cuda")
+    experts = m.FewTokenExperts(m.config_from_spec(spec), w, w_r)
+    ws = m.few_tokens_workspace(experts, T)
+    out = torch.empty_like(x)
+    ids = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    wts = torch.empty(T, k, device="cuda")
+    m.moe_few_tokens(experts, x, out, ws, ids, wts)
+    torch.cuda.synchronize()
+    assert m.moe_check_device_status(ws) == m.MOE_OK
+    rel = 16 * U + (2.0**-11 if dtype == BF16 else 2.0**-22)
+    for t in range(T):
+        picks = [("w_", "", int(e), float(p)) for e, p in zip(ids[t], wts[t])] + \
+            ([("shared_", "shared_", None, 1.0)] if Is else [])
+        want, tol = (torch.zeros(H, dtype=torch.float64, device="cuda") for _ in range(2))
+        for prefix, infix, e, p in picks:
+            a, b = exact_matrix(w, prefix + "down", infix, "down", e)
+            h = hs[e, t]
+            want += p * (a @ h)
+            tol += p * ((rel + 30 * U) * (a.abs() @ h) + 8 * U * (b @ h))
+        tol = tol + torch.finfo(dtype).eps / 2 * (want.abs() + tol) + TINY[dtype]
+        over = ((out[t].double() - want).abs() - tol).max()
+        assert float(over) <= 0, (t, float(over), float(tol.median()))
+
+
+def up_to(v, to):
+    return -(-v // to) * to
