@@ -16,15 +16,16 @@ constexpr int kFewSub = 2048;     // bytes of the weights of a ring stage: 16 ro
 constexpr int kFewMaxStages = 4;
 constexpr int kFewSmem = 226 * 1024;  // dynamic; the kernel has a few words besides
 constexpr int kFewUnitBytes = 8;
+constexpr int kFewParts = 2 * kFewTeams * kFewTeamWarps * 16 * 8 * 4;  // bytes of the tiles' parts
 
-// Layout of a CTA's shared memory: x, its block sums, units, passes, rows of h, parts, rings.
+// Layout of a CTA's shared memory: x, its block sums, units, rows of h, parts, rings.
 struct FewPlan {
   int step_k;          // K of a stage: 256 four-bit or 64 sixteen-bit weights a row
   int xpitch;          // bytes between two tokens
   int block;           // K that shares a scale: 32, 64 or 128
   int hpitch, hrest;   // bytes between two rows of h there, to what 16-bit operands leave; 0:
                        // h does not fit
-  int sum_at, unit_at, pass_at, row_at, red_at, queue_at, ring_at;
+  int sum_at, unit_at, row_at, red_at, queue_at, ring_at;
   int swords, zwords;  // 4-byte words of scales and zero points a row has in a stage
   int s_eight, z_eight;  // bytes from a row's groups to those eight rows on
   int s_next, z_next;    // bytes from a block's scale (zero point) to the next one's, or 0
@@ -42,12 +43,6 @@ inline int few_words(int n, int size, int64_t row) {
   const int bytes = n * size;
   return row % 4 == 0 && bytes % 4 == 0 ? bytes / 4 : (bytes + 4 - size + 3) / 4;
 }
-
-// The down projection goes through a unit's tokens in passes of as many as the MMAs' eight columns
-// hold: four where a token's h takes two columns.
-constexpr int kFewPassBytes = 8;
-constexpr int kFewPairs = kFewMaxT / 2;
-inline int few_passes(int units, int rows) { return units + rows / (kFewPairs + 1); }
 
 // units, rows: experts with tokens and rows of h, at most; inter: the longest row of h.
 // group: 0 (a row), 32, 64, 128; rows_aligned: every row's scales (zero points) begin at a
@@ -78,10 +73,9 @@ inline FewPlan few_plan(int T, int H, int inter, int units, int rows, bool four_
   const int x_bytes = p.sum_at + blocks * kFewMaxT * 4;
   auto place = [&](int front) {
     p.unit_at = few_round(front, 16);
-    p.pass_at = p.unit_at + units * kFewUnitBytes;
-    p.row_at = p.pass_at + few_passes(units, rows) * kFewPassBytes;
+    p.row_at = p.unit_at + units * kFewUnitBytes;
     p.red_at = few_round(p.row_at + (units + 1 + rows) * 4, 16);
-    p.queue_at = p.red_at + 2 * kFewTeams * kFewTeamWarps * 16 * 8 * 4;
+    p.queue_at = p.red_at + kFewParts;
     p.ring_at = few_round(p.queue_at + kFewTeams * 16 * 4, 128);
     p.stages = std::min(kFewMaxStages, (kFewSmem - p.ring_at) / (kFewWarps * p.sub_bytes));
   };

@@ -76,12 +76,16 @@ struct FewUnit {
   uint32_t tokens;  // bit t: token t picked it
 };
 static_assert(sizeof(FewUnit) == kFewUnitBytes, "the plan's size");
-// Tokens of a unit that the down projection takes at once.
+// Tokens of a unit that the down projection takes at once: as many as the MMAs' eight columns hold,
+// kFewPairs where a token's h takes two of them.  That list lies over the gate/up tiles' parts.
 struct FewPass {
   int unit;
   uint32_t tokens;
 };
-static_assert(sizeof(FewPass) == kFewPassBytes, "the plan's size");
+constexpr int kFewPairs = kFewMaxT / 2;
+static_assert((kFewMaxPicks + 1 + (kFewMaxPicks + kFewMaxT) / (kFewPairs + 1)) * sizeof(FewPass) <=
+                  kFewParts,
+              "every unit's passes");
 
 // Workspace after the status block.  `ticket` is zero between calls; the rest is
 // written by the first kernel.
@@ -948,8 +952,8 @@ __device__ __forceinline__ void stage_h(const FewArgs& a, unsigned char* smem,
 
 template <typename K>
 __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, const FewUnit* units,
-                                     const FewTiles& n, const FewPass* passes, const int* npasses,
-                                     int nunits, const float* zero_w) {
+                                     const FewTiles& n, const FewPass* passes, int routed_passes,
+                                     int shared_passes, int nunits, const float* zero_w) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int g = lane / 4, tg = lane % 4;
   const FewShape rs = shape_of<K>(a, a.I), ss = shape_of<K>(a, a.Is);
@@ -961,10 +965,10 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
   const int share = (a.H + gridDim.x - 1) / gridDim.x;
   const int c_begin = min(a.H, (int)blockIdx.x * share), c_end = min(a.H, c_begin + share);
   // every pass's steps, the routed experts' first
-  const int routed = npasses[0] * rs.steps, flat = routed + npasses[1] * ss.steps;
+  const int routed = routed_passes * rs.steps, flat = routed + shared_passes * ss.steps;
   const int f0 = (int)((int64_t)flat * warp / kFewWarps);
   const int f1 = (int)((int64_t)flat * (warp + 1) / kFewWarps);
-  const int d0 = f0 < routed ? f0 / rs.steps : npasses[0] + (f0 - routed) / max(1, ss.steps);
+  const int d0 = f0 < routed ? f0 / rs.steps : routed_passes + (f0 - routed) / max(1, ss.steps);
   const int step0 = f0 < routed ? f0 % rs.steps : (f0 - routed) % max(1, ss.steps);
   const int dst = lane / 8 * 128;
   const uint32_t dst0 = dst + K::swizzle(lane / 8, lane % 8) * 16;
@@ -973,6 +977,12 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
   const int* row0 = reinterpret_cast<const int*>(smem + a.p.row_at);
   const bool inside = a.p.hpitch > 0;
   bool waited = false;
+  auto pass_at = [&](int d) {
+    if constexpr (K::kPaired)
+      return passes[d];
+    else
+      return FewPass{d, units[d].tokens};
+  };
 
   for (int c0 = c_begin; c0 < c_end; c0 += 16 * kFewDownTiles) {
     const int channels = min(c_end - c0, 16 * kFewDownTiles);
@@ -984,7 +994,7 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
     const unsigned char *w = nullptr, *sp = nullptr, *zp = nullptr;
     int64_t four = 0;  // bytes of four rows
     auto enter = [&]() {
-      const int e = units[passes[next_d].unit].expert;
+      const int e = units[pass_at(next_d).unit].expert;
       const FewMatrix& m = e < 0 ? a.shared[2] : a.m[2];
       next_steps = e < 0 ? ss.steps : rs.steps;
       next_groups = e < 0 ? ss.groups : rs.groups;
@@ -1090,11 +1100,12 @@ __device__ __forceinline__ void down(const FewArgs& a, unsigned char* smem, cons
           step = 0;
           ++d;
         }
-        const int u = passes[d].unit, e = units[u].expert;
+        const FewPass pass = pass_at(d);
+        const int u = pass.unit, e = units[u].expert;
         const FewShape& sh = e < 0 ? ss : rs;
         steps = sh.steps;
         kmax = sh.K;
-        const uint32_t tokens = passes[d].tokens;
+        const uint32_t tokens = pass.tokens;
         in0 = (tokens >> (2 * tg)) & 1u;
         in1 = (tokens >> (2 * tg + 1)) & 1u;
         int t = g;  // the token of the lane's column
@@ -1299,7 +1310,7 @@ template <typename K>
 __global__ void __launch_bounds__(kFewThreads, 1) few_ffn_kernel(const __grid_constant__ FewArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float x_inverse[kFewMaxT], zero_w[kFewMaxT];
-  __shared__ int npasses[2];  // of routed experts, of the shared one
+  __shared__ int npasses[K::kPaired ? 2 : 1];  // of routed experts, of the shared one
   const int tid = threadIdx.x;
   // x is complete: the routing kernel let this one start only after its own wait for
   // everything before it.  What the routing kernel writes is read after the wait here.
@@ -1316,28 +1327,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_ffn_kernel(const __grid_co
     reinterpret_cast<uint32_t*>(units)[i] = __ldcg(reinterpret_cast<const uint32_t*>(a.head->unit) + i);
   if (tid < kFewMaxT) zero_w[tid] = __ldcg(&a.head->zero_w[tid]);
   __syncthreads();
-  // the passes of the down projection and, where h is kept here, its rows (read after the next
-  // barrier)
   const int nunits = n.units + shared;
-  FewPass* passes = reinterpret_cast<FewPass*>(smem + a.p.pass_at);
-  constexpr int kMost = K::kPaired ? kFewPairs : kFewMaxT;  // tokens of a pass
-  for (int u = tid; u <= nunits; u += kFewThreads) {
+  if (a.p.hpitch > 0) {  // the rows of h (read after the next barrier)
     int* row0 = reinterpret_cast<int*>(smem + a.p.row_at);
-    int first = 0, pass = 0;
-    for (int i = 0; i < u; ++i) {
-      const int tokens = __popc(units[i].tokens);
-      first += tokens;
-      pass += tokens > kMost ? 2 : 1;
-    }
-    if (u == n.units) npasses[0] = pass;
-    if (u == nunits) npasses[1] = shared ? __popc(units[n.units].tokens) > kMost ? 2 : 1 : 0;
-    if (u < nunits) {
-      uint32_t rest = units[u].tokens;
-      for (int i = 0; i < kMost; ++i) rest &= rest - 1u;
-      passes[pass] = {u, units[u].tokens ^ rest};
-      if (rest) passes[pass + 1] = {u, rest};
-    }
-    if (a.p.hpitch > 0) {
+    for (int u = tid; u <= nunits; u += kFewThreads) {
+      int first = 0;
+      for (int i = 0; i < u; ++i) first += __popc(units[i].tokens);
       row0[u] = first;
       if (u < nunits)
         for (int t = 0; t < kFewMaxT; ++t)
@@ -1347,7 +1342,25 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_ffn_kernel(const __grid_co
   gate_up<K>(a, smem, units, n, x_inverse);
   __syncthreads();
   pdl_trigger();
-  down<K>(a, smem, units, n, passes, npasses, nunits, zero_w);
+  FewPass* passes = reinterpret_cast<FewPass*>(smem + a.p.red_at);
+  if constexpr (K::kPaired) {
+    auto count = [&](int u) { return __popc(units[u].tokens) > kFewPairs ? 2 : 1; };
+    for (int u = tid; u <= nunits; u += kFewThreads) {
+      int at = 0;
+      for (int i = 0; i < u; ++i) at += count(i);
+      if (u == n.units) npasses[0] = at;
+      if (u == n.units) npasses[1] = shared ? count(u) : 0;
+      if (u < nunits) {
+        uint32_t rest = units[u].tokens;
+        for (int i = 0; i < kFewPairs; ++i) rest &= rest - 1u;
+        passes[at] = {u, units[u].tokens ^ rest};
+        if (rest) passes[at + 1] = {u, rest};
+      }
+    }
+    __syncthreads();
+  }
+  const int routed = K::kPaired ? npasses[0] : n.units;
+  down<K>(a, smem, units, n, passes, routed, K::kPaired ? npasses[1] : shared, nunits, zero_w);
 }
 
 // ------------------------------------------------------------------ launch --
