@@ -423,6 +423,8 @@ def moe_clip_grad_norm(tensors, max_norm, norm, ws, eps=1e-6, stream=None):
     if not isinstance(tensors, TensorList):
         tensors = TensorList(tensors)
     n = len(tensors)
+    if not n:
+        _a_tensor(ws, "ws")
     dev = tensors.device if n else ws.get_device()
     written = tensors.written
     for i, t in enumerate(written):

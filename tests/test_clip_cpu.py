@@ -76,3 +76,10 @@ def test_lists_are_checked(moe, monkeypatch):
     operators.TensorList([t[:0], t, t[5:5]])
     with pytest.raises(ValueError, match="not on the current CUDA device"):
         operators.moe_clip_grad_norm([t], 1.0, None, operators.clip_workspace("cpu"))
+
+
+def test_no_tensors_and_no_workspace(moe):
+    with pytest.raises(TypeError, match="ws: expected a tensor"):
+        moe.moe_clip_grad_norm([], 1.0, None, None)
+    with pytest.raises(ValueError, match="not on the current CUDA device"):
+        moe.moe_clip_grad_norm([], 1.0, torch.zeros(1), moe.clip_workspace("cpu"))
