@@ -405,8 +405,11 @@ moe_status moe_w4_gemv(int32_t n_experts, int32_t N, int32_t K, int32_t group, i
  * 4-bit weights.  moe_layer_forward's result,
  *   out[t] = sum over picks of w * (expert's FFN, or x_t for zero-computation experts)
  *            + shared expert,
- * for decode steps and short drafts, where that call's launches would take longer than
- * the picked experts' weights.  Logits and statistics are fp32; 16-bit weights meet x
+ * for decode steps and short drafts.  With bf16 weights it is the faster call from about
+ * 1000 channels on (one token, 6 of 64 experts, cold, us against that call's: 1024 channels 33
+ * and 50, 5120 97 and 132; eight tokens 57 and 63, 326 and 335), that one below (256 channels,
+ * 2 of 8 experts: 28 and 20) and for eight tokens of the widest (7168 channels, 8 of 64
+ * experts: 731 and 657); 4-bit weights have this call only.  Logits and statistics are fp32; 16-bit weights meet x
  * as it is and h as a sum of two 16-bit numbers.  4-bit weights meet x in fp16, scaled so
  * that elements down to 2^-23 of a token's largest are exact (their MMAs add products cut
  * off at 2^-15 of the largest x of sixteen), and h as a sum of two fp16 numbers where x is

@@ -20,8 +20,8 @@
 //
 // Measured on a GB300, cold, us (at 6.78 TB/s): one row, rank 16, 5120 to 5120 channels 7.1 (a
 // launch and three dependent reads); 64 rows of 48 adapters, 7168 to 2048 8.8 (1.6); 8192 rows,
-// 5120 to 5120, rank 16 65 (37), 64 75 (38), 128 131 (39); gradients of 8192 rows, rank 16, 7168
-// and 5120 channels 104 (48), rank 64, 5120 and 5120 164 (41).
+// 5120 to 5120, rank 16 65 (37), 64 75 (39), 128 126 (40); gradients of 8192 rows, rank 16, 7168
+// and 5120 channels 104 (48), rank 64, 5120 and 5120 168 (41).
 #include <math.h>
 
 #include <algorithm>
@@ -981,9 +981,11 @@ struct OuterShape {
 // after the other).  Rows of x and terms of v lie as the MMAs read them, both transposed.  After
 // every kFlush stages the accumulators are added, rounded, to sums in registers: MMAs cut theirs
 // off where fp32 ends.  Waits for stages at 44% issue: 201 MB of x and dy at rank 16 in 51 us, 4.1
-// TB/s.  With mma.sync and ldmatrix the gradients of 8192 rows took 107 us instead of 104 (rank 16,
-// 7168 and 5120 channels), 218 instead of 164 (64, 5120 and 5120) and 260 instead of 177 (128, 2048
-// and 2048); columns in twos of 128 up to 32 ranks, as tensor memory holds two CTAs' sums.
+// TB/s; at ranks 64 (5120 and 5120) and 128 (2048 and 2048) 110 and 102 us at 44 and 30% issue, where
+// the terms of v are made again for each tile of columns.  With mma.sync and ldmatrix the gradients
+// of 8192 rows took 107 us instead of 104 (rank 16, 7168 and 5120 channels), 218 instead of 177 (64,
+// 5120 and 5120) and 260 instead of 203 (128, 2048 and 2048); the split of positions has changed
+// since.  Columns in twos of 128 up to 32 ranks, as tensor memory holds two CTAs' sums.
 template <typename T, int RT>
 __global__ void __launch_bounds__(kOuterThreads, kOuterPerSm<RT>) adapters_outer_kernel(OuterArgs a) {
   extern __shared__ unsigned char raw[];

@@ -4,10 +4,11 @@
 // of the list of chunks of 32 KB; the first kernel goes through it forwards and the second
 // backwards, so that what the first read last is still in L2 when the second starts there.
 //
-// Bound by memory: a product needs the norm, so what L2 does not hold is read twice.  48 fp32
-// tensors of 25 MB 12.1 us (read and written once: 7.4 at 6.78 TB/s; two launches and a sum of all
-// slots are the rest); 37 tensors of all types, 40 MB 22; 3 GB of bf16 in three tensors 1370 (two
-// reads and a write: 1335; 7.0 TB/s in the first kernel, 6.5 in the second).
+// Bound by memory where L2 can not hold the tensors: a product needs the norm, so they are read
+// twice, 3 GB of bf16 in three tensors in 1370 us (two reads and a write: 1335 at 6.78 TB/s; 7.0 in
+// the first kernel, 6.5 in the second).  Smaller ones wait for two launches with a sum of all slots
+// between them: 48 fp32 tensors, 12.6 MB, 12.1 us (read and written once: 3.7); 37 tensors of all
+// types, 40 MB, 22 (11.8).
 //
 // The squares of a thread's 64 elements of a chunk (fp32: 32) are added in fp32, its
 // chunks and the threads as pairs of fp32, each CTA's sum in a slot of its own, and the slots
@@ -219,8 +220,7 @@ struct ClipWalk {
 };
 
 // A sum as hi + lo, lo the rounding errors of hi's additions (Knuth's exact addition).  fp64
-// would do it shorter, but its rate here is so low that the additions of 608 CTAs' threads took
-// longer than 20 MB of data.  hi is inf or NaN where the sum is; lo means nothing then.
+// would do it shorter, but its rate here is so low that with it 12.6 MB took 19.7 us instead of 12.1.  hi is inf or NaN where the sum is; lo means nothing then.
 struct ClipSum {
   float hi, lo;
 };

@@ -24,10 +24,11 @@
 //
 // Measured on a GB300, cold (the weights at 6.78 TB/s): one token through 8 of 256 4-bit experts
 // and a shared one, 7168 and 2048 channels, groups of 128: 59 us (31); eight tokens through 64
-// bf16 experts, 5120 and 1536 channels: 325 (311); five tokens, groups of 32 with zero points, 2304
-// and 736 channels: 52 (8.4).  Of the 59: router, picks and the start of the second kernel 14, gate
-// and up 28, the wait for the last CTA 4, h 2, down 15 with its sums.  The bf16 layer waits for memory,
-// the 4-bit ones for the latency of short tiles (three to seven steps a warp) at 42% issue.
+// bf16 experts, 5120 and 1536 channels: 330 (311); five tokens in fp16, groups of 32 with zero points,
+// 2304 and 736 channels: 58 (8.4).  By time stamps, with which the 59 are 66: router, picks and the
+// start of the second kernel 13, gate and up 28, the wait for the last CTA 4, h 2, down 16, its sums
+// 3.  The bf16 layer waits for memory, the 4-bit ones for the latency of short tiles (three to seven
+// steps a warp) at 42% issue.
 //
 // 4-bit weights: a nibble alone in the low bits of a half is the fp16 subnormal
 // q * 2^-24 (four bits up: q * 2^-20, its x is divided by 16), so a weight costs part of

@@ -372,7 +372,8 @@ def clip_workspace(device="cuda"):
 
 class TensorList:
     """Tensors as moe_clip_grad_norm takes them, checked once: a program whose
-    gradients stay where they are makes one list and calls with it every step.
+    gradients stay where they are makes one list and calls with it every step (a new
+    list costs about 2.2 us of host time a tensor).
 
     tensors: contiguous bf16, fp16 or fp32 tensors of any shapes on one CUDA device.
     outs: None (in place), or for each tensor one of its shape and type, the tensor
@@ -444,7 +445,8 @@ def moe_clip_grad_norm(tensors, max_norm, norm, ws, eps=1e-6, stream=None):
 
 
 class FewTokenExperts:
-    """A layer's description and weights as moe_few_tokens takes them, checked once.
+    """A layer's description and weights as moe_few_tokens takes them, checked once (and
+    held: their values may change, their storage may not be exchanged).
 
     cfg: MoeConfig with the wdtype of a bf16 layer, whatever the weights are.
     weights: w_gate, w_up [E, I, H] and w_down [E, H, I], with a shared expert also
