@@ -687,3 +687,45 @@ def test_h_of_fp16_layers_has_two_terms(m, T, E, k, Is, I, group, zeros, dtype):
 
 def up_to(v, to):
     return -(-v // to) * to
+
+
+@pytest.mark.parametrize("T", [3, 8])
+def test_paired_columns_stay_apart(m, T):
+    """fp16 and 4-bit weights: tokens and experts that are not finite reach their own tokens only, and
+    calls give the same bits, in a graph too."""
+    c = make("deep", T, FP16, 4, 64, seed=3)
+    k = c["spec"]["top_k"]
+    experts = experts_of(m, c)
+    ws = m.few_tokens_workspace(experts, T)
+    good, out = torch.empty_like(c["x"]), torch.empty_like(c["x"])
+    ids = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    m.moe_few_tokens(experts, c["x"], good, ws, ids)
+    for _ in range(10):
+        m.moe_few_tokens(experts, c["x"], out.fill_(7), ws)
+        assert torch.equal(out, good)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.moe_few_tokens(experts, c["x"], out, ws)
+    out.fill_(7)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, good)
+    # a token
+    for bad in (float("nan"), float("inf")):
+        x = c["x"].clone()
+        x[1, 5] = bad
+        m.moe_few_tokens(experts, x, out, ws)
+        rest = [t for t in range(T) if t != 1]
+        assert torch.isfinite(out[rest]).all() and not torch.isfinite(out[1]).all()
+        # (the other token's picks may differ, and with them the order of the sums)
+        assert ((out[rest].double() - good[rest].double()).abs()
+                <= 2.0**-10 * good[rest].double().abs() + 1e-4).all()
+    # an expert
+    e = int(ids[0, 0])
+    picked = (ids == e).any(1)
+    c["w"]["s_gate"][e].fill_(float("inf"))
+    c["w"]["s_down"][e].fill_(float("inf"))
+    m.moe_few_tokens(experts, c["x"], out, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(out[~picked], good[~picked])
+    assert not torch.isfinite(out[picked]).any()
