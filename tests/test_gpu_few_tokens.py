@@ -52,7 +52,6 @@ LAYERS = {
                    bias_mode="select", bias_kind="iid", renormalize=True),
     "only_zero": dict(hidden=256, inter=32, n_routed=0, n_zero=8, top_k=2, renormalize=True),
     "only_shared": dict(hidden=256, inter=32, n_routed=0, n_zero=4, top_k=1, shared_inter=160),
-    "unused_inter": dict(hidden=256, inter=50, n_routed=0, n_zero=4, top_k=1, shared_inter=32),
     "all": dict(hidden=160, inter=64, n_routed=32, top_k=32, renormalize=True),
     "one": dict(hidden=32, inter=32, n_routed=1, top_k=1),
     "flat256": dict(hidden=64, inter=32, n_routed=250, top_k=9, renormalize=True),
@@ -215,7 +214,7 @@ def test_sixteen_bit_weights(m, name, T, dtype):
     check(m, make(name, T, dtype, 16))
 
 
-FOUR = ["flat", "flat512", "flat768", "groups", "per_group", "zero", "select", "only_zero", "only_shared", "unused_inter", "all", "one",
+FOUR = ["flat", "flat512", "flat768", "groups", "per_group", "zero", "select", "only_zero", "only_shared", "all", "one",
         "wide", "deep"]
 
 
@@ -729,3 +728,14 @@ def test_paired_columns_stay_apart(m, T):
     torch.cuda.synchronize()
     assert torch.equal(out[~picked], good[~picked])
     assert not torch.isfinite(out[picked]).any()
+
+
+@pytest.mark.parametrize("T", [1, 2, 5, 8])
+@pytest.mark.parametrize("dtype,bits,zeros", [(BF16, 16, False), (FP16, 16, False), (BF16, 4, False),
+                                              (FP16, 4, True)])
+@pytest.mark.parametrize("inter", [50, 33, 4097])
+def test_an_inter_that_no_expert_has(m, monkeypatch, inter, dtype, bits, zeros, T):
+    # rows of h are the shared expert's, whole 16-byte pieces
+    monkeypatch.setitem(LAYERS, "unused_inter", dict(hidden=256, inter=inter, n_routed=0, n_zero=4,
+                                                     top_k=1, shared_inter=32))
+    check(m, make("unused_inter", T, dtype, bits, 32, zeros, None))
